@@ -16,16 +16,24 @@ from .binding import (  # noqa: F401
     KvFp8Error,
     LIB,
     LIB_PATH,
+    MAX_CACHES,
     check_scale_host,
+    compact_blocks,
+    compact_blocks_workspace_size,
+    copy_blocks,
     dequant,
+    dequant_fp4,
     paged_attention_multi,
+    paged_attention_multi_fp4,
     paged_attention_multi_mixed,
     paged_attention_multi_workspace_size,
     paged_decode_attention,
+    paged_decode_attention_fp4,
     paged_decode_attention_mixed,
     paged_decode_attention_noalloc,
     paged_decode_workspace_size,
     reshape_and_cache,
+    reshape_and_cache_fp4,
     reshape_and_cache_mixed,
     rope_reshape_and_cache,
     status_string,

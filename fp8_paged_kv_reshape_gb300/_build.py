@@ -19,7 +19,8 @@ WITHHOLD_DEFINE = "-DKVFP8_TEST_WITHHOLD_FIRST_CHUNK=1"
 HEADER = os.path.join(ROOT, "include", "kvfp8.h")
 
 SOURCES = ["kvfp8_api.cu", "reshape_and_cache.cu", "paged_decode.cu", "paged_decode_mixed.cu",
-           "prefill_attention.cu", "dequant.cu", "decode_noalloc.cu"]
+           "prefill_attention.cu", "dequant.cu", "decode_noalloc.cu", "fp4_cache.cu",
+           "paged_decode_fp4.cu", "block_copy.cu"]
 DEPS = ["kvfp8_device.cuh", "kvfp8_internal.h", "paged_decode_kernel.cuh"]
 
 NVCC_FLAGS = [

@@ -6,6 +6,7 @@ fallback: if the library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -20,6 +21,7 @@ BF16 = 0
 F32 = 1
 CACHE_E4M3 = 0
 CACHE_BF16 = 1
+MAX_CACHES = 128  # KVFP8_MAX_CACHES
 
 DEV_BAD_SCALE = 1 << 0
 DEV_BAD_SLOT = 1 << 1
@@ -39,6 +41,13 @@ ABI_FUNCTIONS = (
     "kvfp8_paged_decode_attention_mixed",
     "kvfp8_paged_attention_multi_mixed",
     "kvfp8_dequant",
+    "kvfp8_reshape_and_cache_fp4",
+    "kvfp8_dequant_fp4",
+    "kvfp8_paged_decode_attention_fp4",
+    "kvfp8_paged_attention_multi_fp4",
+    "kvfp8_copy_blocks",
+    "kvfp8_compact_blocks_workspace_size",
+    "kvfp8_compact_blocks",
     "kvfp8_check_scale_host",
     "kvfp8_status_string",
 )
@@ -95,6 +104,26 @@ def _load() -> ctypes.CDLL:
     lib.kvfp8_paged_attention_multi_mixed.restype = ctypes.c_int
     lib.kvfp8_dequant.argtypes = [P, ctypes.c_int, P, i64, P, ctypes.c_int, P]
     lib.kvfp8_dequant.restype = ctypes.c_int
+    lib.kvfp8_reshape_and_cache_fp4.argtypes = [P, P, ctypes.c_int, i64, i64, i64, P, P, P, P, i32,
+                                                i32, i32, i32, P, P, P, ctypes.c_int, P, P]
+    lib.kvfp8_reshape_and_cache_fp4.restype = ctypes.c_int
+    lib.kvfp8_dequant_fp4.argtypes = [P, ctypes.c_int, P, P, i32, i32, i32, i32, P, i64, P,
+                                      ctypes.c_int, P, P]
+    lib.kvfp8_dequant_fp4.restype = ctypes.c_int
+    lib.kvfp8_paged_decode_attention_fp4.argtypes = [P, P, P, P, P, P, P, i32, P, i32, i32, i32,
+                                                     i32, i32, i32, f32, P, P, ctypes.c_int, P, sz,
+                                                     P, P]
+    lib.kvfp8_paged_decode_attention_fp4.restype = ctypes.c_int
+    lib.kvfp8_paged_attention_multi_fp4.argtypes = [P, P, P, i32, i32, P, P, P, P, P, i32, P, i32,
+                                                    i32, i32, i32, i32, i32, f32, P, P,
+                                                    ctypes.c_int, P, sz, P, P]
+    lib.kvfp8_paged_attention_multi_fp4.restype = ctypes.c_int
+    lib.kvfp8_copy_blocks.argtypes = [P, P, i32, i32, P, P, i64, P, P]
+    lib.kvfp8_copy_blocks.restype = ctypes.c_int
+    lib.kvfp8_compact_blocks_workspace_size.argtypes = [i32]
+    lib.kvfp8_compact_blocks_workspace_size.restype = sz
+    lib.kvfp8_compact_blocks.argtypes = [P, P, i32, i32, i32, P, i32, P, i32, P, P, P, sz, P, P]
+    lib.kvfp8_compact_blocks.restype = ctypes.c_int
     lib.kvfp8_check_scale_host.argtypes = [f32]
     lib.kvfp8_check_scale_host.restype = ctypes.c_int
     lib.kvfp8_status_string.argtypes = [ctypes.c_int]
@@ -479,3 +508,288 @@ def dequant(src: torch.Tensor, dst_dtype: torch.dtype = torch.float32,
                            src.numel(), _ptr(scale), sdt, _stream(stream))
     _check(rc, "kvfp8_dequant")
     return out
+
+
+# ---------------------------------------------------------------- 4-bit cache, pages
+
+def _check_device(**tensors):
+    """Every given tensor on the current CUDA device, where the kernels run."""
+    here = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _check_status(status: torch.Tensor | None):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 [1] tensor")
+
+
+def _on(stream):
+    """Allocations for a call on `stream` belong to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _check_fp4_side(cache: torch.Tensor, scales: torch.Tensor):
+    """One side of a 4-bit cache; returns (num_blocks, block_size, n_kv, head_dim)."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
+        raise ValueError("4-bit codes must be contiguous uint8 [num_blocks, block_size, n_kv, head_dim/2]")
+    nb, bs, n_kv, half = cache.shape
+    if half % 8 != 0 or scales.dtype != torch.uint8 or \
+            tuple(scales.shape) != (nb, n_kv, bs, half // 8) or not scales.is_contiguous():
+        raise ValueError("their scales must be contiguous uint8 [num_blocks, n_kv, block_size, head_dim/16]")
+    return nb, bs, n_kv, 2 * half
+
+
+def _check_fp4_caches(key_cache, value_cache, key_scales, value_scales):
+    shape = _check_fp4_side(key_cache, key_scales)
+    if _check_fp4_side(value_cache, value_scales) != shape:
+        raise ValueError("key and value caches must have one shape")
+    return shape
+
+
+def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
+                          value_cache: torch.Tensor, key_scales: torch.Tensor,
+                          value_scales: torch.Tensor, slot_mapping: torch.Tensor,
+                          k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None, stream=None) -> None:
+    """kvfp8_reshape_and_cache_fp4: rows into the 4-bit cache.
+
+    key/value as for reshape_and_cache.  Codes: uint8 [num_blocks, block_size, n_kv,
+    head_dim/2]; scales: uint8 [num_blocks, n_kv, block_size, head_dim/16], all contiguous.
+    slot_mapping: int64 [num_tokens] (-1 = padding), no slot twice.
+    """
+    if key.dtype != value.dtype or key.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("key and value must share one dtype, bfloat16 or float32")
+    if key.dim() != 3 or value.shape != key.shape:
+        raise ValueError("key/value must be [num_tokens, n_kv, head_dim] with equal shapes")
+    n, n_kv, hd = key.shape
+    for t in (key, value):
+        if n > 0 and (t.stride(2) != 1 or (n_kv > 1 and t.stride(1) != hd)):
+            raise ValueError("key/value inner dims [n_kv, head_dim] must be dense")
+    nb, bs, c_kv, c_hd = _check_fp4_caches(key_cache, value_cache, key_scales, value_scales)
+    if (c_kv, c_hd) != (n_kv, hd):
+        raise ValueError("the caches' n_kv and head_dim must be those of key and value")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != n or \
+            not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
+    sdt = _scale_args(k_scale, v_scale)
+    _check_status(status)
+    _check_device(key=key, value=value, key_cache=key_cache, value_cache=value_cache,
+                  key_scales=key_scales, value_scales=value_scales, slot_mapping=slot_mapping,
+                  k_scale=k_scale, v_scale=v_scale, status=status)
+    # (the stride of a single row is never used, and may be anything)
+    ks, vs = (key.stride(0), value.stride(0)) if n > 1 else (n_kv * hd, n_kv * hd)
+    rc = LIB.kvfp8_reshape_and_cache_fp4(
+        _ptr(key), _ptr(value), F32 if key.dtype == torch.float32 else BF16, ks, vs, n,
+        _ptr(key_cache), _ptr(value_cache), _ptr(key_scales), _ptr(value_scales), nb, bs, n_kv, hd,
+        _ptr(slot_mapping), _ptr(k_scale), _ptr(v_scale), sdt, _ptr(status), _stream(stream))
+    _check(rc, "kvfp8_reshape_and_cache_fp4")
+
+
+def dequant_fp4(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.Tensor,
+                dst_dtype: torch.dtype = torch.bfloat16, scale: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """kvfp8_dequant_fp4: the rows of one side of a 4-bit cache at slot_mapping's slots, as
+    bfloat16 or float32 [num_tokens, n_kv, head_dim] (slot -1: a zero row)."""
+    nb, bs, n_kv, hd = _check_fp4_side(cache, scales)
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
+    if dst_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dst_dtype must be float32 or bfloat16")
+    n = slot_mapping.numel()
+    if out is not None and (out.dtype != dst_dtype or tuple(out.shape) != (n, n_kv, hd) or
+                            not out.is_contiguous()):
+        raise ValueError("out must be a contiguous dst_dtype [num_tokens, n_kv, head_dim] tensor")
+    sdt = _scale_args(scale, None)
+    _check_status(status)
+    _check_device(cache=cache, scales=scales, slot_mapping=slot_mapping, scale=scale, out=out,
+                  status=status)
+    if out is None:
+        with _on(stream):
+            out = torch.empty((n, n_kv, hd), dtype=dst_dtype, device=cache.device)
+    rc = LIB.kvfp8_dequant_fp4(_ptr(out), BF16 if dst_dtype == torch.bfloat16 else F32, _ptr(cache),
+                               _ptr(scales), nb, bs, n_kv, hd, _ptr(slot_mapping), n, _ptr(scale),
+                               sdt, _ptr(status), _stream(stream))
+    _check(rc, "kvfp8_dequant_fp4")
+    return out
+
+
+def _check_attention_fp4(query, key_cache, value_cache, key_scales, value_scales, block_tables,
+                         seq_lens, k_scale, v_scale, out, workspace, status, num_seqs, **more):
+    """The checks both 4-bit attention calls make; returns (rows, n_q, head_dim, num_blocks,
+    block_size, n_kv, scale dtype)."""
+    if query.dtype != torch.bfloat16 or query.dim() != 3 or not query.is_contiguous():
+        raise ValueError("query must be a contiguous bf16 [rows, n_q, head_dim] tensor")
+    rows, n_q, hd = query.shape
+    nb, bs, n_kv, c_hd = _check_fp4_caches(key_cache, value_cache, key_scales, value_scales)
+    if c_hd != hd:
+        raise ValueError("the caches' head_dim must be the query's")
+    _check_tables(block_tables, seq_lens, num_seqs)
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != query.shape or
+                            not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 tensor shaped like query")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    sdt = _scale_args(k_scale, v_scale)
+    _check_status(status)
+    _check_device(query=query, key_cache=key_cache, value_cache=value_cache, key_scales=key_scales,
+                  value_scales=value_scales, block_tables=block_tables, seq_lens=seq_lens,
+                  k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace, status=status,
+                  **more)
+    return rows, n_q, hd, nb, bs, n_kv, sdt
+
+
+def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, key_scales: torch.Tensor,
+                               value_scales: torch.Tensor, block_tables: torch.Tensor,
+                               seq_lens: torch.Tensor, k_scale: torch.Tensor | None = None,
+                               v_scale: torch.Tensor | None = None, sm_scale: float = 0.0,
+                               out: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None,
+                               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvfp8_paged_decode_attention_fp4: paged_decode_attention over a 4-bit cache (codes and
+    scales as reshape_and_cache_fp4 writes them); returns out (bf16 [num_seqs, n_q, hd])."""
+    num_seqs = query.shape[0] if query.dim() == 3 else 0
+    num_seqs, n_q, hd, nb, bs, n_kv, sdt = _check_attention_fp4(
+        query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
+        v_scale, out, workspace, status, num_seqs)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(query)
+        if workspace is None:
+            workspace = torch.empty(max(paged_decode_workspace_size(num_seqs, n_q, hd), 16),
+                                    dtype=torch.uint8, device=query.device)
+    rc = LIB.kvfp8_paged_decode_attention_fp4(
+        _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
+        _ptr(value_scales), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), num_seqs,
+        n_q, n_kv, hd, bs, nb, float(sm_scale), _ptr(k_scale), _ptr(v_scale), sdt, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(rc, "kvfp8_paged_decode_attention_fp4")
+    return out
+
+
+def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor,
+                              max_query_len: int, key_cache: torch.Tensor,
+                              value_cache: torch.Tensor, key_scales: torch.Tensor,
+                              value_scales: torch.Tensor, block_tables: torch.Tensor,
+                              seq_lens: torch.Tensor, k_scale: torch.Tensor | None = None,
+                              v_scale: torch.Tensor | None = None, sm_scale: float = 0.0,
+                              out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None,
+                              status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvfp8_paged_attention_multi_fp4: paged_attention_multi (causal, any chunk length) over a
+    4-bit cache."""
+    num_seqs = seq_lens.numel()
+    if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != num_seqs + 1 or \
+            not query_start_loc.is_contiguous():
+        raise ValueError("query_start_loc must be a contiguous int32 [num_seqs + 1] tensor")
+    rows, n_q, hd, nb, bs, n_kv, sdt = _check_attention_fp4(
+        query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
+        v_scale, out, workspace, status, num_seqs, query_start_loc=query_start_loc)
+    need = paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, hd, max_query_len)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(query)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = LIB.kvfp8_paged_attention_multi_fp4(
+        _ptr(out), _ptr(query), _ptr(query_start_loc), rows, max_query_len, _ptr(key_cache),
+        _ptr(value_cache), _ptr(key_scales), _ptr(value_scales), _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), num_seqs, n_q, n_kv, hd, bs, nb, float(sm_scale),
+        _ptr(k_scale), _ptr(v_scale), sdt, _ptr(workspace), ws_bytes, _ptr(status),
+        _stream(stream))
+    _check(rc, "kvfp8_paged_attention_multi_fp4")
+    return out
+
+
+def _cache_list(caches):
+    """The page calls' caches as C arrays: (pointers, bytes per block, count, num_blocks)."""
+    caches = list(caches)
+    if not 1 <= len(caches) <= MAX_CACHES:
+        raise ValueError(f"1 to {MAX_CACHES} caches")
+    for c in caches:
+        if not isinstance(c, torch.Tensor) or c.dim() < 2 or not c.is_contiguous() or \
+                c.numel() == 0 or c.shape[0] != caches[0].shape[0]:
+            raise ValueError("caches must be contiguous tensors [num_blocks, ...] of one num_blocks")
+    nb = caches[0].shape[0]
+    spans = sorted((c.data_ptr(), c.numel() * c.element_size()) for c in caches)
+    if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+        raise ValueError("caches must not overlap")
+    _check_device(**{f"caches[{i}]": c for i, c in enumerate(caches)})
+    ptrs = (ctypes.c_void_p * len(caches))(*(c.data_ptr() for c in caches))
+    sizes = (ctypes.c_int64 * len(caches))(*(c.numel() // nb * c.element_size() for c in caches))
+    return ptrs, sizes, len(caches), nb
+
+
+def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
+                status: torch.Tensor | None = None, stream=None) -> None:
+    """kvfp8_copy_blocks: in every cache, block dst_blocks[i] becomes a copy of src_blocks[i].
+
+    caches: contiguous tensors [num_blocks, ...] (the K and V caches, 4-bit scales, of any
+    layers); src_blocks/dst_blocks: int32 [num_pairs], -1 = padding.  A pair that would race
+    with another one (a destination named twice, a source that is a destination) is skipped and
+    sets DEV_BAD_BLOCK in status.
+    """
+    ptrs, sizes, count, nb = _cache_list(caches)
+    for t in (src_blocks, dst_blocks):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError("src_blocks and dst_blocks must be contiguous int32 [num_pairs] tensors")
+    if src_blocks.numel() != dst_blocks.numel():
+        raise ValueError("src_blocks and dst_blocks must have one length")
+    _check_status(status)
+    _check_device(src_blocks=src_blocks, dst_blocks=dst_blocks, status=status)
+    rc = LIB.kvfp8_copy_blocks(ptrs, sizes, count, nb, _ptr(src_blocks), _ptr(dst_blocks),
+                               src_blocks.numel(), _ptr(status), _stream(stream))
+    _check(rc, "kvfp8_copy_blocks")
+
+
+def compact_blocks_workspace_size(num_blocks: int) -> int:
+    return int(LIB.kvfp8_compact_blocks_workspace_size(num_blocks))
+
+
+def compact_blocks(caches, block_tables: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
+                   new_block_tables: torch.Tensor | None = None,
+                   num_used: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, stream=None):
+    """kvfp8_compact_blocks: the blocks that the sequences use move to the lowest ids of every
+    cache; returns (new_block_tables, num_used), the tables with the new ids and an int32 [1]
+    tensor: ids from num_used on are free.
+
+    new_block_tables may be block_tables itself.
+    """
+    ptrs, sizes, count, nb = _cache_list(caches)
+    _check_tables(block_tables, seq_lens, seq_lens.numel())
+    if new_block_tables is not None and (new_block_tables.dtype != torch.int32 or
+                                         new_block_tables.shape != block_tables.shape or
+                                         not new_block_tables.is_contiguous()):
+        raise ValueError("new_block_tables must be a contiguous int32 tensor shaped like block_tables")
+    if num_used is not None and (num_used.dtype != torch.int32 or num_used.numel() != 1):
+        raise ValueError("num_used must be an int32 [1] tensor")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_status(status)
+    _check_device(block_tables=block_tables, seq_lens=seq_lens, new_block_tables=new_block_tables,
+                  num_used=num_used, workspace=workspace, status=status)
+    with _on(stream):
+        if new_block_tables is None:
+            new_block_tables = torch.empty_like(block_tables)
+        if num_used is None:
+            num_used = torch.empty(1, dtype=torch.int32, device=block_tables.device)
+        if workspace is None:
+            workspace = torch.empty(compact_blocks_workspace_size(nb), dtype=torch.uint8,
+                                    device=block_tables.device)
+    rc = LIB.kvfp8_compact_blocks(
+        ptrs, sizes, count, nb, block_size, _ptr(block_tables), block_tables.shape[1],
+        _ptr(seq_lens), seq_lens.numel(), _ptr(new_block_tables), _ptr(num_used), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(rc, "kvfp8_compact_blocks")
+    return new_block_tables, num_used

@@ -1,0 +1,374 @@
+// The 4-bit paged cache's writer and its rows read back, sm_103a.
+//
+// A group of 16 dims of a token's kv head is stored as 16 E2M1 codes and one E4M3 scale byte B;
+// with the layer's scalar s the value of a dim is code * (B * s).  Writing a group:
+//   a = max |x|,  B = E4M3((a / |s|) / 6),  d = B * |s|,  code = sign, E2M1(|x| / d)
+// every quotient and product a float rounded to nearest even (the header gives the corner
+// cases).  Both kernels are HBM streams: the writer reads 2 (bf16) or 4 bytes per element and
+// writes 0.5625, the reader the reverse.
+//
+// One lane takes one group: its 16 source elements are 32 contiguous bytes of bf16 (one load),
+// the codes one 8-byte store, and the maximum needs no exchange between lanes.  A row is spread
+// over lanes_per_row lanes (a power of two, at most 32), so short rows share a warp; longer rows
+// are cut into passes of 32 groups along gridDim.y.  gridDim.z is the side (K or V), so a warp
+// has one layer scale.  Warps stride over the rows and hold the next row's elements, and the
+// slot after it, while they convert the present one.
+//
+// The quotient |x| / d has to be the float quotient, because halfway cases are common (a bf16 x
+// over a d of few bits) and decide the code.  It takes the reciprocal-and-two-residuals divide
+// of the 8-bit writer (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. R&D 34(1), 1990), in packed pairs; groups whose scale saturates
+// or whose d is outside [2^-60, 2^60] divide element by element.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kvfp8_device.cuh"
+#include "kvfp8_internal.h"
+
+namespace kvfp8 {
+namespace {
+
+constexpr int kWarps = 8;  // per CTA
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// maxima that a NaN operand turns into NaN
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void ld_v8(const uint8_t *p, uint32_t *w) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void ld_v4(const uint8_t *p, uint32_t *w) {
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+}
+__device__ __forceinline__ void st_v8(uint8_t *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// Sixteen elements of a source row as they lie in memory.
+template <bool kF32>
+struct Group16 {
+    static constexpr int kWords = kF32 ? 16 : 8;
+    uint32_t w[kWords];
+    // kWide: 32-byte loads (p 32-byte aligned), else 16-byte ones
+    template <bool kWide>
+    __device__ __forceinline__ void load(const uint8_t *p) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 8) {
+            if (kWide) {
+                ld_v8(p + 4 * i, w + i);
+            } else {
+                ld_v4(p + 4 * i, w + i);
+                ld_v4(p + 4 * i + 16, w + i + 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&x)[16]) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if (kF32) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                x[2 * i] = bf16lo(w[i]);
+                x[2 * i + 1] = bf16hi(w[i]);
+            }
+        }
+    }
+    // max |x|, NaN if any element is
+    __device__ __forceinline__ float amax() const {
+        if (kF32) {
+            float m = fabsf(__uint_as_float(w[0]));
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) m = max_nan(m, fabsf(__uint_as_float(w[i])));
+            return m;
+        }
+        uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < kWords; ++i) m = max_nan_bf16x2(m, w[i] & 0x7FFF7FFFu);
+        return max_nan(bf16lo(m), bf16hi(m));
+    }
+};
+
+// the magnitudes of a group whose scale saturated or whose d is out of the fast range
+__device__ __noinline__ uint2 quantize_slow(const float (&x)[16], float d) {
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float ax = fabsf(x[i]);
+        const float m = isinf(ax) ? 6.f : d == 0.f ? 0.f : __fdiv_rn(ax, d);
+        q[i] = x[i] < 0.f ? -m : m;
+    }
+    return make_uint2(e2m1x8_from_f32(q), e2m1x8_from_f32(q + 8));
+}
+
+// Sixteen elements -> their codes and the group's scale byte.  sa = |s|, neg = 0x88888888 when
+// s < 0.
+template <bool kF32>
+__device__ __forceinline__ uint2 quantize16(const Group16<kF32> &g, float sa, uint32_t neg, uint32_t &byte) {
+    const float a = g.amax();
+    if (isnan(a)) {
+        byte = 0x7Fu;
+        return make_uint2(0u, 0u);
+    }
+    byte = e4m3x2_from_f32(__fdiv_rn(__fdiv_rn(a, sa), 6.f), 0.f) & 0xFFu;
+    const float B = __half2float(__ushort_as_half(static_cast<uint16_t>(f16x2_from_e4m3x2(byte) & 0xFFFFu)));
+    const float d = __fmul_rn(B, sa);
+    float x[16];
+    g.unpack(x);
+    uint2 c;
+    if (__builtin_expect(byte == 0x7Eu || (d != 0.f && !(d >= 0x1p-60f && d <= 0x1p60f)), 0)) {
+        c = quantize_slow(x, d);
+    } else {
+        // q0 = x*y, then two residual steps q += (x - q*d)*y.  d = 0 takes y = 0, which gives
+        // zeros with the sign of x; x = -0 gives +0.
+        const float y = d == 0.f ? 0.f : __frcp_rn(d);
+        const uint64_t y2 = pack2(y, y), nd2 = pack2(-d, -d);
+        float q[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const uint64_t v = pack2(x[i], x[i + 1]);
+            const uint64_t q0 = mul2(v, y2);
+            const uint64_t q1 = fma2(fma2(q0, nd2, v), y2, q0);
+            unpack2(fma2(fma2(q1, nd2, v), y2, q1), q[i], q[i + 1]);
+        }
+        c = make_uint2(e2m1x8_from_f32(q), e2m1x8_from_f32(q + 8));
+    }
+    return make_uint2(c.x ^ neg, c.y ^ neg);
+}
+
+// How rows map to lanes: gpr groups a row over 1 << lpr_log2 lanes.
+struct RowMap {
+    int32_t gpr, lpr_log2;
+    int32_t gph_log2;    // log2 of the groups of a kv head
+    int32_t bs_log2;
+};
+
+// Scale byte of group g of the row at `slot`.
+__device__ __forceinline__ int64_t scale_index(const RowMap &m, int n_kv, int64_t slot, int g) {
+    const int64_t blk = slot >> m.bs_log2, off = slot & ((1 << m.bs_log2) - 1);
+    const int64_t head = g >> m.gph_log2;
+    return ((((blk * n_kv + head) << m.bs_log2) + off) << m.gph_log2) + (g & ((1 << m.gph_log2) - 1));
+}
+
+template <bool kF32, bool kWide>
+__global__ void __launch_bounds__(32 * kWarps)
+write_fp4_kernel(const Fp4WriteArgs a, const RowMap m) {
+    const int lane = threadIdx.x & 31, side = blockIdx.z;
+    const float s0 = load_scale(a.scale[0], a.scale_dtype), s1 = load_scale(a.scale[1], a.scale_dtype);
+    if (!scale_ok(s0) || !scale_ok(s1)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && side == 0 && threadIdx.x == 0)
+            flag(a.status, KVFP8_DEV_BAD_SCALE);
+        return;
+    }
+    const float s = side == 0 ? s0 : s1, sa = fabsf(s);
+    const uint32_t neg = signbit(s) ? 0x88888888u : 0u;
+    const int g = (blockIdx.y << 5) + (lane & ((1 << m.lpr_log2) - 1));
+    const bool there = g < m.gpr;  // this lane's group exists
+    const int64_t rpw = 32 >> m.lpr_log2;  // rows a warp takes at a time
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * rpw;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * rpw + (lane >> m.lpr_log2);
+    constexpr int kEsz = kF32 ? 4 : 2;
+    const uint8_t *src = static_cast<const uint8_t *>(a.src[side]) + static_cast<int64_t>(g) * 16 * kEsz;
+    const int64_t stride = a.stride[side] * kEsz;
+    const int64_t row_codes = static_cast<int64_t>(m.gpr) * 8;
+
+    auto slot_of = [&](int64_t i) { return i < a.num_tokens ? __ldg(a.slot_mapping + i) : int64_t{-1}; };
+    // a row is written when its slot is in range; -1 is padding, anything else is flagged
+    auto usable = [&](int64_t i, int64_t slot) {
+        if (slot >= 0 && slot < a.num_slots) return there;
+        if (slot != -1 && g == 0 && side == 0 && i < a.num_tokens) flag(a.status, KVFP8_DEV_BAD_SLOT);
+        return false;
+    };
+    int64_t slot = slot_of(t), slot_next = slot_of(t + step);
+    bool ok = usable(t, slot);
+    Group16<kF32> cur, nxt;
+    if (ok) cur.template load<kWide>(src + t * stride);
+    for (; t < a.num_tokens; t += step) {
+        const int64_t slot_after = slot_of(t + 2 * step);
+        const bool ok_next = usable(t + step, slot_next);
+        if (ok_next) nxt.template load<kWide>(src + (t + step) * stride);
+        if (ok) {
+            uint32_t byte;
+            const uint2 c = quantize16<kF32>(cur, sa, neg, byte);
+            *reinterpret_cast<uint2 *>(a.codes[side] + slot * row_codes + g * 8) = c;
+            a.scales[side][scale_index(m, a.n_kv, slot, g)] = static_cast<uint8_t>(byte);
+        }
+        cur = nxt;
+        ok = ok_next;
+        slot = slot_next;
+        slot_next = slot_after;
+    }
+}
+
+// Rows by slot, dequantized: the reader of the layout above.
+template <bool kBF16Out>
+__global__ void __launch_bounds__(32 * kWarps)
+read_fp4_kernel(const Fp4ReadArgs a, const RowMap m, const int32_t wide) {
+    const int lane = threadIdx.x & 31;
+    const float s = load_scale(a.scale, a.scale_dtype);
+    if (!scale_ok(s)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
+        return;
+    }
+    const int g = (blockIdx.y << 5) + (lane & ((1 << m.lpr_log2) - 1));
+    if (g >= m.gpr) return;
+    const int64_t rpw = 32 >> m.lpr_log2;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * rpw;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * rpw + (lane >> m.lpr_log2);
+    const int64_t row_codes = static_cast<int64_t>(m.gpr) * 8;
+    constexpr int kBytes = 16 * (kBF16Out ? 2 : 4);
+    uint8_t *dst = static_cast<uint8_t *>(a.dst) + static_cast<int64_t>(g) * kBytes;
+    const int64_t row_bytes = static_cast<int64_t>(m.gpr) * kBytes;
+
+    auto slot_of = [&](int64_t i) { return i < a.num_tokens ? __ldg(a.slot_mapping + i) : int64_t{-1}; };
+    int64_t slot = slot_of(t), slot_next = slot_of(t + step);
+    // the group's codes and scale; a row without a slot reads as zeros
+    auto fetch = [&](int64_t i, int64_t sl, uint2 &c, uint32_t &b) {
+        c = make_uint2(0u, 0u);
+        b = 0u;
+        if (sl >= 0 && sl < a.num_slots) {
+            c = __ldg(reinterpret_cast<const uint2 *>(a.codes + sl * row_codes + g * 8));
+            b = __ldg(a.scales + scale_index(m, a.n_kv, sl, g));
+        } else if (sl != -1 && g == 0 && i < a.num_tokens) {
+            flag(a.status, KVFP8_DEV_BAD_SLOT);
+        }
+    };
+    uint2 c, c_next;
+    uint32_t b, b_next;
+    fetch(t, slot, c, b);
+    for (; t < a.num_tokens; t += step) {
+        const int64_t slot_after = slot_of(t + 2 * step);
+        fetch(t + step, slot_next, c_next, b_next);
+        const float B = __half2float(__ushort_as_half(static_cast<uint16_t>(f16x2_from_e4m3x2(b) & 0xFFFFu)));
+        const float d = __fmul_rn(B, s);
+        uint32_t h[8], o[16];
+        f16x2_from_e2m1x8(c.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+        f16x2_from_e2m1x8(c.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+            const float lo = __fmul_rn(v.x, d), hi = __fmul_rn(v.y, d);
+            if (kBF16Out) {
+                o[i] = bf16x2_from_f32(lo, hi);
+            } else {
+                o[2 * i] = __float_as_uint(lo);
+                o[2 * i + 1] = __float_as_uint(hi);
+            }
+        }
+        uint8_t *p = dst + t * row_bytes;
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; i += 8) {
+            if (wide) {
+                st_v8(p + 4 * i, o + i);
+            } else {
+                *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                *reinterpret_cast<uint4 *>(p + 4 * i + 16) = make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+            }
+        }
+        c = c_next;
+        b = b_next;
+        slot_next = slot_after;
+    }
+}
+
+int log2_of(int32_t x) {  // of a power of two
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+RowMap row_map(int32_t n_kv, int32_t head_dim, int32_t block_size) {
+    RowMap m;
+    m.gpr = n_kv * (head_dim / 16);
+    m.lpr_log2 = 0;
+    while (m.lpr_log2 < 5 && (1 << m.lpr_log2) < m.gpr) ++m.lpr_log2;
+    m.gph_log2 = log2_of(head_dim / 16);
+    m.bs_log2 = log2_of(block_size);
+    return m;
+}
+
+// CTAs along x: one wave of resident warps over all passes and sides, fewer for few rows
+int rows_grid(int64_t tokens, const RowMap &m, int sms, int occ, int planes) {
+    const int64_t rows_per_cta = static_cast<int64_t>(kWarps) * (32 >> m.lpr_log2);
+    const int64_t want = (tokens + rows_per_cta - 1) / rows_per_cta;
+    const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(sms) * occ / planes);
+    return static_cast<int>(std::min(want, wave));
+}
+
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+template <bool kF32, bool kWide>
+cudaError_t run_write(const Fp4WriteArgs &a, const RowMap &m, cudaStream_t stream) {
+    DeviceFacts f;
+    cudaError_t err = device_facts(&f);
+    if (err != cudaSuccess) return err;
+    auto kern = write_fp4_kernel<kF32, kWide>;
+    int occ = 0;
+    if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
+    const int passes = (m.gpr + 31) / 32;
+    const dim3 grid(rows_grid(a.num_tokens, m, f.sms, std::max(occ, 1), 2 * passes), passes, 2);
+    kern<<<grid, 32 * kWarps, 0, stream>>>(a, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_reshape_and_cache_fp4(const Fp4WriteArgs &a, cudaStream_t stream) {
+    const RowMap m = row_map(a.n_kv, a.head_dim, a.block_size);
+    const int esz = a.src_dtype == KVFP8_F32 ? 4 : 2;
+    const bool wide = aligned32(a.src[0]) && aligned32(a.src[1]) && a.stride[0] * esz % 32 == 0 &&
+                      a.stride[1] * esz % 32 == 0;
+    if (a.src_dtype == KVFP8_F32)
+        return wide ? run_write<true, true>(a, m, stream) : run_write<true, false>(a, m, stream);
+    return wide ? run_write<false, true>(a, m, stream) : run_write<false, false>(a, m, stream);
+}
+
+cudaError_t launch_dequant_fp4(const Fp4ReadArgs &a, cudaStream_t stream) {
+    DeviceFacts f;
+    cudaError_t err = device_facts(&f);
+    if (err != cudaSuccess) return err;
+    const RowMap m = row_map(a.n_kv, a.head_dim, a.block_size);
+    const int passes = (m.gpr + 31) / 32;
+    const bool bf16 = a.dst_dtype == KVFP8_BF16;
+    auto kern = bf16 ? read_fp4_kernel<true> : read_fp4_kernel<false>;
+    int occ = 0;
+    if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
+    const dim3 grid(rows_grid(a.num_tokens, m, f.sms, std::max(occ, 1), passes), passes);
+    kern<<<grid, 32 * kWarps, 0, stream>>>(a, m, aligned32(a.dst) ? 1 : 0);
+    return cudaGetLastError();
+}
+
+}  // namespace kvfp8

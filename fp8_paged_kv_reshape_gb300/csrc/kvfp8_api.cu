@@ -27,6 +27,34 @@ bool block_size_ok_for_decode(int32_t bs) {
     return bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs == 128 || bs == 256;
 }
 
+// the 4-bit cache's shape rules, shared by its entry points
+kvfp8_status check_fp4_cache(int32_t num_blocks, int32_t block_size, int32_t n_kv, int32_t head_dim) {
+    if (num_blocks < 1 || n_kv < 1 || !block_size_ok_for_decode(block_size) ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return KVFP8_ERR_SHAPE;
+    // tensor-map extents and row indices are 32 bits
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7FFFFFFFLL ||
+        static_cast<int64_t>(num_blocks) * n_kv > 0x7FFFFFFFLL || n_kv > (1 << 20))
+        return KVFP8_ERR_SHAPE;
+    return KVFP8_OK;
+}
+
+// the cache list of the page calls: KVFP8_OK with *out filled, or what is wrong with it
+kvfp8_status make_cache_list(void *const *caches, const int64_t *block_bytes, int32_t num_caches,
+                             int32_t num_blocks, kvfp8::CacheList *out) {
+    if (num_caches < 1 || num_caches > KVFP8_MAX_CACHES || num_blocks < 1) return KVFP8_ERR_SHAPE;
+    if (!caches || !block_bytes) return KVFP8_ERR_NULL;
+    for (int32_t c = 0; c < num_caches; ++c) {
+        if (block_bytes[c] < 1 || block_bytes[c] > (int64_t{1} << 40)) return KVFP8_ERR_SHAPE;
+        if (!caches[c]) return KVFP8_ERR_NULL;
+        if (!aligned16(caches[c]) || block_bytes[c] % 16 != 0) return KVFP8_ERR_ALIGN;
+        out->ptr[c] = static_cast<uint8_t *>(caches[c]);
+        out->block_bytes[c] = block_bytes[c];
+    }
+    out->count = num_caches;
+    return KVFP8_OK;
+}
+
 }  // namespace
 
 namespace kvfp8 {
@@ -488,6 +516,237 @@ kvfp8_status kvfp8_dequant(void *dst, kvfp8_dtype dst_dtype, const uint8_t *src,
     if (!aligned16(dst) || !aligned16(src)) return KVFP8_ERR_ALIGN;
     return from_cuda(kvfp8::launch_dequant(dst, dst_dtype, src, n, scale, scale_dtype,
                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_reshape_and_cache_fp4(
+    const void *key, const void *value, kvfp8_dtype src_dtype, int64_t key_stride,
+    int64_t value_stride, int64_t num_tokens, uint8_t *key_cache, uint8_t *value_cache,
+    uint8_t *key_scales, uint8_t *value_scales, int32_t num_blocks, int32_t block_size,
+    int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping, const void *k_scale,
+    const void *v_scale, kvfp8_dtype scale_dtype, uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(src_dtype) || !dtype_ok(scale_dtype)) return KVFP8_ERR_DTYPE;
+    if (num_tokens < 0) return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
+    if (sh != KVFP8_OK) return sh;
+    const int64_t row = static_cast<int64_t>(n_kv) * head_dim;
+    if (row > (1 << 20) || key_stride < row || value_stride < row) return KVFP8_ERR_SHAPE;
+    if (num_tokens == 0) return KVFP8_OK;
+    if (!key || !value || !key_cache || !value_cache || !key_scales || !value_scales ||
+        !slot_mapping)
+        return KVFP8_ERR_NULL;
+    const int64_t esz = src_dtype == KVFP8_F32 ? 4 : 2;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        !aligned16(key_scales) || !aligned16(value_scales) || (key_stride * esz) % 16 != 0 ||
+        (value_stride * esz) % 16 != 0 || !aligned(slot_mapping, 8))
+        return KVFP8_ERR_ALIGN;
+    kvfp8::Fp4WriteArgs a;
+    a.src[0] = key;
+    a.src[1] = value;
+    a.stride[0] = key_stride;
+    a.stride[1] = value_stride;
+    a.codes[0] = key_cache;
+    a.codes[1] = value_cache;
+    a.scales[0] = key_scales;
+    a.scales[1] = value_scales;
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.src_dtype = src_dtype;
+    a.scale_dtype = scale_dtype;
+    a.num_tokens = num_tokens;
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.block_size = block_size;
+    a.n_kv = n_kv;
+    a.head_dim = head_dim;
+    a.slot_mapping = slot_mapping;
+    a.status = status;
+    return from_cuda(kvfp8::launch_reshape_and_cache_fp4(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const uint8_t *codes,
+                               const uint8_t *scales, int32_t num_blocks, int32_t block_size,
+                               int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping,
+                               int64_t num_tokens, const void *scale, kvfp8_dtype scale_dtype,
+                               uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(dst_dtype) || !dtype_ok(scale_dtype)) return KVFP8_ERR_DTYPE;
+    if (num_tokens < 0) return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
+    if (sh != KVFP8_OK) return sh;
+    if (static_cast<int64_t>(n_kv) * head_dim > (1 << 20)) return KVFP8_ERR_SHAPE;
+    if (num_tokens == 0) return KVFP8_OK;
+    if (!dst || !codes || !scales || !slot_mapping) return KVFP8_ERR_NULL;
+    if (!aligned16(dst) || !aligned16(codes) || !aligned16(scales) || !aligned(slot_mapping, 8))
+        return KVFP8_ERR_ALIGN;
+    kvfp8::Fp4ReadArgs a;
+    a.dst = dst;
+    a.dst_dtype = dst_dtype;
+    a.scale_dtype = scale_dtype;
+    a.codes = codes;
+    a.scales = scales;
+    a.scale = scale;
+    a.num_tokens = num_tokens;
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.block_size = block_size;
+    a.n_kv = n_kv;
+    a.head_dim = head_dim;
+    a.slot_mapping = slot_mapping;
+    a.status = status;
+    return from_cuda(kvfp8::launch_dequant_fp4(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_paged_decode_attention_fp4(
+    void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
+    const uint8_t *key_scales, const uint8_t *value_scales, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, int32_t n_q,
+    int32_t n_kv, int32_t head_dim, int32_t block_size, int32_t num_blocks, float sm_scale,
+    const void *k_scale, const void *v_scale, kvfp8_dtype scale_dtype, void *workspace,
+    size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream) {
+    bool nothing_to_do = false;
+    const kvfp8_status v = kvfp8::validate_decode(
+        out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+        n_q, n_kv, head_dim, block_size, num_blocks, sm_scale, scale_dtype, &nothing_to_do);
+    if (v != KVFP8_OK || nothing_to_do) return v;
+    const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
+    if (sh != KVFP8_OK) return sh;
+    if (!key_scales || !value_scales || !workspace) return KVFP8_ERR_NULL;
+    if (!aligned16(key_scales) || !aligned16(value_scales) || !aligned16(workspace))
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes < kvfp8_paged_decode_workspace_size(num_seqs, n_q, head_dim))
+        return KVFP8_ERR_WORKSPACE;
+    kvfp8::DecodeArgs d;
+    d.out = out;
+    d.query = query;
+    d.key_cache = key_cache;
+    d.value_cache = value_cache;
+    d.key_scales = key_scales;
+    d.value_scales = value_scales;
+    d.block_tables = block_tables;
+    d.max_blocks_per_seq = max_blocks_per_seq;
+    d.seq_lens = seq_lens;
+    d.num_seqs = num_seqs;
+    d.n_q = n_q;
+    d.n_kv = n_kv;
+    d.head_dim = head_dim;
+    d.block_size = block_size;
+    d.num_blocks = num_blocks;
+    d.sm_scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+    d.k_scale = k_scale;
+    d.v_scale = v_scale;
+    d.scale_dtype = scale_dtype;
+    d.workspace = workspace;
+    d.status = status;
+    d.qsl = nullptr;
+    d.qmax = 1;
+    d.qrows = num_seqs;
+    d.k_bf16 = 0;
+    d.v_bf16 = 0;
+    return from_cuda(kvfp8::launch_paged_decode_fp4(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_paged_attention_multi_fp4(
+    void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,
+    int32_t max_query_len, const uint8_t *key_cache, const uint8_t *value_cache,
+    const uint8_t *key_scales, const uint8_t *value_scales, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, int32_t n_q,
+    int32_t n_kv, int32_t head_dim, int32_t block_size, int32_t num_blocks, float sm_scale,
+    const void *k_scale, const void *v_scale, kvfp8_dtype scale_dtype, void *workspace,
+    size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(scale_dtype)) return KVFP8_ERR_DTYPE;
+    if (num_seqs < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || max_query_len < 1 ||
+        num_query_rows < 0 || max_blocks_per_seq < 1)
+        return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
+    if (sh != KVFP8_OK) return sh;
+    const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
+    if (!split_kv && (n_q / n_kv > 128 ||
+                      (static_cast<int64_t>(max_query_len) * (n_q / n_kv) + 127) / 128 * n_kv *
+                              num_seqs > 0x7FFFFFFFLL))
+        return KVFP8_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
+    if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
+    if (num_seqs == 0) return KVFP8_OK;
+    if (!out || !query || !query_start_loc || !key_cache || !value_cache || !key_scales ||
+        !value_scales || !block_tables || !seq_lens || (split_kv && !workspace))
+        return KVFP8_ERR_NULL;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) ||
+        !aligned16(value_cache) || !aligned16(key_scales) || !aligned16(value_scales) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) ||
+        (split_kv && !aligned16(workspace)))
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes <
+        kvfp8_paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len))
+        return KVFP8_ERR_WORKSPACE;
+    kvfp8::DecodeArgs d;
+    d.out = out;
+    d.query = query;
+    d.key_cache = key_cache;
+    d.value_cache = value_cache;
+    d.key_scales = key_scales;
+    d.value_scales = value_scales;
+    d.block_tables = block_tables;
+    d.max_blocks_per_seq = max_blocks_per_seq;
+    d.seq_lens = seq_lens;
+    d.num_seqs = num_seqs;
+    d.n_q = n_q;
+    d.n_kv = n_kv;
+    d.head_dim = head_dim;
+    d.block_size = block_size;
+    d.num_blocks = num_blocks;
+    d.sm_scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+    d.k_scale = k_scale;
+    d.v_scale = v_scale;
+    d.scale_dtype = scale_dtype;
+    d.workspace = workspace;
+    d.status = status;
+    d.qsl = query_start_loc;
+    d.qmax = max_query_len;
+    d.qrows = num_query_rows;
+    d.k_bf16 = 0;
+    d.v_bf16 = 0;
+    return from_cuda(kvfp8::launch_paged_decode_fp4(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_copy_blocks(void *const *caches, const int64_t *block_bytes, int32_t num_caches,
+                               int32_t num_blocks, const int32_t *src_blocks,
+                               const int32_t *dst_blocks, int64_t num_pairs, uint32_t *status,
+                               kvfp8_stream_t stream) {
+    kvfp8::CacheList list;
+    const kvfp8_status v = make_cache_list(caches, block_bytes, num_caches, num_blocks, &list);
+    if (v != KVFP8_OK) return v;
+    if (num_pairs < 0 || num_pairs > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
+    if (num_pairs == 0) return KVFP8_OK;
+    if (!src_blocks || !dst_blocks) return KVFP8_ERR_NULL;
+    if (!aligned(src_blocks, 4) || !aligned(dst_blocks, 4)) return KVFP8_ERR_ALIGN;
+    return from_cuda(kvfp8::launch_copy_blocks(list, num_blocks, src_blocks, dst_blocks,
+                                               static_cast<int32_t>(num_pairs), status,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvfp8_compact_blocks_workspace_size(int32_t num_blocks) {
+    return num_blocks < 1 ? 0 : kvfp8::compact_workspace_size(num_blocks);
+}
+
+kvfp8_status kvfp8_compact_blocks(void *const *caches, const int64_t *block_bytes,
+                                  int32_t num_caches, int32_t num_blocks, int32_t block_size,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *seq_lens, int32_t num_seqs,
+                                  int32_t *new_block_tables, int32_t *num_used, void *workspace,
+                                  size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream) {
+    kvfp8::CacheList list;
+    const kvfp8_status v = make_cache_list(caches, block_bytes, num_caches, num_blocks, &list);
+    if (v != KVFP8_OK) return v;
+    if (block_size < 1 || num_seqs < 0 || max_blocks_per_seq < 1 ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL)
+        return KVFP8_ERR_SHAPE;
+    if (!num_used || !workspace ||
+        (num_seqs > 0 && (!block_tables || !seq_lens || !new_block_tables)))
+        return KVFP8_ERR_NULL;
+    if (!aligned16(workspace) || !aligned(num_used, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4) || !aligned(new_block_tables, 4))
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes < kvfp8::compact_workspace_size(num_blocks)) return KVFP8_ERR_WORKSPACE;
+    return from_cuda(kvfp8::launch_compact_blocks(
+        list, num_blocks, block_size, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+        new_block_tables, num_used, workspace, status, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvfp8_status kvfp8_check_scale_host(float s) {

@@ -154,6 +154,9 @@ struct DecodeArgs {
     // mixed cache dtypes: 1 = that side's cache is bf16 (2 bytes per element, no scale)
     int32_t k_bf16;
     int32_t v_bf16;
+    // 4-bit cache (both sides): the groups' scale bytes; nullptr for the other formats
+    const uint8_t *key_scales = nullptr;
+    const uint8_t *value_scales = nullptr;
 };
 
 // Workspace layout, shared by the size query and the launcher; rows = query rows per
@@ -171,6 +174,10 @@ cudaError_t launch_paged_decode_mixed(const DecodeArgs &a, cudaStream_t stream);
 // True when the split-KV kernel has a mixed-dtype instance for this shape (up to 16 score
 // columns per kv head, 8 at head_dim 256); the tensor-core kernel has none.
 bool mixed_uses_decode_kernel(int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t max_query_len);
+
+// The split-KV kernel over the 4-bit cache (key_scales / value_scales set), for shapes
+// multi_uses_decode_kernel accepts; longer query chunks take launch_prefill_attention.
+cudaError_t launch_paged_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
 
 // Multi-query (causal) attention on the tensor cores (tcgen05): long query chunks, or kv-head
 // counts the split-KV decode kernel does not cover.  Needs no workspace.
@@ -198,6 +205,50 @@ kvfp8_status launch_decode_validated(void *out, const void *query, const uint8_t
                                      float sm_scale, const void *k_scale, const void *v_scale,
                                      int scale_dtype, void *workspace, uint32_t *status,
                                      kvfp8_stream_t stream);
+
+// The 4-bit cache's writer and its rows read back by slot.
+struct Fp4WriteArgs {
+    const void *src[2];      // K, V
+    int64_t stride[2];       // elements
+    uint8_t *codes[2];
+    uint8_t *scales[2];
+    const void *scale[2];    // layer scalars, nullptr = 1
+    int src_dtype, scale_dtype;
+    int64_t num_tokens, num_slots;
+    int32_t block_size, n_kv, head_dim;
+    const int64_t *slot_mapping;
+    uint32_t *status;
+};
+cudaError_t launch_reshape_and_cache_fp4(const Fp4WriteArgs &a, cudaStream_t stream);
+
+struct Fp4ReadArgs {
+    void *dst;
+    int dst_dtype, scale_dtype;
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const void *scale;
+    int64_t num_tokens, num_slots;
+    int32_t block_size, n_kv, head_dim;
+    const int64_t *slot_mapping;
+    uint32_t *status;
+};
+cudaError_t launch_dequant_fp4(const Fp4ReadArgs &a, cudaStream_t stream);
+
+// Page copies: the caches' device pointers and block sizes travel as a kernel parameter.
+struct CacheList {
+    uint8_t *ptr[KVFP8_MAX_CACHES];
+    int64_t block_bytes[KVFP8_MAX_CACHES];  // multiples of 16
+    int32_t count;
+};
+cudaError_t launch_copy_blocks(const CacheList &caches, int32_t num_blocks, const int32_t *src,
+                               const int32_t *dst, int32_t num_pairs, uint32_t *status,
+                               cudaStream_t stream);
+size_t compact_workspace_size(int32_t num_blocks);
+cudaError_t launch_compact_blocks(const CacheList &caches, int32_t num_blocks, int32_t block_size,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *seq_lens, int32_t num_seqs,
+                                  int32_t *new_block_tables, int32_t *num_used, void *workspace,
+                                  uint32_t *status, cudaStream_t stream);
 
 cudaError_t launch_dequant(void *dst, int dst_dtype, const uint8_t *src, int64_t n,
                            const void *scale, int scale_dtype, cudaStream_t stream);

@@ -234,7 +234,7 @@ __device__ __forceinline__ float ex2(float x) {
 // TMA wrote with SEG-byte swizzle (box base aligned to the swizzle span).
 template <int SEG>
 __device__ __forceinline__ uint32_t swz(int row, int cc) {
-    const int x = (SEG == 128) ? (row & 7) : ((row >> 1) & 3);
+    const int x = SEG == 128 ? (row & 7) : SEG == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1);
     return static_cast<uint32_t>(row * SEG + ((cc ^ x) << 4));
 }
 
@@ -266,7 +266,7 @@ struct PartMerge {
     }
     // four bf16 outputs: scale * acc / den (zeros when no part saw a token)
     __device__ __forceinline__ uint2 result(float scale) const {
-        const float inv = den > 0.f ? scale / den : 0.f;
+        const float inv = den == 0.f ? 0.f : scale / den;  // (a NaN part stays NaN)
         return make_uint2(bf16x2_from_f32(acc.x * inv, acc.y * inv),
                           bf16x2_from_f32(acc.z * inv, acc.w * inv));
     }
@@ -483,12 +483,12 @@ __global__ void __launch_bounds__(256 * kCombineSlices) combine_kernel(const Ker
     sm_acc[slice][t] = mg.acc;
     __syncthreads();
     if (slice != 0 || !valid) return;
-    // merge the slices' running states (a slice that saw no part has M = -inf, den = 0)
+    // merge the slices' running states (a slice that saw no part has den = 0)
     PartMerge all;
 #pragma unroll
     for (int sl = 0; sl < kCombineSlices; ++sl) {
         const float m = sm_m[sl][t];
-        if (m == -INFINITY) continue;
+        if (sm_den[sl][t] == 0.f) continue;
         if (m > all.M) {
             const float r = ex2(all.M - m);  // 0 while all.M is still -inf
             all.den *= r;
@@ -1121,6 +1121,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
+// the swizzle whose span is one box row of seg bytes (128, 64 or 32)
+CUtensorMapSwizzle swizzle_of(int seg) {
+    return seg == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+           : seg == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                       : CU_TENSOR_MAP_SWIZZLE_32B;
+}
+
 // The cache as a 3-D byte tensor (SEG bytes, n_kv*head_dim/SEG segments, rows) read in
 // [box_rows x SEG] boxes with SEG-byte swizzle.
 cudaError_t encode_cache_map(CUtensorMap *map, const uint8_t *cache, int64_t rows, int row_bytes,
@@ -1136,8 +1143,8 @@ cudaError_t encode_cache_map(CUtensorMap *map, const uint8_t *cache, int64_t row
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(cache),
                            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           swizzle_of(seg), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1161,8 +1168,8 @@ cudaError_t encode_cache_map_whole(CUtensorMap *map, const uint8_t *cache, int64
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(cache),
                            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           swizzle_of(seg), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -229,7 +229,79 @@ struct PrefillArgs {
     uint32_t *status;
     int32_t box_rows;
     int32_t row_tiles;  // tiles of 128 score rows per (sequence, kv head)
+    const uint8_t *key_scales, *value_scales;  // 4-bit cache: the groups' scale bytes
 };
+
+// ---------------------------------------------------------------- the 4-bit cache
+//
+// F4: the cache holds E2M1 codes with an E4M3 scale byte per 16 dims instead of E4M3 bytes.  Only
+// what fills the f16 operands differs: a stage holds the codes of its keys (boxes of one head's
+// head_dim/2-byte rows) and their scale bytes (contiguous per block and head, fetched by bulk
+// copies), and the conversion multiplies each fp16 pair of codes by its group's scale (exact:
+// code * scale is an fp16 number).
+//
+// NaN: a scale byte 0x7F makes its 16 dims NaN.  In K that makes the key's scores NaN, which the
+// masks keep from rows that do not see it.  In V it would reach every row of the tile (0 * NaN), so
+// such scales are taken as 0, the CTA remembers that it met one, and at the end each of its rows
+// looks up which groups of the values it sees are NaN (a slow scan that no finite cache runs).
+
+__device__ __forceinline__ bool is_nan_byte(uint32_t b) { return (b & 0x7Fu) == 0x7Fu; }
+
+// the fp16 pair (s, s) of an E4M3 byte
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    return __byte_perm(f16x2_from_e4m3x2(byte), 0u, 0x1010);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// eight codes times a scale pair
+__device__ __forceinline__ uint4 dequant8(uint32_t codes, uint32_t scale) {
+    uint32_t h[4];
+    f16x2_from_e2m1x8(codes, h);
+    return make_uint4(mul_f16x2(h[0], scale), mul_f16x2(h[1], scale), mul_f16x2(h[2], scale),
+                      mul_f16x2(h[3], scale));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The two scale bytes of a V key's 32 dims (0 for a key that is not valid; a NaN byte is taken
+// as 0 and remembered).
+__device__ __forceinline__ uint32_t value_scales_of(const uint8_t *p, bool valid, volatile int32_t *nan_seen) {
+    uint32_t b = *reinterpret_cast<const uint16_t *>(p);
+    if (!valid) return 0u;
+    const uint32_t n = nan_byte_mask(b);
+    if (n != 0u) {
+        b &= ~n;
+        *nan_seen = 1;
+    }
+    return b;
+}
+
+// The groups (bit g: dims 16g..16g+15) in which some value of tokens 0..last of the sequence is
+// NaN; blocks out of range hold no tokens.
+template <int HD>
+__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq, int kvh, int last) {
+    const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+    uint32_t groups = 0;
+    for (int t = 0; t <= last; ++t) {
+        const int32_t blk = bt[t / a.block_size];
+        if (blk < 0 || blk >= a.num_blocks) continue;
+        const uint8_t *row = a.value_scales +
+                             ((static_cast<int64_t>(blk) * a.n_kv + kvh) * a.block_size + t % a.block_size) * (HD / 16);
+        for (int g = 0; g < HD / 16; ++g)
+            if (is_nan_byte(row[g])) groups |= 1u << g;
+    }
+    return groups;
+}
+// bf16 pair of dims d, d+1, NaN where the pair's group is in `groups`
+__device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t groups, int d) {
+    return (groups >> (d >> 4)) & 1u ? 0x7FFF7FFFu : w;
+}
 
 // ---------------------------------------------------------------- work order
 //
@@ -338,10 +410,11 @@ __device__ __forceinline__ int seq_of_rank(const int32_t *seq_lens, int num_seqs
 // Shared-memory plan (byte offsets from a 1024-aligned base).  Q is converted once; K and
 // V^T (f16) have NB buffers, and so do the scores in tensor memory; the FP8 staging ring has
 // NS stages.  At head_dim 256 the f16 buffers fill the shared memory: NB = 2, NS = 1.
-template <int HD>
+template <int HD, bool F4>
 struct PfSmem {
-    static constexpr int kSeg = HD >= 128 ? 128 : 64;             // fp8 TMA box row (swizzle span)
-    static constexpr int kSegs = HD / kSeg;
+    static constexpr int kRow = F4 ? HD / 2 : HD;                  // cache bytes of a key's head
+    static constexpr int kSeg = kRow >= 128 ? 128 : kRow;          // TMA box row (swizzle span)
+    static constexpr int kSegs = kRow / kSeg;
     static constexpr int kNB = HD >= 256 ? 2 : 3;                  // f16 K/V^T and S buffers
     static constexpr int kNS = HD >= 256 ? 1 : 4;                  // FP8 staging stages
     static constexpr int kQ = 0;                                   // Q f16: HD/64 blocks x 128 rows x 128 B
@@ -356,7 +429,10 @@ struct PfSmem {
     static constexpr int kK = kQ + HD * 256;
     static constexpr int kV = kK + kNB * kKBuf;
     static constexpr int kStage = kV + kNB * kVBuf;                // fp8 K then V, per stage
-    static constexpr int kStageBytes = 2 * kPfKeys * HD;
+    // F4: K codes, V codes, then the scale bytes of K and of V
+    static constexpr int kScaleSide = F4 ? kPfKeys * (HD / 16) : 0;
+    static constexpr int kScales = 2 * kPfKeys * kRow;
+    static constexpr int kStageBytes = kScales + 2 * kScaleSide;
     static constexpr int kBars = kStage + kNS * kStageBytes;
     // mbarriers: full[NS], empty[NS], then per buffer kv_ready, kv_free, s_ready, p_ready,
     // and one to drain the tensor core on a timeout.  kv_free[b] completes when the products
@@ -368,7 +444,7 @@ struct PfSmem {
     static constexpr int kDrain = kPReady + 8 * kNB;
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // valid-key mask per K/V buffer
-    static constexpr int kMisc = kBufMask + 8 * kNB;               // tmem base, abort flag
+    static constexpr int kMisc = kBufMask + 8 * kNB;               // tmem base, abort flag, NaN seen
     static constexpr int kTotal = kMisc + 16;
     // tensor memory: S[NB] (64 fp32 columns each; P as f16 over the first 32), then O
     static constexpr uint32_t kColO = 64 * kNB;
@@ -382,11 +458,11 @@ constexpr int kPfConvWarps = 8;
 constexpr int kPfMmaWarp = 4 + kPfConvWarps, kPfTmaWarp = kPfMmaWarp + 1;
 constexpr int kPfWarps = kPfTmaWarp + 1;
 
-template <int HD>
+template <int HD, bool F4>
 __global__ void __launch_bounds__(kPfWarps * 32, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                const PrefillArgs a) {
-    using L = PfSmem<HD>;
+    using L = PfSmem<HD, F4>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -395,6 +471,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     volatile uint64_t *buf_mask = reinterpret_cast<volatile uint64_t *>(bp + L::kBufMask);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bp + L::kMisc);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 4);
+    volatile int32_t *nan_seen = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 8);
     auto bar = [&](int off, int i) { return base + static_cast<uint32_t>(off + 8 * i); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -463,6 +540,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
+        if (F4) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPfMmaWarp) {
@@ -495,7 +573,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         const int p = k_lane ? lane : lane - nbox;  // this lane's box within the tile
         const bool box_lane = lane < 2 * nbox;
         const CUtensorMap *map = k_lane ? &tmk : &tmv;
-        const uint32_t side = k_lane ? 0u : static_cast<uint32_t>(kPfKeys * HD);
+        const uint32_t side = k_lane ? 0u : static_cast<uint32_t>(kPfKeys * L::kRow);
         int wbase = -(1 << 30);
         int32_t win = -1;
         int issued = 0;
@@ -532,7 +610,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     meta[st] = mask;
                     const uint32_t full = bar(L::kFull, st);
                     if (boxes > 0)
-                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * L::kSegs * 2 * br * L::kSeg));
+                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * (L::kRow + L::kScaleSide / kPfKeys)));
                     else
                         mbar_arrive(full);
                     ++issued;
@@ -549,6 +627,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 for (int sgi = 0; sgi < L::kSegs; ++sgi)
                     tma_load_3d(dst + static_cast<uint32_t>(sgi * kPfKeys * L::kSeg), map, 0,
                                 kvh * L::kSegs + sgi, row, full);
+                if constexpr (F4) {  // br tokens' scale bytes: a multiple of 32
+                    constexpr int kGph = HD / 16;
+                    const uint8_t *sc = (k_lane ? a.key_scales : a.value_scales) +
+                                        ((static_cast<int64_t>(blk) * a.n_kv + kvh) * bs + (t & (bs - 1))) * kGph;
+                    bulk_load(base + L::kStage + st * L::kStageBytes + L::kScales +
+                                  (k_lane ? 0u : static_cast<uint32_t>(L::kScaleSide)) +
+                                  static_cast<uint32_t>(p * br * kGph),
+                              sc, static_cast<uint32_t>(br * kGph), full);
+                }
             }
         }
         if (aborted && lane == 0) {
@@ -648,7 +735,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             if (!ok) break;
             const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
-            const uint8_t *vst = kst + kPfKeys * HD;
+            const uint8_t *vst = kst + kPfKeys * L::kRow;
+            const uint8_t *ksc = kst + L::kScales, *vsc = ksc + L::kScaleSide;  // F4
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf;
             uint8_t *vdst = bp + L::kV + b * L::kVBuf;
             // K: 64 keys x HD/8 chunks of 8 fp8 -> one 16-byte f16 chunk (invalid keys: zeros);
@@ -674,6 +762,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const int key = ko * 8 + (lane >> 2);
                     const int sgi = (32 * dg) / L::kSeg, cc = ((32 * dg) % L::kSeg) >> 4;
+                    if constexpr (F4) {  // the 32 dims' 16 code bytes and their two scale bytes
+                        vw[j][0] = *reinterpret_cast<const uint4 *>(vst + swz<L::kSeg>(key, dg));
+                        vw[j][1].x = value_scales_of(vsc + key * (HD / 16) + 2 * dg, (mask >> key) & 1ull, nan_seen);
+                        continue;
+                    }
                     const uint8_t *vrow = vst + sgi * kPfKeys * L::kSeg;
                     vw[j][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[j][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
@@ -686,6 +779,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     const int blk = w4 + (g0 + j) * kPfConvWarps;
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const uint4 lo = vw[j][0], hi = vw[j][1];
+                    if constexpr (F4) {
+                        const uint32_t wd4[4] = {lo.x, lo.y, lo.z, lo.w};
+                        const uint32_t s0 = scale_pair(hi.x), s1 = scale_pair(hi.x >> 8);
+                        uint32_t h4[4];
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4)  // dims 8e + 2(t%4), +1 of the key's 32
+                            h4[e4] = mul_f16x2(f16x2_from_e2m1x2(__byte_perm(wd4[e4], 0u, lane & 3)), e4 < 2 ? s0 : s1);
+                        const int n4 = 32 * dg + 8 * (lane >> 3) + (lane & 7);
+                        stsm_x4_t(vbase + sw128(n4, ko), h4[0], h4[1], h4[2], h4[3]);
+                        continue;
+                    }
                     const uint32_t wd[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     uint32_t r[4];
 #pragma unroll
@@ -699,6 +803,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             for (int j = 0; j < kKT; ++j) {
                 const int task = ct + j * kCT;
                 const int key = task / (HD / 8), c = task % (HD / 8);  // dims 8c .. 8c+7
+                if constexpr (F4) {  // four code bytes and their group's scale byte
+                    kw[j].x = *reinterpret_cast<const uint32_t *>(kst + swz<L::kSeg>(key, c >> 2) + 4 * (c & 3));
+                    kw[j].y = ksc[key * (HD / 16) + (c >> 1)];
+                    if (!((mask >> key) & 1ull)) kw[j] = make_uint2(0u, 0u);
+                    continue;
+                }
                 const int sgi = (8 * c) / L::kSeg, within = (8 * c) % L::kSeg;
                 kw[j] = *reinterpret_cast<const uint2 *>(kst + sgi * kPfKeys * L::kSeg +
                                                          swz<L::kSeg>(key, within >> 4) + (within & 8));
@@ -711,10 +821,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 const int key = task / (HD / 8), c = task % (HD / 8);
                 const uint2 w = kw[j];
                 uint4 h;
-                h.x = f16x2_from_e4m3x2(w.x);
-                h.y = f16x2_from_e4m3x2_hi(w.x);
-                h.z = f16x2_from_e4m3x2(w.y);
-                h.w = f16x2_from_e4m3x2_hi(w.y);
+                if constexpr (F4) {
+                    h = dequant8(w.x, scale_pair(w.y));
+                } else {
+                    h.x = f16x2_from_e4m3x2(w.x);
+                    h.y = f16x2_from_e4m3x2_hi(w.x);
+                    h.z = f16x2_from_e4m3x2(w.y);
+                    h.w = f16x2_from_e4m3x2_hi(w.y);
+                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kPfKeys * 128) + sw128(key, c & 7)) = h;
             }
             v_store(0);
@@ -842,6 +956,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 lsum = __uint_as_float(o[0]);
             }
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
+            uint32_t nan_groups = 0;
+            if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -857,6 +973,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                         w.y = bf16x2_from_f32(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
                         w.z = bf16x2_from_f32(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv);
                         w.w = bf16x2_from_f32(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv);
+                        if (F4 && nan_groups != 0u) {
+                            const int d = c0 + c;
+                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
+                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
+                        }
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -904,11 +1025,12 @@ constexpr int kP2ConvWarps = 4;
 constexpr int kP2MmaWarp = 8 + kP2ConvWarps, kP2TmaWarp = kP2MmaWarp + 1;
 constexpr int kP2Warps = kP2TmaWarp + 1;
 
-template <int HD>
+template <int HD, bool F4>
 struct Pf2Smem {
-    static constexpr int kSeg = HD >= 128 ? 128 : 64;
-    static constexpr int kSegs = HD / kSeg;
-    static constexpr int kNS = HD >= 128 ? 2 : 4;                  // FP8 staging halves
+    static constexpr int kRow = F4 ? HD / 2 : HD;
+    static constexpr int kSeg = kRow >= 128 ? 128 : kRow;
+    static constexpr int kSegs = kRow / kSeg;
+    static constexpr int kNS = HD < 128 ? 4 : F4 ? 3 : 2;          // staging halves
     static constexpr int kQTile = HD * 256;                        // one row tile of Q (f16)
     static constexpr int kQ = 0;
     // K f16: HD/64 blocks x 128 keys x 128 B; V^T f16: 2 key blocks x HD rows x 128 B
@@ -916,7 +1038,9 @@ struct Pf2Smem {
     static constexpr int kK = kQ + 2 * kQTile;
     static constexpr int kV = kK + 2 * kKBuf;
     static constexpr int kStage = kV + 2 * kVBuf;
-    static constexpr int kStageBytes = 2 * kPfKeys * HD;           // FP8 K then V of 64 keys
+    static constexpr int kScaleSide = F4 ? kPfKeys * (HD / 16) : 0;
+    static constexpr int kScales = 2 * kPfKeys * kRow;             // K then V of 64 keys, then (F4)
+    static constexpr int kStageBytes = kScales + 2 * kScaleSide;   // their scale bytes
     static constexpr int kBars = kStage + kNS * kStageBytes;
     // mbarriers: full[NS], empty[NS], then per buffer k_ready, v_ready, k_free, v_free, then
     // per row tile s_ready, p_ready, o_done, and one to drain the tensor core on a timeout
@@ -926,7 +1050,7 @@ struct Pf2Smem {
     static constexpr int kDrain = kODone + 16;
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // per V^T buffer, two halves
-    static constexpr int kMisc = kBufMask + 32;                    // tmem base, abort flag
+    static constexpr int kMisc = kBufMask + 32;                    // tmem base, abort flag, NaN seen
     static constexpr int kTotal = kMisc + 16;
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t col_s(int r) { return static_cast<uint32_t>(128 * r); }
@@ -961,11 +1085,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  : "memory");
 }
 
-template <int HD>
+template <int HD, bool F4>
 __global__ void __launch_bounds__(kP2Warps * 32, 1)
 prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const PrefillArgs a) {
-    using L = Pf2Smem<HD>;
+    using L = Pf2Smem<HD, F4>;
     static_assert(L::kTotal + 1024 <= 232448, "shared memory");
     static_assert(L::col_o(1) + HD <= L::kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
@@ -976,6 +1100,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     volatile uint64_t *buf_mask = reinterpret_cast<volatile uint64_t *>(bp + L::kBufMask);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bp + L::kMisc);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 4);
+    volatile int32_t *nan_seen = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 8);
     auto bar = [&](int off, int i) { return base + static_cast<uint32_t>(off + 8 * i); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1037,6 +1162,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
+        if (F4) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kP2MmaWarp) {
@@ -1065,7 +1191,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const int p = k_lane ? lane : lane - nbox;
         const bool box_lane = lane < 2 * nbox;
         const CUtensorMap *map = k_lane ? &tmk : &tmv;
-        const uint32_t side = k_lane ? 0u : static_cast<uint32_t>(kPfKeys * HD);
+        const uint32_t side = k_lane ? 0u : static_cast<uint32_t>(kPfKeys * L::kRow);
         int wbase = -(1 << 30);
         int32_t win = -1;
         int issued = 0;
@@ -1103,7 +1229,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     meta[st] = mask;
                     const uint32_t full = bar(L::kFull, st);
                     if (boxes > 0)
-                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * L::kSegs * 2 * br * L::kSeg));
+                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * (L::kRow + L::kScaleSide / kPfKeys)));
                     else
                         mbar_arrive(full);
                     ++issued;
@@ -1119,6 +1245,15 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 for (int sgi = 0; sgi < L::kSegs; ++sgi)
                     tma_load_3d(dst + static_cast<uint32_t>(sgi * kPfKeys * L::kSeg), map, 0,
                                 kvh * L::kSegs + sgi, row, full);
+                if constexpr (F4) {  // br tokens' scale bytes: a multiple of 32
+                    constexpr int kGph = HD / 16;
+                    const uint8_t *sc = (k_lane ? a.key_scales : a.value_scales) +
+                                        ((static_cast<int64_t>(blk) * a.n_kv + kvh) * bs + (t & (bs - 1))) * kGph;
+                    bulk_load(base + L::kStage + st * L::kStageBytes + L::kScales +
+                                  (k_lane ? 0u : static_cast<uint32_t>(L::kScaleSide)) +
+                                  static_cast<uint32_t>(p * br * kGph),
+                              sc, static_cast<uint32_t>(br * kGph), full);
+                }
             }
         }
         if (aborted && lane == 0) {
@@ -1235,7 +1370,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             if (!ok) break;
             const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
-            const uint8_t *vst = kst + kPfKeys * HD;
+            const uint8_t *vst = kst + kPfKeys * L::kRow;
+            const uint8_t *ksc = kst + L::kScales, *vsc = ksc + L::kScaleSide;  // F4
             // this half's 64 keys: rows 64*hf.. of every 64-dim block of the K buffer
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf + hf * (kPfKeys * 128);
             // and key block hf of the V^T buffer
@@ -1248,6 +1384,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const int key = ko * 8 + (lane >> 2);
                     const int sgi = (32 * dg) / L::kSeg, cc = ((32 * dg) % L::kSeg) >> 4;
+                    if constexpr (F4) {  // the 32 dims' 16 code bytes and their two scale bytes
+                        vw[q][0] = *reinterpret_cast<const uint4 *>(vst + swz<L::kSeg>(key, dg));
+                        vw[q][1].x = value_scales_of(vsc + key * (HD / 16) + 2 * dg, (mask >> key) & 1ull, nan_seen);
+                        continue;
+                    }
                     const uint8_t *vrow = vst + sgi * kPfKeys * L::kSeg;
                     vw[q][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[q][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
@@ -1260,6 +1401,17 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     const int blk = w8 + (g0 + q) * kP2ConvWarps;
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const uint4 lo = vw[q][0], hi = vw[q][1];
+                    if constexpr (F4) {
+                        const uint32_t wd4[4] = {lo.x, lo.y, lo.z, lo.w};
+                        const uint32_t s0 = scale_pair(hi.x), s1 = scale_pair(hi.x >> 8);
+                        uint32_t h4[4];
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4)  // dims 8e + 2(t%4), +1 of the key's 32
+                            h4[e4] = mul_f16x2(f16x2_from_e2m1x2(__byte_perm(wd4[e4], 0u, lane & 3)), e4 < 2 ? s0 : s1);
+                        const int n4 = 32 * dg + 8 * (lane >> 3) + (lane & 7);
+                        stsm_x4_t(vbase + sw128(n4, ko), h4[0], h4[1], h4[2], h4[3]);
+                        continue;
+                    }
                     const uint32_t wd[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     uint32_t rv[4];
 #pragma unroll
@@ -1275,6 +1427,12 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             for (int q = 0; q < kKT; ++q) {
                 const int task = ct + q * kCT;
                 const int key = task / (HD / 8), c = task % (HD / 8);
+                if constexpr (F4) {  // four code bytes and their group's scale byte
+                    kw[q].x = *reinterpret_cast<const uint32_t *>(kst + swz<L::kSeg>(key, c >> 2) + 4 * (c & 3));
+                    kw[q].y = ksc[key * (HD / 16) + (c >> 1)];
+                    if (!((mask >> key) & 1ull)) kw[q] = make_uint2(0u, 0u);
+                    continue;
+                }
                 const int sgi = (8 * c) / L::kSeg, within = (8 * c) % L::kSeg;
                 kw[q] = *reinterpret_cast<const uint2 *>(kst + sgi * kPfKeys * L::kSeg +
                                                          swz<L::kSeg>(key, within >> 4) + (within & 8));
@@ -1286,10 +1444,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 const int key = task / (HD / 8), c = task % (HD / 8);
                 const uint2 w = kw[q];
                 uint4 h;
-                h.x = f16x2_from_e4m3x2(w.x);
-                h.y = f16x2_from_e4m3x2_hi(w.x);
-                h.z = f16x2_from_e4m3x2(w.y);
-                h.w = f16x2_from_e4m3x2_hi(w.y);
+                if constexpr (F4) {
+                    h = dequant8(w.x, scale_pair(w.y));
+                } else {
+                    h.x = f16x2_from_e4m3x2(w.x);
+                    h.y = f16x2_from_e4m3x2_hi(w.x);
+                    h.z = f16x2_from_e4m3x2(w.y);
+                    h.w = f16x2_from_e4m3x2_hi(w.y);
+                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kP2Keys * 128) + sw128(key, c & 7)) = h;
             }
             if (hf == 1) {  // both halves of the tile's K are in place
@@ -1445,6 +1607,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float2 ls = upk2(lsum2);
             const float lsum = ls.x + ls.y;
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
+            uint32_t nan_groups = 0;
+            if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1460,6 +1624,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                         w.y = bf16x2_from_f32(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
                         w.z = bf16x2_from_f32(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv);
                         w.w = bf16x2_from_f32(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv);
+                        if (F4 && nan_groups != 0u) {
+                            const int d = c0 + c;
+                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
+                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
+                        }
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -1477,10 +1646,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     }
 }
 
-template <int HD>
+template <int HD, bool F4>
 cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
-    using L = PfSmem<HD>;
-    const int row_bytes = d.n_kv * HD;
+    using L = PfSmem<HD, F4>;
+    const int row_bytes = d.n_kv * L::kRow;
     const int box_rows = d.block_size >= kPfKeys ? kPfKeys : d.block_size;  // whole tile when one block holds it
     const int64_t rows = static_cast<int64_t>(d.num_blocks) * d.block_size;
     CUtensorMap tmk, tmv;
@@ -1511,11 +1680,13 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     a.scale_dtype = d.scale_dtype;
     a.status = d.status;
     a.box_rows = box_rows;
+    a.key_scales = d.key_scales;
+    a.value_scales = d.value_scales;
     // more than one tile of 128 rows per kv head (a multi-query call): 256 rows per CTA
     if constexpr (HD <= 128) {
         if (d.qsl != nullptr && d.qmax * a.group > kPfRows) {
-            const size_t smem2 = Pf2Smem<HD>::kTotal + 1024;
-            auto kern2 = prefill2_kernel<HD>;
+            const size_t smem2 = Pf2Smem<HD, F4>::kTotal + 1024;
+            auto kern2 = prefill2_kernel<HD, F4>;
             int occ2 = 0;  // also raises the kernel's shared memory limit, once per device
             if ((err = kernel_occupancy(kern2, kP2Warps * 32, smem2, &occ2)) != cudaSuccess)
                 return err;
@@ -1526,7 +1697,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         }
     }
     const size_t smem = L::kTotal + 1024;
-    auto kern = prefill_kernel<HD>;
+    auto kern = prefill_kernel<HD, F4>;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
     a.row_tiles = (d.qmax * a.group + kPfRows - 1) / kPfRows;
@@ -1543,10 +1714,11 @@ cudaError_t launch_prefill_attention(const DecodeArgs &d, cudaStream_t stream) {
     if (d.n_q / d.n_kv > kPfRows) return cudaErrorNotSupported;
     const int64_t row_tiles = (static_cast<int64_t>(d.qmax) * (d.n_q / d.n_kv) + kPfRows - 1) / kPfRows;
     if (row_tiles * d.n_kv * d.num_seqs > 0x7FFFFFFF) return cudaErrorNotSupported;
+    const bool f4 = d.key_scales != nullptr;
     switch (d.head_dim) {
-        case 64: return run_prefill<64>(d, stream);
-        case 128: return run_prefill<128>(d, stream);
-        case 256: return run_prefill<256>(d, stream);
+        case 64: return f4 ? run_prefill<64, true>(d, stream) : run_prefill<64, false>(d, stream);
+        case 128: return f4 ? run_prefill<128, true>(d, stream) : run_prefill<128, false>(d, stream);
+        case 256: return f4 ? run_prefill<256, true>(d, stream) : run_prefill<256, false>(d, stream);
         default: return cudaErrorNotSupported;
     }
 }

@@ -373,6 +373,147 @@ KVFP8_API kvfp8_status kvfp8_dequant(void *dst, kvfp8_dtype dst_dtype, const uin
                            const void *scale, kvfp8_dtype scale_dtype, kvfp8_stream_t stream);
 
 /*
+ * The 4-bit cache: E2M1 codes with one E4M3 scale per 16 dims, 0.5625 bytes per element.
+ *
+ * The source pages stop at 8 bits; this is the same path at half the bytes, in the block
+ * format of sm_100's 4-bit conversions (E2M1 elements, E4M3 scales over 16).  Per side:
+ *   codes   uint8 [num_blocks][block_size][n_kv][head_dim/2]   dim 2i in the low nibble of
+ *                                                              byte i, dim 2i+1 in the high
+ *   scales  uint8 [num_blocks][n_kv][block_size][head_dim/16]  (a kv head's scales of a block
+ *                                                              are contiguous)
+ * A code is sign (bit 3) and magnitude code m: 0, 0.5, 1, 1.5, 2, 3, 4, 6.  With B the decoded
+ * scale of the dim's group and s the layer's scalar scale the element's value is
+ *   code * (B * s)          (B*s a float product, code*(B*s) a float product)
+ *
+ * Writing a group of 16 elements x_i (all quotients and products are float, to nearest even):
+ *   a = max |x_i|,  b = E4M3((a / |s|) / 6) (nearest even, saturating at 448),  B = dec(b)
+ *   d = B * |s|,    m_i = E2M1(|x_i| / d)   (nearest even, saturating at 6; 0 when d = 0)
+ *   sign_i = (x_i < 0) xor (s < 0)
+ * An infinite element gets magnitude 6 (its group's scale is 448); a NaN element makes its
+ * whole group NaN: scale byte 0x7F, codes 0.
+ *
+ * Everywhere below head_dim is 64, 128 or 256 and block_size 8, 16, 32, 64, 128 or 256; all
+ * device pointers 16-byte aligned.
+ *
+ * kvfp8_reshape_and_cache_fp4: as kvfp8_reshape_and_cache, into codes and scales.  Slots of
+ * different tokens must differ: a slot named twice ends up with parts of either token.
+ */
+KVFP8_API kvfp8_status kvfp8_reshape_and_cache_fp4(
+    const void *key, const void *value, kvfp8_dtype src_dtype, int64_t key_stride,
+    int64_t value_stride, int64_t num_tokens, uint8_t *key_cache, uint8_t *value_cache,
+    uint8_t *key_scales, uint8_t *value_scales, int32_t num_blocks, int32_t block_size,
+    int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping, const void *k_scale,
+    const void *v_scale, kvfp8_dtype scale_dtype, uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * Rows of one side of the 4-bit cache read back by slot (the rope-shift path: dequantize,
+ * rotate, requantize with kvfp8_reshape_and_cache_fp4):
+ *   dst[i][h][d] = code * (B * s), rounded to dst_dtype (bf16: nearest even)
+ * for the token slot slot_mapping[i].  Slot -1 gives a zero row; any other slot outside
+ * [0, num_blocks*block_size) gives a zero row and sets KVFP8_DEV_BAD_SLOT; a scale that is
+ * zero or not finite sets KVFP8_DEV_BAD_SCALE and nothing is written.  A slot may be named
+ * several times.  A NaN scale byte (0x7F) gives NaN for its 16 dims.
+ *
+ * dst   device, dst_dtype [num_tokens][n_kv][head_dim]
+ * scale device scalar of scale_dtype, or NULL for 1
+ */
+KVFP8_API kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const uint8_t *codes,
+                                         const uint8_t *scales, int32_t num_blocks,
+                                         int32_t block_size, int32_t n_kv, int32_t head_dim,
+                                         const int64_t *slot_mapping, int64_t num_tokens,
+                                         const void *scale, kvfp8_dtype scale_dtype,
+                                         uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * kvfp8_paged_decode_attention over the 4-bit cache:
+ *   s_t = sm_scale * k_scale * sum_d q[b][h][d] * Kcode(t, kv, d) * KB(t, kv, d / 16)
+ *   out[b][h][d] = v_scale * sum_t softmax(s)_t * Vcode(t, kv, d) * VB(t, kv, d / 16)
+ * code*B has at most six significant bits and enters the tensor cores as fp16 exactly;
+ * accumulation is fp32.  A token's NaN reaches exactly the outputs that see the token (all of
+ * a row for a NaN in K, the group's 16 dims for a NaN in V).  Workspace:
+ * kvfp8_paged_decode_workspace_size(num_seqs, n_q, head_dim).  Everything else (group sizes,
+ * empty sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
+ */
+KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
+    void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
+    const uint8_t *key_scales, const uint8_t *value_scales, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, int32_t n_q,
+    int32_t n_kv, int32_t head_dim, int32_t block_size, int32_t num_blocks, float sm_scale,
+    const void *k_scale, const void *v_scale, kvfp8_dtype scale_dtype, void *workspace,
+    size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * kvfp8_paged_attention_multi (causal, several new tokens per sequence, any chunk length) over
+ * the 4-bit cache.  Workspace: kvfp8_paged_attention_multi_workspace_size(...).
+ */
+KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
+    void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,
+    int32_t max_query_len, const uint8_t *key_cache, const uint8_t *value_cache,
+    const uint8_t *key_scales, const uint8_t *value_scales, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs, int32_t n_q,
+    int32_t n_kv, int32_t head_dim, int32_t block_size, int32_t num_blocks, float sm_scale,
+    const void *k_scale, const void *v_scale, kvfp8_dtype scale_dtype, void *workspace,
+    size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * Pages of any cache.  A cache here is a device array whose block i is the block_bytes bytes
+ * at i * block_bytes (a multiple of 16): either side of an FP8, bf16 or 4-bit cache, or its
+ * scales, of one layer or of several.
+ *
+ * kvfp8_copy_blocks: for every pair i and every cache c, block dst_blocks[i] becomes a copy of
+ * block src_blocks[i] (a fork's copy on write, pages moved before a pool is cut).  One source
+ * may serve several destinations.  All pairs are carried out at once, so no block may be
+ * written by one pair and read or written by another: every pair whose destination is another
+ * pair's destination too, or whose source is another pair's destination, is skipped and sets
+ * KVFP8_DEV_BAD_BLOCK; the others are carried out.  src == dst does nothing.  A pair with -1
+ * on either side is padding; any other id outside [0, num_blocks) is skipped and sets
+ * KVFP8_DEV_BAD_BLOCK.  (The conflict rule counts the pairs that are left after these.)
+ *
+ * caches, block_bytes  host arrays [num_caches] of device pointers and sizes; num_caches in
+ *                      [1, KVFP8_MAX_CACHES]; the caches must not overlap
+ * src_blocks, dst_blocks  device int32 [num_pairs], 4-byte aligned; num_pairs >= 0, < 2^31
+ */
+#define KVFP8_MAX_CACHES 128
+#define KVFP8_MAX_COPY_BLOCKS 900000 /* larger pools return KVFP8_ERR_UNSUPPORTED */
+KVFP8_API kvfp8_status kvfp8_copy_blocks(void *const *caches, const int64_t *block_bytes,
+                                         int32_t num_caches, int32_t num_blocks,
+                                         const int32_t *src_blocks, const int32_t *dst_blocks,
+                                         int64_t num_pairs, uint32_t *status,
+                                         kvfp8_stream_t stream);
+
+/* Workspace bytes of kvfp8_compact_blocks.  Pure host arithmetic. */
+KVFP8_API size_t kvfp8_compact_blocks_workspace_size(int32_t num_blocks);
+
+/*
+ * kvfp8_compact_blocks: moves the used blocks of a pool to its lowest ids, so that every id
+ * from *num_used on is free (to be handed out again, or cut off the pool).
+ *
+ * Block b is used when some sequence names it among its first ceil(seq_lens[s] / block_size)
+ * table entries; several may (forks).  With U used blocks, the k-th used block with an id >= U
+ * (ascending) is copied in every cache to the k-th free id below U; all others stay where they
+ * are.  new_block_tables holds the new ids; the entries past a sequence's length come out as
+ * -1.  An entry within the length that is outside [0, num_blocks) comes out as -1 and sets
+ * KVFP8_DEV_BAD_BLOCK, as does a length that is negative (taken as 0) or above
+ * max_blocks_per_seq*block_size (clamped).  The old blocks keep their bytes.
+ *
+ * caches, block_bytes  as for kvfp8_copy_blocks
+ * block_size        >= 1, tokens per block
+ * block_tables, new_block_tables  device int32 [num_seqs][max_blocks_per_seq]; may be the same
+ *                   array, and must not overlap otherwise
+ * num_used          device int32 [1]
+ * workspace         device, >= kvfp8_compact_blocks_workspace_size(num_blocks) bytes; calls
+ *                   that overlap on the GPU must not share it
+ */
+KVFP8_API kvfp8_status kvfp8_compact_blocks(void *const *caches, const int64_t *block_bytes,
+                                            int32_t num_caches, int32_t num_blocks,
+                                            int32_t block_size, const int32_t *block_tables,
+                                            int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                            int32_t num_seqs, int32_t *new_block_tables,
+                                            int32_t *num_used, void *workspace,
+                                            size_t workspace_bytes, uint32_t *status,
+                                            kvfp8_stream_t stream);
+
+/*
  * Host-side scale check: KVFP8_OK if s is finite and nonzero, else KVFP8_ERR_SCALE.
  * [P1] llama-context.cpp llama_init_from_model ("must be finite and nonzero").
  */
