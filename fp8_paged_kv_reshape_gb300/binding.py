@@ -6,7 +6,6 @@ fallback: if the library is missing, importing this module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -512,18 +511,28 @@ def dequant(src: torch.Tensor, dst_dtype: torch.dtype = torch.float32,
 
 # ---------------------------------------------------------------- 4-bit cache, pages
 
-def _check_device(**tensors):
-    """Every given tensor on the current CUDA device, where the kernels run."""
-    here = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if here is None:
-            here = torch.cuda.current_device()
-        if t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+# The wrappers below run once per layer and step, where a kernel may take a few microseconds: they
+# read each tensor attribute once, pass addresses as plain integers and ask torch for the raw stream.
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _check_device(*tensors: torch.Tensor | None) -> int:
+    """The index of the current CUDA device, which every given tensor has to be on."""
+    here = tensors[0].get_device()  # -1 on the CPU
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
+    if here < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if here != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{here}, the current device is cuda:{torch.cuda.current_device()}")
+    return here
+
+
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _check_status(status: torch.Tensor | None):
@@ -531,9 +540,21 @@ def _check_status(status: torch.Tensor | None):
         raise ValueError("status must be an int32 [1] tensor")
 
 
-def _on(stream):
-    """Allocations for a call on `stream` belong to that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, device: int, stream):
+    """A tensor for a call on `stream`, from that stream's memory pool."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
+
+
+class _Devices(dict):
+    def __missing__(self, index):
+        self[index] = torch.device("cuda", index)
+        return self[index]
+
+
+_DEVICES = _Devices()
 
 
 def _check_fp4_side(cache: torch.Tensor, scales: torch.Tensor):
@@ -542,7 +563,7 @@ def _check_fp4_side(cache: torch.Tensor, scales: torch.Tensor):
         raise ValueError("4-bit codes must be contiguous uint8 [num_blocks, block_size, n_kv, head_dim/2]")
     nb, bs, n_kv, half = cache.shape
     if half % 8 != 0 or scales.dtype != torch.uint8 or \
-            tuple(scales.shape) != (nb, n_kv, bs, half // 8) or not scales.is_contiguous():
+            scales.shape != (nb, n_kv, bs, half // 8) or not scales.is_contiguous():
         raise ValueError("their scales must be contiguous uint8 [num_blocks, n_kv, block_size, head_dim/16]")
     return nb, bs, n_kv, 2 * half
 
@@ -581,15 +602,14 @@ def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, key_cache: tor
         raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
     sdt = _scale_args(k_scale, v_scale)
     _check_status(status)
-    _check_device(key=key, value=value, key_cache=key_cache, value_cache=value_cache,
-                  key_scales=key_scales, value_scales=value_scales, slot_mapping=slot_mapping,
-                  k_scale=k_scale, v_scale=v_scale, status=status)
+    dev = _check_device(key, value, key_cache, value_cache, key_scales, value_scales, slot_mapping,
+                        k_scale, v_scale, status)
     # (the stride of a single row is never used, and may be anything)
     ks, vs = (key.stride(0), value.stride(0)) if n > 1 else (n_kv * hd, n_kv * hd)
     rc = LIB.kvfp8_reshape_and_cache_fp4(
-        _ptr(key), _ptr(value), F32 if key.dtype == torch.float32 else BF16, ks, vs, n,
-        _ptr(key_cache), _ptr(value_cache), _ptr(key_scales), _ptr(value_scales), nb, bs, n_kv, hd,
-        _ptr(slot_mapping), _ptr(k_scale), _ptr(v_scale), sdt, _ptr(status), _stream(stream))
+        _addr(key), _addr(value), F32 if key.dtype == torch.float32 else BF16, ks, vs, n,
+        _addr(key_cache), _addr(value_cache), _addr(key_scales), _addr(value_scales), nb, bs, n_kv, hd,
+        _addr(slot_mapping), _addr(k_scale), _addr(v_scale), sdt, _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_reshape_and_cache_fp4")
 
 
@@ -605,27 +625,26 @@ def dequant_fp4(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.T
     if dst_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("dst_dtype must be float32 or bfloat16")
     n = slot_mapping.numel()
-    if out is not None and (out.dtype != dst_dtype or tuple(out.shape) != (n, n_kv, hd) or
+    if out is not None and (out.dtype != dst_dtype or out.shape != (n, n_kv, hd) or
                             not out.is_contiguous()):
         raise ValueError("out must be a contiguous dst_dtype [num_tokens, n_kv, head_dim] tensor")
     sdt = _scale_args(scale, None)
     _check_status(status)
-    _check_device(cache=cache, scales=scales, slot_mapping=slot_mapping, scale=scale, out=out,
-                  status=status)
+    dev = _check_device(cache, scales, slot_mapping, scale, out, status)
     if out is None:
-        with _on(stream):
-            out = torch.empty((n, n_kv, hd), dtype=dst_dtype, device=cache.device)
-    rc = LIB.kvfp8_dequant_fp4(_ptr(out), BF16 if dst_dtype == torch.bfloat16 else F32, _ptr(cache),
-                               _ptr(scales), nb, bs, n_kv, hd, _ptr(slot_mapping), n, _ptr(scale),
-                               sdt, _ptr(status), _stream(stream))
+        out = _empty((n, n_kv, hd), dst_dtype, dev, stream)
+    rc = LIB.kvfp8_dequant_fp4(_addr(out), BF16 if dst_dtype == torch.bfloat16 else F32, _addr(cache),
+                               _addr(scales), nb, bs, n_kv, hd, _addr(slot_mapping), n, _addr(scale),
+                               sdt, _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_dequant_fp4")
     return out
 
 
 def _check_attention_fp4(query, key_cache, value_cache, key_scales, value_scales, block_tables,
-                         seq_lens, k_scale, v_scale, out, workspace, status, num_seqs, **more):
+                         seq_lens, k_scale, v_scale, out, workspace, status, num_seqs,
+                         query_start_loc=None):
     """The checks both 4-bit attention calls make; returns (rows, n_q, head_dim, num_blocks,
-    block_size, n_kv, scale dtype)."""
+    block_size, n_kv, scale dtype, device)."""
     if query.dtype != torch.bfloat16 or query.dim() != 3 or not query.is_contiguous():
         raise ValueError("query must be a contiguous bf16 [rows, n_q, head_dim] tensor")
     rows, n_q, hd = query.shape
@@ -640,11 +659,9 @@ def _check_attention_fp4(query, key_cache, value_cache, key_scales, value_scales
         raise ValueError("workspace must be contiguous")
     sdt = _scale_args(k_scale, v_scale)
     _check_status(status)
-    _check_device(query=query, key_cache=key_cache, value_cache=value_cache, key_scales=key_scales,
-                  value_scales=value_scales, block_tables=block_tables, seq_lens=seq_lens,
-                  k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace, status=status,
-                  **more)
-    return rows, n_q, hd, nb, bs, n_kv, sdt
+    dev = _check_device(query, key_cache, value_cache, key_scales, value_scales, block_tables,
+                        seq_lens, k_scale, v_scale, out, workspace, status, query_start_loc)
+    return rows, n_q, hd, nb, bs, n_kv, sdt, dev
 
 
 def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
@@ -658,20 +675,19 @@ def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
     """kvfp8_paged_decode_attention_fp4: paged_decode_attention over a 4-bit cache (codes and
     scales as reshape_and_cache_fp4 writes them); returns out (bf16 [num_seqs, n_q, hd])."""
     num_seqs = query.shape[0] if query.dim() == 3 else 0
-    num_seqs, n_q, hd, nb, bs, n_kv, sdt = _check_attention_fp4(
+    num_seqs, n_q, hd, nb, bs, n_kv, sdt, dev = _check_attention_fp4(
         query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
         v_scale, out, workspace, status, num_seqs)
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(query)
-        if workspace is None:
-            workspace = torch.empty(max(paged_decode_workspace_size(num_seqs, n_q, hd), 16),
-                                    dtype=torch.uint8, device=query.device)
+    if out is None:
+        out = _empty(query.shape, torch.bfloat16, dev, stream)
+    if workspace is None:
+        workspace = _empty(LIB.kvfp8_paged_decode_workspace_size(num_seqs, n_q, hd), torch.uint8, dev,
+                           stream)
     rc = LIB.kvfp8_paged_decode_attention_fp4(
-        _ptr(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
-        _ptr(value_scales), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), num_seqs,
-        n_q, n_kv, hd, bs, nb, float(sm_scale), _ptr(k_scale), _ptr(v_scale), sdt, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+        _addr(out), _addr(query), _addr(key_cache), _addr(value_cache), _addr(key_scales),
+        _addr(value_scales), _addr(block_tables), block_tables.shape[1], _addr(seq_lens), num_seqs,
+        n_q, n_kv, hd, bs, nb, float(sm_scale), _addr(k_scale), _addr(v_scale), sdt, _addr(workspace),
+        workspace.numel() * workspace.element_size(), _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_paged_decode_attention_fp4")
     return out
 
@@ -691,43 +707,47 @@ def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor
     if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != num_seqs + 1 or \
             not query_start_loc.is_contiguous():
         raise ValueError("query_start_loc must be a contiguous int32 [num_seqs + 1] tensor")
-    rows, n_q, hd, nb, bs, n_kv, sdt = _check_attention_fp4(
+    rows, n_q, hd, nb, bs, n_kv, sdt, dev = _check_attention_fp4(
         query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
-        v_scale, out, workspace, status, num_seqs, query_start_loc=query_start_loc)
+        v_scale, out, workspace, status, num_seqs, query_start_loc)
     need = paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, hd, max_query_len)
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(query)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    if out is None:
+        out = _empty(query.shape, torch.bfloat16, dev, stream)
+    if workspace is None and need > 0:
+        workspace = _empty(need, torch.uint8, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = LIB.kvfp8_paged_attention_multi_fp4(
-        _ptr(out), _ptr(query), _ptr(query_start_loc), rows, max_query_len, _ptr(key_cache),
-        _ptr(value_cache), _ptr(key_scales), _ptr(value_scales), _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), num_seqs, n_q, n_kv, hd, bs, nb, float(sm_scale),
-        _ptr(k_scale), _ptr(v_scale), sdt, _ptr(workspace), ws_bytes, _ptr(status),
-        _stream(stream))
+        _addr(out), _addr(query), _addr(query_start_loc), rows, max_query_len, _addr(key_cache),
+        _addr(value_cache), _addr(key_scales), _addr(value_scales), _addr(block_tables),
+        block_tables.shape[1], _addr(seq_lens), num_seqs, n_q, n_kv, hd, bs, nb, float(sm_scale),
+        _addr(k_scale), _addr(v_scale), sdt, _addr(workspace), ws_bytes, _addr(status),
+        _raw_stream(stream, dev))
     _check(rc, "kvfp8_paged_attention_multi_fp4")
     return out
 
 
 def _cache_list(caches):
-    """The page calls' caches as C arrays: (pointers, bytes per block, count, num_blocks)."""
+    """The page calls' caches: (pointers and bytes per block as C arrays, count, num_blocks, caches)."""
     caches = list(caches)
-    if not 1 <= len(caches) <= MAX_CACHES:
+    count = len(caches)
+    if not 1 <= count <= MAX_CACHES:
         raise ValueError(f"1 to {MAX_CACHES} caches")
-    for c in caches:
-        if not isinstance(c, torch.Tensor) or c.dim() < 2 or not c.is_contiguous() or \
-                c.numel() == 0 or c.shape[0] != caches[0].shape[0]:
+    nb = caches[0].shape[0] if caches[0].dim() > 1 else 0
+    ptrs, sizes = (ctypes.c_void_p * count)(), (ctypes.c_int64 * count)()
+    spans = []
+    for i, c in enumerate(caches):
+        total = c.numel() * c.element_size()
+        if c.dim() < 2 or c.shape[0] != nb or total == 0 or not c.is_contiguous():
             raise ValueError("caches must be contiguous tensors [num_blocks, ...] of one num_blocks")
-    nb = caches[0].shape[0]
-    spans = sorted((c.data_ptr(), c.numel() * c.element_size()) for c in caches)
-    if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
-        raise ValueError("caches must not overlap")
-    _check_device(**{f"caches[{i}]": c for i, c in enumerate(caches)})
-    ptrs = (ctypes.c_void_p * len(caches))(*(c.data_ptr() for c in caches))
-    sizes = (ctypes.c_int64 * len(caches))(*(c.numel() // nb * c.element_size() for c in caches))
-    return ptrs, sizes, len(caches), nb
+        at = c.data_ptr()
+        ptrs[i] = at
+        sizes[i] = total // nb
+        spans.append((at, at + total))
+    spans.sort()
+    for (_, end), (start, _) in zip(spans, spans[1:]):
+        if end > start:
+            raise ValueError("caches must not overlap")
+    return ptrs, sizes, count, nb, caches
 
 
 def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
@@ -739,16 +759,16 @@ def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
     with another one (a destination named twice, a source that is a destination) is skipped and
     sets DEV_BAD_BLOCK in status.
     """
-    ptrs, sizes, count, nb = _cache_list(caches)
+    ptrs, sizes, count, nb, caches = _cache_list(caches)
     for t in (src_blocks, dst_blocks):
         if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
             raise ValueError("src_blocks and dst_blocks must be contiguous int32 [num_pairs] tensors")
     if src_blocks.numel() != dst_blocks.numel():
         raise ValueError("src_blocks and dst_blocks must have one length")
     _check_status(status)
-    _check_device(src_blocks=src_blocks, dst_blocks=dst_blocks, status=status)
-    rc = LIB.kvfp8_copy_blocks(ptrs, sizes, count, nb, _ptr(src_blocks), _ptr(dst_blocks),
-                               src_blocks.numel(), _ptr(status), _stream(stream))
+    dev = _check_device(*caches, src_blocks, dst_blocks, status)
+    rc = LIB.kvfp8_copy_blocks(ptrs, sizes, count, nb, _addr(src_blocks), _addr(dst_blocks),
+                               src_blocks.numel(), _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_copy_blocks")
 
 
@@ -766,7 +786,7 @@ def compact_blocks(caches, block_tables: torch.Tensor, seq_lens: torch.Tensor, b
 
     new_block_tables may be block_tables itself.
     """
-    ptrs, sizes, count, nb = _cache_list(caches)
+    ptrs, sizes, count, nb, caches = _cache_list(caches)
     _check_tables(block_tables, seq_lens, seq_lens.numel())
     if new_block_tables is not None and (new_block_tables.dtype != torch.int32 or
                                          new_block_tables.shape != block_tables.shape or
@@ -777,19 +797,16 @@ def compact_blocks(caches, block_tables: torch.Tensor, seq_lens: torch.Tensor, b
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _check_status(status)
-    _check_device(block_tables=block_tables, seq_lens=seq_lens, new_block_tables=new_block_tables,
-                  num_used=num_used, workspace=workspace, status=status)
-    with _on(stream):
-        if new_block_tables is None:
-            new_block_tables = torch.empty_like(block_tables)
-        if num_used is None:
-            num_used = torch.empty(1, dtype=torch.int32, device=block_tables.device)
-        if workspace is None:
-            workspace = torch.empty(compact_blocks_workspace_size(nb), dtype=torch.uint8,
-                                    device=block_tables.device)
+    dev = _check_device(*caches, block_tables, seq_lens, new_block_tables, num_used, workspace, status)
+    if new_block_tables is None:
+        new_block_tables = _empty(block_tables.shape, torch.int32, dev, stream)
+    if num_used is None:
+        num_used = _empty(1, torch.int32, dev, stream)
+    if workspace is None:
+        workspace = _empty(compact_blocks_workspace_size(nb), torch.uint8, dev, stream)
     rc = LIB.kvfp8_compact_blocks(
-        ptrs, sizes, count, nb, block_size, _ptr(block_tables), block_tables.shape[1],
-        _ptr(seq_lens), seq_lens.numel(), _ptr(new_block_tables), _ptr(num_used), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+        ptrs, sizes, count, nb, block_size, _addr(block_tables), block_tables.shape[1],
+        _addr(seq_lens), seq_lens.numel(), _addr(new_block_tables), _addr(num_used), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_compact_blocks")
     return new_block_tables, num_used
