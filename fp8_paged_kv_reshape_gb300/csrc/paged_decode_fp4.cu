@@ -28,12 +28,27 @@
 namespace kvfp8 {
 namespace {
 
+constexpr int kTok = 32;  // tokens of a chunk: two 16-token tiles
+constexpr float kLag = 8.f;  // log2: how far scores may rise above the reference maximum
+
 struct Fp4KernelArgs {
     KernelArgs k;
-    uint32_t code_box;   // bytes of one code box (hpc heads x box_rows tokens)
-    uint32_t scale_box;  // smem bytes of one scale box, rounded up to 128
+    uint32_t code_box;         // bytes of one code box (hpc heads x box_rows tokens)
+    uint32_t scale_box;        // smem bytes of one scale box, rounded up to 128
     uint32_t scale_box_bytes;  // bytes a scale box brings
     uint32_t stage_bytes;
+    // Offsets within a side of a chunk's 8-token groups: group g starts at (g & 1) * x1 + (g >> 1)
+    // * x2 past the head's first row (codes, scales).
+    uint32_t c1, c2, s1, s2;
+};
+
+// A chunk's record: bit t of mask is set when token tok0 + t exists (within the length, in a
+// block of the pool).
+struct Fp4Chunk {
+    int32_t seq;
+    int32_t tok0;
+    uint32_t mask;
+    int32_t flags;
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
@@ -94,12 +109,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     const int S = a.stages;
     const int hpc = a.hpc, h0 = static_cast<int>(blockIdx.y) * hpc;
     const uint32_t stage_bytes = f.stage_bytes;
-    // a stage: K codes, V codes (a 16-token chunk each), K scale boxes, V scale boxes
-    const uint32_t code_bytes = static_cast<uint32_t>(kChunkTokens * hpc * SEG);
-    const int boxes_per_chunk = kChunkTokens / a.box_rows;  // 1 or 2
-    const uint32_t scales_off = 2 * code_bytes, vscales_off = scales_off + boxes_per_chunk * f.scale_box;
+    // a stage: the chunk's K code boxes, V code boxes, K scale boxes, V scale boxes
+    const uint32_t code_bytes = static_cast<uint32_t>(kTok * hpc * SEG);
+    const uint32_t scales_off = 2 * code_bytes, vscales_off = scales_off + kTok / a.box_rows * f.scale_box;
     const uint32_t bars = base + static_cast<uint32_t>(S) * stage_bytes;  // full[S], empty[S]
-    ChunkMeta *meta = reinterpret_cast<ChunkMeta *>(base_ptr + S * stage_bytes + 16 * S);
+    Fp4Chunk *meta = reinterpret_cast<Fp4Chunk *>(base_ptr + S * stage_bytes + 16 * S);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(meta + S);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,71 +164,68 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int wbase = -1 << 30;  // first block-table entry held in the lane window
         int32_t win = 0;
         prefetch_q<HD>(a, s, h0, lane);
+        const int lbr = 31 - __clz(a.box_rows), lbs = 31 - __clz(a.block_size);  // powers of two
         for (int64_t x = chunk_lo; x < chunk_hi; ++x) {
             if (x >= ce) {
                 while (x >= ce) {
                     ++s;
                     cs = ce;
-                    ce = cs + seq_chunks(a, s, L);
+                    ce = cs + seq_chunks<kTok>(a, s, L);
                 }
                 wbase = -1 << 30;
                 prefetch_q<HD>(a, s, h0, lane);
             }
-            const int j = static_cast<int>(x - cs);
-            const int tok0 = j * kChunkTokens;
-            int nvalid = min(kChunkTokens, L - tok0);
-            const int nloads = (nvalid + a.box_rows - 1) / a.box_rows;
-            const int e0 = tok0 / a.block_size;
-            if (e0 < wbase || e0 + nloads - 1 >= wbase + 32) {
+            // lane p < nloads has box p of the chunk (every side and both arrays of it)
+            const int tok0 = static_cast<int>(x - cs) * kTok;
+            const int nvalid = min(kTok, L - tok0);
+            const int nloads = (nvalid + a.box_rows - 1) >> lbr;
+            const int e0 = tok0 >> lbs, e1 = (tok0 + nvalid - 1) >> lbs;
+            if (e0 < wbase || e1 >= wbase + 32) {
                 wbase = e0;
                 const int e = wbase + lane;
                 win = (e < a.max_blocks_per_seq)
                           ? a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + e]
                           : -1;
             }
-            int blks[2], offs[2];
-            bool ok = true;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int t = tok0 + p * a.box_rows;
-                blks[p] = __shfl_sync(0xFFFFFFFFu, win, (t / a.block_size - wbase) & 31);
-                offs[p] = t % a.block_size;
-                if (p < nloads) ok = ok && blks[p] >= 0 && blks[p] < a.num_blocks;
+            const int t = tok0 + (lane << lbr);
+            const int blk = __shfl_sync(0xFFFFFFFFu, win, ((t >> lbs) - wbase) & 31);
+            const bool mine = lane < nloads;
+            const bool good = mine && blk >= 0 && blk < a.num_blocks;
+            if (mine && !good) flag(a.status, KVFP8_DEV_BAD_BLOCK);
+            uint32_t bits = 0;  // this box's tokens
+            if (good) {
+                const int first = lane << lbr, n = min(a.box_rows, nvalid - first);
+                bits = (n == 32 ? ~0u : (1u << n) - 1u) << first;
             }
+            const uint32_t mask = __reduce_or_sync(0xFFFFFFFFu, bits);
+            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, good));
             int32_t flags = 0;
             if (x == chunk_lo || x == cs) flags |= kFirst;
             if (x == chunk_hi - 1 || x == ce - 1) flags |= kLast;
             if (cs >= chunk_lo && ce <= chunk_hi) flags |= kDirect;
+            const uint32_t full = bars + 8 * stage;
             if (lane == 0) {
                 if (!mbar_wait(bars + 8 * (S + stage), phase ^ 1u, abort_flag)) {
                     aborted = true;
                 } else {
-                    if (!ok) {
-                        flag(a.status, KVFP8_DEV_BAD_BLOCK);
-                        nvalid = 0;
-                    }
-                    meta[stage] = ChunkMeta{s, tok0, nvalid, flags};
-                    const uint32_t full = bars + 8 * stage;
-                    if (nvalid > 0) {
-                        mbar_arrive_tx(full, nloads * 2 * (f.code_box + f.scale_box_bytes));
-                        const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            if (p >= nloads) break;
-                            const int row = blks[p] * a.block_size + offs[p];
-                            tma_load_3d(st + p * f.code_box, &tmk, 0, row, h0, full);
-                            tma_load_3d(st + code_bytes + p * f.code_box, &tmv, 0, row, h0, full);
-                            const int sx = offs[p] * GPH, sy = blks[p] * a.n_kv + h0;
-                            tma_load_2d(st + scales_off + p * f.scale_box, &tmks, sx, sy, full);
-                            tma_load_2d(st + vscales_off + p * f.scale_box, &tmvs, sx, sy, full);
-                        }
-                    } else {
+                    meta[stage] = Fp4Chunk{s, tok0, mask, flags};
+                    if (boxes > 0)
+                        mbar_arrive_tx(full, boxes * 2 * (f.code_box + f.scale_box_bytes));
+                    else
                         mbar_arrive(full);
-                    }
                 }
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
             if (aborted) break;
+            if (good) {  // the expected bytes are posted: each lane copies its box
+                const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
+                const int off = t & (a.block_size - 1), row = (blk << lbs) + off;
+                const int sx = off * GPH / 4, sy = blk * a.n_kv + h0;
+                tma_load_3d(st + lane * f.code_box, &tmk, 0, row, h0, full);
+                tma_load_3d(st + code_bytes + lane * f.code_box, &tmv, 0, row, h0, full);
+                tma_load_2d(st + scales_off + lane * f.scale_box, &tmks, sx, sy, full);
+                tma_load_2d(st + vscales_off + lane * f.scale_box, &tmvs, sx, sy, full);
+            }
             ++issued;
             if (++stage == S) {
                 stage = 0;
@@ -226,7 +237,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 if (!mbar_wait(bars + 8 * (S + stage), phase ^ 1u, abort_flag)) {
                     aborted = true;
                 } else {
-                    meta[stage] = ChunkMeta{0, 0, 0, kDone};
+                    meta[stage] = Fp4Chunk{0, 0, 0, kDone};
                     mbar_arrive(bars + 8 * stage);
                 }
             }
@@ -247,9 +258,12 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         // ------------------------------------------------------------ consumer warp
         const int kvh = h0 + warp;
         const int gid = lane >> 2, tig = lane & 3;
-        const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
+        float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
+        if (score_scale == 0.f) score_scale = 0x1p-126f;  // underflow: equal weights, -inf stays -inf
 
         float o[KP][2][NT][4];
+        // per score column: the reference maximum (log2 domain) the weights are taken against, and
+        // this lane's part of the sum of weights
         float m[NT][2], l[NT][2];
         uint32_t qb[KP][NT][4];
         // multi-query form: per score column (query token j, head g) the last cache position it
@@ -257,15 +271,12 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int plim[NT][2], crow[NT][2];
         int q0 = 0, first_lim = 0;  // first_lim: the smallest plim of the sequence's columns
 
-        // Offsets of this lane in a stage.  Row r of a chunk: its 8-row half r >> 3 starts at
-        // half_codes / half_scales, row r & 7 within it.
-        const uint32_t half_codes = a.box_rows == kChunkTokens ? 8u * SEG : f.code_box;
-        const uint32_t half_scales = a.box_rows == kChunkTokens ? 8u * GPH : f.scale_box;
+        // Offsets of this lane in a stage, for the first 16-token tile (the second: c2, s2 further).
         const uint32_t head_codes = static_cast<uint32_t>(warp * a.box_rows * SEG);
         const uint32_t head_scales = static_cast<uint32_t>(warp * a.box_rows * GPH);
-        const uint32_t krow_off = head_codes + ((lane >> 3) & 1) * half_codes;
+        const uint32_t krow_off = head_codes + ((lane >> 3) & 1) * f.c1;
         const int kchunk_hi = lane >> 4;
-        const uint32_t vrow_off = code_bytes + head_codes + (lane >> 4) * half_codes;
+        const uint32_t vrow_off = code_bytes + head_codes + (lane >> 4) * f.c1;
         const int vchunk_hi = (lane >> 3) & 1;
         const uint32_t ks_off = scales_off + head_scales + gid * GPH;
         const uint32_t vs_off = vscales_off + head_scales + 2 * tig * GPH;
@@ -282,7 +293,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
                 break;
             }
-            const ChunkMeta mt = meta[stage];
+            const Fp4Chunk mt = meta[stage];
             if (mt.flags & kDone) break;
 
             if (mt.flags & kFirst) {
@@ -335,184 +346,231 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             for (int r = 0; r < 4; ++r) o[e][j][nt][r] = 0.f;
             }
 
-            const int nvalid = mt.nvalid;
-            if (nvalid > 0) {
+            if (mt.mask != 0u) {
                 const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
 
-                // ---- scores S^T[token][head] = K . q^T
-                uint32_t sc_lo[KP / 2], sc_hi[KP / 2];  // bytes of this lane's groups, rows gid and +8
-                {
-                    uint32_t wl[GPH / 4], wh[GPH / 4];
-                    lds(st + ks_off, wl);
-                    lds(st + ks_off + half_scales, wh);
-                    if constexpr (KP == 2) {
-                        sc_lo[0] = __byte_perm(wl[0], 0u, ksel);
-                        sc_hi[0] = __byte_perm(wh[0], 0u, ksel);
-                    } else {
+                // ---- scores S^T[token][head] = K . q^T, two tiles of 16 tokens
+                float sacc[2][NT][4];
 #pragma unroll
-                        for (int i = 0; i < KP / 2; i += 2) {
-                            const uint32_t bl = __byte_perm(wl[i], wl[i + 1], ksel);
-                            const uint32_t bh = __byte_perm(wh[i], wh[i + 1], ksel);
-                            sc_lo[i] = bl;
-                            sc_lo[i + 1] = bl >> 16;
-                            sc_hi[i] = bh;
-                            sc_hi[i + 1] = bh >> 16;
+                for (int tt = 0; tt < 2; ++tt) {
+                    uint32_t sc_lo[KP / 2], sc_hi[KP / 2];  // bytes of this lane's groups, rows gid and +8
+                    {
+                        uint32_t wl[GPH / 4], wh[GPH / 4];
+                        lds(st + ks_off + tt * f.s2, wl);
+                        lds(st + ks_off + tt * f.s2 + f.s1, wh);
+                        if constexpr (KP == 2) {
+                            sc_lo[0] = __byte_perm(wl[0], 0u, ksel);
+                            sc_hi[0] = __byte_perm(wh[0], 0u, ksel);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < KP / 2; i += 2) {
+                                const uint32_t bl = __byte_perm(wl[i], wl[i + 1], ksel);
+                                const uint32_t bh = __byte_perm(wh[i], wh[i + 1], ksel);
+                                sc_lo[i] = bl;
+                                sc_lo[i + 1] = bl >> 16;
+                                sc_hi[i] = bh;
+                                sc_hi[i + 1] = bh >> 16;
+                            }
                         }
                     }
-                }
-                float sacc[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
+                        sacc[tt][nt][0] = sacc[tt][nt][1] = sacc[tt][nt][2] = sacc[tt][nt][3] = 0.f;
 #pragma unroll
-                for (int cp = 0; cp < KP / 2; ++cp) {
-                    uint32_t r[4];
-                    ldsm_x4(st + krow_off + swz<SEG>(lane & 7, 2 * cp + kchunk_hi), r[0], r[1], r[2], r[3]);
-                    const uint32_t fl = f16x2_from_e4m3x2(sc_lo[cp]), fh = f16x2_from_e4m3x2(sc_hi[cp]);
+                    for (int cp = 0; cp < KP / 2; ++cp) {
+                        uint32_t r[4];
+                        ldsm_x4(st + krow_off + tt * f.c2 + swz<SEG>(lane & 7, 2 * cp + kchunk_hi), r[0], r[1],
+                                r[2], r[3]);
+                        const uint32_t fl = f16x2_from_e4m3x2(sc_lo[cp]), fh = f16x2_from_e4m3x2(sc_hi[cp]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {  // chunk 2cp + e
-                        const uint32_t sl = __byte_perm(fl, 0u, e ? 0x3232 : 0x1010);
-                        const uint32_t sh = __byte_perm(fh, 0u, e ? 0x3232 : 0x1010);
-                        uint32_t ka[4], kb[4];
-                        f16x2_from_e2m1x8(r[2 * e], ka);
-                        f16x2_from_e2m1x8(r[2 * e + 1], kb);
+                        for (int e = 0; e < 2; ++e) {  // chunk 2cp + e
+                            const uint32_t sl = __byte_perm(fl, 0u, e ? 0x3232 : 0x1010);
+                            const uint32_t sh = __byte_perm(fh, 0u, e ? 0x3232 : 0x1010);
+                            uint32_t ka[4], kb[4];
+                            f16x2_from_e2m1x8(r[2 * e], ka);
+                            f16x2_from_e2m1x8(r[2 * e + 1], kb);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            ka[i] = hmul2(ka[i], sl);
-                            kb[i] = hmul2(kb[i], sh);
-                        }
+                            for (int i = 0; i < 4; ++i) {
+                                ka[i] = hmul2(ka[i], sl);
+                                kb[i] = hmul2(kb[i], sh);
+                            }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t(&q)[4] = qb[2 * cp + e][nt];
-                            mma16816(sacc[nt], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
-                            mma16816(sacc[nt], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t(&q)[4] = qb[2 * cp + e][nt];
+                                mma16816(sacc[tt][nt], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
+                                mma16816(sacc[tt][nt], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
+                            }
                         }
                     }
                 }
 
-                // ---- online softmax per head column (log2 domain)
-                const bool lo_ok = gid < nvalid, hi_ok = gid + 8 < nvalid;
-                uint32_t pb[NT][2];
+                // ---- weights 2^(score - m) per head column (log2 domain).  m only has to be near the
+                // running maximum: it moves when a score passes it by more than kLag, so most chunks
+                // take no maximum over the lanes and rescale nothing, and weights stay <= 2^kLag.
+                // Tokens a column does not see get -inf (chunks with such tokens only).
+                const bool partial = mt.mask != ~0u || (kMulti && mt.tok0 + kTok - 1 > first_lim);
+                auto sees = [&](int row, int nt, int c) {  // row of the chunk
+                    return ((mt.mask >> row) & 1u) != 0u && (!kMulti || mt.tok0 + row <= plim[nt][c]);
+                };
+                if (partial) {  // a score of -inf (whatever the scale's sign), a weight of 0
+                    const float none = score_scale > 0.f ? -INFINITY : INFINITY;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (!sees(16 * tt + 8 * h + gid, nt, c)) sacc[tt][nt][c + 2 * h] = none;
+                }
+                float top = -INFINITY;  // the highest score over its column's m
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        bool lo_c = lo_ok, hi_c = hi_ok;
-                        if (kMulti) {  // causal: token tok0+row is visible up to plim
-                            lo_c = lo_c && mt.tok0 + gid <= plim[nt][c];
-                            hi_c = hi_c && mt.tok0 + gid + 8 <= plim[nt][c];
-                        }
-                        const float s_lo = lo_c ? sacc[nt][c] * score_scale : -INFINITY;
-                        const float s_hi = hi_c ? sacc[nt][c + 2] * score_scale : -INFINITY;
-                        float mx = fmaxf(s_lo, s_hi);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                        const float m_old = m[nt][c];
-                        const float m_new = fmaxf(m_old, mx);
-                        const float alpha = (m_old == -INFINITY) ? 0.f : ex2(m_old - m_new);
-                        // a column that has seen no visible (or only NaN) tokens yet
-                        const float m_sub = (m_new == -INFINITY) ? 0.f : m_new;
-                        p[c] = ex2(s_lo - m_sub);
-                        p[c + 2] = ex2(s_hi - m_sub);
-                        // (no running sum to rescale before the first maximum; a NaN in it stays)
-                        l[nt][c] = (m_old == -INFINITY ? l[nt][c] : l[nt][c] * alpha) + p[c] + p[c + 2];
-                        m[nt][c] = m_new;
-                        if (alpha != 1.f && m_old != -INFINITY) {
-#pragma unroll
-                            for (int e = 0; e < KP; ++e)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    o[e][j][nt][c] *= alpha;
-                                    o[e][j][nt][c + 2] *= alpha;
-                                }
-                        }
+                        const float a0 = sacc[0][nt][c], a1 = sacc[0][nt][c + 2];
+                        const float a2 = sacc[1][nt][c], a3 = sacc[1][nt][c + 2];
+                        const float x = score_scale > 0.f ? fmaxf(fmaxf(a0, a1), fmaxf(a2, a3))
+                                                          : fminf(fminf(a0, a1), fminf(a2, a3));
+                        // (m starts at -inf, which any score passes; a column of -inf passes nothing)
+                        top = fmaxf(top, x * score_scale - m[nt][c]);
                     }
-                    pb[nt][0] = movm_t(f16x2_from_f32(p[0], p[1]));  // tokens 0-7
-                    pb[nt][1] = movm_t(f16x2_from_f32(p[2], p[3]));  // tokens 8-15
+                if (__any_sync(0xFFFFFFFFu, top > kLag)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float a0 = sacc[0][nt][c], a1 = sacc[0][nt][c + 2];
+                            const float a2 = sacc[1][nt][c], a3 = sacc[1][nt][c + 2];
+                            float x = score_scale > 0.f ? fmaxf(fmaxf(a0, a1), fmaxf(a2, a3))
+                                                        : fminf(fminf(a0, a1), fminf(a2, a3));
+                            x *= score_scale;
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                            if (x > m[nt][c]) {
+                                // nothing but zeros (or a NaN, which stays) before the first score
+                                const float alpha = m[nt][c] == -INFINITY ? 1.f : ex2(m[nt][c] - x);
+                                m[nt][c] = x;
+                                l[nt][c] *= alpha;
+#pragma unroll
+                                for (int e = 0; e < KP; ++e)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        o[e][j][nt][c] *= alpha;
+                                        o[e][j][nt][c + 2] *= alpha;
+                                    }
+                            }
+                        }
+                }
+                uint32_t pb[2][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // a column that has seen no score yet: -inf - 0 for every token
+                        const float sub = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+#pragma unroll
+                        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float p = ex2(fmaf(sacc[tt][nt][c + 2 * h], score_scale, -sub));
+                                sacc[tt][nt][c + 2 * h] = p;
+                            }
+                        l[nt][c] += (sacc[0][nt][c] + sacc[0][nt][c + 2]) + (sacc[1][nt][c] + sacc[1][nt][c + 2]);
+                    }
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)  // tokens 16 tt + 8 h ..+7
+                            pb[tt][nt][h] = movm_t(f16x2_from_f32(sacc[tt][nt][2 * h], sacc[tt][nt][2 * h + 1]));
                 }
 
                 // ---- O^T[dim][head] += V^T . P^T
-                uint32_t vs_lo[KP], vs_hi[KP];  // scale pairs of tokens 2t, 2t+1 and 2t+8, 2t+9
-                {
-                    uint32_t wl[GPH / 2], wh[GPH / 2];  // the two tokens' scale bytes
-                    lds(st + vs_off, wl);
-                    lds(st + vs_off + half_scales, wh);
 #pragma unroll
-                    for (int i = 0; i < GPH / 4; ++i) {
-                        const uint32_t bl = __byte_perm(wl[i], wl[i + GPH / 4], vsel);
-                        const uint32_t bh = __byte_perm(wh[i], wh[i + GPH / 4], vsel);
-                        vs_lo[2 * i] = f16x2_from_e4m3x2(bl);
-                        vs_lo[2 * i + 1] = f16x2_from_e4m3x2_hi(bl);
-                        vs_hi[2 * i] = f16x2_from_e4m3x2(bh);
-                        vs_hi[2 * i + 1] = f16x2_from_e4m3x2_hi(bh);
-                    }
-                }
-                if (nvalid < kChunkTokens) {  // zero the scales of tokens past the end
-                    const uint32_t mlo = (2 * tig < nvalid ? 0x0000FFFFu : 0u) |
-                                         (2 * tig + 1 < nvalid ? 0xFFFF0000u : 0u);
-                    const uint32_t mhi = (2 * tig + 8 < nvalid ? 0x0000FFFFu : 0u) |
-                                         (2 * tig + 9 < nvalid ? 0xFFFF0000u : 0u);
+                for (int tt = 0; tt < 2; ++tt) {
+                    uint32_t vs_lo[KP], vs_hi[KP];  // scale pairs of tokens 2t, 2t+1 and 2t+8, 2t+9
+                    {
+                        uint32_t wl[GPH / 2], wh[GPH / 2];  // the two tokens' scale bytes
+                        lds(st + vs_off + tt * f.s2, wl);
+                        lds(st + vs_off + tt * f.s2 + f.s1, wh);
 #pragma unroll
-                    for (int c = 0; c < KP; ++c) {
-                        vs_lo[c] &= mlo;
-                        vs_hi[c] &= mhi;
-                    }
-                }
-                if (kMulti && mt.tok0 + kChunkTokens - 1 > first_lim) {
-                    // Some column does not see all of the chunk, and its weights are 0 there: a
-                    // NaN scale would make 0 * NaN of them.
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int c = 0; c < KP; ++c) any |= nan_ones(vs_lo[c]) | nan_ones(vs_hi[c]);
-                    if (__any_sync(0xFFFFFFFFu, any != 0u)) {
-                        uint32_t sb[NT][2];  // fp16 ones where the column sees the token
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            auto seen = [&](int row, int c) {
-                                return row < nvalid && mt.tok0 + row <= plim[nt][c] ? 0x3C00u : 0u;
-                            };
-                            sb[nt][0] = movm_t(seen(gid, 0) | seen(gid, 1) << 16);
-                            sb[nt][1] = movm_t(seen(gid + 8, 0) | seen(gid + 8, 1) << 16);
+                        for (int i = 0; i < GPH / 4; ++i) {
+                            const uint32_t bl = __byte_perm(wl[i], wl[i + GPH / 4], vsel);
+                            const uint32_t bh = __byte_perm(wh[i], wh[i + GPH / 4], vsel);
+                            vs_lo[2 * i] = f16x2_from_e4m3x2(bl);
+                            vs_lo[2 * i + 1] = f16x2_from_e4m3x2_hi(bl);
+                            vs_hi[2 * i] = f16x2_from_e4m3x2(bh);
+                            vs_hi[2 * i + 1] = f16x2_from_e4m3x2_hi(bh);
                         }
+                    }
+                    if (partial) {
+                        // tokens that are not there: scale 0
+                        const uint32_t bits = mt.mask >> (16 * tt + 2 * tig);
+                        const uint32_t mlo = (bits & 1u ? 0x0000FFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
+                        const uint32_t mhi = (bits & 0x100u ? 0x0000FFFFu : 0u) | (bits & 0x200u ? 0xFFFF0000u : 0u);
 #pragma unroll
                         for (int c = 0; c < KP; ++c) {
-                            const uint32_t nl = nan_ones(vs_lo[c]), nh = nan_ones(vs_hi[c]);
+                            vs_lo[c] &= mlo;
+                            vs_hi[c] &= mhi;
+                        }
+                        if (kMulti) {
+                            // A column that does not see a token has weight 0 for it, and a NaN scale would
+                            // make 0 * NaN of that.
+                            uint32_t any = 0;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                // NaN tokens per (dims of the lane's group, column)
-                                float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma16816(cnt, nl, nl, nh, nh, sb[nt][0], sb[nt][1]);
+                            for (int c = 0; c < KP; ++c) any |= nan_ones(vs_lo[c]) | nan_ones(vs_hi[c]);
+                            if (__any_sync(0xFFFFFFFFu, any != 0u)) {
+                                uint32_t sb[NT][2];  // fp16 ones where the column sees the token
 #pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    if (cnt[r] > 0.f)
-                                        o[c][0][nt][r] = o[c][1][nt][r] = __uint_as_float(0x7FC00000u);
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const int row = 16 * tt + 8 * h + gid;
+                                        sb[nt][h] = movm_t((sees(row, nt, 0) ? 0x3C00u : 0u) |
+                                                           (sees(row, nt, 1) ? 0x3C000000u : 0u));
+                                    }
+#pragma unroll
+                                for (int c = 0; c < KP; ++c) {
+                                    const uint32_t nl = nan_ones(vs_lo[c]), nh = nan_ones(vs_hi[c]);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        // NaN tokens per (dims of the lane's group, column)
+                                        float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma16816(cnt, nl, nl, nh, nh, sb[nt][0], sb[nt][1]);
+#pragma unroll
+                                        for (int r = 0; r < 4; ++r)
+                                            if (cnt[r] > 0.f)
+                                                o[c][0][nt][r] = o[c][1][nt][r] = __uint_as_float(0x7FC00000u);
+                                    }
+                                    vs_lo[c] &= ~(nl / 0x3C00u * 0xFFFFu);
+                                    vs_hi[c] &= ~(nh / 0x3C00u * 0xFFFFu);
+                                }
                             }
-                            vs_lo[c] &= ~(nl / 0x3C00u * 0xFFFFu);
-                            vs_hi[c] &= ~(nh / 0x3C00u * 0xFFFFu);
                         }
                     }
-                }
 #pragma unroll
-                for (int cp = 0; cp < KP / 2; ++cp) {
-                    uint32_t r[4];
-                    ldsm_x4_t(st + vrow_off + swz<SEG>(lane & 7, 2 * cp + vchunk_hi), r[0], r[1], r[2], r[3]);
+                    for (int cp = 0; cp < KP / 2; ++cp) {
+                        uint32_t r[4];
+                        ldsm_x4_t(st + vrow_off + tt * f.c2 + swz<SEG>(lane & 7, 2 * cp + vchunk_hi), r[0], r[1],
+                                  r[2], r[3]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {  // chunk 2cp + e: tokens 0-7 in r[e], 8-15 in r[2+e]
-                        uint32_t x[4], y[4];
-                        f16x2_from_e2m1x8(r[e], x);
-                        f16x2_from_e2m1x8(r[2 + e], y);
-                        const uint32_t sl = vs_lo[2 * cp + e], sh = vs_hi[2 * cp + e];
+                        for (int e = 0; e < 2; ++e) {  // chunk 2cp + e: tokens 0-7 in r[e], 8-15 in r[2+e]
+                            uint32_t x[4], y[4];
+                            f16x2_from_e2m1x8(r[e], x);
+                            f16x2_from_e2m1x8(r[2 + e], y);
+                            const uint32_t sl = vs_lo[2 * cp + e], sh = vs_hi[2 * cp + e];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {  // dims 4g + 2j, 4g + 2j + 1
-                            const uint32_t a0 = hmul2(__byte_perm(x[j], x[j + 2], 0x5410), sl);
-                            const uint32_t a1 = hmul2(__byte_perm(x[j], x[j + 2], 0x7632), sl);
-                            const uint32_t a2 = hmul2(__byte_perm(y[j], y[j + 2], 0x5410), sh);
-                            const uint32_t a3 = hmul2(__byte_perm(y[j], y[j + 2], 0x7632), sh);
+                            for (int j = 0; j < 2; ++j) {  // dims 4g + 2j, 4g + 2j + 1
+                                const uint32_t a0 = hmul2(__byte_perm(x[j], x[j + 2], 0x5410), sl);
+                                const uint32_t a1 = hmul2(__byte_perm(x[j], x[j + 2], 0x7632), sl);
+                                const uint32_t a2 = hmul2(__byte_perm(y[j], y[j + 2], 0x5410), sh);
+                                const uint32_t a3 = hmul2(__byte_perm(y[j], y[j + 2], 0x7632), sh);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816(o[2 * cp + e][j][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816(o[2 * cp + e][j][nt], a0, a1, a2, a3, pb[tt][nt][0], pb[tt][nt][1]);
+                            }
                         }
                     }
                 }
@@ -585,17 +643,17 @@ cudaError_t encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, i
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Scales as a 2-D byte tensor (a head's bytes of a block, block * n_kv + head).  A box starts at
-// a multiple of 8 tokens, so at a multiple of 32 bytes.
+// Scales as a 2-D tensor of words of four bytes (a head's words of a block, block * n_kv + head).
+// A box starts at a multiple of 8 tokens, so at a multiple of 32 bytes.
 cudaError_t encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t block_heads, int head_bytes,
                           int box_bytes, int hpc) {
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_bytes), static_cast<cuuint64_t>(block_heads)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_bytes / 4), static_cast<cuuint64_t>(block_heads)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_bytes)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(hpc)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes / 4), static_cast<cuuint32_t>(hpc)};
     const cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(scales), dims,
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t *>(scales), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -613,15 +671,20 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     int hpc = std::min(d.n_kv, kMaxKvHeads);
     while (d.n_kv % hpc != 0) --hpc;
     const int groups = d.n_kv / hpc;
-    const int box_rows = std::min(d.block_size, kChunkTokens);
+    const int box_rows = std::min(d.block_size, kTok);
     Fp4KernelArgs f;
     f.code_box = static_cast<uint32_t>(hpc * box_rows * (HD / 2));
     f.scale_box_bytes = static_cast<uint32_t>(hpc * box_rows * (HD / 16));
     f.scale_box = (f.scale_box_bytes + 127u) & ~127u;
-    const uint32_t boxes = kChunkTokens / box_rows;
+    const uint32_t boxes = kTok / box_rows;
     f.stage_bytes = (2 * boxes * (f.code_box + f.scale_box) + 1023u) & ~1023u;
+    // two 8-token groups a box of 16, four a box of 32, one a box of 8
+    f.c1 = box_rows >= 16 ? 8 * (HD / 2) : f.code_box;
+    f.c2 = box_rows == 32 ? 16 * (HD / 2) : box_rows == 16 ? f.code_box : 2 * f.code_box;
+    f.s1 = box_rows >= 16 ? 8 * (HD / 16) : f.scale_box;
+    f.s2 = box_rows == 32 ? 16 * (HD / 16) : box_rows == 16 ? f.scale_box : 2 * f.scale_box;
     const int ctas_per_sm = fp4_ctas_per_sm<HD, NT>();
-    constexpr int kMaxStages = 12;
+    constexpr int kMaxStages = 8;
     auto smem_for = [&](int st) { return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024; };
     const size_t sm_budget = static_cast<size_t>(smem_optin) + 1024;
     int stages = kMaxStages;
@@ -679,7 +742,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     k.rows_per_seq = d.qmax * d.n_q;
     k.qrows = d.qrows;
 
-    plan_kernel<<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
+    plan_kernel<kTok><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
                                         num_ctas, reinterpret_cast<int32_t *>(w + ws.cstart_off),
                                         reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
                                         d.n_q * HD, d.status);

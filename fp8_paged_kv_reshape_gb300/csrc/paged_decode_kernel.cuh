@@ -278,13 +278,14 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 
 // Per-call plan, one CTA of 1024 threads:
-//  * cstart[s] = first chunk of sequence s (exclusive prefix of its 16-token chunk
+//  * cstart[s] = first chunk of sequence s (exclusive prefix of its kTok-token chunk
 //    counts), cstart[num_seqs] = total;
 //  * the output rows of empty sequences are zeroed (no CTA visits them);
 //  * one CtaPlan record per decode CTA (the prefix and the clamped lengths are kept in
 //    shared memory when they fit, else read back from global memory).
 constexpr int kPlanSmemSeqs = 4096;
 
+template <int kTok>
 __global__ void __launch_bounds__(1024)
 plan_kernel(const int32_t *seq_lens, const int32_t *qsl, int32_t qmax, int32_t qrows,
             int32_t num_seqs, int32_t max_len, int32_t num_ctas, int32_t *cstart,
@@ -314,7 +315,7 @@ plan_kernel(const int32_t *seq_lens, const int32_t *qsl, int32_t qmax, int32_t q
                 if (nq != raw) flag(status, KVFP8_DEV_BAD_BLOCK);  // rows out of range: skipped
                 if (nq > L) flag(status, KVFP8_DEV_BAD_BLOCK);     // positions below zero
             }
-            n = nq > 0 ? (L + kChunkTokens - 1) / kChunkTokens : 0;
+            n = nq > 0 ? (L + kTok - 1) / kTok : 0;
             if (in_smem) len_smem[i] = L;
         }
         unsigned empty = __ballot_sync(0xFFFFFFFFu, i < num_seqs && n == 0);
@@ -384,12 +385,13 @@ plan_kernel(const int32_t *seq_lens, const int32_t *qsl, int32_t qmax, int32_t q
     }
 }
 
-// Chunks of sequence i (and its clamped length): 16-token chunks of its L cached tokens, or
+// Chunks of sequence i (and its clamped length): kTok-token chunks of its L cached tokens, or
 // none when it has no query rows.  The same rule the plan kernel applies.
+template <int kTok>
 __device__ __forceinline__ int seq_chunks(const KernelArgs &a, int i, int &L) {
     L = min(max(a.seq_lens[i], 0), a.max_len);
     const int nq = a.qsl ? query_range(a.qsl, i, a.rows_per_seq / a.n_q, a.qrows).count : 1;
-    return nq > 0 ? (L + kChunkTokens - 1) / kChunkTokens : 0;
+    return nq > 0 ? (L + kTok - 1) / kTok : 0;
 }
 
 // Bring the query rows a CTA's consumers will read for sequence s (its head group's rows,
@@ -624,7 +626,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ C
                     while (x >= ce) {
                         ++s;
                         cs = ce;
-                        ce = cs + seq_chunks(a, s, L);
+                        ce = cs + seq_chunks<kChunkTokens>(a, s, L);
                     }
                     wbase = -1 << 30;
                     prefetch_q<HD>(a, s, h0, lane);
@@ -1265,7 +1267,7 @@ cudaError_t run(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t str
     k.k_bf16 = KT16 ? 1 : 0;
     k.v_bf16 = VT16 ? 1 : 0;
 
-    plan_kernel<<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
+    plan_kernel<kChunkTokens><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
                                         num_ctas, reinterpret_cast<int32_t *>(w + ws.cstart_off),
                                         reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
                                         d.n_q * HD, d.status);
