@@ -25,6 +25,8 @@
 //    made NaN from a product of indicators.
 #include "paged_decode_kernel.cuh"
 
+#include <type_traits>
+
 namespace kvfp8 {
 namespace {
 
@@ -346,8 +348,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             for (int r = 0; r < 4; ++r) o[e][j][nt][r] = 0.f;
             }
 
-            if (mt.mask != 0u) {
-                const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
+            const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
+            // kPartial: some column does not see some token of the chunk.  The common chunk has a body
+            // without those tests: one basic block from the weights to the last product.
+            auto chunk = [&](auto partial_tag) {
+                constexpr bool kPartial = decltype(partial_tag)::value;
 
                 // ---- scores S^T[token][head] = K . q^T, two tiles of 16 tokens
                 float sacc[2][NT][4];
@@ -408,11 +413,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 // running maximum: it moves when a score passes it by more than kLag, so most chunks
                 // take no maximum over the lanes and rescale nothing, and weights stay <= 2^kLag.
                 // Tokens a column does not see get -inf (chunks with such tokens only).
-                const bool partial = mt.mask != ~0u || (kMulti && mt.tok0 + kTok - 1 > first_lim);
                 auto sees = [&](int row, int nt, int c) {  // row of the chunk
                     return ((mt.mask >> row) & 1u) != 0u && (!kMulti || mt.tok0 + row <= plim[nt][c]);
                 };
-                if (partial) {  // a score of -inf (whatever the scale's sign), a weight of 0
+                if constexpr (kPartial) {  // a score of -inf (whatever the scale's sign), a weight of 0
                     const float none = score_scale > 0.f ? -INFINITY : INFINITY;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -505,7 +509,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             vs_hi[2 * i + 1] = f16x2_from_e4m3x2_hi(bh);
                         }
                     }
-                    if (partial) {
+                    if constexpr (kPartial) {
                         // tokens that are not there: scale 0
                         const uint32_t bits = mt.mask >> (16 * tt + 2 * tig);
                         const uint32_t mlo = (bits & 1u ? 0x0000FFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
@@ -574,7 +578,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         }
                     }
                 }
-            }
+            };
+            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim))
+                chunk(std::false_type{});
+            else if (mt.mask != 0u)
+                chunk(std::true_type{});
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + 8 * (S + stage));
             if (++stage == S) {
