@@ -84,17 +84,51 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
     }
 }
 
+// one half of an fp16 pair in both halves (an operand selector of the packed multiply)
+__device__ __forceinline__ uint32_t bcast_lo(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t bcast_hi(uint32_t x) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// A token's scale bytes (GPH of them): those that sel picks (every second one) as fp16 pairs, one
+// per two 32-dim chunks.
+template <int KP>
+__device__ __forceinline__ void lane_scales(const uint32_t *w, uint32_t sel, uint32_t (&out)[KP / 2]) {
+    if constexpr (KP == 2) {
+        out[0] = f16x2_from_e4m3x2(__byte_perm(w[0], 0u, sel));
+    } else {
+#pragma unroll
+        for (int i = 0; i < KP / 2; i += 2) {
+            const uint32_t b = __byte_perm(w[i], w[i + 1], sel);
+            out[i] = f16x2_from_e4m3x2(b);
+            out[i + 1] = f16x2_from_e4m3x2_hi(b);
+        }
+    }
+}
+
 // 0x3C00 (fp16 one) in each half of an fp16 pair that is NaN
 __device__ __forceinline__ uint32_t nan_ones(uint32_t h) {
     return ((h & 0x7FFFu) > 0x7C00u ? 0x3C00u : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0x3C000000u : 0u);
 }
 
-// As for the 8-bit kernel: two CTAs per SM where the accumulators allow it.
-template <int HD, int NT>
-__host__ __device__ constexpr int fp4_ctas_per_sm() { return HD * NT <= 128 ? 2 : 1; }
+// NV: output tiles of 4 score columns per kv head.  kv heads (consumer warps) per CTA at most, and
+// CTAs per SM: as many warps as the accumulators and q leave registers for.  Two score tiles at
+// head_dim 128 keep q in shared memory.
+template <int HD, int NV>
+__host__ __device__ constexpr int fp4_max_heads() { return HD * NV >= 256 ? 4 : kMaxKvHeads; }
+template <int HD, int NV>
+__host__ __device__ constexpr int fp4_ctas_per_sm() { return HD <= 128 && HD * NV >= 256 ? 3 : 2; }
+template <int HD, int NV>
+__host__ __device__ constexpr bool fp4_q_in_smem() { return HD == 128 && NV > 2; }
 
-template <int HD, int NT, bool kMulti>
-__global__ void __launch_bounds__(kThreadsMax, fp4_ctas_per_sm<HD, NT>())
+template <int HD, int NV, bool kMulti>
+__global__ void __launch_bounds__(32 * (fp4_max_heads<HD, NV>() + 1), fp4_ctas_per_sm<HD, NV>())
 decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const __grid_constant__ CUtensorMap tmks, const __grid_constant__ CUtensorMap tmvs,
                   const Fp4KernelArgs f) {
@@ -102,6 +136,9 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     constexpr int SEG = HD / 2;    // code bytes of a token's kv head
     constexpr int GPH = HD / 16;   // scale bytes of it
     constexpr int KP = HD / 32;    // 32-dim chunks
+    constexpr int NS = (NV + 1) / 2;  // score tiles of 8 columns
+    constexpr bool kPair = NV <= 2;   // how V and the weights meet, see below
+    constexpr int TT = NV <= 2 ? 2 : 1;  // 16-token tiles a consumer takes at a time (registers)
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -117,6 +154,9 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     const uint32_t bars = base + static_cast<uint32_t>(S) * stage_bytes;  // full[S], empty[S]
     Fp4Chunk *meta = reinterpret_cast<Fp4Chunk *>(base_ptr + S * stage_bytes + 16 * S);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(meta + S);
+    constexpr bool kQS = fp4_q_in_smem<HD, NV>();
+    // kQS: q fragments past the abort flag, 16 bytes a lane per warp, 32-dim chunk and score tile
+    const uint32_t q_smem = (smem_u32(const_cast<int32_t *>(abort_flag)) + 31u) & ~15u;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -261,33 +301,50 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         const int kvh = h0 + warp;
         const int gid = lane >> 2, tig = lane & 3;
         float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
+        // a negative scale's sign goes into q, so the highest product is always the highest score
+        const uint32_t q_sign = score_scale < 0.f ? 0x80008000u : 0u;
+        score_scale = fabsf(score_scale);
         if (score_scale == 0.f) score_scale = 0x1p-126f;  // underflow: equal weights, -inf stays -inf
 
-        float o[KP][2][NT][4];
-        // per score column: the reference maximum (log2 domain) the weights are taken against, and
-        // this lane's part of the sum of weights
-        float m[NT][2], l[NT][2];
-        uint32_t qb[KP][NT][4];
-        // multi-query form: per score column (query token j, head g) the last cache position it
-        // may see, and its row within the sequence (-1: a padding column)
-        int plim[NT][2], crow[NT][2];
-        int q0 = 0, first_lim = 0;  // first_lim: the smallest plim of the sequence's columns
+        // The lane's score columns, v = 0..NV-1 (column x: query token x / group, head x % group).
+        // kPair: x = 4v + tig, which is n = 2 tig + v % 2 of score tile v / 2.
+        // Otherwise columns are in order, n = x % 8 of tile x / 8, so x = 8 (v / 2) + 2 tig + v % 2.
+        auto column = [&](int v) { return kPair ? 4 * v + tig : 8 * (v / 2) + 2 * tig + v % 2; };
+        float o[NV][KP][4];
+        // dim 32c + 4 gid + r of column v
+        auto at = [&](int v, int c, int r) -> float & {
+            return kPair ? o[v][c][r] : o[(v & ~1) + (r >> 1)][c][(v & 1) + 2 * (r & 1)];
+        };
+        // per column: the reference maximum (log2 domain) the weights are taken against, and this
+        // lane's part of the sum of weights
+        float m[NV], l[NV];
+        uint32_t qb[kQS ? 1 : KP][NS][4];
+        const uint32_t q_lane = q_smem + static_cast<uint32_t>((warp * KP * NS * 32 + lane) * 16);
+        // multi-query form: the sequence's first query row, its query tokens and the last cache position
+        // the first of them may see
+        int q0 = 0, nq = 1, first_lim = 0;
 
         // Offsets of this lane in a stage, for the first 16-token tile (the second: c2, s2 further).
         const uint32_t head_codes = static_cast<uint32_t>(warp * a.box_rows * SEG);
         const uint32_t head_scales = static_cast<uint32_t>(warp * a.box_rows * GPH);
-        const uint32_t krow_off = head_codes + ((lane >> 3) & 1) * f.c1;
-        const int kchunk_hi = lane >> 4;
-        const uint32_t vrow_off = code_bytes + head_codes + (lane >> 4) * f.c1;
-        const int vchunk_hi = (lane >> 3) & 1;
+        // (an 8-token group of a head is aligned to 8 SEG bytes, so a chunk pair further is an xor)
+        const uint32_t krow_off = head_codes + ((lane >> 3) & 1) * f.c1 + swz<SEG>(lane & 7, lane >> 4);
+        // V: at head_dim 64 one ldmatrix takes both halves of a tile (the matrices are half, chunk), else
+        // four chunks of one half
+        const uint32_t vrow_off =
+            code_bytes + head_codes +
+            (HD == 64 ? (lane >> 4) * f.c1 + swz<SEG>(lane & 7, (lane >> 3) & 1) : swz<SEG>(lane & 7, lane >> 3));
         const uint32_t ks_off = scales_off + head_scales + gid * GPH;
         const uint32_t vs_off = vscales_off + head_scales + 2 * tig * GPH;
         const uint32_t ksel = 0x6420u + 0x1111u * (tig >> 1);  // bytes of this lane's K groups
-        const uint32_t vsel = 0x6240u + 0x1111u * (gid >> 2);  // (token, next token) of its V groups
+        const uint32_t vsel = 0x6420u + 0x1111u * (gid >> 2);  // and of its V groups
+        // halves of a token pair's weights -> B fragment words (token, dim parity) of column gid
+        const uint32_t bsel0 = gid & 1 ? 0x1044u : 0x4410u, bsel1 = gid & 1 ? 0x3244u : 0x4432u;
 
         int stage = 0;
         uint32_t phase = 0;
         for (;;) {
+            // every lane waits (acquire on the TMA bytes); the outcome is made warp-uniform
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(bars + 8 * stage, phase, abort_flag))) {
                 if (lane == 0) {
                     flag(a.status, KVFP8_DEV_TIMEOUT);
@@ -299,30 +356,18 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             if (mt.flags & kDone) break;
 
             if (mt.flags & kFirst) {
-                int nq = 1;
                 if (kMulti) {
                     const QueryRange qr = query_range(a.qsl, mt.seq, a.rows_per_seq / a.n_q, a.qrows);
                     q0 = qr.q0;
                     nq = qr.count;
-                    const int L = min(max(a.seq_lens[mt.seq], 0), a.max_len);
-                    first_lim = L - nq;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int n = nt * 8 + 2 * tig + c;
-                            const int j = n / a.group, g = n % a.group;
-                            plim[nt][c] = j < nq ? L - nq + j : -1;
-                            crow[nt][c] = j < nq ? j * a.n_q + kvh * a.group + g : -1;
-                        }
+                    first_lim = min(max(a.seq_lens[mt.seq], 0), a.max_len) - nq;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    // column gid of n-tile nt: query token jq, head gq of the group
-                    const int n = nt * 8 + gid;
-                    const int jq = kMulti ? n / a.group : 0;
-                    const int gq = kMulti ? n % a.group : n;
-                    const bool qv = kMulti ? jq < nq : n < a.group;
+                for (int s = 0; s < NS; ++s) {
+                    const int x = 8 * s + (kPair ? (gid >> 1) + 4 * (gid & 1) : gid);  // column gid of score tile s
+                    const int jq = kMulti ? x / a.group : 0;
+                    const int gq = kMulti ? x % a.group : x;
+                    const bool qv = kMulti ? jq < nq : x < a.group;
                     const __nv_bfloat16 *qrow =
                         a.query +
                         ((static_cast<int64_t>(kMulti ? q0 + jq : mt.seq)) * a.n_q + kvh * a.group + gq) * HD;
@@ -330,259 +375,303 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int c = 0; c < KP; ++c) {
                         uint4 w = make_uint4(0u, 0u, 0u, 0u);
                         if (qv) w = *reinterpret_cast<const uint4 *>(qrow + 32 * c + 8 * tig);
-                        qb[c][nt][0] = f16x2_from_f32(bf16lo(w.x), bf16hi(w.x));
-                        qb[c][nt][1] = f16x2_from_f32(bf16lo(w.y), bf16hi(w.y));
-                        qb[c][nt][2] = f16x2_from_f32(bf16lo(w.z), bf16hi(w.z));
-                        qb[c][nt][3] = f16x2_from_f32(bf16lo(w.w), bf16hi(w.w));
-                    }
-                    m[nt][0] = m[nt][1] = -INFINITY;
-                    l[nt][0] = l[nt][1] = 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < KP; ++e)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o[e][j][nt][r] = 0.f;
-            }
-
-            const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
-            // kPartial: some column does not see some token of the chunk.  The common chunk has a body
-            // without those tests: one basic block from the weights to the last product.
-            auto chunk = [&](auto partial_tag) {
-                constexpr bool kPartial = decltype(partial_tag)::value;
-
-                // ---- scores S^T[token][head] = K . q^T, two tiles of 16 tokens
-                float sacc[2][NT][4];
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    uint32_t sc_lo[KP / 2], sc_hi[KP / 2];  // bytes of this lane's groups, rows gid and +8
-                    {
-                        uint32_t wl[GPH / 4], wh[GPH / 4];
-                        lds(st + ks_off + tt * f.s2, wl);
-                        lds(st + ks_off + tt * f.s2 + f.s1, wh);
-                        if constexpr (KP == 2) {
-                            sc_lo[0] = __byte_perm(wl[0], 0u, ksel);
-                            sc_hi[0] = __byte_perm(wh[0], 0u, ksel);
+                        const uint32_t h[4] = {f16x2_from_f32(bf16lo(w.x), bf16hi(w.x)) ^ q_sign,
+                                               f16x2_from_f32(bf16lo(w.y), bf16hi(w.y)) ^ q_sign,
+                                               f16x2_from_f32(bf16lo(w.z), bf16hi(w.z)) ^ q_sign,
+                                               f16x2_from_f32(bf16lo(w.w), bf16hi(w.w)) ^ q_sign};
+                        if constexpr (kQS) {  // read back by the same lane only
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             q_lane + static_cast<uint32_t>((c * NS + s) * 512)),
+                                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                         : "memory");
                         } else {
 #pragma unroll
-                            for (int i = 0; i < KP / 2; i += 2) {
-                                const uint32_t bl = __byte_perm(wl[i], wl[i + 1], ksel);
-                                const uint32_t bh = __byte_perm(wh[i], wh[i + 1], ksel);
-                                sc_lo[i] = bl;
-                                sc_lo[i + 1] = bl >> 16;
-                                sc_hi[i] = bh;
-                                sc_hi[i + 1] = bh >> 16;
-                            }
+                            for (int i = 0; i < 4; ++i) qb[c][s][i] = h[i];
                         }
                     }
+                }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        sacc[tt][nt][0] = sacc[tt][nt][1] = sacc[tt][nt][2] = sacc[tt][nt][3] = 0.f;
+                for (int v = 0; v < NV; ++v) {
+                    m[v] = -INFINITY;
+                    l[v] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < KP; ++c)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[v][c][r] = 0.f;
+                }
+            }
+
+            // One pass over TT 16-token tiles of the chunk, from tile t0 on.
+            // kPartial: some column does not see some token of the chunk.  The common chunk has a body
+            // without those tests: one basic block from the weights to the last product.
+            auto pass = [&](auto partial_tag, const int t0) {
+                constexpr bool kPartial = decltype(partial_tag)::value;
+                const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
+                const int row0 = 16 * t0;
+                auto sees = [&](int row, int v) {  // row of the chunk
+                    if (((mt.mask >> row) & 1u) == 0u) return false;
+                    if (!kMulti) return true;
+                    const int j = column(v) / a.group;  // its query token; padding columns see nothing
+                    return j < nq && mt.tok0 + row <= first_lim + j;
+                };
+
+                // ---- scores S^T[token][column] = K . q^T, tiles of 16 tokens
+                float sacc[TT][NS][4];
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    // scale pairs (chunk 2cp, 2cp + 1) of this lane's groups, rows gid and +8
+                    uint32_t sl[KP / 2], sh[KP / 2];
+                    {
+                        uint32_t w[2][GPH / 4];
+                        lds(st + ks_off + (t0 + tt) * f.s2, w[0]);
+                        lds(st + ks_off + (t0 + tt) * f.s2 + f.s1, w[1]);
+                        lane_scales<KP>(w[0], ksel, sl);
+                        lane_scales<KP>(w[1], ksel, sh);
+                    }
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        sacc[tt][s][0] = sacc[tt][s][1] = sacc[tt][s][2] = sacc[tt][s][3] = 0.f;
 #pragma unroll
                     for (int cp = 0; cp < KP / 2; ++cp) {
                         uint32_t r[4];
-                        ldsm_x4(st + krow_off + tt * f.c2 + swz<SEG>(lane & 7, 2 * cp + kchunk_hi), r[0], r[1],
-                                r[2], r[3]);
-                        const uint32_t fl = f16x2_from_e4m3x2(sc_lo[cp]), fh = f16x2_from_e4m3x2(sc_hi[cp]);
+                        ldsm_x4((st + krow_off + (t0 + tt) * f.c2) ^ (cp << 5), r[0], r[1], r[2], r[3]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {  // chunk 2cp + e
-                            const uint32_t sl = __byte_perm(fl, 0u, e ? 0x3232 : 0x1010);
-                            const uint32_t sh = __byte_perm(fh, 0u, e ? 0x3232 : 0x1010);
+                            const uint32_t xl = e ? bcast_hi(sl[cp]) : bcast_lo(sl[cp]);
+                            const uint32_t xh = e ? bcast_hi(sh[cp]) : bcast_lo(sh[cp]);
                             uint32_t ka[4], kb[4];
                             f16x2_from_e2m1x8(r[2 * e], ka);
                             f16x2_from_e2m1x8(r[2 * e + 1], kb);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                ka[i] = hmul2(ka[i], sl);
-                                kb[i] = hmul2(kb[i], sh);
+                                ka[i] = hmul2(ka[i], xl);
+                                kb[i] = hmul2(kb[i], xh);
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t(&q)[4] = qb[2 * cp + e][nt];
-                                mma16816(sacc[tt][nt], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
-                                mma16816(sacc[tt][nt], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
+                            for (int s = 0; s < NS; ++s) {
+                                uint32_t q[4];
+                                if constexpr (kQS) {
+                                    lds(q_lane + static_cast<uint32_t>(((2 * cp + e) * NS + s) * 512), q);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) q[i] = qb[2 * cp + e][s][i];
+                                }
+                                mma16816(sacc[tt][s], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
+                                mma16816(sacc[tt][s], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
                             }
                         }
                     }
                 }
 
-                // ---- weights 2^(score - m) per head column (log2 domain).  m only has to be near the
-                // running maximum: it moves when a score passes it by more than kLag, so most chunks
-                // take no maximum over the lanes and rescale nothing, and weights stay <= 2^kLag.
-                // Tokens a column does not see get -inf (chunks with such tokens only).
-                auto sees = [&](int row, int nt, int c) {  // row of the chunk
-                    return ((mt.mask >> row) & 1u) != 0u && (!kMulti || mt.tok0 + row <= plim[nt][c]);
-                };
-                if constexpr (kPartial) {  // a score of -inf (whatever the scale's sign), a weight of 0
-                    const float none = score_scale > 0.f ? -INFINITY : INFINITY;
+                // ---- weights 2^(score - m) per column (log2 domain).  m only has to be near the running
+                // maximum: it moves when a score passes it by more than kLag, so most chunks take no
+                // maximum over the lanes and rescale nothing, and weights stay <= 2^kLag.  Tokens a
+                // column does not see get -inf.
+                if constexpr (kPartial) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int v = 0; v < NV; ++v)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                            for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    if (!sees(16 * tt + 8 * h + gid, nt, c)) sacc[tt][nt][c + 2 * h] = none;
+                            for (int h = 0; h < 2; ++h)
+                                if (!sees(row0 + 16 * tt + 8 * h + gid, v)) sacc[tt][v / 2][v % 2 + 2 * h] = -INFINITY;
                 }
+                auto column_top = [&](int v) {  // this lane's highest score of column v
+                    float x = fmaxf(sacc[0][v / 2][v % 2], sacc[0][v / 2][v % 2 + 2]);
+                    if constexpr (TT == 2)
+                        x = fmaxf(x, fmaxf(sacc[TT - 1][v / 2][v % 2], sacc[TT - 1][v / 2][v % 2 + 2]));
+                    return x * score_scale;
+                };
                 float top = -INFINITY;  // the highest score over its column's m
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float a0 = sacc[0][nt][c], a1 = sacc[0][nt][c + 2];
-                        const float a2 = sacc[1][nt][c], a3 = sacc[1][nt][c + 2];
-                        const float x = score_scale > 0.f ? fmaxf(fmaxf(a0, a1), fmaxf(a2, a3))
-                                                          : fminf(fminf(a0, a1), fminf(a2, a3));
-                        // (m starts at -inf, which any score passes; a column of -inf passes nothing)
-                        top = fmaxf(top, x * score_scale - m[nt][c]);
-                    }
+                for (int v = 0; v < NV; ++v)
+                    // (m starts at -inf, which any score passes; a column of -inf passes nothing)
+                    top = fmaxf(top, column_top(v) - m[v]);
                 if (__any_sync(0xFFFFFFFFu, top > kLag)) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int v = 0; v < NV; ++v) {
+                        float x = column_top(v);
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        if (x > m[v]) {
+                            // nothing but zeros (or a NaN, which stays) before the first score
+                            const float alpha = m[v] == -INFINITY ? 1.f : ex2(m[v] - x);
+                            m[v] = x;
+                            l[v] *= alpha;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float a0 = sacc[0][nt][c], a1 = sacc[0][nt][c + 2];
-                            const float a2 = sacc[1][nt][c], a3 = sacc[1][nt][c + 2];
-                            float x = score_scale > 0.f ? fmaxf(fmaxf(a0, a1), fmaxf(a2, a3))
-                                                        : fminf(fminf(a0, a1), fminf(a2, a3));
-                            x *= score_scale;
-                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                            if (x > m[nt][c]) {
-                                // nothing but zeros (or a NaN, which stays) before the first score
-                                const float alpha = m[nt][c] == -INFINITY ? 1.f : ex2(m[nt][c] - x);
-                                m[nt][c] = x;
-                                l[nt][c] *= alpha;
+                            for (int c = 0; c < KP; ++c)
 #pragma unroll
-                                for (int e = 0; e < KP; ++e)
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        o[e][j][nt][c] *= alpha;
-                                        o[e][j][nt][c + 2] *= alpha;
-                                    }
-                            }
+                                for (int r = 0; r < 4; ++r) at(v, c, r) *= alpha;
                         }
+                    }
                 }
-                uint32_t pb[2][NT][2];
+                // Weights as B fragments, through a register transpose.  kPair: of 8 tokens for output tile
+                // v, whose product runs over (token, dim parity): A's rows are pairs of dims as the
+                // conversion leaves them, and column n of B has the weights of column 4v + n / 2 at the
+                // parity n % 2, zeros at the other.  Otherwise of 16 tokens for score tile s.
+                auto fragment = [&](uint32_t w, uint32_t (&b)[2]) {  // w: tokens 2 tig, +1 of column gid / 2
+                    b[0] = __byte_perm(w, 0u, bsel0);
+                    b[1] = __byte_perm(w, 0u, bsel1);
+                };
+                constexpr int NW = kPair ? NV : NS;
+                uint32_t pw[TT][2][NW];  // tokens 16 tt + 8 h + 2 tig, + 1
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int w = 0; w < NW; ++w) {
+                    constexpr int kCols = kPair ? 1 : 2;  // columns of a word
+                    float p[kCols][TT][2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int k = 0; k < kCols; ++k) {
+                        const int v = kPair ? w : 2 * w + k;
                         // a column that has seen no score yet: -inf - 0 for every token
-                        const float sub = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+                        const float sub = m[v] == -INFINITY ? 0.f : m[v];
 #pragma unroll
-                        for (int tt = 0; tt < 2; ++tt)
+                        for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float p = ex2(fmaf(sacc[tt][nt][c + 2 * h], score_scale, -sub));
-                                sacc[tt][nt][c + 2 * h] = p;
-                            }
-                        l[nt][c] += (sacc[0][nt][c] + sacc[0][nt][c + 2]) + (sacc[1][nt][c] + sacc[1][nt][c + 2]);
+                            for (int h = 0; h < 2; ++h)
+                                p[k][tt][h] = ex2(fmaf(sacc[tt][v / 2][v % 2 + 2 * h], score_scale, -sub));
+                        l[v] += TT == 2 ? (p[k][0][0] + p[k][0][1]) + (p[k][TT - 1][0] + p[k][TT - 1][1])
+                                        : p[k][0][0] + p[k][0][1];
                     }
 #pragma unroll
-                    for (int tt = 0; tt < 2; ++tt)
+                    for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)  // tokens 16 tt + 8 h ..+7
-                            pb[tt][nt][h] = movm_t(f16x2_from_f32(sacc[tt][nt][2 * h], sacc[tt][nt][2 * h + 1]));
+                        for (int h = 0; h < 2; ++h)
+                            pw[tt][h][w] = movm_t(f16x2_from_f32(p[0][tt][h], p[kCols - 1][tt][h]));
                 }
 
-                // ---- O^T[dim][head] += V^T . P^T
+                // ---- O^T[dim][column] += V^T . P^T
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-                    uint32_t vs_lo[KP], vs_hi[KP];  // scale pairs of tokens 2t, 2t+1 and 2t+8, 2t+9
-                    {
-                        uint32_t wl[GPH / 2], wh[GPH / 2];  // the two tokens' scale bytes
-                        lds(st + vs_off + tt * f.s2, wl);
-                        lds(st + vs_off + tt * f.s2 + f.s1, wh);
+                for (int tt = 0; tt < TT; ++tt) {
+                    // scale pairs (chunk 2cp, 2cp + 1) of this lane's groups: tokens 8h + 2 tig and +1
+                    auto value_scales = [&](int h, uint32_t (&vs)[2][KP / 2]) {
+                        uint32_t w[GPH / 2];  // both tokens' bytes
+                        lds(st + vs_off + (t0 + tt) * f.s2 + h * f.s1, w);
+                        lane_scales<KP>(w, vsel, vs[0]);
+                        lane_scales<KP>(w + GPH / 4, vsel, vs[1]);
+                        if constexpr (kPartial) {
+                            // Tokens that are not there: scale 0.  A column that does not see a token has
+                            // weight 0 for it, and a NaN scale would make 0 * NaN of that, so NaN scales
+                            // become 0 too and the outputs that do see the token are made NaN.
+                            uint32_t nan[2][KP / 2], any = 0;  // fp16 ones at NaN scales
 #pragma unroll
-                        for (int i = 0; i < GPH / 4; ++i) {
-                            const uint32_t bl = __byte_perm(wl[i], wl[i + GPH / 4], vsel);
-                            const uint32_t bh = __byte_perm(wh[i], wh[i + GPH / 4], vsel);
-                            vs_lo[2 * i] = f16x2_from_e4m3x2(bl);
-                            vs_lo[2 * i + 1] = f16x2_from_e4m3x2_hi(bl);
-                            vs_hi[2 * i] = f16x2_from_e4m3x2(bh);
-                            vs_hi[2 * i + 1] = f16x2_from_e4m3x2_hi(bh);
-                        }
-                    }
-                    if constexpr (kPartial) {
-                        // tokens that are not there: scale 0
-                        const uint32_t bits = mt.mask >> (16 * tt + 2 * tig);
-                        const uint32_t mlo = (bits & 1u ? 0x0000FFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
-                        const uint32_t mhi = (bits & 0x100u ? 0x0000FFFFu : 0u) | (bits & 0x200u ? 0xFFFF0000u : 0u);
+                            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int c = 0; c < KP; ++c) {
-                            vs_lo[c] &= mlo;
-                            vs_hi[c] &= mhi;
-                        }
-                        if (kMulti) {
-                            // A column that does not see a token has weight 0 for it, and a NaN scale would
-                            // make 0 * NaN of that.
-                            uint32_t any = 0;
+                                for (int cp = 0; cp < KP / 2; ++cp) {
+                                    if (!((mt.mask >> (row0 + 16 * tt + 8 * h + 2 * tig + k)) & 1u)) vs[k][cp] = 0u;
+                                    nan[k][cp] = kMulti ? nan_ones(vs[k][cp]) : 0u;
+                                    any |= nan[k][cp];
+                                }
+                            if (!kMulti || !__any_sync(0xFFFFFFFFu, any != 0u)) return;
 #pragma unroll
-                            for (int c = 0; c < KP; ++c) any |= nan_ones(vs_lo[c]) | nan_ones(vs_hi[c]);
-                            if (__any_sync(0xFFFFFFFFu, any != 0u)) {
-                                uint32_t sb[NT][2];  // fp16 ones where the column sees the token
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        const int row = 16 * tt + 8 * h + gid;
-                                        sb[nt][h] = movm_t((sees(row, nt, 0) ? 0x3C00u : 0u) |
-                                                           (sees(row, nt, 1) ? 0x3C000000u : 0u));
-                                    }
+                            for (int v = 0; v < NV; ++v) {
+                                uint32_t seen[2];  // fp16 ones where the column sees the token (at both parities)
+                                fragment(movm_t(sees(row0 + 16 * tt + 8 * h + gid, v) ? 0x3C003C00u : 0u), seen);
 #pragma unroll
                                 for (int c = 0; c < KP; ++c) {
-                                    const uint32_t nl = nan_ones(vs_lo[c]), nh = nan_ones(vs_hi[c]);
+                                    const uint32_t n0 = c % 2 ? bcast_hi(nan[0][c / 2]) : bcast_lo(nan[0][c / 2]);
+                                    const uint32_t n1 = c % 2 ? bcast_hi(nan[1][c / 2]) : bcast_lo(nan[1][c / 2]);
+                                    // NaN tokens that the lane's column v sees (every element the same count)
+                                    float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816(cnt, n0, n0, n1, n1, seen[0], seen[1]);
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        // NaN tokens per (dims of the lane's group, column)
-                                        float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-                                        mma16816(cnt, nl, nl, nh, nh, sb[nt][0], sb[nt][1]);
+                                    for (int r = 0; r < 4; ++r)
+                                        if (cnt[0] > 0.f) at(v, c, r) = __uint_as_float(0x7FC00000u);
+                                }
+                            }
 #pragma unroll
-                                        for (int r = 0; r < 4; ++r)
-                                            if (cnt[r] > 0.f)
-                                                o[c][0][nt][r] = o[c][1][nt][r] = __uint_as_float(0x7FC00000u);
-                                    }
-                                    vs_lo[c] &= ~(nl / 0x3C00u * 0xFFFFu);
-                                    vs_hi[c] &= ~(nh / 0x3C00u * 0xFFFFu);
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int cp = 0; cp < KP / 2; ++cp)
+                                    vs[k][cp] &= ~(nan[k][cp] / 0x3C00u * 0xFFFFu);
+                        }
+                    };
+                    // the codes of chunks 4 c4.. of half h (at head_dim 64 one load has both halves)
+                    uint32_t r64[4];
+                    if constexpr (HD == 64)
+                        ldsm_x4_t(st + vrow_off + (t0 + tt) * f.c2, r64[0], r64[1], r64[2], r64[3]);
+                    auto value_codes = [&](int h, int c4, uint32_t (&r)[4]) {
+                        if constexpr (HD == 64) {
+                            r[0] = r64[2 * h];
+                            r[1] = r64[2 * h + 1];
+                        } else {
+                            ldsm_x4_t((st + vrow_off + (t0 + tt) * f.c2 + h * f.c1) ^ (c4 << 6), r[0], r[1], r[2], r[3]);
+                        }
+                    };
+                    constexpr int kC = KP < 4 ? KP : 4;  // chunks of a load
+                    if constexpr (kPair) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t vs[2][KP / 2], pb[NV][2];
+                            value_scales(h, vs);
+#pragma unroll
+                            for (int v = 0; v < NV; ++v) fragment(pw[tt][h][v], pb[v]);
+#pragma unroll
+                            for (int c4 = 0; c4 < (KP + 3) / 4; ++c4) {
+                                uint32_t r[4];
+                                value_codes(h, c4, r);
+#pragma unroll
+                                for (int e = 0; e < kC; ++e) {
+                                    const int c = 4 * c4 + e;
+                                    uint32_t x[4];  // token 2 tig: dims 4g, +1 and +2, +3; then token 2 tig + 1
+                                    f16x2_from_e2m1x8(r[e], x);
+                                    const uint32_t s0 = c % 2 ? bcast_hi(vs[0][c / 2]) : bcast_lo(vs[0][c / 2]);
+                                    const uint32_t s1 = c % 2 ? bcast_hi(vs[1][c / 2]) : bcast_lo(vs[1][c / 2]);
+                                    x[0] = hmul2(x[0], s0);
+                                    x[1] = hmul2(x[1], s0);
+                                    x[2] = hmul2(x[2], s1);
+                                    x[3] = hmul2(x[3], s1);
+#pragma unroll
+                                    for (int v = 0; v < NV; ++v)
+                                        mma16816(o[v][c], x[0], x[1], x[2], x[3], pb[v][0], pb[v][1]);
                                 }
                             }
                         }
-                    }
+                    } else {
+                        uint32_t vs[2][2][KP / 2];
+                        value_scales(0, vs[0]);
+                        value_scales(1, vs[1]);
 #pragma unroll
-                    for (int cp = 0; cp < KP / 2; ++cp) {
-                        uint32_t r[4];
-                        ldsm_x4_t(st + vrow_off + tt * f.c2 + swz<SEG>(lane & 7, 2 * cp + vchunk_hi), r[0], r[1],
-                                  r[2], r[3]);
+                        for (int c4 = 0; c4 < (KP + 3) / 4; ++c4) {
+                            uint32_t r[2][4];
+                            value_codes(0, c4, r[0]);
+                            value_codes(1, c4, r[1]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {  // chunk 2cp + e: tokens 0-7 in r[e], 8-15 in r[2+e]
-                            uint32_t x[4], y[4];
-                            f16x2_from_e2m1x8(r[e], x);
-                            f16x2_from_e2m1x8(r[2 + e], y);
-                            const uint32_t sl = vs_lo[2 * cp + e], sh = vs_hi[2 * cp + e];
+                            for (int e = 0; e < kC; ++e) {
+                                const int c = 4 * c4 + e;
+                                // per half: scaled dims (4g, +1), (4g + 2, +3) of token 2 tig, then of 2 tig + 1
+                                uint32_t x[2][4];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {  // dims 4g + 2j, 4g + 2j + 1
-                                const uint32_t a0 = hmul2(__byte_perm(x[j], x[j + 2], 0x5410), sl);
-                                const uint32_t a1 = hmul2(__byte_perm(x[j], x[j + 2], 0x7632), sl);
-                                const uint32_t a2 = hmul2(__byte_perm(y[j], y[j + 2], 0x5410), sh);
-                                const uint32_t a3 = hmul2(__byte_perm(y[j], y[j + 2], 0x7632), sh);
+                                for (int h = 0; h < 2; ++h) {
+                                    f16x2_from_e2m1x8(r[h][e], x[h]);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816(o[2 * cp + e][j][nt], a0, a1, a2, a3, pb[tt][nt][0], pb[tt][nt][1]);
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint32_t sp = vs[h][i >> 1][c / 2];
+                                        x[h][i] = hmul2(x[h][i], c % 2 ? bcast_hi(sp) : bcast_lo(sp));
+                                    }
+                                }
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {  // token pairs of dims 4g + 2j, 4g + 2j + 1
+                                    const uint32_t a0 = __byte_perm(x[0][j], x[0][j + 2], 0x5410);
+                                    const uint32_t a1 = __byte_perm(x[0][j], x[0][j + 2], 0x7632);
+                                    const uint32_t a2 = __byte_perm(x[1][j], x[1][j + 2], 0x5410);
+                                    const uint32_t a3 = __byte_perm(x[1][j], x[1][j + 2], 0x7632);
+#pragma unroll
+                                    for (int s = 0; s < NS; ++s)
+                                        mma16816(o[2 * s + j][c], a0, a1, a2, a3, pw[tt][0][s], pw[tt][1][s]);
+                                }
                             }
                         }
                     }
                 }
             };
-            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim))
-                chunk(std::false_type{});
-            else if (mt.mask != 0u)
-                chunk(std::true_type{});
+            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim)) {
+#pragma unroll 1
+                for (int t = 0; t < 2; t += TT) pass(std::false_type{}, t);
+            } else if (mt.mask != 0u) {
+#pragma unroll 1
+                for (int t = 0; t < 2; t += TT) pass(std::true_type{}, t);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + 8 * (S + stage));
             if (++stage == S) {
@@ -594,36 +683,32 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 const bool direct = (mt.flags & kDirect) != 0;
                 const int64_t pidx = static_cast<int64_t>(mt.seq) + blockIdx.x;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int v = 0; v < NV; ++v) {
+                    float lt = l[v];
+                    lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 4);
+                    lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 8);
+                    lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 16);
+                    const int x = column(v);
+                    if (kMulti ? x / a.group >= nq : x >= a.group) continue;  // padding column
+                    const int srow = kMulti ? x / a.group * a.n_q + kvh * a.group + x % a.group : kvh * a.group + x;
+                    const int64_t orow_idx = kMulti ? static_cast<int64_t>(q0) * a.n_q + srow
+                                                    : static_cast<int64_t>(mt.seq) * a.n_q + srow;
+                    // zero where no token was visible; a NaN sum makes the row NaN
+                    const float inv = lt == 0.f ? 0.f : (direct ? sv : 1.f) / lt;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float lt = l[nt][c];
-                        lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 4);
-                        lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 8);
-                        lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 16);
-                        const int g = nt * 8 + 2 * tig + c;
-                        if (kMulti ? crow[nt][c] < 0 : g >= a.group) continue;  // padding column
-                        const int srow = kMulti ? crow[nt][c] : kvh * a.group + g;
-                        const int64_t orow_idx = kMulti ? static_cast<int64_t>(q0) * a.n_q + srow
-                                                        : static_cast<int64_t>(mt.seq) * a.n_q + srow;
-                        // zero where no token was visible; a NaN sum makes the row NaN
-                        const float inv = lt == 0.f ? 0.f : (direct ? sv : 1.f) / lt;
-#pragma unroll
-                        for (int e = 0; e < KP; ++e) {
-                            const int d = 32 * e + 4 * gid;  // four consecutive dims
-                            const float x0 = o[e][0][nt][c] * inv, x1 = o[e][0][nt][c + 2] * inv;
-                            const float x2 = o[e][1][nt][c] * inv, x3 = o[e][1][nt][c + 2] * inv;
-                            if (direct)
-                                *reinterpret_cast<uint2 *>(a.out + orow_idx * HD + d) =
-                                    make_uint2(bf16x2_from_f32(x0, x1), bf16x2_from_f32(x2, x3));
-                            else
-                                *reinterpret_cast<float4 *>(a.part_o + (pidx * a.rows_per_seq + srow) * HD + d) =
-                                    make_float4(x0, x1, x2, x3);
-                        }
-                        if (!direct && gid == 0)
-                            a.part_lse[pidx * a.rows_per_seq + srow] =
-                                lt == 0.f ? -INFINITY : m[nt][c] + __log2f(lt);
+                    for (int c = 0; c < KP; ++c) {
+                        const int d = 32 * c + 4 * gid;
+                        const float x0 = at(v, c, 0) * inv, x1 = at(v, c, 1) * inv;
+                        const float x2 = at(v, c, 2) * inv, x3 = at(v, c, 3) * inv;
+                        if (direct)
+                            *reinterpret_cast<uint2 *>(a.out + orow_idx * HD + d) =
+                                make_uint2(bf16x2_from_f32(x0, x1), bf16x2_from_f32(x2, x3));
+                        else
+                            *reinterpret_cast<float4 *>(a.part_o + (pidx * a.rows_per_seq + srow) * HD + d) =
+                                make_float4(x0, x1, x2, x3);
                     }
+                    if (!direct && gid == 0)
+                        a.part_lse[pidx * a.rows_per_seq + srow] = lt == 0.f ? -INFINITY : m[v] + __log2f(lt);
                 }
             }
         }
@@ -668,15 +753,15 @@ cudaError_t encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t block
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int HD, int NT, bool kMulti>
+template <int HD, int NV, bool kMulti>
 cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t stream) {
     DeviceFacts facts;
     cudaError_t err = device_facts(&facts);
     if (err != cudaSuccess) return err;
     const int sms = facts.sms, smem_optin = facts.smem_optin;
 
-    // kv heads per CTA: the largest divisor of n_kv up to 8; the groups are a grid dimension
-    int hpc = std::min(d.n_kv, kMaxKvHeads);
+    // kv heads per CTA: the largest divisor of n_kv up to the limit; the groups are a grid dimension
+    int hpc = std::min(d.n_kv, fp4_max_heads<HD, NV>());
     while (d.n_kv % hpc != 0) --hpc;
     const int groups = d.n_kv / hpc;
     const int box_rows = std::min(d.block_size, kTok);
@@ -691,16 +776,19 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     f.c2 = box_rows == 32 ? 16 * (HD / 2) : box_rows == 16 ? f.code_box : 2 * f.code_box;
     f.s1 = box_rows >= 16 ? 8 * (HD / 16) : f.scale_box;
     f.s2 = box_rows == 32 ? 16 * (HD / 16) : box_rows == 16 ? f.scale_box : 2 * f.scale_box;
-    const int ctas_per_sm = fp4_ctas_per_sm<HD, NT>();
+    const int ctas_per_sm = fp4_ctas_per_sm<HD, NV>();
     constexpr int kMaxStages = 8;
-    auto smem_for = [&](int st) { return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024; };
+    const size_t q_bytes = fp4_q_in_smem<HD, NV>() ? static_cast<size_t>(hpc) * (HD / 32) * ((NV + 1) / 2) * 512 + 16 : 0;
+    auto smem_for = [&](int st) {
+        return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024 + q_bytes;
+    };
     const size_t sm_budget = static_cast<size_t>(smem_optin) + 1024;
     int stages = kMaxStages;
     while (stages > 2 && (smem_for(stages) + 1024) * ctas_per_sm > sm_budget) --stages;
     const size_t smem = smem_for(stages);
     if (smem > static_cast<size_t>(smem_optin)) return cudaErrorNotSupported;
 
-    auto kern = decode_fp4_kernel<HD, NT, kMulti>;
+    auto kern = decode_fp4_kernel<HD, NV, kMulti>;
     const int threads = 32 * (hpc + 1);
     int occ = 0;
     if ((err = kernel_occupancy(kern, threads, smem, &occ)) != cudaSuccess) return err;
@@ -786,6 +874,16 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 1>, k);
 }
 
+template <int HD>
+cudaError_t run_tiles(const DecodeArgs &d, const DecodeWorkspace &ws, int tiles, cudaStream_t stream) {
+    const bool multi = d.qsl != nullptr;
+    if (tiles <= 1) return multi ? run_fp4<HD, 1, true>(d, ws, stream) : run_fp4<HD, 1, false>(d, ws, stream);
+    if (tiles <= 2) return multi ? run_fp4<HD, 2, true>(d, ws, stream) : run_fp4<HD, 2, false>(d, ws, stream);
+    if constexpr (HD <= 128)
+        return multi ? run_fp4<HD, 4, true>(d, ws, stream) : run_fp4<HD, 4, false>(d, ws, stream);
+    return cudaErrorNotSupported;
+}
+
 }  // namespace
 
 cudaError_t launch_paged_decode_fp4(const DecodeArgs &d, cudaStream_t stream) {
@@ -793,19 +891,11 @@ cudaError_t launch_paged_decode_fp4(const DecodeArgs &d, cudaStream_t stream) {
     if (!multi_uses_decode_kernel(d.n_q, d.n_kv, d.head_dim, d.qmax))
         return launch_prefill_attention(d, stream);
     const DecodeWorkspace ws = decode_workspace_layout(d.num_seqs, d.qmax * d.n_q, d.head_dim);
-    const bool one = d.qmax * (d.n_q / d.n_kv) <= 8;  // n-tiles of 8 score columns
-    if (d.qsl == nullptr) {
-        switch (d.head_dim) {
-            case 64: return one ? run_fp4<64, 1, false>(d, ws, stream) : run_fp4<64, 2, false>(d, ws, stream);
-            case 128: return one ? run_fp4<128, 1, false>(d, ws, stream) : run_fp4<128, 2, false>(d, ws, stream);
-            case 256: return one ? run_fp4<256, 1, false>(d, ws, stream) : cudaErrorNotSupported;
-            default: return cudaErrorNotSupported;
-        }
-    }
+    const int tiles = (d.qmax * (d.n_q / d.n_kv) + 3) / 4;  // of 4 score columns
     switch (d.head_dim) {
-        case 64: return one ? run_fp4<64, 1, true>(d, ws, stream) : run_fp4<64, 2, true>(d, ws, stream);
-        case 128: return one ? run_fp4<128, 1, true>(d, ws, stream) : run_fp4<128, 2, true>(d, ws, stream);
-        case 256: return one ? run_fp4<256, 1, true>(d, ws, stream) : cudaErrorNotSupported;
+        case 64: return run_tiles<64>(d, ws, tiles, stream);
+        case 128: return run_tiles<128>(d, ws, tiles, stream);
+        case 256: return run_tiles<256>(d, ws, tiles, stream);
         default: return cudaErrorNotSupported;
     }
 }
