@@ -117,6 +117,78 @@ __device__ __forceinline__ uint32_t nan_ones(uint32_t h) {
     return ((h & 0x7FFFu) > 0x7C00u ? 0x3C00u : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0x3C000000u : 0u);
 }
 
+// Batches of up to kOwnPlanSeqs sequences take no plan kernel: each CTA's producer warp reads the
+// lengths and works out its CTA's range with a warp scan, while the other warps set up (64 sequences:
+// one launch and ~3 us less than the plan kernel in front).  CTA 0 leaves the chunk prefix for the
+// combine kernel.
+constexpr int kOwnPlanSeqs = 256;
+
+__device__ __forceinline__ CtaPlan own_plan(const KernelArgs &a, int lane) {
+    constexpr int kRounds = kOwnPlanSeqs / 32;
+    int n[kRounds];  // chunks of sequence 32 r + lane
+    int sum = 0, L = 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int i = 32 * r + lane;
+        n[r] = i < a.num_seqs ? seq_chunks<kTok>(a, i, L) : 0;
+        sum += n[r];
+    }
+    const int T = __reduce_add_sync(0xFFFFFFFFu, sum);
+    const int P = min(T, a.num_ctas), c = blockIdx.x;
+    CtaPlan p = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < P) {
+        p.lo = static_cast<int32_t>(static_cast<int64_t>(c) * T / P);
+        p.hi = static_cast<int32_t>(static_cast<int64_t>(c + 1) * T / P);
+    }
+    const bool write = c == 0 && blockIdx.y == 0;
+    int32_t *cstart = const_cast<int32_t *>(a.cstart);
+    int run = 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (32 * r < a.num_seqs) {
+            int x = n[r];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int before = run + x - n[r];
+            if (write && 32 * r + lane < a.num_seqs) cstart[32 * r + lane] = before;
+            const unsigned here = __ballot_sync(0xFFFFFFFFu, before <= p.lo && p.lo < before + n[r]);
+            if (here != 0u) {
+                const int from = __ffs(here) - 1;
+                p.s = 32 * r + from;
+                p.cs = __shfl_sync(0xFFFFFFFFu, before, from);
+                p.ce = p.cs + __shfl_sync(0xFFFFFFFFu, n[r], from);
+            }
+            run += __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+    }
+    if (write && lane == 0) cstart[a.num_seqs] = T;
+    p.L = min(max(a.seq_lens[p.s], 0), a.max_len);
+    return p;
+}
+
+// The plan kernel's other duties, by the producer warps once their copies are issued: the rows of
+// sequences without chunks are zeroed, errors of lengths and query rows flagged.
+template <int HD>
+__device__ __forceinline__ void finish_plan(const KernelArgs &a, int lane) {
+    const int qmax = a.rows_per_seq / a.n_q;
+    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
+        const int raw_len = a.seq_lens[s];
+        int L;
+        const int n = seq_chunks<kTok>(a, s, L);
+        const QueryRange qr = a.qsl ? query_range(a.qsl, s, qmax, a.qrows) : QueryRange{s, 1};
+        const int raw_nq = a.qsl ? a.qsl[s + 1] - a.qsl[s] : 1;
+        if (lane == 0 && (raw_len < 0 || raw_len > a.max_len || qr.count != raw_nq || (a.qsl && qr.count > L)))
+            flag(a.status, KVFP8_DEV_BAD_BLOCK);
+        if (n > 0) continue;
+        const int64_t row = static_cast<int64_t>(a.n_q) * HD;
+        uint4 *rows = reinterpret_cast<uint4 *>(a.out + qr.q0 * row);
+        for (int64_t k = lane; k < qr.count * row / 8; k += 32) rows[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 // NV: output tiles of 4 score columns per kv head.  kv heads (consumer warps) per CTA at most, and
 // CTAs per SM: as many warps as the accumulators and q leave registers for.  Two score tiles at
 // head_dim 128 keep q in shared memory.
@@ -188,10 +260,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
         return;
     }
-    const CtaPlan *rec = a.cta_plan + blockIdx.x;
-    const int32_t pl_lo = rec->lo, pl_hi = rec->hi;
-    if (pl_lo >= pl_hi) return;
-    const int64_t chunk_lo = pl_lo, chunk_hi = pl_hi;
+    if (a.cta_plan != nullptr && a.cta_plan[blockIdx.x].lo >= a.cta_plan[blockIdx.x].hi) return;
     __syncthreads();
 
     if (warp == hpc) {
@@ -200,12 +269,14 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         int stage = 0;
         uint32_t phase = 0;
         bool aborted = false;
-        int s = rec->s;  // sequence holding chunk_lo, its chunks and length (from the plan)
-        int64_t cs = rec->cs, ce = rec->ce;
-        int L = rec->L;
+        // this CTA's chunks, the sequence holding the first, that one's chunks and length
+        const CtaPlan rec = a.cta_plan != nullptr ? a.cta_plan[blockIdx.x] : own_plan(a, lane);
+        const int64_t chunk_lo = rec.lo, chunk_hi = rec.hi;
+        int s = rec.s, L = rec.L;
+        int64_t cs = rec.cs, ce = rec.ce;
         int wbase = -1 << 30;  // first block-table entry held in the lane window
         int32_t win = 0;
-        prefetch_q<HD>(a, s, h0, lane);
+        if (chunk_lo < chunk_hi) prefetch_q<HD>(a, s, h0, lane);
         const int lbr = 31 - __clz(a.box_rows), lbs = 31 - __clz(a.block_size);  // powers of two
         for (int64_t x = chunk_lo; x < chunk_hi; ++x) {
             if (x >= ce) {
@@ -285,6 +356,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
         }
+        if (a.cta_plan == nullptr && blockIdx.y == 0) finish_plan<HD>(a, lane);
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -838,11 +910,17 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     k.rows_per_seq = d.qmax * d.n_q;
     k.qrows = d.qrows;
 
-    plan_kernel<kTok><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
-                                        num_ctas, reinterpret_cast<int32_t *>(w + ws.cstart_off),
-                                        reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
-                                        d.n_q * HD, d.status);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    const bool own_plan = d.num_seqs <= kOwnPlanSeqs;
+    if (own_plan) {
+        k.cta_plan = nullptr;
+    } else {
+        plan_kernel<kTok><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs,
+                                                  k.max_len, num_ctas,
+                                                  reinterpret_cast<int32_t *>(w + ws.cstart_off),
+                                                  reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
+                                                  d.n_q * HD, d.status);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
 
     // programmatic dependent launches, as for the 8-bit kernel
     cudaLaunchConfig_t cfg = {};
@@ -854,11 +932,12 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = own_plan ? 0 : 1;  // (only a kernel of this call may be overtaken)
     if ((err = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, tmks, tmvs, f)) != cudaSuccess) return err;
 
     constexpr int kHeadsPerCta = 256 / (HD / 4);
     cudaLaunchConfig_t ccfg = cfg;
+    ccfg.numAttrs = 1;
     ccfg.gridDim = dim3(d.num_seqs, (k.rows_per_seq + kHeadsPerCta - 1) / kHeadsPerCta);
     ccfg.dynamicSmemBytes = 0;
     const int64_t parts = (static_cast<int64_t>(num_ctas) + d.num_seqs) / std::max(1, d.num_seqs);
