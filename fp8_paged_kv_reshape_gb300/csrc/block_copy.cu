@@ -81,33 +81,46 @@ __device__ __forceinline__ void copy_segment(const SegMap &m, int32_t x, int32_t
 // kvfp8_copy_blocks.  Pairs that name one block twice would race, so each CTA first marks every
 // pair's destination in a bitmap of the pool in shared memory (and in a second one the blocks
 // that are a destination twice); a pair is carried out when its destination is not in the second
-// and its source is in neither.  That costs each CTA one pass over the pairs (from L2) and no
-// memory of the caller's.
+// and its source is in neither.  That costs each CTA one pass over the pairs (from L2, the loads of
+// eight pairs a thread in flight together) and no memory of the caller's.
+constexpr int kCopyThreads = 1024;
+
 template <bool kWide>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kCopyThreads)
 copy_blocks_kernel(const __grid_constant__ SegMap m, const int32_t num_blocks, const int32_t *src,
                    const int32_t *dst, const int32_t num_pairs, uint32_t *status) {
     extern __shared__ uint32_t marks[];
     const int words = (num_blocks + 31) >> 5;
     uint32_t *once = marks, *twice = marks + words;
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int i = tid; i < 2 * words; i += kThreads) marks[i] = 0u;
+    for (int i = tid; i < 2 * words; i += kCopyThreads) marks[i] = 0u;
     __syncthreads();
     auto inside = [&](int32_t b) { return b >= 0 && b < num_blocks; };
-    for (int64_t i = tid; i < num_pairs; i += kThreads) {
-        const int32_t s = __ldg(src + i), d = __ldg(dst + i);
-        if (inside(s) && inside(d)) {
-            if (s != d && (atomicOr(&once[d >> 5], 1u << (d & 31)) >> (d & 31)) & 1u)
-                atomicOr(&twice[d >> 5], 1u << (d & 31));
-        } else if (blockIdx.x == 0 && s != -1 && d != -1) {
-            flag(status, KVFP8_DEV_BAD_BLOCK);
+    constexpr int kBatch = 8;
+    for (int64_t i0 = tid; i0 < num_pairs; i0 += kBatch * kCopyThreads) {
+        int32_t s[kBatch], d[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t i = i0 + k * kCopyThreads;
+            s[k] = i < num_pairs ? __ldg(src + i) : -1;
+            d[k] = i < num_pairs ? __ldg(dst + i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (inside(s[k]) && inside(d[k])) {
+                const uint32_t bit = 1u << (d[k] & 31);
+                if (s[k] != d[k] && (atomicOr(&once[d[k] >> 5], bit) & bit) != 0u) atomicOr(&twice[d[k] >> 5], bit);
+            } else if (blockIdx.x == 0 && s[k] != -1 && d[k] != -1) {
+                flag(status, KVFP8_DEV_BAD_BLOCK);
+            }
         }
     }
     __syncthreads();
     const int32_t segs = m.seg0[m.caches.count];
     const int64_t total = static_cast<int64_t>(num_pairs) * segs;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWarps + (tid >> 5); it < total; it += step) {
+    // consecutive segments go to consecutive CTAs: a few blocks occupy every SM
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32);
+    for (int64_t it = blockIdx.x + static_cast<int64_t>(gridDim.x) * (tid >> 5); it < total; it += step) {
         const int64_t p = it / segs;
         const int32_t x = static_cast<int32_t>(it - p * segs);
         const int32_t s = __ldg(src + p), d = __ldg(dst + p);
@@ -313,10 +326,10 @@ cudaError_t launch_copy_blocks(const CacheList &caches, int32_t num_blocks, cons
     if (!make_segments(caches, num_pairs, f.sms, &m)) return cudaErrorNotSupported;
     auto kern = wide_ok(caches) ? copy_blocks_kernel<true> : copy_blocks_kernel<false>;
     int occ = 0;
-    if ((err = kernel_occupancy(kern, kThreads, smem, &occ)) != cudaSuccess) return err;
-    const int64_t want = (static_cast<int64_t>(num_pairs) * m.seg0[caches.count] + kWarps - 1) / kWarps;
-    const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(f.sms) * std::max(occ, 1)));
-    kern<<<grid, kThreads, smem, stream>>>(m, num_blocks, src, dst, num_pairs, status);
+    if ((err = kernel_occupancy(kern, kCopyThreads, smem, &occ)) != cudaSuccess) return err;
+    const int64_t items = static_cast<int64_t>(num_pairs) * m.seg0[caches.count];
+    const int grid = static_cast<int>(std::min<int64_t>(items, static_cast<int64_t>(f.sms) * std::max(occ, 1)));
+    kern<<<grid, kCopyThreads, smem, stream>>>(m, num_blocks, src, dst, num_pairs, status);
     return cudaGetLastError();
 }
 

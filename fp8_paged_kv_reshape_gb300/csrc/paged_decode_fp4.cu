@@ -500,9 +500,15 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         lane_scales<KP>(w[0], ksel, sl);
                         lane_scales<KP>(w[1], ksel, sh);
                     }
+                    // kSums running sums, so that a product waits for the one before the last only (170.0
+                    // against 171.7 us on eight long sequences; for 16 columns the registers cost more)
+                    constexpr int kSums = NV <= 2 ? 2 : 1;
+                    float part[kSums][NS][4];
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        sacc[tt][s][0] = sacc[tt][s][1] = sacc[tt][s][2] = sacc[tt][s][3] = 0.f;
+                    for (int k = 0; k < kSums; ++k)
+#pragma unroll
+                        for (int s = 0; s < NS; ++s)
+                            part[k][s][0] = part[k][s][1] = part[k][s][2] = part[k][s][3] = 0.f;
 #pragma unroll
                     for (int cp = 0; cp < KP / 2; ++cp) {
                         uint32_t r[4];
@@ -528,11 +534,16 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                                     for (int i = 0; i < 4; ++i) q[i] = qb[2 * cp + e][s][i];
                                 }
-                                mma16816(sacc[tt][s], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
-                                mma16816(sacc[tt][s], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
+                                mma16816(part[0][s], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
+                                mma16816(part[kSums - 1][s], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
                             }
                         }
                     }
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sacc[tt][s][i] = kSums == 2 ? part[0][s][i] + part[kSums - 1][s][i] : part[0][s][i];
                 }
 
                 // ---- weights 2^(score - m) per column (log2 domain).  m only has to be near the running
