@@ -50,9 +50,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 // maxima that a NaN operand turns into NaN
-__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t max_abs_nan_bf16x2(uint32_t a, uint32_t b) {  // (of either sign)
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -115,45 +115,77 @@ struct Group16 {
             for (int i = 1; i < kWords; ++i) m = max_nan(m, fabsf(__uint_as_float(w[i])));
             return m;
         }
-        uint32_t m = w[0] & 0x7FFF7FFFu;
+        uint32_t m = w[0];
 #pragma unroll
-        for (int i = 1; i < kWords; ++i) m = max_nan_bf16x2(m, w[i] & 0x7FFF7FFFu);
-        return max_nan(bf16lo(m), bf16hi(m));
+        for (int i = 1; i < kWords; ++i) m = max_abs_nan_bf16x2(m, w[i]);
+        return max_nan(fabsf(bf16lo(m)), fabsf(bf16hi(m)));
     }
 };
 
-// the magnitudes of a group whose scale saturated or whose d is out of the fast range
-__device__ __noinline__ uint2 quantize_slow(const float (&x)[16], float d) {
-    float q[16];
+// The layer scale of a side.  fast: |s| in [2^-50, 2^50], so that every d = B |s| that is not zero
+// lies in [2^-60, 2^60], the range of the reciprocal divide.
+struct LayerScale {
+    float sa, y;    // |s|, RN(1 / |s|)
+    uint32_t neg;   // 0x88888888 when s < 0
+    bool fast;
+    __device__ __forceinline__ explicit LayerScale(float s) {
+        sa = fabsf(s);
+        y = __frcp_rn(sa);
+        neg = signbit(s) ? 0x88888888u : 0u;
+        fast = sa >= 0x1p-50f && sa <= 0x1p50f;
+    }
+};
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(f16x2_from_e4m3x2(byte) & 0xFFFFu)));
+}
+
+// Eight codes by plain divisions.  (By value: an array argument would put every group's elements on
+// the stack.)
+__device__ __noinline__ uint32_t quantize_slow8(float x0, float x1, float x2, float x3, float x4, float x5,
+                                                float x6, float x7, float d) {
+    const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float ax = fabsf(x[i]);
         const float m = isinf(ax) ? 6.f : d == 0.f ? 0.f : __fdiv_rn(ax, d);
         q[i] = x[i] < 0.f ? -m : m;
     }
-    return make_uint2(e2m1x8_from_f32(q), e2m1x8_from_f32(q + 8));
+    return e2m1x8_from_f32(q);
+}
+__device__ __noinline__ uint32_t scale_byte_slow(float a, float sa) {
+    return isnan(a) ? 0x7Fu : e4m3x2_from_f32(__fdiv_rn(__fdiv_rn(a, sa), 6.f), 0.f) & 0xFFu;
 }
 
-// Sixteen elements -> their codes and the group's scale byte.  sa = |s|, neg = 0x88888888 when
-// s < 0.
+// RN(x / d) for x >= 0 from y = RN(1 / d) by the two residual steps, wherever the quotient is in
+// the range that decides an E4M3 code; NaN and a quotient that overflows on the way give 2^100.
+__device__ __forceinline__ float quotient(float x, float d, float y) {
+    const float q0 = x * y;
+    const float q1 = fmaf(fmaf(q0, -d, x), y, q0);
+    return fminf(fmaf(fmaf(q1, -d, x), y, q1), 0x1p100f);
+}
+
+// Sixteen elements -> their codes and the group's scale byte.  The rare groups (a scale that
+// saturates or may, infinite or NaN elements, a layer scale out of range) all show byte 0x7E or
+// !fast.
 template <bool kF32>
-__device__ __forceinline__ uint2 quantize16(const Group16<kF32> &g, float sa, uint32_t neg, uint32_t &byte) {
+__device__ __forceinline__ uint2 quantize16(const Group16<kF32> &g, const LayerScale &s, uint32_t &byte) {
     const float a = g.amax();
-    if (isnan(a)) {
-        byte = 0x7Fu;
-        return make_uint2(0u, 0u);
-    }
-    byte = e4m3x2_from_f32(__fdiv_rn(__fdiv_rn(a, sa), 6.f), 0.f) & 0xFFu;
-    const float B = __half2float(__ushort_as_half(static_cast<uint16_t>(f16x2_from_e4m3x2(byte) & 0xFFFFu)));
-    const float d = __fmul_rn(B, sa);
+    byte = e4m3x2_from_f32(quotient(quotient(a, s.sa, s.y), 6.f, 0x1.555556p-3f), 0.f) & 0xFFu;  // RN(1/6)
     float x[16];
     g.unpack(x);
     uint2 c;
-    if (__builtin_expect(byte == 0x7Eu || (d != 0.f && !(d >= 0x1p-60f && d <= 0x1p60f)), 0)) {
-        c = quantize_slow(x, d);
+    if (__builtin_expect(byte == 0x7Eu || !s.fast, 0)) {
+        byte = scale_byte_slow(a, s.sa);
+        if (byte == 0x7Fu) return make_uint2(0u, 0u);  // a NaN among them
+        const float d = __fmul_rn(e4m3_value(byte), s.sa);
+        c.x = quantize_slow8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], d);
+        c.y = quantize_slow8(x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15], d);
     } else {
         // q0 = x*y, then two residual steps q += (x - q*d)*y.  d = 0 takes y = 0, which gives
         // zeros with the sign of x; x = -0 gives +0.
+        const float d = __fmul_rn(e4m3_value(byte), s.sa);
         const float y = d == 0.f ? 0.f : __frcp_rn(d);
         const uint64_t y2 = pack2(y, y), nd2 = pack2(-d, -d);
         float q[16];
@@ -166,7 +198,7 @@ __device__ __forceinline__ uint2 quantize16(const Group16<kF32> &g, float sa, ui
         }
         c = make_uint2(e2m1x8_from_f32(q), e2m1x8_from_f32(q + 8));
     }
-    return make_uint2(c.x ^ neg, c.y ^ neg);
+    return make_uint2(c.x ^ s.neg, c.y ^ s.neg);
 }
 
 // How rows map to lanes: gpr groups a row over 1 << lpr_log2 lanes.
@@ -176,15 +208,17 @@ struct RowMap {
     int32_t bs_log2;
 };
 
-// Scale byte of group g of the row at `slot`.
-__device__ __forceinline__ int64_t scale_index(const RowMap &m, int n_kv, int64_t slot, int g) {
-    const int64_t blk = slot >> m.bs_log2, off = slot & ((1 << m.bs_log2) - 1);
-    const int64_t head = g >> m.gph_log2;
-    return ((((blk * n_kv + head) << m.bs_log2) + off) << m.gph_log2) + (g & ((1 << m.gph_log2) - 1));
+// Scale byte of group g of the row at `slot` (slots and (block, head) pairs fit 32 bits).
+__device__ __forceinline__ int64_t scale_index(const RowMap &m, int n_kv, int32_t slot, int g) {
+    const int32_t blk = slot >> m.bs_log2, off = slot & ((1 << m.bs_log2) - 1);
+    const int32_t head = g >> m.gph_log2;
+    return (((static_cast<int64_t>(blk * n_kv + head) << m.bs_log2) + off) << m.gph_log2) +
+           (g & ((1 << m.gph_log2) - 1));
 }
 
-template <bool kF32, bool kWide>
-__global__ void __launch_bounds__(32 * kWarps)
+// kG: groups of a row per lane, 32 apart.
+template <bool kF32, bool kWide, int kG>
+__global__ void __launch_bounds__(32 * kWarps, kF32 ? 2 : 3)
 write_fp4_kernel(const Fp4WriteArgs a, const RowMap m) {
     const int lane = threadIdx.x & 31, side = blockIdx.z;
     const float s0 = load_scale(a.scale[0], a.scale_dtype), s1 = load_scale(a.scale[1], a.scale_dtype);
@@ -193,41 +227,63 @@ write_fp4_kernel(const Fp4WriteArgs a, const RowMap m) {
             flag(a.status, KVFP8_DEV_BAD_SCALE);
         return;
     }
-    const float s = side == 0 ? s0 : s1, sa = fabsf(s);
-    const uint32_t neg = signbit(s) ? 0x88888888u : 0u;
-    const int g = (blockIdx.y << 5) + (lane & ((1 << m.lpr_log2) - 1));
-    const bool there = g < m.gpr;  // this lane's group exists
-    const int64_t rpw = 32 >> m.lpr_log2;  // rows a warp takes at a time
+    const LayerScale s(side == 0 ? s0 : s1);
+    const int g = (blockIdx.y << 5) * kG + (lane & ((1 << m.lpr_log2) - 1));
+    const int rpw = 32 >> m.lpr_log2;  // rows a warp takes at a time
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * rpw;
     int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * rpw + (lane >> m.lpr_log2);
+    // rows the warp's first lane sees (its lanes stay together: groups of four share a store)
+    int64_t rounds = (a.num_tokens - (t - (lane >> m.lpr_log2)) + step - 1) / step;
     constexpr int kEsz = kF32 ? 4 : 2;
-    const uint8_t *src = static_cast<const uint8_t *>(a.src[side]) + static_cast<int64_t>(g) * 16 * kEsz;
-    const int64_t stride = a.stride[side] * kEsz;
-    const int64_t row_codes = static_cast<int64_t>(m.gpr) * 8;
+    const int64_t src_step = step * a.stride[side] * kEsz;
+    const uint8_t *src = static_cast<const uint8_t *>(a.src[side]) + t * a.stride[side] * kEsz +
+                         static_cast<int64_t>(g) * 16 * kEsz;
+    const uint32_t row_codes = static_cast<uint32_t>(m.gpr) * 8;
+    uint8_t *codes = a.codes[side] + static_cast<int64_t>(g) * 8;
+    // scale bytes of group g: block (slot >> bs_log2), offset (slot & off_mask) of it
+    uint8_t *scales = a.scales[side] + (static_cast<int64_t>(g >> m.gph_log2) << (m.bs_log2 + m.gph_log2)) +
+                      (g & ((1 << m.gph_log2) - 1));
+    const uint32_t block_scales = static_cast<uint32_t>(a.n_kv) << (m.bs_log2 + m.gph_log2);
+    const int32_t off_mask = (1 << m.bs_log2) - 1;
+    const uint32_t scales_32 = 32u << m.bs_log2;  // 32 groups further
 
-    auto slot_of = [&](int64_t i) { return i < a.num_tokens ? __ldg(a.slot_mapping + i) : int64_t{-1}; };
-    // a row is written when its slot is in range; -1 is padding, anything else is flagged
-    auto usable = [&](int64_t i, int64_t slot) {
-        if (slot >= 0 && slot < a.num_slots) return there;
-        if (slot != -1 && g == 0 && side == 0 && i < a.num_tokens) flag(a.status, KVFP8_DEV_BAD_SLOT);
-        return false;
+    // The slot of row t (-1: not written).  A row is written when its slot is in range; -1 is
+    // padding, anything else is flagged.
+    const int64_t *slots = a.slot_mapping;
+    auto slot_at = [&](int64_t i) -> int32_t {
+        if (i >= a.num_tokens) return -1;
+        const int64_t sl = __ldg(slots + i);
+        if (sl >= 0 && sl < a.num_slots) return static_cast<int32_t>(sl);
+        if (sl != -1 && g == 0 && side == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
+        return -1;
     };
-    int64_t slot = slot_of(t), slot_next = slot_of(t + step);
-    bool ok = usable(t, slot);
-    Group16<kF32> cur, nxt;
-    if (ok) cur.template load<kWide>(src + t * stride);
-    for (; t < a.num_tokens; t += step) {
-        const int64_t slot_after = slot_of(t + 2 * step);
-        const bool ok_next = usable(t + step, slot_next);
-        if (ok_next) nxt.template load<kWide>(src + (t + step) * stride);
-        if (ok) {
-            uint32_t byte;
-            const uint2 c = quantize16<kF32>(cur, sa, neg, byte);
-            *reinterpret_cast<uint2 *>(a.codes[side] + slot * row_codes + g * 8) = c;
-            a.scales[side][scale_index(m, a.n_kv, slot, g)] = static_cast<uint8_t>(byte);
+    auto load_row = [&](const uint8_t *p, int32_t slot, Group16<kF32> (&x)[kG]) {
+#pragma unroll
+        for (int k = 0; k < kG; ++k)
+            if (slot >= 0 && g + 32 * k < m.gpr) x[k].template load<kWide>(p + k * 512 * kEsz);
+    };
+    int32_t slot = slot_at(t), slot_next = slot_at(t + step);
+    Group16<kF32> cur[kG], nxt[kG];
+    load_row(src, slot, cur);
+    for (; rounds > 0; --rounds) {
+        src += src_step;
+        load_row(src, slot_next, nxt);
+        t += step;
+        const int32_t slot_after = slot_at(t + step);
+        uint8_t *c_row = codes + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * row_codes;
+        uint8_t *s_row = scales + static_cast<uint64_t>(static_cast<uint32_t>(slot >> m.bs_log2)) * block_scales +
+                         ((slot & off_mask) << m.gph_log2);
+#pragma unroll
+        for (int k = 0; k < kG; ++k) {
+            const bool write = slot >= 0 && g + 32 * k < m.gpr;
+            uint32_t byte = 0;
+            if (write) *reinterpret_cast<uint2 *>(c_row + k * 256) = quantize16<kF32>(cur[k], s, byte);
+            // four groups' scale bytes (of one head: it has 4, 8 or 16 groups) leave as one word
+            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 1) << 8;
+            byte |= __shfl_down_sync(0xFFFFFFFFu, byte, 2) << 16;
+            if (write && (lane & 3) == 0) *reinterpret_cast<uint32_t *>(s_row + k * scales_32) = byte;
+            cur[k] = nxt[k];
         }
-        cur = nxt;
-        ok = ok_next;
         slot = slot_next;
         slot_next = slot_after;
     }
@@ -261,7 +317,7 @@ read_fp4_kernel(const Fp4ReadArgs a, const RowMap m, const int32_t wide) {
         b = 0u;
         if (sl >= 0 && sl < a.num_slots) {
             c = __ldg(reinterpret_cast<const uint2 *>(a.codes + sl * row_codes + g * 8));
-            b = __ldg(a.scales + scale_index(m, a.n_kv, sl, g));
+            b = __ldg(a.scales + scale_index(m, a.n_kv, static_cast<int32_t>(sl), g));
         } else if (sl != -1 && g == 0 && i < a.num_tokens) {
             flag(a.status, KVFP8_DEV_BAD_SLOT);
         }
@@ -272,8 +328,7 @@ read_fp4_kernel(const Fp4ReadArgs a, const RowMap m, const int32_t wide) {
     for (; t < a.num_tokens; t += step) {
         const int64_t slot_after = slot_of(t + 2 * step);
         fetch(t + step, slot_next, c_next, b_next);
-        const float B = __half2float(__ushort_as_half(static_cast<uint16_t>(f16x2_from_e4m3x2(b) & 0xFFFFu)));
-        const float d = __fmul_rn(B, s);
+        const float d = __fmul_rn(e4m3_value(b), s);
         uint32_t h[8], o[16];
         f16x2_from_e2m1x8(c.x, *reinterpret_cast<uint32_t(*)[4]>(h));
         f16x2_from_e2m1x8(c.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
@@ -330,15 +385,15 @@ int rows_grid(int64_t tokens, const RowMap &m, int sms, int occ, int planes) {
 
 bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-template <bool kF32, bool kWide>
+template <bool kF32, bool kWide, int kG>
 cudaError_t run_write(const Fp4WriteArgs &a, const RowMap &m, cudaStream_t stream) {
     DeviceFacts f;
     cudaError_t err = device_facts(&f);
     if (err != cudaSuccess) return err;
-    auto kern = write_fp4_kernel<kF32, kWide>;
+    auto kern = write_fp4_kernel<kF32, kWide, kG>;
     int occ = 0;
     if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
-    const int passes = (m.gpr + 31) / 32;
+    const int passes = (m.gpr + 32 * kG - 1) / (32 * kG);
     const dim3 grid(rows_grid(a.num_tokens, m, f.sms, std::max(occ, 1), 2 * passes), passes, 2);
     kern<<<grid, 32 * kWarps, 0, stream>>>(a, m);
     return cudaGetLastError();
@@ -348,12 +403,16 @@ cudaError_t run_write(const Fp4WriteArgs &a, const RowMap &m, cudaStream_t strea
 
 cudaError_t launch_reshape_and_cache_fp4(const Fp4WriteArgs &a, cudaStream_t stream) {
     const RowMap m = row_map(a.n_kv, a.head_dim, a.block_size);
-    const int esz = a.src_dtype == KVFP8_F32 ? 4 : 2;
+    const bool f32 = a.src_dtype == KVFP8_F32;
+    const int esz = f32 ? 4 : 2;
     const bool wide = aligned32(a.src[0]) && aligned32(a.src[1]) && a.stride[0] * esz % 32 == 0 &&
                       a.stride[1] * esz % 32 == 0;
-    if (a.src_dtype == KVFP8_F32)
-        return wide ? run_write<true, true>(a, m, stream) : run_write<true, false>(a, m, stream);
-    return wide ? run_write<false, true>(a, m, stream) : run_write<false, false>(a, m, stream);
+    if (m.gpr <= 32) {
+        if (f32) return wide ? run_write<true, true, 1>(a, m, stream) : run_write<true, false, 1>(a, m, stream);
+        return wide ? run_write<false, true, 1>(a, m, stream) : run_write<false, false, 1>(a, m, stream);
+    }
+    if (f32) return wide ? run_write<true, true, 2>(a, m, stream) : run_write<true, false, 2>(a, m, stream);
+    return wide ? run_write<false, true, 2>(a, m, stream) : run_write<false, false, 2>(a, m, stream);
 }
 
 cudaError_t launch_dequant_fp4(const Fp4ReadArgs &a, cudaStream_t stream) {
