@@ -245,41 +245,123 @@ struct PrefillArgs {
 // such scales are taken as 0, the CTA remembers that it met one, and at the end each of its rows
 // looks up which groups of the values it sees are NaN (a slow scan that no finite cache runs).
 
+// Conversion goes by units of 32 rows of 16 code bytes (8 keys x 4 chunks of 32 dims; 16 keys x 2 at
+// head_dim 64; at 256 a key group has two units).  One ldmatrix gives a lane, per chunk, the codes of
+// dims 8u..8u+7 of a key (u = lane % 4): as K they are one 16-byte piece of the key's operand row; as V
+// the pairs of dims are stored transposed with stmatrix.  The dims of a 32-dim chunk are then permuted
+// in V^T's rows, row 8j + 2a + b holding dim 8a + 2j + b, and so in O's columns: O's word (pair of
+// columns) 4j + a is the output's word 4a + j.
+
 __device__ __forceinline__ bool is_nan_byte(uint32_t b) { return (b & 0x7Fu) == 0x7Fu; }
 
-// the fp16 pair (s, s) of an E4M3 byte
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-    return __byte_perm(f16x2_from_e4m3x2(byte), 0u, 0x1010);
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// eight codes times a scale pair
-__device__ __forceinline__ uint4 dequant8(uint32_t codes, uint32_t scale) {
-    uint32_t h[4];
-    f16x2_from_e2m1x8(codes, h);
-    return make_uint4(mul_f16x2(h[0], scale), mul_f16x2(h[1], scale), mul_f16x2(h[2], scale),
-                      mul_f16x2(h[3], scale));
+// half k of an fp16 pair in both halves
+template <int k>
+__device__ __forceinline__ uint32_t half_pair(uint32_t x) {
+    uint32_t r;
+    if (k == 0)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(x));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(x));
+    return r;
 }
+
+template <int HD>
+struct F4Unit {
+    static constexpr int kPer64 = HD == 64 ? 4 : HD / 16;  // units of 64 keys
+    static constexpr int kRow = HD / 2, kGph = HD / 16;
+    uint32_t r[4];   // the lane's eight codes of chunk c(m), key(m), m = 0..3
+    uint32_t bytes;  // their scale bytes
+
+    __device__ __forceinline__ static int first_key(int unit) { return HD == 64 ? 16 * unit : HD == 128 ? 8 * unit : 8 * (unit >> 1); }
+    // chunk of matrix m
+    __device__ __forceinline__ static int chunk(int unit, int m) { return HD == 64 ? m & 1 : HD == 128 ? m : 4 * (unit & 1) + m; }
+    // the key of row i of a matrix, past first_key: for K rows 2i, 2i + 1 are keys i and i + 4, so that
+    // the stores of eight lanes (two rows) fall on different banks
+    template <bool kK>
+    __device__ __forceinline__ static int row_key(int i) { return kK ? (i >> 1) + 4 * (i & 1) : i; }
+    template <bool kK>
+    __device__ __forceinline__ static int key(int unit, int m, int lane) {
+        return first_key(unit) + row_key<kK>(lane >> 2) + (HD == 64 ? 8 * (m >> 1) : 0);
+    }
+
+    // codes, scales: the stage's shared-memory addresses of this side; keys not in mask read as zeros
+    template <bool kK>
+    __device__ __forceinline__ void load(uint32_t codes, uint32_t scales, uint64_t mask, int unit, int lane) {
+        const int m = lane >> 3, k = first_key(unit) + row_key<kK>(lane & 7) + (HD == 64 ? 8 * (m >> 1) : 0);
+        const uint32_t addr = codes + swz<kRow>(k, chunk(unit, m));
+        ldsm_x4(addr, r[0], r[1], r[2], r[3]);
+        const int k0 = key<kK>(unit, 0, lane), k1 = key<kK>(unit, 2, lane);
+        uint32_t w0, w1;  // scale bytes of the chunks of m = 0, 1 and of m = 2, 3
+        if (HD == 64) {
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(scales + k0 * kGph));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(scales + k1 * kGph));
+        } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(scales + k0 * kGph + 2 * chunk(unit, 0)));
+        }
+        if (!((mask >> k0) & 1ull)) w0 = 0u;
+        if (!((mask >> k1) & 1ull)) w1 = 0u;
+        bytes = __byte_perm(w0, w1, 0x6420u + 0x1111u * ((lane & 3) >> 1));
+    }
+    // the eight values of matrix m as fp16 pairs
+    template <int m>
+    __device__ __forceinline__ void values(uint32_t (&h)[4]) const {
+        const uint32_t s = half_pair<m & 1>(m < 2 ? f16x2_from_e4m3x2(bytes) : f16x2_from_e4m3x2_hi(bytes));
+        f16x2_from_e2m1x8(r[m], h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = mul_f16x2(h[i], s);
+    }
+    // K: rows of the K-major operand blocks of 64 dims at dst, block_bytes apart
+    template <int m>
+    __device__ __forceinline__ void store_k1(uint32_t dst, uint32_t block_bytes, int unit, int lane) const {
+        uint32_t h[4];
+        values<m>(h);
+        const int c = chunk(unit, m);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         dst + (c >> 1) * block_bytes + sw128(key<true>(unit, m, lane), 4 * (c & 1) + (lane & 3))),
+                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                     : "memory");
+    }
+    __device__ __forceinline__ void store_k(uint32_t dst, uint32_t block_bytes, int unit, int lane) const {
+        store_k1<0>(dst, block_bytes, unit, lane);
+        store_k1<1>(dst, block_bytes, unit, lane);
+        store_k1<2>(dst, block_bytes, unit, lane);
+        store_k1<3>(dst, block_bytes, unit, lane);
+    }
+    // V: 8 keys of the V^T rows at dst (a key block's 64 keys)
+    template <int m>
+    __device__ __forceinline__ void store_v1(uint32_t dst, int unit, int lane) const {
+        uint32_t h[4];
+        values<m>(h);
+        const int ko = first_key(unit) / 8 + (HD == 64 ? m >> 1 : 0);
+        stsm_x4_t(dst + sw128(32 * chunk(unit, m) + lane, ko), h[0], h[1], h[2], h[3]);
+    }
+    __device__ __forceinline__ void store_v(uint32_t dst, int unit, int lane) const {
+        store_v1<0>(dst, unit, lane);
+        store_v1<1>(dst, unit, lane);
+        store_v1<2>(dst, unit, lane);
+        store_v1<3>(dst, unit, lane);
+    }
+    // NaN scales of V are taken as 0 and remembered
+    __device__ __forceinline__ void drop_nan(volatile int32_t *nan_seen) {
+        if ((((bytes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u) {
+            bytes &= ~nan_byte_mask(bytes);
+            *nan_seen = 1;
+        }
+    }
+};
+// the word of O's 32 columns that holds the output's dims 2w, 2w + 1 of the chunk
+template <bool F4>
+__host__ __device__ constexpr int o_word(int w) { return F4 ? 4 * (w & 3) + (w >> 2) : w; }
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
-}
-
-// The two scale bytes of a V key's 32 dims (0 for a key that is not valid; a NaN byte is taken
-// as 0 and remembered).
-__device__ __forceinline__ uint32_t value_scales_of(const uint8_t *p, bool valid, volatile int32_t *nan_seen) {
-    uint32_t b = *reinterpret_cast<const uint16_t *>(p);
-    if (!valid) return 0u;
-    const uint32_t n = nan_byte_mask(b);
-    if (n != 0u) {
-        b &= ~n;
-        *nan_seen = 1;
-    }
-    return b;
 }
 
 // The groups (bit g: dims 16g..16g+15) in which some value of tokens 0..last of the sequence is
@@ -736,7 +818,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
-            const uint8_t *ksc = kst + L::kScales, *vsc = ksc + L::kScaleSide;  // F4
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf;
             uint8_t *vdst = bp + L::kV + b * L::kVBuf;
             // K: 64 keys x HD/8 chunks of 8 fp8 -> one 16-byte f16 chunk (invalid keys: zeros);
@@ -762,11 +843,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const int key = ko * 8 + (lane >> 2);
                     const int sgi = (32 * dg) / L::kSeg, cc = ((32 * dg) % L::kSeg) >> 4;
-                    if constexpr (F4) {  // the 32 dims' 16 code bytes and their two scale bytes
-                        vw[j][0] = *reinterpret_cast<const uint4 *>(vst + swz<L::kSeg>(key, dg));
-                        vw[j][1].x = value_scales_of(vsc + key * (HD / 16) + 2 * dg, (mask >> key) & 1ull, nan_seen);
-                        continue;
-                    }
                     const uint8_t *vrow = vst + sgi * kPfKeys * L::kSeg;
                     vw[j][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[j][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
@@ -779,17 +855,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     const int blk = w4 + (g0 + j) * kPfConvWarps;
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const uint4 lo = vw[j][0], hi = vw[j][1];
-                    if constexpr (F4) {
-                        const uint32_t wd4[4] = {lo.x, lo.y, lo.z, lo.w};
-                        const uint32_t s0 = scale_pair(hi.x), s1 = scale_pair(hi.x >> 8);
-                        uint32_t h4[4];
-#pragma unroll
-                        for (int e4 = 0; e4 < 4; ++e4)  // dims 8e + 2(t%4), +1 of the key's 32
-                            h4[e4] = mul_f16x2(f16x2_from_e2m1x2(__byte_perm(wd4[e4], 0u, lane & 3)), e4 < 2 ? s0 : s1);
-                        const int n4 = 32 * dg + 8 * (lane >> 3) + (lane & 7);
-                        stsm_x4_t(vbase + sw128(n4, ko), h4[0], h4[1], h4[2], h4[3]);
-                        continue;
-                    }
                     const uint32_t wd[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     uint32_t r[4];
 #pragma unroll
@@ -799,16 +864,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     stsm_x4_t(vbase + sw128(n, ko), r[0], r[1], r[2], r[3]);
                 }
             };
+            if constexpr (F4) {
+                // K units, then V units, over the warps
+                constexpr int kU = F4Unit<HD>::kPer64, kMine = 2 * kU / kPfConvWarps;
+                const uint32_t codes = base + L::kStage + st * L::kStageBytes, scales = codes + L::kScales;
+                F4Unit<HD> un[kMine];
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const int u = w4 + j * kPfConvWarps;
+                    if (u < kU)
+                        un[j].template load<true>(codes, scales, mask, u, lane);
+                    else
+                        un[j].template load<false>(codes + kPfKeys * L::kRow, scales + L::kScaleSide, mask, u - kU, lane);
+                }
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const int u = w4 + j * kPfConvWarps;
+                    if (u < kU) {
+                        un[j].store_k(base + L::kK + b * L::kKBuf, kPfKeys * 128, u, lane);
+                    } else {
+                        un[j].drop_nan(nan_seen);
+                        un[j].store_v(vbase, u - kU, lane);
+                    }
+                }
+            } else {
 #pragma unroll
             for (int j = 0; j < kKT; ++j) {
                 const int task = ct + j * kCT;
                 const int key = task / (HD / 8), c = task % (HD / 8);  // dims 8c .. 8c+7
-                if constexpr (F4) {  // four code bytes and their group's scale byte
-                    kw[j].x = *reinterpret_cast<const uint32_t *>(kst + swz<L::kSeg>(key, c >> 2) + 4 * (c & 3));
-                    kw[j].y = ksc[key * (HD / 16) + (c >> 1)];
-                    if (!((mask >> key) & 1ull)) kw[j] = make_uint2(0u, 0u);
-                    continue;
-                }
                 const int sgi = (8 * c) / L::kSeg, within = (8 * c) % L::kSeg;
                 kw[j] = *reinterpret_cast<const uint2 *>(kst + sgi * kPfKeys * L::kSeg +
                                                          swz<L::kSeg>(key, within >> 4) + (within & 8));
@@ -821,14 +904,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 const int key = task / (HD / 8), c = task % (HD / 8);
                 const uint2 w = kw[j];
                 uint4 h;
-                if constexpr (F4) {
-                    h = dequant8(w.x, scale_pair(w.y));
-                } else {
-                    h.x = f16x2_from_e4m3x2(w.x);
-                    h.y = f16x2_from_e4m3x2_hi(w.x);
-                    h.z = f16x2_from_e4m3x2(w.y);
-                    h.w = f16x2_from_e4m3x2_hi(w.y);
-                }
+                h.x = f16x2_from_e4m3x2(w.x);
+                h.y = f16x2_from_e4m3x2_hi(w.x);
+                h.z = f16x2_from_e4m3x2(w.y);
+                h.w = f16x2_from_e4m3x2_hi(w.y);
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kPfKeys * 128) + sw128(key, c & 7)) = h;
             }
             v_store(0);
@@ -836,6 +915,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             for (int g0 = kVG; g0 < kVB; g0 += kVG) {
                 v_load(g0);
                 v_store(g0);
+            }
             }
             if (ct == 0) buf_mask[b] = mask;  // for the softmax warps, released with kv_ready
             fence_proxy_async();
@@ -969,10 +1049,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         uint4 w;
-                        w.x = bf16x2_from_f32(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
-                        w.y = bf16x2_from_f32(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
-                        w.z = bf16x2_from_f32(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv);
-                        w.w = bf16x2_from_f32(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv);
+                        auto word = [&](int k) {  // output word k of the 32 dims
+                            const int e = 2 * o_word<F4>(k);
+                            return bf16x2_from_f32(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        };
+                        w.x = word(c / 2);
+                        w.y = word(c / 2 + 1);
+                        w.z = word(c / 2 + 2);
+                        w.w = word(c / 2 + 3);
                         if (F4 && nan_groups != 0u) {
                             const int d = c0 + c;
                             w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
@@ -1371,7 +1455,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
-            const uint8_t *ksc = kst + L::kScales, *vsc = ksc + L::kScaleSide;  // F4
             // this half's 64 keys: rows 64*hf.. of every 64-dim block of the K buffer
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf + hf * (kPfKeys * 128);
             // and key block hf of the V^T buffer
@@ -1384,11 +1467,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const int key = ko * 8 + (lane >> 2);
                     const int sgi = (32 * dg) / L::kSeg, cc = ((32 * dg) % L::kSeg) >> 4;
-                    if constexpr (F4) {  // the 32 dims' 16 code bytes and their two scale bytes
-                        vw[q][0] = *reinterpret_cast<const uint4 *>(vst + swz<L::kSeg>(key, dg));
-                        vw[q][1].x = value_scales_of(vsc + key * (HD / 16) + 2 * dg, (mask >> key) & 1ull, nan_seen);
-                        continue;
-                    }
                     const uint8_t *vrow = vst + sgi * kPfKeys * L::kSeg;
                     vw[q][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[q][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
@@ -1401,17 +1479,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     const int blk = w8 + (g0 + q) * kP2ConvWarps;
                     const int ko = blk % (kPfKeys / 8), dg = blk / (kPfKeys / 8);
                     const uint4 lo = vw[q][0], hi = vw[q][1];
-                    if constexpr (F4) {
-                        const uint32_t wd4[4] = {lo.x, lo.y, lo.z, lo.w};
-                        const uint32_t s0 = scale_pair(hi.x), s1 = scale_pair(hi.x >> 8);
-                        uint32_t h4[4];
-#pragma unroll
-                        for (int e4 = 0; e4 < 4; ++e4)  // dims 8e + 2(t%4), +1 of the key's 32
-                            h4[e4] = mul_f16x2(f16x2_from_e2m1x2(__byte_perm(wd4[e4], 0u, lane & 3)), e4 < 2 ? s0 : s1);
-                        const int n4 = 32 * dg + 8 * (lane >> 3) + (lane & 7);
-                        stsm_x4_t(vbase + sw128(n4, ko), h4[0], h4[1], h4[2], h4[3]);
-                        continue;
-                    }
                     const uint32_t wd[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     uint32_t rv[4];
 #pragma unroll
@@ -1421,18 +1488,28 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     stsm_x4_t(vbase + sw128(n, ko), rv[0], rv[1], rv[2], rv[3]);
                 }
             };
+            constexpr int kU4 = F4Unit<HD>::kPer64 / kP2ConvWarps;  // F4: units a warp has of each side
+            F4Unit<HD> uv[kU4];
+            if constexpr (F4) {
+                const uint32_t codes = base + L::kStage + st * L::kStageBytes, scales = codes + L::kScales;
+                F4Unit<HD> uk[kU4];
+#pragma unroll
+                for (int q = 0; q < kU4; ++q) {
+                    uk[q].template load<true>(codes, scales, mask, w8 + q * kP2ConvWarps, lane);
+                    uv[q].template load<false>(codes + kPfKeys * L::kRow, scales + L::kScaleSide, mask,
+                                               w8 + q * kP2ConvWarps, lane);
+                }
+#pragma unroll
+                for (int q = 0; q < kU4; ++q)
+                    uk[q].store_k(base + L::kK + b * L::kKBuf + hf * (kPfKeys * 128), kP2Keys * 128,
+                                  w8 + q * kP2ConvWarps, lane);
+            } else {
             // K: every load of the half before its conversions
             uint2 kw[kKT];
 #pragma unroll
             for (int q = 0; q < kKT; ++q) {
                 const int task = ct + q * kCT;
                 const int key = task / (HD / 8), c = task % (HD / 8);
-                if constexpr (F4) {  // four code bytes and their group's scale byte
-                    kw[q].x = *reinterpret_cast<const uint32_t *>(kst + swz<L::kSeg>(key, c >> 2) + 4 * (c & 3));
-                    kw[q].y = ksc[key * (HD / 16) + (c >> 1)];
-                    if (!((mask >> key) & 1ull)) kw[q] = make_uint2(0u, 0u);
-                    continue;
-                }
                 const int sgi = (8 * c) / L::kSeg, within = (8 * c) % L::kSeg;
                 kw[q] = *reinterpret_cast<const uint2 *>(kst + sgi * kPfKeys * L::kSeg +
                                                          swz<L::kSeg>(key, within >> 4) + (within & 8));
@@ -1444,15 +1521,12 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 const int key = task / (HD / 8), c = task % (HD / 8);
                 const uint2 w = kw[q];
                 uint4 h;
-                if constexpr (F4) {
-                    h = dequant8(w.x, scale_pair(w.y));
-                } else {
-                    h.x = f16x2_from_e4m3x2(w.x);
-                    h.y = f16x2_from_e4m3x2_hi(w.x);
-                    h.z = f16x2_from_e4m3x2(w.y);
-                    h.w = f16x2_from_e4m3x2_hi(w.y);
-                }
+                h.x = f16x2_from_e4m3x2(w.x);
+                h.y = f16x2_from_e4m3x2_hi(w.x);
+                h.z = f16x2_from_e4m3x2(w.y);
+                h.w = f16x2_from_e4m3x2_hi(w.y);
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kP2Keys * 128) + sw128(key, c & 7)) = h;
+            }
             }
             if (hf == 1) {  // both halves of the tile's K are in place
                 fence_proxy_async();
@@ -1464,12 +1538,20 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kVFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            v_load(0);
-            v_store(0);
+            if constexpr (F4) {
 #pragma unroll
-            for (int g0 = kVG; g0 < kVB; g0 += kVG) {
-                v_load(g0);
-                v_store(g0);
+                for (int q = 0; q < kU4; ++q) {
+                    uv[q].drop_nan(nan_seen);
+                    uv[q].store_v(vbase, w8 + q * kP2ConvWarps, lane);
+                }
+            } else {
+                v_load(0);
+                v_store(0);
+#pragma unroll
+                for (int g0 = kVG; g0 < kVB; g0 += kVG) {
+                    v_load(g0);
+                    v_store(g0);
+                }
             }
             if (ct == 0) buf_mask[2 * b + hf] = mask;  // for the softmax warps, released with v_ready
             fence_proxy_async();
@@ -1620,10 +1702,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         uint4 w;
-                        w.x = bf16x2_from_f32(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv);
-                        w.y = bf16x2_from_f32(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
-                        w.z = bf16x2_from_f32(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv);
-                        w.w = bf16x2_from_f32(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv);
+                        auto word = [&](int k) {  // output word k of the 32 dims
+                            const int e = 2 * o_word<F4>(k);
+                            return bf16x2_from_f32(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        };
+                        w.x = word(c / 2);
+                        w.y = word(c / 2 + 1);
+                        w.z = word(c / 2 + 2);
+                        w.w = word(c / 2 + 3);
                         if (F4 && nan_groups != 0u) {
                             const int d = c0 + c;
                             w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
