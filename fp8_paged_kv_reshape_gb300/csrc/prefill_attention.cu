@@ -236,9 +236,8 @@ struct PrefillArgs {
 //
 // F4: the cache holds E2M1 codes with an E4M3 scale byte per 16 dims instead of E4M3 bytes.  Only
 // what fills the f16 operands differs: a stage holds the codes of its keys (boxes of one head's
-// head_dim/2-byte rows) and their scale bytes (contiguous per block and head, fetched by bulk
-// copies), and the conversion multiplies each fp16 pair of codes by its group's scale (exact:
-// code * scale is an fp16 number).
+// head_dim/2-byte rows) and their scale bytes (contiguous per block and head), and the conversion
+// multiplies each fp16 pair of codes by its group's scale (exact: code * scale is an fp16 number).
 //
 // NaN: a scale byte 0x7F makes its 16 dims NaN.  In K that makes the key's scores NaN, which the
 // masks keep from rows that do not see it.  In V it would reach every row of the tile (0 * NaN), so
@@ -358,10 +357,31 @@ struct F4Unit {
 template <bool F4>
 __host__ __device__ constexpr int o_word(int w) { return F4 ? 4 * (w & 3) + (w >> 2) : w; }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
+
+// The scale bytes of 64 keys from t0 on (K's at dst, V's side_bytes further), by all lanes of the
+// TMA warp: 16-byte asynchronous copies, each of 1 to 4 keys of one block, whose completion every lane
+// adds to the stage's barrier.  (As bulk copies they cost this warp one issue per block and side: 74
+// against 69 us for 16 chunks of 32 tokens over 4096 keys in 16-token blocks, 105 against 84 in 8-token
+// ones.)
+// win: the lane window of block-table entries from wbase on.
+template <int HD>
+__device__ __forceinline__ void copy_scales(const PrefillArgs &a, int kvh, int t0, int kend, int lbs, int32_t win,
+                                            int wbase, uint32_t dst, uint32_t side_bytes, uint32_t bar, int lane) {
+    constexpr int kGph = HD / 16, kKeys = 16 / kGph, kChunks = kPfKeys / kKeys;  // of a side
+#pragma unroll
+    for (int c = lane; c < 2 * kChunks; c += 32) {
+        const int k = c % kChunks * kKeys, t = t0 + k;
+        const int blk = __shfl_sync(0xFFFFFFFFu, win, ((t >> lbs) - wbase) & 31);
+        if (t < kend && blk >= 0 && blk < a.num_blocks) {
+            const uint8_t *src = (c < kChunks ? a.key_scales : a.value_scales) +
+                                 (((static_cast<int64_t>(blk) * a.n_kv + kvh) << lbs) + (t & (a.block_size - 1))) * kGph;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             dst + (c < kChunks ? 0u : side_bytes) + static_cast<uint32_t>(k * kGph)),
+                         "l"(src)
+                         : "memory");
+        }
+    }
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // The groups (bit g: dims 16g..16g+15) in which some value of tokens 0..last of the sequence is
@@ -498,7 +518,7 @@ struct PfSmem {
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;          // TMA box row (swizzle span)
     static constexpr int kSegs = kRow / kSeg;
     static constexpr int kNB = HD >= 256 ? 2 : 3;                  // f16 K/V^T and S buffers
-    static constexpr int kNS = HD >= 256 ? 1 : 4;                  // FP8 staging stages
+    static constexpr int kNS = HD >= 256 ? 1 : F4 ? 8 : 4;         // staging stages
     static constexpr int kQ = 0;                                   // Q f16: HD/64 blocks x 128 rows x 128 B
     static constexpr int kKBuf = HD * 128;                         // one K f16 buffer: HD/64 x 64 rows x 128 B
     // Up to head_dim 128, V^T carries 16 more rows: a row of ones then zeros, so the O
@@ -611,7 +631,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), 1);
+            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kPfConvWarps);
         }
         for (int b = 0; b < L::kNB; ++b) {
@@ -692,7 +712,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     meta[st] = mask;
                     const uint32_t full = bar(L::kFull, st);
                     if (boxes > 0)
-                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * (L::kRow + L::kScaleSide / kPfKeys)));
+                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * L::kRow));
                     else
                         mbar_arrive(full);
                     ++issued;
@@ -709,17 +729,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 for (int sgi = 0; sgi < L::kSegs; ++sgi)
                     tma_load_3d(dst + static_cast<uint32_t>(sgi * kPfKeys * L::kSeg), map, 0,
                                 kvh * L::kSegs + sgi, row, full);
-                if constexpr (F4) {  // br tokens' scale bytes: a multiple of 32
-                    constexpr int kGph = HD / 16;
-                    const uint8_t *sc = (k_lane ? a.key_scales : a.value_scales) +
-                                        ((static_cast<int64_t>(blk) * a.n_kv + kvh) * bs + (t & (bs - 1))) * kGph;
-                    bulk_load(base + L::kStage + st * L::kStageBytes + L::kScales +
-                                  (k_lane ? 0u : static_cast<uint32_t>(L::kScaleSide)) +
-                                  static_cast<uint32_t>(p * br * kGph),
-                              sc, static_cast<uint32_t>(br * kGph), full);
-                }
+            }
+            if constexpr (F4) {
+                const uint32_t stage = base + L::kStage + st * L::kStageBytes;
+                copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
+                                bar(L::kFull, st), lane);
             }
         }
+        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -1114,7 +1131,7 @@ struct Pf2Smem {
     static constexpr int kRow = F4 ? HD / 2 : HD;
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;
     static constexpr int kSegs = kRow / kSeg;
-    static constexpr int kNS = HD < 128 ? 4 : F4 ? 3 : 2;          // staging halves
+    static constexpr int kNS = HD < 128 ? (F4 ? 8 : 4) : F4 ? 3 : 2;  // staging halves
     static constexpr int kQTile = HD * 256;                        // one row tile of Q (f16)
     static constexpr int kQ = 0;
     // K f16: HD/64 blocks x 128 keys x 128 B; V^T f16: 2 key blocks x HD rows x 128 B
@@ -1232,7 +1249,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), 1);
+            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kP2ConvWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -1313,7 +1330,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     meta[st] = mask;
                     const uint32_t full = bar(L::kFull, st);
                     if (boxes > 0)
-                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * (L::kRow + L::kScaleSide / kPfKeys)));
+                        mbar_arrive_tx(full, static_cast<uint32_t>(boxes * 2 * br * L::kRow));
                     else
                         mbar_arrive(full);
                     ++issued;
@@ -1329,17 +1346,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 for (int sgi = 0; sgi < L::kSegs; ++sgi)
                     tma_load_3d(dst + static_cast<uint32_t>(sgi * kPfKeys * L::kSeg), map, 0,
                                 kvh * L::kSegs + sgi, row, full);
-                if constexpr (F4) {  // br tokens' scale bytes: a multiple of 32
-                    constexpr int kGph = HD / 16;
-                    const uint8_t *sc = (k_lane ? a.key_scales : a.value_scales) +
-                                        ((static_cast<int64_t>(blk) * a.n_kv + kvh) * bs + (t & (bs - 1))) * kGph;
-                    bulk_load(base + L::kStage + st * L::kStageBytes + L::kScales +
-                                  (k_lane ? 0u : static_cast<uint32_t>(L::kScaleSide)) +
-                                  static_cast<uint32_t>(p * br * kGph),
-                              sc, static_cast<uint32_t>(br * kGph), full);
-                }
+            }
+            if constexpr (F4) {
+                const uint32_t stage = base + L::kStage + st * L::kStageBytes;
+                copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
+                                bar(L::kFull, st), lane);
             }
         }
+        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
