@@ -96,25 +96,19 @@ __device__ __forceinline__ uint32_t bcast_hi(uint32_t x) {
     return r;
 }
 
-// A token's scale bytes (GPH of them): those that sel picks (every second one) as fp16 pairs, one
-// per two 32-dim chunks.
+// A token's scale bytes (2 KP of them): those that sel picks (every second one, one per 32-dim
+// chunk), four a word.
 template <int KP>
-__device__ __forceinline__ void lane_scales(const uint32_t *w, uint32_t sel, uint32_t (&out)[KP / 2]) {
-    if constexpr (KP == 2) {
-        out[0] = f16x2_from_e4m3x2(__byte_perm(w[0], 0u, sel));
-    } else {
+__device__ __forceinline__ void lane_bytes(const uint32_t *w, uint32_t sel, uint32_t (&out)[(KP + 3) / 4]) {
 #pragma unroll
-        for (int i = 0; i < KP / 2; i += 2) {
-            const uint32_t b = __byte_perm(w[i], w[i + 1], sel);
-            out[i] = f16x2_from_e4m3x2(b);
-            out[i + 1] = f16x2_from_e4m3x2_hi(b);
-        }
-    }
+    for (int i = 0; i < (KP + 3) / 4; ++i) out[i] = __byte_perm(w[2 * i], KP > 2 ? w[2 * i + 1] : 0u, sel);
 }
-
-// 0x3C00 (fp16 one) in each half of an fp16 pair that is NaN
-__device__ __forceinline__ uint32_t nan_ones(uint32_t h) {
-    return ((h & 0x7FFFu) > 0x7C00u ? 0x3C00u : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0x3C000000u : 0u);
+// the scale of chunk c as an fp16 pair (the conversion of two chunks is shared)
+template <int N>
+__device__ __forceinline__ uint32_t chunk_scale(const uint32_t (&bytes)[N], int c) {
+    const uint32_t b = bytes[c >> 2];
+    const uint32_t two = c & 2 ? f16x2_from_e4m3x2_hi(b) : f16x2_from_e4m3x2(b);
+    return c & 1 ? bcast_hi(two) : bcast_lo(two);
 }
 
 // Batches of up to kOwnPlanSeqs sequences take no plan kernel: each CTA's producer warp reads the
@@ -491,14 +485,14 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 float sacc[TT][NS][4];
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
-                    // scale pairs (chunk 2cp, 2cp + 1) of this lane's groups, rows gid and +8
-                    uint32_t sl[KP / 2], sh[KP / 2];
+                    // scale bytes of this lane's groups, rows gid and +8
+                    uint32_t sl[(KP + 3) / 4], sh[(KP + 3) / 4];
                     {
                         uint32_t w[2][GPH / 4];
                         lds(st + ks_off + (t0 + tt) * f.s2, w[0]);
                         lds(st + ks_off + (t0 + tt) * f.s2 + f.s1, w[1]);
-                        lane_scales<KP>(w[0], ksel, sl);
-                        lane_scales<KP>(w[1], ksel, sh);
+                        lane_bytes<KP>(w[0], ksel, sl);
+                        lane_bytes<KP>(w[1], ksel, sh);
                     }
                     // kSums running sums, so that a product waits for the one before the last only (170.0
                     // against 171.7 us on eight long sequences; for 16 columns the registers cost more)
@@ -515,8 +509,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                         ldsm_x4((st + krow_off + (t0 + tt) * f.c2) ^ (cp << 5), r[0], r[1], r[2], r[3]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {  // chunk 2cp + e
-                            const uint32_t xl = e ? bcast_hi(sl[cp]) : bcast_lo(sl[cp]);
-                            const uint32_t xh = e ? bcast_hi(sh[cp]) : bcast_lo(sh[cp]);
+                            const uint32_t xl = chunk_scale(sl, 2 * cp + e), xh = chunk_scale(sh, 2 * cp + e);
                             uint32_t ka[4], kb[4];
                             f16x2_from_e2m1x8(r[2 * e], ka);
                             f16x2_from_e2m1x8(r[2 * e + 1], kb);
@@ -626,24 +619,24 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 // ---- O^T[dim][column] += V^T . P^T
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
-                    // scale pairs (chunk 2cp, 2cp + 1) of this lane's groups: tokens 8h + 2 tig and +1
-                    auto value_scales = [&](int h, uint32_t (&vs)[2][KP / 2]) {
+                    // scale bytes of this lane's groups: tokens 8h + 2 tig and + 1
+                    auto value_scales = [&](int h, uint32_t (&vs)[2][(KP + 3) / 4]) {
                         uint32_t w[GPH / 2];  // both tokens' bytes
                         lds(st + vs_off + (t0 + tt) * f.s2 + h * f.s1, w);
-                        lane_scales<KP>(w, vsel, vs[0]);
-                        lane_scales<KP>(w + GPH / 4, vsel, vs[1]);
+                        lane_bytes<KP>(w, vsel, vs[0]);
+                        lane_bytes<KP>(w + GPH / 4, vsel, vs[1]);
                         if constexpr (kPartial) {
                             // Tokens that are not there: scale 0.  A column that does not see a token has
                             // weight 0 for it, and a NaN scale would make 0 * NaN of that, so NaN scales
                             // become 0 too and the outputs that do see the token are made NaN.
-                            uint32_t nan[2][KP / 2], any = 0;  // fp16 ones at NaN scales
+                            uint32_t nan[2][(KP + 3) / 4], any = 0;
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                                for (int cp = 0; cp < KP / 2; ++cp) {
-                                    if (!((mt.mask >> (row0 + 16 * tt + 8 * h + 2 * tig + k)) & 1u)) vs[k][cp] = 0u;
-                                    nan[k][cp] = kMulti ? nan_ones(vs[k][cp]) : 0u;
-                                    any |= nan[k][cp];
+                                for (int i = 0; i < (KP + 3) / 4; ++i) {
+                                    if (!((mt.mask >> (row0 + 16 * tt + 8 * h + 2 * tig + k)) & 1u)) vs[k][i] = 0u;
+                                    nan[k][i] = kMulti ? nan_byte_mask(vs[k][i]) : 0u;
+                                    any |= nan[k][i];
                                 }
                             if (!kMulti || !__any_sync(0xFFFFFFFFu, any != 0u)) return;
 #pragma unroll
@@ -652,8 +645,8 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                                 fragment(movm_t(sees(row0 + 16 * tt + 8 * h + gid, v) ? 0x3C003C00u : 0u), seen);
 #pragma unroll
                                 for (int c = 0; c < KP; ++c) {
-                                    const uint32_t n0 = c % 2 ? bcast_hi(nan[0][c / 2]) : bcast_lo(nan[0][c / 2]);
-                                    const uint32_t n1 = c % 2 ? bcast_hi(nan[1][c / 2]) : bcast_lo(nan[1][c / 2]);
+                                    const uint32_t n0 = (nan[0][c >> 2] >> (8 * (c & 3))) & 1u ? 0x3C003C00u : 0u;
+                                    const uint32_t n1 = (nan[1][c >> 2] >> (8 * (c & 3))) & 1u ? 0x3C003C00u : 0u;
                                     // NaN tokens that the lane's column v sees (every element the same count)
                                     float cnt[4] = {0.f, 0.f, 0.f, 0.f};
                                     mma16816(cnt, n0, n0, n1, n1, seen[0], seen[1]);
@@ -665,8 +658,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                                for (int cp = 0; cp < KP / 2; ++cp)
-                                    vs[k][cp] &= ~(nan[k][cp] / 0x3C00u * 0xFFFFu);
+                                for (int i = 0; i < (KP + 3) / 4; ++i) vs[k][i] &= ~nan[k][i];
                         }
                     };
                     // the codes of chunks 4 c4.. of half h (at head_dim 64 one load has both halves)
@@ -685,7 +677,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     if constexpr (kPair) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t vs[2][KP / 2], pb[NV][2];
+                            uint32_t vs[2][(KP + 3) / 4], pb[NV][2];
                             value_scales(h, vs);
 #pragma unroll
                             for (int v = 0; v < NV; ++v) fragment(pw[tt][h][v], pb[v]);
@@ -698,8 +690,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                                     const int c = 4 * c4 + e;
                                     uint32_t x[4];  // token 2 tig: dims 4g, +1 and +2, +3; then token 2 tig + 1
                                     f16x2_from_e2m1x8(r[e], x);
-                                    const uint32_t s0 = c % 2 ? bcast_hi(vs[0][c / 2]) : bcast_lo(vs[0][c / 2]);
-                                    const uint32_t s1 = c % 2 ? bcast_hi(vs[1][c / 2]) : bcast_lo(vs[1][c / 2]);
+                                    const uint32_t s0 = chunk_scale(vs[0], c), s1 = chunk_scale(vs[1], c);
                                     x[0] = hmul2(x[0], s0);
                                     x[1] = hmul2(x[1], s0);
                                     x[2] = hmul2(x[2], s1);
@@ -711,7 +702,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             }
                         }
                     } else {
-                        uint32_t vs[2][2][KP / 2];
+                        uint32_t vs[2][2][(KP + 3) / 4];
                         value_scales(0, vs[0]);
                         value_scales(1, vs[1]);
 #pragma unroll
@@ -728,10 +719,8 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                                 for (int h = 0; h < 2; ++h) {
                                     f16x2_from_e2m1x8(r[h][e], x[h]);
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint32_t sp = vs[h][i >> 1][c / 2];
-                                        x[h][i] = hmul2(x[h][i], c % 2 ? bcast_hi(sp) : bcast_lo(sp));
-                                    }
+                                    for (int i = 0; i < 4; ++i)
+                                        x[h][i] = hmul2(x[h][i], chunk_scale(vs[h][i >> 1], c));
                                 }
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {  // token pairs of dims 4g + 2j, 4g + 2j + 1
