@@ -23,6 +23,7 @@ from .binding import (  # noqa: F401
     copy_blocks,
     dequant,
     dequant_fp4,
+    paged_attention_fp4_workspace_size,
     paged_attention_multi,
     paged_attention_multi_fp4,
     paged_attention_multi_mixed,

@@ -42,6 +42,7 @@ ABI_FUNCTIONS = (
     "kvfp8_dequant",
     "kvfp8_reshape_and_cache_fp4",
     "kvfp8_dequant_fp4",
+    "kvfp8_paged_attention_fp4_workspace_size",
     "kvfp8_paged_decode_attention_fp4",
     "kvfp8_paged_attention_multi_fp4",
     "kvfp8_copy_blocks",
@@ -109,6 +110,8 @@ def _load() -> ctypes.CDLL:
     lib.kvfp8_dequant_fp4.argtypes = [P, ctypes.c_int, P, P, i32, i32, i32, i32, P, i64, P,
                                       ctypes.c_int, P, P]
     lib.kvfp8_dequant_fp4.restype = ctypes.c_int
+    lib.kvfp8_paged_attention_fp4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.kvfp8_paged_attention_fp4_workspace_size.restype = sz
     lib.kvfp8_paged_decode_attention_fp4.argtypes = [P, P, P, P, P, P, P, i32, P, i32, i32, i32,
                                                      i32, i32, i32, f32, P, P, ctypes.c_int, P, sz,
                                                      P, P]
@@ -640,6 +643,14 @@ def dequant_fp4(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.T
     return out
 
 
+def paged_attention_fp4_workspace_size(num_seqs: int, n_q: int, n_kv: int, head_dim: int,
+                                       max_query_len: int, max_blocks_per_seq: int,
+                                       block_size: int) -> int:
+    """Workspace bytes of paged_decode_attention_fp4 (max_query_len 1) and paged_attention_multi_fp4."""
+    return LIB.kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
+                                                        max_blocks_per_seq, block_size)
+
+
 def _check_attention_fp4(query, key_cache, value_cache, key_scales, value_scales, block_tables,
                          seq_lens, k_scale, v_scale, out, workspace, status, num_seqs,
                          query_start_loc=None):
@@ -681,13 +692,16 @@ def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
     if out is None:
         out = _empty(query.shape, torch.bfloat16, dev, stream)
     if workspace is None:
-        workspace = _empty(LIB.kvfp8_paged_decode_workspace_size(num_seqs, n_q, hd), torch.uint8, dev,
-                           stream)
+        need = LIB.kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, hd, 1,
+                                                            block_tables.shape[1], bs)
+        if need > 0:
+            workspace = _empty(need, torch.uint8, dev, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = LIB.kvfp8_paged_decode_attention_fp4(
         _addr(out), _addr(query), _addr(key_cache), _addr(value_cache), _addr(key_scales),
         _addr(value_scales), _addr(block_tables), block_tables.shape[1], _addr(seq_lens), num_seqs,
-        n_q, n_kv, hd, bs, nb, float(sm_scale), _addr(k_scale), _addr(v_scale), sdt, _addr(workspace),
-        workspace.numel() * workspace.element_size(), _addr(status), _raw_stream(stream, dev))
+        n_q, n_kv, hd, bs, nb, float(sm_scale), _addr(k_scale), _addr(v_scale), sdt,
+        _addr(workspace), ws_bytes, _addr(status), _raw_stream(stream, dev))
     _check(rc, "kvfp8_paged_decode_attention_fp4")
     return out
 
@@ -710,7 +724,8 @@ def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor
     rows, n_q, hd, nb, bs, n_kv, sdt, dev = _check_attention_fp4(
         query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
         v_scale, out, workspace, status, num_seqs, query_start_loc)
-    need = paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, hd, max_query_len)
+    need = paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, hd, max_query_len,
+                                              block_tables.shape[1], bs)
     if out is None:
         out = _empty(query.shape, torch.bfloat16, dev, stream)
     if workspace is None and need > 0:

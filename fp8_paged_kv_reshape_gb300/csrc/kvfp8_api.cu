@@ -593,6 +593,15 @@ kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const uint8_t *
     return from_cuda(kvfp8::launch_dequant_fp4(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
+                                                int32_t head_dim, int32_t max_query_len,
+                                                int32_t max_blocks_per_seq, int32_t block_size) {
+    if (max_blocks_per_seq < 1 || block_size < 1 ||
+        kvfp8::fp4_takes_sequences_whole(max_blocks_per_seq, block_size))
+        return 0;
+    return kvfp8_paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len);
+}
+
 kvfp8_status kvfp8_paged_decode_attention_fp4(
     void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
     const uint8_t *key_scales, const uint8_t *value_scales, const int32_t *block_tables,
@@ -607,11 +616,12 @@ kvfp8_status kvfp8_paged_decode_attention_fp4(
     if (v != KVFP8_OK || nothing_to_do) return v;
     const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
     if (sh != KVFP8_OK) return sh;
-    if (!key_scales || !value_scales || !workspace) return KVFP8_ERR_NULL;
-    if (!aligned16(key_scales) || !aligned16(value_scales) || !aligned16(workspace))
+    const size_t need = kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, head_dim, 1,
+                                                                 max_blocks_per_seq, block_size);
+    if (!key_scales || !value_scales || (need > 0 && !workspace)) return KVFP8_ERR_NULL;
+    if (!aligned16(key_scales) || !aligned16(value_scales) || (need > 0 && !aligned16(workspace)))
         return KVFP8_ERR_ALIGN;
-    if (workspace_bytes < kvfp8_paged_decode_workspace_size(num_seqs, n_q, head_dim))
-        return KVFP8_ERR_WORKSPACE;
+    if (workspace_bytes < need) return KVFP8_ERR_WORKSPACE;
     kvfp8::DecodeArgs d;
     d.out = out;
     d.query = query;
@@ -664,17 +674,17 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
     if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
     if (num_seqs == 0) return KVFP8_OK;
+    const size_t need = kvfp8_paged_attention_fp4_workspace_size(
+        num_seqs, n_q, n_kv, head_dim, max_query_len, max_blocks_per_seq, block_size);
     if (!out || !query || !query_start_loc || !key_cache || !value_cache || !key_scales ||
-        !value_scales || !block_tables || !seq_lens || (split_kv && !workspace))
+        !value_scales || !block_tables || !seq_lens || (need > 0 && !workspace))
         return KVFP8_ERR_NULL;
     if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) ||
         !aligned16(value_cache) || !aligned16(key_scales) || !aligned16(value_scales) ||
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) ||
-        (split_kv && !aligned16(workspace)))
+        (need > 0 && !aligned16(workspace)))
         return KVFP8_ERR_ALIGN;
-    if (workspace_bytes <
-        kvfp8_paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len))
-        return KVFP8_ERR_WORKSPACE;
+    if (workspace_bytes < need) return KVFP8_ERR_WORKSPACE;
     kvfp8::DecodeArgs d;
     d.out = out;
     d.query = query;

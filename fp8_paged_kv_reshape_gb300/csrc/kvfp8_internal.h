@@ -178,6 +178,8 @@ bool mixed_uses_decode_kernel(int32_t n_q, int32_t n_kv, int32_t head_dim, int32
 // The split-KV kernel over the 4-bit cache (key_scales / value_scales set), for shapes
 // multi_uses_decode_kernel accepts; longer query chunks take launch_prefill_attention.
 cudaError_t launch_paged_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
+// True when that kernel splits no sequence of tables this wide, and so needs no workspace.
+bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
 
 // Multi-query (causal) attention on the tensor cores (tcgen05): long query chunks, or kv-head
 // counts the split-KV decode kernel does not cover.  Needs no workspace.

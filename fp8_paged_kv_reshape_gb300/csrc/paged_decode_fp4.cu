@@ -114,10 +114,18 @@ __device__ __forceinline__ uint32_t chunk_scale(const uint32_t (&bytes)[N], int 
 // Batches of up to kOwnPlanSeqs sequences take no plan kernel: each CTA's producer warp reads the
 // lengths and works out its CTA's range with a warp scan, while the other warps set up (64 sequences:
 // one launch and ~3 us less than the plan kernel in front).  CTA 0 leaves the chunk prefix for the
-// combine kernel.
+// combine kernel.  Where no sequence can be longer than kWholeTokens (the width of the block tables
+// says so) nothing is split: one CTA per sequence and head group, no partial results, no workspace
+// and no combine kernel (num_ctas = 0; four sequences of up to 100 tokens: 10.3 to 8.3 us).
 constexpr int kOwnPlanSeqs = 256;
+constexpr int kWholeTokens = 256;
 
 __device__ __forceinline__ CtaPlan own_plan(const KernelArgs &a, int lane) {
+    if (a.num_ctas == 0) {  // short sequences: CTA s takes sequence s whole
+        CtaPlan p = {0, 0, static_cast<int32_t>(blockIdx.x), 0, 0, 0, 0, 0};
+        p.hi = p.ce = seq_chunks<kTok>(a, p.s, p.L);
+        return p;
+    }
     constexpr int kRounds = kOwnPlanSeqs / 32;
     int n[kRounds];  // chunks of sequence 32 r + lane
     int sum = 0, L = 0;
@@ -910,9 +918,11 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     k.rows_per_seq = d.qmax * d.n_q;
     k.qrows = d.qrows;
 
-    const bool own_plan = d.num_seqs <= kOwnPlanSeqs;
+    const bool whole = fp4_takes_sequences_whole(d.max_blocks_per_seq, d.block_size);
+    const bool own_plan = whole || d.num_seqs <= kOwnPlanSeqs;
     if (own_plan) {
         k.cta_plan = nullptr;
+        if (whole) k.num_ctas = 0;
     } else {
         plan_kernel<kTok><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs,
                                                   k.max_len, num_ctas,
@@ -924,7 +934,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
 
     // programmatic dependent launches, as for the 8-bit kernel
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_ctas, groups);
+    cfg.gridDim = dim3(whole ? d.num_seqs : num_ctas, groups);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -933,7 +943,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = own_plan ? 0 : 1;  // (only a kernel of this call may be overtaken)
-    if ((err = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, tmks, tmvs, f)) != cudaSuccess) return err;
+    if ((err = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, tmks, tmvs, f)) != cudaSuccess || whole) return err;
 
     constexpr int kHeadsPerCta = 256 / (HD / 4);
     cudaLaunchConfig_t ccfg = cfg;
@@ -964,6 +974,10 @@ cudaError_t run_tiles(const DecodeArgs &d, const DecodeWorkspace &ws, int tiles,
 }
 
 }  // namespace
+
+bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size) {
+    return static_cast<int64_t>(max_blocks_per_seq) * block_size <= kWholeTokens;
+}
 
 cudaError_t launch_paged_decode_fp4(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;

@@ -425,14 +425,24 @@ KVFP8_API kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const
                                          uint32_t *status, kvfp8_stream_t stream);
 
 /*
+ * Workspace bytes of the two calls below (decode: max_query_len 1): the split-KV partials, at most
+ * kvfp8_paged_attention_multi_workspace_size's; 0, where the workspace may be NULL, when the
+ * tensor-core kernel serves the shape or the block tables hold at most 256 tokens per sequence
+ * (sequences are then not split).  Pure host arithmetic.
+ */
+KVFP8_API size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
+                                                          int32_t head_dim, int32_t max_query_len,
+                                                          int32_t max_blocks_per_seq,
+                                                          int32_t block_size);
+
+/*
  * kvfp8_paged_decode_attention over the 4-bit cache:
  *   s_t = sm_scale * k_scale * sum_d q[b][h][d] * Kcode(t, kv, d) * KB(t, kv, d / 16)
  *   out[b][h][d] = v_scale * sum_t softmax(s)_t * Vcode(t, kv, d) * VB(t, kv, d / 16)
  * code*B has at most six significant bits and enters the tensor cores as fp16 exactly;
  * accumulation is fp32.  A token's NaN reaches exactly the outputs that see the token (all of
- * a row for a NaN in K, the group's 16 dims for a NaN in V).  Workspace:
- * kvfp8_paged_decode_workspace_size(num_seqs, n_q, head_dim).  Everything else (group sizes,
- * empty sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
+ * a row for a NaN in K, the group's 16 dims for a NaN in V).  Everything else (group sizes, empty
+ * sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
  */
 KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
     void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
@@ -444,7 +454,7 @@ KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
 
 /*
  * kvfp8_paged_attention_multi (causal, several new tokens per sequence, any chunk length) over
- * the 4-bit cache.  Workspace: kvfp8_paged_attention_multi_workspace_size(...).
+ * the 4-bit cache.
  */
 KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
     void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,

@@ -133,6 +133,18 @@ def test_compact_refusals(over, code):
     assert _compact(**over) == code
 
 
+def test_attention_workspace_follows_the_route():
+    ws = kv.paged_attention_fp4_workspace_size
+    assert ws(4, 32, 8, 128, 1, 256, 16) == kv.paged_decode_workspace_size(4, 32, 128) > 0
+    assert ws(4, 32, 8, 128, 4, 256, 16) == kv.paged_attention_multi_workspace_size(4, 32, 8, 128, 4) > 0
+    assert ws(4, 32, 8, 128, 5, 256, 16) == 0                                 # 20 columns: tensor cores
+    assert ws(4, 32, 8, 128, 1, 16, 16) == 0 < ws(4, 32, 8, 128, 1, 17, 16)   # 256 tokens: not split
+    assert ws(-1, 32, 8, 128, 1, 256, 16) == ws(4, 32, 8, 128, 1, 0, 16) == 0
+    assert _decode(max_blocks_per_seq=16, workspace=None, workspace_bytes=0, num_blocks=0) == binding.ERR_SHAPE
+    assert _decode(max_blocks_per_seq=17, workspace=None) == binding.ERR_NULL
+    assert _multi(max_blocks_per_seq=16, workspace=None, workspace_bytes=0, qsl=None) == binding.ERR_NULL
+
+
 def test_compact_workspace_size():
     assert kv.compact_blocks_workspace_size(0) == 0
     assert 0 < kv.compact_blocks_workspace_size(1) <= kv.compact_blocks_workspace_size(100000)
