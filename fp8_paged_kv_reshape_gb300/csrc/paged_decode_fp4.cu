@@ -191,15 +191,17 @@ __device__ __forceinline__ void finish_plan(const KernelArgs &a, int lane) {
     }
 }
 
-// NV: output tiles of 4 score columns per kv head.  kv heads (consumer warps) per CTA at most, and
-// CTAs per SM: as many warps as the accumulators and q leave registers for.  Two score tiles at
-// head_dim 128 keep q in shared memory.
+// NV: output tiles of 4 score columns per kv head (1, 2 or 4).  kv heads (consumer warps) per CTA at
+// most, and CTAs per SM, by the registers of the accumulators (HD * NV / 8 of a lane) and of q.  16
+// columns at head_dim 128: eight warps of 168 registers that take 32 tokens at a time (55.0 us for 32
+// sequences of 4 new tokens each) against twelve of 128 that take 16 and keep q in shared memory
+// (57.4): independent work within a warp counts for more than warps here.
 template <int HD, int NV>
-__host__ __device__ constexpr int fp4_max_heads() { return HD * NV >= 256 ? 4 : kMaxKvHeads; }
+__host__ __device__ constexpr int fp4_max_heads() { return HD == 128 && NV == 4 ? 8 : HD * NV >= 256 ? 4 : 8; }
 template <int HD, int NV>
-__host__ __device__ constexpr int fp4_ctas_per_sm() { return HD <= 128 && HD * NV >= 256 ? 3 : 2; }
-template <int HD, int NV>
-__host__ __device__ constexpr bool fp4_q_in_smem() { return HD == 128 && NV > 2; }
+__host__ __device__ constexpr int fp4_ctas_per_sm() {
+    return HD == 128 && NV == 4 ? 1 : HD <= 128 && HD * NV >= 256 ? 3 : 2;
+}
 
 template <int HD, int NV, bool kMulti>
 __global__ void __launch_bounds__(32 * (fp4_max_heads<HD, NV>() + 1), fp4_ctas_per_sm<HD, NV>())
@@ -212,7 +214,6 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     constexpr int KP = HD / 32;    // 32-dim chunks
     constexpr int NS = (NV + 1) / 2;  // score tiles of 8 columns
     constexpr bool kPair = NV <= 2;   // how V and the weights meet, see below
-    constexpr int TT = NV <= 2 ? 2 : 1;  // 16-token tiles a consumer takes at a time (registers)
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -228,9 +229,6 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
     const uint32_t bars = base + static_cast<uint32_t>(S) * stage_bytes;  // full[S], empty[S]
     Fp4Chunk *meta = reinterpret_cast<Fp4Chunk *>(base_ptr + S * stage_bytes + 16 * S);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(meta + S);
-    constexpr bool kQS = fp4_q_in_smem<HD, NV>();
-    // kQS: q fragments past the abort flag, 16 bytes a lane per warp, 32-dim chunk and score tile
-    const uint32_t q_smem = (smem_u32(const_cast<int32_t *>(abort_flag)) + 31u) & ~15u;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -392,8 +390,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         // per column: the reference maximum (log2 domain) the weights are taken against, and this
         // lane's part of the sum of weights
         float m[NV], l[NV];
-        uint32_t qb[kQS ? 1 : KP][NS][4];
-        const uint32_t q_lane = q_smem + static_cast<uint32_t>((warp * KP * NS * 32 + lane) * 16);
+        uint32_t qb[KP][NS][4];
         // multi-query form: the sequence's first query row, its query tokens and the last cache position
         // the first of them may see
         int q0 = 0, nq = 1, first_lim = 0;
@@ -449,19 +446,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     for (int c = 0; c < KP; ++c) {
                         uint4 w = make_uint4(0u, 0u, 0u, 0u);
                         if (qv) w = *reinterpret_cast<const uint4 *>(qrow + 32 * c + 8 * tig);
-                        const uint32_t h[4] = {f16x2_from_f32(bf16lo(w.x), bf16hi(w.x)) ^ q_sign,
-                                               f16x2_from_f32(bf16lo(w.y), bf16hi(w.y)) ^ q_sign,
-                                               f16x2_from_f32(bf16lo(w.z), bf16hi(w.z)) ^ q_sign,
-                                               f16x2_from_f32(bf16lo(w.w), bf16hi(w.w)) ^ q_sign};
-                        if constexpr (kQS) {  // read back by the same lane only
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             q_lane + static_cast<uint32_t>((c * NS + s) * 512)),
-                                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                                         : "memory");
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) qb[c][s][i] = h[i];
-                        }
+                        qb[c][s][0] = f16x2_from_f32(bf16lo(w.x), bf16hi(w.x)) ^ q_sign;
+                        qb[c][s][1] = f16x2_from_f32(bf16lo(w.y), bf16hi(w.y)) ^ q_sign;
+                        qb[c][s][2] = f16x2_from_f32(bf16lo(w.z), bf16hi(w.z)) ^ q_sign;
+                        qb[c][s][3] = f16x2_from_f32(bf16lo(w.w), bf16hi(w.w)) ^ q_sign;
                     }
                 }
 #pragma unroll
@@ -475,13 +463,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
             }
 
-            // One pass over TT 16-token tiles of the chunk, from tile t0 on.
             // kPartial: some column does not see some token of the chunk.  The common chunk has a body
             // without those tests: one basic block from the weights to the last product.
-            auto pass = [&](auto partial_tag, const int t0) {
+            auto chunk = [&](auto partial_tag) {
                 constexpr bool kPartial = decltype(partial_tag)::value;
                 const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
-                const int row0 = 16 * t0;
                 auto sees = [&](int row, int v) {  // row of the chunk
                     if (((mt.mask >> row) & 1u) == 0u) return false;
                     if (!kMulti) return true;
@@ -490,15 +476,15 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 };
 
                 // ---- scores S^T[token][column] = K . q^T, tiles of 16 tokens
-                float sacc[TT][NS][4];
+                float sacc[2][NS][4];
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
+                for (int tt = 0; tt < 2; ++tt) {
                     // scale bytes of this lane's groups, rows gid and +8
                     uint32_t sl[(KP + 3) / 4], sh[(KP + 3) / 4];
                     {
                         uint32_t w[2][GPH / 4];
-                        lds(st + ks_off + (t0 + tt) * f.s2, w[0]);
-                        lds(st + ks_off + (t0 + tt) * f.s2 + f.s1, w[1]);
+                        lds(st + ks_off + tt * f.s2, w[0]);
+                        lds(st + ks_off + tt * f.s2 + f.s1, w[1]);
                         lane_bytes<KP>(w[0], ksel, sl);
                         lane_bytes<KP>(w[1], ksel, sh);
                     }
@@ -514,7 +500,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                     for (int cp = 0; cp < KP / 2; ++cp) {
                         uint32_t r[4];
-                        ldsm_x4((st + krow_off + (t0 + tt) * f.c2) ^ (cp << 5), r[0], r[1], r[2], r[3]);
+                        ldsm_x4((st + krow_off + tt * f.c2) ^ (cp << 5), r[0], r[1], r[2], r[3]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {  // chunk 2cp + e
                             const uint32_t xl = chunk_scale(sl, 2 * cp + e), xh = chunk_scale(sh, 2 * cp + e);
@@ -528,13 +514,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             }
 #pragma unroll
                             for (int s = 0; s < NS; ++s) {
-                                uint32_t q[4];
-                                if constexpr (kQS) {
-                                    lds(q_lane + static_cast<uint32_t>(((2 * cp + e) * NS + s) * 512), q);
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) q[i] = qb[2 * cp + e][s][i];
-                                }
+                                const uint32_t(&q)[4] = qb[2 * cp + e][s];
                                 mma16816(part[0][s], ka[0], kb[0], ka[1], kb[1], q[0], q[1]);
                                 mma16816(part[kSums - 1][s], ka[2], kb[2], ka[3], kb[3], q[2], q[3]);
                             }
@@ -555,16 +535,15 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
 #pragma unroll
-                        for (int tt = 0; tt < TT; ++tt)
+                        for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                if (!sees(row0 + 16 * tt + 8 * h + gid, v)) sacc[tt][v / 2][v % 2 + 2 * h] = -INFINITY;
+                                if (!sees(16 * tt + 8 * h + gid, v)) sacc[tt][v / 2][v % 2 + 2 * h] = -INFINITY;
                 }
                 auto column_top = [&](int v) {  // this lane's highest score of column v
-                    float x = fmaxf(sacc[0][v / 2][v % 2], sacc[0][v / 2][v % 2 + 2]);
-                    if constexpr (TT == 2)
-                        x = fmaxf(x, fmaxf(sacc[TT - 1][v / 2][v % 2], sacc[TT - 1][v / 2][v % 2 + 2]));
-                    return x * score_scale;
+                    const int s = v / 2, c = v % 2;
+                    return score_scale *
+                           fmaxf(fmaxf(sacc[0][s][c], sacc[0][s][c + 2]), fmaxf(sacc[1][s][c], sacc[1][s][c + 2]));
                 };
                 float top = -INFINITY;  // the highest score over its column's m
 #pragma unroll
@@ -599,26 +578,25 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     b[1] = __byte_perm(w, 0u, bsel1);
                 };
                 constexpr int NW = kPair ? NV : NS;
-                uint32_t pw[TT][2][NW];  // tokens 16 tt + 8 h + 2 tig, + 1
+                uint32_t pw[2][2][NW];  // tokens 16 tt + 8 h + 2 tig, + 1
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     constexpr int kCols = kPair ? 1 : 2;  // columns of a word
-                    float p[kCols][TT][2];
+                    float p[kCols][2][2];
 #pragma unroll
                     for (int k = 0; k < kCols; ++k) {
                         const int v = kPair ? w : 2 * w + k;
                         // a column that has seen no score yet: -inf - 0 for every token
                         const float sub = m[v] == -INFINITY ? 0.f : m[v];
 #pragma unroll
-                        for (int tt = 0; tt < TT; ++tt)
+                        for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
                                 p[k][tt][h] = ex2(fmaf(sacc[tt][v / 2][v % 2 + 2 * h], score_scale, -sub));
-                        l[v] += TT == 2 ? (p[k][0][0] + p[k][0][1]) + (p[k][TT - 1][0] + p[k][TT - 1][1])
-                                        : p[k][0][0] + p[k][0][1];
+                        l[v] += (p[k][0][0] + p[k][0][1]) + (p[k][1][0] + p[k][1][1]);
                     }
 #pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
+                    for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             pw[tt][h][w] = movm_t(f16x2_from_f32(p[0][tt][h], p[kCols - 1][tt][h]));
@@ -626,11 +604,11 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 
                 // ---- O^T[dim][column] += V^T . P^T
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) {
+                for (int tt = 0; tt < 2; ++tt) {
                     // scale bytes of this lane's groups: tokens 8h + 2 tig and + 1
                     auto value_scales = [&](int h, uint32_t (&vs)[2][(KP + 3) / 4]) {
                         uint32_t w[GPH / 2];  // both tokens' bytes
-                        lds(st + vs_off + (t0 + tt) * f.s2 + h * f.s1, w);
+                        lds(st + vs_off + tt * f.s2 + h * f.s1, w);
                         lane_bytes<KP>(w, vsel, vs[0]);
                         lane_bytes<KP>(w + GPH / 4, vsel, vs[1]);
                         if constexpr (kPartial) {
@@ -642,7 +620,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
                                 for (int i = 0; i < (KP + 3) / 4; ++i) {
-                                    if (!((mt.mask >> (row0 + 16 * tt + 8 * h + 2 * tig + k)) & 1u)) vs[k][i] = 0u;
+                                    if (!((mt.mask >> (16 * tt + 8 * h + 2 * tig + k)) & 1u)) vs[k][i] = 0u;
                                     nan[k][i] = kMulti ? nan_byte_mask(vs[k][i]) : 0u;
                                     any |= nan[k][i];
                                 }
@@ -650,7 +628,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
 #pragma unroll
                             for (int v = 0; v < NV; ++v) {
                                 uint32_t seen[2];  // fp16 ones where the column sees the token (at both parities)
-                                fragment(movm_t(sees(row0 + 16 * tt + 8 * h + gid, v) ? 0x3C003C00u : 0u), seen);
+                                fragment(movm_t(sees(16 * tt + 8 * h + gid, v) ? 0x3C003C00u : 0u), seen);
 #pragma unroll
                                 for (int c = 0; c < KP; ++c) {
                                     const uint32_t n0 = (nan[0][c >> 2] >> (8 * (c & 3))) & 1u ? 0x3C003C00u : 0u;
@@ -672,13 +650,13 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     // the codes of chunks 4 c4.. of half h (at head_dim 64 one load has both halves)
                     uint32_t r64[4];
                     if constexpr (HD == 64)
-                        ldsm_x4_t(st + vrow_off + (t0 + tt) * f.c2, r64[0], r64[1], r64[2], r64[3]);
+                        ldsm_x4_t(st + vrow_off + tt * f.c2, r64[0], r64[1], r64[2], r64[3]);
                     auto value_codes = [&](int h, int c4, uint32_t (&r)[4]) {
                         if constexpr (HD == 64) {
                             r[0] = r64[2 * h];
                             r[1] = r64[2 * h + 1];
                         } else {
-                            ldsm_x4_t((st + vrow_off + (t0 + tt) * f.c2 + h * f.c1) ^ (c4 << 6), r[0], r[1], r[2], r[3]);
+                            ldsm_x4_t((st + vrow_off + tt * f.c2 + h * f.c1) ^ (c4 << 6), r[0], r[1], r[2], r[3]);
                         }
                     };
                     constexpr int kC = KP < 4 ? KP : 4;  // chunks of a load
@@ -745,13 +723,10 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                     }
                 }
             };
-            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim)) {
-#pragma unroll 1
-                for (int t = 0; t < 2; t += TT) pass(std::false_type{}, t);
-            } else if (mt.mask != 0u) {
-#pragma unroll 1
-                for (int t = 0; t < 2; t += TT) pass(std::true_type{}, t);
-            }
+            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim))
+                chunk(std::false_type{});
+            else if (mt.mask != 0u)
+                chunk(std::true_type{});
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + 8 * (S + stage));
             if (++stage == S) {
@@ -858,10 +833,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     f.s2 = box_rows == 32 ? 16 * (HD / 16) : box_rows == 16 ? f.scale_box : 2 * f.scale_box;
     const int ctas_per_sm = fp4_ctas_per_sm<HD, NV>();
     constexpr int kMaxStages = 8;
-    const size_t q_bytes = fp4_q_in_smem<HD, NV>() ? static_cast<size_t>(hpc) * (HD / 32) * ((NV + 1) / 2) * 512 + 16 : 0;
-    auto smem_for = [&](int st) {
-        return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024 + q_bytes;
-    };
+    auto smem_for = [&](int st) { return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024; };
     const size_t sm_budget = static_cast<size_t>(smem_optin) + 1024;
     int stages = kMaxStages;
     while (stages > 2 && (smem_for(stages) + 1024) * ctas_per_sm > sm_budget) --stages;
