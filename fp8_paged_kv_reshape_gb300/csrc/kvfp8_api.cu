@@ -42,7 +42,8 @@ kvfp8_status check_fp4_cache(int32_t num_blocks, int32_t block_size, int32_t n_k
 // the cache list of the page calls: KVFP8_OK with *out filled, or what is wrong with it
 kvfp8_status make_cache_list(void *const *caches, const int64_t *block_bytes, int32_t num_caches,
                              int32_t num_blocks, kvfp8::CacheList *out) {
-    if (num_caches < 1 || num_caches > KVFP8_MAX_CACHES || num_blocks < 1) return KVFP8_ERR_SHAPE;
+    if (num_caches < 1 || num_caches > KVFP8_MAX_CACHES || num_blocks < 1 || num_blocks > (1 << 30))
+        return KVFP8_ERR_SHAPE;
     if (!caches || !block_bytes) return KVFP8_ERR_NULL;
     for (int32_t c = 0; c < num_caches; ++c) {
         if (block_bytes[c] < 1 || block_bytes[c] > (int64_t{1} << 40)) return KVFP8_ERR_SHAPE;
@@ -744,7 +745,7 @@ kvfp8_status kvfp8_compact_blocks(void *const *caches, const int64_t *block_byte
     kvfp8::CacheList list;
     const kvfp8_status v = make_cache_list(caches, block_bytes, num_caches, num_blocks, &list);
     if (v != KVFP8_OK) return v;
-    if (block_size < 1 || num_seqs < 0 || max_blocks_per_seq < 1 ||
+    if (block_size < 1 || num_seqs < 0 || max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 30) ||
         static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL)
         return KVFP8_ERR_SHAPE;
     if (!num_used || !workspace ||

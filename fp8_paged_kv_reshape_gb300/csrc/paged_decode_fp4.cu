@@ -1,13 +1,15 @@
 // Paged decode attention over the 4-bit cache (E2M1 codes, an E4M3 scale per 16 dims), sm_103a:
 //   s_t = sm_scale * k_scale * q . (code_K B_K)_t,   out = v_scale * softmax(s) . (code_V B_V)
 //
-// The split of the work, the plan and combine kernels, the ring of TMA stages with one producer
-// warp and one consumer warp per kv head, and the online softmax are those of the 8-bit kernel
-// (paged_decode_kernel.cuh).  What differs is what a chunk of 16 tokens holds and how a consumer
-// makes tensor-core operands of it:
-//  * 0.5625 bytes per element: per side a box of [heads][16 tokens][head_dim/2] code bytes
-//    (swizzled over its 32-, 64- or 128-byte rows) and one of [heads][16 tokens][head_dim/16]
-//    scale bytes, four TMA loads per chunk (eight when 8-token blocks cut it in two).
+// The split of the work, the combine kernel, the ring of TMA stages with one producer warp and one
+// consumer warp per kv head are those of the 8-bit kernel (paged_decode_kernel.cuh).  A cached
+// element is 0.5625 bytes, so at the HBM rate nearly twice as many elements a second have to be
+// converted, and what a consumer does per element decides (an SM has 412 issue slots a scheduler for
+// 16 tokens of a head at 6.8 TB/s; conversions, permutes and maxima go at half that rate):
+//  * Chunks of 32 tokens: barriers, records and the softmax's bookkeeping are paid half as often.
+//    Per side a box of [heads][tokens][head_dim/2] code bytes (swizzled over its 32-, 64- or 128-byte
+//    rows) and one of [heads][tokens][head_dim/16] scale bytes; a block of less than 32 tokens is a
+//    box, and lane p of the producer issues box p of each.
 //  * code * B has at most 2 + 4 significant bits and lies between 2^-10 and 2688, so it is an
 //    fp16 number: codes convert to fp16 pairs, one packed multiply applies the group's scale
 //    exactly, and the products are those of fp16 mma.sync with fp32 accumulation.
@@ -15,14 +17,25 @@
 //    32-dim chunk (t = lane % 4) for token rows lane/4 and +8; the k order of the two products
 //    of a chunk is that order, for q too.  All 8 lie in one group of 16, so a lane needs one
 //    scale per row and chunk.
+//  * Weights are taken against a reference maximum that lags the running one (see below), so most
+//    chunks need no maximum over lanes and rescale nothing.
 //  * V (A operand, dims x tokens): ldmatrix.trans gives the 4 codes of dims 4g..4g+3 (g =
-//    lane / 4) of two tokens; they are converted, regrouped into token pairs per dim (one byte
-//    permute each) and multiplied by the tokens' scale pair.  A lane ends up with 4 consecutive
-//    output dims per chunk.
+//    lane / 4) of two tokens, and conversion leaves them as pairs of dims, where a product over
+//    tokens wants pairs of tokens.  Up to 8 score columns the product runs over (token, dim parity)
+//    instead: rows are pairs of dims, and the other operand holds the weights at one parity and zeros
+//    at the other, 4 columns to a tile of 8.  The four converted words of a lane are then an A
+//    fragment as they are; without it each took a byte permute (127 against 113 us for 128 x 4096
+//    tokens, 4 columns).  At 16 columns the doubled products would bind (384 of the 412 slots), and the
+//    permutes are shared by two tiles: that form regroups.
+//    A lane ends up with 4 consecutive output dims per 32-dim chunk.
 //  * NaN: a scale byte of 0x7F makes its 16 dims NaN.  Tokens past the end have their V scales
 //    zeroed.  In the multi-query form a chunk that some columns see only in part takes a second
 //    look: NaN scales of V are zeroed too, and the outputs whose column does see the token are
 //    made NaN from a product of indicators.
+//
+// 64 sequences of 4096 tokens, 32 / 8 heads of 128: 64.8 us a call (302 MB: 4.67 TB/s; the slope between
+// 64 and 128 sequences is 6.4 TB/s, so the rest is start, tail and combine); 8 sequences of 33k to 131k
+// tokens, 64 / 8 heads: 168 us (864 MB: 5.14 TB/s).
 #include "paged_decode_kernel.cuh"
 
 #include <type_traits>

@@ -480,7 +480,7 @@ KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
  * KVFP8_DEV_BAD_BLOCK.  (The conflict rule counts the pairs that are left after these.)
  *
  * caches, block_bytes  host arrays [num_caches] of device pointers and sizes; num_caches in
- *                      [1, KVFP8_MAX_CACHES]; the caches must not overlap
+ *                      [1, KVFP8_MAX_CACHES]; the caches must not overlap; num_blocks <= 2^30
  * src_blocks, dst_blocks  device int32 [num_pairs], 4-byte aligned; num_pairs >= 0, < 2^31
  */
 #define KVFP8_MAX_CACHES 128

@@ -114,7 +114,7 @@ def test_multi_refusals(over, code):
 
 @pytest.mark.parametrize("over, code", [
     (dict(num_caches=0), binding.ERR_SHAPE), (dict(num_caches=129), binding.ERR_SHAPE),
-    (dict(num_blocks=0), binding.ERR_SHAPE), (dict(pairs=-1), binding.ERR_SHAPE), (dict(pairs=1 << 31), binding.ERR_SHAPE),
+    (dict(num_blocks=0), binding.ERR_SHAPE), (dict(num_blocks=(1 << 30) + 1), binding.ERR_SHAPE), (dict(pairs=-1), binding.ERR_SHAPE), (dict(pairs=1 << 31), binding.ERR_SHAPE),
     (dict(caches=None), binding.ERR_NULL), (dict(block_bytes=None), binding.ERR_NULL), (dict(src=None), binding.ERR_NULL),
     (dict(ptrs=(16, 0)), binding.ERR_NULL), (dict(sizes=(1024, 0)), binding.ERR_SHAPE),
     (dict(sizes=(1024, 24)), binding.ERR_ALIGN), (dict(ptrs=(16, 4104)), binding.ERR_ALIGN),

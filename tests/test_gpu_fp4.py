@@ -311,6 +311,28 @@ def test_multi_matches_the_oracle(n_q, n_kv, hd, bs, lengths, qlens):
     check_attention(out, case, lengths, one_tile=route_one_tile(n_q, n_kv, hd, max(qlens)))
 
 
+@pytest.mark.parametrize("n", [255, 256, 257, 700])
+@pytest.mark.parametrize("longest", [250, 300])
+def test_many_short_sequences(n, longest):
+    """Both plans of the split, and sequences taken whole; some empty, some without queries."""
+    r = np.random.default_rng(n + longest)
+    lengths = r.integers(0, longest + 1, n)
+    lengths[5] = longest
+    lengths = lengths.tolist()
+    case = build(4, 2, 64, 16, lengths, [1] * n, 26)
+    st = status()
+    out = decode(case, lengths, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_attention(out, case, lengths)
+    qlens = np.minimum(r.integers(0, 4, n), lengths).tolist()
+    case = build(4, 2, 64, 16, lengths, qlens, 27)
+    out = multi(case, lengths, 3, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_attention(out, case, lengths)
+
+
 def test_multi_of_one_query_each_is_decode():
     lengths = [333, 17, 1200]
     case = build(32, 8, 128, 16, lengths, [1, 1, 1], 4)
