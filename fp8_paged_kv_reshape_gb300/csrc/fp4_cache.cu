@@ -208,14 +208,6 @@ struct RowMap {
     int32_t bs_log2;
 };
 
-// Scale byte of group g of the row at `slot` (slots and (block, head) pairs fit 32 bits).
-__device__ __forceinline__ int64_t scale_index(const RowMap &m, int n_kv, int32_t slot, int g) {
-    const int32_t blk = slot >> m.bs_log2, off = slot & ((1 << m.bs_log2) - 1);
-    const int32_t head = g >> m.gph_log2;
-    return (((static_cast<int64_t>(blk * n_kv + head) << m.bs_log2) + off) << m.gph_log2) +
-           (g & ((1 << m.gph_log2) - 1));
-}
-
 // kG: groups of a row per lane, 32 apart.
 template <bool kF32, bool kWide, int kG>
 __global__ void __launch_bounds__(32 * kWarps, kF32 ? 2 : 3)
@@ -289,8 +281,8 @@ write_fp4_kernel(const Fp4WriteArgs a, const RowMap m) {
     }
 }
 
-// Rows by slot, dequantized: the reader of the layout above.
-template <bool kBF16Out>
+// Rows by slot, dequantized: the reader of the layout above, with the same split of a row.
+template <bool kBF16Out, int kG>
 __global__ void __launch_bounds__(32 * kWarps)
 read_fp4_kernel(const Fp4ReadArgs a, const RowMap m, const int32_t wide) {
     const int lane = threadIdx.x & 31;
@@ -299,63 +291,84 @@ read_fp4_kernel(const Fp4ReadArgs a, const RowMap m, const int32_t wide) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
         return;
     }
-    const int g = (blockIdx.y << 5) + (lane & ((1 << m.lpr_log2) - 1));
+    const int g = (blockIdx.y << 5) * kG + (lane & ((1 << m.lpr_log2) - 1));
     if (g >= m.gpr) return;
-    const int64_t rpw = 32 >> m.lpr_log2;
+    const int rpw = 32 >> m.lpr_log2;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * rpw;
     int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * rpw + (lane >> m.lpr_log2);
-    const int64_t row_codes = static_cast<int64_t>(m.gpr) * 8;
     constexpr int kBytes = 16 * (kBF16Out ? 2 : 4);
-    uint8_t *dst = static_cast<uint8_t *>(a.dst) + static_cast<int64_t>(g) * kBytes;
     const int64_t row_bytes = static_cast<int64_t>(m.gpr) * kBytes;
+    uint8_t *dst = static_cast<uint8_t *>(a.dst) + t * row_bytes + static_cast<int64_t>(g) * kBytes;
+    const uint32_t row_codes = static_cast<uint32_t>(m.gpr) * 8;
+    const uint8_t *codes = a.codes + static_cast<int64_t>(g) * 8;
+    const uint8_t *scales = a.scales + (static_cast<int64_t>(g >> m.gph_log2) << (m.bs_log2 + m.gph_log2)) +
+                            (g & ((1 << m.gph_log2) - 1));
+    const uint32_t block_scales = static_cast<uint32_t>(a.n_kv) << (m.bs_log2 + m.gph_log2);
+    const int32_t off_mask = (1 << m.bs_log2) - 1;
+    const uint32_t scales_32 = 32u << m.bs_log2;  // 32 groups further
 
-    auto slot_of = [&](int64_t i) { return i < a.num_tokens ? __ldg(a.slot_mapping + i) : int64_t{-1}; };
-    int64_t slot = slot_of(t), slot_next = slot_of(t + step);
-    // the group's codes and scale; a row without a slot reads as zeros
-    auto fetch = [&](int64_t i, int64_t sl, uint2 &c, uint32_t &b) {
-        c = make_uint2(0u, 0u);
-        b = 0u;
-        if (sl >= 0 && sl < a.num_slots) {
-            c = __ldg(reinterpret_cast<const uint2 *>(a.codes + sl * row_codes + g * 8));
-            b = __ldg(a.scales + scale_index(m, a.n_kv, static_cast<int32_t>(sl), g));
-        } else if (sl != -1 && g == 0 && i < a.num_tokens) {
-            flag(a.status, KVFP8_DEV_BAD_SLOT);
+    // the slot of row t; -1 (and, flagged, anything out of range): the row reads as zeros
+    auto slot_at = [&](int64_t i) -> int32_t {
+        if (i >= a.num_tokens) return -1;
+        const int64_t sl = __ldg(a.slot_mapping + i);
+        if (sl >= 0 && sl < a.num_slots) return static_cast<int32_t>(sl);
+        if (sl != -1 && g == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
+        return -1;
+    };
+    auto fetch = [&](int32_t slot, uint2 (&c)[kG], uint32_t (&b)[kG]) {
+        const uint8_t *cp = codes + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * row_codes;
+        const uint8_t *sp = scales + static_cast<uint64_t>(static_cast<uint32_t>(slot >> m.bs_log2)) * block_scales +
+                            ((slot & off_mask) << m.gph_log2);
+#pragma unroll
+        for (int k = 0; k < kG; ++k) {
+            c[k] = make_uint2(0u, 0u);
+            b[k] = 0u;
+            if (slot >= 0 && g + 32 * k < m.gpr) {
+                c[k] = __ldg(reinterpret_cast<const uint2 *>(cp + k * 256));
+                b[k] = __ldg(sp + k * scales_32);
+            }
         }
     };
-    uint2 c, c_next;
-    uint32_t b, b_next;
-    fetch(t, slot, c, b);
-    for (; t < a.num_tokens; t += step) {
-        const int64_t slot_after = slot_of(t + 2 * step);
-        fetch(t + step, slot_next, c_next, b_next);
-        const float d = __fmul_rn(e4m3_value(b), s);
-        uint32_t h[8], o[16];
-        f16x2_from_e2m1x8(c.x, *reinterpret_cast<uint32_t(*)[4]>(h));
-        f16x2_from_e2m1x8(c.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+    int32_t slot_next = slot_at(t + step);
+    uint2 c[kG], c_next[kG];
+    uint32_t b[kG], b_next[kG];
+    fetch(slot_at(t), c, b);
+    for (; t < a.num_tokens; t += step, dst += step * row_bytes) {
+        fetch(slot_next, c_next, b_next);
+        slot_next = slot_at(t + 2 * step);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            const float lo = __fmul_rn(v.x, d), hi = __fmul_rn(v.y, d);
-            if (kBF16Out) {
-                o[i] = bf16x2_from_f32(lo, hi);
-            } else {
-                o[2 * i] = __float_as_uint(lo);
-                o[2 * i + 1] = __float_as_uint(hi);
-            }
-        }
-        uint8_t *p = dst + t * row_bytes;
+        for (int k = 0; k < kG; ++k) {
+            const float d = __fmul_rn(e4m3_value(b[k]), s);
+            uint32_t h[8], o[16];
+            f16x2_from_e2m1x8(c[k].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+            f16x2_from_e2m1x8(c[k].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
 #pragma unroll
-        for (int i = 0; i < kBytes / 4; i += 8) {
-            if (wide) {
-                st_v8(p + 4 * i, o + i);
-            } else {
-                *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                *reinterpret_cast<uint4 *>(p + 4 * i + 16) = make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                const float lo = __fmul_rn(v.x, d), hi = __fmul_rn(v.y, d);
+                if (kBF16Out) {
+                    o[i] = bf16x2_from_f32(lo, hi);
+                } else {
+                    o[2 * i] = __float_as_uint(lo);
+                    o[2 * i + 1] = __float_as_uint(hi);
+                }
             }
+            if (g + 32 * k < m.gpr) {
+                uint8_t *p = dst + k * 32 * kBytes;
+#pragma unroll
+                for (int i = 0; i < kBytes / 4; i += 8) {
+                    if (wide) {
+                        st_v8(p + 4 * i, o + i);
+                    } else {
+                        *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        *reinterpret_cast<uint4 *>(p + 4 * i + 16) =
+                            make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+                    }
+                }
+            }
+            c[k] = c_next[k];
+            b[k] = b_next[k];
         }
-        c = c_next;
-        b = b_next;
-        slot_next = slot_after;
     }
 }
 
@@ -420,9 +433,10 @@ cudaError_t launch_dequant_fp4(const Fp4ReadArgs &a, cudaStream_t stream) {
     cudaError_t err = device_facts(&f);
     if (err != cudaSuccess) return err;
     const RowMap m = row_map(a.n_kv, a.head_dim, a.block_size);
-    const int passes = (m.gpr + 31) / 32;
-    const bool bf16 = a.dst_dtype == KVFP8_BF16;
-    auto kern = bf16 ? read_fp4_kernel<true> : read_fp4_kernel<false>;
+    const bool bf16 = a.dst_dtype == KVFP8_BF16, two = m.gpr > 32;
+    const int passes = (m.gpr + (two ? 63 : 31)) / (two ? 64 : 32);
+    auto kern = bf16 ? (two ? read_fp4_kernel<true, 2> : read_fp4_kernel<true, 1>)
+                     : (two ? read_fp4_kernel<false, 2> : read_fp4_kernel<false, 1>);
     int occ = 0;
     if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
     const dim3 grid(rows_grid(a.num_tokens, m, f.sms, std::max(occ, 1), passes), passes);
