@@ -44,7 +44,11 @@ namespace kvfp8 {
 namespace {
 
 constexpr int kTok = 32;  // tokens of a chunk: two 16-token tiles
-constexpr float kLag = 8.f;  // log2: how far scores may rise above the reference maximum
+constexpr float kLag = 8.f;  // log2: how far scores may rise above the highest one when the reference was set
+// log2: the reference lies this far below that score, so that the weights fill fp16's range from its
+// top (2^(kLag + kHead) = 2^15): a weight keeps its 11 bits down to 2^-21 of the highest and is above zero
+// down to 2^-32, which counts where a long tail of small weights stands against a few large ones.
+constexpr float kHead = 7.f;
 
 struct Fp4KernelArgs {
     KernelArgs k;
@@ -400,7 +404,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         auto at = [&](int v, int c, int r) -> float & {
             return kPair ? o[v][c][r] : o[(v & ~1) + (r >> 1)][c][(v & 1) + 2 * (r & 1)];
         };
-        // per column: the reference maximum (log2 domain) the weights are taken against, and this
+        // per column: the reference (log2 domain) the weights are taken against, and this
         // lane's part of the sum of weights
         float m[NV], l[NV];
         uint32_t qb[KP][NS][4];
@@ -541,9 +545,9 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 }
 
                 // ---- weights 2^(score - m) per column (log2 domain).  m only has to be near the running
-                // maximum: it moves when a score passes it by more than kLag, so most chunks take no
-                // maximum over the lanes and rescale nothing, and weights stay <= 2^kLag.  Tokens a
-                // column does not see get -inf.
+                // maximum less kHead: it moves when a score passes it by more than kLag + kHead, so most
+                // chunks take no maximum over the lanes and rescale nothing, and weights stay <= 2^(kLag +
+                // kHead).  Tokens a column does not see get -inf.
                 if constexpr (kPartial) {
 #pragma unroll
                     for (int v = 0; v < NV; ++v)
@@ -563,13 +567,13 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
                 for (int v = 0; v < NV; ++v)
                     // (m starts at -inf, which any score passes; a column of -inf passes nothing)
                     top = fmaxf(top, column_top(v) - m[v]);
-                if (__any_sync(0xFFFFFFFFu, top > kLag)) {
+                if (__any_sync(0xFFFFFFFFu, top > kLag + kHead)) {
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         float x = column_top(v);
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16)) - kHead;
                         if (x > m[v]) {
                             // nothing but zeros (or a NaN, which stays) before the first score
                             const float alpha = m[v] == -INFINITY ? 1.f : ex2(m[v] - x);

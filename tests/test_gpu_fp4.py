@@ -333,6 +333,27 @@ def test_many_short_sequences(n, longest):
     check_attention(out, case, lengths)
 
 
+@pytest.mark.parametrize("length", [200, 5000])  # taken whole, and split
+@pytest.mark.parametrize("hd, n_q, n", [(64, 4, 1), (128, 8, 1), (128, 16, 1), (256, 8, 1), (64, 8, 2), (128, 4, 2)])
+def test_a_tail_of_small_weights_beside_one_large(hd, n_q, n, length):
+    """Weights 2^-25.5 of the highest, whose value is zero: the output is the tail's share alone.
+
+    The weights are off by 2^-25 in fp16 at 2^7 times their ratio, so by 2^-6.5 of themselves, and the
+    output's rounding by 2^-8 more: within 2^-6, the float32 errors of scores near 77 included."""
+    bs = 16
+    nb = -(-length // bs)
+    codes = np.full((nb, bs, 1, hd // 2), 0x22, np.uint8)       # 1.0
+    kc, vc = codes.copy(), codes.copy()
+    kc[0, 0], vc[0, 0] = 0x33, 0                                # 1.5 and 0 at token 0
+    one = np.full((nb, 1, bs, hd // 16), 0x38, np.uint8)
+    q = torch.ones(n, n_q, hd, dtype=torch.bfloat16)
+    case = (q, np.array([0, n], np.int32), kc, vc, one, one.copy(), np.arange(nb, dtype=np.int32)[None])
+    sm = 25.5 * math.log(2) / (hd / 2)
+    got = multi(case, [length], n, 1.0, 1.0, sm_scale=sm) if n > 1 else decode(case, [length], 1.0, 1.0, sm_scale=sm)
+    ref, _ = fp4.attention(q.double().numpy(), case[1], kc, vc, one, one, case[6], [length], 1.0, 1.0, sm)
+    assert np.abs(got.double().cpu().numpy() / ref - 1).max() < 2.0 ** -6
+
+
 def test_multi_of_one_query_each_is_decode():
     lengths = [333, 17, 1200]
     case = build(32, 8, 128, 16, lengths, [1, 1, 1], 4)
