@@ -393,7 +393,7 @@ bool make_segments(const CacheList &c, int64_t pairs, int sms, SegMap *m) {
     m->caches = c;
     int64_t bytes = 0;
     for (int i = 0; i < c.count; ++i) bytes += c.block_bytes[i];
-    m->seg_bytes = pairs * (bytes / 4096) >= static_cast<int64_t>(sms) * 64 ? 4096 : 1024;
+    m->seg_bytes = pairs >= static_cast<int64_t>(sms) * 64 / std::max<int64_t>(1, bytes / 4096) ? 4096 : 1024;
     int64_t at = 0;
     for (int i = 0; i < c.count; ++i) {
         m->seg0[i] = static_cast<int32_t>(at);

@@ -2,6 +2,7 @@
 // Declarations, argument meanings and error behaviour: include/kvfp8.h.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -668,9 +669,9 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
     const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
     if (sh != KVFP8_OK) return sh;
     const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
-    if (!split_kv && (n_q / n_kv > 128 ||
-                      (static_cast<int64_t>(max_query_len) * (n_q / n_kv) + 127) / 128 * n_kv *
-                              num_seqs > 0x7FFFFFFFLL))
+    if (!split_kv && (n_q / n_kv > 128 ||  // the tensor-core kernel's row tiles are its grid
+                      (static_cast<int64_t>(max_query_len) * (n_q / n_kv) + 127) / 128 >
+                          0x7FFFFFFFLL / n_kv / std::max(1, num_seqs)))
         return KVFP8_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
     if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;

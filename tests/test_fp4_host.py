@@ -107,6 +107,8 @@ def test_decode_refusals(over, code):
     (dict(qmax=64, workspace=None, workspace_bytes=0, value_scales=None), binding.ERR_NULL),
     (dict(qsl=ctypes.c_void_p(18)), binding.ERR_ALIGN), (dict(workspace_bytes=64), binding.ERR_WORKSPACE),
     (dict(n_q=129 * 8), binding.ERR_UNSUPPORTED), (dict(num_seqs=1 << 20, n_q=128 * 8, qmax=1 << 12), binding.ERR_UNSUPPORTED),
+    # 2^64 row tiles
+    (dict(num_seqs=1 << 20, n_q=1 << 20, n_kv=1 << 20, num_blocks=1, qmax=(1 << 31) - 1), binding.ERR_UNSUPPORTED),
     (dict(sm_scale=float("inf")), binding.ERR_SCALE), (dict(num_seqs=0, query=None), binding.OK)])
 def test_multi_refusals(over, code):
     assert _multi(**over) == code
