@@ -1,4 +1,5 @@
-"""Build libkvfp8.so in-tree for sm_103a (nvcc, one -gencode, units compiled in parallel)."""
+"""Build libkvfp8.so in-tree for sm_103a (nvcc, one -gencode, units compiled in parallel), and beside it
+the module of calls on torch tensors (host code, against the installed torch)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,6 +7,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -13,6 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libkvfp8.so")
+# host code on torch tensors over the library's C calls
+TORCH_SRC = "torch_calls.cpp"
 # test-only variant for the bounded-wait timeout test (never loaded by the package)
 WITHHOLD_LIB = os.path.join(LIB_DIR, "libkvfp8_withhold.so")
 WITHHOLD_DEFINE = "-DKVFP8_TEST_WITHHOLD_FIRST_CHUNK=1"
@@ -38,11 +42,19 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the kvfp8 CUDA library cannot be built")
 
 
-def _stale(lib: str) -> bool:
+def torch_module() -> str:
+    """The path of the module on torch tensors; it is bound to one torch and one Python, so their
+    versions are in the name."""
+    import torch
+
+    return os.path.join(LIB_DIR, f"kvfp8_torch-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _stale(lib: str, files=None) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    inputs = [os.path.join(CSRC, f) for f in SOURCES + DEPS] + [HEADER, __file__]
+    inputs = [os.path.join(CSRC, f) for f in files or SOURCES + DEPS] + [HEADER, __file__]
     return any(os.path.getmtime(p) > t for p in inputs)
 
 
@@ -67,17 +79,57 @@ def _link(nvcc: str, objs, lib: str) -> str:
     return lib
 
 
+def _compile_torch_calls(obj: str) -> str:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = ["g++", "-c", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", "-DTORCH_EXTENSION_NAME=kvfp8_torch"]
+    for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_path("include"), cuda):
+        cmd += ["-isystem", d]
+    r = subprocess.run([*cmd, os.path.join(CSRC, TORCH_SRC), "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_torch_calls(obj: str, module: str) -> str:
+    import torch
+
+    tmp = module + f".tmp{os.getpid()}"
+    # libkvfp8.so beside it; torch's own libraries are in the process before it is loaded
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{LIB_DIR}", "-lkvfp8", "-Wl,-rpath,$ORIGIN",
+           f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, module)
+    return module
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link the library if it is missing or older than its sources."""
-    if not force and not _stale(LIB):
+    """Compile and link the library, and the module on torch tensors, where missing or older than
+    their sources."""
+    module = torch_module()
+    lib_stale, module_stale = force or _stale(LIB), force or _stale(module, [TORCH_SRC])
+    if not lib_stale and not module_stale:
         return LIB
-    nvcc = _nvcc()
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda src: _compile(nvcc, src, os.path.join(OBJ_DIR, src.replace(".cu", ".o")),
-                                                verbose=verbose), SOURCES))
-    return _link(nvcc, objs, LIB)
+    torch_obj = os.path.join(OBJ_DIR, "torch_calls.o")
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_torch_calls, torch_obj) if module_stale else None
+        if lib_stale:
+            nvcc = _nvcc()
+            objs = list(ex.map(lambda src: _compile(nvcc, src, os.path.join(OBJ_DIR, src.replace(".cu", ".o")),
+                                                    verbose=verbose), SOURCES))
+            _link(nvcc, objs, LIB)
+        if calls is not None:
+            _link_torch_calls(calls.result(), module)
+    return LIB
 
 
 def build_withhold_variant(verbose: bool = False) -> str:

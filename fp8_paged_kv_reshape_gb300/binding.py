@@ -1,12 +1,16 @@
 """Thin Python binding over the kvfp8 C ABI (include/kvfp8.h).
 
 Argument marshalling only: every step of the path runs in libkvfp8.so's CUDA kernels.
-PyTorch supplies device memory and the current stream.  There is no CPU or eager
-fallback: if the library is missing, importing this module raises.
+PyTorch supplies device memory and the current stream.  The calls of the 4-bit cache and of
+pages are marshalled by compiled code (csrc/torch_calls.cpp), the others here.  There is no CPU
+or eager fallback: if the library or that module is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -514,68 +518,27 @@ def dequant(src: torch.Tensor, dst_dtype: torch.dtype = torch.float32,
 
 # ---------------------------------------------------------------- 4-bit cache, pages
 
-# The wrappers below run once per layer and step, where a kernel may take a few microseconds: they
-# read each tensor attribute once, pass addresses as plain integers and ask torch for the raw stream.
-
-def _addr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
-
-
-def _check_device(*tensors: torch.Tensor | None) -> int:
-    """The index of the current CUDA device, which every given tensor has to be on."""
-    here = tensors[0].get_device()  # -1 on the CPU
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors on different devices: {t.device} and {tensors[0].device}")
-    if here < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    if here != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{here}, the current device is cuda:{torch.cuda.current_device()}")
-    return here
+def _load_calls():
+    """The compiled wrappers; they call the same loaded libkvfp8.so."""
+    path = _build.torch_module()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+    loader = importlib.machinery.ExtensionFileLoader("kvfp8_torch", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("kvfp8_torch", path, loader=loader))
+    loader.exec_module(module)
+    module.on_status(_check)
+    return module
 
 
-def _raw_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+_CALLS = _load_calls()
+_HERE = contextlib.nullcontext()
 
 
-def _check_status(status: torch.Tensor | None):
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise ValueError("status must be an int32 [1] tensor")
-
-
-def _empty(shape, dtype, device: int, stream):
-    """A tensor for a call on `stream`, from that stream's memory pool."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=_DEVICES[device])
-
-
-class _Devices(dict):
-    def __missing__(self, index):
-        self[index] = torch.device("cuda", index)
-        return self[index]
-
-
-_DEVICES = _Devices()
-
-
-def _check_fp4_side(cache: torch.Tensor, scales: torch.Tensor):
-    """One side of a 4-bit cache; returns (num_blocks, block_size, n_kv, head_dim)."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
-        raise ValueError("4-bit codes must be contiguous uint8 [num_blocks, block_size, n_kv, head_dim/2]")
-    nb, bs, n_kv, half = cache.shape
-    if half % 8 != 0 or scales.dtype != torch.uint8 or \
-            scales.shape != (nb, n_kv, bs, half // 8) or not scales.is_contiguous():
-        raise ValueError("their scales must be contiguous uint8 [num_blocks, n_kv, block_size, head_dim/16]")
-    return nb, bs, n_kv, 2 * half
-
-
-def _check_fp4_caches(key_cache, value_cache, key_scales, value_scales):
-    shape = _check_fp4_side(key_cache, key_scales)
-    if _check_fp4_side(value_cache, value_scales) != shape:
-        raise ValueError("key and value caches must have one shape")
-    return shape
+def _on(stream):
+    """A call on `stream` is a call with that stream current: its outputs and workspace are that
+    stream's memory."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
@@ -587,33 +550,12 @@ def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, key_cache: tor
 
     key/value as for reshape_and_cache.  Codes: uint8 [num_blocks, block_size, n_kv,
     head_dim/2]; scales: uint8 [num_blocks, n_kv, block_size, head_dim/16], all contiguous.
-    slot_mapping: int64 [num_tokens] (-1 = padding), no slot twice.
+    slot_mapping: int64 [num_tokens] (-1 = padding), no slot twice.  Every tensor of this call
+    and of those below is on the current device.
     """
-    if key.dtype != value.dtype or key.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("key and value must share one dtype, bfloat16 or float32")
-    if key.dim() != 3 or value.shape != key.shape:
-        raise ValueError("key/value must be [num_tokens, n_kv, head_dim] with equal shapes")
-    n, n_kv, hd = key.shape
-    for t in (key, value):
-        if n > 0 and (t.stride(2) != 1 or (n_kv > 1 and t.stride(1) != hd)):
-            raise ValueError("key/value inner dims [n_kv, head_dim] must be dense")
-    nb, bs, c_kv, c_hd = _check_fp4_caches(key_cache, value_cache, key_scales, value_scales)
-    if (c_kv, c_hd) != (n_kv, hd):
-        raise ValueError("the caches' n_kv and head_dim must be those of key and value")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != n or \
-            not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
-    sdt = _scale_args(k_scale, v_scale)
-    _check_status(status)
-    dev = _check_device(key, value, key_cache, value_cache, key_scales, value_scales, slot_mapping,
-                        k_scale, v_scale, status)
-    # (the stride of a single row is never used, and may be anything)
-    ks, vs = (key.stride(0), value.stride(0)) if n > 1 else (n_kv * hd, n_kv * hd)
-    rc = LIB.kvfp8_reshape_and_cache_fp4(
-        _addr(key), _addr(value), F32 if key.dtype == torch.float32 else BF16, ks, vs, n,
-        _addr(key_cache), _addr(value_cache), _addr(key_scales), _addr(value_scales), nb, bs, n_kv, hd,
-        _addr(slot_mapping), _addr(k_scale), _addr(v_scale), sdt, _addr(status), _raw_stream(stream, dev))
-    _check(rc, "kvfp8_reshape_and_cache_fp4")
+    with _on(stream):
+        _CALLS.reshape_and_cache_fp4(key, value, key_cache, value_cache, key_scales, value_scales, slot_mapping,
+                                     k_scale, v_scale, status)
 
 
 def dequant_fp4(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.Tensor,
@@ -622,25 +564,10 @@ def dequant_fp4(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.T
                 stream=None) -> torch.Tensor:
     """kvfp8_dequant_fp4: the rows of one side of a 4-bit cache at slot_mapping's slots, as
     bfloat16 or float32 [num_tokens, n_kv, head_dim] (slot -1: a zero row)."""
-    nb, bs, n_kv, hd = _check_fp4_side(cache, scales)
-    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
     if dst_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("dst_dtype must be float32 or bfloat16")
-    n = slot_mapping.numel()
-    if out is not None and (out.dtype != dst_dtype or out.shape != (n, n_kv, hd) or
-                            not out.is_contiguous()):
-        raise ValueError("out must be a contiguous dst_dtype [num_tokens, n_kv, head_dim] tensor")
-    sdt = _scale_args(scale, None)
-    _check_status(status)
-    dev = _check_device(cache, scales, slot_mapping, scale, out, status)
-    if out is None:
-        out = _empty((n, n_kv, hd), dst_dtype, dev, stream)
-    rc = LIB.kvfp8_dequant_fp4(_addr(out), BF16 if dst_dtype == torch.bfloat16 else F32, _addr(cache),
-                               _addr(scales), nb, bs, n_kv, hd, _addr(slot_mapping), n, _addr(scale),
-                               sdt, _addr(status), _raw_stream(stream, dev))
-    _check(rc, "kvfp8_dequant_fp4")
-    return out
+    with _on(stream):
+        return _CALLS.dequant_fp4(cache, scales, slot_mapping, dst_dtype == torch.bfloat16, scale, out, status)
 
 
 def paged_attention_fp4_workspace_size(num_seqs: int, n_q: int, n_kv: int, head_dim: int,
@@ -649,30 +576,6 @@ def paged_attention_fp4_workspace_size(num_seqs: int, n_q: int, n_kv: int, head_
     """Workspace bytes of paged_decode_attention_fp4 (max_query_len 1) and paged_attention_multi_fp4."""
     return LIB.kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
                                                         max_blocks_per_seq, block_size)
-
-
-def _check_attention_fp4(query, key_cache, value_cache, key_scales, value_scales, block_tables,
-                         seq_lens, k_scale, v_scale, out, workspace, status, num_seqs,
-                         query_start_loc=None):
-    """The checks both 4-bit attention calls make; returns (rows, n_q, head_dim, num_blocks,
-    block_size, n_kv, scale dtype, device)."""
-    if query.dtype != torch.bfloat16 or query.dim() != 3 or not query.is_contiguous():
-        raise ValueError("query must be a contiguous bf16 [rows, n_q, head_dim] tensor")
-    rows, n_q, hd = query.shape
-    nb, bs, n_kv, c_hd = _check_fp4_caches(key_cache, value_cache, key_scales, value_scales)
-    if c_hd != hd:
-        raise ValueError("the caches' head_dim must be the query's")
-    _check_tables(block_tables, seq_lens, num_seqs)
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != query.shape or
-                            not out.is_contiguous()):
-        raise ValueError("out must be a contiguous bf16 tensor shaped like query")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    sdt = _scale_args(k_scale, v_scale)
-    _check_status(status)
-    dev = _check_device(query, key_cache, value_cache, key_scales, value_scales, block_tables,
-                        seq_lens, k_scale, v_scale, out, workspace, status, query_start_loc)
-    return rows, n_q, hd, nb, bs, n_kv, sdt, dev
 
 
 def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
@@ -685,25 +588,10 @@ def paged_decode_attention_fp4(query: torch.Tensor, key_cache: torch.Tensor,
                                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kvfp8_paged_decode_attention_fp4: paged_decode_attention over a 4-bit cache (codes and
     scales as reshape_and_cache_fp4 writes them); returns out (bf16 [num_seqs, n_q, hd])."""
-    num_seqs = query.shape[0] if query.dim() == 3 else 0
-    num_seqs, n_q, hd, nb, bs, n_kv, sdt, dev = _check_attention_fp4(
-        query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
-        v_scale, out, workspace, status, num_seqs)
-    if out is None:
-        out = _empty(query.shape, torch.bfloat16, dev, stream)
-    if workspace is None:
-        need = LIB.kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, hd, 1,
-                                                            block_tables.shape[1], bs)
-        if need > 0:
-            workspace = _empty(need, torch.uint8, dev, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = LIB.kvfp8_paged_decode_attention_fp4(
-        _addr(out), _addr(query), _addr(key_cache), _addr(value_cache), _addr(key_scales),
-        _addr(value_scales), _addr(block_tables), block_tables.shape[1], _addr(seq_lens), num_seqs,
-        n_q, n_kv, hd, bs, nb, float(sm_scale), _addr(k_scale), _addr(v_scale), sdt,
-        _addr(workspace), ws_bytes, _addr(status), _raw_stream(stream, dev))
-    _check(rc, "kvfp8_paged_decode_attention_fp4")
-    return out
+    with _on(stream):
+        return _CALLS.paged_decode_attention_fp4(query, key_cache, value_cache, key_scales, value_scales,
+                                                 block_tables, seq_lens, k_scale, v_scale, sm_scale, out, workspace,
+                                                 status)
 
 
 def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor,
@@ -717,52 +605,10 @@ def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor
                               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kvfp8_paged_attention_multi_fp4: paged_attention_multi (causal, any chunk length) over a
     4-bit cache."""
-    num_seqs = seq_lens.numel()
-    if query_start_loc.dtype != torch.int32 or query_start_loc.numel() != num_seqs + 1 or \
-            not query_start_loc.is_contiguous():
-        raise ValueError("query_start_loc must be a contiguous int32 [num_seqs + 1] tensor")
-    rows, n_q, hd, nb, bs, n_kv, sdt, dev = _check_attention_fp4(
-        query, key_cache, value_cache, key_scales, value_scales, block_tables, seq_lens, k_scale,
-        v_scale, out, workspace, status, num_seqs, query_start_loc)
-    need = paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, hd, max_query_len,
-                                              block_tables.shape[1], bs)
-    if out is None:
-        out = _empty(query.shape, torch.bfloat16, dev, stream)
-    if workspace is None and need > 0:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = LIB.kvfp8_paged_attention_multi_fp4(
-        _addr(out), _addr(query), _addr(query_start_loc), rows, max_query_len, _addr(key_cache),
-        _addr(value_cache), _addr(key_scales), _addr(value_scales), _addr(block_tables),
-        block_tables.shape[1], _addr(seq_lens), num_seqs, n_q, n_kv, hd, bs, nb, float(sm_scale),
-        _addr(k_scale), _addr(v_scale), sdt, _addr(workspace), ws_bytes, _addr(status),
-        _raw_stream(stream, dev))
-    _check(rc, "kvfp8_paged_attention_multi_fp4")
-    return out
-
-
-def _cache_list(caches):
-    """The page calls' caches: (pointers and bytes per block as C arrays, count, num_blocks, caches)."""
-    caches = list(caches)
-    count = len(caches)
-    if not 1 <= count <= MAX_CACHES:
-        raise ValueError(f"1 to {MAX_CACHES} caches")
-    nb = caches[0].shape[0] if caches[0].dim() > 1 else 0
-    ptrs, sizes = (ctypes.c_void_p * count)(), (ctypes.c_int64 * count)()
-    spans = []
-    for i, c in enumerate(caches):
-        total = c.numel() * c.element_size()
-        if c.dim() < 2 or c.shape[0] != nb or total == 0 or not c.is_contiguous():
-            raise ValueError("caches must be contiguous tensors [num_blocks, ...] of one num_blocks")
-        at = c.data_ptr()
-        ptrs[i] = at
-        sizes[i] = total // nb
-        spans.append((at, at + total))
-    spans.sort()
-    for (_, end), (start, _) in zip(spans, spans[1:]):
-        if end > start:
-            raise ValueError("caches must not overlap")
-    return ptrs, sizes, count, nb, caches
+    with _on(stream):
+        return _CALLS.paged_attention_multi_fp4(query, query_start_loc, max_query_len, key_cache, value_cache,
+                                                key_scales, value_scales, block_tables, seq_lens, k_scale, v_scale,
+                                                sm_scale, out, workspace, status)
 
 
 def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
@@ -774,17 +620,8 @@ def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
     with another one (a destination named twice, a source that is a destination) is skipped and
     sets DEV_BAD_BLOCK in status.
     """
-    ptrs, sizes, count, nb, caches = _cache_list(caches)
-    for t in (src_blocks, dst_blocks):
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
-            raise ValueError("src_blocks and dst_blocks must be contiguous int32 [num_pairs] tensors")
-    if src_blocks.numel() != dst_blocks.numel():
-        raise ValueError("src_blocks and dst_blocks must have one length")
-    _check_status(status)
-    dev = _check_device(*caches, src_blocks, dst_blocks, status)
-    rc = LIB.kvfp8_copy_blocks(ptrs, sizes, count, nb, _addr(src_blocks), _addr(dst_blocks),
-                               src_blocks.numel(), _addr(status), _raw_stream(stream, dev))
-    _check(rc, "kvfp8_copy_blocks")
+    with _on(stream):
+        _CALLS.copy_blocks(list(caches), src_blocks, dst_blocks, status)
 
 
 def compact_blocks_workspace_size(num_blocks: int) -> int:
@@ -801,27 +638,6 @@ def compact_blocks(caches, block_tables: torch.Tensor, seq_lens: torch.Tensor, b
 
     new_block_tables may be block_tables itself.
     """
-    ptrs, sizes, count, nb, caches = _cache_list(caches)
-    _check_tables(block_tables, seq_lens, seq_lens.numel())
-    if new_block_tables is not None and (new_block_tables.dtype != torch.int32 or
-                                         new_block_tables.shape != block_tables.shape or
-                                         not new_block_tables.is_contiguous()):
-        raise ValueError("new_block_tables must be a contiguous int32 tensor shaped like block_tables")
-    if num_used is not None and (num_used.dtype != torch.int32 or num_used.numel() != 1):
-        raise ValueError("num_used must be an int32 [1] tensor")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _check_status(status)
-    dev = _check_device(*caches, block_tables, seq_lens, new_block_tables, num_used, workspace, status)
-    if new_block_tables is None:
-        new_block_tables = _empty(block_tables.shape, torch.int32, dev, stream)
-    if num_used is None:
-        num_used = _empty(1, torch.int32, dev, stream)
-    if workspace is None:
-        workspace = _empty(compact_blocks_workspace_size(nb), torch.uint8, dev, stream)
-    rc = LIB.kvfp8_compact_blocks(
-        ptrs, sizes, count, nb, block_size, _addr(block_tables), block_tables.shape[1],
-        _addr(seq_lens), seq_lens.numel(), _addr(new_block_tables), _addr(num_used), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _addr(status), _raw_stream(stream, dev))
-    _check(rc, "kvfp8_compact_blocks")
-    return new_block_tables, num_used
+    with _on(stream):
+        return _CALLS.compact_blocks(list(caches), block_tables, seq_lens, block_size, new_block_tables, num_used,
+                                     workspace, status)
