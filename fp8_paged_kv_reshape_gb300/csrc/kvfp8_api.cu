@@ -598,9 +598,13 @@ kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const uint8_t *
 size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
                                                 int32_t head_dim, int32_t max_query_len,
                                                 int32_t max_blocks_per_seq, int32_t block_size) {
-    if (max_blocks_per_seq < 1 || block_size < 1 ||
-        kvfp8::fp4_takes_sequences_whole(max_blocks_per_seq, block_size))
+    if (num_seqs < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || max_query_len < 1 || max_blocks_per_seq < 1 ||
+        block_size < 1)
         return 0;
+    if (!kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len))
+        return kvfp8::fp4_prefill_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
+                                                 static_cast<int64_t>(max_blocks_per_seq) * block_size);
+    if (kvfp8::fp4_takes_sequences_whole(max_blocks_per_seq, block_size)) return 0;
     return kvfp8_paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len);
 }
 

@@ -182,8 +182,11 @@ cudaError_t launch_paged_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
 bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
 
 // Multi-query (causal) attention on the tensor cores (tcgen05): long query chunks, or kv-head
-// counts the split-KV decode kernel does not cover.  Needs no workspace.
+// counts the split-KV decode kernel does not cover.  Needs no workspace, but over a 4-bit cache
+// (key_scales set) the one below where few row tiles have their keys split.
 cudaError_t launch_prefill_attention(const DecodeArgs &a, cudaStream_t stream);
+size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+                                  int64_t max_len);
 // True when kvfp8_paged_attention_multi takes the split-KV decode kernel for this shape
 // (and so needs a workspace); false when it takes the prefill kernel.
 bool multi_uses_decode_kernel(int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t max_query_len);

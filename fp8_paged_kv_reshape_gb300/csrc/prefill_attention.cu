@@ -230,6 +230,10 @@ struct PrefillArgs {
     int32_t box_rows;
     int32_t row_tiles;  // tiles of 128 score rows per (sequence, kv head)
     const uint8_t *key_scales, *value_scales;  // 4-bit cache: the groups' scale bytes
+    // 4-bit cache: parts a (sequence, kv head, row tile)'s keys are cut into at most (gridDim.y), and the
+    // parts' results, [CTA of the unsplit grid, in sequence order][part][row of the tile]
+    int32_t splits;
+    float *part_o, *part_lse;
 };
 
 // ---------------------------------------------------------------- the 4-bit cache
@@ -400,9 +404,30 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
     }
     return groups;
 }
+// Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
+// their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
+// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part
+// is kMinPartKeys keys at least; a row tile of one part writes its output itself.
+constexpr int kSplitSms = 152;
+constexpr int kMinPartKeys = 256;
+__host__ __device__ constexpr int split_parts(int splits, int key_tiles, int tile_keys) {
+    const int most = key_tiles / (kMinPartKeys / tile_keys);
+    return splits < most ? splits : most > 1 ? most : 1;
+}
 // bf16 pair of dims d, d+1, NaN where the pair's group is in `groups`
 __device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t groups, int d) {
     return (groups >> (d >> 4)) & 1u ? 0x7FFF7FFFu : w;
+}
+// 32 dims from d0 on of a part's row, from O's columns, as float; NaN in `groups`
+__device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], float inv, uint32_t groups, int d0) {
+#pragma unroll
+    for (int w = 0; w < 16; w += 2) {  // dims 2w..2w+3
+        const int e = 2 * o_word<true>(w), f = 2 * o_word<true>(w + 1);
+        float4 v = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                               __uint_as_float(o[f]) * inv, __uint_as_float(o[f + 1]) * inv);
+        if ((groups >> ((d0 + 2 * w) >> 4)) & 1u) v.x = v.y = v.z = v.w = __uint_as_float(0x7FC00000u);
+        *reinterpret_cast<float4 *>(row + d0 + 2 * w) = v;
+    }
 }
 
 // ---------------------------------------------------------------- work order
@@ -609,12 +634,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     if (row0 >= nb * G) return;                      // no rows here
     const int j_last = min(nb, (row0 + kPfRows + G - 1) / G) - 1;
     const int kend = Ls - nb + j_last + 1;           // keys the tile's last row may see
-    const int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
+    int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
+    int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
+    if constexpr (F4) {
+        parts = split_parts(a.splits, ntiles, kPfKeys);
+        const int part = static_cast<int>(blockIdx.y);
+        if (part >= parts) return;
+        tile_lo = static_cast<int>(static_cast<int64_t>(part) * ntiles / parts);
+        ntiles = static_cast<int>(static_cast<int64_t>(part + 1) * ntiles / parts) - tile_lo;
+    }
     // The row tiles of one (sequence, kv head) run side by side on one K/V stream; each
     // starts its pass at its own key tile (the online softmax takes the keys in any order),
     // so they read different lines of the stream at any one time.
     const int rot = ntiles > 0 ? static_cast<int>((static_cast<int64_t>(tile) * ntiles) / a.row_tiles) % ntiles : 0;
-    auto key_tile = [&](int i) { const int k = i + rot; return k >= ntiles ? k - ntiles : k; };
+    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (F4 ? tile_lo : 0); };
 
     if (ntiles == 0) {  // every row of the tile sees no key: zero rows
         if (tid < kPfRows) {
@@ -1055,6 +1088,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
+            // this row in the parts' results, when there are several
+            const int64_t prow = F4 && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
+                                                     blockIdx.y) * kPfRows) + tid : 0;
+            const float part_inv = lsum == 0.f ? 0.f : 1.f / lsum;
+            if (F4 && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1062,7 +1100,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::kColO + c0, o);
                 tmem_wait_ld();
-                if (row_ok) {
+                if (F4 && parts > 1) {
+                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
+                } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         uint4 w;
@@ -1230,9 +1270,17 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     if (row0 >= nb * G) return;
     const int j_last = min(nb, (row0 + kP2Rows + G - 1) / G) - 1;
     const int kend = Ls - nb + j_last + 1;            // keys the CTA's last row may see
-    const int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
+    int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
+    int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
+    if constexpr (F4) {
+        parts = split_parts(a.splits, ntiles, kP2Keys);
+        const int part = static_cast<int>(blockIdx.y);
+        if (part >= parts) return;
+        tile_lo = static_cast<int>(static_cast<int64_t>(part) * ntiles / parts);
+        ntiles = static_cast<int>(static_cast<int64_t>(part + 1) * ntiles / parts) - tile_lo;
+    }
     const int rot = ntiles > 0 ? static_cast<int>((static_cast<int64_t>(ctile) * ntiles) / a.row_tiles) % ntiles : 0;
-    auto key_tile = [&](int i) { const int k = i + rot; return k >= ntiles ? k - ntiles : k; };
+    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (F4 ? tile_lo : 0); };
 
     if (ntiles == 0) {  // every row of the CTA sees no key: zero rows
         if (tid < kP2Rows) {
@@ -1705,6 +1753,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
+            // this row in the parts' results, when there are several
+            const int64_t prow = F4 && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
+                                                     blockIdx.y) * kP2Rows) + tid : 0;
+            const float part_inv = lsum == 0.f ? 0.f : 1.f / lsum;
+            if (F4 && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1712,7 +1765,9 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
-                if (row_ok) {
+                if (F4 && parts > 1) {
+                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
+                } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         uint4 w;
@@ -1744,6 +1799,86 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }
+}
+
+// Joins the parts of each row: CTA (x, y) takes 256 / (HD / 4) rows of row tile x (of tile_rows rows, keys in
+// tiles of tile_keys).
+template <int HD>
+__global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs a, int tile_rows, int tile_keys) {
+    constexpr int kLanes = HD / 4;  // threads of a row, four dims each
+    const int kvh = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.n_kv));
+    const int tile = static_cast<int>((blockIdx.x / static_cast<unsigned>(a.n_kv)) % static_cast<unsigned>(a.row_tiles));
+    const int seq = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.n_kv * a.row_tiles));
+    const int lr = static_cast<int>(blockIdx.y) * (256 / kLanes) + static_cast<int>(threadIdx.x) / kLanes;
+    const int d = static_cast<int>(threadIdx.x) % kLanes * 4;
+    pdl_wait();  // the parts are visible from here on
+    const float sk = load_scale(a.k_scale, a.scale_dtype), sv = load_scale(a.v_scale, a.scale_dtype);
+    if (!scale_ok(sk) || !scale_ok(sv)) return;
+    const QueryRange qr = a.qsl ? query_range(a.qsl, seq, a.qmax, a.qrows) : QueryRange{seq, 1};
+    const int Ls = min(max(a.seq_lens[seq], 0), a.max_len);
+    const int nb = qr.count, G = a.group, row0 = tile * tile_rows, r = row0 + lr;
+    if (r >= nb * G) return;
+    // the row tile's parts, as its CTAs worked them out
+    const int j_last = min(nb, (row0 + tile_rows + G - 1) / G) - 1;
+    const int kend = Ls - nb + j_last + 1;
+    const int parts = split_parts(a.splits, kend > 0 ? (kend + tile_keys - 1) / tile_keys : 0, tile_keys);
+    if (parts == 1) return;
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
+    PartMerge mg;
+    for (int c0 = 0; c0 < parts; c0 += 8) {
+        float l[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            l[i] = -INFINITY;
+            if (c0 + i < parts) {
+                const int64_t p = p0 + static_cast<int64_t>(c0 + i) * tile_rows;
+                l[i] = a.part_lse[p];
+                v[i] = *reinterpret_cast<const float4 *>(a.part_o + p * HD + d);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mg.add(l[i], v[i]);
+    }
+    *reinterpret_cast<uint2 *>(a.out + ((static_cast<int64_t>(qr.q0) + r / G) * a.n_q + kvh * G + r % G) * HD + d) =
+        mg.result(sv);
+}
+
+// How the 4-bit form is cut: the row tiles' size, and the parts per row tile that fill the SMs.
+struct SplitPlan {
+    int tile_rows = kPfRows, tile_keys = kPfKeys, splits = 1;
+    size_t part_rows = 0, lse_off = 0, total = 0;  // workspace
+};
+SplitPlan split_plan(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax, int64_t max_len) {
+    SplitPlan p;
+    const int64_t group_rows = static_cast<int64_t>(qmax) * (n_q / n_kv);
+    if (head_dim <= 128 && group_rows > kPfRows) {
+        p.tile_rows = kP2Rows;
+        p.tile_keys = kP2Keys;
+    }
+    const int64_t tiles = (group_rows + p.tile_rows - 1) / p.tile_rows;
+    if (tiles > kSplitSms || tiles * n_kv > kSplitSms || tiles * n_kv * num_seqs > kSplitSms / 2) return p;
+    const int64_t ctas = tiles * n_kv * num_seqs;
+    p.splits = static_cast<int>(std::max<int64_t>(1, std::min(kSplitSms / ctas, max_len / kMinPartKeys)));
+    if (p.splits == 1) return p;
+    p.part_rows = static_cast<size_t>(ctas) * p.splits * p.tile_rows;
+    p.lse_off = p.part_rows * head_dim * sizeof(float);
+    p.total = p.lse_off + p.part_rows * sizeof(float);
+    return p;
+}
+
+template <int HD>
+cudaError_t join_parts(const PrefillArgs &a, const SplitPlan &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_seqs * a.row_tiles * a.n_kv, p.tile_rows / (256 / (HD / 4)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD>, a, p.tile_rows, p.tile_keys);
 }
 
 template <int HD, bool F4>
@@ -1782,6 +1917,11 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     a.box_rows = box_rows;
     a.key_scales = d.key_scales;
     a.value_scales = d.value_scales;
+    SplitPlan sp;
+    if (F4) sp = split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
+    a.splits = sp.splits;
+    a.part_o = static_cast<float *>(d.workspace);
+    a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(d.workspace) + sp.lse_off);
     // more than one tile of 128 rows per kv head (a multi-query call): 256 rows per CTA
     if constexpr (HD <= 128) {
         if (d.qsl != nullptr && d.qmax * a.group > kPfRows) {
@@ -1792,8 +1932,9 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
                 return err;
             a.row_tiles = (d.qmax * a.group + kP2Rows - 1) / kP2Rows;
             const int64_t ctas = static_cast<int64_t>(d.num_seqs) * a.row_tiles * d.n_kv;
-            kern2<<<static_cast<unsigned>(ctas), kP2Warps * 32, smem2, stream>>>(tmk, tmv, a);
-            return cudaGetLastError();
+            kern2<<<dim3(static_cast<unsigned>(ctas), sp.splits), kP2Warps * 32, smem2, stream>>>(tmk, tmv, a);
+            if ((err = cudaGetLastError()) != cudaSuccess || sp.splits == 1) return err;
+            return join_parts<HD>(a, sp, stream);
         }
     }
     const size_t smem = L::kTotal + 1024;
@@ -1802,11 +1943,17 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
     a.row_tiles = (d.qmax * a.group + kPfRows - 1) / kPfRows;
     const int64_t ctas = static_cast<int64_t>(d.num_seqs) * a.row_tiles * d.n_kv;
-    kern<<<static_cast<unsigned>(ctas), kPfWarps * 32, smem, stream>>>(tmk, tmv, a);
-    return cudaGetLastError();
+    kern<<<dim3(static_cast<unsigned>(ctas), sp.splits), kPfWarps * 32, smem, stream>>>(tmk, tmv, a);
+    if ((err = cudaGetLastError()) != cudaSuccess || sp.splits == 1) return err;
+    return join_parts<HD>(a, sp, stream);
 }
 
 }  // namespace
+
+size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+                                  int64_t max_len) {
+    return split_plan(num_seqs, n_q, n_kv, head_dim, qmax, max_len).total;
+}
 
 cudaError_t launch_prefill_attention(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;

@@ -425,10 +425,10 @@ KVFP8_API kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const
                                          uint32_t *status, kvfp8_stream_t stream);
 
 /*
- * Workspace bytes of the two calls below (decode: max_query_len 1): the split-KV partials, at most
- * kvfp8_paged_attention_multi_workspace_size's; 0, where the workspace may be NULL, when the
- * tensor-core kernel serves the shape or the block tables hold at most 256 tokens per sequence
- * (sequences are then not split).  Pure host arithmetic.
+ * Workspace bytes of the two calls below (decode: max_query_len 1): the results of the parts that
+ * long sequences are split into.  0, where the workspace may be NULL, when nothing is split: block
+ * tables of at most 256 tokens per sequence, or enough long query chunks to fill the GPU.  Pure host
+ * arithmetic.
  */
 KVFP8_API size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
                                                           int32_t head_dim, int32_t max_query_len,

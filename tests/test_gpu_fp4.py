@@ -333,6 +333,53 @@ def test_many_short_sequences(n, longest):
     check_attention(out, case, lengths)
 
 
+SPLIT = [
+    # few rows on long contexts: the tensor-core kernels' keys are split
+    # n_q, n_kv, head_dim, block, lengths, new tokens, width of the tables beyond the longest
+    (14, 2, 64, 32, [3000], [37], 0),             # 259 rows: two tiles of 256
+    (14, 2, 64, 16, [4000, 700, 30], [9, 18, 2], 0),
+    (8, 2, 128, 16, [2500], [5], 0),
+    (24, 8, 128, 8, [3000, 100], [60, 60], 3000),  # wide tables
+    (4, 4, 128, 64, [1300], [300], 0),            # the first rows see 1001 keys
+    (16, 4, 256, 8, [2100], [8], 0),
+    (6, 2, 256, 32, [1000, 515, 0, 256], [40, 100, 0, 256], 500),
+]
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, bs, lengths, qlens, wide", SPLIT)
+def test_multi_with_split_keys(n_q, n_kv, hd, bs, lengths, qlens, wide):
+    case = list(build(n_q, n_kv, hd, bs, lengths, qlens, 41))
+    case[6] = np.concatenate([case[6], np.full((len(lengths), wide), -1, np.int32)], 1)
+    assert kv.paged_attention_fp4_workspace_size(len(lengths), n_q, n_kv, hd, max(qlens), case[6].shape[1], bs) > 0
+    check_attention(multi(tuple(case), lengths, max(qlens)), tuple(case), lengths, one_tile=True)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, lengths", [(20, 1, 128, [3000, 0, 129]), (64, 2, 64, [5000]), (36, 4, 256, [1500, 10])])
+def test_decode_of_wide_groups_with_split_keys(n_q, n_kv, hd, lengths):
+    case = build(n_q, n_kv, hd, 16, lengths, [1] * len(lengths), 42)
+    check_attention(decode(case, lengths), case, lengths, one_tile=True)
+
+
+def test_split_keys_nan_bad_blocks_and_a_workspace_of_the_callers():
+    lengths, n = [2000], 40
+    for side, hd, n_q in (("k", 128, 8), ("v", 128, 8), ("v", 256, 4), ("v", 64, 4)):
+        case = build(n_q, 2, hd, 16, lengths, [n], 43)
+        q, qsl, kc, vc, kg, vg, bt = case
+        (vg if side == "v" else kg)[bt[0, 1980 // 16], 1, 1980 % 16, 2] = 0x7F  # seen by the last 20 rows
+        check_attention(multi(case, lengths, n), case, lengths, one_tile=True)
+    case = list(build(8, 2, 128, 16, lengths, [n], 44))
+    case[6] = case[6].copy()
+    case[6][0, 20] = -5
+    st, need = status(), kv.paged_attention_fp4_workspace_size(1, 8, 2, 128, n, 125, 16)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = multi(tuple(case), lengths, n, workspace=ws[:need], status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == kv.DEV_BAD_BLOCK and bool((ws[need:] == 0xFF).all())
+    check_attention(got, tuple(case), lengths, one_tile=True)
+    with pytest.raises(kv.KvFp8Error):
+        multi(tuple(case), lengths, n, workspace=ws[:need - 16])
+
+
 @pytest.mark.parametrize("length", [200, 5000])  # taken whole, and split
 @pytest.mark.parametrize("hd, n_q, n", [(64, 4, 1), (128, 8, 1), (128, 16, 1), (256, 8, 1), (64, 8, 2), (128, 4, 2)])
 def test_a_tail_of_small_weights_beside_one_large(hd, n_q, n, length):
