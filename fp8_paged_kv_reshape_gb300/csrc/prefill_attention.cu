@@ -406,10 +406,13 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
 }
 // Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
 // their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
-// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part
-// is kMinPartKeys keys at least; a row tile of one part writes its output itself.
+// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A row
+// tile of one part writes its output itself.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
+// 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing
+// is split when more than half the SMs have a row tile: 80 to 216 tiles gained at most 7 % from any number
+// of parts and lost up to 60 %.
 constexpr int kSplitSms = 152;
-constexpr int kMinPartKeys = 256;
+constexpr int kMinPartKeys = 128;
 __host__ __device__ constexpr int split_parts(int splits, int key_tiles, int tile_keys) {
     const int most = key_tiles / (kMinPartKeys / tile_keys);
     return splits < most ? splits : most > 1 ? most : 1;

@@ -141,7 +141,7 @@ def test_attention_workspace_follows_the_route():
     assert ws(4, 32, 8, 128, 4, 256, 16) == kv.paged_attention_multi_workspace_size(4, 32, 8, 128, 4) > 0
     # 20 columns: tensor cores.  32 row tiles leave SMs idle, so their keys are split over four parts
     assert ws(4, 32, 8, 128, 5, 256, 16) == 32 * 4 * 128 * (128 + 1) * 4
-    assert ws(4, 32, 8, 128, 5, 31, 16) == 0                                  # fewer than two parts of 256 keys
+    assert ws(4, 32, 8, 128, 5, 15, 16) == 0                                  # fewer than two parts of 128 keys
     assert ws(10, 32, 8, 128, 5, 256, 16) == 0 and ws(4, 32, 8, 128, 512, 256, 16) == 0  # enough row tiles
     assert ws(4, 32, 8, 128, 1, 16, 16) == 0 < ws(4, 32, 8, 128, 1, 17, 16)   # 256 tokens: not split
     assert ws(-1, 32, 8, 128, 1, 256, 16) == ws(4, 32, 8, 128, 1, 0, 16) == 0
