@@ -429,15 +429,15 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t T, int64_t P) {
 // kCombineSlices slices of a sequence's parts are merged side by side (256 threads each),
 // then the slices' running states are merged: sequences cut into many parts (few, long
 // sequences over a full grid) get several loads in flight per output element.
-template <int HD, int kCombineSlices>
-__global__ void __launch_bounds__(256 * kCombineSlices) combine_kernel(const KernelArgs a) {
-    constexpr int TPH = HD / 4;     // threads per head
-    constexpr int HPB = 256 / TPH;  // heads per CTA
-    __shared__ float sm_m[kCombineSlices][256], sm_den[kCombineSlices][256];
-    __shared__ float4 sm_acc[kCombineSlices][256];
+template <int HD, int kCombineSlices, int kRows = 256 / (HD / 4)>
+__global__ void __launch_bounds__(kRows * (HD / 4) * kCombineSlices) combine_kernel(const KernelArgs a) {
+    constexpr int TPH = HD / 4;       // threads per row
+    constexpr int TS = kRows * TPH;   // threads of a slice: kRows rows per CTA
+    __shared__ float sm_m[kCombineSlices][TS], sm_den[kCombineSlices][TS];
+    __shared__ float4 sm_acc[kCombineSlices][TS];
     const int seq = blockIdx.x;
-    const int slice = threadIdx.x / 256, t = threadIdx.x % 256;
-    const int row = blockIdx.y * HPB + t / TPH;  // row of the sequence
+    const int slice = threadIdx.x / TS, t = threadIdx.x % TS;
+    const int row = blockIdx.y * kRows + t / TPH;  // row of the sequence
     const int d = (t % TPH) * 4;
     pdl_wait();  // the decode grid's partials are visible from here on
     const float sk = a.k_bf16 ? 1.f : load_scale(a.k_scale, a.scale_dtype);
