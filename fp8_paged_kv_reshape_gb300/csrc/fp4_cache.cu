@@ -7,12 +7,20 @@
 // cases).  Both kernels are HBM streams: the writer reads 2 (bf16) or 4 bytes per element and
 // writes 0.5625, the reader the reverse.
 //
-// One lane takes one group: its 16 source elements are 32 contiguous bytes of bf16 (one load),
-// the codes one 8-byte store, and the maximum needs no exchange between lanes.  A row is spread
-// over lanes_per_row lanes (a power of two, at most 32), so short rows share a warp; longer rows
-// are cut into passes of 32 groups along gridDim.y.  gridDim.z is the side (K or V), so a warp
-// has one layer scale.  Warps stride over the rows and hold the next row's elements, and the
-// slot after it, while they convert the present one.
+// A lane takes whole groups: a group's 16 source elements are 32 contiguous bytes of bf16 (one load),
+// its codes one 8-byte store, and the maximum needs no exchange between lanes; four lanes' scale
+// bytes leave as one word.  A row is spread over a power of two of lanes, at most 32, so short rows
+// share a warp; a row of more than 32 groups gives each lane two, 32 apart (two loads and two
+// independent conversions in flight; 32768 rows of 64 groups 60 to 38 us with the word stores), and
+// passes of 64 groups go along gridDim.y.  gridDim.z is the side (K or V), so a warp has one layer
+// scale.  Warps stride over the rows and hold the next row's elements, and the slot after it, while
+// they convert the present one.
+//
+// 32768 rows of 8 heads of 128, bf16, both sides: the write 37.4 us (172 MB: 4.6 TB/s; twice the rows
+// cost 5.3 TB/s more, the rest is start and end), a side read back 14.3 to 16.7 us (86 MB: 5.2 to 6.0
+// TB/s).  The writer issues 182 instructions per 32 groups, 82 of them to the FMA pipe for the
+// quotients: a warp waits as much for the pipes and its own dependencies as for memory.  Source
+// rows staged by bulk copies in a ring of three per warp instead of in registers: 43 us.
 //
 // The quotient |x| / d has to be the float quotient, because halfway cases are common (a bf16 x
 // over a d of few bits) and decide the code.  It takes the reciprocal-and-two-residuals divide

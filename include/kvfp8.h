@@ -1,7 +1,7 @@
 /*
  * kvfp8 -- FP8 (OCP E4M3) paged KV cache for GB300 (sm_103a): C ABI.
  *
- * Three operations, all enqueued on a caller-supplied CUDA stream:
+ * The operations, all enqueued on a caller-supplied CUDA stream:
  *   kvfp8_reshape_and_cache       bf16/f32 K,V rows -> divide by a per-layer scalar
  *                                 scale -> E4M3 (RNE, saturating at +-448) -> scatter
  *                                 into paged blocks at one byte per element
@@ -10,6 +10,9 @@
  *                                 scales, and computes softmax(q.K^T * s) V with GQA
  *   kvfp8_dequant                 bytes -> scale * value, for the rope-shift path
  *                                 (dequantize, rotate, requantize)
+ *   kvfp8_*_fp4                   the same over a cache of 4-bit codes with a scale per 16 dims
+ *   kvfp8_copy_blocks, kvfp8_compact_blocks
+ *                                 pages of any cache copied, and a pool's used pages gathered
  *
  * Sources, by page title and section:
  *   [P1] llama.cpp commit 202c1a229 "llama : Add FP8 KV-cache support (#28392)"
@@ -427,8 +430,8 @@ KVFP8_API kvfp8_status kvfp8_dequant_fp4(void *dst, kvfp8_dtype dst_dtype, const
 /*
  * Workspace bytes of the two calls below (decode: max_query_len 1): the results of the parts that
  * long sequences are split into.  0, where the workspace may be NULL, when nothing is split: block
- * tables of at most 256 tokens per sequence, or enough long query chunks to fill the GPU.  Pure host
- * arithmetic.
+ * tables of at most 256 tokens per sequence, or enough long query chunks to fill the GPU.  Calls that
+ * overlap on the GPU must not share a workspace.  Pure host arithmetic.
  */
 KVFP8_API size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
                                                           int32_t head_dim, int32_t max_query_len,
