@@ -410,7 +410,8 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
 // tile of one part writes its output itself.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
 // 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing
 // is split when more than half the SMs have a row tile: 80 to 216 tiles gained at most 7 % from any number
-// of parts and lost up to 60 %.
+// of parts and lost up to 60 %.  (kSplit is an instance of its own: the few instructions cost the unsplit
+// kernel of two row tiles 11 %, 531 against 478 us for 512 new tokens of 16 sequences of 4096.)
 constexpr int kSplitSms = 152;
 constexpr int kMinPartKeys = 128;
 __host__ __device__ constexpr int split_parts(int splits, int key_tiles, int tile_keys) {
@@ -588,7 +589,7 @@ constexpr int kPfConvWarps = 8;
 constexpr int kPfMmaWarp = 4 + kPfConvWarps, kPfTmaWarp = kPfMmaWarp + 1;
 constexpr int kPfWarps = kPfTmaWarp + 1;
 
-template <int HD, bool F4>
+template <int HD, bool F4, bool kSplit>
 __global__ void __launch_bounds__(kPfWarps * 32, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                const PrefillArgs a) {
@@ -639,7 +640,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     const int kend = Ls - nb + j_last + 1;           // keys the tile's last row may see
     int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
     int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
-    if constexpr (F4) {
+    if constexpr (kSplit) {
         parts = split_parts(a.splits, ntiles, kPfKeys);
         const int part = static_cast<int>(blockIdx.y);
         if (part >= parts) return;
@@ -650,7 +651,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     // starts its pass at its own key tile (the online softmax takes the keys in any order),
     // so they read different lines of the stream at any one time.
     const int rot = ntiles > 0 ? static_cast<int>((static_cast<int64_t>(tile) * ntiles) / a.row_tiles) % ntiles : 0;
-    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (F4 ? tile_lo : 0); };
+    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (kSplit ? tile_lo : 0); };
 
     if (ntiles == 0) {  // every row of the tile sees no key: zero rows
         if (tid < kPfRows) {
@@ -1092,10 +1093,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             // this row in the parts' results, when there are several
-            const int64_t prow = F4 && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
+            const int64_t prow = kSplit && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kPfRows) + tid : 0;
-            const float part_inv = lsum == 0.f ? 0.f : 1.f / lsum;
-            if (F4 && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
+            const float part_inv = !kSplit || lsum == 0.f ? 0.f : 1.f / lsum;
+            if (kSplit && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1103,7 +1104,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::kColO + c0, o);
                 tmem_wait_ld();
-                if (F4 && parts > 1) {
+                if (kSplit && parts > 1) {
                     if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
@@ -1229,7 +1230,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  : "memory");
 }
 
-template <int HD, bool F4>
+template <int HD, bool F4, bool kSplit>
 __global__ void __launch_bounds__(kP2Warps * 32, 1)
 prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const PrefillArgs a) {
@@ -1275,7 +1276,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const int kend = Ls - nb + j_last + 1;            // keys the CTA's last row may see
     int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
     int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
-    if constexpr (F4) {
+    if constexpr (kSplit) {
         parts = split_parts(a.splits, ntiles, kP2Keys);
         const int part = static_cast<int>(blockIdx.y);
         if (part >= parts) return;
@@ -1283,7 +1284,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         ntiles = static_cast<int>(static_cast<int64_t>(part + 1) * ntiles / parts) - tile_lo;
     }
     const int rot = ntiles > 0 ? static_cast<int>((static_cast<int64_t>(ctile) * ntiles) / a.row_tiles) % ntiles : 0;
-    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (F4 ? tile_lo : 0); };
+    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + (kSplit ? tile_lo : 0); };
 
     if (ntiles == 0) {  // every row of the CTA sees no key: zero rows
         if (tid < kP2Rows) {
@@ -1757,10 +1758,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             // this row in the parts' results, when there are several
-            const int64_t prow = F4 && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
+            const int64_t prow = kSplit && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kP2Rows) + tid : 0;
-            const float part_inv = lsum == 0.f ? 0.f : 1.f / lsum;
-            if (F4 && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
+            const float part_inv = !kSplit || lsum == 0.f ? 0.f : 1.f / lsum;
+            if (kSplit && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1768,7 +1769,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
-                if (F4 && parts > 1) {
+                if (kSplit && parts > 1) {
                     if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
@@ -1929,7 +1930,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     if constexpr (HD <= 128) {
         if (d.qsl != nullptr && d.qmax * a.group > kPfRows) {
             const size_t smem2 = Pf2Smem<HD, F4>::kTotal + 1024;
-            auto kern2 = prefill2_kernel<HD, F4>;
+            auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, F4, F4> : prefill2_kernel<HD, F4, false>;
             int occ2 = 0;  // also raises the kernel's shared memory limit, once per device
             if ((err = kernel_occupancy(kern2, kP2Warps * 32, smem2, &occ2)) != cudaSuccess)
                 return err;
@@ -1941,7 +1942,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         }
     }
     const size_t smem = L::kTotal + 1024;
-    auto kern = prefill_kernel<HD, F4>;
+    auto kern = sp.splits > 1 ? prefill_kernel<HD, F4, F4> : prefill_kernel<HD, F4, false>;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
     a.row_tiles = (d.qmax * a.group + kPfRows - 1) / kPfRows;
