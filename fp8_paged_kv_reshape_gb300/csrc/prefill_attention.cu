@@ -406,8 +406,7 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
 }
 // Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
 // their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
-// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A row
-// tile of one part writes its output itself.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
+// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
 // 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing
 // is split when more than half the SMs have a row tile: 80 to 216 tiles gained at most 7 % from any number
 // of parts and lost up to 60 %.  (kSplit is an instance of its own: the few instructions cost the unsplit
@@ -639,9 +638,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     const int j_last = min(nb, (row0 + kPfRows + G - 1) / G) - 1;
     const int kend = Ls - nb + j_last + 1;           // keys the tile's last row may see
     int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
-    int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
+    int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
-        parts = split_parts(a.splits, ntiles, kPfKeys);
+        const int parts = split_parts(a.splits, ntiles, kPfKeys);
         const int part = static_cast<int>(blockIdx.y);
         if (part >= parts) return;
         tile_lo = static_cast<int>(static_cast<int64_t>(part) * ntiles / parts);
@@ -1093,10 +1092,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             // this row in the parts' results, when there are several
-            const int64_t prow = kSplit && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
+            const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kPfRows) + tid : 0;
             const float part_inv = !kSplit || lsum == 0.f ? 0.f : 1.f / lsum;
-            if (kSplit && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
+            if (kSplit && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1104,7 +1103,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::kColO + c0, o);
                 tmem_wait_ld();
-                if (kSplit && parts > 1) {
+                if constexpr (kSplit) {
                     if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
@@ -1275,9 +1274,9 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const int j_last = min(nb, (row0 + kP2Rows + G - 1) / G) - 1;
     const int kend = Ls - nb + j_last + 1;            // keys the CTA's last row may see
     int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
-    int tile_lo = 0, parts = 1;  // this CTA's key tiles: ntiles from tile_lo on
+    int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
-        parts = split_parts(a.splits, ntiles, kP2Keys);
+        const int parts = split_parts(a.splits, ntiles, kP2Keys);
         const int part = static_cast<int>(blockIdx.y);
         if (part >= parts) return;
         tile_lo = static_cast<int>(static_cast<int64_t>(part) * ntiles / parts);
@@ -1758,10 +1757,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             uint32_t nan_groups = 0;
             if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
             // this row in the parts' results, when there are several
-            const int64_t prow = kSplit && parts > 1 ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
+            const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kP2Rows) + tid : 0;
             const float part_inv = !kSplit || lsum == 0.f ? 0.f : 1.f / lsum;
-            if (kSplit && parts > 1 && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
+            if (kSplit && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
             uint4 *orow = reinterpret_cast<uint4 *>(
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
@@ -1769,7 +1768,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
-                if (kSplit && parts > 1) {
+                if constexpr (kSplit) {
                     if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
@@ -1825,8 +1824,8 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs a, in
     // the row tile's parts, as its CTAs worked them out
     const int j_last = min(nb, (row0 + tile_rows + G - 1) / G) - 1;
     const int kend = Ls - nb + j_last + 1;
-    const int parts = split_parts(a.splits, kend > 0 ? (kend + tile_keys - 1) / tile_keys : 0, tile_keys);
-    if (parts == 1) return;
+    if (kend <= 0) return;  // zeroed by its CTA
+    const int parts = split_parts(a.splits, (kend + tile_keys - 1) / tile_keys, tile_keys);
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
     PartMerge mg;
     for (int c0 = 0; c0 < parts; c0 += 8) {
