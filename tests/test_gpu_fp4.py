@@ -460,6 +460,21 @@ def test_bad_blocks_lengths_and_query_rows_are_flagged():
                         one_tile=qmax > 4)
 
 
+@pytest.mark.parametrize("n_q, hd, length, qmax", [(4, 64, 100, 2), (8, 128, 900, 2), (8, 128, 2000, 40), (8, 128, 300, 200)])
+def test_rows_behind_the_last_sequence_are_left(n_q, hd, length, qmax):
+    """A padded batch: sequences of no new tokens, query rows that no sequence has, an empty sequence."""
+    lengths, qlens = [length, 0, length], [qmax, 0, 0]
+    case = list(build(n_q, 2, hd, 16, lengths, qlens, 27))
+    q = case[0]
+    padded = torch.cat([q, torch.full((5, n_q, hd), math.nan).bfloat16()])
+    out = torch.full(padded.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    st = status()
+    multi((padded, *case[1:]), lengths, qmax, out=out, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and bool((out[qmax:] == 7).all())
+    check_attention(out[:qmax], case, lengths, one_tile=True)
+
+
 def test_streams_and_graphs():
     """A call on another stream, two calls at once with workspaces of their own, and a captured write and
     read replayed on new inputs."""
@@ -491,6 +506,30 @@ def test_streams_and_graphs():
         host = [a.cpu().numpy() for a in t]
         check_attention(first, (q, np.arange(3), host[0], host[1], host[2], host[3], bt), lengths)
         assert torch.equal(kv.paged_decode_attention_fp4(qc, *t, lens, ks, vs), first)
+
+
+def test_a_captured_chunk_with_split_keys():
+    """A short chunk on a long context captured with its workspace from the graph's memory, replayed between
+    eager calls on another stream; the current device's streams are the callers' own."""
+    lengths = [3000]
+    case = build(32, 8, 128, 16, lengths, [16], 28)
+    q, qsl, kc, vc, kg, vg, bt = case
+    t = [dev(a) for a in (kc, vc, kg, vg, bt)]
+    lens, start, ks, vs, qc = dev(np.array(lengths, np.int32)), dev(qsl), scalar(KS), scalar(VS), q.cuda()
+    call = lambda **more: kv.paged_attention_multi_fp4(qc, start, 16, *t, lens, ks, vs, **more)
+    want = call()
+    check_attention(want, case, lengths, one_tile=True)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        got = call()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(5):
+        got.zero_()
+        g.replay()
+        outs += [call(stream=side), got.clone()]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
 
 
 def test_large_offsets():
