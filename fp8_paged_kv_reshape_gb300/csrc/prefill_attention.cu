@@ -255,8 +255,6 @@ struct PrefillArgs {
 // in V^T's rows, row 8j + 2a + b holding dim 8a + 2j + b, and so in O's columns: O's word (pair of
 // columns) 4j + a is the output's word 4a + j.
 
-__device__ __forceinline__ bool is_nan_byte(uint32_t b) { return (b & 0x7Fu) == 0x7Fu; }
-
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -388,22 +386,35 @@ __device__ __forceinline__ void copy_scales(const PrefillArgs &a, int kvh, int t
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The groups (bit g: dims 16g..16g+15) in which some value of tokens 0..last of the sequence is
-// NaN; blocks out of range hold no tokens.
+// The groups (bit g: dims 16g..16g+15) in which some value of tokens first..last of the sequence is NaN, for
+// each lane's own last (negative: none); blocks out of range hold no tokens.  Called by whole warps: the
+// tokens that every lane has are shared out over the lanes, the few after them are each lane's own.
 template <int HD>
-__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq, int kvh, int last) {
+__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq, int kvh, int first, int last) {
     const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
     uint32_t groups = 0;
-    for (int t = 0; t <= last; ++t) {
+    auto look = [&](int t) {
         const int32_t blk = bt[t / a.block_size];
-        if (blk < 0 || blk >= a.num_blocks) continue;
-        const uint8_t *row = a.value_scales +
-                             ((static_cast<int64_t>(blk) * a.n_kv + kvh) * a.block_size + t % a.block_size) * (HD / 16);
-        for (int g = 0; g < HD / 16; ++g)
-            if (is_nan_byte(row[g])) groups |= 1u << g;
-    }
+        if (blk < 0 || blk >= a.num_blocks) return;
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(
+            a.value_scales +
+            ((static_cast<int64_t>(blk) * a.n_kv + kvh) * a.block_size + t % a.block_size) * (HD / 16));
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            const uint32_t nan = nan_byte_mask(row[i]) & 0x08040201u;
+            groups |= ((nan | nan >> 8 | nan >> 16 | nan >> 24) & 0xFu) << (4 * i);
+        }
+    };
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int all = __reduce_min_sync(0xFFFFFFFFu, last < 0 ? INT32_MAX : last);  // tokens first..all are every lane's
+    if (all != INT32_MAX)
+        for (int t = first + lane; t <= all; t += 32) look(t);
+    groups = __reduce_or_sync(0xFFFFFFFFu, groups);
+    if (last < 0) return 0u;
+    for (int t = max(first, all + 1); t <= last; ++t) look(t);
     return groups;
 }
+
 // Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
 // their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
 // normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
@@ -1090,7 +1101,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             }
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
             uint32_t nan_groups = 0;
-            if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
+            if (F4 && *nan_seen) {
+                const int key0 = kSplit ? tile_lo * kPfKeys : 0;  // of this part's keys
+                nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
+                                                  row_ok ? kSplit ? min(pos, key0 + ntiles * kPfKeys - 1) : pos : -1);
+            }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kPfRows) + tid : 0;
@@ -1755,7 +1770,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float lsum = ls.x + ls.y;
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
             uint32_t nan_groups = 0;
-            if (F4 && row_ok && *nan_seen) nan_groups = nan_value_groups<HD>(a, seq, kvh, pos);
+            if (F4 && *nan_seen) {
+                const int key0 = kSplit ? tile_lo * kP2Keys : 0;  // of this part's keys
+                nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
+                                                  row_ok ? kSplit ? min(pos, key0 + ntiles * kP2Keys - 1) : pos : -1);
+            }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
                                                      blockIdx.y) * kP2Rows) + tid : 0;

@@ -422,6 +422,18 @@ def test_a_nan_reaches_exactly_the_rows_and_dims_that_see_it(n_q, n_kv, hd, bs, 
         assert bool(seen.any()) and not bool(seen[-1])
 
 
+def test_long_chunks_of_caches_full_of_nans():
+    """NaN groups all over V, at every row's last tokens among them: each row sees its own."""
+    r = np.random.default_rng(45)
+    for n_q, hd, lengths, qlens in ((8, 128, [700, 90], [200, 90]), (4, 64, [1500], [30]), (4, 256, [600], [70])):
+        case = build(n_q, 2, hd, 16, lengths, qlens, 46)
+        vg, bt = case[5], case[6]
+        for s, length in enumerate(lengths):
+            for t in r.integers(max(0, length - max(qlens) - 20), length, 12):
+                vg[bt[s, t // 16], r.integers(2), t % 16, r.integers(hd // 16)] = 0x7F
+        check_attention(multi(case, lengths, max(qlens)), case, lengths, one_tile=True)
+
+
 def test_decode_nan_in_a_split_sequence():
     lengths = [9000, 40]
     for side in ("k", "v"):
