@@ -874,8 +874,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         for (int i = 0; i < ntiles && ok; ++i) {
             const int st = i % L::kNS, b = i % L::kNB;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kFull, st), (i / L::kNS) & 1, abort_flag));
-            // the buffer's previous tile (i-NB) has been through both products
-            if (ok)
+            // the buffer's previous tile (i-NB) has been through both products (F4: waited for below)
+            if (!F4 && ok)
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kKvFree, b), ((i / L::kNB) & 1) ^ 1u, abort_flag));
             if (!ok) break;
@@ -941,6 +941,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     else
                         un[j].template load<false>(codes + kPfKeys * L::kRow, scales + L::kScaleSide, mask, u - kU, lane);
                 }
+                // the codes are in registers: the stage is refilled while the tile's buffer is waited for
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kEmpty, st));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kKvFree, b), ((i / L::kNB) & 1) ^ 1u, abort_flag));
+                if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < kMine; ++j) {
                     const int u = w4 + j * kPfConvWarps;
@@ -985,7 +990,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bar(L::kEmpty, st));     // the FP8 stage may be refilled
+                if (!F4) mbar_arrive(bar(L::kEmpty, st));  // the FP8 stage may be refilled
                 mbar_arrive(bar(L::kKvReady, b));    // K(i), V^T(i) (and Q) are ready
             }
         }
