@@ -415,6 +415,12 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
     return groups;
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
 // their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
 // normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
@@ -781,6 +787,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 const uint32_t stage = base + L::kStage + st * L::kStageBytes;
                 copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
                                 bar(L::kFull, st), lane);
+            }
+            if constexpr (F4 && L::kNS == 1) {
+                // one stage: the next copies start when this tile has been read, so their lines are brought
+                // into L2 meanwhile, as far as the window of block-table entries goes (head_dim 256, 32 tokens
+                // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128)
+                const int e = ((t + kPfKeys) >> lbs) - wbase;
+                const int next = __shfl_sync(0xFFFFFFFFu, win, e & 31);
+                if (box_lane && t + kPfKeys < kend && e < 32 && next >= 0 && next < a.num_blocks) {
+                    const int nrow = next * bs + (t & (bs - 1));
+#pragma unroll
+                    for (int sgi = 0; sgi < L::kSegs; ++sgi) tma_prefetch_3d(map, 0, kvh * L::kSegs + sgi, nrow);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        (k_lane ? a.key_scales : a.value_scales) +
+                        (((static_cast<int64_t>(next) * a.n_kv + kvh) << lbs) + (t & (bs - 1))) * (HD / 16)));
+                }
             }
         }
         if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
