@@ -348,6 +348,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
             if (aborted) break;
+            __syncwarp();  // what lane 0 waited for (the stage has been read) holds for every lane's copies
             if (good) {  // the expected bytes are posted: each lane copies its box
                 const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
                 const int off = t & (a.block_size - 1), row = (blk << lbs) + off;

@@ -773,6 +773,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
             if (aborted) break;
+            __syncwarp();  // what lane 0 waited for (the stage has been read) holds for every lane's copies
             // the expected bytes are posted: each lane with a box copies it
             if (good) {
                 const uint32_t full = bar(L::kFull, st);
@@ -1430,6 +1431,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
             if (aborted) break;
+            __syncwarp();  // as in the one-row-tile kernel
             if (good) {
                 const uint32_t full = bar(L::kFull, st);
                 const uint32_t dst = base + L::kStage + st * L::kStageBytes + side +
