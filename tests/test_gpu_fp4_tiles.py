@@ -45,6 +45,16 @@ FEW = [  # fewer: the keys are split, over many tiles of a part
     (8, 4, 128, 16, 17, 70, 2800, 3300),
     (20, 1, 128, 16, 1, 1, 20011, 20011),
 ]
+DECODE = [  # up to 16 score rows: chunks of 32 keys, in ranges of equal length over the CTAs
+    (8, 2, 64, 16, 3, 1, 9000, 20011),
+    (32, 8, 128, 16, 3, 1, 9000, 20011),
+    (32, 2, 128, 8, 2, 1, 9000, 20011),
+    (8, 2, 256, 16, 3, 1, 9000, 20011),
+    (4, 1, 64, 64, 300, 1, 100, 900),
+    (32, 8, 128, 32, 5, 4, 3000, 9000),
+    (4, 4, 64, 8, 5, 3, 3000, 9000),
+    (4, 2, 256, 16, 5, 4, 3000, 9000),
+]
 
 
 def shared_case(n_kv, hd, bs, seqs, n, lo, hi, seed):
@@ -81,7 +91,7 @@ def call(q, qsl, n, kc, vc, kg, vg, bt, lens, ks, vs, sm, st):
     return kv.paged_attention_multi_fp4(q.cuda(), dev(qsl), n, *args, scalar(ks), scalar(vs), sm, status=st)
 
 
-@pytest.mark.parametrize("n_q, n_kv, hd, bs, seqs, n, lo, hi", WIDE + FEW)
+@pytest.mark.parametrize("n_q, n_kv, hd, bs, seqs, n, lo, hi", WIDE + FEW + DECODE)
 def test_each_dim_counts_its_tokens(n_q, n_kv, hd, bs, seqs, n, lo, hi):
     r, lens, row, nb, bt, qsl = shared_case(n_kv, hd, bs, seqs, n, lo, hi, hd + seqs + hi)
     split = kv.paged_attention_fp4_workspace_size(seqs, n_q, n_kv, hd, n, bt.shape[1], bs) > 0
@@ -103,7 +113,7 @@ def test_each_dim_counts_its_tokens(n_q, n_kv, hd, bs, seqs, n, lo, hi):
     assert np.all(np.abs(got - want[:, :, :, None]) <= (2.0 ** -8 + 2.0 ** -18) * want[:, :, :, None])
 
 
-@pytest.mark.parametrize("n_q, n_kv, hd, bs, seqs, n, lo, hi", WIDE + FEW)
+@pytest.mark.parametrize("n_q, n_kv, hd, bs, seqs, n, lo, hi", WIDE + FEW + DECODE)
 def test_every_row_finds_its_needle(n_q, n_kv, hd, bs, seqs, n, lo, hi):
     r, lens, row, nb, bt, qsl = shared_case(n_kv, hd, bs, seqs, n, lo, hi, hd + seqs + hi + 1)
     k = r.choice([-1.0, 1.0], (hi, n_kv, hd))
