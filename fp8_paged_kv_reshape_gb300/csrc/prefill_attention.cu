@@ -1096,9 +1096,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     tmem_st32(lane_addr + L::kColO + c0, o);
                 }
             }
-            // P = 2^(s*mult - m) as f16 pairs over the first 32 columns of this S buffer: one
-            // packed fma, one f16 pack and one f16x2 exp2 per pair (x <= 2^3 by the rescale
-            // rule, so P <= 2^8)
+            // P = 2^(s*mult - m) as f16 pairs over the first 32 columns of this S buffer.  E4M3: one
+            // packed fma, one f16 pack and one f16x2 exp2 per pair (x <= 2^3 by the rescale rule, so
+            // P <= 2^8).  F4: the exponent stays float and the weight is rounded, once: an fp16 exponent
+            // of 8 to 16 moves a weight by up to 2^-8.5, a rounded weight by 2^-11.
             uint32_t p[32];
             const float msub = m_used == -INFINITY ? 0.f : m_used;
             const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(-msub, -msub);
@@ -1106,7 +1107,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             for (int c = 0; c < 32; ++c) {
                 const int h = c >> 4, e = (2 * c) & 31;
                 const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), mul2, sub2));
-                p[c] = ex2_f16x2(f16x2_from_f32(x.x, x.y));
+                p[c] = F4 ? f16x2_from_f32(ex2(x.x), ex2(x.y)) : ex2_f16x2(f16x2_from_f32(x.x, x.y));
                 if (!L::kSumCol) lsum += f16lo_f32(p[c]) + f16hi_f32(p[c]);
             }
             tmem_st32(lane_addr + 64 * b, p);
