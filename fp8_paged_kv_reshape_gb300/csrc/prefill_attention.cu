@@ -248,6 +248,11 @@ struct PrefillArgs {
 // such scales are taken as 0, the CTA remembers that it met one, and at the end each of its rows
 // looks up which groups of the values it sees are NaN (a slow scan that no finite cache runs).
 
+// Weights are taken against a reference 2^7 below the row's highest score at the time (the E4M3 forms:
+// that score), so they reach up to 2^15 and keep their 11 bits down to 2^-21 of the highest and are above
+// zero down to 2^-32, as in the decode kernel over the same cache (paged_decode_fp4.cu).
+constexpr float kF4Head = 7.f;
+
 // Conversion goes by units of 32 rows of 16 code bytes (8 keys x 4 chunks of 32 dims; 16 keys x 2 at
 // head_dim 64; at 256 a key group has two units).  One ldmatrix gives a lane, per chunk, the codes of
 // dims 8u..8u+7 of a key (u = lane % 4): as K they are one 16-byte piece of the key's operand row; as V
@@ -1028,6 +1033,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         const int pos = Ls - nb + jq;               // last key position the row may see
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        constexpr float kHead = F4 ? kF4Head : 0.f;
         float m_used = -INFINITY, lsum = 0.f;
         bool ok = true;
         for (int i = 0; i < ntiles && ok; ++i) {
@@ -1073,10 +1079,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             float factor = 1.f;
             if (mx > -INFINITY) {
                 if (m_used == -INFINITY) {
-                    m_used = mx;
-                } else if (mx > m_used + 8.f) {
-                    factor = ex2(m_used - mx);
-                    m_used = mx;
+                    m_used = mx - kHead;
+                } else if (mx > m_used + 8.f + kHead) {
+                    factor = ex2(m_used - (mx - kHead));
+                    m_used = mx - kHead;
                 }
             }
             if (__any_sync(0xFFFFFFFFu, factor != 1.f)) {
@@ -1098,7 +1104,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             }
             // P = 2^(s*mult - m) as f16 pairs over the first 32 columns of this S buffer.  E4M3: one
             // packed fma, one f16 pack and one f16x2 exp2 per pair (x <= 2^3 by the rescale rule, so
-            // P <= 2^8).  F4: the exponent stays float and the weight is rounded, once: an fp16 exponent
+            // P <= 2^8; F4: 2^15).  F4: the exponent stays float and the weight is rounded, once: an fp16 exponent
             // of 8 to 16 moves a weight by up to 2^-8.5, a rounded weight by 2^-11.
             uint32_t p[32];
             const float msub = m_used == -INFINITY ? 0.f : m_used;
@@ -1685,6 +1691,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scol = lane_addr + L::col_s(rt);
+        constexpr float kHead = F4 ? kF4Head : 0.f;
         float m_used = -INFINITY;
         uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
         bool ok = true;
@@ -1734,10 +1741,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             float factor = 1.f;
             if (mx > -INFINITY) {
                 if (m_used == -INFINITY) {
-                    m_used = mx;
-                } else if (mx > m_used + 8.f) {
-                    factor = ex2(m_used - mx);
-                    m_used = mx;
+                    m_used = mx - kHead;
+                } else if (mx > m_used + 8.f + kHead) {
+                    factor = ex2(m_used - (mx - kHead));
+                    m_used = mx - kHead;
                 }
             }
             if (__any_sync(0xFFFFFFFFu, factor != 1.f)) {

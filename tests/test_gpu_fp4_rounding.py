@@ -64,3 +64,52 @@ def test_weights_are_rounded_once(n_q, n_kv, hd, n, seqs):
             half = 2.0 ** (np.floor(np.log2(ref * (1 + 2.0 ** -10))) - 8)
             over = np.abs(got - ref) - (half + 2.0 ** -10.5 * ref)
             assert over.max() <= 0, (x, ks, (np.abs(got - ref) / ref).max())
+
+
+@pytest.mark.parametrize("length", [200, 5000])
+@pytest.mark.parametrize("n_q, n_kv, hd, n, seqs", ROUTES)
+def test_a_tail_of_small_weights_counts_on_every_route(n_q, n_kv, hd, n, seqs, length):
+    """Weights 2^-25.5 of the highest, whose values are zero: the outputs are the tail's share alone.
+
+    The highest weight of a row is 2^7 at least, so the others are 2^-18.5 at least, 45 of fp16's smallest
+    steps: half a step is 2^-6.5 of them.  The output's rounding adds 2^-8 and the scores 2^-10.5 as above, with
+    77 for 42 log2: within 2^-6 in all."""
+    for top in (0, length // 2) if n == 1 else (0,):
+        got, ref = one_and_many(n_q, hd, n, seqs, length, top, 25.5)
+        assert np.abs(got / ref - 1).max() < 2.0 ** -6, top
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, n, seqs", ROUTES)
+def test_scores_rising_along_the_keys(n_q, n_kv, hd, n, seqs):
+    """The highest score comes up by a step every 64 tokens, so the weights' reference moves with it (or lags): by
+    3 log2 (six tiles reach past what a reference may lag behind), by 14, by 15.5 and by 40.
+
+    Each output dim belongs to one token class of 64, with value 1, so that its output is that class's
+    share.  The classes' weights are fp16 numbers (2^-11 each) above 2^-14 of 2^7, and the class shares of a row
+    differ by powers 2^-step; shares below 2^-20 are not compared closely.  bf16: 2^-8."""
+    bs, length = 16, 64 * 9 + 5
+    nb = -(-length // bs)
+    cls = np.arange(length) // 64
+    for step in (3.0, 14.0, 15.5, 40.0):
+        kc = np.zeros((nb, bs, 1, hd // 2), np.uint8)
+        kg, vg = (np.full((nb, 1, bs, hd // 16), 0x38, np.uint8) for _ in "kv")
+        vc = np.zeros((nb, bs, 1, hd // 2), np.uint8)
+        for t in range(length):
+            kc[t // bs, t % bs, 0, 0] = 0x02                     # dim 0 is 1 under a scale of 1 + class
+            kg[t // bs, 0, t % bs, 0] = (0x00, 0x38, 0x40, 0x44, 0x48, 0x4A, 0x4C, 0x4E, 0x50, 0x51)[cls[t]]
+            vc[t // bs, t % bs, 0, cls[t]] = 0x22                # dims 2c, 2c + 1
+        q = torch.zeros(seqs * n, n_q, hd, dtype=torch.bfloat16)
+        q[..., 0] = 1.0
+        qsl = (np.arange(seqs + 1) * n).astype(np.int32)
+        bt = np.arange(nb, dtype=np.int32)[None].repeat(seqs, 0)
+        lens = np.full(seqs, length, np.int32)
+        args = [dev(a) for a in (kc, vc, kg, vg, bt, lens)] + [scalar(1.0), scalar(1.0), step * math.log(2)]
+        out = kv.paged_decode_attention_fp4(q.cuda(), *args) if n == 1 else \
+            kv.paged_attention_multi_fp4(q.cuda(), dev(qsl), n, *args)
+        got = out.double().cpu().numpy().reshape(seqs, n, n_q, hd)
+        assert np.array_equal(got, got[:1].repeat(seqs, 0))
+        ref, _ = fp4.attention(q[:n].double().numpy(), np.array([0, n]), kc, vc, kg, vg, bt, lens[:1], 1.0, 1.0,
+                               step * math.log(2))
+        # (2^-16 of float32 error in scores of up to 360 log2)
+        near = np.where(ref > 2.0 ** -20, (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * ref, 2.0 ** -6 * ref + 2.0 ** -30)
+        assert np.all(np.abs(got[0] - ref) <= near), step
