@@ -2,7 +2,6 @@
 // Declarations, argument meanings and error behaviour: include/kvfp8.h.
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -282,10 +281,7 @@ kvfp8_status kvfp8_paged_attention_multi(
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return KVFP8_ERR_SHAPE;
     if (!block_size_ok_for_decode(block_size)) return KVFP8_ERR_SHAPE;
     const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
-    if (!split_kv && (n_q / n_kv > 128 ||
-                      (static_cast<int64_t>(max_query_len) * (n_q / n_kv) + 127) / 128 * n_kv *
-                              num_seqs > 0x7FFFFFFFLL))
-        return KVFP8_ERR_UNSUPPORTED;
+    if (!split_kv && !kvfp8::prefill_takes(n_q, n_kv, max_query_len, num_seqs)) return KVFP8_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(num_blocks) * block_size > 0x7FFFFFFFLL ||
         static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL)
         return KVFP8_ERR_SHAPE;
@@ -673,10 +669,7 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
     const kvfp8_status sh = check_fp4_cache(num_blocks, block_size, n_kv, head_dim);
     if (sh != KVFP8_OK) return sh;
     const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
-    if (!split_kv && (n_q / n_kv > 128 ||  // the tensor-core kernel's row tiles are its grid
-                      (static_cast<int64_t>(max_query_len) * (n_q / n_kv) + 127) / 128 >
-                          0x7FFFFFFFLL / n_kv / std::max(1, num_seqs)))
-        return KVFP8_ERR_UNSUPPORTED;
+    if (!split_kv && !kvfp8::prefill_takes(n_q, n_kv, max_query_len, num_seqs)) return KVFP8_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
     if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
     if (num_seqs == 0) return KVFP8_OK;

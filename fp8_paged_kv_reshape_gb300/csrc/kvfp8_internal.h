@@ -187,6 +187,8 @@ bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
 cudaError_t launch_prefill_attention(const DecodeArgs &a, cudaStream_t stream);
 size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
                                   int64_t max_len);
+// True when its grid and its 32-bit row numbers hold this many score rows (host arithmetic).
+bool prefill_takes(int32_t n_q, int32_t n_kv, int32_t max_query_len, int32_t num_seqs);
 // True when kvfp8_paged_attention_multi takes the split-KV decode kernel for this shape
 // (and so needs a workspace); false when it takes the prefill kernel.
 bool multi_uses_decode_kernel(int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t max_query_len);

@@ -1980,15 +1980,16 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     a.splits = sp.splits;
     a.part_o = static_cast<float *>(d.workspace);
     a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(d.workspace) + sp.lse_off);
+    const int group_rows = d.qmax * a.group;  // score rows of a kv head (prefill_takes: below 2^31 - 511)
     // more than one tile of 128 rows per kv head (a multi-query call): 256 rows per CTA
     if constexpr (HD <= 128) {
-        if (d.qsl != nullptr && d.qmax * a.group > kPfRows) {
+        if (d.qsl != nullptr && group_rows > kPfRows) {
             const size_t smem2 = Pf2Smem<HD, F4>::kTotal + 1024;
             auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, F4, F4> : prefill2_kernel<HD, F4, false>;
             int occ2 = 0;  // also raises the kernel's shared memory limit, once per device
             if ((err = kernel_occupancy(kern2, kP2Warps * 32, smem2, &occ2)) != cudaSuccess)
                 return err;
-            a.row_tiles = (d.qmax * a.group + kP2Rows - 1) / kP2Rows;
+            a.row_tiles = (group_rows + kP2Rows - 1) / kP2Rows;
             const int64_t ctas = static_cast<int64_t>(d.num_seqs) * a.row_tiles * d.n_kv;
             kern2<<<dim3(static_cast<unsigned>(ctas), sp.splits), kP2Warps * 32, smem2, stream>>>(tmk, tmv, a);
             if ((err = cudaGetLastError()) != cudaSuccess || sp.splits == 1) return err;
@@ -1999,7 +2000,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     auto kern = sp.splits > 1 ? prefill_kernel<HD, F4, F4> : prefill_kernel<HD, F4, false>;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
-    a.row_tiles = (d.qmax * a.group + kPfRows - 1) / kPfRows;
+    a.row_tiles = (group_rows + kPfRows - 1) / kPfRows;
     const int64_t ctas = static_cast<int64_t>(d.num_seqs) * a.row_tiles * d.n_kv;
     kern<<<dim3(static_cast<unsigned>(ctas), sp.splits), kPfWarps * 32, smem, stream>>>(tmk, tmv, a);
     if ((err = cudaGetLastError()) != cudaSuccess || sp.splits == 1) return err;
@@ -2013,12 +2014,18 @@ size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, i
     return split_plan(num_seqs, n_q, n_kv, head_dim, qmax, max_len).total;
 }
 
+bool prefill_takes(int32_t n_q, int32_t n_kv, int32_t max_query_len, int32_t num_seqs) {
+    // score rows of a (sequence, kv head) are ints, up to the end of the last tile and a group of heads past it
+    constexpr int64_t kMostRows = 0x80000000LL - 512;
+    const int64_t rows = static_cast<int64_t>(max_query_len) * (n_q / n_kv);
+    if (n_q / n_kv > kPfRows || rows > kMostRows) return false;
+    return (rows + kPfRows - 1) / kPfRows <= 0x7FFFFFFFLL / n_kv / std::max(1, num_seqs);
+}
+
 cudaError_t launch_prefill_attention(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;
     if (d.k_bf16 || d.v_bf16) return cudaErrorNotSupported;
-    if (d.n_q / d.n_kv > kPfRows) return cudaErrorNotSupported;
-    const int64_t row_tiles = (static_cast<int64_t>(d.qmax) * (d.n_q / d.n_kv) + kPfRows - 1) / kPfRows;
-    if (row_tiles * d.n_kv * d.num_seqs > 0x7FFFFFFF) return cudaErrorNotSupported;
+    if (!prefill_takes(d.n_q, d.n_kv, d.qmax, d.num_seqs)) return cudaErrorNotSupported;
     const bool f4 = d.key_scales != nullptr;
     switch (d.head_dim) {
         case 64: return f4 ? run_prefill<64, true>(d, stream) : run_prefill<64, false>(d, stream);
