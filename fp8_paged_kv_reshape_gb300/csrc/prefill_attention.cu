@@ -420,6 +420,19 @@ __device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs &a, int seq,
     return groups;
 }
 
+// Where the key one tile after key t lies: its block-table entry, and the row within that block.
+struct KeyPlace {
+    int entry, row;
+};
+__host__ __device__ constexpr KeyPlace next_tile_place(int t, int lbs) {
+    return {(t + kPfKeys) >> lbs, (t + kPfKeys) & ((1 << lbs) - 1)};
+}
+static_assert(next_tile_place(0, 4).entry == 4 && next_tile_place(0, 4).row == 0 && next_tile_place(16, 4).entry == 5);
+static_assert(next_tile_place(64, 6).entry == 2 && next_tile_place(64, 6).row == 0);
+static_assert(next_tile_place(0, 7).entry == 0 && next_tile_place(0, 7).row == 64, "the second half of a block of 128");
+static_assert(next_tile_place(64, 7).entry == 1 && next_tile_place(64, 7).row == 0);
+static_assert(next_tile_place(128, 8).entry == 0 && next_tile_place(128, 8).row == 192);
+
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                  "r"(c0), "r"(c1), "r"(c2)
@@ -798,16 +811,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 // one stage: the next copies start when this tile has been read, so their lines are brought
                 // into L2 meanwhile, as far as the window of block-table entries goes (head_dim 256, 32 tokens
                 // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128)
-                const int e = ((t + kPfKeys) >> lbs) - wbase;
-                const int next = __shfl_sync(0xFFFFFFFFu, win, e & 31);
-                if (box_lane && t + kPfKeys < kend && e < 32 && next >= 0 && next < a.num_blocks) {
-                    const int nrow = next * bs + (t & (bs - 1));
+                const KeyPlace box = next_tile_place(t, lbs);
+                const int next = __shfl_sync(0xFFFFFFFFu, win, (box.entry - wbase) & 31);
+                if (box_lane && t + kPfKeys < kend && box.entry - wbase < 32 && next >= 0 && next < a.num_blocks) {
 #pragma unroll
-                    for (int sgi = 0; sgi < L::kSegs; ++sgi) tma_prefetch_3d(map, 0, kvh * L::kSegs + sgi, nrow);
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                        (k_lane ? a.key_scales : a.value_scales) +
-                        (((static_cast<int64_t>(next) * a.n_kv + kvh) << lbs) + (t & (bs - 1))) * (HD / 16)));
+                    for (int sgi = 0; sgi < L::kSegs; ++sgi)
+                        tma_prefetch_3d(map, 0, kvh * L::kSegs + sgi, next * bs + box.row);
                 }
+                // and the scale bytes, kLineKeys keys of a side by each of the first lanes
+                constexpr int kLineKeys = 128 / (HD / 16), kLines = kPfKeys / kLineKeys;
+                const int lt = t0 + lane % kLines * kLineKeys;
+                const KeyPlace line = next_tile_place(lt, lbs);
+                const int lblk = __shfl_sync(0xFFFFFFFFu, win, (line.entry - wbase) & 31);
+                if (lane < 2 * kLines && lt + kPfKeys < kend && line.entry - wbase < 32 && lblk >= 0 && lblk < a.num_blocks)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        (lane < kLines ? a.key_scales : a.value_scales) +
+                        (((static_cast<int64_t>(lblk) * a.n_kv + kvh) << lbs) + line.row) * (HD / 16)));
             }
         }
         if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
