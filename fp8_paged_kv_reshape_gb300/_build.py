@@ -42,6 +42,14 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the kvfp8 CUDA library cannot be built")
 
 
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def torch_module() -> str:
     """The path of the module on torch tensors; it is bound to one torch and one Python, so their
     versions are in the name."""
@@ -112,9 +120,9 @@ def _link_torch_calls(obj: str, module: str) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the library, and the module on torch tensors, where missing or older than
-    their sources."""
-    module = torch_module()
-    lib_stale, module_stale = force or _stale(LIB), force or _stale(module, [TORCH_SRC])
+    their sources.  Without a torch there is only the library."""
+    module = torch_module() if _has_torch() else None
+    lib_stale, module_stale = force or _stale(LIB), module and (force or _stale(module, [TORCH_SRC]))
     if not lib_stale and not module_stale:
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)

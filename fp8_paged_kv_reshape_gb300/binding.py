@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the path runs in libkvfp8.so's CUDA kernels.
 PyTorch supplies device memory and the current stream.  The calls of the 4-bit cache and of
 pages are marshalled by compiled code (csrc/torch_calls.cpp), the others here.  There is no CPU
-or eager fallback: if the library or that module is missing, importing this module raises.
+or eager fallback: importing this module raises if the library is missing, and those calls raise if
+the compiled code is (it is built against one torch, the library against none).
 """
 from __future__ import annotations
 
@@ -531,7 +532,16 @@ def _load_calls():
     return module
 
 
-_CALLS = _load_calls()
+class _Calls:
+    """The compiled wrappers, loaded at the first call of one."""
+
+    def __getattr__(self, name):
+        module = _load_calls()
+        self.__dict__.update((k, v) for k, v in vars(module).items() if not k.startswith("_"))
+        return getattr(module, name)
+
+
+_CALLS = _Calls()
 _HERE = contextlib.nullcontext()
 
 
