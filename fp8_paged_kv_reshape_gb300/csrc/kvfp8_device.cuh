@@ -92,15 +92,6 @@ __device__ __forceinline__ uint32_t e2m1x8_from_f32(const float *x) {
     return r;
 }
 
-// The two E2M1 codes in the low byte of v -> an fp16 pair, low nibble in the low half.
-__device__ __forceinline__ uint32_t f16x2_from_e2m1x2(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
-        : "=r"(r)
-        : "r"(v));
-    return r;
-}
-
 // Eight E2M1 codes -> four fp16 pairs (nibbles 2i, 2i+1 in the halves of r[i]).
 __device__ __forceinline__ void f16x2_from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
