@@ -838,6 +838,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     int hpc = std::min(d.n_kv, fp4_max_heads<HD, NV>());
     while (d.n_kv % hpc != 0) --hpc;
     const int groups = d.n_kv / hpc;
+    if (groups > 65535) return cudaErrorNotSupported;  // gridDim.y (a large prime n_kv)
     const int box_rows = std::min(d.block_size, kTok);
     Fp4KernelArgs f;
     f.code_box = static_cast<uint32_t>(hpc * box_rows * (HD / 2));

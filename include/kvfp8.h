@@ -444,8 +444,9 @@ KVFP8_API size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int3
  *   out[b][h][d] = v_scale * sum_t softmax(s)_t * Vcode(t, kv, d) * VB(t, kv, d / 16)
  * code*B has at most six significant bits and enters the tensor cores as fp16 exactly;
  * accumulation is fp32.  A token's NaN reaches exactly the outputs that see the token (all of
- * a row for a NaN in K, the group's 16 dims for a NaN in V).  Everything else (group sizes, empty
- * sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
+ * a row for a NaN in K, the group's 16 dims for a NaN in V).  An n_kv that falls into more
+ * than 65535 equal groups of kv heads (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Everything else (group
+ * sizes, empty sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
  */
 KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
     void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,

@@ -178,3 +178,15 @@ def test_nan_and_bad_blocks_late_in_the_keys(n_q, n_kv, hd, bs, seqs, n, lo, hi)
     nan[:, n_q - group:, hd - 16:] |= ((last >= middle) & there[:, middle])[:, None, None]
     nan[:, :group] |= ((last >= top) & there[:, top])[:, None, None]
     assert np.array_equal(torch.isnan(out).cpu().numpy(), nan)
+
+
+def test_more_head_groups_than_the_grid_holds_are_refused():
+    """65537 kv heads, a prime: a group of CTAs for each."""
+    n_kv, bs, hd = 65537, 8, 64
+    c = torch.zeros(1, bs, n_kv, hd // 2, dtype=torch.uint8, device="cuda")
+    g = torch.zeros(1, n_kv, bs, hd // 16, dtype=torch.uint8, device="cuda")
+    q = torch.zeros(1, n_kv, hd, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(kv.KvFp8Error) as e:
+        kv.paged_decode_attention_fp4(q, c, c, g, g, dev(np.zeros((1, 1), np.int32)), dev(np.array([8], np.int32)))
+    assert e.value.status == kv.ERR_UNSUPPORTED
+    assert int(torch.ones(3, device="cuda").sum().item()) == 3  # and no error is left behind
