@@ -25,7 +25,7 @@ HEADER = os.path.join(ROOT, "include", "kvfp8.h")
 SOURCES = ["kvfp8_api.cu", "reshape_and_cache.cu", "paged_decode.cu", "paged_decode_mixed.cu",
            "prefill_attention.cu", "dequant.cu", "decode_noalloc.cu", "fp4_cache.cu",
            "paged_decode_fp4.cu", "block_copy.cu"]
-DEPS = ["kvfp8_device.cuh", "kvfp8_internal.h", "paged_decode_kernel.cuh"]
+DEPS = ["kvfp8_device.cuh", "kvfp8_e2m1.cuh", "kvfp8_internal.h", "paged_decode_kernel.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

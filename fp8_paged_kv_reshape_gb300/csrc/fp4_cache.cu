@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "kvfp8_device.cuh"
+#include "kvfp8_e2m1.cuh"
 #include "kvfp8_internal.h"
 
 namespace kvfp8 {

@@ -37,6 +37,7 @@
 // 64 and 128 sequences is 6.4 TB/s, so the rest is start, tail and combine); 8 sequences of 33k to 131k
 // tokens, 64 / 8 heads: 168 us (864 MB: 5.14 TB/s).  A warp's chain of 32 tokens takes ~1.5 us however few
 // run beside it, so one or two kv heads, with 6 consumer warps an SM, stay at 1.3 to 2 TB/s.
+#include "kvfp8_e2m1.cuh"
 #include "paged_decode_kernel.cuh"
 
 #include <type_traits>

@@ -35,6 +35,7 @@
 //        apply v_scale and store bf16.
 //  * All waits are bounded (mbarriers with a clock64 limit); a wait that runs out sets
 //    KVFP8_DEV_TIMEOUT.  Tensor memory is always released before the CTA exits.
+#include "kvfp8_e2m1.cuh"
 #include "paged_decode_kernel.cuh"
 
 namespace kvfp8 {
