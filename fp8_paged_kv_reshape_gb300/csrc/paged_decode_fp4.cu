@@ -18,7 +18,9 @@
 //    of a chunk is that order, for q too.  All 8 lie in one group of 16, so a lane needs one
 //    scale per row and chunk.
 //  * Weights are taken against a reference maximum that lags the running one (see below), so most
-//    chunks need no maximum over lanes and rescale nothing.
+//    chunks need no maximum over lanes and rescale nothing.  They are rounded to fp16 for the product with V,
+//    their sum is not: 11 bits, which moves outputs by 0.0004 of their norm (64 sequences of 4096; an
+//    output's rounding to bf16 0.0016), where a second fp16 part would double those products.
 //  * V (A operand, dims x tokens): ldmatrix.trans gives the 4 codes of dims 4g..4g+3 (g =
 //    lane / 4) of two tokens, and conversion leaves them as pairs of dims, where a product over
 //    tokens wants pairs of tokens.  Up to 8 score columns the product runs over (token, dim parity)

@@ -251,7 +251,8 @@ struct PrefillArgs {
 
 // Weights are taken against a reference 2^7 below the row's highest score at the time (the E4M3 forms:
 // that score), so they reach up to 2^15 and keep their 11 bits down to 2^-21 of the highest and are above
-// zero down to 2^-32, as in the decode kernel over the same cache (paged_decode_fp4.cu).
+// zero down to 2^-32, as in the decode kernel over the same cache (paged_decode_fp4.cu).  fp16 weights
+// move outputs by 0.0003 to 0.0006 of their norm, where rounding an output to bf16 moves it by 0.0016.
 constexpr float kF4Head = 7.f;
 
 // Conversion goes by units of 32 rows of 16 code bytes (8 keys x 4 chunks of 32 dims; 16 keys x 2 at

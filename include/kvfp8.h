@@ -442,11 +442,18 @@ KVFP8_API size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int3
  * kvfp8_paged_decode_attention over the 4-bit cache:
  *   s_t = sm_scale * k_scale * sum_d q[b][h][d] * Kcode(t, kv, d) * KB(t, kv, d / 16)
  *   out[b][h][d] = v_scale * sum_t softmax(s)_t * Vcode(t, kv, d) * VB(t, kv, d / 16)
- * code*B has at most six significant bits and enters the tensor cores as fp16 exactly;
- * accumulation is fp32.  A token's NaN reaches exactly the outputs that see the token (all of
- * a row for a NaN in K, the group's 16 dims for a NaN in V).  An n_kv that falls into more
- * than 65535 equal groups of kv heads (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Everything else (group
- * sizes, empty sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
+ * code*B has at most six significant bits and enters the tensor cores as fp16 exactly.  q
+ * enters as fp16: exactly from 2^-17 to 65504 (above, as for the 8-bit calls, it is outside the
+ * call's domain), below 2^-17 rounded to a multiple of 2^-24.  Scores, the exponential, the sum
+ * of the weights and the accumulation are fp32.  The weights enter the product with V as fp16,
+ * 2^7 to 2^15 at a row's highest score: 11 bits down to 2^-21 of the highest weight, multiples
+ * of 2^-24 below, none below 2^-32.  (This moves an output by about a quarter of what its own
+ * rounding to bf16 does.)  All of this holds for every query length and group size.
+ *
+ * A token's NaN reaches exactly the outputs that see the token (all of a row for a NaN in K, the
+ * group's 16 dims for a NaN in V).  An n_kv that falls into more than 65535 equal groups of kv
+ * heads (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Everything else (group sizes, empty
+ * sequences, bad blocks, errors) as kvfp8_paged_decode_attention.
  */
 KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
     void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,

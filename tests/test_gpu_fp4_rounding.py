@@ -113,3 +113,24 @@ def test_scores_rising_along_the_keys(n_q, n_kv, hd, n, seqs):
         # (2^-16 of float32 error in scores of up to 360 log2)
         near = np.where(ref > 2.0 ** -20, (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * ref, 2.0 ** -6 * ref + 2.0 ** -30)
         assert np.all(np.abs(got[0] - ref) <= near), step
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, n, seqs", ROUTES)
+def test_small_queries_are_multiples_of_2_to_the_minus_24(n_q, n_kv, hd, n, seqs):
+    """q of multiples of 2^-24 (here up to 2^-17) enters exactly; with a softmax scale that makes
+    scores of order 1 the outputs are those of the same q times 2^20, to the bit: every product, sum and scaled
+    score is a power of two apart."""
+    r = np.random.default_rng(n_q + hd)
+    bs, length = 16, 700
+    nb = -(-length // bs)
+    caches = [r.integers(0, 256, (nb, bs, 1, hd // 2)).astype(np.uint8) for _ in "kv"]
+    caches += [r.integers(0x28, 0x38, (nb, 1, bs, hd // 16)).astype(np.uint8) for _ in "kv"]
+    q = torch.from_numpy(r.integers(-128, 129, (seqs * n, n_q, hd)) * 2.0 ** -24).bfloat16().cuda()
+    args = [dev(a) for a in caches] + [dev(np.arange(nb, dtype=np.int32)[None].repeat(seqs, 0)),
+                                       dev(np.full(seqs, length, np.int32)), scalar(1.0), scalar(1.0)]
+    qsl = dev((np.arange(seqs + 1) * n).astype(np.int32))
+    small, large = (kv.paged_decode_attention_fp4(x, *args, sm) if n == 1 else
+                    kv.paged_attention_multi_fp4(x, qsl, n, *args, sm)
+                    for x, sm in ((q, 2.0 ** 14), (q * 2.0 ** 20, 2.0 ** -6)))
+    assert torch.equal(small, large) and bool(torch.isfinite(small).all())
+    assert len(torch.unique(small)) > 100
