@@ -672,7 +672,7 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
     if (!split_kv && !kvfp8::prefill_takes(n_q, n_kv, max_query_len, num_seqs)) return KVFP8_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
     if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
-    if (num_seqs == 0) return KVFP8_OK;
+    if (num_seqs == 0 || num_query_rows == 0) return KVFP8_OK;
     const size_t need = kvfp8_paged_attention_fp4_workspace_size(
         num_seqs, n_q, n_kv, head_dim, max_query_len, max_blocks_per_seq, block_size);
     if (!out || !query || !query_start_loc || !key_cache || !value_cache || !key_scales ||

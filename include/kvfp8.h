@@ -465,7 +465,7 @@ KVFP8_API kvfp8_status kvfp8_paged_decode_attention_fp4(
 
 /*
  * kvfp8_paged_attention_multi (causal, several new tokens per sequence, any chunk length) over
- * the 4-bit cache.
+ * the 4-bit cache.  Without query rows (num_query_rows 0) there is nothing to do: KVFP8_OK.
  */
 KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
     void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,

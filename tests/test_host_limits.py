@@ -34,3 +34,12 @@ def test_score_rows_past_32_bits(fp4, qmax, group, num_seqs, n_kv):
 @pytest.mark.parametrize("qmax, group, num_seqs, n_kv", [(1 << 20, 128, 1, 1), (512, 16, 64, 8), ((1 << 24) - 4, 128, 1, 1)])
 def test_large_chunks_below_that(fp4, qmax, group, num_seqs, n_kv):
     assert multi(fp4, qmax, group, num_seqs, n_kv) == binding.ERR_NULL
+
+
+def test_a_batch_without_new_tokens_has_nothing_to_do():
+    """No query rows: torch's empty tensors have null pointers."""
+    call = lambda rows, q: kv.LIB.kvfp8_paged_attention_multi_fp4(  # noqa: E731
+        q, q, P16, rows, 4, P16, P16, P16, P16, P16, 256, P16, 4, 32, 8, 128, 16, 1024, 0.0, None, None,
+        binding.F32, P16, 1 << 30, None, None)
+    assert call(0, None) == binding.OK
+    assert call(1, None) == binding.ERR_NULL
