@@ -72,7 +72,7 @@ def scale_values(scales: np.ndarray) -> np.ndarray:
 
 def code_values(codes: np.ndarray) -> np.ndarray:
     """uint8 [..., n] -> float64 [..., 2n]"""
-    c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
     return np.where(c >= 8, -E2M1[c & 7], E2M1[c & 7])
 
 

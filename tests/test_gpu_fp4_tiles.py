@@ -180,6 +180,27 @@ def test_nan_and_bad_blocks_late_in_the_keys(n_q, n_kv, hd, bs, seqs, n, lo, hi)
     assert np.array_equal(torch.isnan(out).cpu().numpy(), nan)
 
 
+@pytest.mark.parametrize("n_q, n_kv, hd, n, length, others", [
+    (4, 2, 64, 1, 90, 2), (32, 8, 128, 1, 5000, 2), (8, 2, 256, 3, 700, 1), (20, 1, 128, 1, 900, 1), (20, 1, 128, 1, 900, 90),
+    (8, 2, 256, 20, 900, 1), (4, 1, 64, 75, 900, 1), (4, 1, 128, 75, 900, 50)])
+def test_sequences_whose_blocks_are_all_outside_the_pool(n_q, n_kv, hd, n, length, others):
+    """Their rows are zero, and the other sequences are as without them."""
+    bs, seqs = 16, others + 2
+    r, lens, row, nb, bt, qsl = shared_case(n_kv, hd, bs, seqs, n, length, length, 3)
+    bt[0], bt[-1] = nb + 1, -1
+    kc, vc = (r.integers(0, 256, (nb, bs, n_kv, hd // 2)).astype(np.uint8) for _ in "kv")
+    kg, vg = (r.integers(0x28, 0x38, (nb, n_kv, bs, hd // 16)).astype(np.uint8) for _ in "kv")
+    q = torch.from_numpy(r.standard_normal((seqs * n, n_q, hd))).bfloat16()
+    st = status()
+    out = call(q, qsl, n, kc, vc, kg, vg, bt, lens, 0.05, 0.04, 0.0, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == kv.DEV_BAD_BLOCK
+    assert bool((out[:n] == 0).all()) and bool((out[-n:] == 0).all())
+    for s in {1, seqs - 2}:
+        rows = slice(s * n, (s + 1) * n)
+        check_attention(out[rows], (q[rows], np.array([0, n]), kc, vc, kg, vg, bt[s:s + 1]), [length], ks=0.05, vs=0.04)
+
+
 def test_more_head_groups_than_the_grid_holds_are_refused():
     """65537 kv heads, a prime: a group of CTAs for each."""
     n_kv, bs, hd = 65537, 8, 64

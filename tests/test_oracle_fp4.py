@@ -123,3 +123,12 @@ def test_page_moves():
     # used {3, 5, 7}: 3 -> 0, 5 -> 1, 7 -> 2
     assert new.tolist() == [[2, 0, -1], [2, 1, -1]]
     assert a[:, 0].tolist() == [3, 5, 7, 3, 4, 5, 6, 7]
+
+
+def test_attention_of_a_sequence_whose_blocks_are_all_outside():
+    r = np.random.default_rng(5)
+    kc, kg = r.integers(0, 256, (2, 8, 1, 32)).astype(np.uint8), r.integers(0, 0x40, (2, 1, 8, 4)).astype(np.uint8)
+    q = r.standard_normal((3, 2, 64))
+    bt = np.array([[-1, 2], [0, 1], [2, 1]], np.int32)
+    out, weight = fp4.attention(q, np.arange(4), kc, kc, kg, kg, bt, [16, 16, 8], 0.3, 0.5)
+    assert not out[0].any() and not weight[0].any() and out[1].any() and not out[2].any()
