@@ -239,10 +239,11 @@ struct PrefillArgs {
 
 // ---------------------------------------------------------------- the 4-bit cache
 //
-// F4: the cache holds E2M1 codes with an E4M3 scale byte per 16 dims instead of E4M3 bytes.  Only
-// what fills the f16 operands differs: a stage holds the codes of its keys (boxes of one head's
+// F4: the cache holds E2M1 codes with an E4M3 scale byte per 16 dims instead of E4M3 bytes.  What
+// fills the f16 operands differs: a stage holds the codes of its keys (boxes of one head's
 // head_dim/2-byte rows) and their scale bytes (contiguous per block and head), and the conversion
-// multiplies each fp16 pair of codes by its group's scale (exact: code * scale is an fp16 number).
+// multiplies each fp16 pair of codes by its group's scale (exact: code * scale is an fp16 number).  So
+// do the softmax weights' reference and rounding (kF4Head), and the split of the keys (kSplit).
 //
 // NaN: a scale byte 0x7F makes its 16 dims NaN.  In K that makes the key's scores NaN, which the
 // masks keep from rows that do not see it.  In V it would reach every row of the tile (0 * NaN), so
@@ -366,7 +367,6 @@ struct F4Unit {
 template <bool F4>
 __host__ __device__ constexpr int o_word(int w) { return F4 ? 4 * (w & 3) + (w >> 2) : w; }
 
-
 // The scale bytes of 64 keys from t0 on (K's at dst, V's side_bytes further), by all lanes of the
 // TMA warp: 16-byte asynchronous copies, each of 1 to 4 keys of one block, whose completion every lane
 // adds to the stage's barrier.  (As bulk copies they cost this warp one issue per block and side: 74
@@ -443,11 +443,12 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, 
 
 // Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
 // their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
-// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part is 128 keys at least (8 tokens on 1024, 32 / 8 heads of
-// 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing
-// is split when more than half the SMs have a row tile: 80 to 216 tiles gained at most 7 % from any number
-// of parts and lost up to 60 %.  (kSplit is an instance of its own: the few instructions cost the unsplit
-// kernel of two row tiles 11 %, 531 against 478 us for 512 new tokens of 16 sequences of 4096.)
+// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part
+// is 128 keys at least (8 tokens on 1024, 32 / 8 heads of 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with
+// parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing is split when more than half the SMs have
+// a row tile: 80 to 216 tiles of equal lengths gained at most 7 % from any number of parts and lost up to
+// 60 % (unequal ones were not measured).  (kSplit is an instance of its own: the few instructions cost the
+// unsplit kernel of two row tiles 11 %, 531 against 478 us for 512 new tokens of 16 sequences of 4096.)
 constexpr int kSplitSms = 152;
 constexpr int kMinPartKeys = 128;
 __host__ __device__ constexpr int split_parts(int splits, int key_tiles, int tile_keys) {
@@ -812,7 +813,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             if constexpr (F4 && L::kNS == 1) {
                 // one stage: the next copies start when this tile has been read, so their lines are brought
                 // into L2 meanwhile, as far as the window of block-table entries goes (head_dim 256, 32 tokens
-                // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128)
+                // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128; with all lines
+                // of the scale bytes 3 us less)
                 const KeyPlace box = next_tile_place(t, lbs);
                 const int next = __shfl_sync(0xFFFFFFFFu, win, (box.entry - wbase) & 31);
                 if (box_lane && t + kPfKeys < kend && box.entry - wbase < 32 && next >= 0 && next < a.num_blocks) {
