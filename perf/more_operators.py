@@ -14,7 +14,7 @@ positions, as cases that can be timed.
 Block-scaled format: E4M3 codes uint8 [blocks][block_size][n_kv][head_dim], and a float32 scale
 per block and kv head; an element is code * scale.  A write that holds a block's first token
 starts the block anew; any other write keeps its scale or raises it, and the block's older codes
-are then rounded to the new one.  A scale that a write makes is the smallest power of two (2^-100
+are then rounded to the new one.  A scale that a write makes is the smallest power of two (2^-60
 at least) that takes the largest finite element to 448 or less.
 """
 import math
@@ -234,10 +234,10 @@ def _encode(y):
 
 
 def _power(a):
-    """The smallest power of two, 2^-100 at least, with 448 times it not below a (float32)."""
+    """The smallest power of two, 2^-60 at least, with 448 times it not below a (float32)."""
     m, e = torch.frexp(a)
-    k = (e - 9 + (m > 0.875).int()).clamp(min=-100)
-    return ((torch.where(a > 0, k, -100) + 127) << 23).view(torch.float32)
+    k = (e - 9 + (m > 0.875).int()).clamp(min=-60)
+    return ((torch.where(a > 0, k, -60) + 127) << 23).view(torch.float32)
 
 
 def _values(codes, scales):
@@ -389,9 +389,9 @@ def _exact_written(x, slots, codes, scales):
     src, dst = torch.from_numpy(order).cuda(), torch.from_numpy(slots[order]).cuda()
     top = rows[src].abs().amax(-1)
     top = torch.zeros(len(first), n_kv, dtype=torch.float64, device="cuda").index_reduce_(0, group, top, "amax")
-    k = torch.full_like(top, -100.0)
-    for e in range(-100, 121):  # the smallest exponent that holds the largest element
-        k = torch.where(top > 448.0 * 2.0 ** (e - 1), max(e, -100), k)
+    k = torch.full_like(top, -60.0)
+    for e in range(-60, 121):  # the smallest exponent that holds the largest element
+        k = torch.where(top > 448.0 * 2.0 ** (e - 1), max(e, -60), k)
     old = torch.where(starts_anew[:, None], 0.0, scale[ids, :n_kv])
     new = torch.maximum(old, torch.exp2(k))
     grown = (new > old) & (old > 0)
