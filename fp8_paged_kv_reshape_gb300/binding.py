@@ -1,8 +1,9 @@
 """Thin Python binding over the kvfp8 C ABI (include/kvfp8.h).
 
 Argument marshalling only: every step of the path runs in libkvfp8.so's CUDA kernels.
-PyTorch supplies device memory and the current stream.  The calls of the 4-bit cache and of
-pages are marshalled by compiled code (csrc/torch_calls.cpp), the others here.  There is no CPU
+PyTorch supplies device memory and the current stream.  The calls of the 4-bit cache, of the cache
+with block scales, of rotary positions and of pages are marshalled by compiled code
+(csrc/torch_calls.cpp), the others here.  There is no CPU
 or eager fallback: importing this module raises if the library is missing, and those calls raise if
 the compiled code is (it is built against one torch, the library against none).
 """
@@ -12,6 +13,7 @@ import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 
 import torch
@@ -50,6 +52,13 @@ ABI_FUNCTIONS = (
     "kvfp8_paged_attention_fp4_workspace_size",
     "kvfp8_paged_decode_attention_fp4",
     "kvfp8_paged_attention_multi_fp4",
+    "kvfp8_reshape_and_cache_block_scaled_workspace_size",
+    "kvfp8_reshape_and_cache_block_scaled",
+    "kvfp8_dequant_block_scaled",
+    "kvfp8_paged_attention_block_scaled_workspace_size",
+    "kvfp8_paged_decode_attention_block_scaled",
+    "kvfp8_paged_attention_multi_block_scaled",
+    "kvfp8_rotary_embedding",
     "kvfp8_copy_blocks",
     "kvfp8_compact_blocks_workspace_size",
     "kvfp8_compact_blocks",
@@ -125,6 +134,26 @@ def _load() -> ctypes.CDLL:
                                                     i32, i32, i32, i32, i32, f32, P, P,
                                                     ctypes.c_int, P, sz, P, P]
     lib.kvfp8_paged_attention_multi_fp4.restype = ctypes.c_int
+    lib.kvfp8_reshape_and_cache_block_scaled_workspace_size.argtypes = [i64, i32, i32]
+    lib.kvfp8_reshape_and_cache_block_scaled_workspace_size.restype = sz
+    lib.kvfp8_reshape_and_cache_block_scaled.argtypes = [P, P, ctypes.c_int, i64, i64, i64, P, P, P, P,
+                                                         i32, i32, i32, i32, i32, P, P, sz, P, P]
+    lib.kvfp8_reshape_and_cache_block_scaled.restype = ctypes.c_int
+    lib.kvfp8_dequant_block_scaled.argtypes = [P, ctypes.c_int, P, P, i32, i32, i32, i32, i32, P, i64, P,
+                                               P]
+    lib.kvfp8_dequant_block_scaled.restype = ctypes.c_int
+    lib.kvfp8_paged_attention_block_scaled_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.kvfp8_paged_attention_block_scaled_workspace_size.restype = sz
+    lib.kvfp8_paged_decode_attention_block_scaled.argtypes = [P, P, P, P, P, P, i32, P, i32, P, i32, i32,
+                                                              i32, i32, i32, i32, f32, P, sz, P, P]
+    lib.kvfp8_paged_decode_attention_block_scaled.restype = ctypes.c_int
+    lib.kvfp8_paged_attention_multi_block_scaled.argtypes = [P, P, P, i32, i32, i32, P, P, P, P, i32, P,
+                                                             i32, P, i32, i32, i32, i32, i32, i32, f32, P,
+                                                             sz, P, P]
+    lib.kvfp8_paged_attention_multi_block_scaled.restype = ctypes.c_int
+    lib.kvfp8_rotary_embedding.argtypes = [P, P, i64, i64, P, P, i64, i64, ctypes.c_int, i64, i32, i32,
+                                           i32, i32, i32, i32, P, P, f32, P, P]
+    lib.kvfp8_rotary_embedding.restype = ctypes.c_int
     lib.kvfp8_copy_blocks.argtypes = [P, P, i32, i32, P, P, i64, P, P]
     lib.kvfp8_copy_blocks.restype = ctypes.c_int
     lib.kvfp8_compact_blocks_workspace_size.argtypes = [i32]
@@ -517,7 +546,7 @@ def dequant(src: torch.Tensor, dst_dtype: torch.dtype = torch.float32,
     return out
 
 
-# ---------------------------------------------------------------- 4-bit cache, pages
+# ---------------------------------------------------------------- compiled calls
 
 def _load_calls():
     """The compiled wrappers; they call the same loaded libkvfp8.so."""
@@ -619,6 +648,135 @@ def paged_attention_multi_fp4(query: torch.Tensor, query_start_loc: torch.Tensor
         return _CALLS.paged_attention_multi_fp4(query, query_start_loc, max_query_len, key_cache, value_cache,
                                                 key_scales, value_scales, block_tables, seq_lens, k_scale, v_scale,
                                                 sm_scale, out, workspace, status)
+
+
+def block_scales(num_blocks: int, n_kv: int, device="cuda") -> torch.Tensor:
+    """The scales of one side of a pool with block scales, none of its blocks written yet: float32
+    zeros [num_blocks, n_kv rounded up to a multiple of 4]."""
+    return torch.zeros(num_blocks, -(-n_kv // 4) * 4, dtype=torch.float32, device=device)
+
+
+def reshape_and_cache_block_scaled_workspace_size(num_tokens: int, num_blocks: int, block_size: int) -> int:
+    return LIB.kvfp8_reshape_and_cache_block_scaled_workspace_size(num_tokens, num_blocks, block_size)
+
+
+def reshape_and_cache_block_scaled(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
+                                   value_cache: torch.Tensor, key_scales: torch.Tensor,
+                                   value_scales: torch.Tensor, slot_mapping: torch.Tensor,
+                                   workspace: torch.Tensor | None = None,
+                                   status: torch.Tensor | None = None, stream=None) -> None:
+    """kvfp8_reshape_and_cache_block_scaled: rows into the FP8 cache with block scales, which are made here.
+
+    key/value as for reshape_and_cache; caches uint8 [num_blocks, block_size, n_kv, head_dim], block
+    sizes from 16; scales as block_scales() makes them.  A call that writes a block's first token starts
+    the block anew; others keep its scales or raise them, and round its older codes to the new ones.
+    """
+    with _on(stream):
+        _CALLS.reshape_and_cache_block_scaled(key, value, key_cache, value_cache, key_scales, value_scales,
+                                              slot_mapping, workspace, status)
+
+
+def dequant_block_scaled(cache: torch.Tensor, scales: torch.Tensor, slot_mapping: torch.Tensor,
+                         dst_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvfp8_dequant_block_scaled: the rows of one side of a cache with block scales at slot_mapping's
+    slots, as bfloat16 or float32 [num_tokens, n_kv, head_dim] (slot -1: a zero row)."""
+    if dst_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dst_dtype must be float32 or bfloat16")
+    with _on(stream):
+        return _CALLS.dequant_block_scaled(cache, scales, slot_mapping, dst_dtype == torch.bfloat16, out, status)
+
+
+def paged_attention_block_scaled_workspace_size(num_seqs: int, n_q: int, n_kv: int, head_dim: int,
+                                                max_query_len: int, max_blocks_per_seq: int,
+                                                block_size: int) -> int:
+    """Workspace bytes of paged_decode_attention_block_scaled (max_query_len 1) and
+    paged_attention_multi_block_scaled."""
+    return LIB.kvfp8_paged_attention_block_scaled_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
+                                                                 max_blocks_per_seq, block_size)
+
+
+def paged_decode_attention_block_scaled(query: torch.Tensor, key_cache: torch.Tensor,
+                                        value_cache: torch.Tensor, key_scales: torch.Tensor,
+                                        value_scales: torch.Tensor, block_tables: torch.Tensor,
+                                        seq_lens: torch.Tensor, sm_scale: float = 0.0,
+                                        out: torch.Tensor | None = None,
+                                        workspace: torch.Tensor | None = None,
+                                        status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvfp8_paged_decode_attention_block_scaled: paged_decode_attention over a cache with block scales;
+    returns out (bf16 [num_seqs, n_q, head_dim])."""
+    with _on(stream):
+        return _CALLS.paged_decode_attention_block_scaled(query, key_cache, value_cache, key_scales, value_scales,
+                                                          block_tables, seq_lens, sm_scale, out, workspace, status)
+
+
+def paged_attention_multi_block_scaled(query: torch.Tensor, query_start_loc: torch.Tensor,
+                                       max_query_len: int, key_cache: torch.Tensor,
+                                       value_cache: torch.Tensor, key_scales: torch.Tensor,
+                                       value_scales: torch.Tensor, block_tables: torch.Tensor,
+                                       seq_lens: torch.Tensor, causal: bool = True,
+                                       sm_scale: float = 0.0, out: torch.Tensor | None = None,
+                                       workspace: torch.Tensor | None = None,
+                                       status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kvfp8_paged_attention_multi_block_scaled: several query tokens per sequence over a cache with block
+    scales; causal (the queries are the sequence's last tokens) or not (every query sees every cached
+    token of its sequence: cross attention to an encoder's states)."""
+    with _on(stream):
+        return _CALLS.paged_attention_multi_block_scaled(query, query_start_loc, max_query_len, key_cache,
+                                                         value_cache, key_scales, value_scales, block_tables,
+                                                         seq_lens, causal, sm_scale, out, workspace, status)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original_len: int = 0, low_turns: float = 1.0, high_turns: float = 32.0,
+                       device="cuda"):
+    """(frequencies, magnitude) for rotary_embedding: float64 [rot_dim / 2], radians a position, and what the
+    rotated values are multiplied by.
+
+    Unscaled, f_j = base^(-2j / rot_dim).  For contexts `factor` times as long as trained on:
+      "linear"  f_j / factor (positions interpolated)
+      "base"    base * factor^(rot_dim / (rot_dim - 2)) in base's place: the slowest pair turns `factor`
+                times slower, the fastest as before
+      "parts"   by the turns that a pair makes in original_len positions, n_j = original_len * f_j / 2 pi: kept
+                from high_turns on, f_j / factor up to low_turns, in between k f_j + (1 - k) f_j / factor with
+                k = (n_j - low_turns) / (high_turns - low_turns); magnitude 0.1 ln(factor) + 1
+    """
+    if rot_dim < 2 or rot_dim % 2 != 0:
+        raise ValueError("rot_dim must be even and positive")
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive and finite")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError('scaling must be None, "linear", "base" or "parts"')
+    if scaling == "base" and rot_dim > 2:
+        base *= factor ** (rot_dim / (rot_dim - 2))
+    f = [base ** (-2 * j / rot_dim) for j in range(rot_dim // 2)]
+    magnitude = 1.0
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "parts":
+        if original_len < 1 or not low_turns < high_turns:
+            raise ValueError('"parts" needs original_len and low_turns < high_turns')
+        keep = [min(1.0, max(0.0, (original_len * x / (2 * math.pi) - low_turns) / (high_turns - low_turns))) for x in f]
+        f = [x * k + x / factor * (1 - k) for x, k in zip(f, keep)]
+        magnitude = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(f, dtype=torch.float64, device=device), magnitude
+
+
+def rotary_embedding(query: torch.Tensor, key: torch.Tensor | None, positions: torch.Tensor,
+                     frequencies: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0,
+                     transpose: bool = False, query_out: torch.Tensor | None = None,
+                     key_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """kvfp8_rotary_embedding: (query, key) with their heads rotated by positions; key may be None.
+
+    query [num_tokens, n_q, head_dim], key [num_tokens, n_k, head_dim] (bfloat16 or float32, slices of a
+    fused row allowed); positions int64 [num_tokens]; frequencies float64 [rot_dim / 2] (rotary_frequencies
+    makes them), rot_dim a multiple of 16 up to head_dim.  Pairs are dims (j, j + rot_dim / 2), or (2j, 2j + 1)
+    when interleaved.  transpose: turned back (the gradient; at magnitude 1 the inverse).  An output may be
+    its own input.
+    """
+    with _on(stream):
+        return _CALLS.rotary_embedding(query, key, positions, frequencies, interleaved, magnitude, transpose,
+                                       query_out, key_out, status)
 
 
 def copy_blocks(caches, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,

@@ -39,6 +39,23 @@ kvfp8_status check_fp4_cache(int32_t num_blocks, int32_t block_size, int32_t n_k
     return KVFP8_OK;
 }
 
+// the shape rules of the FP8 cache with block scales, shared by its entry points
+kvfp8_status check_block_cache(int32_t num_blocks, int32_t block_size, int32_t n_kv, int32_t head_dim,
+                               int32_t scale_stride) {
+    if (num_blocks < 1 || n_kv < 1 || !block_size_ok_for_decode(block_size) || block_size < 16 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256) || scale_stride < n_kv || scale_stride % 4 != 0)
+        return KVFP8_ERR_SHAPE;
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7FFFFFFFLL || static_cast<int64_t>(n_kv) * head_dim > (1 << 20))
+        return KVFP8_ERR_SHAPE;
+    return KVFP8_OK;
+}
+
+int32_t log2_of(int32_t x) {  // of a power of two
+    int32_t n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
 // the cache list of the page calls: KVFP8_OK with *out filled, or what is wrong with it
 kvfp8_status make_cache_list(void *const *caches, const int64_t *block_bytes, int32_t num_caches,
                              int32_t num_blocks, kvfp8::CacheList *out) {
@@ -598,9 +615,9 @@ size_t kvfp8_paged_attention_fp4_workspace_size(int32_t num_seqs, int32_t n_q, i
         block_size < 1)
         return 0;
     if (!kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len))
-        return kvfp8::fp4_prefill_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
+        return kvfp8::split_prefill_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len,
                                                  static_cast<int64_t>(max_blocks_per_seq) * block_size);
-    if (kvfp8::fp4_takes_sequences_whole(max_blocks_per_seq, block_size)) return 0;
+    if (kvfp8::decode_takes_sequences_whole(max_blocks_per_seq, block_size)) return 0;
     return kvfp8_paged_attention_multi_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len);
 }
 
@@ -712,6 +729,245 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
     d.k_bf16 = 0;
     d.v_bf16 = 0;
     return from_cuda(kvfp8::launch_paged_decode_fp4(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvfp8_reshape_and_cache_block_scaled_workspace_size(int64_t num_tokens, int32_t num_blocks,
+                                                           int32_t block_size) {
+    if (num_blocks < 1 || block_size < 1 || !kvfp8::block_write_needs_rows(num_tokens)) return 0;
+    return static_cast<size_t>(num_blocks) * static_cast<size_t>(block_size) * sizeof(int32_t);
+}
+
+kvfp8_status kvfp8_reshape_and_cache_block_scaled(
+    const void *key, const void *value, kvfp8_dtype src_dtype, int64_t key_stride,
+    int64_t value_stride, int64_t num_tokens, uint8_t *key_cache, uint8_t *value_cache,
+    float *key_scales, float *value_scales, int32_t scale_stride, int32_t num_blocks,
+    int32_t block_size, int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping,
+    void *workspace, size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(src_dtype)) return KVFP8_ERR_DTYPE;
+    if (num_tokens < 0 || num_tokens > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_block_cache(num_blocks, block_size, n_kv, head_dim, scale_stride);
+    if (sh != KVFP8_OK) return sh;
+    const int64_t row = static_cast<int64_t>(n_kv) * head_dim;
+    if (key_stride < row || value_stride < row) return KVFP8_ERR_SHAPE;
+    if (num_tokens == 0) return KVFP8_OK;
+    const size_t need = kvfp8_reshape_and_cache_block_scaled_workspace_size(num_tokens, num_blocks, block_size);
+    if (!key || !value || !key_cache || !value_cache || !key_scales || !value_scales || !slot_mapping ||
+        (need > 0 && !workspace))
+        return KVFP8_ERR_NULL;
+    const int64_t esz = src_dtype == KVFP8_F32 ? 4 : 2;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        !aligned16(key_scales) || !aligned16(value_scales) || !aligned(slot_mapping, 8) ||
+        (need > 0 && !aligned16(workspace)) || key_stride * esz % 16 != 0 || value_stride * esz % 16 != 0)
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes < need) return KVFP8_ERR_WORKSPACE;
+    kvfp8::BlockWriteArgs a;
+    a.src[0] = key;
+    a.src[1] = value;
+    a.stride[0] = key_stride;
+    a.stride[1] = value_stride;
+    a.codes[0] = key_cache;
+    a.codes[1] = value_cache;
+    a.scales[0] = key_scales;
+    a.scales[1] = value_scales;
+    a.scale_stride = scale_stride;
+    a.src_dtype = src_dtype;
+    a.num_tokens = num_tokens;
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.block_shift = log2_of(block_size);
+    a.n_kv = n_kv;
+    a.head_dim = head_dim;
+    a.slot_mapping = slot_mapping;
+    a.row_of = need > 0 ? static_cast<int32_t *>(workspace) : nullptr;
+    a.status = status;
+    return from_cuda(kvfp8::launch_reshape_and_cache_block_scaled(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_dequant_block_scaled(void *dst, kvfp8_dtype dst_dtype, const uint8_t *codes, const float *scales,
+                                        int32_t scale_stride, int32_t num_blocks, int32_t block_size,
+                                        int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping,
+                                        int64_t num_tokens, uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(dst_dtype)) return KVFP8_ERR_DTYPE;
+    if (num_tokens < 0) return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_block_cache(num_blocks, block_size, n_kv, head_dim, scale_stride);
+    if (sh != KVFP8_OK) return sh;
+    if (num_tokens == 0) return KVFP8_OK;
+    if (!dst || !codes || !scales || !slot_mapping) return KVFP8_ERR_NULL;
+    if (!aligned16(dst) || !aligned16(codes) || !aligned16(scales) || !aligned(slot_mapping, 8))
+        return KVFP8_ERR_ALIGN;
+    kvfp8::BlockReadArgs a;
+    a.dst = dst;
+    a.dst_dtype = dst_dtype;
+    a.codes = codes;
+    a.scales = scales;
+    a.scale_stride = scale_stride;
+    a.num_tokens = num_tokens;
+    a.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+    a.block_shift = log2_of(block_size);
+    a.n_kv = n_kv;
+    a.head_dim = head_dim;
+    a.head_shift = log2_of(head_dim / 16);
+    a.slot_mapping = slot_mapping;
+    a.status = status;
+    return from_cuda(kvfp8::launch_dequant_block_scaled(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv,
+                                                         int32_t head_dim, int32_t max_query_len,
+                                                         int32_t max_blocks_per_seq, int32_t block_size) {
+    // (work is split as over the 4-bit cache)
+    return kvfp8_paged_attention_fp4_workspace_size(num_seqs, n_q, n_kv, head_dim, max_query_len, max_blocks_per_seq,
+                                                    block_size);
+}
+
+kvfp8_status kvfp8_paged_decode_attention_block_scaled(
+    void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
+    const float *key_scales, const float *value_scales, int32_t scale_stride,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, float sm_scale, void *workspace, size_t workspace_bytes, uint32_t *status,
+    kvfp8_stream_t stream) {
+    bool nothing_to_do = false;
+    const kvfp8_status v = kvfp8::validate_decode(
+        out, query, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs,
+        n_q, n_kv, head_dim, block_size, num_blocks, sm_scale, KVFP8_F32, &nothing_to_do);
+    if (v != KVFP8_OK) return v;
+    const kvfp8_status sh = check_block_cache(num_blocks, block_size, n_kv, head_dim, scale_stride);
+    if (sh != KVFP8_OK || nothing_to_do) return sh;
+    const size_t need = kvfp8_paged_attention_block_scaled_workspace_size(num_seqs, n_q, n_kv, head_dim, 1,
+                                                                          max_blocks_per_seq, block_size);
+    if (!key_scales || !value_scales || (need > 0 && !workspace)) return KVFP8_ERR_NULL;
+    if (!aligned16(key_scales) || !aligned16(value_scales) || (need > 0 && !aligned16(workspace)))
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes < need) return KVFP8_ERR_WORKSPACE;
+    kvfp8::DecodeArgs d = {};
+    d.out = out;
+    d.query = query;
+    d.key_cache = key_cache;
+    d.value_cache = value_cache;
+    d.key_block_scales = key_scales;
+    d.value_block_scales = value_scales;
+    d.block_scale_stride = scale_stride;
+    d.block_tables = block_tables;
+    d.max_blocks_per_seq = max_blocks_per_seq;
+    d.seq_lens = seq_lens;
+    d.num_seqs = num_seqs;
+    d.n_q = n_q;
+    d.n_kv = n_kv;
+    d.head_dim = head_dim;
+    d.block_size = block_size;
+    d.num_blocks = num_blocks;
+    d.sm_scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+    d.scale_dtype = KVFP8_F32;
+    d.workspace = workspace;
+    d.status = status;
+    d.qmax = 1;
+    d.qrows = num_seqs;
+    return from_cuda(kvfp8::launch_paged_decode_block_scaled(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_paged_attention_multi_block_scaled(
+    void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,
+    int32_t max_query_len, int32_t causal, const uint8_t *key_cache, const uint8_t *value_cache,
+    const float *key_scales, const float *value_scales, int32_t scale_stride,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, float sm_scale, void *workspace, size_t workspace_bytes, uint32_t *status,
+    kvfp8_stream_t stream) {
+    if (num_seqs < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || max_query_len < 1 ||
+        num_query_rows < 0 || max_blocks_per_seq < 1)
+        return KVFP8_ERR_SHAPE;
+    const kvfp8_status sh = check_block_cache(num_blocks, block_size, n_kv, head_dim, scale_stride);
+    if (sh != KVFP8_OK) return sh;
+    const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
+    if (!split_kv && !kvfp8::prefill_takes(n_q, n_kv, max_query_len, num_seqs)) return KVFP8_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
+    if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
+    if (num_seqs == 0 || num_query_rows == 0) return KVFP8_OK;
+    const size_t need = kvfp8_paged_attention_block_scaled_workspace_size(
+        num_seqs, n_q, n_kv, head_dim, max_query_len, max_blocks_per_seq, block_size);
+    if (!out || !query || !query_start_loc || !key_cache || !value_cache || !key_scales ||
+        !value_scales || !block_tables || !seq_lens || (need > 0 && !workspace))
+        return KVFP8_ERR_NULL;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) ||
+        !aligned16(value_cache) || !aligned16(key_scales) || !aligned16(value_scales) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) ||
+        (need > 0 && !aligned16(workspace)))
+        return KVFP8_ERR_ALIGN;
+    if (workspace_bytes < need) return KVFP8_ERR_WORKSPACE;
+    kvfp8::DecodeArgs d = {};
+    d.out = out;
+    d.query = query;
+    d.key_cache = key_cache;
+    d.value_cache = value_cache;
+    d.key_block_scales = key_scales;
+    d.value_block_scales = value_scales;
+    d.block_scale_stride = scale_stride;
+    d.causal = causal != 0;
+    d.block_tables = block_tables;
+    d.max_blocks_per_seq = max_blocks_per_seq;
+    d.seq_lens = seq_lens;
+    d.num_seqs = num_seqs;
+    d.n_q = n_q;
+    d.n_kv = n_kv;
+    d.head_dim = head_dim;
+    d.block_size = block_size;
+    d.num_blocks = num_blocks;
+    d.sm_scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+    d.scale_dtype = KVFP8_F32;
+    d.workspace = workspace;
+    d.status = status;
+    d.qsl = query_start_loc;
+    d.qmax = max_query_len;
+    d.qrows = num_query_rows;
+    return from_cuda(kvfp8::launch_paged_decode_block_scaled(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvfp8_status kvfp8_rotary_embedding(void *query_out, void *key_out, int64_t query_out_stride,
+                                    int64_t key_out_stride, const void *query, const void *key,
+                                    int64_t query_stride, int64_t key_stride, kvfp8_dtype dtype,
+                                    int64_t num_tokens, int32_t n_q, int32_t n_k, int32_t head_dim,
+                                    int32_t rot_dim, int32_t interleaved, int32_t transpose,
+                                    const int64_t *positions, const double *frequencies,
+                                    float magnitude, uint32_t *status, kvfp8_stream_t stream) {
+    if (!dtype_ok(dtype)) return KVFP8_ERR_DTYPE;
+    if (num_tokens < 0 || num_tokens > 0x7FFFFFFFLL || n_q < 1 || n_k < 0 || head_dim < 16 || head_dim > 256 ||
+        head_dim % 8 != 0 || rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0 ||
+        static_cast<int64_t>(n_q) * head_dim > (1 << 20) || static_cast<int64_t>(n_k) * head_dim > (1 << 20))
+        return KVFP8_ERR_SHAPE;
+    const int64_t q_row = static_cast<int64_t>(n_q) * head_dim, k_row = static_cast<int64_t>(n_k) * head_dim;
+    if (query_stride < q_row || query_out_stride < q_row || (n_k > 0 && (key_stride < k_row || key_out_stride < k_row)))
+        return KVFP8_ERR_SHAPE;
+    if (!std::isfinite(magnitude)) return KVFP8_ERR_SCALE;
+    if (num_tokens == 0) return KVFP8_OK;
+    if (!query_out || !query || (n_k > 0 && (!key_out || !key)) || !positions || !frequencies) return KVFP8_ERR_NULL;
+    const int64_t esz = dtype == KVFP8_F32 ? 4 : 2;
+    if (!aligned16(query_out) || !aligned16(query) || !aligned(positions, 8) || !aligned(frequencies, 8) ||
+        query_stride * esz % 16 != 0 || query_out_stride * esz % 16 != 0 ||
+        (n_k > 0 && (!aligned16(key_out) || !aligned16(key) || key_stride * esz % 16 != 0 ||
+                     key_out_stride * esz % 16 != 0)))
+        return KVFP8_ERR_ALIGN;
+    kvfp8::RotaryArgs a;
+    a.src[0] = query;
+    a.src[1] = key;
+    a.dst[0] = query_out;
+    a.dst[1] = key_out;
+    a.stride[0] = query_stride;
+    a.stride[1] = key_stride;
+    a.dst_stride[0] = query_out_stride;
+    a.dst_stride[1] = key_out_stride;
+    a.heads[0] = n_q;
+    a.heads[1] = n_k;
+    a.dtype = dtype;
+    a.num_tokens = num_tokens;
+    a.head_dim = head_dim;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.positions = positions;
+    a.frequencies = frequencies;
+    a.magnitude = magnitude;
+    a.sin_magnitude = transpose ? -magnitude : magnitude;
+    a.status = status;
+    return from_cuda(kvfp8::launch_rotary(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvfp8_status kvfp8_copy_blocks(void *const *caches, const int64_t *block_bytes, int32_t num_caches,

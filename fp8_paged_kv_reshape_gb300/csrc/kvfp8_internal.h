@@ -157,6 +157,12 @@ struct DecodeArgs {
     // 4-bit cache (both sides): the groups' scale bytes; nullptr for the other formats
     const uint8_t *key_scales = nullptr;
     const uint8_t *value_scales = nullptr;
+    // FP8 cache with a scale per block and kv head (both sides): [block][block_scale_stride]; nullptr for
+    // the other formats, which are always causal
+    const float *key_block_scales = nullptr;
+    const float *value_block_scales = nullptr;
+    int32_t block_scale_stride = 0;
+    int32_t causal = 1;
 };
 
 // Workspace layout, shared by the size query and the launcher; rows = query rows per
@@ -178,14 +184,16 @@ bool mixed_uses_decode_kernel(int32_t n_q, int32_t n_kv, int32_t head_dim, int32
 // The split-KV kernel over the 4-bit cache (key_scales / value_scales set), for shapes
 // multi_uses_decode_kernel accepts; longer query chunks take launch_prefill_attention.
 cudaError_t launch_paged_decode_fp4(const DecodeArgs &a, cudaStream_t stream);
-// True when that kernel splits no sequence of tables this wide, and so needs no workspace.
-bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
+// The same over the FP8 cache with block scales (key_block_scales / value_block_scales set).
+cudaError_t launch_paged_decode_block_scaled(const DecodeArgs &a, cudaStream_t stream);
+// True when these two split no sequence of tables this wide, and so need no workspace.
+bool decode_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
 
 // Multi-query (causal) attention on the tensor cores (tcgen05): long query chunks, or kv-head
-// counts the split-KV decode kernel does not cover.  Needs no workspace, but over a 4-bit cache
-// (key_scales set) the one below where few row tiles have their keys split.
+// counts the split-KV decode kernel does not cover.  Needs no workspace, but over a 4-bit cache or one
+// with block scales the one below where few row tiles have their keys split.
 cudaError_t launch_prefill_attention(const DecodeArgs &a, cudaStream_t stream);
-size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+size_t split_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
                                   int64_t max_len);
 // True when its grid and its 32-bit row numbers hold this many score rows (host arithmetic).
 bool prefill_takes(int32_t n_q, int32_t n_kv, int32_t max_query_len, int32_t num_seqs);
@@ -240,6 +248,53 @@ struct Fp4ReadArgs {
     uint32_t *status;
 };
 cudaError_t launch_dequant_fp4(const Fp4ReadArgs &a, cudaStream_t stream);
+
+// The writer of the FP8 cache with block scales and its rows read back by slot.
+struct BlockWriteArgs {
+    const void *src[2];      // K, V
+    int64_t stride[2];       // elements
+    uint8_t *codes[2];
+    float *scales[2];        // [block][scale_stride]
+    int32_t scale_stride;
+    int src_dtype;
+    int64_t num_tokens, num_slots;
+    int32_t block_shift, n_kv, head_dim;  // blocks of 1 << block_shift tokens
+    const int64_t *slot_mapping;
+    int32_t *row_of;         // [num_slots], any contents; nullptr where block_write_needs_rows is false
+    uint32_t *status;
+};
+cudaError_t launch_reshape_and_cache_block_scaled(const BlockWriteArgs &a, cudaStream_t stream);
+// True when a call of this many rows finds a block's rows through a workspace.
+bool block_write_needs_rows(int64_t num_tokens);
+
+struct BlockReadArgs {
+    void *dst;
+    int dst_dtype;
+    const uint8_t *codes;
+    const float *scales;
+    int32_t scale_stride;
+    int64_t num_tokens, num_slots;
+    int32_t block_shift, n_kv, head_dim, head_shift;  // head_dim = 16 << head_shift
+    const int64_t *slot_mapping;
+    uint32_t *status;
+};
+cudaError_t launch_dequant_block_scaled(const BlockReadArgs &a, cudaStream_t stream);
+
+// Rotary positions on the heads of q and of k (heads[1] may be 0).
+struct RotaryArgs {
+    const void *src[2];
+    void *dst[2];
+    int64_t stride[2], dst_stride[2];  // of a token, elements
+    int32_t heads[2];
+    int dtype;
+    int64_t num_tokens;
+    int32_t head_dim, rot, interleaved;
+    const int64_t *positions;
+    const double *frequencies;  // [rot / 2], radians a position
+    float magnitude, sin_magnitude;  // of the cosines and of the sines (negative: turned back)
+    uint32_t *status;
+};
+cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream);
 
 // Page copies: the caches' device pointers and block sizes travel as a kernel parameter.
 struct CacheList {

@@ -40,7 +40,7 @@
 // tokens, 64 / 8 heads: 168 us (864 MB: 5.14 TB/s).  A warp's chain of 32 tokens takes ~1.5 us however few
 // run beside it, so one or two kv heads, with 6 consumer warps an SM, stay at 1.3 to 2 TB/s.
 #include "kvfp8_e2m1.cuh"
-#include "paged_decode_kernel.cuh"
+#include "paged_decode_own_plan.cuh"
 
 #include <type_traits>
 
@@ -132,86 +132,6 @@ __device__ __forceinline__ uint32_t chunk_scale(const uint32_t (&bytes)[N], int 
     return c & 1 ? bcast_hi(two) : bcast_lo(two);
 }
 
-// Batches of up to kOwnPlanSeqs sequences take no plan kernel: each CTA's producer warp reads the
-// lengths and works out its CTA's range with a warp scan, while the other warps set up (64 sequences:
-// one launch and ~3 us less than the plan kernel in front).  CTA 0 leaves the chunk prefix for the
-// combine kernel.  Where no sequence can be longer than kWholeTokens (the width of the block tables
-// says so) nothing is split: one CTA per sequence and head group, no partial results, no workspace
-// and no combine kernel (num_ctas = 0; four sequences of up to 100 tokens: 10.3 to 8.3 us).
-constexpr int kOwnPlanSeqs = 256;
-constexpr int kWholeTokens = 256;
-
-__device__ __forceinline__ CtaPlan own_plan(const KernelArgs &a, int lane) {
-    if (a.num_ctas == 0) {  // short sequences: CTA s takes sequence s whole
-        CtaPlan p = {0, 0, static_cast<int32_t>(blockIdx.x), 0, 0, 0, 0, 0};
-        p.hi = p.ce = seq_chunks<kTok>(a, p.s, p.L);
-        return p;
-    }
-    constexpr int kRounds = kOwnPlanSeqs / 32;
-    int n[kRounds];  // chunks of sequence 32 r + lane
-    int sum = 0, L = 0;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int i = 32 * r + lane;
-        n[r] = i < a.num_seqs ? seq_chunks<kTok>(a, i, L) : 0;
-        sum += n[r];
-    }
-    const int T = __reduce_add_sync(0xFFFFFFFFu, sum);
-    const int P = min(T, a.num_ctas), c = blockIdx.x;
-    CtaPlan p = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < P) {
-        p.lo = static_cast<int32_t>(static_cast<int64_t>(c) * T / P);
-        p.hi = static_cast<int32_t>(static_cast<int64_t>(c + 1) * T / P);
-    }
-    const bool write = c == 0 && blockIdx.y == 0;
-    int32_t *cstart = const_cast<int32_t *>(a.cstart);
-    int run = 0;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        if (32 * r < a.num_seqs) {
-            int x = n[r];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
-            }
-            const int before = run + x - n[r];
-            if (write && 32 * r + lane < a.num_seqs) cstart[32 * r + lane] = before;
-            const unsigned here = __ballot_sync(0xFFFFFFFFu, before <= p.lo && p.lo < before + n[r]);
-            if (here != 0u) {
-                const int from = __ffs(here) - 1;
-                p.s = 32 * r + from;
-                p.cs = __shfl_sync(0xFFFFFFFFu, before, from);
-                p.ce = p.cs + __shfl_sync(0xFFFFFFFFu, n[r], from);
-            }
-            run += __shfl_sync(0xFFFFFFFFu, x, 31);
-        }
-    }
-    if (write && lane == 0) cstart[a.num_seqs] = T;
-    p.L = min(max(a.seq_lens[p.s], 0), a.max_len);
-    return p;
-}
-
-// The plan kernel's other duties, by the producer warps once their copies are issued: the rows of
-// sequences without chunks are zeroed, errors of lengths and query rows flagged.
-template <int HD>
-__device__ __forceinline__ void finish_plan(const KernelArgs &a, int lane) {
-    const int qmax = a.rows_per_seq / a.n_q;
-    for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
-        const int raw_len = a.seq_lens[s];
-        int L;
-        const int n = seq_chunks<kTok>(a, s, L);
-        const QueryRange qr = a.qsl ? query_range(a.qsl, s, qmax, a.qrows) : QueryRange{s, 1};
-        const int raw_nq = a.qsl ? a.qsl[s + 1] - a.qsl[s] : 1;
-        if (lane == 0 && (raw_len < 0 || raw_len > a.max_len || qr.count != raw_nq || (a.qsl && qr.count > L)))
-            flag(a.status, KVFP8_DEV_BAD_BLOCK);
-        if (n > 0) continue;
-        const int64_t row = static_cast<int64_t>(a.n_q) * HD;
-        uint4 *rows = reinterpret_cast<uint4 *>(a.out + qr.q0 * row);
-        for (int64_t k = lane; k < qr.count * row / 8; k += 32) rows[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
-}
-
 // NV: output tiles of 4 score columns per kv head (1, 2 or 4).  kv heads (consumer warps) per CTA at
 // most, and CTAs per SM, by the registers of the accumulators (HD * NV / 8 of a lane) and of q.  16
 // columns at head_dim 128: eight warps of 168 registers that take 32 tokens at a time (55.0 us for 32
@@ -291,7 +211,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
         uint32_t phase = 0;
         bool aborted = false;
         // this CTA's chunks, the sequence holding the first, that one's chunks and length
-        const CtaPlan rec = a.cta_plan != nullptr ? a.cta_plan[blockIdx.x] : own_plan(a, lane);
+        const CtaPlan rec = a.cta_plan != nullptr ? a.cta_plan[blockIdx.x] : own_plan<kTok>(a, lane);
         const int64_t chunk_lo = rec.lo, chunk_hi = rec.hi;
         int s = rec.s, L = rec.L;
         int64_t cs = rec.cs, ce = rec.ce;
@@ -378,7 +298,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant
             }
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
         }
-        if (a.cta_plan == nullptr && blockIdx.y == 0) finish_plan<HD>(a, lane);
+        if (a.cta_plan == nullptr && blockIdx.y == 0) finish_plan<HD, kTok>(a, lane, true);
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -915,7 +835,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
     k.rows_per_seq = d.qmax * d.n_q;
     k.qrows = d.qrows;
 
-    const bool whole = fp4_takes_sequences_whole(d.max_blocks_per_seq, d.block_size);
+    const bool whole = decode_takes_sequences_whole(d.max_blocks_per_seq, d.block_size);
     const bool own_plan = whole || d.num_seqs <= kOwnPlanSeqs;
     if (own_plan) {
         k.cta_plan = nullptr;
@@ -925,7 +845,7 @@ cudaError_t run_fp4(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t
                                                   k.max_len, num_ctas,
                                                   reinterpret_cast<int32_t *>(w + ws.cstart_off),
                                                   reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
-                                                  d.n_q * HD, d.status);
+                                                  d.n_q * HD, d.status, true);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
 
@@ -980,7 +900,7 @@ cudaError_t run_tiles(const DecodeArgs &d, const DecodeWorkspace &ws, int tiles,
 
 }  // namespace
 
-bool fp4_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size) {
+bool decode_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size) {
     return static_cast<int64_t>(max_blocks_per_seq) * block_size <= kWholeTokens;
 }
 

@@ -289,7 +289,7 @@ template <int kTok>
 __global__ void __launch_bounds__(1024)
 plan_kernel(const int32_t *seq_lens, const int32_t *qsl, int32_t qmax, int32_t qrows,
             int32_t num_seqs, int32_t max_len, int32_t num_ctas, int32_t *cstart,
-            CtaPlan *cta_plan, __nv_bfloat16 *out, int32_t out_row_elems, uint32_t *status) {
+            CtaPlan *cta_plan, __nv_bfloat16 *out, int32_t out_row_elems, uint32_t *status, bool causal) {
     pdl_trigger();  // the decode grid may start its prologue; it waits for this grid's writes
     __shared__ int32_t warp_tot[32];
     __shared__ int32_t carry;
@@ -313,7 +313,7 @@ plan_kernel(const int32_t *seq_lens, const int32_t *qsl, int32_t qmax, int32_t q
                 const int raw = qsl[i + 1] - qsl[i];
                 nq = query_range(qsl, i, qmax, qrows).count;
                 if (nq != raw) flag(status, KVFP8_DEV_BAD_BLOCK);  // rows out of range: skipped
-                if (nq > L) flag(status, KVFP8_DEV_BAD_BLOCK);     // positions below zero
+                if (causal && nq > L) flag(status, KVFP8_DEV_BAD_BLOCK);  // positions below zero
             }
             n = nq > 0 ? (L + kTok - 1) / kTok : 0;
             if (in_smem) len_smem[i] = L;
@@ -1270,7 +1270,7 @@ cudaError_t run(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStream_t str
     plan_kernel<kChunkTokens><<<1, 1024, 0, stream>>>(d.seq_lens, d.qsl, d.qmax, d.qrows, d.num_seqs, k.max_len,
                                         num_ctas, reinterpret_cast<int32_t *>(w + ws.cstart_off),
                                         reinterpret_cast<CtaPlan *>(w + ws.cta_off), k.out,
-                                        d.n_q * HD, d.status);
+                                        d.n_q * HD, d.status, true);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
 
     // Programmatic dependent launch: the decode grid starts its prologue while the plan

@@ -35,6 +35,7 @@
 //        apply v_scale and store bf16.
 //  * All waits are bounded (mbarriers with a clock64 limit); a wait that runs out sets
 //    KVFP8_DEV_TIMEOUT.  Tensor memory is always released before the CTA exits.
+#include "kvfp8_block_scale.cuh"
 #include "kvfp8_e2m1.cuh"
 #include "paged_decode_kernel.cuh"
 
@@ -231,21 +232,36 @@ struct PrefillCommon {
     int32_t box_rows;
     int32_t row_tiles;  // tiles of 128 score rows per (sequence, kv head)
 };
-// The 4-bit form's arguments are its own: carried along by the E4M3 kernels they cost the two-row-tile one
-// 0.8 % (911 against 919 TFLOP/s on 512 new tokens of 64 sequences of 4096).
-template <bool F4>
+// What the cache holds: E4M3 codes (a scale per layer), E2M1 codes with scale bytes per 16 dims, or E4M3
+// codes with a float scale per block and kv head.
+enum class Cache { kE4M3, kE2M1, kBlocks };
+
+// The other forms' arguments are their own: carried along by the E4M3 kernels the 4-bit ones cost the
+// two-row-tile kernel 0.8 % (911 against 919 TFLOP/s on 512 new tokens of 64 sequences of 4096).
+template <Cache C>
 struct PrefillArgs : PrefillCommon {
     // (named by shared code, read by nothing)
     static constexpr int32_t splits = 1;
     static constexpr float *part_o = nullptr, *part_lse = nullptr;
+    static constexpr bool causal = true;
 };
-template <>
-struct PrefillArgs<true> : PrefillCommon {
-    const uint8_t *key_scales, *value_scales;  // the groups' scale bytes
+struct PrefillSplitArgs : PrefillCommon {
     // parts a (sequence, kv head, row tile)'s keys are cut into at most (gridDim.y), and the parts'
     // results, [CTA of the unsplit grid, in sequence order][part][row of the tile]
     int32_t splits;
     float *part_o, *part_lse;
+};
+template <>
+struct PrefillArgs<Cache::kE2M1> : PrefillSplitArgs {
+    const uint8_t *key_scales, *value_scales;  // the groups' scale bytes
+    static constexpr bool causal = true;
+};
+template <>
+struct PrefillArgs<Cache::kBlocks> : PrefillSplitArgs {
+    const float *key_scales, *value_scales;  // [block][scale_stride], a kv head's at its index
+    const uint8_t *value_cache;
+    int32_t scale_stride;
+    bool causal;  // else every query sees every cached token
 };
 
 // ---------------------------------------------------------------- the 4-bit cache
@@ -385,7 +401,7 @@ __host__ __device__ constexpr int o_word(int w) { return F4 ? 4 * (w & 3) + (w >
 // ones.)
 // win: the lane window of block-table entries from wbase on.
 template <int HD>
-__device__ __forceinline__ void copy_scales(const PrefillArgs<true> &a, int kvh, int t0, int kend, int lbs, int32_t win,
+__device__ __forceinline__ void copy_scales(const PrefillArgs<Cache::kE2M1> &a, int kvh, int t0, int kend, int lbs, int32_t win,
                                             int wbase, uint32_t dst, uint32_t side_bytes, uint32_t bar, int lane) {
     constexpr int kGph = HD / 16, kKeys = 16 / kGph, kChunks = kPfKeys / kKeys;  // of a side
 #pragma unroll
@@ -408,7 +424,7 @@ __device__ __forceinline__ void copy_scales(const PrefillArgs<true> &a, int kvh,
 // each lane's own last (negative: none); blocks out of range hold no tokens.  Called by whole warps: the
 // tokens that every lane has are shared out over the lanes, the few after them are each lane's own.
 template <int HD>
-__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs<true> &a, int seq, int kvh, int first, int last) {
+__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs<Cache::kE2M1> &a, int seq, int kvh, int first, int last) {
     const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
     uint32_t groups = 0;
     auto look = [&](int t) {
@@ -466,20 +482,148 @@ __host__ __device__ constexpr int split_parts(int splits, int key_tiles, int til
     const int most = key_tiles / (kMinPartKeys / tile_keys);
     return splits < most ? splits : most > 1 ? most : 1;
 }
-// bf16 pair of dims d, d+1, NaN where the pair's group is in `groups`
-__device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t groups, int d) {
-    return (groups >> (d >> 4)) & 1u ? 0x7FFF7FFFu : w;
+// Whether dim d (past the 32 dims' first, d0) is NaN: kE2M1's groups of 16 dims of a head, kBlocks' dims of
+// the 32.
+template <Cache C>
+__device__ __forceinline__ bool is_nan_dim(uint32_t nan, int d0, int d) {
+    return (nan >> (C == Cache::kE2M1 ? (d0 + d) >> 4 : d)) & 1u;
 }
-// 32 dims from d0 on of a part's row, from O's columns, as float; NaN in `groups`
-__device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], float inv, uint32_t groups, int d0) {
+// bf16 pair of dims d, d+1 with those that are NaN
+template <Cache C>
+__device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t nan, int d0, int d) {
+    if (is_nan_dim<C>(nan, d0, d)) w = (w & 0xFFFF0000u) | 0x7FFFu;
+    if (is_nan_dim<C>(nan, d0, d + 1)) w = (w & 0xFFFFu) | 0x7FFF0000u;
+    return w;
+}
+// 32 dims from d0 on of a part's row, from O's columns, as float; NaN where `nan` says
+template <Cache C>
+__device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], float inv, uint32_t nan, int d0) {
 #pragma unroll
     for (int w = 0; w < 16; w += 2) {  // dims 2w..2w+3
-        const int e = 2 * o_word<true>(w), f = 2 * o_word<true>(w + 1);
-        float4 v = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                               __uint_as_float(o[f]) * inv, __uint_as_float(o[f + 1]) * inv);
-        if ((groups >> ((d0 + 2 * w) >> 4)) & 1u) v.x = v.y = v.z = v.w = __uint_as_float(0x7FC00000u);
-        *reinterpret_cast<float4 *>(row + d0 + 2 * w) = v;
+        const int e = 2 * o_word<C == Cache::kE2M1>(w), f = 2 * o_word<C == Cache::kE2M1>(w + 1);
+        const int from[4] = {e, e + 1, f, f + 1};
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = is_nan_dim<C>(nan, d0, 2 * w + i) ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[from[i]]) * inv;
+        *reinterpret_cast<float4 *>(row + d0 + 2 * w) = make_float4(v[0], v[1], v[2], v[3]);
     }
+}
+
+// ---------------------------------------------------------------- block scales
+//
+// Cache::kBlocks: a block is 16 keys at least, so 16 keys in a row (a group) have one K and one V scale.  The
+// codes are converted as they are.  The softmax multiplies a group's scores by its ks; its vs goes into the
+// exponent, so that the weights that meet V are 2^(s + log2 vs - m) with m near the highest s + log2 vs,
+// within fp16's range whatever the scales, and the row's sum adds a group's weights times 1 / vs.  Weights
+// are held as over the 4-bit cache (kF4Head).
+//
+// NaN: a NaN code in K makes the key's scores NaN, which the masks keep from rows that do not see it.  One
+// in V may reach all rows where all of them see the key.  Where not (the last tiles of a causal call), such codes are
+// taken as 0, the CTA remembers that it met one, and at the end its rows look up which dims of the values
+// they see are NaN (a slow scan that no finite cache runs).
+
+// what the softmax takes of a group's scales: scores * kmul are in the log2 domain
+struct BlockMul {
+    float kmul, vlog, vinv;
+};
+__device__ __forceinline__ BlockMul block_mul(float ks, float vs, float score_scale) {
+    // (kmul is kept away from 0 and infinity, which would make a NaN of a score of infinity or 0)
+    return BlockMul{fminf(fmaxf(ks * score_scale, 0x1p-126f), 0x1p126f), __log2f(vs), 1.f / vs};
+}
+__device__ __forceinline__ BlockMul get_block_mul(uint32_t addr) {
+    BlockMul m;
+    float none;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(m.kmul), "=f"(m.vlog), "=f"(m.vinv), "=f"(none) : "r"(addr));
+    return m;
+}
+
+// The scales of 64 keys from t0 on, [side][16 keys] at dst, by the TMA warp; every lane adds the completion of
+// its copies to the stage's barrier.  win: the lane window of block-table entries from wbase on.
+__device__ __forceinline__ void copy_block_scales(const PrefillArgs<Cache::kBlocks> &a, int kvh, int t0, int kend, int lbs,
+                                                  int32_t win, int wbase, uint32_t dst, uint32_t bar, int lane) {
+    const int t = t0 + 16 * (lane & 3);
+    const int blk = __shfl_sync(0xFFFFFFFFu, win, ((t >> lbs) - wbase) & 31);
+    if (lane < 8 && t < kend && blk >= 0 && blk < a.num_blocks)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * lane),
+                     "l"((lane < 4 ? a.key_scales : a.value_scales) + static_cast<int64_t>(blk) * a.scale_stride + kvh)
+                     : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The keys of a stage, in groups of 16, without those whose block has no valid scales.
+__device__ __forceinline__ uint64_t keys_with_scales(uint32_t scales, uint64_t mask, bool report, uint32_t *status) {
+    float ks[4], vs[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(ks[0]), "=f"(ks[1]), "=f"(ks[2]), "=f"(ks[3]) : "r"(scales));
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(vs[0]), "=f"(vs[1]), "=f"(vs[2]), "=f"(vs[3]) : "r"(scales + 16));
+    uint64_t without = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        if (!(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) without |= 0xFFFFull << (16 * g);
+    if (report && (mask & without) != 0ull) flag(status, KVFP8_DEV_BAD_SCALE);
+    return mask & ~without;
+}
+// What the softmax takes of group g's scales, at out.
+__device__ __forceinline__ void put_block_mul(uint32_t scales, int g, float score_scale, uint32_t out) {
+    float ks, vs;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(scales + 4 * g));
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(scales + 16 + 4 * g));
+    const bool ok = block_scale_ok(ks) && block_scale_ok(vs);  // (else its keys are masked)
+    const BlockMul m = block_mul(ok ? ks : 1.f, ok ? vs : 1.f, score_scale);
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(out + 16 * g), "f"(m.kmul), "f"(m.vlog), "f"(m.vinv),
+                 "f"(0.f)
+                 : "memory");
+}
+
+// NaN codes of V -> 0, remembered
+__device__ __forceinline__ void drop_nan_codes(uint4 &v, volatile int32_t *nan_seen) {
+    const uint4 n = make_uint4(nan_byte_mask(v.x), nan_byte_mask(v.y), nan_byte_mask(v.z), nan_byte_mask(v.w));
+    if ((n.x | n.y | n.z | n.w) != 0u) {
+        v.x &= ~n.x;
+        v.y &= ~n.y;
+        v.z &= ~n.z;
+        v.w &= ~n.w;
+        *nan_seen = 1;
+    }
+}
+
+// The dims d0..d0+31 (bit i: d0 + i) in which some value of tokens first..last of the sequence is NaN, for each
+// lane's own last (negative: none); blocks out of range or without valid scales hold no tokens.  Called by
+// whole warps, as nan_value_groups.
+template <int HD>
+__device__ __noinline__ uint32_t nan_value_dims(const PrefillArgs<Cache::kBlocks> &a, int seq, int kvh, int d0, int first,
+                                                int last) {
+    const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+    uint32_t dims = 0;
+    auto look = [&](int t) {
+        const int32_t blk = bt[t / a.block_size];
+        if (blk < 0 || blk >= a.num_blocks) return;
+        const int64_t s = static_cast<int64_t>(blk) * a.scale_stride + kvh;
+        if (!block_scale_ok(a.key_scales[s]) || !block_scale_ok(a.value_scales[s])) return;
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(
+            a.value_cache + ((static_cast<int64_t>(blk) * a.block_size + t % a.block_size) * a.n_kv + kvh) * HD + d0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t nan = nan_byte_mask(row[i]) & 0x08040201u;
+            dims |= ((nan | nan >> 8 | nan >> 16 | nan >> 24) & 0xFu) << (4 * i);
+        }
+    };
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int all = __reduce_min_sync(0xFFFFFFFFu, last < 0 ? INT32_MAX : last);  // tokens first..all are every lane's
+    if (all != INT32_MAX)
+        for (int t = first + lane; t <= all; t += 32) look(t);
+    dims = __reduce_or_sync(0xFFFFFFFFu, dims);
+    if (last < 0) return 0u;
+    for (int t = max(first, all + 1); t <= last; ++t) look(t);
+    return dims;
+}
+
+// the largest of 16 scores
+__device__ __forceinline__ float max16(const uint32_t *s) {
+    auto v = [&](int c) { return __uint_as_float(s[c]); };
+    const float a = max3f(max3f(v(0), v(1), v(2)), v(3), v(4)), b = max3f(max3f(v(5), v(6), v(7)), v(8), v(9));
+    const float c = max3f(max3f(v(10), v(11), v(12)), v(13), v(14));
+    return max3f(max3f(a, b, c), v(15), v(15));
 }
 
 // ---------------------------------------------------------------- work order
@@ -589,8 +733,9 @@ __device__ __forceinline__ int seq_of_rank(const int32_t *seq_lens, int num_seqs
 // Shared-memory plan (byte offsets from a 1024-aligned base).  Q is converted once; K and
 // V^T (f16) have NB buffers, and so do the scores in tensor memory; the FP8 staging ring has
 // NS stages.  At head_dim 256 the f16 buffers fill the shared memory: NB = 2, NS = 1.
-template <int HD, bool F4>
+template <int HD, Cache C>
 struct PfSmem {
+    static constexpr bool F4 = C == Cache::kE2M1, BS = C == Cache::kBlocks;
     static constexpr int kRow = F4 ? HD / 2 : HD;                  // cache bytes of a key's head
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;          // TMA box row (swizzle span)
     static constexpr int kSegs = kRow / kSeg;
@@ -602,7 +747,7 @@ struct PfSmem {
     // product also accumulates each score row's sum of P (column HD of O) in fp32.  At 256
     // there is no room (the product's N would pass 256 and shared memory would overflow):
     // the softmax warps sum P themselves.
-    static constexpr bool kSumCol = HD <= 128;
+    static constexpr bool kSumCol = HD <= 128 && !BS;  // (BS: the sum is not of the weights that meet V)
     static constexpr int kVRows = HD + (kSumCol ? 16 : 0);
     static constexpr int kVBuf = kVRows * 128;                     // one V^T f16 buffer: rows x 128 B
     static constexpr int kK = kQ + HD * 256;
@@ -624,7 +769,9 @@ struct PfSmem {
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // valid-key mask per K/V buffer
     static constexpr int kMisc = kBufMask + 8 * kNB;               // tmem base, abort flag, NaN seen
-    static constexpr int kTotal = kMisc + 16;
+    // BS: a stage's scales ([side][16 keys]) and, per buffer, what the softmax takes of them (BlockMul)
+    static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
+    static constexpr int kTotal = kBufBs + (BS ? 64 * kNB : 0);
     // tensor memory: S[NB] (64 fp32 columns each; P as f16 over the first 32), then O
     static constexpr uint32_t kColO = 64 * kNB;
     static constexpr uint32_t kTmemCols = kColO + HD + 32 <= 256 ? 256 : 512;
@@ -637,11 +784,12 @@ constexpr int kPfConvWarps = 8;
 constexpr int kPfMmaWarp = 4 + kPfConvWarps, kPfTmaWarp = kPfMmaWarp + 1;
 constexpr int kPfWarps = kPfTmaWarp + 1;
 
-template <int HD, bool F4, bool kSplit>
+template <int HD, Cache C, bool kSplit>
 __global__ void __launch_bounds__(kPfWarps * 32, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-               const PrefillArgs<F4> a) {
-    using L = PfSmem<HD, F4>;
+               const PrefillArgs<C> a) {
+    using L = PfSmem<HD, C>;
+    constexpr bool F4 = L::F4, BS = L::BS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -679,13 +827,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     // (more new tokens than cached ones is an error of the multi-query form only: a decode
     // query on an empty sequence gives a zero row)
     if (tile == 0 && kvh == 0 && tid == 0 &&
-        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.qsl && qr.count > Ls)))
+        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.qsl && a.causal && qr.count > Ls)))
         flag(a.status, KVFP8_DEV_BAD_BLOCK);
     const int nb = qr.count, G = a.group;
     const int row0 = tile * kPfRows;                 // first score row of this tile
     if (row0 >= nb * G) return;                      // no rows here
     const int j_last = min(nb, (row0 + kPfRows + G - 1) / G) - 1;
-    const int kend = Ls - nb + j_last + 1;           // keys the tile's last row may see
+    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;  // keys the tile's last row may see
+    const int all_see = a.causal ? Ls - nb + row0 / G + 1 : Ls;  // (the keys before it every row sees)
     int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
     int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
@@ -716,7 +865,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
+            mbar_init(bar(L::kFull, s), F4 || BS ? 33 : 1);  // and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kPfConvWarps);
         }
         for (int b = 0; b < L::kNB; ++b) {
@@ -727,7 +876,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
-        if (F4) *nan_seen = 0;
+        if (F4 || BS) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPfMmaWarp) {
@@ -821,7 +970,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
                                 bar(L::kFull, st), lane);
             }
-            if constexpr (F4 && L::kNS == 1) {
+            if constexpr (BS)
+                copy_block_scales(a, kvh, t0, kend, lbs, win, wbase, base + L::kStageBs + 32 * st, bar(L::kFull, st), lane);
+            if constexpr ((F4 || BS) && L::kNS == 1) {
                 // one stage: the next copies start when this tile has been read, so their lines are brought
                 // into L2 meanwhile, as far as the window of block-table entries goes (head_dim 256, 32 tokens
                 // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128; with all lines
@@ -833,18 +984,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     for (int sgi = 0; sgi < L::kSegs; ++sgi)
                         tma_prefetch_3d(map, 0, kvh * L::kSegs + sgi, next * bs + box.row);
                 }
-                // and the scale bytes, kLineKeys keys of a side by each of the first lanes
-                constexpr int kLineKeys = 128 / (HD / 16), kLines = kPfKeys / kLineKeys;
-                const int lt = t0 + lane % kLines * kLineKeys;
-                const KeyPlace line = next_tile_place(lt, lbs);
-                const int lblk = __shfl_sync(0xFFFFFFFFu, win, (line.entry - wbase) & 31);
-                if (lane < 2 * kLines && lt + kPfKeys < kend && line.entry - wbase < 32 && lblk >= 0 && lblk < a.num_blocks)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                        (lane < kLines ? a.key_scales : a.value_scales) +
-                        (((static_cast<int64_t>(lblk) * a.n_kv + kvh) << lbs) + line.row) * (HD / 16)));
+                if constexpr (F4) {
+                    // and the scale bytes, kLineKeys keys of a side by each of the first lanes
+                    constexpr int kLineKeys = 128 / (HD / 16), kLines = kPfKeys / kLineKeys;
+                    const int lt = t0 + lane % kLines * kLineKeys;
+                    const KeyPlace line = next_tile_place(lt, lbs);
+                    const int lblk = __shfl_sync(0xFFFFFFFFu, win, (line.entry - wbase) & 31);
+                    if (lane < 2 * kLines && lt + kPfKeys < kend && line.entry - wbase < 32 && lblk >= 0 && lblk < a.num_blocks)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            (lane < kLines ? a.key_scales : a.value_scales) +
+                            (((static_cast<int64_t>(lblk) * a.n_kv + kvh) << lbs) + line.row) * (HD / 16)));
+                }
             }
         }
-        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
+        if ((F4 || BS) && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -940,7 +1093,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kKvFree, b), ((i / L::kNB) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            const uint64_t mask = meta[st];
+            uint64_t mask = meta[st];
+            if constexpr (BS) {
+                const uint32_t scales = base + L::kStageBs + 32 * st;
+                mask = keys_with_scales(scales, mask, ct == 0, a.status);
+                if (ct < 4) put_block_mul(scales, ct, a.sm_scale * 1.4426950408889634f, base + L::kBufBs + 64 * b);
+            }
+            // where some row does not see every key, NaN codes of V are taken out
+            const bool drop_nan = BS && (key_tile(i) + 1) * kPfKeys > all_see;
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf;
@@ -972,6 +1132,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     vw[j][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[j][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
                     if (!((mask >> key) & 1ull)) vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (drop_nan) {
+                        drop_nan_codes(vw[j][0], nan_seen);
+                        drop_nan_codes(vw[j][1], nan_seen);
+                    }
                 }
             };
             auto v_store = [&](int g0) {
@@ -1064,10 +1228,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         const int r = row0 + tid;                   // this thread's score row (TMEM lane tid)
         const bool row_ok = r < nb * G;
         const int jq = row_ok ? r / G : 0, gq = row_ok ? r % G : 0;
-        const int pos = Ls - nb + jq;               // last key position the row may see
+        const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        constexpr float kHead = F4 ? kF4Head : 0.f;
+        constexpr float kHead = F4 || BS ? kF4Head : 0.f;
         float m_used = -INFINITY, lsum = 0.f;
         bool ok = true;
         for (int i = 0; i < ntiles && ok; ++i) {
@@ -1090,8 +1254,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             const int k0 = key_tile(i) * kPfKeys;
             const int vis_n = row_ok ? min(kPfKeys, max(0, pos - k0 + 1)) : 0;  // keys 0..vis_n-1
             const uint64_t vis = mask & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
-            float mx, mult;
-            if (__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
+            float mx, mult = 1.f;
+            BlockMul group[4];  // BS: of 16 keys each
+            if constexpr (BS) {
+                if (!__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((vis >> (32 * h + c)) & 1ull)) s[h][c] = 0xFF800000u;  // -infinity
+                }
+                mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    group[g] = get_block_mul(base + L::kBufBs + 64 * b + 16 * g);
+                    mx = fmaxf(mx, fmaf(max16(s[g >> 1] + 16 * (g & 1)), group[g].kmul, group[g].vlog));
+                }
+            } else if (__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
                 mx = (score_scale >= 0.f ? extreme64<true>(s) : extreme64<false>(s)) * score_scale;
                 mult = score_scale;
             } else {
@@ -1143,8 +1322,26 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             uint32_t p[32];
             const float msub = m_used == -INFINITY ? 0.f : m_used;
             const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(-msub, -msub);
+            if constexpr (BS) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
+                for (int g = 0; g < 4; ++g) {
+                    const float less = group[g].vlog - msub;
+                    const uint64_t gmul2 = pk2(group[g].kmul, group[g].kmul), gsub2 = pk2(less, less);
+                    uint64_t sum2 = pk2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 8 * g; c < 8 * g + 8; ++c) {
+                        const int h = c >> 4, e = (2 * c) & 31;
+                        const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), gmul2, gsub2));
+                        const float e0 = ex2(x.x), e1 = ex2(x.y);
+                        p[c] = f16x2_from_f32(e0, e1);
+                        sum2 = add_f32x2(sum2, pk2(e0, e1));
+                    }
+                    const float2 sum = upk2(sum2);
+                    lsum = fmaf(sum.x + sum.y, group[g].vinv, lsum);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < (BS ? 0 : 32); ++c) {
                 const int h = c >> 4, e = (2 * c) & 31;
                 const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), mul2, sub2));
                 p[c] = F4 ? f16x2_from_f32(ex2(x.x), ex2(x.y)) : ex2_f16x2(f16x2_from_f32(x.x, x.y));
@@ -1168,13 +1365,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 lsum = __uint_as_float(o[0]);
             }
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
-            uint32_t nan_groups = 0;
+            // what this row sees of the values that were taken out as NaN: tokens nan_first..nan_last
+            uint32_t nan_bits = 0;
+            const int key0 = kSplit ? tile_lo * kPfKeys : 0;  // of this part's keys
+            const int nan_last = row_ok ? kSplit ? min(pos, key0 + ntiles * kPfKeys - 1) : pos : -1;
+            const bool any_nan = (F4 || BS) && *nan_seen;
             if constexpr (F4) {
-                if (*nan_seen) {
-                    const int key0 = kSplit ? tile_lo * kPfKeys : 0;  // of this part's keys
-                    nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
-                                                      row_ok ? kSplit ? min(pos, key0 + ntiles * kPfKeys - 1) : pos : -1);
-                }
+                if (any_nan) nan_bits = nan_value_groups<HD>(a, seq, kvh, key0, nan_last);
             }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
@@ -1188,8 +1385,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::kColO + c0, o);
                 tmem_wait_ld();
+                if constexpr (BS) {
+                    if (any_nan)
+                        nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
+                }
                 if constexpr (kSplit) {
-                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
+                    if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
                 } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
@@ -1202,11 +1403,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                         w.y = word(c / 2 + 1);
                         w.z = word(c / 2 + 2);
                         w.w = word(c / 2 + 3);
-                        if (F4 && nan_groups != 0u) {
-                            const int d = c0 + c;
-                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
-                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
-                        }
+                        if ((F4 || BS) && nan_bits != 0u)
+                            w = make_uint4(nan_in<C>(w.x, nan_bits, c0, c), nan_in<C>(w.y, nan_bits, c0, c + 2),
+                                           nan_in<C>(w.z, nan_bits, c0, c + 4), nan_in<C>(w.w, nan_bits, c0, c + 6));
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -1254,8 +1453,9 @@ constexpr int kP2ConvWarps = 4;
 constexpr int kP2MmaWarp = 8 + kP2ConvWarps, kP2TmaWarp = kP2MmaWarp + 1;
 constexpr int kP2Warps = kP2TmaWarp + 1;
 
-template <int HD, bool F4>
+template <int HD, Cache C>
 struct Pf2Smem {
+    static constexpr bool F4 = C == Cache::kE2M1, BS = C == Cache::kBlocks;
     static constexpr int kRow = F4 ? HD / 2 : HD;
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;
     static constexpr int kSegs = kRow / kSeg;
@@ -1280,7 +1480,9 @@ struct Pf2Smem {
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // per V^T buffer, two halves
     static constexpr int kMisc = kBufMask + 32;                    // tmem base, abort flag, NaN seen
-    static constexpr int kTotal = kMisc + 16;
+    // BS: a stage's scales ([side][16 keys]) and, per buffer of two halves, what the softmax takes of them
+    static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
+    static constexpr int kTotal = kBufBs + (BS ? 256 : 0);
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t col_s(int r) { return static_cast<uint32_t>(128 * r); }
     __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(256 + HD * r); }
@@ -1314,11 +1516,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  : "memory");
 }
 
-template <int HD, bool F4, bool kSplit>
+template <int HD, Cache C, bool kSplit>
 __global__ void __launch_bounds__(kP2Warps * 32, 1)
 prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                const PrefillArgs<F4> a) {
-    using L = Pf2Smem<HD, F4>;
+                const PrefillArgs<C> a) {
+    using L = Pf2Smem<HD, C>;
+    constexpr bool F4 = L::F4, BS = L::BS;
     static_assert(L::kTotal + 1024 <= 232448, "shared memory");
     static_assert(L::col_o(1) + HD <= L::kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
@@ -1351,13 +1554,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const int Lraw = a.seq_lens[seq];
     const int Ls = min(max(Lraw, 0), a.max_len);
     if (ctile == 0 && kvh == 0 && tid == 0 &&
-        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || qr.count > Ls))
+        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.causal && qr.count > Ls)))
         flag(a.status, KVFP8_DEV_BAD_BLOCK);
     const int nb = qr.count, G = a.group;
     const int row0 = ctile * kP2Rows;                 // first score row of this CTA
     if (row0 >= nb * G) return;
     const int j_last = min(nb, (row0 + kP2Rows + G - 1) / G) - 1;
-    const int kend = Ls - nb + j_last + 1;            // keys the CTA's last row may see
+    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;  // keys the CTA's last row may see
+    const int all_see = a.causal ? Ls - nb + row0 / G + 1 : Ls;  // (the keys before it every row sees)
     int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
     int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
@@ -1385,7 +1589,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
+            mbar_init(bar(L::kFull, s), F4 || BS ? 33 : 1);  // and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kP2ConvWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -1399,7 +1603,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
-        if (F4) *nan_seen = 0;
+        if (F4 || BS) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kP2MmaWarp) {
@@ -1489,8 +1693,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
                                 bar(L::kFull, st), lane);
             }
+            if constexpr (BS)
+                copy_block_scales(a, kvh, t0, kend, lbs, win, wbase, base + L::kStageBs + 32 * st, bar(L::kFull, st), lane);
         }
-        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
+        if ((F4 || BS) && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -1603,7 +1809,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kKFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            const uint64_t mask = meta[st];
+            uint64_t mask = meta[st];
+            const uint32_t scales_at = base + L::kStageBs + 32 * st;
+            if (BS) mask = keys_with_scales(scales_at, mask, ct == 0, a.status);
+            const bool drop_nan = BS && key_tile(i) * kP2Keys + (hf + 1) * kPfKeys > all_see;  // as in the one-row-tile kernel
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
             // this half's 64 keys: rows 64*hf.. of every 64-dim block of the K buffer
@@ -1622,6 +1831,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     vw[q][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[q][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
                     if (!((mask >> key) & 1ull)) vw[q][0] = vw[q][1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (drop_nan) {
+                        drop_nan_codes(vw[q][0], nan_seen);
+                        drop_nan_codes(vw[q][1], nan_seen);
+                    }
                 }
             };
             auto v_store = [&](int g0) {
@@ -1689,6 +1902,9 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kVFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
+            if constexpr (BS) {
+                if (ct < 4) put_block_mul(scales_at, ct, a.sm_scale * 1.4426950408889634f, base + L::kBufBs + 128 * b + 64 * hf);
+            }
             if constexpr (F4) {
 #pragma unroll
                 for (int q = 0; q < kU4; ++q) {
@@ -1723,11 +1939,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const int r = row0 + tid;                   // this thread's score row
         const bool row_ok = r < nb * G;
         const int jq = row_ok ? r / G : 0, gq = row_ok ? r % G : 0;
-        const int pos = Ls - nb + jq;               // last key position the row may see
+        const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scol = lane_addr + L::col_s(rt);
-        constexpr float kHead = F4 ? kF4Head : 0.f;
+        constexpr float kHead = F4 || BS ? kF4Head : 0.f;
         float m_used = -INFINITY;
         uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
         bool ok = true;
@@ -1753,8 +1969,24 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             // registers for pass 2.
             uint32_t sa[32], sb[32];
             float mx = -INFINITY, ext = score_scale >= 0.f ? -INFINITY : INFINITY;
-            auto chunk_max = [&](const uint32_t (&sc)[32], int c) {
-                if (whole) {
+            const uint32_t scales_at = base + L::kBufBs + 128 * b;  // BS: of 16 keys each
+            auto hide = [&](uint32_t (&sc)[32], int c) {  // BS: keys that the row does not see
+                if (!whole) {
+                    const uint32_t bits = vis_bits(c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) sc[e] = 0xFF800000u;  // -infinity
+                }
+            };
+            auto chunk_max = [&](uint32_t (&sc)[32], int c) {
+                if constexpr (BS) {
+                    hide(sc, c);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const BlockMul mul = get_block_mul(scales_at + 32 * c + 16 * g);
+                        mx = fmaxf(mx, fmaf(max16(sc + 16 * g), mul.kmul, mul.vlog));
+                    }
+                } else if (whole) {
                     ext = score_scale >= 0.f ? fmaxf(ext, extreme32<true>(sc)) : fminf(ext, extreme32<false>(sc));
                 } else {
                     const uint32_t bits = vis_bits(c);
@@ -1773,7 +2005,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             tmem_wait_ld();
             chunk_max(sa, 2);
             chunk_max(sb, 3);
-            if (whole) mx = ext * score_scale;
+            if (!BS && whole) mx = ext * score_scale;
             float factor = 1.f;
             if (mx > -INFINITY) {
                 if (m_used == -INFINITY) {
@@ -1804,6 +2036,27 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float mult = whole ? score_scale : 1.f;
             const uint64_t mul2 = pk2(mult, mult);
             auto chunk_p = [&](uint32_t (&sc)[32], int c) {
+                if constexpr (BS) {
+                    if (c < 2) hide(sc, c);  // (loaded again)
+                    uint32_t p[16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const BlockMul mul = get_block_mul(scales_at + 32 * c + 16 * g);
+                        const float less = mul.vlog - msub;
+                        const uint64_t gmul2 = pk2(mul.kmul, mul.kmul), gsub2 = pk2(less, less);
+                        uint64_t sum2 = pk2(0.f, 0.f);
+#pragma unroll
+                        for (int w = 8 * g; w < 8 * g + 8; ++w) {
+                            const float2 x = upk2(fma_f32x2(pk2u(sc[2 * w], sc[2 * w + 1]), gmul2, gsub2));
+                            const float e0 = ex2(x.x), e1 = ex2(x.y);
+                            p[w] = f16x2_from_f32(e0, e1);
+                            sum2 = add_f32x2(sum2, pk2(e0, e1));
+                        }
+                        lsum2 = fma_f32x2(sum2, pk2(mul.vinv, mul.vinv), lsum2);
+                    }
+                    tmem_st16(scol + 32 * c, p);
+                    return;
+                }
                 if (!whole) {
                     const uint32_t bits = vis_bits(c);
 #pragma unroll
@@ -1841,13 +2094,13 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float2 ls = upk2(lsum2);
             const float lsum = ls.x + ls.y;
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
-            uint32_t nan_groups = 0;
+            // what this row sees of the values that were taken out as NaN: tokens nan_first..nan_last
+            uint32_t nan_bits = 0;
+            const int key0 = kSplit ? tile_lo * kP2Keys : 0;  // of this part's keys
+            const int nan_last = row_ok ? kSplit ? min(pos, key0 + ntiles * kP2Keys - 1) : pos : -1;
+            const bool any_nan = (F4 || BS) && *nan_seen;
             if constexpr (F4) {
-                if (*nan_seen) {
-                    const int key0 = kSplit ? tile_lo * kP2Keys : 0;  // of this part's keys
-                    nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
-                                                      row_ok ? kSplit ? min(pos, key0 + ntiles * kP2Keys - 1) : pos : -1);
-                }
+                if (any_nan) nan_bits = nan_value_groups<HD>(a, seq, kvh, key0, nan_last);
             }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
@@ -1861,8 +2114,12 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
+                if constexpr (BS) {
+                    if (any_nan)
+                        nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
+                }
                 if constexpr (kSplit) {
-                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
+                    if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
                 } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
@@ -1875,11 +2132,9 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                         w.y = word(c / 2 + 1);
                         w.z = word(c / 2 + 2);
                         w.w = word(c / 2 + 3);
-                        if (F4 && nan_groups != 0u) {
-                            const int d = c0 + c;
-                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
-                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
-                        }
+                        if ((F4 || BS) && nan_bits != 0u)
+                            w = make_uint4(nan_in<C>(w.x, nan_bits, c0, c), nan_in<C>(w.y, nan_bits, c0, c + 2),
+                                           nan_in<C>(w.z, nan_bits, c0, c + 4), nan_in<C>(w.w, nan_bits, c0, c + 6));
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -1899,8 +2154,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
 // Joins the parts of each row: CTA (x, y) takes 256 / (HD / 4) rows of row tile x (of tile_rows rows, keys in
 // tiles of tile_keys).
-template <int HD>
-__global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<true> a, int tile_rows, int tile_keys) {
+template <int HD, Cache C>
+__global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<C> a, int tile_rows, int tile_keys) {
     constexpr int kLanes = HD / 4;  // threads of a row, four dims each
     const int kvh = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.n_kv));
     const int tile = static_cast<int>((blockIdx.x / static_cast<unsigned>(a.n_kv)) % static_cast<unsigned>(a.row_tiles));
@@ -1916,7 +2171,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<true>
     if (r >= nb * G) return;
     // the row tile's parts, as its CTAs worked them out
     const int j_last = min(nb, (row0 + tile_rows + G - 1) / G) - 1;
-    const int kend = Ls - nb + j_last + 1;
+    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;
     if (kend <= 0) return;  // zeroed by its CTA
     const int parts = split_parts(a.splits, (kend + tile_keys - 1) / tile_keys, tile_keys);
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
@@ -1963,8 +2218,8 @@ SplitPlan split_plan(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_d
     return p;
 }
 
-template <int HD>
-cudaError_t join_parts(const PrefillArgs<true> &a, const SplitPlan &p, cudaStream_t stream) {
+template <int HD, Cache C>
+cudaError_t join_parts(const PrefillArgs<C> &a, const SplitPlan &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_seqs * a.row_tiles * a.n_kv, p.tile_rows / (256 / (HD / 4)));
     cfg.blockDim = dim3(256);
@@ -1974,12 +2229,13 @@ cudaError_t join_parts(const PrefillArgs<true> &a, const SplitPlan &p, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD>, a, p.tile_rows, p.tile_keys);
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD, C>, a, p.tile_rows, p.tile_keys);
 }
 
-template <int HD, bool F4>
+template <int HD, Cache C>
 cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
-    using L = PfSmem<HD, F4>;
+    using L = PfSmem<HD, C>;
+    constexpr bool kParts = C != Cache::kE4M3;
     const int row_bytes = d.n_kv * L::kRow;
     const int box_rows = d.block_size >= kPfKeys ? kPfKeys : d.block_size;  // whole tile when one block holds it
     const int64_t rows = static_cast<int64_t>(d.num_blocks) * d.block_size;
@@ -1989,7 +2245,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         return err;
     if ((err = encode_cache_map(&tmv, d.value_cache, rows, row_bytes, L::kSeg, box_rows)) != cudaSuccess)
         return err;
-    PrefillArgs<F4> a;
+    PrefillArgs<C> a;
     a.out = static_cast<__nv_bfloat16 *>(d.out);
     a.query = static_cast<const __nv_bfloat16 *>(d.query);
     a.qsl = d.qsl;
@@ -2012,18 +2268,27 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     a.status = d.status;
     a.box_rows = box_rows;
     SplitPlan sp;
-    if constexpr (F4) {
-        sp = split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
+    if constexpr (C == Cache::kE2M1) {
         a.key_scales = d.key_scales;
         a.value_scales = d.value_scales;
+    }
+    if constexpr (C == Cache::kBlocks) {
+        a.key_scales = d.key_block_scales;
+        a.value_scales = d.value_block_scales;
+        a.value_cache = d.value_cache;
+        a.scale_stride = d.block_scale_stride;
+        a.causal = d.causal != 0;
+    }
+    if constexpr (kParts) {
+        sp = split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
         a.splits = sp.splits;
         a.part_o = static_cast<float *>(d.workspace);
         a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(d.workspace) + sp.lse_off);
     }
     auto launched = [&]() -> cudaError_t {
         const cudaError_t e = cudaGetLastError();
-        if constexpr (F4) {
-            if (e == cudaSuccess && sp.splits > 1) return join_parts<HD>(a, sp, stream);
+        if constexpr (kParts) {
+            if (e == cudaSuccess && sp.splits > 1) return join_parts<HD, C>(a, sp, stream);
         }
         return e;
     };
@@ -2031,8 +2296,8 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     // more than one tile of 128 rows per kv head (a multi-query call): 256 rows per CTA
     if constexpr (HD <= 128) {
         if (d.qsl != nullptr && group_rows > kPfRows) {
-            const size_t smem2 = Pf2Smem<HD, F4>::kTotal + 1024;
-            auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, F4, F4> : prefill2_kernel<HD, F4, false>;
+            const size_t smem2 = Pf2Smem<HD, C>::kTotal + 1024;
+            auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, C, kParts> : prefill2_kernel<HD, C, false>;
             int occ2 = 0;  // also raises the kernel's shared memory limit, once per device
             if ((err = kernel_occupancy(kern2, kP2Warps * 32, smem2, &occ2)) != cudaSuccess)
                 return err;
@@ -2043,7 +2308,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         }
     }
     const size_t smem = L::kTotal + 1024;
-    auto kern = sp.splits > 1 ? prefill_kernel<HD, F4, F4> : prefill_kernel<HD, F4, false>;
+    auto kern = sp.splits > 1 ? prefill_kernel<HD, C, kParts> : prefill_kernel<HD, C, false>;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
     a.row_tiles = (group_rows + kPfRows - 1) / kPfRows;
@@ -2052,9 +2317,19 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     return launched();
 }
 
+template <Cache C>
+cudaError_t run_head_dim(const DecodeArgs &d, cudaStream_t stream) {
+    switch (d.head_dim) {
+        case 64: return run_prefill<64, C>(d, stream);
+        case 128: return run_prefill<128, C>(d, stream);
+        case 256: return run_prefill<256, C>(d, stream);
+        default: return cudaErrorNotSupported;
+    }
+}
+
 }  // namespace
 
-size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+size_t split_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
                                   int64_t max_len) {
     return split_plan(num_seqs, n_q, n_kv, head_dim, qmax, max_len).total;
 }
@@ -2071,13 +2346,8 @@ cudaError_t launch_prefill_attention(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;
     if (d.k_bf16 || d.v_bf16) return cudaErrorNotSupported;
     if (!prefill_takes(d.n_q, d.n_kv, d.qmax, d.num_seqs)) return cudaErrorNotSupported;
-    const bool f4 = d.key_scales != nullptr;
-    switch (d.head_dim) {
-        case 64: return f4 ? run_prefill<64, true>(d, stream) : run_prefill<64, false>(d, stream);
-        case 128: return f4 ? run_prefill<128, true>(d, stream) : run_prefill<128, false>(d, stream);
-        case 256: return f4 ? run_prefill<256, true>(d, stream) : run_prefill<256, false>(d, stream);
-        default: return cudaErrorNotSupported;
-    }
+    if (d.key_block_scales != nullptr) return run_head_dim<Cache::kBlocks>(d, stream);
+    return d.key_scales != nullptr ? run_head_dim<Cache::kE2M1>(d, stream) : run_head_dim<Cache::kE4M3>(d, stream);
 }
 
 }  // namespace kvfp8

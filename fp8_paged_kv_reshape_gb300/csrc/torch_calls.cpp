@@ -1,4 +1,4 @@
-// The calls of the 4-bit cache and of pages on torch tensors: argument checks, allocation and the
+// The calls of the 4-bit cache, of the cache with block scales, of rotary positions and of pages on torch tensors: argument checks, allocation and the
 // C call, for binding.py.
 //
 // These run once per layer and step, where a kernel takes a few microseconds, and the checks look at
@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <optional>
 #include <utility>
 #include <vector>
@@ -256,6 +257,220 @@ Tensor paged_attention_multi_fp4(const Tensor &query, const Tensor &qsl, int64_t
                          workspace, status);
 }
 
+// ---------------------------------------------------------------- FP8 cache with block scales
+
+struct BlockCache {
+    CacheShape shape;
+    int32_t scale_stride;
+};
+
+// one side: codes and block scales
+BlockCache check_block_side(const Tensor &codes, const Tensor &scales) {
+    TORCH_CHECK_VALUE(dense(codes, at::kByte) && codes.dim() == 4,
+                      "caches must be contiguous uint8 [num_blocks, block_size, n_kv, head_dim]");
+    const auto s = codes.sizes();
+    TORCH_CHECK_VALUE(dense(scales, at::kFloat) && scales.dim() == 2 && scales.size(0) == s[0] && scales.size(1) >= s[2] &&
+                          scales.size(1) % 4 == 0,
+                      "their scales must be contiguous float32 [num_blocks, n_kv rounded up to a multiple of 4]");
+    return {{i32(s[0], "num_blocks"), i32(s[1], "block_size"), i32(s[2], "n_kv"), i32(s[3], "head_dim")},
+            i32(scales.size(1), "the scales' row")};
+}
+
+BlockCache check_block_caches(const Tensor &kc, const Tensor &vc, const Tensor &ks, const Tensor &vs) {
+    const BlockCache k = check_block_side(kc, ks), v = check_block_side(vc, vs);
+    TORCH_CHECK_VALUE(k.shape == v.shape && k.scale_stride == v.scale_stride, "key and value caches must have one shape");
+    return k;
+}
+
+void reshape_and_cache_block_scaled(const Tensor &key, const Tensor &value, const Tensor &kc, const Tensor &vc,
+                                    const Tensor &ks, const Tensor &vs, const Tensor &slots, const Opt &workspace,
+                                    const Opt &status) {
+    const auto dt = key.scalar_type();
+    TORCH_CHECK_TYPE(value.scalar_type() == dt && (dt == at::kBFloat16 || dt == at::kFloat),
+                     "key and value must share one dtype, bfloat16 or float32");
+    TORCH_CHECK_VALUE(key.dim() == 3 && value.sizes() == key.sizes(),
+                      "key/value must be [num_tokens, n_kv, head_dim] with equal shapes");
+    const int64_t n = key.size(0), n_kv = key.size(1), hd = key.size(2);
+    for (const Tensor *t : {&key, &value})
+        TORCH_CHECK_VALUE(n == 0 || (t->stride(2) == 1 && (n_kv == 1 || t->stride(1) == hd)),
+                          "key/value inner dims [n_kv, head_dim] must be dense");
+    const BlockCache b = check_block_caches(kc, vc, ks, vs);
+    const CacheShape &c = b.shape;
+    TORCH_CHECK_VALUE(c.n_kv == n_kv && c.head_dim == hd,
+                      "the caches' n_kv and head_dim must be those of key and value");
+    check_slots(slots, n);
+    check_workspace(workspace);
+    check_status(status);
+    Call call(key);
+    call.on(value).on(kc).on(vc).on(ks).on(vs).on(slots).on(workspace).on(status).start();
+    Opt ws = workspace;
+    if (!ws) {
+        const size_t need = kvfp8_reshape_and_cache_block_scaled_workspace_size(n, c.num_blocks, c.block_size);
+        if (need > 0) ws = call.empty({static_cast<int64_t>(need)}, at::kByte);
+    }
+    // (the stride of a single row is never used, and may be anything)
+    const int64_t row = n_kv * hd, kst = n > 1 ? key.stride(0) : row, vst = n > 1 ? value.stride(0) : row;
+    check(kvfp8_reshape_and_cache_block_scaled(
+              ptr(key), ptr(value), dt == at::kFloat ? KVFP8_F32 : KVFP8_BF16, kst, vst, n, ptr<uint8_t>(kc),
+              ptr<uint8_t>(vc), ptr<float>(ks), ptr<float>(vs), b.scale_stride, c.num_blocks, c.block_size, c.n_kv,
+              c.head_dim, ptr<int64_t>(slots), ptr(ws), ws ? ws->nbytes() : 0, status_ptr(status), call.stream()),
+          "kvfp8_reshape_and_cache_block_scaled");
+}
+
+Tensor dequant_block_scaled(const Tensor &codes, const Tensor &scales, const Tensor &slots, bool to_bf16, const Opt &out,
+                            const Opt &status) {
+    const BlockCache b = check_block_side(codes, scales);
+    const CacheShape &c = b.shape;
+    TORCH_CHECK_VALUE(slots.dim() == 1, "slot_mapping must be a contiguous int64 [num_tokens] tensor");
+    const int64_t n = slots.size(0);
+    check_slots(slots, n);
+    const auto dt = to_bf16 ? at::kBFloat16 : at::kFloat;
+    const int64_t shape[3] = {n, c.n_kv, c.head_dim};
+    TORCH_CHECK_VALUE(!out || (dense(*out, dt) && out->sizes() == at::IntArrayRef(shape)),
+                      "out must be a contiguous dst_dtype [num_tokens, n_kv, head_dim] tensor");
+    check_status(status);
+    Call call(codes);
+    call.on(scales).on(slots).on(out).on(status).start();
+    Tensor dst = out ? *out : call.empty(shape, dt);
+    check(kvfp8_dequant_block_scaled(ptr(dst), to_bf16 ? KVFP8_BF16 : KVFP8_F32, ptr<uint8_t>(codes), ptr<float>(scales),
+                                     b.scale_stride, c.num_blocks, c.block_size, c.n_kv, c.head_dim, ptr<int64_t>(slots),
+                                     n, status_ptr(status), call.stream()),
+          "kvfp8_dequant_block_scaled");
+    return dst;
+}
+
+// Both attention calls (qsl: the multi-query form).
+Tensor attention_block_scaled(const Tensor &query, const Opt &qsl, int64_t max_query_len, bool causal, const Tensor &kc,
+                              const Tensor &vc, const Tensor &ks, const Tensor &vs, const Tensor &tables,
+                              const Tensor &lens, double sm_scale, const Opt &out, const Opt &workspace,
+                              const Opt &status) {
+    TORCH_CHECK_VALUE(dense(query, at::kBFloat16) && query.dim() == 3,
+                      "query must be a contiguous bf16 [rows, n_q, head_dim] tensor");
+    const int64_t num_seqs = qsl ? lens.numel() : query.size(0);
+    TORCH_CHECK_VALUE(!qsl || (dense(*qsl, at::kInt) && qsl->numel() == num_seqs + 1),
+                      "query_start_loc must be a contiguous int32 [num_seqs + 1] tensor");
+    const BlockCache b = check_block_caches(kc, vc, ks, vs);
+    const CacheShape &c = b.shape;
+    TORCH_CHECK_VALUE(c.head_dim == query.size(2), "the caches' head_dim must be the query's");
+    check_tables(tables, lens, num_seqs);
+    TORCH_CHECK_VALUE(!out || (dense(*out, at::kBFloat16) && out->sizes() == query.sizes()),
+                      "out must be a contiguous bf16 tensor shaped like query");
+    check_workspace(workspace);
+    check_status(status);
+    Call call(query);
+    call.on(kc).on(vc).on(ks).on(vs).on(tables).on(lens).on(out).on(workspace).on(status).on(qsl).start();
+    const int32_t seqs = i32(num_seqs, "num_seqs"), rows = i32(query.size(0), "query rows"),
+                  n_q = i32(query.size(1), "n_q"), most = i32(tables.size(1), "max_blocks"),
+                  qmax = i32(std::max<int64_t>(max_query_len, 0), "max_query_len");
+    Tensor dst = out ? *out : call.empty(query.sizes(), at::kBFloat16);
+    Opt ws = workspace;
+    if (!ws) {
+        const size_t need = kvfp8_paged_attention_block_scaled_workspace_size(seqs, n_q, c.n_kv, c.head_dim, qmax, most,
+                                                                              c.block_size);
+        if (need > 0) ws = call.empty({static_cast<int64_t>(need)}, at::kByte);
+    }
+    const size_t ws_bytes = ws ? ws->nbytes() : 0;
+    if (qsl)
+        check(kvfp8_paged_attention_multi_block_scaled(
+                  ptr(dst), ptr(query), ptr<int32_t>(*qsl), rows, qmax, causal, ptr<uint8_t>(kc), ptr<uint8_t>(vc),
+                  ptr<float>(ks), ptr<float>(vs), b.scale_stride, ptr<int32_t>(tables), most, ptr<int32_t>(lens), seqs, n_q,
+                  c.n_kv, c.head_dim, c.block_size, c.num_blocks, static_cast<float>(sm_scale), ptr(ws), ws_bytes,
+                  status_ptr(status), call.stream()),
+              "kvfp8_paged_attention_multi_block_scaled");
+    else
+        check(kvfp8_paged_decode_attention_block_scaled(
+                  ptr(dst), ptr(query), ptr<uint8_t>(kc), ptr<uint8_t>(vc), ptr<float>(ks), ptr<float>(vs), b.scale_stride,
+                  ptr<int32_t>(tables), most, ptr<int32_t>(lens), seqs, n_q, c.n_kv, c.head_dim, c.block_size,
+                  c.num_blocks, static_cast<float>(sm_scale), ptr(ws), ws_bytes, status_ptr(status), call.stream()),
+              "kvfp8_paged_decode_attention_block_scaled");
+    return dst;
+}
+
+Tensor paged_decode_attention_block_scaled(const Tensor &query, const Tensor &kc, const Tensor &vc, const Tensor &ks,
+                                           const Tensor &vs, const Tensor &tables, const Tensor &lens, double sm_scale,
+                                           const Opt &out, const Opt &workspace, const Opt &status) {
+    return attention_block_scaled(query, std::nullopt, 1, true, kc, vc, ks, vs, tables, lens, sm_scale, out, workspace,
+                                  status);
+}
+
+Tensor paged_attention_multi_block_scaled(const Tensor &query, const Tensor &qsl, int64_t max_query_len, const Tensor &kc,
+                                          const Tensor &vc, const Tensor &ks, const Tensor &vs, const Tensor &tables,
+                                          const Tensor &lens, bool causal, double sm_scale, const Opt &out,
+                                          const Opt &workspace, const Opt &status) {
+    return attention_block_scaled(query, qsl, max_query_len, causal, kc, vc, ks, vs, tables, lens, sm_scale, out, workspace,
+                                  status);
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+// Rows of heads whose inner dims are dense; their stride (that of a single row is never used).
+int64_t head_rows(const Tensor &t, const char *what) {
+    const int64_t n = t.size(0), row = t.size(1) * t.size(2);
+    TORCH_CHECK_VALUE(n == 0 || (t.stride(2) == 1 && (t.size(1) == 1 || t.stride(1) == t.size(2))), what,
+                      "'s inner dims [heads, head_dim] must be dense");
+    return n > 1 ? t.stride(0) : row;
+}
+
+// An output is its own input or apart from `other`.
+void check_apart(const Tensor &out, const Tensor &other, bool may_be_same) {
+    if (out.numel() == 0 || other.numel() == 0) return;
+    if (may_be_same && out.data_ptr() == other.data_ptr() && (out.size(0) == 1 || out.stride(0) == other.stride(0))) return;
+    auto end = [](const Tensor &t) {
+        return ptr<char>(t) + ((t.size(0) - 1) * t.stride(0) + t.size(1) * t.size(2)) * t.element_size();
+    };
+    if (end(out) <= ptr<char>(other) || end(other) <= ptr<char>(out)) return;
+    // slices of one fused row: the same stride, and apart within it
+    const int64_t stride = out.stride(0) * out.element_size(), gap = std::abs(ptr<char>(out) - ptr<char>(other));
+    const Tensor &low = ptr<char>(out) < ptr<char>(other) ? out : other, &high = &low == &out ? other : out;
+    TORCH_CHECK_VALUE(out.stride(0) == other.stride(0) && gap >= low.size(1) * low.size(2) * low.element_size() &&
+                          gap + high.size(1) * high.size(2) * high.element_size() <= stride,
+                      "outputs must not overlap the inputs or each other (an output may be its own input)");
+}
+
+std::pair<Tensor, Opt> rotary_embedding(const Tensor &query, const Opt &key, const Tensor &positions,
+                                        const Tensor &frequencies, bool interleaved, double magnitude, bool transpose,
+                                        const Opt &query_out, const Opt &key_out, const Opt &status) {
+    const auto dt = query.scalar_type();
+    TORCH_CHECK_TYPE((dt == at::kBFloat16 || dt == at::kFloat) && (!key || key->scalar_type() == dt),
+                     "query and key must share one dtype, bfloat16 or float32");
+    TORCH_CHECK_VALUE(query.dim() == 3, "query must be [num_tokens, n_q, head_dim]");
+    TORCH_CHECK_VALUE(!key || (key->dim() == 3 && key->size(0) == query.size(0) && key->size(2) == query.size(2)),
+                      "key must be [num_tokens, n_k, head_dim] of query's tokens and head_dim");
+    const int64_t n = query.size(0);
+    TORCH_CHECK_VALUE(dense(positions, at::kLong) && positions.numel() == n,
+                      "positions must be a contiguous int64 [num_tokens] tensor");
+    TORCH_CHECK_VALUE(dense(frequencies, at::kDouble) && frequencies.dim() == 1,
+                      "frequencies must be a contiguous float64 [rot_dim / 2] tensor");
+    TORCH_CHECK_VALUE(!query_out || (query_out->scalar_type() == dt && query_out->sizes() == query.sizes()),
+                      "query_out must have query's shape and dtype");
+    TORCH_CHECK_VALUE(!key_out || (key && key_out->scalar_type() == dt && key_out->sizes() == key->sizes()),
+                      "key_out must have key's shape and dtype");
+    check_status(status);
+    Call call(query);
+    call.on(key).on(positions).on(frequencies).on(query_out).on(key_out).on(status).start();
+    const int64_t q_stride = head_rows(query, "query"), k_stride = key ? head_rows(*key, "key") : 0;
+    const Tensor q_to = query_out ? *query_out : call.empty(query.sizes(), dt);
+    const Opt k_to = !key ? Opt() : key_out ? *key_out : Opt(call.empty(key->sizes(), dt));
+    const int64_t q_to_stride = head_rows(q_to, "query_out"), k_to_stride = key ? head_rows(*k_to, "key_out") : 0;
+    if (query_out) {
+        check_apart(q_to, query, true);
+        if (key) check_apart(q_to, *key, false);
+    }
+    if (key_out) {
+        check_apart(*k_to, *key, true);
+        check_apart(*k_to, query, false);
+        check_apart(*k_to, q_to, false);
+    }
+    check(kvfp8_rotary_embedding(ptr(q_to), ptr(k_to), q_to_stride, k_to_stride, ptr(query), ptr(key), q_stride, k_stride,
+                                 dt == at::kFloat ? KVFP8_F32 : KVFP8_BF16, n, i32(query.size(1), "n_q"),
+                                 key ? i32(key->size(1), "n_k") : 0, i32(query.size(2), "head_dim"),
+                                 i32(2 * frequencies.size(0), "rot_dim"), interleaved, transpose, ptr<int64_t>(positions),
+                                 ptr<double>(frequencies), static_cast<float>(magnitude), status_ptr(status),
+                                 call.stream()),
+          "kvfp8_rotary_embedding");
+    return {q_to, k_to};
+}
+
 // ---------------------------------------------------------------- pages
 
 struct Caches {
@@ -338,6 +553,11 @@ PYBIND11_MODULE(kvfp8_torch, m) {
     m.def("dequant_fp4", torch::wrap_pybind_function(dequant_fp4));
     m.def("paged_decode_attention_fp4", torch::wrap_pybind_function(paged_decode_attention_fp4));
     m.def("paged_attention_multi_fp4", torch::wrap_pybind_function(paged_attention_multi_fp4));
+    m.def("reshape_and_cache_block_scaled", torch::wrap_pybind_function(reshape_and_cache_block_scaled));
+    m.def("dequant_block_scaled", torch::wrap_pybind_function(dequant_block_scaled));
+    m.def("paged_decode_attention_block_scaled", torch::wrap_pybind_function(paged_decode_attention_block_scaled));
+    m.def("paged_attention_multi_block_scaled", torch::wrap_pybind_function(paged_attention_multi_block_scaled));
+    m.def("rotary_embedding", torch::wrap_pybind_function(rotary_embedding));
     m.def("copy_blocks", torch::wrap_pybind_function(copy_blocks));
     m.def("compact_blocks", torch::wrap_pybind_function(compact_blocks));
     m.def("on_status", [](py::object f) { raise_status() = std::move(f); });

@@ -11,6 +11,9 @@
  *   kvfp8_dequant                 bytes -> scale * value, for the rope-shift path
  *                                 (dequantize, rotate, requantize)
  *   kvfp8_*_fp4                   the same over a cache of 4-bit codes with a scale per 16 dims
+ *   kvfp8_*_block_scaled          the same over a cache of E4M3 codes with a scale per block and kv
+ *                                 head, made as rows are written; attention causal or not
+ *   kvfp8_rotary_embedding        query and key heads rotated by their positions
  *   kvfp8_copy_blocks, kvfp8_compact_blocks
  *                                 pages of any cache copied, and a pool's used pages gathered
  *
@@ -475,6 +478,153 @@ KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
     int32_t n_kv, int32_t head_dim, int32_t block_size, int32_t num_blocks, float sm_scale,
     const void *k_scale, const void *v_scale, kvfp8_dtype scale_dtype, void *workspace,
     size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * The FP8 cache with block scales: E4M3 codes with one float scale per block and kv head, made as
+ * rows are written (no scale has to be known beforehand, and heads and blocks of different
+ * magnitude each use the whole range of E4M3).  Per side:
+ *   codes   uint8 [num_blocks][block_size][n_kv][head_dim]   (as the FP8 cache's)
+ *   scales  float [num_blocks][scale_stride], a kv head's at its index; scale_stride >= n_kv, a
+ *           multiple of 4 (so that a block's scales are whole 16-byte pieces, as the page calls want)
+ * An element's value is dec(code) * scale.  A valid scale lies in [2^-60, 2^120]; 0 says that nothing was
+ * written to the block (a pool starts with scales of 0).
+ *
+ * Everywhere below head_dim is 64, 128 or 256 and block_size 16, 32, 64, 128 or 256; n_kv * head_dim <=
+ * 2^20; all device pointers 16-byte aligned.
+ *
+ * kvfp8_reshape_and_cache_block_scaled: K and V rows quantized and scattered by slot, as
+ * kvfp8_reshape_and_cache.  For every block that has rows in the call, per side and kv head, with a the largest
+ * finite |x| of the call's rows in it (0 without any):
+ *   P = the smallest power of two, 2^-60 at least, with 448 * P >= a
+ *   s = P                      when the call writes the block's first token (offset 0): the block starts anew,
+ *                              whatever it held; codes of its other tokens that the call does not write
+ *                              stay as they are, and have no meaning
+ *   s = max(old scale, P)      otherwise; when that raises it, every code c of the block that the call does not
+ *                              write becomes E4M3(dec(c) * (old / s)), the products in float, NaN codes kept
+ *   code = E4M3(x / s)         the float quotient, as kvfp8_reshape_and_cache: nearest even, saturating
+ *                              (infinities too), NaN -> sign | 0x7F
+ * P being a power of two, raising a scale loses only what leaves E4M3's range at the bottom, however
+ * often it happens.  Tokens of a block that are written again singly must not be its first; write a block's
+ * tokens together to change them all (after a rope shift, say).
+ *
+ * A slot that is -1 is padding, any other outside [0, num_blocks*block_size) is skipped and sets
+ * KVFP8_DEV_BAD_SLOT.  An old scale that is neither 0 nor valid (where it counts) sets
+ * KVFP8_DEV_BAD_SCALE, and that side and head of the block stay as they are.  Of rows that name one slot
+ * one is written, as a whole.  A call's rows may stand in any order.
+ *
+ * src_dtype, strides  as kvfp8_reshape_and_cache (16-byte rows); num_tokens < 2^31
+ * workspace           device, >= kvfp8_reshape_and_cache_block_scaled_workspace_size(...) bytes, any contents;
+ *                     calls that overlap on the GPU must not share it.  0 bytes, and then NULL will do, for calls of up to 512 rows.
+ */
+KVFP8_API size_t kvfp8_reshape_and_cache_block_scaled_workspace_size(int64_t num_tokens,
+                                                                     int32_t num_blocks,
+                                                                     int32_t block_size);
+
+KVFP8_API kvfp8_status kvfp8_reshape_and_cache_block_scaled(
+    const void *key, const void *value, kvfp8_dtype src_dtype, int64_t key_stride,
+    int64_t value_stride, int64_t num_tokens, uint8_t *key_cache, uint8_t *value_cache,
+    float *key_scales, float *value_scales, int32_t scale_stride, int32_t num_blocks,
+    int32_t block_size, int32_t n_kv, int32_t head_dim, const int64_t *slot_mapping,
+    void *workspace, size_t workspace_bytes, uint32_t *status, kvfp8_stream_t stream);
+
+/*
+ * Rows of one side of that cache read back by slot:
+ *   dst[i][h][d] = dec(code) * scale, a float product, rounded to dst_dtype (bf16: nearest even)
+ * for the token slot slot_mapping[i].  Slot -1 gives a zero row; any other slot out of range gives a zero
+ * row and sets KVFP8_DEV_BAD_SLOT; a scale that is not valid gives zeros for its head and sets
+ * KVFP8_DEV_BAD_SCALE.  A slot may be named several times.
+ *
+ * dst   device, dst_dtype [num_tokens][n_kv][head_dim]
+ */
+KVFP8_API kvfp8_status kvfp8_dequant_block_scaled(void *dst, kvfp8_dtype dst_dtype, const uint8_t *codes,
+                                                  const float *scales, int32_t scale_stride,
+                                                  int32_t num_blocks, int32_t block_size, int32_t n_kv,
+                                                  int32_t head_dim, const int64_t *slot_mapping,
+                                                  int64_t num_tokens, uint32_t *status,
+                                                  kvfp8_stream_t stream);
+
+/*
+ * Workspace bytes of the two calls below (decode: max_query_len 1): as
+ * kvfp8_paged_attention_fp4_workspace_size.  Pure host arithmetic.
+ */
+KVFP8_API size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_seqs, int32_t n_q,
+                                                                   int32_t n_kv, int32_t head_dim,
+                                                                   int32_t max_query_len,
+                                                                   int32_t max_blocks_per_seq,
+                                                                   int32_t block_size);
+
+/*
+ * kvfp8_paged_decode_attention over the FP8 cache with block scales: with ks_t, vs_t the scales of token t's
+ * block and kv head,
+ *   s_t = sm_scale * ks_t * sum_d q[b][h][d] * dec(K(t, kv, d))
+ *   out[b][h][d] = sum_t softmax(s)_t * vs_t * dec(V(t, kv, d))
+ * Codes enter the tensor cores as fp16 exactly, q as for the other calls (exactly from 2^-17 to 65504).
+ * Scores, the exponential, the sum of the weights and the accumulation are float.  softmax(s)_t * vs_t
+ * enters the product with V as fp16, 2^7 to 2^15 at a row's highest: 11 bits down to 2^-21 of the highest,
+ * multiples of 2^-24 below, none below 2^-32.  All of this holds for every query length and group size.
+ *
+ * A block whose scales are not valid (of either side) holds no tokens for that head and sets
+ * KVFP8_DEV_BAD_SCALE.  A token's NaN reaches exactly the outputs that see the token (all of a row for
+ * one in K, its own dim for one in V).  An n_kv that falls into more than 65535 equal groups of kv heads
+ * (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Everything else (group sizes, empty sequences, bad blocks,
+ * errors) as kvfp8_paged_decode_attention.
+ */
+KVFP8_API kvfp8_status kvfp8_paged_decode_attention_block_scaled(
+    void *out, const void *query, const uint8_t *key_cache, const uint8_t *value_cache,
+    const float *key_scales, const float *value_scales, int32_t scale_stride,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, float sm_scale, void *workspace, size_t workspace_bytes, uint32_t *status,
+    kvfp8_stream_t stream);
+
+/*
+ * kvfp8_paged_attention_multi over that cache, causal or not.
+ *   causal != 0  as kvfp8_paged_attention_multi: the queries are the sequence's last tokens
+ *   causal == 0  every query of sequence b sees all seq_lens[b] cached tokens (cross attention to an
+ *                encoder's states, or a prefix that all queries share); a sequence may have more query rows
+ *                than tokens
+ * Without query rows (num_query_rows 0) there is nothing to do: KVFP8_OK.
+ */
+KVFP8_API kvfp8_status kvfp8_paged_attention_multi_block_scaled(
+    void *out, const void *query, const int32_t *query_start_loc, int32_t num_query_rows,
+    int32_t max_query_len, int32_t causal, const uint8_t *key_cache, const uint8_t *value_cache,
+    const float *key_scales, const float *value_scales, int32_t scale_stride,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, float sm_scale, void *workspace, size_t workspace_bytes, uint32_t *status,
+    kvfp8_stream_t stream);
+
+/*
+ * Rotary positions on the heads of a token's query and key rows (before a cache write, where
+ * kvfp8_rope_reshape_and_cache rotates keys only; or keys read back, for a rope shift).  Token i's pair j, at
+ * angle t = positions[i] * frequencies[j]:
+ *   a' = magnitude * (a cos t - b sin t),   b' = magnitude * (a sin t + b cos t)
+ * Pairs are dims (j, j + rot_dim/2) or, interleaved != 0, (2j, 2j+1), j < rot_dim/2; dims >= rot_dim are
+ * copied.  transpose != 0 turns the other way (t -> -t): the transposed map, which is the gradient's, and,
+ * at magnitude 1, the inverse.
+ *
+ * Angles are within 2^-27 turn at any position; cosines, sines, products and sums are float, rounded once to
+ * dtype.
+ * Frequencies must be finite and below 2^31 in magnitude.  A position outside (-2^31, 2^31) leaves the
+ * token's output rows unwritten and sets KVFP8_DEV_BAD_SLOT.
+ *
+ * query, key, outputs  device, dtype [num_tokens][heads][head_dim], row strides in elements (>= heads *
+ *                      head_dim; 16-byte rows); an output may be its own input (the same pointer and stride), and
+ *                      must not overlap inputs or the other output otherwise
+ * n_k                  0 without keys (key and key_out may be NULL then)
+ * head_dim             a multiple of 8, 16 to 256; rot_dim a multiple of 16, 16 to head_dim
+ * positions            device int64 [num_tokens]
+ * frequencies          device double [rot_dim/2], radians a position, 8-byte aligned
+ * magnitude            finite; num_tokens < 2^31; heads * head_dim <= 2^20
+ */
+KVFP8_API kvfp8_status kvfp8_rotary_embedding(void *query_out, void *key_out, int64_t query_out_stride,
+                                              int64_t key_out_stride, const void *query, const void *key,
+                                              int64_t query_stride, int64_t key_stride, kvfp8_dtype dtype,
+                                              int64_t num_tokens, int32_t n_q, int32_t n_k,
+                                              int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                              int32_t transpose, const int64_t *positions,
+                                              const double *frequencies, float magnitude,
+                                              uint32_t *status, kvfp8_stream_t stream);
 
 /*
  * Pages of any cache.  A cache here is a device array whose block i is the block_bytes bytes
