@@ -7,9 +7,8 @@
 // The angle is taken in turns as a 64-bit fraction: F = frequency / 2 pi in units of 2^-64 turn (its
 // whole turns dropped, which positions being whole numbers allow), and position * F modulo 2^64
 // drops the whole turns of the product exactly.  What is left is off by at most |position| * 2^-65 turn: far positions
-// are as exact as near ones, at one 64-bit multiplication per pair and token where a float64 product and
-// sine would go through the FP64 pipe (2 results a clock and SM here).  The nearest quarter turn is then
-// split off as an integer and sinpif / cospif see |x| <= 1/4.
+// are as exact as near ones, at one 64-bit multiplication per pair and token.  The nearest quarter turn is
+// then split off as an integer and sinpif / cospif see |x| <= 1/4.
 //
 // HBM-bound: each element is read and written once.  A warp takes a token's heads (or a part of them when
 // there are few tokens): its lanes share out the token's sines over shared memory once, then each lane
@@ -27,12 +26,25 @@ namespace {
 constexpr int kRotWarps = 8;
 constexpr int kMaxPairs = 128;  // of a head (head_dim <= 256)
 
-// frequency (radians a position) -> 2^-64 turns a position, whole turns dropped.  1 / 2 pi as the sum of
-// two doubles: the product is exact to 2^-100 of itself, so F is rounded once.
+// frequency (radians a position) -> 2^-64 turns a position, whole turns dropped, within one unit: its 53 bits
+// times 1 / 2 pi as a 128-bit fraction, shifted to where the exponent says.  (By float64 arithmetic the FP64
+// pipe was busy for 16 us of each call: 2 results a clock and SM.)
 __device__ __forceinline__ uint64_t turns_of(double f) {
-    const double c = 0.15915494309189535, c_lo = -9.839338337591243e-18;  // 1 / 2 pi
-    const double hi = f * c, lo = fma(f, c, -hi) + f * c_lo;
-    return __double2ull_rn((hi - floor(hi)) * 0x1p64) + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64));
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+    const int e = max(static_cast<int>((bits >> 52) & 0x7FFu), 1);
+    uint64_t m = bits & ((1ull << 52) - 1);
+    if ((bits >> 52) & 0x7FFu) m |= 1ull << 52;  // f = m 2^(e - 1075)
+    constexpr uint64_t kHi = 0xA2F9836E4E441529ull, kLo = 0xFC2757D1F534DDC0ull;  // 2^66 / 2 pi, 128 bits
+    uint64_t hi = __umul64hi(m, kHi);
+    const uint64_t part = __umul64hi(m, kLo), lo = m * kHi + part;
+    hi += lo < part;
+    const int s = 1077 - e;  // the product, as 2^-64 turns, is (hi, lo) >> s
+    uint64_t t = 0;
+    if (s >= 64)
+        t = s < 128 ? hi >> (s - 64) : 0;
+    else if (s > 0)  // (frequencies below 2^54)
+        t = hi << (64 - s) | lo >> s;
+    return bits >> 63 ? 0 - t : t;
 }
 
 // cosine and sine of phase * 2^-64 turns
