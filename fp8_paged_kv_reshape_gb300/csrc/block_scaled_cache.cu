@@ -2,17 +2,20 @@
 // are written) and read back by slot.
 //
 // Writing.  A block's new scale takes the largest element of all of this call's rows in the block, so the
-// rows of a block have to be found first: they may stand anywhere in the call.  A first kernel leaves
-// row_of[slot] = row for every row; nothing initializes row_of, because a row that it names counts only if
-// slot_mapping of that row is the slot, which holds exactly for the rows of this call whatever was there
-// before.  Of a block's rows the one with the lowest offset leads; the CTA that meets it writes the block.
-// (Calls of up to kDirectTokens rows look through slot_mapping instead: one launch.)
-//
-// A team of one to eight warps takes a (block, side, kv head): rows into registers, their maximum (of the
-// integer bits: a positive float's order is its bits' order), the scale, the codes.  A scale made here is a
-// power of two, so x / s is a multiplication, exact; and when a later call raises it, the
-// block's older codes are multiplied by a power of two and lose nothing but what leaves the bottom of E4M3's
-// range.  HBM-bound: rows are read once (blocks whose rows exceed a team's registers are read again, from L2).
+// rows of a block have to be found first: they may stand anywhere in the call.
+//  * Calls of up to kDirectTokens rows: a CTA per row looks through slot_mapping for the other rows of its
+//    row's block, and goes on if its row's offset is the lowest.  One launch.
+//  * Longer ones: mark_rows_kernel leaves row_of[slot] = row for every row.  Nothing initializes row_of: a row that
+//    it names counts only if slot_mapping of that row is the slot, which holds for the rows of this call alone, whatever
+//    was there before.  find_blocks_kernel lets the row of a block's lowest offset check the block's
+//    entries of row_of (-1 for those that do not count) and list the block; write_blocks_kernel, a persistent
+//    grid, takes the listed blocks.
+// The unit of work is a (block, side, kv head), by one warp, or by a team of warps where the block has more rows than
+// a warp's registers hold: rows into registers, their maximum (of the integer bits: a positive float's order is its
+// bits' order), the scale, the codes.  A scale made here is a power of two, so x / s is an exact
+// multiplication, and when a later call raises it the block's older codes are multiplied by a power of two and lose
+// nothing but what leaves the bottom of E4M3's range.
+// HBM-bound: rows are read once (those past a team's registers again, from L2).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,17 +27,12 @@
 namespace kvfp8 {
 namespace {
 
-constexpr int kWarps = 8;            // of a CTA
-constexpr int kDirectTokens = 512;   // rows up to which slot_mapping is searched instead of row_of
-constexpr int kPasses = 8;           // 32 * 8 elements each, held by a lane
-constexpr int kListWords = 4096;     // row lists of a CTA's leaders
+constexpr int kWarps = 8;           // of a CTA
+constexpr int kDirectTokens = 512;  // rows up to which slot_mapping is searched instead of row_of
 
-__global__ void __launch_bounds__(256) mark_rows_kernel(const BlockWriteArgs a) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= a.num_tokens) return;
-    const int64_t slot = a.slot_mapping[i];
-    if (slot >= 0 && slot < a.num_slots) a.row_of[slot] = static_cast<int32_t>(i);
-}
+// between the kernels of a long call (programmatic dependent launches)
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // The smallest k >= kMinScaleExp with 448 * 2^k >= a, as that power of two; a's bits, finite and not negative.
 __device__ __forceinline__ float power_for(uint32_t bits) {
@@ -59,31 +57,52 @@ __device__ __forceinline__ void team_sync(int id, int warps) {
 // eight elements of a row, in 16 bytes (bf16) or 32 (float)
 template <bool kF32>
 struct Elems {
-    uint32_t w[kF32 ? 8 : 4];
+    static constexpr int kPieces = kF32 ? 2 : 1;
+    uint4 v[kPieces];
     __device__ __forceinline__ void load(const char *p) {
 #pragma unroll
-        for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
+        for (int i = 0; i < kPieces; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0u;
+        for (int i = 0; i < kPieces; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     // the largest magnitude's bits (bf16: in either half)
     __device__ __forceinline__ uint32_t top(uint32_t m) const {
 #pragma unroll
-        for (int i = 0; i < (kF32 ? 8 : 4); ++i)
-            m = kF32 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (kF32)
+                m = max(max(max(m, v[i].x & 0x7FFFFFFFu), max(v[i].y & 0x7FFFFFFFu, v[i].z & 0x7FFFFFFFu)), v[i].w & 0x7FFFFFFFu);
+            else
+                m = __vmaxu2(__vmaxu2(m, v[i].x & 0x7FFF7FFFu),
+                             __vmaxu2(__vmaxu2(v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu), v[i].w & 0x7FFF7FFFu));
+        }
         return m;
     }
     __device__ __forceinline__ float at(int i) const {
-        if (kF32) return __uint_as_float(w[i]);
-        return i & 1 ? bf16hi(w[i / 2]) : bf16lo(w[i / 2]);
+        if constexpr (kF32) {
+            const uint4 &q = v[i / 4];
+            return __uint_as_float(i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w);
+        } else {
+            const uint32_t w = i / 2 == 0 ? v[0].x : i / 2 == 1 ? v[0].y : i / 2 == 2 ? v[0].z : v[0].w;
+            return i % 2 ? bf16hi(w) : bf16lo(w);
+        }
+    }
+    // the codes of these times inv, the inverse of a power of two (the products are the quotients)
+    __device__ __forceinline__ uint2 codes(float inv) const {
+        return make_uint2(codes4(__fmul_rn(at(0), inv), __fmul_rn(at(1), inv), __fmul_rn(at(2), inv), __fmul_rn(at(3), inv)),
+                          codes4(__fmul_rn(at(4), inv), __fmul_rn(at(5), inv), __fmul_rn(at(6), inv), __fmul_rn(at(7), inv)));
+    }
+    // the codes of the NaN among these: the element's sign and 0x7F
+    __device__ __forceinline__ void sign_nan(uint2 &w) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint(at(i));
+            if ((b & 0x7FFFFFFFu) > 0x7F800000u) {
+                uint32_t &word = i < 4 ? w.x : w.y;
+                word = (word & ~(0xFFu << (8 * (i % 4)))) | (0x7Fu | (b >> 31) << 7) << (8 * (i % 4));
+            }
+        }
     }
     // the largest finite magnitude's float bits
     __device__ __forceinline__ uint32_t finite_top(uint32_t m) const {
@@ -96,204 +115,399 @@ struct Elems {
     }
 };
 
+// passes of 32 lanes x 8 elements that a warp holds: 4 KB
+template <bool kF32>
+__host__ __device__ constexpr int passes() { return kF32 ? 4 : 8; }
 template <int HD, bool kF32>
-__global__ void __launch_bounds__(32 * kWarps) write_blocks_kernel(const BlockWriteArgs a, int rows_per_cta, int team_warps) {
-    constexpr int kEsz = kF32 ? 4 : 2;
-    constexpr int kLanes = HD / 8;         // lanes of a row
-    constexpr int kRows = 32 / kLanes;     // rows of a pass
-    extern __shared__ int32_t lists[];     // [rows_per_cta][block_size]: the leaders' rows by offset, -1 = none
-    __shared__ int64_t leader[128];        // their blocks
-    __shared__ int num_leaders;
-    __shared__ uint32_t team_top[kWarps], team_odd[kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int bs = 1 << a.block_shift, n = static_cast<int>(a.num_tokens);
-    if (threadIdx.x == 0) num_leaders = 0;
-    __syncthreads();
+__host__ __device__ constexpr int warp_rows() { return 32 / (HD / 8) * passes<kF32>(); }
 
-    // the rows that lead a block, and their blocks' rows
-    const int row0 = static_cast<int>(blockIdx.x) * rows_per_cta;
-    for (int r = warp; r < rows_per_cta && row0 + r < n; r += kWarps) {
-        const int i = row0 + r;
-        const int64_t slot = a.slot_mapping[i];
-        if (slot < 0 || slot >= a.num_slots) {
-            if (slot != -1 && lane == 0 && blockIdx.y == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
-            continue;
+constexpr int kMostHeld = 32;  // rows of 64 bf16
+
+// Shared memory of the teams.
+struct TeamTops {
+    uint32_t all[kWarps], finite[kWarps];
+    int2 rows[kWarps][kMostHeld];  // one warp to a task: its rows (offset, row)
+};
+
+// A (block, side, head) and the team that has it.
+struct Task {
+    const char *src;         // this lane's eight dims of row 0
+    uint8_t *codes;          // of the block's first token
+    float *scale;
+    const int32_t *list;     // the block's rows by offset, -1 = none
+    int64_t row_bytes;       // of src
+    int32_t code_row;        // bytes from token to token
+    int bs;
+    int team, team_warps, tw, lane;
+
+    // the maximum over the team's warps of one of each
+    __device__ __forceinline__ uint32_t team_max(uint32_t v, uint32_t *slots) const {
+        v = __reduce_max_sync(0xFFFFFFFFu, v);
+        if (team_warps > 1) {
+            if (lane == 0) slots[team * team_warps + tw] = v;
+            team_sync(team, team_warps);
+            for (int w = 0; w < team_warps; ++w) v = max(v, slots[team * team_warps + w]);
+            team_sync(team, team_warps);  // (read before it is written again)
         }
-        const int64_t block = slot >> a.block_shift, slot0 = block << a.block_shift;
-        const int off = static_cast<int>(slot - slot0);
-        if (off > 0 && i > 0 && a.slot_mapping[i - 1] == slot - 1) continue;  // a lower offset is written
-        int32_t *list = lists + r * bs;
-        if (a.row_of == nullptr) {
-            for (int o = lane; o < bs; o += 32) list[o] = -1;
-            __syncwarp();
-            for (int j = lane; j < n; j += 32) {
-                const int64_t s = a.slot_mapping[j];
-                if (s >= slot0 && s < slot0 + bs) atomicMax(&list[s - slot0], j);
+        return v;
+    }
+
+    // The block's new scale for rows of this maximum (0: none, what the block holds has no meaning), with its older codes
+    // under that.
+    template <int HD>
+    __device__ __forceinline__ float rescale(uint32_t top, float stored, uint32_t *status) const {
+        const float old = list[0] >= 0 ? 0.f : stored;  // the first token starts the block anew
+        if (old != 0.f && !block_scale_ok(old)) {
+            if (lane == 0 && tw == 0) flag(status, KVFP8_DEV_BAD_SCALE);
+            return 0.f;
+        }
+        const float s = fmaxf(old, power_for(top));
+        if (lane == 0 && tw == 0 && s != stored) *scale = s;
+        if (s == old || old == 0.f) return s;
+        round_older<HD>(old * block_scale_inverse(s));  // (exact, or below 2^-126, where all codes go to 0)
+        return s;
+    }
+
+    // The block's codes that the call does not write, times factor.
+    template <int HD>
+    __device__ __forceinline__ void round_older(float factor) const {
+        constexpr int kPieces = HD / 16, kBatch = 4;
+        const int step = 32 * team_warps;
+        for (int u = tw * 32 + lane; u < bs * kPieces; u += kBatch * step) {
+            uint4 v[kBatch];
+            uint4 *at[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int o = (u + b * step) / kPieces;
+                at[b] = o < bs && list[o] < 0
+                            ? reinterpret_cast<uint4 *>(codes + static_cast<int64_t>(o) * code_row + (u + b * step) % kPieces * 16)
+                            : nullptr;
+                if (at[b] != nullptr) v[b] = *at[b];
             }
-            __syncwarp();
-        }
-        bool lower = false;
-        for (int o = lane; o < bs; o += 32) {
-            int j;
-            if (a.row_of == nullptr) {
-                j = list[o];
-            } else {
-                j = a.row_of[slot0 + o];
-                if (static_cast<uint32_t>(j) >= static_cast<uint32_t>(n) || a.slot_mapping[j] != slot0 + o) j = -1;
-                list[o] = j;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (at[b] == nullptr) continue;
+                uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 lo = h2(f16x2_from_e4m3x2(w[i])), hi = h2(f16x2_from_e4m3x2_hi(w[i]));
+                    const uint32_t nan = nan_byte_mask(w[i]), was = w[i];
+                    w[i] = codes4(__fmul_rn(__low2float(lo), factor), __fmul_rn(__high2float(lo), factor),
+                                  __fmul_rn(__low2float(hi), factor), __fmul_rn(__high2float(hi), factor));
+                    w[i] = (w[i] & ~nan) | (was & nan);  // a NaN code stays as it is
+                }
+                *at[b] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            lower |= o < off && j >= 0;
-        }
-        __syncwarp();
-        if (!__any_sync(0xFFFFFFFFu, lower) && list[off] == i && lane == 0) {
-            const int k = atomicAdd(&num_leaders, 1);
-            leader[k] = static_cast<int64_t>(r) << 32 | block;
         }
     }
+
+    // The rows' codes under s, any elements; rows are read, a few at a time.
+    template <int HD, bool kF32>
+    __device__ __forceinline__ void write_codes(float s) const {
+        constexpr int kLanes = HD / 8, kRows = 32 / kLanes, kBatch = 4;
+        const float inv = block_scale_inverse(s);
+        const int step = team_warps * kRows;
+        for (int o = tw * kRows + lane / kLanes; o < bs; o += kBatch * step) {
+            Elems<kF32> x[kBatch];
+            int j[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                j[b] = o + b * step < bs ? list[o + b * step] : -1;
+                x[b].zero();
+                if (j[b] >= 0) x[b].load(src + j[b] * row_bytes);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (j[b] < 0) continue;
+                uint2 w = x[b].codes(inv);
+                x[b].sign_nan(w);
+                *reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(o + b * step) * code_row + lane % kLanes * 8) = w;
+            }
+        }
+    }
+
+    // The whole task, for rows that the team's registers do not hold or that have an infinity or NaN (the finite
+    // elements decide the scale then).
+    template <int HD, bool kF32>
+    __device__ __noinline__ void write_streamed(float stored, uint32_t *slots, uint32_t *status) const {
+        constexpr int kLanes = HD / 8, kRows = 32 / kLanes, kBatch = 4;
+        uint32_t top = 0;
+        const int step = team_warps * kRows;
+        for (int o = tw * kRows + lane / kLanes; o < bs; o += kBatch * step) {
+            Elems<kF32> x[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int j = o + b * step < bs ? list[o + b * step] : -1;
+                x[b].zero();
+                if (j >= 0) x[b].load(src + j * row_bytes);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) top = x[b].finite_top(top);
+        }
+        finish<HD, kF32>(team_max(top, slots), stored, status);
+    }
+
+    // What follows the maximum, for any scale.
+    template <int HD, bool kF32>
+    __device__ __noinline__ void finish(uint32_t top, float stored, uint32_t *status) const {
+        const float s = rescale<HD>(top, stored, status);
+        if (s != 0.f) write_codes<HD, kF32>(s);
+    }
+};
+
+template <int HD, bool kF32>
+__device__ __forceinline__ void write_task(const BlockWriteArgs &a, TeamTops &tops, int64_t block, const int32_t *list,
+                                           int task, int team, int team_warps, int tw, int lane) {
+    constexpr int kEsz = kF32 ? 4 : 2;
+    constexpr int kLanes = HD / 8;      // lanes of a row
+    constexpr int kRows = 32 / kLanes;  // rows of a pass
+    constexpr int kPasses = passes<kF32>();
+    const int side = task >= a.n_kv, head = task - (side ? a.n_kv : 0);
+    Task t;
+    t.src = static_cast<const char *>(a.src[side]) + (static_cast<int64_t>(head) * HD + lane % kLanes * 8) * kEsz;
+    t.codes = a.codes[side] + ((block << a.block_shift) * a.n_kv + head) * HD;
+    t.scale = a.scales[side] + block * a.scale_stride + head;
+    t.list = list;
+    t.row_bytes = a.stride[side] * kEsz;
+    t.code_row = a.n_kv * HD;
+    t.bs = 1 << a.block_shift;
+    t.team = team;
+    t.team_warps = team_warps;
+    t.tw = tw;
+    t.lane = lane;
+    const float stored = *t.scale;
+    // Pass p of this warp: the lane's row (x: its offset, y: itself, -1 = none).  A team takes the offsets as they
+    // are, one warp the rows that there are, one after the other.
+    int2 *mine = tops.rows[team];
+    int count = 0;
+    if (team_warps == 1) {
+        static_assert(warp_rows<HD, kF32>() <= kMostHeld, "rows");
+        __syncwarp();  // (the last task's have been read)
+        for (int o0 = 0; o0 < t.bs; o0 += 32) {
+            const int j = o0 + lane < t.bs ? list[o0 + lane] : -1;
+            const unsigned there = __ballot_sync(0xFFFFFFFFu, j >= 0);
+            const int at = count + __popc(there & ((1u << lane) - 1u));
+            if (j >= 0 && at < kMostHeld) mine[at] = make_int2(o0 + lane, j);
+            count += __popc(there);
+        }
+        __syncwarp();
+    }
+    auto row = [&](int p) {
+        if (team_warps == 1) {
+            const int e = p * kRows + lane / kLanes;
+            return e < count ? mine[e] : make_int2(0, -1);
+        }
+        const int o = (p * team_warps + tw) * kRows + lane / kLanes;
+        return make_int2(o, o < t.bs ? list[o] : -1);
+    };
+    Elems<kF32> x[kPasses];
+    uint32_t top = 0x7F800000u;
+    if (team_warps == 1 ? count <= warp_rows<HD, kF32>() : team_warps * warp_rows<HD, kF32>() >= t.bs) {
+        int j[kPasses];
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) j[p] = row(p).y;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            x[p].zero();
+            if (j[p] >= 0) x[p].load(t.src + j[p] * t.row_bytes);
+        }
+        top = 0;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) top = x[p].top(top);
+        if (!kF32) top = max(top & 0xFFFFu, top >> 16) << 16;
+        top = t.team_max(top, tops.all);
+    }
+    if (top >= 0x7F800000u) {
+        t.write_streamed<HD, kF32>(stored, tops.finite, a.status);
+        return;
+    }
+    // A block that starts anew, or whose scale holds the new rows; others (older codes to round again, a scale that
+    // is not valid) read their rows again.
+    const float old = list[0] >= 0 ? 0.f : stored, s = fmaxf(old, power_for(top));
+    if (old != 0.f && !(s == old && block_scale_ok(old))) {
+        t.finish<HD, kF32>(top, stored, a.status);
+        return;
+    }
+    if (lane == 0 && tw == 0 && s != stored) *t.scale = s;
+    const float inv = block_scale_inverse(s);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int2 at = row(p);
+        if (at.y >= 0)
+            *reinterpret_cast<uint2 *>(t.codes + static_cast<int64_t>(at.x) * t.code_row + lane % kLanes * 8) =
+                x[p].codes(inv);
+    }
+}
+
+// ---------------------------------------------------------------- short calls
+
+// CTA x: row x, if it leads its block; CTAs y share the block's tasks out.
+template <int HD, bool kF32>
+__global__ void __launch_bounds__(32 * kWarps, 4) write_rows_kernel(const __grid_constant__ BlockWriteArgs a) {
+    __shared__ int32_t list[256];
+    __shared__ TeamTops tops;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bs = 1 << a.block_shift, n = static_cast<int>(a.num_tokens);
+    const int i = static_cast<int>(blockIdx.x);
+    const int64_t slot = a.slot_mapping[i];
+    int64_t others[kDirectTokens / (32 * kWarps)];  // slots of rows threadIdx.x + 256 k
+#pragma unroll
+    for (int k = 0; k < kDirectTokens / (32 * kWarps); ++k) {
+        const int j = static_cast<int>(threadIdx.x) + 32 * kWarps * k;
+        others[k] = j < n ? a.slot_mapping[j] : -1;
+    }
+    list[threadIdx.x] = -1;
+    if (slot < 0 || slot >= a.num_slots) {
+        if (slot != -1 && threadIdx.x == 0 && blockIdx.y == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
+        return;
+    }
     __syncthreads();
+    const int64_t block = slot >> a.block_shift, slot0 = block << a.block_shift;
+#pragma unroll
+    for (int k = 0; k < kDirectTokens / (32 * kWarps); ++k)
+        if (others[k] >= slot0 && others[k] < slot0 + bs)  // (of a slot named twice, its last row)
+            atomicMax(&list[others[k] - slot0], static_cast<int>(threadIdx.x) + 32 * kWarps * k);
+    __syncthreads();
+    const int off = static_cast<int>(slot - slot0);
+    int rows = 0;  // of the block
+    bool leads = list[off] == i;
+    for (int o = 0; o < bs; o += 32) {
+        const bool there = o + lane < bs && list[o + lane] >= 0;
+        rows += __popc(__ballot_sync(0xFFFFFFFFu, there));
+        if (__any_sync(0xFFFFFFFFu, there && o + lane < off)) leads = false;
+    }
+    if (!leads) return;
+    // a warp to a task, unless the rows there are fill several
+    constexpr int kHeld = warp_rows<HD, kF32>();
+    int team_warps = 1;
+    if (rows > kHeld)
+        while (team_warps < kWarps && team_warps * kHeld < bs) team_warps *= 2;
+    const int teams = kWarps / team_warps, team = warp / team_warps;
+    for (int task = static_cast<int>(blockIdx.y) * teams + team; task < 2 * a.n_kv; task += static_cast<int>(gridDim.y) * teams)
+        write_task<HD, kF32>(a, tops, block, list, task, team, team_warps, warp % team_warps, lane);
+}
 
-    const int teams = kWarps / team_warps, team = warp / team_warps, tw = warp % team_warps;
+// ---------------------------------------------------------------- long calls
+
+// The workspace: row_of [num_slots], then the listed blocks [num_blocks], those whose rows a warp holds from the
+// front, the others from the back, then the number of either.
+__device__ __forceinline__ int32_t *listed_blocks(const BlockWriteArgs &a) { return a.row_of + a.num_slots; }
+__device__ __forceinline__ int32_t *listed_counts(const BlockWriteArgs &a) {
+    return listed_blocks(a) + (a.num_slots >> a.block_shift);
+}
+
+__global__ void __launch_bounds__(256) mark_rows_kernel(const __grid_constant__ BlockWriteArgs a) {
+    pdl_trigger();  // the next kernel may be launched; it waits for what this one writes
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i < 2) listed_counts(a)[i] = 0;
+    if (i >= a.num_tokens) return;
+    const int64_t slot = a.slot_mapping[i];
+    if (slot >= 0 && slot < a.num_slots)
+        a.row_of[slot] = static_cast<int32_t>(i);
+    else if (slot != -1)
+        flag(a.status, KVFP8_DEV_BAD_SLOT);
+}
+
+// A warp takes rows_per_warp (at most 32) rows; those whose slot does not follow the slot of the row before may lead a
+// block.
+__global__ void __launch_bounds__(256) find_blocks_kernel(const __grid_constant__ BlockWriteArgs a, int held, int rows_per_warp) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t n = a.num_tokens;
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * rows_per_warp + lane;
+    const int bs = 1 << a.block_shift;
+    const bool mine = lane < rows_per_warp && i < n;
+    const int64_t slot = mine ? a.slot_mapping[i] : -1, before = mine && i > 0 ? a.slot_mapping[i - 1] : -1;
+    const bool may = slot >= 0 && slot < a.num_slots && ((slot & (bs - 1)) == 0 || before != slot - 1);
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, may); left != 0u; left &= left - 1u) {
+        const int from = __ffs(left) - 1;
+        const int64_t s = __shfl_sync(0xFFFFFFFFu, slot, from);
+        const int row = static_cast<int>(__shfl_sync(0xFFFFFFFFu, i, from));
+        const int64_t slot0 = s & ~static_cast<int64_t>(bs - 1);
+        constexpr int kMost = 8;  // 32 offsets each
+        int j[kMost];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) j[k] = 32 * k + lane < bs ? a.row_of[slot0 + 32 * k + lane] : -1;
+        int64_t names[kMost];  // the slot of the row that an entry names
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            names[k] = static_cast<uint32_t>(j[k]) < static_cast<uint32_t>(n) ? a.slot_mapping[j[k]] : -1;
+        int first = -1, rows = 0;  // the row at the lowest offset
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const bool counts = names[k] == slot0 + 32 * k + lane;
+            const unsigned there = __ballot_sync(0xFFFFFFFFu, counts);
+            const int row_k = __shfl_sync(0xFFFFFFFFu, j[k], there != 0u ? __ffs(there) - 1 : 0);
+            if (rows == 0 && there != 0u) first = row_k;
+            rows += __popc(there);
+        }
+        if (first != row) continue;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            if (32 * k + lane < bs && names[k] != slot0 + 32 * k + lane) a.row_of[slot0 + 32 * k + lane] = -1;
+        if (lane == 0) {
+            const int many = rows > held;
+            const int at = atomicAdd(&listed_counts(a)[many], 1);
+            listed_blocks(a)[many ? (a.num_slots >> a.block_shift) - 1 - at : at] = static_cast<int32_t>(slot0 >> a.block_shift);
+        }
+    }
+}
+
+template <int HD, bool kF32>
+__global__ void __launch_bounds__(32 * kWarps, 4) write_blocks_kernel(const __grid_constant__ BlockWriteArgs a, int team_warps) {
+    __shared__ TeamTops tops;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
     const int tasks = 2 * a.n_kv;
-    const int col = lane % kLanes;  // the lane's eight dims
-    const int per_round = team_warps * kRows * kPasses;
-    const int rounds = (bs + per_round - 1) / per_round;
-    for (int li = 0; li < num_leaders; ++li) {
-        const int64_t block = leader[li] & 0xFFFFFFFF;
-        const int32_t *list = lists + (leader[li] >> 32) * bs;
-        const bool anew = list[0] >= 0;
-        for (int task = static_cast<int>(blockIdx.y) * teams + team; task < tasks; task += static_cast<int>(gridDim.y) * teams) {
-            const int side = task >= a.n_kv, head = task - (side ? a.n_kv : 0);
-            float *scale_at = a.scales[side] + block * a.scale_stride + head;
-            const float old = anew ? 0.f : *scale_at;
-            const char *src = static_cast<const char *>(a.src[side]) + (static_cast<int64_t>(head) * HD + col * 8) * kEsz;
-            const int64_t row_bytes = a.stride[side] * kEsz;
-            uint8_t *codes = a.codes[side] + ((block << a.block_shift) * a.n_kv + head) * HD;
-            const int64_t code_row = static_cast<int64_t>(a.n_kv) * HD;
-
-            Elems<kF32> x[kPasses];
-            auto offset = [&](int round, int p) { return ((round * kPasses + p) * team_warps + tw) * kRows + lane / kLanes; };
-            auto fetch = [&](int round) {
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    const int o = offset(round, p);
-                    const int j = o < bs ? list[o] : -1;
-                    if (j >= 0)
-                        x[p].load(src + j * row_bytes);
-                    else
-                        x[p].zero();
-                }
-            };
-            uint32_t top = 0;
-            for (int round = 0; round < rounds; ++round) {
-                fetch(round);
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) top = x[p].top(top);
-            }
-            if (!kF32) top = max(top & 0xFFFFu, top >> 16) << 16;
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            if (team_warps > 1) {
-                if (lane == 0) team_top[warp] = top;
-                team_sync(team, team_warps);
-                for (int w = 0; w < team_warps; ++w) top = max(top, team_top[team * team_warps + w]);
-                team_sync(team, team_warps);  // (read before it is written again)
-            }
-            const bool odd = top >= 0x7F800000u;  // an infinity or NaN somewhere: the finite elements decide
-            if (odd) {
-                top = 0;
-                for (int round = 0; round < rounds; ++round) {
-                    if (rounds > 1) fetch(round);
-#pragma unroll
-                    for (int p = 0; p < kPasses; ++p) top = x[p].finite_top(top);
-                }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                if (team_warps > 1) {
-                    if (lane == 0) team_odd[warp] = top;
-                    team_sync(team, team_warps);
-                    for (int w = 0; w < team_warps; ++w) top = max(top, team_odd[team * team_warps + w]);
-                    team_sync(team, team_warps);
-                }
-            }
-            if (old != 0.f && !block_scale_ok(old)) {  // what the block holds has no meaning: left as it is
-                if (lane == 0 && tw == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
-                continue;
-            }
-            const float s = fmaxf(old, power_for(top));
-            // 1 / s is exact where s is a power of two (always, but for scales that a user brought)
-            const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
-            const float inv = 1.f / s;
-            if (lane == 0 && tw == 0 && s != old) *scale_at = s;
-
-            if (s > old && old > 0.f) {  // older codes under the new scale
-                const float factor = old * inv;  // (s is a power of two here: exact, or below 2^-126 and all codes go to 0)
-                constexpr int kPieces = HD / 16;
-                for (int u = tw * 32 + lane; u < bs * kPieces; u += 32 * team_warps) {
-                    const int o = u / kPieces;
-                    if (list[o] >= 0) continue;
-                    uint4 *at = reinterpret_cast<uint4 *>(codes + o * code_row + u % kPieces * 16);
-                    const uint4 v = *at;
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __half2 lo = h2(f16x2_from_e4m3x2(w[i])), hi = h2(f16x2_from_e4m3x2_hi(w[i]));
-                        const uint32_t nan = nan_byte_mask(w[i]), was = w[i];
-                        w[i] = codes4(__fmul_rn(__low2float(lo), factor), __fmul_rn(__high2float(lo), factor),
-                                      __fmul_rn(__low2float(hi), factor), __fmul_rn(__high2float(hi), factor));
-                        w[i] = (w[i] & ~nan) | (was & nan);  // a NaN code stays as it is
-                    }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            for (int round = 0; round < rounds; ++round) {
-                if (rounds > 1) fetch(round);
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p) {
-                    const int o = offset(round, p);
-                    if (o >= bs || list[o] < 0) continue;
-                    float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = power ? __fmul_rn(x[p].at(i), inv) : __fdiv_rn(x[p].at(i), s);
-                    uint32_t w[2] = {codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7])};
-                    if (odd) {  // NaN: the element's sign and 0x7F
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t b = __float_as_uint(x[p].at(i));
-                            if ((b & 0x7FFFFFFFu) > 0x7F800000u) {
-                                const uint32_t code = 0x7Fu | (b >> 31) << 7;
-                                w[i / 4] = (w[i / 4] & ~(0xFFu << (8 * (i % 4)))) | code << (8 * (i % 4));
-                            }
-                        }
-                    }
-                    *reinterpret_cast<uint2 *>(codes + o * code_row + col * 8) = make_uint2(w[0], w[1]);
-                }
-            }
+    const int32_t *blocks = listed_blocks(a);
+    const int64_t num_blocks = a.num_slots >> a.block_shift;
+#pragma unroll 1
+    for (int many = 1; many >= 0; --many) {
+        const int w = many ? team_warps : 1;  // warps of a team
+        const int teams = kWarps / w, team = warp / w;
+        const int64_t items = static_cast<int64_t>(listed_counts(a)[many]) * tasks;
+#pragma unroll 1
+        for (int64_t item = static_cast<int64_t>(blockIdx.x) * teams + team; item < items; item += static_cast<int64_t>(gridDim.x) * teams) {
+            const int at = static_cast<int>(item / tasks), task = static_cast<int>(item - static_cast<int64_t>(at) * tasks);
+            const int64_t block = blocks[many ? num_blocks - 1 - at : at];
+            write_task<HD, kF32>(a, tops, block, a.row_of + (block << a.block_shift), task, team, w, warp % w, lane);
         }
     }
 }
 
 // ---------------------------------------------------------------- rows read back
 
-// A thread takes 16 codes of a row at a time, kUnits of them in flight.
-template <bool kBF16>
+// A thread takes 16 codes of a row at a time, kUnits of them in flight.  kWide: 32-byte stores.
+template <bool kBF16, bool kWide>
 __global__ void __launch_bounds__(256) read_blocks_kernel(const BlockReadArgs a) {
     constexpr int kUnits = 4;
-    const int64_t pieces = static_cast<int64_t>(a.n_kv) * a.head_dim / 16;  // of a row
+    const uint32_t pieces = static_cast<uint32_t>(a.n_kv) * a.head_dim / 16;  // of a row
     const int64_t units = a.num_tokens * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    const int head_shift = a.head_shift;  // log2(head_dim / 16)
-    for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; u0 < units; u0 += kUnits * step) {
+    int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    int64_t row = u / pieces;
+    uint32_t piece = static_cast<uint32_t>(u - row * pieces);
+    const int64_t row_step = step / pieces;
+    const uint32_t piece_step = static_cast<uint32_t>(step - row_step * pieces);
+    while (u < units) {
         int64_t slot[kUnits];
-        int piece[kUnits];
+        uint32_t at[kUnits];
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
-            const int64_t u = u0 + k * step;
             slot[k] = -1;
-            if (u < units) {
-                const int64_t row = u / pieces;
-                piece[k] = static_cast<int>(u - row * pieces);
-                slot[k] = a.slot_mapping[row];
+            at[k] = piece;
+            if (u + k * step < units) {
+                slot[k] = __ldg(a.slot_mapping + row);
                 if (slot[k] < -1 || slot[k] >= a.num_slots) {
-                    if (piece[k] == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
+                    if (piece == 0) flag(a.status, KVFP8_DEV_BAD_SLOT);
                     slot[k] = -1;
                 }
+            }
+            row += row_step;
+            piece += piece_step;
+            if (piece >= pieces) {
+                piece -= pieces;
+                ++row;
             }
         }
         uint4 c[kUnits];
@@ -303,19 +517,18 @@ __global__ void __launch_bounds__(256) read_blocks_kernel(const BlockReadArgs a)
             c[k] = make_uint4(0u, 0u, 0u, 0u);
             s[k] = 1.f;
             if (slot[k] >= 0) {
-                c[k] = __ldg(reinterpret_cast<const uint4 *>(a.codes) + slot[k] * pieces + piece[k]);
-                s[k] = __ldg(a.scales + (slot[k] >> a.block_shift) * a.scale_stride + (piece[k] >> head_shift));
-                if (!block_scale_ok(s[k])) {
-                    flag(a.status, KVFP8_DEV_BAD_SCALE);
-                    c[k] = make_uint4(0u, 0u, 0u, 0u);
-                    s[k] = 1.f;
-                }
+                c[k] = __ldg(reinterpret_cast<const uint4 *>(a.codes) + slot[k] * pieces + at[k]);
+                s[k] = __ldg(a.scales + (slot[k] >> a.block_shift) * a.scale_stride + (at[k] >> a.head_shift));
             }
         }
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int64_t u = u0 + k * step;
+        for (int k = 0; k < kUnits; ++k, u += step) {
             if (u >= units) break;
+            if (!block_scale_ok(s[k])) {
+                flag(a.status, KVFP8_DEV_BAD_SCALE);
+                c[k] = make_uint4(0u, 0u, 0u, 0u);
+                s[k] = 1.f;
+            }
             const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
             uint32_t o[16];
 #pragma unroll
@@ -329,9 +542,19 @@ __global__ void __launch_bounds__(256) read_blocks_kernel(const BlockReadArgs a)
                     o[2 * i + 1] = __float_as_uint(hi);
                 }
             }
-            uint4 *p = static_cast<uint4 *>(a.dst) + u * (kBF16 ? 2 : 4);
+            uint8_t *p = static_cast<uint8_t *>(a.dst) + u * (kBF16 ? 32 : 64);
 #pragma unroll
-            for (int i = 0; i < (kBF16 ? 2 : 4); ++i) p[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < (kBF16 ? 8 : 16); i += 8) {
+                if (kWide) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 4 * i), "r"(o[i]),
+                                 "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                                 "r"(o[i + 7])
+                                 : "memory");
+                } else {
+                    *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    *reinterpret_cast<uint4 *>(p + 4 * i + 16) = make_uint4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+                }
+            }
         }
     }
 }
@@ -341,29 +564,44 @@ cudaError_t run_write(const BlockWriteArgs &a, cudaStream_t stream) {
     DeviceFacts f;
     cudaError_t err = device_facts(&f);
     if (err != cudaSuccess) return err;
-    const int bs = 1 << a.block_shift;
-    constexpr int kTeamRows = 32 / (HD / 8) * kPasses;
-    const int team_warps = std::max(1, std::min(kWarps, bs / kTeamRows));
-    // Rows a CTA looks at: 16 of the rows of a long call, one of a few hundred.
-    const int rows_per_cta = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(std::min(128, std::max(1, kListWords / bs)), a.num_tokens / (4 * f.sms))));
-    const int64_t ctas = (a.num_tokens + rows_per_cta - 1) / rows_per_cta;
-    // the (side, head) tasks of a block over several CTAs where there are few blocks
-    const int teams = kWarps / team_warps, most = (2 * a.n_kv + teams - 1) / teams;
-    const int64_t blocks = std::max<int64_t>(1, a.num_tokens / bs);
-    const int y = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most, 8 * f.sms / blocks, 65535})));
-    if (a.row_of != nullptr) {
-        mark_rows_kernel<<<static_cast<unsigned>((a.num_tokens + 255) / 256), 256, 0, stream>>>(a);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    constexpr int kHeld = warp_rows<HD, kF32>();
+    if (a.row_of == nullptr) {
+        const int64_t most = (2 * a.n_kv + kWarps - 1) / kWarps;  // CTAs that a block's tasks fill, a warp each
+        const int y = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({most, 4 * f.sms / a.num_tokens, 65535})));
+        write_rows_kernel<HD, kF32><<<dim3(static_cast<unsigned>(a.num_tokens), y), 32 * kWarps, 0, stream>>>(a);
+        return cudaGetLastError();
     }
-    write_blocks_kernel<HD, kF32><<<dim3(static_cast<unsigned>(ctas), y), 32 * kWarps, rows_per_cta * bs * sizeof(int32_t), stream>>>(
-        a, rows_per_cta, team_warps);
-    return cudaGetLastError();
+    const unsigned by_row = static_cast<unsigned>((a.num_tokens + 255) / 256);
+    mark_rows_kernel<<<by_row, 256, 0, stream>>>(a);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    // (a row that may lead costs a warp two reads one after the other: as many warps as the GPU holds)
+    const int rows_per_warp = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, a.num_tokens / (32 * f.sms))));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.num_tokens + kWarps * rows_per_warp - 1) / (kWarps * rows_per_warp)));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((err = cudaLaunchKernelEx(&cfg, find_blocks_kernel, a, kHeld, rows_per_warp)) != cudaSuccess) return err;
+    auto kern = write_blocks_kernel<HD, kF32>;
+    int occ = 0;
+    if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
+    const int team_warps = std::max(1, std::min(kWarps, (1 << a.block_shift) / kHeld));
+    const int64_t warps = a.num_tokens * 2 * a.n_kv;  // a warp to a row's heads is the most there can be
+    const int ctas = static_cast<int>(std::min<int64_t>((warps + kWarps - 1) / kWarps, static_cast<int64_t>(f.sms) * std::max(occ, 1)));
+    cfg.gridDim = dim3(ctas);
+    return cudaLaunchKernelEx(&cfg, kern, a, team_warps);
 }
 
 }  // namespace
 
-bool block_write_needs_rows(int64_t num_tokens) { return num_tokens > kDirectTokens; }
+size_t block_write_workspace_size(int64_t num_tokens, int32_t num_blocks, int32_t block_size) {
+    if (num_tokens <= kDirectTokens) return 0;
+    return (static_cast<size_t>(num_blocks) * block_size + num_blocks + 2) * sizeof(int32_t);
+}
 
 cudaError_t launch_reshape_and_cache_block_scaled(const BlockWriteArgs &a, cudaStream_t stream) {
     const bool f32 = a.src_dtype == KVFP8_F32;
@@ -379,7 +617,9 @@ cudaError_t launch_dequant_block_scaled(const BlockReadArgs &a, cudaStream_t str
     DeviceFacts f;
     cudaError_t err = device_facts(&f);
     if (err != cudaSuccess) return err;
-    auto kern = a.dst_dtype == KVFP8_BF16 ? read_blocks_kernel<true> : read_blocks_kernel<false>;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.dst) & 31u) == 0;
+    auto kern = a.dst_dtype == KVFP8_BF16 ? (wide ? read_blocks_kernel<true, true> : read_blocks_kernel<true, false>)
+                                          : (wide ? read_blocks_kernel<false, true> : read_blocks_kernel<false, false>);
     int occ = 0;
     if ((err = kernel_occupancy(kern, 256, 0, &occ)) != cudaSuccess) return err;
     const int64_t units = a.num_tokens * a.n_kv * (a.head_dim / 16);

@@ -733,8 +733,8 @@ kvfp8_status kvfp8_paged_attention_multi_fp4(
 
 size_t kvfp8_reshape_and_cache_block_scaled_workspace_size(int64_t num_tokens, int32_t num_blocks,
                                                            int32_t block_size) {
-    if (num_blocks < 1 || block_size < 1 || !kvfp8::block_write_needs_rows(num_tokens)) return 0;
-    return static_cast<size_t>(num_blocks) * static_cast<size_t>(block_size) * sizeof(int32_t);
+    if (num_blocks < 1 || block_size < 1) return 0;
+    return kvfp8::block_write_workspace_size(num_tokens, num_blocks, block_size);
 }
 
 kvfp8_status kvfp8_reshape_and_cache_block_scaled(

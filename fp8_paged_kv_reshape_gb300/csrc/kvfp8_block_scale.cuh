@@ -7,13 +7,19 @@
 
 namespace kvfp8 {
 
-// Scales lie between 2^-60 and 2^120.  120 is what the largest float needs (448 * 2^120 >= 2^128).  -60
-// keeps 1 / s, which the attention kernels sum weights by, and such a sum over 2^31 tokens within float's
+// Scales are powers of two from 2^-60 to 2^120.  120 is what the largest float needs (448 * 2^120 >= 2^128).
+// -60 keeps 1 / s, which the attention kernels sum weights by, and such a sum over 2^31 tokens within float's
 // range.
 constexpr int kMinScaleExp = -60, kMaxScaleExp = 120;
 
-// (false for a NaN; 0 is a block that nothing was written to)
-__device__ __forceinline__ bool block_scale_ok(float s) { return s >= 0x1p-60f && s <= 0x1p120f; }
+// (0 is a block that nothing was written to)
+__device__ __forceinline__ bool block_scale_ok(float s) {
+    const uint32_t bits = __float_as_uint(s);
+    constexpr uint32_t kLow = (kMinScaleExp + 127u) << 23, kHigh = (kMaxScaleExp + 127u) << 23;
+    return (bits & 0x7FFFFFu) == 0u && bits - kLow <= kHigh - kLow;
+}
+// 1 / s, exactly
+__device__ __forceinline__ float block_scale_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 __device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 

@@ -260,12 +260,12 @@ struct BlockWriteArgs {
     int64_t num_tokens, num_slots;
     int32_t block_shift, n_kv, head_dim;  // blocks of 1 << block_shift tokens
     const int64_t *slot_mapping;
-    int32_t *row_of;         // [num_slots], any contents; nullptr where block_write_needs_rows is false
+    int32_t *row_of;         // the workspace, any contents; nullptr where its size is 0
     uint32_t *status;
 };
 cudaError_t launch_reshape_and_cache_block_scaled(const BlockWriteArgs &a, cudaStream_t stream);
-// True when a call of this many rows finds a block's rows through a workspace.
-bool block_write_needs_rows(int64_t num_tokens);
+// What a call of this many rows finds the blocks' rows by (0: few rows need none).
+size_t block_write_workspace_size(int64_t num_tokens, int32_t num_blocks, int32_t block_size);
 
 struct BlockReadArgs {
     void *dst;

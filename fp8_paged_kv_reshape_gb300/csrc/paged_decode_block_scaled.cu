@@ -319,8 +319,8 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     }
                     // (kept away from 0 and infinity, which would make a NaN of a score of infinity or 0)
                     kmul[tt] = fminf(fmaxf(ks * score_scale, 0x1p-126f), 0x1p126f);
-                    vlog[tt] = __log2f(vs);
-                    vinv[tt] = 1.f / vs;
+                    vlog[tt] = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
+                    vinv[tt] = block_scale_inverse(vs);
                 }
                 if (bad && lane == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
             }

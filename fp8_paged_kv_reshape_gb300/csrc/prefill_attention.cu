@@ -512,31 +512,73 @@ __device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], 
 
 // ---------------------------------------------------------------- block scales
 //
-// Cache::kBlocks: a block is 16 keys at least, so 16 keys in a row (a group) have one K and one V scale.  The
-// codes are converted as they are.  The softmax multiplies a group's scores by its ks; its vs goes into the
-// exponent, so that the weights that meet V are 2^(s + log2 vs - m) with m near the highest s + log2 vs,
-// within fp16's range whatever the scales, and the row's sum adds a group's weights times 1 / vs.  Weights
-// are held as over the 4-bit cache (kF4Head).
+// Cache::kBlocks: a block is 16 keys at least, so 16 keys in a row (a group) have one K and one V scale, powers of
+// two.  The conversion multiplies a group's fp16 codes by its scale over 2^-7 of the largest of its 64 keys: exact
+// where scales there are within 2^22 of each other (a product is a multiple of fp16's 2^-24 then), a multiple of
+// 2^-24 where 448 times the largest scale is 2^15.8 otherwise.  The softmax is left with one K and one V scale per 64 keys: ks
+// multiplies the scores; vs goes into the exponent, so that the weights that meet V are 2^(s + log2 vs - m) with m
+// near the highest s + log2 vs, within fp16's range whatever the scales, and the row's sum adds the weights
+// times 1 / vs.  Weights are held as over the 4-bit cache (kF4Head).  (With a multiplier per 16 keys in the softmax:
+// 732 us for 512 new tokens of 16 sequences of 4096.)
 //
 // NaN: a NaN code in K makes the key's scores NaN, which the masks keep from rows that do not see it.  One
 // in V may reach all rows where all of them see the key.  Where not (the last tiles of a causal call), such codes are
 // taken as 0, the CTA remembers that it met one, and at the end its rows look up which dims of the values
 // they see are NaN (a slow scan that no finite cache runs).
 
-// what the softmax takes of a group's scales: scores * kmul are in the log2 domain
+// what the softmax takes of 64 keys' scales: scores * kmul are in the log2 domain
 struct BlockMul {
     float kmul, vlog, vinv;
 };
-__device__ __forceinline__ BlockMul block_mul(float ks, float vs, float score_scale) {
-    // (kmul is kept away from 0 and infinity, which would make a NaN of a score of infinity or 0)
-    return BlockMul{fminf(fmaxf(ks * score_scale, 0x1p-126f), 0x1p126f), __log2f(vs), 1.f / vs};
+__device__ __forceinline__ BlockMul get_block_mul(const uint8_t *at) {
+    const float4 v = *reinterpret_cast<const float4 *>(at);
+    return BlockMul{v.x, v.y, v.z};
 }
-__device__ __forceinline__ BlockMul get_block_mul(uint32_t addr) {
-    BlockMul m;
-    float none;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(m.kmul), "=f"(m.vlog), "=f"(m.vinv), "=f"(none) : "r"(addr));
-    return m;
-}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b);
+
+// The scales of 64 keys: which groups have valid ones, the largest of them, and each as an fp16 pair over 2^-7 of
+// the largest.
+struct BlockScales {
+    uint64_t keys;       // those of `mask` in groups with valid scales
+    float kref, vref;    // 1 without any
+    uint32_t k[4], v[4];
+
+    __device__ __forceinline__ static uint32_t over(float s, float ref) {
+        // 2^(7 - d), d = log2(ref / s): an fp16 number, or one of its denormals, or 0
+        const int e = static_cast<int>(__float_as_uint(s) >> 23) - static_cast<int>(__float_as_uint(ref) >> 23) + 22;
+        const uint32_t h = e >= 1 ? static_cast<uint32_t>(e) << 10 : e >= -9 ? 1u << (9 + e) : 0u;
+        return h * 0x10001u;
+    }
+    // (a group without keys has no scales either: what stands there is of another tile)
+    __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask) {
+        const float4 k4 = *reinterpret_cast<const float4 *>(at), v4 = *reinterpret_cast<const float4 *>(at + 16);
+        const float ks[4] = {k4.x, k4.y, k4.z, k4.w}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
+        keys = 0;
+        kref = vref = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint64_t group = mask & (0xFFFFull << (16 * g));
+            if (group == 0ull || !(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) continue;
+            keys |= group;
+            kref = fmaxf(kref, ks[g]);
+            vref = fmaxf(vref, vs[g]);
+        }
+        if (keys == 0ull) kref = vref = 1.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // (0 for a group without, whatever its scales' bits)
+            const bool ok = (keys & (0xFFFFull << (16 * g))) != 0ull;
+            k[g] = ok ? over(ks[g], kref) : 0u;
+            v[g] = ok ? over(vs[g], vref) : 0u;
+        }
+    }
+    __device__ __forceinline__ void put_mul(float score_scale, uint8_t *at) const {
+        // (kmul is kept away from 0 and infinity, which would make a NaN of a score of infinity or 0)
+        *reinterpret_cast<float4 *>(at) =
+            make_float4(fminf(fmaxf(kref * 0x1p-7f * score_scale, 0x1p-126f), 0x1p126f),
+                        static_cast<float>(static_cast<int>(__float_as_uint(vref) >> 23) - 134),
+                        __uint_as_float((261u << 23) - __float_as_uint(vref)), 0.f);
+    }
+};
 
 // The scales of 64 keys from t0 on, [side][16 keys] at dst, by the TMA warp; every lane adds the completion of
 // its copies to the stage's barrier.  win: the lane window of block-table entries from wbase on.
@@ -549,30 +591,6 @@ __device__ __forceinline__ void copy_block_scales(const PrefillArgs<Cache::kBloc
                      "l"((lane < 4 ? a.key_scales : a.value_scales) + static_cast<int64_t>(blk) * a.scale_stride + kvh)
                      : "memory");
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// The keys of a stage, in groups of 16, without those whose block has no valid scales.
-__device__ __forceinline__ uint64_t keys_with_scales(uint32_t scales, uint64_t mask, bool report, uint32_t *status) {
-    float ks[4], vs[4];
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(ks[0]), "=f"(ks[1]), "=f"(ks[2]), "=f"(ks[3]) : "r"(scales));
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(vs[0]), "=f"(vs[1]), "=f"(vs[2]), "=f"(vs[3]) : "r"(scales + 16));
-    uint64_t without = 0;
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-        if (!(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) without |= 0xFFFFull << (16 * g);
-    if (report && (mask & without) != 0ull) flag(status, KVFP8_DEV_BAD_SCALE);
-    return mask & ~without;
-}
-// What the softmax takes of group g's scales, at out.
-__device__ __forceinline__ void put_block_mul(uint32_t scales, int g, float score_scale, uint32_t out) {
-    float ks, vs;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(scales + 4 * g));
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(scales + 16 + 4 * g));
-    const bool ok = block_scale_ok(ks) && block_scale_ok(vs);  // (else its keys are masked)
-    const BlockMul m = block_mul(ok ? ks : 1.f, ok ? vs : 1.f, score_scale);
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(out + 16 * g), "f"(m.kmul), "f"(m.vlog), "f"(m.vinv),
-                 "f"(0.f)
-                 : "memory");
 }
 
 // NaN codes of V -> 0, remembered
@@ -616,14 +634,6 @@ __device__ __noinline__ uint32_t nan_value_dims(const PrefillArgs<Cache::kBlocks
     if (last < 0) return 0u;
     for (int t = max(first, all + 1); t <= last; ++t) look(t);
     return dims;
-}
-
-// the largest of 16 scores
-__device__ __forceinline__ float max16(const uint32_t *s) {
-    auto v = [&](int c) { return __uint_as_float(s[c]); };
-    const float a = max3f(max3f(v(0), v(1), v(2)), v(3), v(4)), b = max3f(max3f(v(5), v(6), v(7)), v(8), v(9));
-    const float c = max3f(max3f(v(10), v(11), v(12)), v(13), v(14));
-    return max3f(max3f(a, b, c), v(15), v(15));
 }
 
 // ---------------------------------------------------------------- work order
@@ -771,7 +781,7 @@ struct PfSmem {
     static constexpr int kMisc = kBufMask + 8 * kNB;               // tmem base, abort flag, NaN seen
     // BS: a stage's scales ([side][16 keys]) and, per buffer, what the softmax takes of them (BlockMul)
     static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
-    static constexpr int kTotal = kBufBs + (BS ? 64 * kNB : 0);
+    static constexpr int kTotal = kBufBs + (BS ? 16 * kNB : 0);
     // tensor memory: S[NB] (64 fp32 columns each; P as f16 over the first 32), then O
     static constexpr uint32_t kColO = 64 * kNB;
     static constexpr uint32_t kTmemCols = kColO + HD + 32 <= 256 ? 256 : 512;
@@ -1094,11 +1104,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                                 mbar_wait(bar(L::kKvFree, b), ((i / L::kNB) & 1) ^ 1u, abort_flag));
             if (!ok) break;
             uint64_t mask = meta[st];
+            BlockScales sc;
             if constexpr (BS) {
-                const uint32_t scales = base + L::kStageBs + 32 * st;
-                mask = keys_with_scales(scales, mask, ct == 0, a.status);
-                if (ct < 4) put_block_mul(scales, ct, a.sm_scale * 1.4426950408889634f, base + L::kBufBs + 64 * b);
+                sc.load(bp + L::kStageBs + 32 * st, mask);
+                if (ct == 0) {
+                    if (mask != sc.keys) flag(a.status, KVFP8_DEV_BAD_SCALE);
+                    sc.put_mul(a.sm_scale * 1.4426950408889634f, bp + L::kBufBs + 16 * b);
+                }
+                mask = sc.keys;
             }
+            // a warp's V blocks are of eight keys, the same in every round
+            const int w4 = warp - 4;
+            const uint32_t vmul[1] = {BS ? (w4 < 4 ? (w4 < 2 ? sc.v[0] : sc.v[1]) : (w4 < 6 ? sc.v[2] : sc.v[3])) : 0u};
             // where some row does not see every key, NaN codes of V are taken out
             const bool drop_nan = BS && (key_tile(i) + 1) * kPfKeys > all_see;
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
@@ -1116,7 +1133,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             constexpr int kKT = kPfKeys * (HD / 8) / kCT;                    // K tasks per thread
             constexpr int kVB = (kPfKeys / 8) * (HD / 32) / kPfConvWarps;    // V^T blocks per warp
             constexpr int kVG = kVB < 4 ? kVB : 4;                           // V^T blocks per round
-            const int w4 = warp - 4;
             const uint32_t vbase = base + L::kV + b * L::kVBuf;
             const uint32_t vsel = static_cast<uint32_t>(2 * (lane & 3)) | static_cast<uint32_t>(2 * (lane & 3) + 1) << 4;
             uint2 kw[kKT];
@@ -1148,7 +1164,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     uint32_t r[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)  // bytes 8q + 2(t%4), +1 of the key's 32
+                    {
                         r[q] = f16x2_from_e4m3x2(__byte_perm(wd[2 * q], wd[2 * q + 1], vsel));
+                        if (BS) r[q] = mul_f16x2(r[q], vmul[0]);
+                    }
                     const int n = 32 * dg + 8 * (lane >> 3) + (lane & 7);  // V^T row this lane addresses
                     stsm_x4_t(vbase + sw128(n, ko), r[0], r[1], r[2], r[3]);
                 }
@@ -1202,6 +1221,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 h.y = f16x2_from_e4m3x2_hi(w.x);
                 h.z = f16x2_from_e4m3x2(w.y);
                 h.w = f16x2_from_e4m3x2_hi(w.y);
+                if constexpr (BS) {
+                    constexpr int kPass = kCT / (HD / 8);  // keys of a round of tasks: 8, 16 or 32
+                    const uint32_t m = kPass <= 16 ? sc.k[j * kPass / 16] : ct < kCT / 2 ? sc.k[2 * j] : sc.k[2 * j + 1];
+                    h = make_uint4(mul_f16x2(h.x, m), mul_f16x2(h.y, m), mul_f16x2(h.z, m), mul_f16x2(h.w, m));
+                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kPfKeys * 128) + sw128(key, c & 7)) = h;
             }
             v_store(0);
@@ -1253,10 +1277,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             // the scale is applied inside the exponent's fma.
             const int k0 = key_tile(i) * kPfKeys;
             const int vis_n = row_ok ? min(kPfKeys, max(0, pos - k0 + 1)) : 0;  // keys 0..vis_n-1
-            const uint64_t vis = mask & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
+            uint64_t vis = mask & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
+            if (BS && !row_ok) vis = ~0ull;  // (a padding row holds no warp back)
             float mx, mult = 1.f;
-            BlockMul group[4];  // BS: of 16 keys each
+            BlockMul mul = {};
             if constexpr (BS) {
+                mul = get_block_mul(bp + L::kBufBs + 16 * b);
                 if (!__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -1264,12 +1290,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                         for (int c = 0; c < 32; ++c)
                             if (!((vis >> (32 * h + c)) & 1ull)) s[h][c] = 0xFF800000u;  // -infinity
                 }
-                mx = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    group[g] = get_block_mul(base + L::kBufBs + 64 * b + 16 * g);
-                    mx = fmaxf(mx, fmaf(max16(s[g >> 1] + 16 * (g & 1)), group[g].kmul, group[g].vlog));
-                }
+                mx = fmaf(extreme64<true>(s), mul.kmul, mul.vlog);
+                mult = mul.kmul;
             } else if (__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
                 mx = (score_scale >= 0.f ? extreme64<true>(s) : extreme64<false>(s)) * score_scale;
                 mult = score_scale;
@@ -1321,31 +1343,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             // of 8 to 16 moves a weight by up to 2^-8.5, a rounded weight by 2^-11.
             uint32_t p[32];
             const float msub = m_used == -INFINITY ? 0.f : m_used;
-            const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(-msub, -msub);
-            if constexpr (BS) {
+            const float shift = (BS ? mul.vlog : 0.f) - msub;
+            const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(shift, shift);
+            uint64_t sum2 = pk2(0.f, 0.f);  // BS: of the tile's weights
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float less = group[g].vlog - msub;
-                    const uint64_t gmul2 = pk2(group[g].kmul, group[g].kmul), gsub2 = pk2(less, less);
-                    uint64_t sum2 = pk2(0.f, 0.f);
-#pragma unroll
-                    for (int c = 8 * g; c < 8 * g + 8; ++c) {
-                        const int h = c >> 4, e = (2 * c) & 31;
-                        const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), gmul2, gsub2));
-                        const float e0 = ex2(x.x), e1 = ex2(x.y);
-                        p[c] = f16x2_from_f32(e0, e1);
-                        sum2 = add_f32x2(sum2, pk2(e0, e1));
-                    }
-                    const float2 sum = upk2(sum2);
-                    lsum = fmaf(sum.x + sum.y, group[g].vinv, lsum);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < (BS ? 0 : 32); ++c) {
+            for (int c = 0; c < 32; ++c) {
                 const int h = c >> 4, e = (2 * c) & 31;
                 const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), mul2, sub2));
+                if constexpr (BS) {
+                    const float e0 = ex2(x.x), e1 = ex2(x.y);
+                    p[c] = f16x2_from_f32(e0, e1);
+                    sum2 = add_f32x2(sum2, pk2(e0, e1));
+                    continue;
+                }
                 p[c] = F4 ? f16x2_from_f32(ex2(x.x), ex2(x.y)) : ex2_f16x2(f16x2_from_f32(x.x, x.y));
                 if (!L::kSumCol) lsum += f16lo_f32(p[c]) + f16hi_f32(p[c]);
+            }
+            if constexpr (BS) {
+                const float2 sum = upk2(sum2);
+                lsum = fmaf(sum.x + sum.y, mul.vinv, lsum);
             }
             tmem_st32(lane_addr + 64 * b, p);
             tmem_wait_st();
@@ -1382,13 +1398,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld32(lane_addr + L::kColO + c0, o);
-                tmem_wait_ld();
                 if constexpr (BS) {
                     if (any_nan)
                         nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
                 }
+                uint32_t o[32];
+                tmem_ld32(lane_addr + L::kColO + c0, o);
+                tmem_wait_ld();
                 if constexpr (kSplit) {
                     if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
                 } else if (row_ok) {
@@ -1480,9 +1496,9 @@ struct Pf2Smem {
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // per V^T buffer, two halves
     static constexpr int kMisc = kBufMask + 32;                    // tmem base, abort flag, NaN seen
-    // BS: a stage's scales ([side][16 keys]) and, per buffer of two halves, what the softmax takes of them
+    // BS: a stage's scales ([side][16 keys]) and, per buffer and half, what the softmax takes of them
     static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
-    static constexpr int kTotal = kBufBs + (BS ? 256 : 0);
+    static constexpr int kTotal = kBufBs + (BS ? 64 : 0);
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t col_s(int r) { return static_cast<uint32_t>(128 * r); }
     __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(256 + HD * r); }
@@ -1810,8 +1826,14 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                                 mbar_wait(bar(L::kKFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
             uint64_t mask = meta[st];
-            const uint32_t scales_at = base + L::kStageBs + 32 * st;
-            if (BS) mask = keys_with_scales(scales_at, mask, ct == 0, a.status);
+            BlockScales sc;
+            if constexpr (BS) {
+                sc.load(bp + L::kStageBs + 32 * st, mask);
+                if (ct == 0 && mask != sc.keys) flag(a.status, KVFP8_DEV_BAD_SCALE);
+                mask = sc.keys;
+            }
+            // a warp's V blocks are of eight keys, 32 apart from round to round
+            const uint32_t vmul[2] = {BS ? (w8 < 2 ? sc.v[0] : sc.v[1]) : 0u, BS ? (w8 < 2 ? sc.v[2] : sc.v[3]) : 0u};
             const bool drop_nan = BS && key_tile(i) * kP2Keys + (hf + 1) * kPfKeys > all_see;  // as in the one-row-tile kernel
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
@@ -1847,7 +1869,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     uint32_t rv[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)  // bytes 8e + 2(t%4), +1 of the key's 32
+                    {
                         rv[e] = f16x2_from_e4m3x2(__byte_perm(wd[2 * e], wd[2 * e + 1], vsel));
+                        if (BS) rv[e] = mul_f16x2(rv[e], vmul[q & 1]);
+                    }
                     const int n = 32 * dg + 8 * (lane >> 3) + (lane & 7);
                     stsm_x4_t(vbase + sw128(n, ko), rv[0], rv[1], rv[2], rv[3]);
                 }
@@ -1889,6 +1914,12 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 h.y = f16x2_from_e4m3x2_hi(w.x);
                 h.z = f16x2_from_e4m3x2(w.y);
                 h.w = f16x2_from_e4m3x2_hi(w.y);
+                if constexpr (BS) {
+                    constexpr int kPass = kCT / (HD / 8);  // keys of a round of tasks: 8 or 16
+                    static_assert(kPass <= 16, "a group a round");
+                    const uint32_t m = sc.k[q * kPass / 16];
+                    h = make_uint4(mul_f16x2(h.x, m), mul_f16x2(h.y, m), mul_f16x2(h.z, m), mul_f16x2(h.w, m));
+                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kP2Keys * 128) + sw128(key, c & 7)) = h;
             }
             }
@@ -1903,7 +1934,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                                 mbar_wait(bar(L::kVFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
             if constexpr (BS) {
-                if (ct < 4) put_block_mul(scales_at, ct, a.sm_scale * 1.4426950408889634f, base + L::kBufBs + 128 * b + 64 * hf);
+                if (ct == 0) sc.put_mul(a.sm_scale * 1.4426950408889634f, bp + L::kBufBs + 32 * b + 16 * hf);
             }
             if constexpr (F4) {
 #pragma unroll
@@ -1957,9 +1988,10 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             tc_fence_after();
             const int k0 = key_tile(i) * kP2Keys;
             const int vis_n = row_ok ? min(kP2Keys, max(0, pos - k0 + 1)) : 0;
-            const uint64_t vis0 = buf_mask[2 * b] & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
-            const uint64_t vis1 = buf_mask[2 * b + 1] &
-                                  (vis_n >= 128 ? ~0ull : vis_n <= 64 ? 0ull : ((1ull << (vis_n - 64)) - 1));
+            uint64_t vis0 = buf_mask[2 * b] & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
+            uint64_t vis1 = buf_mask[2 * b + 1] &
+                            (vis_n >= 128 ? ~0ull : vis_n <= 64 ? 0ull : ((1ull << (vis_n - 64)) - 1));
+            if (BS && !row_ok) vis0 = vis1 = ~0ull;
             const bool whole = __all_sync(0xFFFFFFFFu, (vis0 & vis1) == ~0ull);
             auto vis_bits = [&](int c) {  // the visible keys among columns 32c..32c+31
                 return static_cast<uint32_t>((c < 2 ? vis0 : vis1) >> (32 * (c & 1)));
@@ -1969,7 +2001,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             // registers for pass 2.
             uint32_t sa[32], sb[32];
             float mx = -INFINITY, ext = score_scale >= 0.f ? -INFINITY : INFINITY;
-            const uint32_t scales_at = base + L::kBufBs + 128 * b;  // BS: of 16 keys each
             auto hide = [&](uint32_t (&sc)[32], int c) {  // BS: keys that the row does not see
                 if (!whole) {
                     const uint32_t bits = vis_bits(c);
@@ -1981,11 +2012,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             auto chunk_max = [&](uint32_t (&sc)[32], int c) {
                 if constexpr (BS) {
                     hide(sc, c);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const BlockMul mul = get_block_mul(scales_at + 32 * c + 16 * g);
-                        mx = fmaxf(mx, fmaf(max16(sc + 16 * g), mul.kmul, mul.vlog));
-                    }
+                    const BlockMul m = get_block_mul(bp + L::kBufBs + 32 * b + 16 * (c >> 1));
+                    mx = fmaxf(mx, fmaf(extreme32<true>(sc), m.kmul, m.vlog));
                 } else if (whole) {
                     ext = score_scale >= 0.f ? fmaxf(ext, extreme32<true>(sc)) : fminf(ext, extreme32<false>(sc));
                 } else {
@@ -2038,22 +2066,19 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             auto chunk_p = [&](uint32_t (&sc)[32], int c) {
                 if constexpr (BS) {
                     if (c < 2) hide(sc, c);  // (loaded again)
+                    const BlockMul m = get_block_mul(bp + L::kBufBs + 32 * b + 16 * (c >> 1));
+                    const float shift = m.vlog - msub;
+                    const uint64_t kmul2 = pk2(m.kmul, m.kmul), shift2 = pk2(shift, shift);
+                    uint64_t sum2 = pk2(0.f, 0.f);
                     uint32_t p[16];
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const BlockMul mul = get_block_mul(scales_at + 32 * c + 16 * g);
-                        const float less = mul.vlog - msub;
-                        const uint64_t gmul2 = pk2(mul.kmul, mul.kmul), gsub2 = pk2(less, less);
-                        uint64_t sum2 = pk2(0.f, 0.f);
-#pragma unroll
-                        for (int w = 8 * g; w < 8 * g + 8; ++w) {
-                            const float2 x = upk2(fma_f32x2(pk2u(sc[2 * w], sc[2 * w + 1]), gmul2, gsub2));
-                            const float e0 = ex2(x.x), e1 = ex2(x.y);
-                            p[w] = f16x2_from_f32(e0, e1);
-                            sum2 = add_f32x2(sum2, pk2(e0, e1));
-                        }
-                        lsum2 = fma_f32x2(sum2, pk2(mul.vinv, mul.vinv), lsum2);
+                    for (int w = 0; w < 16; ++w) {
+                        const float2 x = upk2(fma_f32x2(pk2u(sc[2 * w], sc[2 * w + 1]), kmul2, shift2));
+                        const float e0 = ex2(x.x), e1 = ex2(x.y);
+                        p[w] = f16x2_from_f32(e0, e1);
+                        sum2 = add_f32x2(sum2, pk2(e0, e1));
                     }
+                    lsum2 = fma_f32x2(sum2, pk2(m.vinv, m.vinv), lsum2);
                     tmem_st16(scol + 32 * c, p);
                     return;
                 }
@@ -2111,13 +2136,13 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
-                tmem_wait_ld();
                 if constexpr (BS) {
                     if (any_nan)
                         nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
                 }
+                uint32_t o[32];
+                tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
+                tmem_wait_ld();
                 if constexpr (kSplit) {
                     if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
                 } else if (row_ok) {

@@ -486,8 +486,9 @@ KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
  *   codes   uint8 [num_blocks][block_size][n_kv][head_dim]   (as the FP8 cache's)
  *   scales  float [num_blocks][scale_stride], a kv head's at its index; scale_stride >= n_kv, a
  *           multiple of 4 (so that a block's scales are whole 16-byte pieces, as the page calls want)
- * An element's value is dec(code) * scale.  A valid scale lies in [2^-60, 2^120]; 0 says that nothing was
- * written to the block (a pool starts with scales of 0).
+ * An element's value is dec(code) * scale.  A valid scale is a power of two from 2^-60 to 2^120 (E4M3 being a
+ * float, finer steps would gain nothing but at the bottom of its range; a power of two scales and unscales
+ * exactly).  0 says that nothing was written to the block: a pool starts with scales of 0.
  *
  * Everywhere below head_dim is 64, 128 or 256 and block_size 16, 32, 64, 128 or 256; n_kv * head_dim <=
  * 2^20; all device pointers 16-byte aligned.
@@ -562,6 +563,8 @@ KVFP8_API size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_s
  * Scores, the exponential, the sum of the weights and the accumulation are float.  softmax(s)_t * vs_t
  * enters the product with V as fp16, 2^7 to 2^15 at a row's highest: 11 bits down to 2^-21 of the highest,
  * multiples of 2^-24 below, none below 2^-32.  All of this holds for every query length and group size.
+ * (Long query chunks and wide groups take the codes of 64 tokens times their scales over the largest of those
+ * scales: exact while they are within 2^22 of each other, else to 2^-40 of the largest value that scale holds.)
  *
  * A block whose scales are not valid (of either side) holds no tokens for that head and sets
  * KVFP8_DEV_BAD_SCALE.  A token's NaN reaches exactly the outputs that see the token (all of a row for

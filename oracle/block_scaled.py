@@ -21,7 +21,9 @@ INV_2PI = 1 / (2 * Fraction("3.1415926535897932384626433832795028841971693993751
 
 
 def scale_ok(s):
-    return np.isfinite(s) & (s >= 2.0 ** MIN_EXP) & (s <= 2.0 ** MAX_EXP)
+    s = np.asarray(s)
+    with np.errstate(all="ignore"):
+        return np.isfinite(s) & (s >= 2.0 ** MIN_EXP) & (s <= 2.0 ** MAX_EXP) & (np.frexp(s)[0] == 0.5)
 
 
 def power_for(a: float) -> float:

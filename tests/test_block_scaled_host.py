@@ -115,8 +115,8 @@ def test_rotary_refusals(over, code):
 
 def test_workspace_sizes():
     assert kv.reshape_and_cache_block_scaled_workspace_size(512, 100, 16) == 0
-    assert kv.reshape_and_cache_block_scaled_workspace_size(513, 100, 16) == 6400
-    assert kv.reshape_and_cache_block_scaled_workspace_size(513, 1 << 27, 16) == 1 << 33
+    assert kv.reshape_and_cache_block_scaled_workspace_size(513, 100, 16) == 4 * (1600 + 100 + 2)
+    assert kv.reshape_and_cache_block_scaled_workspace_size(513, 1 << 27, 16) == (1 << 33) + (1 << 29) + 8
     assert kv.reshape_and_cache_block_scaled_workspace_size(-1, 100, 16) == 0
     assert kv.paged_attention_block_scaled_workspace_size(4, 32, 8, 128, 1, 16, 16) == 0
     assert kv.paged_attention_block_scaled_workspace_size(4, 32, 8, 128, 1, 256, 16) > 0

@@ -3,9 +3,10 @@ derived bounds.
 
 Bounds of attention, for a row and dim, with A = sum p|v| / sum p and S the largest sm |q| . |k| of the row:
   * the bf16 result is off by at most half a step, 2^-8 of the value;
-  * p * vs enters the product as fp16, 2^7 at least where it is highest: 2^-11 of each, so 2^-11 A, and 2^-25 absolute
-    below 2^-14, so 2^-32 of the highest p * vs: L * 2^-32 * max(vs) * 448, the row's sum being at least
-    its highest p;
+  * p * vs enters the product as fp16 (in long chunks with vs the largest of the token's 64 and V's codes times the rest,
+    multiples of 2^-24 where 448 max(vs) is 2^15.8), 2^7 at least where it is highest: 2^-11 of each, so 2^-11 A, and
+    2^-25 absolute below 2^-14, so 2^-32 of the highest p * vs: L * 2^-32 * max(vs) * 448 covers both, the row's sum
+    being at least its highest p; K scales are within 2^22 of each other here, where its codes times theirs are exact;
   * scores are float sums of hd exact products, (hd + 4) * 2^-24 S at most, and in the log2 domain they are
     multiplied, added to log2 vs and to the reference: three roundings of a number of at most 1.45 S + 80 (|log2 vs| <=
     60 here), with exp2's and log2's own 2^-22: a weight moves by at most d = (hd + 8) * 2^-24 (1.45 S + 80) +
@@ -168,17 +169,8 @@ def test_every_scale_boundary():
     pool.write(every.cuda(), -every.cuda(), np.arange(m) + 1)
 
 
-def test_scales_that_a_user_brought():
-    """Old scales that are no powers of two: quotients, and codes rounded from them when they are raised."""
-    r = np.random.default_rng(9)
-    pool = Pool(12, 16, 3, 64, fill=lambda r, shape: (r.random(shape) * 0.02 + 1e-3).astype(np.float32))
-    slots = r.permutation(12 * 16)[:100].astype(np.int64)
-    x = rows(r, 100, 3, 64, torch.float32)
-    pool.write(x[0], x[1], slots)
-
-
 def test_scales_that_are_not_valid():
-    for bad in (math.nan, math.inf, -1.0, 2.0 ** -61, 2.0 ** 121):
+    for bad in (math.nan, math.inf, -1.0, 2.0 ** -61, 2.0 ** 121, 0.75, 1.0 + 2.0 ** -23):
         pool = Pool(2, 16, 2, 64, fill=lambda r, shape: np.where(np.arange(shape[1]) == 1, bad, 1.0) * np.ones(shape))
         x = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
         pool.write(x, x, np.array([3, 4, 20]), want_status=kv.DEV_BAD_SCALE)  # head 1 stays as it is
@@ -250,7 +242,7 @@ def test_workspace_of_a_caller_may_hold_anything():
     n, nb = 700, 30
     r = np.random.default_rng(3)
     need = kv.reshape_and_cache_block_scaled_workspace_size(n, nb, 32)
-    assert need == nb * 32 * 4
+    assert need >= nb * 32 * 4
     for fill in (0, 0xFF, 1):
         ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
         pool = Pool(nb, 32, 2, 64)
@@ -268,9 +260,8 @@ def test_dequant_matches_the_oracle(dst, n, n_kv, hd, bs):
     nb = 6
     codes = r.integers(0, 256, (nb, bs, n_kv, hd)).astype(np.uint8)
     scales = np.exp2(r.integers(-60, 121, (nb, stride_of(n_kv)))).astype(np.float32)
-    scales[1, 0] = 0.3
     slots = r.integers(-1, nb * bs, n)  # some twice
-    for bad in (0.0, math.nan, -1.0, 2.0 ** 121):
+    for bad in (0.0, math.nan, -1.0, 2.0 ** 121, 0.3):
         scales[2, 0] = bad
         slots[0] = nb * bs
         st = status()
@@ -444,16 +435,26 @@ ROUTES = [(8, 2, 128, 1), (8, 2, 64, 3), (16, 2, 128, 2), (4, 2, 256, 2), (8, 2,
 
 @pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
 def test_scales_of_any_size(n_q, n_kv, hd, qlen):
-    """V scales from 2^-60 to 2^60 side by side, K scales such that scores stay small; and all at one end."""
+    """V scales from 2^-60 to 2^60 side by side, K scales over 2^22 such that scores stay small; and all at one end."""
     lengths, qlens = [300, 77], [qlen, min(qlen, 77)]
 
     def mixed(r, shape):
         return np.exp2(r.integers(-60, 61, shape).astype(np.float64))
 
-    for scale in (mixed, lambda r, shape: np.full(shape, 2.0 ** -60), lambda r, shape: np.full(shape, 2.0 ** 60), lambda r, shape: r.random(shape) + 0.01):
+    for scale in (mixed, lambda r, shape: np.full(shape, 2.0 ** -60), lambda r, shape: np.full(shape, 2.0 ** 60)):
         c = build(n_q, n_kv, hd, 16, lengths, qlens, 7, scale=scale)
         live = c["ks"] > 0
-        c["ks"][live] = np.exp2(np.random.default_rng(8).integers(-10, -5, int(live.sum())))
+        c["ks"][live] = np.exp2(np.random.default_rng(8).integers(-27, -5, int(live.sum())))
+        check_attention(run(multi, c, qlen), c)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+def test_scales_of_an_earlier_call_do_not_linger(n_q, n_kv, hd, qlen):
+    """Calls with scales far apart one after the other, the last tiles cut off inside: nothing of a tile's shared memory
+    that the tile did not fill may count."""
+    for at in (2.0 ** 50, 2.0 ** -55, 1.0, 2.0 ** -60, 2.0 ** 60):
+        c = build(n_q, n_kv, hd, 16, [300, 77, 129], [qlen, min(qlen, 77), min(qlen, 129)], 7, scale=lambda r, shape: np.full(shape, at))
+        c["ks"][c["ks"] > 0] = 2.0 ** -27 if at < 1 else 2.0 ** -6
         check_attention(run(multi, c, qlen), c)
 
 
@@ -465,7 +466,7 @@ def test_bad_blocks_and_scales_hold_no_tokens(n_q, n_kv, hd, qlen):
     c["bt"][0, 3], c["bt"][1, 0], c["bt"][1, 10] = -1, len(c["kc"]), 1 << 30
     c["bt"][2, :] = -5  # a sequence without any
     check_attention(run(multi, c, qlen, want_status=kv.DEV_BAD_BLOCK), c)
-    for bad in (0.0, math.nan, -1.0, math.inf, 2.0 ** -61, 2.0 ** 121):
+    for bad in (0.0, math.nan, -1.0, math.inf, 2.0 ** -61, 2.0 ** 121, 3.0):
         c = dict(base, ks=base["ks"].copy(), vs=base["vs"].copy())
         c["ks"][base["bt"][0, 2], 0] = bad
         c["vs"][base["bt"][0, 18], 1] = bad  # its last block
