@@ -25,9 +25,9 @@ HEADER = os.path.join(ROOT, "include", "kvfp8.h")
 SOURCES = ["kvfp8_api.cu", "reshape_and_cache.cu", "paged_decode.cu", "paged_decode_mixed.cu",
            "prefill_attention.cu", "dequant.cu", "decode_noalloc.cu", "fp4_cache.cu",
            "paged_decode_fp4.cu", "block_copy.cu", "block_scaled_cache.cu",
-           "paged_decode_block_scaled.cu", "rotary.cu"]
+           "paged_decode_block_scaled.cu", "prefill_block_scaled.cu", "rotary.cu"]
 DEPS = ["kvfp8_block_scale.cuh", "kvfp8_device.cuh", "kvfp8_e2m1.cuh", "kvfp8_internal.h",
-        "paged_decode_kernel.cuh", "paged_decode_own_plan.cuh"]
+        "paged_decode_kernel.cuh", "paged_decode_own_plan.cuh", "prefill_common.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

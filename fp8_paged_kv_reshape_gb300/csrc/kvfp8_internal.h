@@ -190,12 +190,16 @@ cudaError_t launch_paged_decode_block_scaled(const DecodeArgs &a, cudaStream_t s
 bool decode_takes_sequences_whole(int32_t max_blocks_per_seq, int32_t block_size);
 
 // Multi-query (causal) attention on the tensor cores (tcgen05): long query chunks, or kv-head
-// counts the split-KV decode kernel does not cover.  Needs no workspace, but over a 4-bit cache or one
-// with block scales the one below where few row tiles have their keys split.
+// counts the split-KV decode kernel does not cover.  Needs no workspace, but over a 4-bit cache
+// (key_scales set) the one below where few row tiles have their keys split.
 cudaError_t launch_prefill_attention(const DecodeArgs &a, cudaStream_t stream);
-size_t split_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
                                   int64_t max_len);
-// True when its grid and its 32-bit row numbers hold this many score rows (host arithmetic).
+// The same over the FP8 cache with block scales, and its workspace.
+cudaError_t launch_prefill_block_scaled(const DecodeArgs &a, cudaStream_t stream);
+size_t block_scaled_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+                                           int64_t max_len);
+// True when their grid and their 32-bit row numbers hold this many score rows (host arithmetic).
 bool prefill_takes(int32_t n_q, int32_t n_kv, int32_t max_query_len, int32_t num_seqs);
 // True when kvfp8_paged_attention_multi takes the split-KV decode kernel for this shape
 // (and so needs a workspace); false when it takes the prefill kernel.

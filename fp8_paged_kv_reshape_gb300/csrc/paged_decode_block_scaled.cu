@@ -716,7 +716,7 @@ cudaError_t run_tiles(const DecodeArgs &d, const DecodeWorkspace &ws, int tiles,
 
 cudaError_t launch_paged_decode_block_scaled(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;
-    if (!multi_uses_decode_kernel(d.n_q, d.n_kv, d.head_dim, d.qmax)) return launch_prefill_attention(d, stream);
+    if (!multi_uses_decode_kernel(d.n_q, d.n_kv, d.head_dim, d.qmax)) return launch_prefill_block_scaled(d, stream);
     const DecodeWorkspace ws = decode_workspace_layout(d.num_seqs, d.qmax * d.n_q, d.head_dim);
     const int tiles = (d.qmax * (d.n_q / d.n_kv) + 3) / 4;  // of 4 score columns
     switch (d.head_dim) {

@@ -35,151 +35,14 @@
 //        apply v_scale and store bf16.
 //  * All waits are bounded (mbarriers with a clock64 limit); a wait that runs out sets
 //    KVFP8_DEV_TIMEOUT.  Tensor memory is always released before the CTA exits.
-#include "kvfp8_block_scale.cuh"
 #include "kvfp8_e2m1.cuh"
-#include "paged_decode_kernel.cuh"
+#include "prefill_common.cuh"
 
 namespace kvfp8 {
 namespace {
 
-constexpr int kPfRows = 128;   // score rows per CTA (TMEM lanes)
 constexpr int kPfKeys = 64;    // keys per tile
 
-// ---------------------------------------------------------------- tcgen05 wrappers
-
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-                 "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-// D (TMEM) (+)= A (shared memory descriptor) x B (shared memory descriptor)
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// D (TMEM) (+)= A (TMEM) x B (shared memory descriptor)
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// arrive on the mbarrier once every tcgen05.mma this thread issued before has completed
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// four 8x8 b16 matrices stored transposed: lane t gives (rows 2(t%4), 2(t%4)+1; column t/4)
-// of matrix j in r[j], and the address of row t%8 of matrix t/8
-__device__ __forceinline__ void stsm_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
-                                          uint32_t r3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
-                 "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-                 : "memory");
-}
-
-// generic-proxy shared-memory writes become visible to the tensor core (async proxy)
-__device__ __forceinline__ void fence_proxy_async() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-                 : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major operand in the 128-byte swizzle layout (rows of
-// 128 bytes, 16-byte chunks XOR-ed with row % 8, 8-row groups 1024 bytes apart).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu)  // start address
-           | (1ull << 16)                                 // leading byte offset (unused here)
-           | (static_cast<uint64_t>(1024 >> 4) << 32)     // stride byte offset: 8 rows
-           | (1ull << 46)                                 // descriptor version
-           | (2ull << 61);                                // 128-byte swizzle
-}
-// The descriptor of an address off bytes (a multiple of 16) past one whose descriptor is d:
-// the start-address field is (address >> 4) in 14 bits, and every shared-memory address of
-// a CTA is below 2^18, so the field never carries into the next one.
-__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t off) { return d + (off >> 4); }
-
-// Instruction descriptor, kind::f16: f16 A and B, fp32 D, both K-major, M x N.
-__host__ __device__ constexpr uint32_t f16_idesc(int m, int n) {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-// byte offset of 16-byte chunk c of row r in a 128-byte-swizzled K-major block
-__device__ __forceinline__ uint32_t sw128(int r, int c) {
-    return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
-}
-
-// packed fp32 pairs (sm_100+ f32x2 arithmetic: two IEEE round-to-nearest operations)
-__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pk2u(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 upk2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-__device__ __forceinline__ float min3f(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 // 2^x on an f16 pair (the tensor core takes P as f16)
 __device__ __forceinline__ uint32_t ex2_f16x2(uint32_t x) {
     uint32_t r;
@@ -214,54 +77,21 @@ __device__ __forceinline__ float extreme64(const uint32_t (&s)[2][32]) {
     return op(a0, a1, kMax ? fmaxf(a2, a3) : fminf(a2, a3));
 }
 
-struct PrefillCommon {
-    __nv_bfloat16 *out;
-    const __nv_bfloat16 *query;
-    const int32_t *qsl;
-    int32_t qmax, qrows;
-    const int32_t *block_tables;
-    int32_t max_blocks_per_seq;
-    const int32_t *seq_lens;
-    int32_t num_seqs;
-    int32_t n_q, n_kv, group, block_size, num_blocks, max_len;
-    float sm_scale;
-    const void *k_scale;
-    const void *v_scale;
-    int32_t scale_dtype;
-    uint32_t *status;
-    int32_t box_rows;
-    int32_t row_tiles;  // tiles of 128 score rows per (sequence, kv head)
-};
-// What the cache holds: E4M3 codes (a scale per layer), E2M1 codes with scale bytes per 16 dims, or E4M3
-// codes with a float scale per block and kv head.
-enum class Cache { kE4M3, kE2M1, kBlocks };
-
-// The other forms' arguments are their own: carried along by the E4M3 kernels the 4-bit ones cost the
-// two-row-tile kernel 0.8 % (911 against 919 TFLOP/s on 512 new tokens of 64 sequences of 4096).
-template <Cache C>
+// The 4-bit form's arguments are its own: carried along by the E4M3 kernels they cost the two-row-tile one
+// 0.8 % (911 against 919 TFLOP/s on 512 new tokens of 64 sequences of 4096).
+template <bool F4>
 struct PrefillArgs : PrefillCommon {
     // (named by shared code, read by nothing)
     static constexpr int32_t splits = 1;
     static constexpr float *part_o = nullptr, *part_lse = nullptr;
-    static constexpr bool causal = true;
 };
-struct PrefillSplitArgs : PrefillCommon {
+template <>
+struct PrefillArgs<true> : PrefillCommon {
+    const uint8_t *key_scales, *value_scales;  // the groups' scale bytes
     // parts a (sequence, kv head, row tile)'s keys are cut into at most (gridDim.y), and the parts'
     // results, [CTA of the unsplit grid, in sequence order][part][row of the tile]
     int32_t splits;
     float *part_o, *part_lse;
-};
-template <>
-struct PrefillArgs<Cache::kE2M1> : PrefillSplitArgs {
-    const uint8_t *key_scales, *value_scales;  // the groups' scale bytes
-    static constexpr bool causal = true;
-};
-template <>
-struct PrefillArgs<Cache::kBlocks> : PrefillSplitArgs {
-    const float *key_scales, *value_scales;  // [block][scale_stride], a kv head's at its index
-    const uint8_t *value_cache;
-    int32_t scale_stride;
-    bool causal;  // else every query sees every cached token
 };
 
 // ---------------------------------------------------------------- the 4-bit cache
@@ -290,11 +120,6 @@ constexpr float kF4Head = 7.f;
 // in V^T's rows, row 8j + 2a + b holding dim 8a + 2j + b, and so in O's columns: O's word (pair of
 // columns) 4j + a is the output's word 4a + j.
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 // half k of an fp16 pair in both halves
 template <int k>
 __device__ __forceinline__ uint32_t half_pair(uint32_t x) {
@@ -401,7 +226,7 @@ __host__ __device__ constexpr int o_word(int w) { return F4 ? 4 * (w & 3) + (w >
 // ones.)
 // win: the lane window of block-table entries from wbase on.
 template <int HD>
-__device__ __forceinline__ void copy_scales(const PrefillArgs<Cache::kE2M1> &a, int kvh, int t0, int kend, int lbs, int32_t win,
+__device__ __forceinline__ void copy_scales(const PrefillArgs<true> &a, int kvh, int t0, int kend, int lbs, int32_t win,
                                             int wbase, uint32_t dst, uint32_t side_bytes, uint32_t bar, int lane) {
     constexpr int kGph = HD / 16, kKeys = 16 / kGph, kChunks = kPfKeys / kKeys;  // of a side
 #pragma unroll
@@ -424,7 +249,7 @@ __device__ __forceinline__ void copy_scales(const PrefillArgs<Cache::kE2M1> &a, 
 // each lane's own last (negative: none); blocks out of range hold no tokens.  Called by whole warps: the
 // tokens that every lane has are shared out over the lanes, the few after them are each lane's own.
 template <int HD>
-__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs<Cache::kE2M1> &a, int seq, int kvh, int first, int last) {
+__device__ __noinline__ uint32_t nan_value_groups(const PrefillArgs<true> &a, int seq, int kvh, int first, int last) {
     const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
     uint32_t groups = 0;
     auto look = [&](int t) {
@@ -468,284 +293,27 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, 
                  : "memory");
 }
 
-// Few row tiles (a short chunk or a wide group of heads on a long context) would leave most SMs idle, so
-// their keys are cut: part p of a row tile takes key tiles [p n / parts, (p + 1) n / parts), leaves its
-// normalized rows and their log2 sums of weights in the workspace, and a second kernel joins them.  A part
-// is 128 keys at least (8 tokens on 1024, 32 / 8 heads of 128: 21.5 us unsplit, 16.4 / 12.7 / 11.1 with
-// parts of 512 / 256 / 128; on 4096 17.6 / 15.0 / 16.0).  Nothing is split when more than half the SMs have
-// a row tile: 80 to 216 tiles of equal lengths gained at most 7 % from any number of parts and lost up to
-// 60 % (unequal ones were not measured).  (kSplit is an instance of its own: the few instructions cost the
-// unsplit kernel of two row tiles 11 %, 531 against 478 us for 512 new tokens of 16 sequences of 4096.)
-constexpr int kSplitSms = 152;
-constexpr int kMinPartKeys = 128;
-__host__ __device__ constexpr int split_parts(int splits, int key_tiles, int tile_keys) {
-    const int most = key_tiles / (kMinPartKeys / tile_keys);
-    return splits < most ? splits : most > 1 ? most : 1;
+// bf16 pair of dims d, d+1, NaN where the pair's group is in `groups`
+__device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t groups, int d) {
+    return (groups >> (d >> 4)) & 1u ? 0x7FFF7FFFu : w;
 }
-// Whether dim d (past the 32 dims' first, d0) is NaN: kE2M1's groups of 16 dims of a head, kBlocks' dims of
-// the 32.
-template <Cache C>
-__device__ __forceinline__ bool is_nan_dim(uint32_t nan, int d0, int d) {
-    return (nan >> (C == Cache::kE2M1 ? (d0 + d) >> 4 : d)) & 1u;
-}
-// bf16 pair of dims d, d+1 with those that are NaN
-template <Cache C>
-__device__ __forceinline__ uint32_t nan_in(uint32_t w, uint32_t nan, int d0, int d) {
-    if (is_nan_dim<C>(nan, d0, d)) w = (w & 0xFFFF0000u) | 0x7FFFu;
-    if (is_nan_dim<C>(nan, d0, d + 1)) w = (w & 0xFFFFu) | 0x7FFF0000u;
-    return w;
-}
-// 32 dims from d0 on of a part's row, from O's columns, as float; NaN where `nan` says
-template <Cache C>
-__device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], float inv, uint32_t nan, int d0) {
+// 32 dims from d0 on of a part's row, from O's columns, as float; NaN in `groups`
+__device__ __forceinline__ void store_part(float *row, const uint32_t (&o)[32], float inv, uint32_t groups, int d0) {
 #pragma unroll
     for (int w = 0; w < 16; w += 2) {  // dims 2w..2w+3
-        const int e = 2 * o_word<C == Cache::kE2M1>(w), f = 2 * o_word<C == Cache::kE2M1>(w + 1);
-        const int from[4] = {e, e + 1, f, f + 1};
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = is_nan_dim<C>(nan, d0, 2 * w + i) ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[from[i]]) * inv;
-        *reinterpret_cast<float4 *>(row + d0 + 2 * w) = make_float4(v[0], v[1], v[2], v[3]);
+        const int e = 2 * o_word<true>(w), f = 2 * o_word<true>(w + 1);
+        float4 v = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                               __uint_as_float(o[f]) * inv, __uint_as_float(o[f + 1]) * inv);
+        if ((groups >> ((d0 + 2 * w) >> 4)) & 1u) v.x = v.y = v.z = v.w = __uint_as_float(0x7FC00000u);
+        *reinterpret_cast<float4 *>(row + d0 + 2 * w) = v;
     }
-}
-
-// ---------------------------------------------------------------- block scales
-//
-// Cache::kBlocks: a block is 16 keys at least, so 16 keys in a row (a group) have one K and one V scale, powers of
-// two.  The conversion multiplies a group's fp16 codes by its scale over 2^-7 of the largest of its 64 keys: exact
-// where scales there are within 2^22 of each other (a product is a multiple of fp16's 2^-24 then), a multiple of
-// 2^-24 where 448 times the largest scale is 2^15.8 otherwise.  The softmax is left with one K and one V scale per 64 keys: ks
-// multiplies the scores; vs goes into the exponent, so that the weights that meet V are 2^(s + log2 vs - m) with m
-// near the highest s + log2 vs, within fp16's range whatever the scales, and the row's sum adds the weights
-// times 1 / vs.  Weights are held as over the 4-bit cache (kF4Head).  (With a multiplier per 16 keys in the softmax:
-// 732 us for 512 new tokens of 16 sequences of 4096.)
-//
-// NaN: a NaN code in K makes the key's scores NaN, which the masks keep from rows that do not see it.  One
-// in V may reach all rows where all of them see the key.  Where not (the last tiles of a causal call), such codes are
-// taken as 0, the CTA remembers that it met one, and at the end its rows look up which dims of the values
-// they see are NaN (a slow scan that no finite cache runs).
-
-// what the softmax takes of 64 keys' scales: scores * kmul are in the log2 domain
-struct BlockMul {
-    float kmul, vlog, vinv;
-};
-__device__ __forceinline__ BlockMul get_block_mul(const uint8_t *at) {
-    const float4 v = *reinterpret_cast<const float4 *>(at);
-    return BlockMul{v.x, v.y, v.z};
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b);
-
-// The scales of 64 keys: which groups have valid ones, the largest of them, and each as an fp16 pair over 2^-7 of
-// the largest.
-struct BlockScales {
-    uint64_t keys;       // those of `mask` in groups with valid scales
-    float kref, vref;    // 1 without any
-    uint32_t k[4], v[4];
-
-    __device__ __forceinline__ static uint32_t over(float s, float ref) {
-        // 2^(7 - d), d = log2(ref / s): an fp16 number, or one of its denormals, or 0
-        const int e = static_cast<int>(__float_as_uint(s) >> 23) - static_cast<int>(__float_as_uint(ref) >> 23) + 22;
-        const uint32_t h = e >= 1 ? static_cast<uint32_t>(e) << 10 : e >= -9 ? 1u << (9 + e) : 0u;
-        return h * 0x10001u;
-    }
-    // (a group without keys has no scales either: what stands there is of another tile)
-    __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(at), v4 = *reinterpret_cast<const float4 *>(at + 16);
-        const float ks[4] = {k4.x, k4.y, k4.z, k4.w}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
-        keys = 0;
-        kref = vref = 0.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint64_t group = mask & (0xFFFFull << (16 * g));
-            if (group == 0ull || !(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) continue;
-            keys |= group;
-            kref = fmaxf(kref, ks[g]);
-            vref = fmaxf(vref, vs[g]);
-        }
-        if (keys == 0ull) kref = vref = 1.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {  // (0 for a group without, whatever its scales' bits)
-            const bool ok = (keys & (0xFFFFull << (16 * g))) != 0ull;
-            k[g] = ok ? over(ks[g], kref) : 0u;
-            v[g] = ok ? over(vs[g], vref) : 0u;
-        }
-    }
-    __device__ __forceinline__ void put_mul(float score_scale, uint8_t *at) const {
-        // (kmul is kept away from 0 and infinity, which would make a NaN of a score of infinity or 0)
-        *reinterpret_cast<float4 *>(at) =
-            make_float4(fminf(fmaxf(kref * 0x1p-7f * score_scale, 0x1p-126f), 0x1p126f),
-                        static_cast<float>(static_cast<int>(__float_as_uint(vref) >> 23) - 134),
-                        __uint_as_float((261u << 23) - __float_as_uint(vref)), 0.f);
-    }
-};
-
-// The scales of 64 keys from t0 on, [side][16 keys] at dst, by the TMA warp; every lane adds the completion of
-// its copies to the stage's barrier.  win: the lane window of block-table entries from wbase on.
-__device__ __forceinline__ void copy_block_scales(const PrefillArgs<Cache::kBlocks> &a, int kvh, int t0, int kend, int lbs,
-                                                  int32_t win, int wbase, uint32_t dst, uint32_t bar, int lane) {
-    const int t = t0 + 16 * (lane & 3);
-    const int blk = __shfl_sync(0xFFFFFFFFu, win, ((t >> lbs) - wbase) & 31);
-    if (lane < 8 && t < kend && blk >= 0 && blk < a.num_blocks)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * lane),
-                     "l"((lane < 4 ? a.key_scales : a.value_scales) + static_cast<int64_t>(blk) * a.scale_stride + kvh)
-                     : "memory");
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// NaN codes of V -> 0, remembered
-__device__ __forceinline__ void drop_nan_codes(uint4 &v, volatile int32_t *nan_seen) {
-    const uint4 n = make_uint4(nan_byte_mask(v.x), nan_byte_mask(v.y), nan_byte_mask(v.z), nan_byte_mask(v.w));
-    if ((n.x | n.y | n.z | n.w) != 0u) {
-        v.x &= ~n.x;
-        v.y &= ~n.y;
-        v.z &= ~n.z;
-        v.w &= ~n.w;
-        *nan_seen = 1;
-    }
-}
-
-// The dims d0..d0+31 (bit i: d0 + i) in which some value of tokens first..last of the sequence is NaN, for each
-// lane's own last (negative: none); blocks out of range or without valid scales hold no tokens.  Called by
-// whole warps, as nan_value_groups.
-template <int HD>
-__device__ __noinline__ uint32_t nan_value_dims(const PrefillArgs<Cache::kBlocks> &a, int seq, int kvh, int d0, int first,
-                                                int last) {
-    const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
-    uint32_t dims = 0;
-    auto look = [&](int t) {
-        const int32_t blk = bt[t / a.block_size];
-        if (blk < 0 || blk >= a.num_blocks) return;
-        const int64_t s = static_cast<int64_t>(blk) * a.scale_stride + kvh;
-        if (!block_scale_ok(a.key_scales[s]) || !block_scale_ok(a.value_scales[s])) return;
-        const uint32_t *row = reinterpret_cast<const uint32_t *>(
-            a.value_cache + ((static_cast<int64_t>(blk) * a.block_size + t % a.block_size) * a.n_kv + kvh) * HD + d0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t nan = nan_byte_mask(row[i]) & 0x08040201u;
-            dims |= ((nan | nan >> 8 | nan >> 16 | nan >> 24) & 0xFu) << (4 * i);
-        }
-    };
-    const int lane = static_cast<int>(threadIdx.x & 31);
-    const int all = __reduce_min_sync(0xFFFFFFFFu, last < 0 ? INT32_MAX : last);  // tokens first..all are every lane's
-    if (all != INT32_MAX)
-        for (int t = first + lane; t <= all; t += 32) look(t);
-    dims = __reduce_or_sync(0xFFFFFFFFu, dims);
-    if (last < 0) return 0u;
-    for (int t = max(first, all + 1); t <= last; ++t) look(t);
-    return dims;
-}
-
-// ---------------------------------------------------------------- work order
-//
-// The CTAs of the sequences with the most keys go first.  The hardware starts CTAs in index
-// order as SMs free up, so giving the low indices to the longest sequences keeps one of them
-// from starting last and running alone at the end (longest-processing-time-first list
-// scheduling; with lengths log-uniform over 16..32768 tokens, as in a serving mix, index
-// order leaves the last SMs busy ~20 % past the mean).  Sequences are ranked by a bucket of
-// their length, four buckets per octave (lengths in one bucket differ by less than 19 %),
-// longest bucket first, and by index within a bucket.
-
-__device__ __forceinline__ int length_bucket(int len, int max_len) {
-    const int l = min(max(len, 0), max_len);
-    if (l == 0) return 0;
-    const int b = 31 - __clz(l);                                     // floor(log2 l), 0..30
-    const int frac = b >= 2 ? (l >> (b - 2)) & 3 : (l << (2 - b)) & 3;  // next two bits
-    return 1 + 4 * b + frac;                                         // 1..124
-}
-
-// The sequence of rank u (0 = longest).  Every thread of the CTA calls it (it synchronizes
-// the CTA); scratch is 168 words of this CTA's shared memory, free until it returns.
-__device__ __forceinline__ int seq_of_rank(const int32_t *seq_lens, int num_seqs, int max_len, int u,
-                           uint32_t *scratch) {
-    if (num_seqs <= 1) return u;
-    uint32_t *cnt = scratch;                      // [128] sequences per bucket
-    // bucket of rank u, rank within it, the result, and whether the result is final
-    volatile uint32_t *pick = scratch + 128;
-    volatile uint32_t *wsum = scratch + 136;      // [32] per-warp counts of one round
-    const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31;
-    const int nwarps = nthr >> 5;
-    // bucket of sequence tid, kept for the histogram and the first round of the scan
-    const int my_bucket = tid < num_seqs ? length_bucket(seq_lens[tid], max_len) : -1;
-    if (num_seqs <= nthr) {  // lengths all in one bucket (a batch of equal lengths): index order
-        const int b0 = length_bucket(seq_lens[0], max_len);
-        if (__syncthreads_and(tid >= num_seqs || my_bucket == b0)) return u;
-    }
-    for (int b = tid; b < 128; b += nthr) cnt[b] = 0u;
-    if (tid == 0) {  // (u < num_seqs always finds its bucket; index order otherwise)
-        pick[0] = 0u;
-        pick[1] = 0u;
-        pick[2] = static_cast<uint32_t>(u);
-        pick[3] = 0u;
-    }
-    __syncthreads();
-    for (int s = tid; s < num_seqs; s += nthr)
-        atomicAdd(&cnt[s == tid ? my_bucket : length_bucket(seq_lens[s], max_len)], 1u);
-    __syncthreads();
-    if (warp == 0) {
-        // lane l holds buckets 127-4l .. 124-4l, so lanes run longest first
-        uint32_t c[4], tot = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            c[q] = cnt[127 - 4 * lane - q];
-            tot += c[q];
-        }
-        uint32_t incl = tot;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        uint32_t before = incl - tot;
-        const uint32_t uu = static_cast<uint32_t>(u);
-        if (uu >= before && uu < incl) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (uu < before + c[q]) {
-                    pick[0] = static_cast<uint32_t>(127 - 4 * lane - q);
-                    pick[1] = uu - before;
-                    // every sequence in one bucket (a batch of equal lengths): index order
-                    if (c[q] == static_cast<uint32_t>(num_seqs)) pick[3] = 1u;
-                    break;
-                }
-                before += c[q];
-            }
-        }
-    }
-    __syncthreads();
-    if (pick[3] != 0u) return u;
-    const int B = static_cast<int>(pick[0]);
-    const uint32_t k = pick[1];
-    // the k-th sequence of bucket B in index order, nthr sequences a round
-    uint32_t seen = 0;
-    for (int s0 = 0; s0 < num_seqs; s0 += nthr) {
-        const int s = s0 + tid;
-        const int b = s0 == 0 ? my_bucket : (s < num_seqs ? length_bucket(seq_lens[s], max_len) : -1);
-        const bool in = s < num_seqs && b == B;
-        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, in);
-        if (lane == 0) wsum[warp] = static_cast<uint32_t>(__popc(bal));
-        __syncthreads();
-        uint32_t pre = seen, tot = 0;
-        for (int w = 0; w < nwarps; ++w) {
-            const uint32_t v = wsum[w];
-            if (w < warp) pre += v;
-            tot += v;
-        }
-        pre += static_cast<uint32_t>(__popc(bal & ((1u << lane) - 1u)));
-        if (in && pre == k) pick[2] = static_cast<uint32_t>(s);
-        seen += tot;
-        __syncthreads();  // pick[2] is written; wsum may be reused
-        if (seen > k) break;
-    }
-    return static_cast<int>(pick[2]);
 }
 
 // Shared-memory plan (byte offsets from a 1024-aligned base).  Q is converted once; K and
 // V^T (f16) have NB buffers, and so do the scores in tensor memory; the FP8 staging ring has
 // NS stages.  At head_dim 256 the f16 buffers fill the shared memory: NB = 2, NS = 1.
-template <int HD, Cache C>
+template <int HD, bool F4>
 struct PfSmem {
-    static constexpr bool F4 = C == Cache::kE2M1, BS = C == Cache::kBlocks;
     static constexpr int kRow = F4 ? HD / 2 : HD;                  // cache bytes of a key's head
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;          // TMA box row (swizzle span)
     static constexpr int kSegs = kRow / kSeg;
@@ -757,7 +325,7 @@ struct PfSmem {
     // product also accumulates each score row's sum of P (column HD of O) in fp32.  At 256
     // there is no room (the product's N would pass 256 and shared memory would overflow):
     // the softmax warps sum P themselves.
-    static constexpr bool kSumCol = HD <= 128 && !BS;  // (BS: the sum is not of the weights that meet V)
+    static constexpr bool kSumCol = HD <= 128;
     static constexpr int kVRows = HD + (kSumCol ? 16 : 0);
     static constexpr int kVBuf = kVRows * 128;                     // one V^T f16 buffer: rows x 128 B
     static constexpr int kK = kQ + HD * 256;
@@ -779,9 +347,7 @@ struct PfSmem {
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // valid-key mask per K/V buffer
     static constexpr int kMisc = kBufMask + 8 * kNB;               // tmem base, abort flag, NaN seen
-    // BS: a stage's scales ([side][16 keys]) and, per buffer, what the softmax takes of them (BlockMul)
-    static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
-    static constexpr int kTotal = kBufBs + (BS ? 16 * kNB : 0);
+    static constexpr int kTotal = kMisc + 16;
     // tensor memory: S[NB] (64 fp32 columns each; P as f16 over the first 32), then O
     static constexpr uint32_t kColO = 64 * kNB;
     static constexpr uint32_t kTmemCols = kColO + HD + 32 <= 256 ? 256 : 512;
@@ -794,12 +360,11 @@ constexpr int kPfConvWarps = 8;
 constexpr int kPfMmaWarp = 4 + kPfConvWarps, kPfTmaWarp = kPfMmaWarp + 1;
 constexpr int kPfWarps = kPfTmaWarp + 1;
 
-template <int HD, Cache C, bool kSplit>
+template <int HD, bool F4, bool kSplit>
 __global__ void __launch_bounds__(kPfWarps * 32, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-               const PrefillArgs<C> a) {
-    using L = PfSmem<HD, C>;
-    constexpr bool F4 = L::F4, BS = L::BS;
+               const PrefillArgs<F4> a) {
+    using L = PfSmem<HD, F4>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -837,14 +402,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     // (more new tokens than cached ones is an error of the multi-query form only: a decode
     // query on an empty sequence gives a zero row)
     if (tile == 0 && kvh == 0 && tid == 0 &&
-        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.qsl && a.causal && qr.count > Ls)))
+        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.qsl && qr.count > Ls)))
         flag(a.status, KVFP8_DEV_BAD_BLOCK);
     const int nb = qr.count, G = a.group;
     const int row0 = tile * kPfRows;                 // first score row of this tile
     if (row0 >= nb * G) return;                      // no rows here
     const int j_last = min(nb, (row0 + kPfRows + G - 1) / G) - 1;
-    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;  // keys the tile's last row may see
-    const int all_see = a.causal ? Ls - nb + row0 / G + 1 : Ls;  // (the keys before it every row sees)
+    const int kend = Ls - nb + j_last + 1;           // keys the tile's last row may see
     int ntiles = kend > 0 ? (kend + kPfKeys - 1) / kPfKeys : 0;
     int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
@@ -875,7 +439,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), F4 || BS ? 33 : 1);  // and every lane's scale copies
+            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kPfConvWarps);
         }
         for (int b = 0; b < L::kNB; ++b) {
@@ -886,7 +450,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
-        if (F4 || BS) *nan_seen = 0;
+        if (F4) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPfMmaWarp) {
@@ -980,9 +544,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
                                 bar(L::kFull, st), lane);
             }
-            if constexpr (BS)
-                copy_block_scales(a, kvh, t0, kend, lbs, win, wbase, base + L::kStageBs + 32 * st, bar(L::kFull, st), lane);
-            if constexpr ((F4 || BS) && L::kNS == 1) {
+            if constexpr (F4 && L::kNS == 1) {
                 // one stage: the next copies start when this tile has been read, so their lines are brought
                 // into L2 meanwhile, as far as the window of block-table entries goes (head_dim 256, 32 tokens
                 // of 32 sequences on 4096: 150 to 124 us; two or three tiles ahead 127 and 128; with all lines
@@ -994,20 +556,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     for (int sgi = 0; sgi < L::kSegs; ++sgi)
                         tma_prefetch_3d(map, 0, kvh * L::kSegs + sgi, next * bs + box.row);
                 }
-                if constexpr (F4) {
-                    // and the scale bytes, kLineKeys keys of a side by each of the first lanes
-                    constexpr int kLineKeys = 128 / (HD / 16), kLines = kPfKeys / kLineKeys;
-                    const int lt = t0 + lane % kLines * kLineKeys;
-                    const KeyPlace line = next_tile_place(lt, lbs);
-                    const int lblk = __shfl_sync(0xFFFFFFFFu, win, (line.entry - wbase) & 31);
-                    if (lane < 2 * kLines && lt + kPfKeys < kend && line.entry - wbase < 32 && lblk >= 0 && lblk < a.num_blocks)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                            (lane < kLines ? a.key_scales : a.value_scales) +
-                            (((static_cast<int64_t>(lblk) * a.n_kv + kvh) << lbs) + line.row) * (HD / 16)));
-                }
+                // and the scale bytes, kLineKeys keys of a side by each of the first lanes
+                constexpr int kLineKeys = 128 / (HD / 16), kLines = kPfKeys / kLineKeys;
+                const int lt = t0 + lane % kLines * kLineKeys;
+                const KeyPlace line = next_tile_place(lt, lbs);
+                const int lblk = __shfl_sync(0xFFFFFFFFu, win, (line.entry - wbase) & 31);
+                if (lane < 2 * kLines && lt + kPfKeys < kend && line.entry - wbase < 32 && lblk >= 0 && lblk < a.num_blocks)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        (lane < kLines ? a.key_scales : a.value_scales) +
+                        (((static_cast<int64_t>(lblk) * a.n_kv + kvh) << lbs) + line.row) * (HD / 16)));
             }
         }
-        if ((F4 || BS) && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -1103,21 +663,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kKvFree, b), ((i / L::kNB) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            uint64_t mask = meta[st];
-            BlockScales sc;
-            if constexpr (BS) {
-                sc.load(bp + L::kStageBs + 32 * st, mask);
-                if (ct == 0) {
-                    if (mask != sc.keys) flag(a.status, KVFP8_DEV_BAD_SCALE);
-                    sc.put_mul(a.sm_scale * 1.4426950408889634f, bp + L::kBufBs + 16 * b);
-                }
-                mask = sc.keys;
-            }
-            // a warp's V blocks are of eight keys, the same in every round
-            const int w4 = warp - 4;
-            const uint32_t vmul[1] = {BS ? (w4 < 4 ? (w4 < 2 ? sc.v[0] : sc.v[1]) : (w4 < 6 ? sc.v[2] : sc.v[3])) : 0u};
-            // where some row does not see every key, NaN codes of V are taken out
-            const bool drop_nan = BS && (key_tile(i) + 1) * kPfKeys > all_see;
+            const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
             uint8_t *kdst0 = bp + L::kK + b * L::kKBuf;
@@ -1133,6 +679,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             constexpr int kKT = kPfKeys * (HD / 8) / kCT;                    // K tasks per thread
             constexpr int kVB = (kPfKeys / 8) * (HD / 32) / kPfConvWarps;    // V^T blocks per warp
             constexpr int kVG = kVB < 4 ? kVB : 4;                           // V^T blocks per round
+            const int w4 = warp - 4;
             const uint32_t vbase = base + L::kV + b * L::kVBuf;
             const uint32_t vsel = static_cast<uint32_t>(2 * (lane & 3)) | static_cast<uint32_t>(2 * (lane & 3) + 1) << 4;
             uint2 kw[kKT];
@@ -1148,10 +695,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     vw[j][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[j][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
                     if (!((mask >> key) & 1ull)) vw[j][0] = vw[j][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (drop_nan) {
-                        drop_nan_codes(vw[j][0], nan_seen);
-                        drop_nan_codes(vw[j][1], nan_seen);
-                    }
                 }
             };
             auto v_store = [&](int g0) {
@@ -1164,10 +707,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                     uint32_t r[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)  // bytes 8q + 2(t%4), +1 of the key's 32
-                    {
                         r[q] = f16x2_from_e4m3x2(__byte_perm(wd[2 * q], wd[2 * q + 1], vsel));
-                        if (BS) r[q] = mul_f16x2(r[q], vmul[0]);
-                    }
                     const int n = 32 * dg + 8 * (lane >> 3) + (lane & 7);  // V^T row this lane addresses
                     stsm_x4_t(vbase + sw128(n, ko), r[0], r[1], r[2], r[3]);
                 }
@@ -1221,11 +761,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 h.y = f16x2_from_e4m3x2_hi(w.x);
                 h.z = f16x2_from_e4m3x2(w.y);
                 h.w = f16x2_from_e4m3x2_hi(w.y);
-                if constexpr (BS) {
-                    constexpr int kPass = kCT / (HD / 8);  // keys of a round of tasks: 8, 16 or 32
-                    const uint32_t m = kPass <= 16 ? sc.k[j * kPass / 16] : ct < kCT / 2 ? sc.k[2 * j] : sc.k[2 * j + 1];
-                    h = make_uint4(mul_f16x2(h.x, m), mul_f16x2(h.y, m), mul_f16x2(h.z, m), mul_f16x2(h.w, m));
-                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kPfKeys * 128) + sw128(key, c & 7)) = h;
             }
             v_store(0);
@@ -1252,10 +787,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
         const int r = row0 + tid;                   // this thread's score row (TMEM lane tid)
         const bool row_ok = r < nb * G;
         const int jq = row_ok ? r / G : 0, gq = row_ok ? r % G : 0;
-        const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
+        const int pos = Ls - nb + jq;               // last key position the row may see
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        constexpr float kHead = F4 || BS ? kF4Head : 0.f;
+        constexpr float kHead = F4 ? kF4Head : 0.f;
         float m_used = -INFINITY, lsum = 0.f;
         bool ok = true;
         for (int i = 0; i < ntiles && ok; ++i) {
@@ -1277,22 +812,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             // the scale is applied inside the exponent's fma.
             const int k0 = key_tile(i) * kPfKeys;
             const int vis_n = row_ok ? min(kPfKeys, max(0, pos - k0 + 1)) : 0;  // keys 0..vis_n-1
-            uint64_t vis = mask & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
-            if (BS && !row_ok) vis = ~0ull;  // (a padding row holds no warp back)
-            float mx, mult = 1.f;
-            BlockMul mul = {};
-            if constexpr (BS) {
-                mul = get_block_mul(bp + L::kBufBs + 16 * b);
-                if (!__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((vis >> (32 * h + c)) & 1ull)) s[h][c] = 0xFF800000u;  // -infinity
-                }
-                mx = fmaf(extreme64<true>(s), mul.kmul, mul.vlog);
-                mult = mul.kmul;
-            } else if (__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
+            const uint64_t vis = mask & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
+            float mx, mult;
+            if (__all_sync(0xFFFFFFFFu, vis == ~0ull)) {
                 mx = (score_scale >= 0.f ? extreme64<true>(s) : extreme64<false>(s)) * score_scale;
                 mult = score_scale;
             } else {
@@ -1343,25 +865,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             // of 8 to 16 moves a weight by up to 2^-8.5, a rounded weight by 2^-11.
             uint32_t p[32];
             const float msub = m_used == -INFINITY ? 0.f : m_used;
-            const float shift = (BS ? mul.vlog : 0.f) - msub;
-            const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(shift, shift);
-            uint64_t sum2 = pk2(0.f, 0.f);  // BS: of the tile's weights
+            const uint64_t mul2 = pk2(mult, mult), sub2 = pk2(-msub, -msub);
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
                 const int h = c >> 4, e = (2 * c) & 31;
                 const float2 x = upk2(fma_f32x2(pk2u(s[h][e], s[h][e + 1]), mul2, sub2));
-                if constexpr (BS) {
-                    const float e0 = ex2(x.x), e1 = ex2(x.y);
-                    p[c] = f16x2_from_f32(e0, e1);
-                    sum2 = add_f32x2(sum2, pk2(e0, e1));
-                    continue;
-                }
                 p[c] = F4 ? f16x2_from_f32(ex2(x.x), ex2(x.y)) : ex2_f16x2(f16x2_from_f32(x.x, x.y));
                 if (!L::kSumCol) lsum += f16lo_f32(p[c]) + f16hi_f32(p[c]);
-            }
-            if constexpr (BS) {
-                const float2 sum = upk2(sum2);
-                lsum = fmaf(sum.x + sum.y, mul.vinv, lsum);
             }
             tmem_st32(lane_addr + 64 * b, p);
             tmem_wait_st();
@@ -1381,13 +891,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 lsum = __uint_as_float(o[0]);
             }
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
-            // what this row sees of the values that were taken out as NaN: tokens nan_first..nan_last
-            uint32_t nan_bits = 0;
-            const int key0 = kSplit ? tile_lo * kPfKeys : 0;  // of this part's keys
-            const int nan_last = row_ok ? kSplit ? min(pos, key0 + ntiles * kPfKeys - 1) : pos : -1;
-            const bool any_nan = (F4 || BS) && *nan_seen;
+            uint32_t nan_groups = 0;
             if constexpr (F4) {
-                if (any_nan) nan_bits = nan_value_groups<HD>(a, seq, kvh, key0, nan_last);
+                if (*nan_seen) {
+                    const int key0 = kSplit ? tile_lo * kPfKeys : 0;  // of this part's keys
+                    nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
+                                                      row_ok ? kSplit ? min(pos, key0 + ntiles * kPfKeys - 1) : pos : -1);
+                }
             }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + tile) * a.n_kv + kvh) * a.splits +
@@ -1398,15 +908,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-                if constexpr (BS) {
-                    if (any_nan)
-                        nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
-                }
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::kColO + c0, o);
                 tmem_wait_ld();
                 if constexpr (kSplit) {
-                    if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
+                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
@@ -1419,9 +925,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                         w.y = word(c / 2 + 1);
                         w.z = word(c / 2 + 2);
                         w.w = word(c / 2 + 3);
-                        if ((F4 || BS) && nan_bits != 0u)
-                            w = make_uint4(nan_in<C>(w.x, nan_bits, c0, c), nan_in<C>(w.y, nan_bits, c0, c + 2),
-                                           nan_in<C>(w.z, nan_bits, c0, c + 4), nan_in<C>(w.w, nan_bits, c0, c + 6));
+                        if (F4 && nan_groups != 0u) {
+                            const int d = c0 + c;
+                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
+                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
+                        }
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -1469,9 +977,8 @@ constexpr int kP2ConvWarps = 4;
 constexpr int kP2MmaWarp = 8 + kP2ConvWarps, kP2TmaWarp = kP2MmaWarp + 1;
 constexpr int kP2Warps = kP2TmaWarp + 1;
 
-template <int HD, Cache C>
+template <int HD, bool F4>
 struct Pf2Smem {
-    static constexpr bool F4 = C == Cache::kE2M1, BS = C == Cache::kBlocks;
     static constexpr int kRow = F4 ? HD / 2 : HD;
     static constexpr int kSeg = kRow >= 128 ? 128 : kRow;
     static constexpr int kSegs = kRow / kSeg;
@@ -1496,9 +1003,7 @@ struct Pf2Smem {
     static constexpr int kMeta = kDrain + 8;                       // valid-key mask per stage
     static constexpr int kBufMask = kMeta + 8 * kNS;               // per V^T buffer, two halves
     static constexpr int kMisc = kBufMask + 32;                    // tmem base, abort flag, NaN seen
-    // BS: a stage's scales ([side][16 keys]) and, per buffer and half, what the softmax takes of them
-    static constexpr int kStageBs = BS ? (kMisc + 31) / 16 * 16 : kMisc + 16, kBufBs = kStageBs + (BS ? 32 * kNS : 0);
-    static constexpr int kTotal = kBufBs + (BS ? 64 : 0);
+    static constexpr int kTotal = kMisc + 16;
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t col_s(int r) { return static_cast<uint32_t>(128 * r); }
     __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(256 + HD * r); }
@@ -1508,36 +1013,11 @@ struct Pf2Smem {
     __host__ __device__ static constexpr uint32_t col_p(int k) { return static_cast<uint32_t>(32 * (k >> 1) + 8 * (k & 1)); }
 };
 
-// the largest (kMax) or smallest of 32 scores, four chains of 3-input ops
-template <bool kMax>
-__device__ __forceinline__ float extreme32(const uint32_t (&s)[32]) {
-    auto v = [&](int c) { return __uint_as_float(s[c]); };
-    auto op = [](float a, float b, float c) { return kMax ? max3f(a, b, c) : min3f(a, b, c); };
-    float a0 = v(0), a1 = v(1), a2 = v(2), a3 = v(3);
-#pragma unroll
-    for (int c = 4; c < 28; c += 8) {
-        a0 = op(a0, v(c), v(c + 1));
-        a1 = op(a1, v(c + 2), v(c + 3));
-        a2 = op(a2, v(c + 4), v(c + 5));
-        a3 = op(a3, v(c + 6), v(c + 7));
-    }
-    a0 = op(a0, v(28), v(29));
-    a1 = op(a1, v(30), v(31));
-    return op(a0, a1, kMax ? fmaxf(a2, a3) : fminf(a2, a3));
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
-}
-
-template <int HD, Cache C, bool kSplit>
+template <int HD, bool F4, bool kSplit>
 __global__ void __launch_bounds__(kP2Warps * 32, 1)
 prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                const PrefillArgs<C> a) {
-    using L = Pf2Smem<HD, C>;
-    constexpr bool F4 = L::F4, BS = L::BS;
+                const PrefillArgs<F4> a) {
+    using L = Pf2Smem<HD, F4>;
     static_assert(L::kTotal + 1024 <= 232448, "shared memory");
     static_assert(L::col_o(1) + HD <= L::kTmemCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
@@ -1570,14 +1050,13 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
     const int Lraw = a.seq_lens[seq];
     const int Ls = min(max(Lraw, 0), a.max_len);
     if (ctile == 0 && kvh == 0 && tid == 0 &&
-        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.causal && qr.count > Ls)))
+        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || qr.count > Ls))
         flag(a.status, KVFP8_DEV_BAD_BLOCK);
     const int nb = qr.count, G = a.group;
     const int row0 = ctile * kP2Rows;                 // first score row of this CTA
     if (row0 >= nb * G) return;
     const int j_last = min(nb, (row0 + kP2Rows + G - 1) / G) - 1;
-    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;  // keys the CTA's last row may see
-    const int all_see = a.causal ? Ls - nb + row0 / G + 1 : Ls;  // (the keys before it every row sees)
+    const int kend = Ls - nb + j_last + 1;            // keys the CTA's last row may see
     int ntiles = kend > 0 ? (kend + kP2Keys - 1) / kP2Keys : 0;
     int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
     if constexpr (kSplit) {
@@ -1605,7 +1084,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
     if (tid == 0) {
         for (int s = 0; s < L::kNS; ++s) {
-            mbar_init(bar(L::kFull, s), F4 || BS ? 33 : 1);  // and every lane's scale copies
+            mbar_init(bar(L::kFull, s), F4 ? 33 : 1);  // F4: and every lane's scale copies
             mbar_init(bar(L::kEmpty, s), kP2ConvWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -1619,7 +1098,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         }
         mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
-        if (F4 || BS) *nan_seen = 0;
+        if (F4) *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kP2MmaWarp) {
@@ -1709,10 +1188,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 copy_scales<HD>(a, kvh, t0, kend, lbs, win, wbase, stage + L::kScales, L::kScaleSide,
                                 bar(L::kFull, st), lane);
             }
-            if constexpr (BS)
-                copy_block_scales(a, kvh, t0, kend, lbs, win, wbase, base + L::kStageBs + 32 * st, bar(L::kFull, st), lane);
         }
-        if ((F4 || BS) && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (F4 && aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
             flag(a.status, KVFP8_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -1825,16 +1302,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kKFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            uint64_t mask = meta[st];
-            BlockScales sc;
-            if constexpr (BS) {
-                sc.load(bp + L::kStageBs + 32 * st, mask);
-                if (ct == 0 && mask != sc.keys) flag(a.status, KVFP8_DEV_BAD_SCALE);
-                mask = sc.keys;
-            }
-            // a warp's V blocks are of eight keys, 32 apart from round to round
-            const uint32_t vmul[2] = {BS ? (w8 < 2 ? sc.v[0] : sc.v[1]) : 0u, BS ? (w8 < 2 ? sc.v[2] : sc.v[3]) : 0u};
-            const bool drop_nan = BS && key_tile(i) * kP2Keys + (hf + 1) * kPfKeys > all_see;  // as in the one-row-tile kernel
+            const uint64_t mask = meta[st];
             const uint8_t *kst = bp + L::kStage + st * L::kStageBytes;
             const uint8_t *vst = kst + kPfKeys * L::kRow;
             // this half's 64 keys: rows 64*hf.. of every 64-dim block of the K buffer
@@ -1853,10 +1321,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     vw[q][0] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc));
                     vw[q][1] = *reinterpret_cast<const uint4 *>(vrow + swz<L::kSeg>(key, cc + 1));
                     if (!((mask >> key) & 1ull)) vw[q][0] = vw[q][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (drop_nan) {
-                        drop_nan_codes(vw[q][0], nan_seen);
-                        drop_nan_codes(vw[q][1], nan_seen);
-                    }
                 }
             };
             auto v_store = [&](int g0) {
@@ -1869,10 +1333,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                     uint32_t rv[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)  // bytes 8e + 2(t%4), +1 of the key's 32
-                    {
                         rv[e] = f16x2_from_e4m3x2(__byte_perm(wd[2 * e], wd[2 * e + 1], vsel));
-                        if (BS) rv[e] = mul_f16x2(rv[e], vmul[q & 1]);
-                    }
                     const int n = 32 * dg + 8 * (lane >> 3) + (lane & 7);
                     stsm_x4_t(vbase + sw128(n, ko), rv[0], rv[1], rv[2], rv[3]);
                 }
@@ -1914,12 +1375,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 h.y = f16x2_from_e4m3x2_hi(w.x);
                 h.z = f16x2_from_e4m3x2(w.y);
                 h.w = f16x2_from_e4m3x2_hi(w.y);
-                if constexpr (BS) {
-                    constexpr int kPass = kCT / (HD / 8);  // keys of a round of tasks: 8 or 16
-                    static_assert(kPass <= 16, "a group a round");
-                    const uint32_t m = sc.k[q * kPass / 16];
-                    h = make_uint4(mul_f16x2(h.x, m), mul_f16x2(h.y, m), mul_f16x2(h.z, m), mul_f16x2(h.w, m));
-                }
                 *reinterpret_cast<uint4 *>(kdst0 + (c >> 3) * (kP2Keys * 128) + sw128(key, c & 7)) = h;
             }
             }
@@ -1933,9 +1388,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 ok = __all_sync(0xFFFFFFFFu,
                                 mbar_wait(bar(L::kVFree, b), ((i >> 1) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            if constexpr (BS) {
-                if (ct == 0) sc.put_mul(a.sm_scale * 1.4426950408889634f, bp + L::kBufBs + 32 * b + 16 * hf);
-            }
             if constexpr (F4) {
 #pragma unroll
                 for (int q = 0; q < kU4; ++q) {
@@ -1970,11 +1422,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
         const int r = row0 + tid;                   // this thread's score row
         const bool row_ok = r < nb * G;
         const int jq = row_ok ? r / G : 0, gq = row_ok ? r % G : 0;
-        const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
+        const int pos = Ls - nb + jq;               // last key position the row may see
         const float score_scale = a.sm_scale * sk * 1.4426950408889634f;  // log2(e)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t scol = lane_addr + L::col_s(rt);
-        constexpr float kHead = F4 || BS ? kF4Head : 0.f;
+        constexpr float kHead = F4 ? kF4Head : 0.f;
         float m_used = -INFINITY;
         uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
         bool ok = true;
@@ -1988,10 +1440,9 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             tc_fence_after();
             const int k0 = key_tile(i) * kP2Keys;
             const int vis_n = row_ok ? min(kP2Keys, max(0, pos - k0 + 1)) : 0;
-            uint64_t vis0 = buf_mask[2 * b] & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
-            uint64_t vis1 = buf_mask[2 * b + 1] &
-                            (vis_n >= 128 ? ~0ull : vis_n <= 64 ? 0ull : ((1ull << (vis_n - 64)) - 1));
-            if (BS && !row_ok) vis0 = vis1 = ~0ull;
+            const uint64_t vis0 = buf_mask[2 * b] & (vis_n >= 64 ? ~0ull : ((1ull << vis_n) - 1));
+            const uint64_t vis1 = buf_mask[2 * b + 1] &
+                                  (vis_n >= 128 ? ~0ull : vis_n <= 64 ? 0ull : ((1ull << (vis_n - 64)) - 1));
             const bool whole = __all_sync(0xFFFFFFFFu, (vis0 & vis1) == ~0ull);
             auto vis_bits = [&](int c) {  // the visible keys among columns 32c..32c+31
                 return static_cast<uint32_t>((c < 2 ? vis0 : vis1) >> (32 * (c & 1)));
@@ -2001,20 +1452,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             // registers for pass 2.
             uint32_t sa[32], sb[32];
             float mx = -INFINITY, ext = score_scale >= 0.f ? -INFINITY : INFINITY;
-            auto hide = [&](uint32_t (&sc)[32], int c) {  // BS: keys that the row does not see
-                if (!whole) {
-                    const uint32_t bits = vis_bits(c);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) sc[e] = 0xFF800000u;  // -infinity
-                }
-            };
-            auto chunk_max = [&](uint32_t (&sc)[32], int c) {
-                if constexpr (BS) {
-                    hide(sc, c);
-                    const BlockMul m = get_block_mul(bp + L::kBufBs + 32 * b + 16 * (c >> 1));
-                    mx = fmaxf(mx, fmaf(extreme32<true>(sc), m.kmul, m.vlog));
-                } else if (whole) {
+            auto chunk_max = [&](const uint32_t (&sc)[32], int c) {
+                if (whole) {
                     ext = score_scale >= 0.f ? fmaxf(ext, extreme32<true>(sc)) : fminf(ext, extreme32<false>(sc));
                 } else {
                     const uint32_t bits = vis_bits(c);
@@ -2033,7 +1472,7 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             tmem_wait_ld();
             chunk_max(sa, 2);
             chunk_max(sb, 3);
-            if (!BS && whole) mx = ext * score_scale;
+            if (whole) mx = ext * score_scale;
             float factor = 1.f;
             if (mx > -INFINITY) {
                 if (m_used == -INFINITY) {
@@ -2064,24 +1503,6 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float mult = whole ? score_scale : 1.f;
             const uint64_t mul2 = pk2(mult, mult);
             auto chunk_p = [&](uint32_t (&sc)[32], int c) {
-                if constexpr (BS) {
-                    if (c < 2) hide(sc, c);  // (loaded again)
-                    const BlockMul m = get_block_mul(bp + L::kBufBs + 32 * b + 16 * (c >> 1));
-                    const float shift = m.vlog - msub;
-                    const uint64_t kmul2 = pk2(m.kmul, m.kmul), shift2 = pk2(shift, shift);
-                    uint64_t sum2 = pk2(0.f, 0.f);
-                    uint32_t p[16];
-#pragma unroll
-                    for (int w = 0; w < 16; ++w) {
-                        const float2 x = upk2(fma_f32x2(pk2u(sc[2 * w], sc[2 * w + 1]), kmul2, shift2));
-                        const float e0 = ex2(x.x), e1 = ex2(x.y);
-                        p[w] = f16x2_from_f32(e0, e1);
-                        sum2 = add_f32x2(sum2, pk2(e0, e1));
-                    }
-                    lsum2 = fma_f32x2(sum2, pk2(m.vinv, m.vinv), lsum2);
-                    tmem_st16(scol + 32 * c, p);
-                    return;
-                }
                 if (!whole) {
                     const uint32_t bits = vis_bits(c);
 #pragma unroll
@@ -2119,13 +1540,13 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
             const float2 ls = upk2(lsum2);
             const float lsum = ls.x + ls.y;
             const float inv = lsum > 0.f ? sv / lsum : 0.f;
-            // what this row sees of the values that were taken out as NaN: tokens nan_first..nan_last
-            uint32_t nan_bits = 0;
-            const int key0 = kSplit ? tile_lo * kP2Keys : 0;  // of this part's keys
-            const int nan_last = row_ok ? kSplit ? min(pos, key0 + ntiles * kP2Keys - 1) : pos : -1;
-            const bool any_nan = (F4 || BS) && *nan_seen;
+            uint32_t nan_groups = 0;
             if constexpr (F4) {
-                if (any_nan) nan_bits = nan_value_groups<HD>(a, seq, kvh, key0, nan_last);
+                if (*nan_seen) {
+                    const int key0 = kSplit ? tile_lo * kP2Keys : 0;  // of this part's keys
+                    nan_groups = nan_value_groups<HD>(a, seq, kvh, key0,
+                                                      row_ok ? kSplit ? min(pos, key0 + ntiles * kP2Keys - 1) : pos : -1);
+                }
             }
             // this row in the parts' results, when there are several
             const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
@@ -2136,15 +1557,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                 a.out + ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD);
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
-                if constexpr (BS) {
-                    if (any_nan)
-                        nan_bits = nan_value_dims<HD>(a, seq, kvh, c0, max(key0, max(all_see, 0) / kPfKeys * kPfKeys), nan_last);
-                }
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
                 if constexpr (kSplit) {
-                    if (row_ok) store_part<C>(a.part_o + prow * HD, o, part_inv, nan_bits, c0);
+                    if (row_ok) store_part(a.part_o + prow * HD, o, part_inv, nan_groups, c0);
                 } else if (row_ok) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
@@ -2157,9 +1574,11 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
                         w.y = word(c / 2 + 1);
                         w.z = word(c / 2 + 2);
                         w.w = word(c / 2 + 3);
-                        if ((F4 || BS) && nan_bits != 0u)
-                            w = make_uint4(nan_in<C>(w.x, nan_bits, c0, c), nan_in<C>(w.y, nan_bits, c0, c + 2),
-                                           nan_in<C>(w.z, nan_bits, c0, c + 4), nan_in<C>(w.w, nan_bits, c0, c + 6));
+                        if (F4 && nan_groups != 0u) {
+                            const int d = c0 + c;
+                            w = make_uint4(nan_in(w.x, nan_groups, d), nan_in(w.y, nan_groups, d),
+                                           nan_in(w.z, nan_groups, d), nan_in(w.w, nan_groups, d));
+                        }
                         orow[(c0 + c) / 8] = w;
                     }
                 }
@@ -2179,8 +1598,8 @@ prefill2_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__
 
 // Joins the parts of each row: CTA (x, y) takes 256 / (HD / 4) rows of row tile x (of tile_rows rows, keys in
 // tiles of tile_keys).
-template <int HD, Cache C>
-__global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<C> a, int tile_rows, int tile_keys) {
+template <int HD>
+__global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<true> a, int tile_rows, int tile_keys) {
     constexpr int kLanes = HD / 4;  // threads of a row, four dims each
     const int kvh = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.n_kv));
     const int tile = static_cast<int>((blockIdx.x / static_cast<unsigned>(a.n_kv)) % static_cast<unsigned>(a.row_tiles));
@@ -2196,7 +1615,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<C> a,
     if (r >= nb * G) return;
     // the row tile's parts, as its CTAs worked them out
     const int j_last = min(nb, (row0 + tile_rows + G - 1) / G) - 1;
-    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;
+    const int kend = Ls - nb + j_last + 1;
     if (kend <= 0) return;  // zeroed by its CTA
     const int parts = split_parts(a.splits, (kend + tile_keys - 1) / tile_keys, tile_keys);
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
@@ -2243,8 +1662,8 @@ SplitPlan split_plan(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_d
     return p;
 }
 
-template <int HD, Cache C>
-cudaError_t join_parts(const PrefillArgs<C> &a, const SplitPlan &p, cudaStream_t stream) {
+template <int HD>
+cudaError_t join_parts(const PrefillArgs<true> &a, const SplitPlan &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_seqs * a.row_tiles * a.n_kv, p.tile_rows / (256 / (HD / 4)));
     cfg.blockDim = dim3(256);
@@ -2254,13 +1673,12 @@ cudaError_t join_parts(const PrefillArgs<C> &a, const SplitPlan &p, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD, C>, a, p.tile_rows, p.tile_keys);
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD>, a, p.tile_rows, p.tile_keys);
 }
 
-template <int HD, Cache C>
+template <int HD, bool F4>
 cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
-    using L = PfSmem<HD, C>;
-    constexpr bool kParts = C != Cache::kE4M3;
+    using L = PfSmem<HD, F4>;
     const int row_bytes = d.n_kv * L::kRow;
     const int box_rows = d.block_size >= kPfKeys ? kPfKeys : d.block_size;  // whole tile when one block holds it
     const int64_t rows = static_cast<int64_t>(d.num_blocks) * d.block_size;
@@ -2270,7 +1688,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         return err;
     if ((err = encode_cache_map(&tmv, d.value_cache, rows, row_bytes, L::kSeg, box_rows)) != cudaSuccess)
         return err;
-    PrefillArgs<C> a;
+    PrefillArgs<F4> a;
     a.out = static_cast<__nv_bfloat16 *>(d.out);
     a.query = static_cast<const __nv_bfloat16 *>(d.query);
     a.qsl = d.qsl;
@@ -2293,27 +1711,18 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     a.status = d.status;
     a.box_rows = box_rows;
     SplitPlan sp;
-    if constexpr (C == Cache::kE2M1) {
+    if constexpr (F4) {
+        sp = split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
         a.key_scales = d.key_scales;
         a.value_scales = d.value_scales;
-    }
-    if constexpr (C == Cache::kBlocks) {
-        a.key_scales = d.key_block_scales;
-        a.value_scales = d.value_block_scales;
-        a.value_cache = d.value_cache;
-        a.scale_stride = d.block_scale_stride;
-        a.causal = d.causal != 0;
-    }
-    if constexpr (kParts) {
-        sp = split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
         a.splits = sp.splits;
         a.part_o = static_cast<float *>(d.workspace);
         a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(d.workspace) + sp.lse_off);
     }
     auto launched = [&]() -> cudaError_t {
         const cudaError_t e = cudaGetLastError();
-        if constexpr (kParts) {
-            if (e == cudaSuccess && sp.splits > 1) return join_parts<HD, C>(a, sp, stream);
+        if constexpr (F4) {
+            if (e == cudaSuccess && sp.splits > 1) return join_parts<HD>(a, sp, stream);
         }
         return e;
     };
@@ -2321,8 +1730,8 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     // more than one tile of 128 rows per kv head (a multi-query call): 256 rows per CTA
     if constexpr (HD <= 128) {
         if (d.qsl != nullptr && group_rows > kPfRows) {
-            const size_t smem2 = Pf2Smem<HD, C>::kTotal + 1024;
-            auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, C, kParts> : prefill2_kernel<HD, C, false>;
+            const size_t smem2 = Pf2Smem<HD, F4>::kTotal + 1024;
+            auto kern2 = sp.splits > 1 ? prefill2_kernel<HD, F4, F4> : prefill2_kernel<HD, F4, false>;
             int occ2 = 0;  // also raises the kernel's shared memory limit, once per device
             if ((err = kernel_occupancy(kern2, kP2Warps * 32, smem2, &occ2)) != cudaSuccess)
                 return err;
@@ -2333,7 +1742,7 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
         }
     }
     const size_t smem = L::kTotal + 1024;
-    auto kern = sp.splits > 1 ? prefill_kernel<HD, C, kParts> : prefill_kernel<HD, C, false>;
+    auto kern = sp.splits > 1 ? prefill_kernel<HD, F4, F4> : prefill_kernel<HD, F4, false>;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
     if ((err = kernel_occupancy(kern, kPfWarps * 32, smem, &occ)) != cudaSuccess) return err;
     a.row_tiles = (group_rows + kPfRows - 1) / kPfRows;
@@ -2342,19 +1751,9 @@ cudaError_t run_prefill(const DecodeArgs &d, cudaStream_t stream) {
     return launched();
 }
 
-template <Cache C>
-cudaError_t run_head_dim(const DecodeArgs &d, cudaStream_t stream) {
-    switch (d.head_dim) {
-        case 64: return run_prefill<64, C>(d, stream);
-        case 128: return run_prefill<128, C>(d, stream);
-        case 256: return run_prefill<256, C>(d, stream);
-        default: return cudaErrorNotSupported;
-    }
-}
-
 }  // namespace
 
-size_t split_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+size_t fp4_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
                                   int64_t max_len) {
     return split_plan(num_seqs, n_q, n_kv, head_dim, qmax, max_len).total;
 }
@@ -2371,8 +1770,13 @@ cudaError_t launch_prefill_attention(const DecodeArgs &d, cudaStream_t stream) {
     if (d.num_seqs == 0) return cudaSuccess;
     if (d.k_bf16 || d.v_bf16) return cudaErrorNotSupported;
     if (!prefill_takes(d.n_q, d.n_kv, d.qmax, d.num_seqs)) return cudaErrorNotSupported;
-    if (d.key_block_scales != nullptr) return run_head_dim<Cache::kBlocks>(d, stream);
-    return d.key_scales != nullptr ? run_head_dim<Cache::kE2M1>(d, stream) : run_head_dim<Cache::kE4M3>(d, stream);
+    const bool f4 = d.key_scales != nullptr;
+    switch (d.head_dim) {
+        case 64: return f4 ? run_prefill<64, true>(d, stream) : run_prefill<64, false>(d, stream);
+        case 128: return f4 ? run_prefill<128, true>(d, stream) : run_prefill<128, false>(d, stream);
+        case 256: return f4 ? run_prefill<256, true>(d, stream) : run_prefill<256, false>(d, stream);
+        default: return cudaErrorNotSupported;
+    }
 }
 
 }  // namespace kvfp8

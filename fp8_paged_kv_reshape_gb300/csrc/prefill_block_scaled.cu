@@ -1,0 +1,947 @@
+// Attention over the FP8 cache with block scales for long query chunks and wide groups of heads, causal or
+// not, sm_103a tensor cores (tcgen05) with accumulators in tensor memory:
+//   s_t = sm_scale * ks(block of t) * q . dec(K_t),   out = sum_t softmax(s)_t * vs(block of t) * dec(V_t)
+//
+// Rows are (query token j, head g of the kv head's group) pairs, row = j*G + g; a CTA takes RT tiles of 128 rows of a
+// (sequence, kv head) and goes over their keys in tiles of 128.  What bounds it is the chain of a row tile's scores,
+// softmax and product with V, so the work beside it is kept small:
+//  * K is not converted.  q is the sum of two E4M3 numbers: with q scaled by a power of two per row, so that its largest
+//    element lies in [128, 256), a = E4M3(q) and b = E4M3(q - a) give a bf16's 8 bits exactly where it is within 2^10 of the
+//    row's largest, and to 2^-18 of that below.  K tiles arrive by TMA as the operand that the product takes
+//    (kind::f8f6f4, twice the rate of f16: two products at half the time), products are exact, sums float.
+//  * V meets fp16 weights, so it is converted to fp16 (exactly) and transposed: ldmatrix gives a lane four
+//    dims of a key, which after the conversion are stored with stmatrix.trans as rows of V^T.
+//  * ks multiplies the scores, 16 keys at a time (a block is 16 keys at least), in the multiplication that takes them
+//    to the log2 domain.  vs: V's codes are multiplied by their scale over 2^-7 of the largest of their 64 keys (a
+//    power of two: exact while scales there are within 2^22 of each other, else to 2^-40 of the largest value that scale
+//    holds), and that one goes into the exponent: the weights that meet V are 2^(s + log2 vs - m) with m near the
+//    highest s + log2 vs, within fp16's range whatever the scales, and the row's sum adds 64 keys' weights
+//    times 1 / vs.  Weights are held as over the 4-bit cache: m lies 2^7 below the highest at the time, weights reach
+//    2^15, so they keep 11 bits down to 2^-21 of the highest and are above zero down to 2^-32.
+//  * P is handed over in two halves of 64 keys: the product with V starts while the second half's exponentials are
+//    taken.
+//
+// Two row tiles (head_dim 64 and 128, more than 128 rows) share the converted V and take turns on the tensor core;
+// one row tile has two score buffers, the next tile's scores being computed meanwhile.
+//
+// NaN: a NaN code in K makes the key's scores NaN, which the masks keep from rows that do not see it.  One
+// in V may reach all rows where all of them see the key.  Where not (the last tiles of a causal call), such codes are
+// taken as 0, the CTA remembers that it met one, and at the end its rows look up which dims of the values
+// they see are NaN (a slow scan that no finite cache runs).
+//
+// Every wait is bounded; one that runs out sets KVFP8_DEV_TIMEOUT, and tensor memory is always released.
+#include "kvfp8_block_scale.cuh"
+#include "prefill_common.cuh"
+
+namespace kvfp8 {
+namespace {
+
+constexpr int kKeys = 128;  // of a tile
+constexpr int kHalf = 64;   // V arrives and is converted in halves
+constexpr int kConvWarps = 4;
+constexpr float kHead = 7.f;  // see above
+constexpr float kLag = 8.f;   // log2: how far scores may rise above the highest one when the reference was set
+
+struct BlockPrefillArgs : PrefillCommon {
+    const uint8_t *value_cache;
+    const float *key_scales, *value_scales;  // [block][scale_stride], a kv head's at its index
+    int32_t scale_stride;
+    bool causal;  // else every query sees every cached token
+    // parts a (sequence, kv head, row tiles)'s keys are cut into at most (gridDim.y), and the parts'
+    // results, [CTA of the unsplit grid, in sequence order][part][row]
+    int32_t splits;
+    float *part_o, *part_lse;
+};
+
+template <int HD, int RT>
+struct PbSmem {
+    static constexpr int kSeg = HD < 128 ? HD : 128, kSegs = HD / kSeg;  // bytes of a TMA box row; of a key's head
+    static constexpr int kNK = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // K tiles
+    static constexpr int kNV = HD == 256 ? 2 : 4;                        // V^T halves
+    static constexpr int kNS = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // staged V halves
+    // q: a row tile's two E4M3 parts, 128 rows of [segment][row][kSeg] each
+    static constexpr int kPart = 128 * HD;
+    static constexpr int kQ = 0;
+    static constexpr int kKBuf = kKeys * HD, kK = kQ + RT * 2 * kPart;   // [segment][128 keys][kSeg]
+    static constexpr int kVBuf = HD * 128, kV = kK + kNK * kKBuf;        // [HD dims][64 keys] f16
+    static constexpr int kStageBuf = kHalf * HD, kStage = kV + kNV * kVBuf;  // [segment][64 keys][kSeg]
+    static constexpr int kInfo = kStage + kNS * kStageBuf;               // HalfInfo per V^T half
+    static constexpr int kScales = kInfo + 48 * kNV;                     // [side][16 keys] per staged half
+    static constexpr int kBars = kScales + 32 * kNS;
+    // mbarriers
+    static constexpr int kKFull = kBars, kKFree = kKFull + 16 * kNK;     // (a K tile's halves; a K tile)
+    static constexpr int kVFull = kKFree + 8 * kNK, kVEmpty = kVFull + 8 * kNS;
+    static constexpr int kVReady = kVEmpty + 8 * kNS, kVFree = kVReady + 8 * kNV;
+    static constexpr int kQReady = kVFree + 8 * kNV;
+    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;  // (per score buffer; per half of it)
+    static constexpr int kODone = kPReady + 32, kDrain = kODone + 16;
+    static constexpr int kMeta = kDrain + 8;                             // valid keys per staged half
+    static constexpr int kMisc = kMeta + 8 * kNS;                        // tmem base, abort flag, NaN seen
+    static constexpr int kTotal = kMisc + 16;
+    static_assert(kTotal + 1024 <= 232448, "shared memory");
+    // tensor memory: two score buffers of 128 columns (a row tile's, or in turns), then O of each row tile
+    static constexpr uint32_t kTmemCols = 512;
+    __host__ __device__ static constexpr uint32_t col_s(int b) { return static_cast<uint32_t>(128 * b); }
+    __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(256 + HD * r); }
+    static_assert(256 + RT * HD <= 512, "tensor memory");
+};
+
+// What the softmax takes of 64 keys: scores (over the row's q scale) times kmul[16 keys] are in the log2 domain, weights
+// carry vlog, their sum vinv; the keys that are there.
+struct HalfInfo {
+    float kmul[4];
+    float vlog, vinv;
+    uint32_t mask[2];
+    uint32_t pad[4];
+};
+static_assert(sizeof(HalfInfo) == 48, "layout");
+
+// P of keys 16k..16k+15 (f16 pairs, 8 columns): the first half of the 32 columns that held the scores of keys
+// 32(k/2)..+31, so each 32-key chunk's P overwrites only its own scores
+__host__ __device__ constexpr uint32_t col_p(int k) { return static_cast<uint32_t>(32 * (k >> 1) + 8 * (k & 1)); }
+
+// ---------------------------------------------------------------- 8-bit operands
+
+// D (TMEM) (+)= A x B, both 8-bit in shared memory
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: E4M3 A and B, fp32 D, both K-major, M x N.
+__host__ __device__ constexpr uint32_t e4m3_idesc(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// Shared-memory matrix descriptor: K-major operand of SEG-byte rows (128 or 64) swizzled over them.
+template <int SEG>
+__device__ __forceinline__ uint64_t k_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) |
+           (static_cast<uint64_t>((8 * SEG) >> 4) << 32)  // 8 rows
+           | (1ull << 46) | (SEG == 128 ? 2ull << 61 : 4ull << 61);
+}
+
+// ---------------------------------------------------------------- block scales
+
+// The V scales of 64 keys over 2^-7 of the largest of them, as fp16 pairs, and that one; the keys whose block has
+// valid scales (of either side).
+struct HalfScales {
+    uint64_t keys;
+    float vref;        // 1 without any
+    float k[4];
+    uint32_t v[4];
+
+    __device__ __forceinline__ static uint32_t over(float s, float ref) {
+        // 2^(7 - d), d = log2(ref / s): an fp16 number, or one of its denormals, or 0
+        const int e = static_cast<int>(__float_as_uint(s) >> 23) - static_cast<int>(__float_as_uint(ref) >> 23) + 22;
+        const uint32_t h = e >= 1 ? static_cast<uint32_t>(e) << 10 : e >= -9 ? 1u << (9 + e) : 0u;
+        return h * 0x10001u;
+    }
+    // (a group without keys has no scales either: what stands there is of another tile)
+    __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask) {
+        const float4 k4 = *reinterpret_cast<const float4 *>(at), v4 = *reinterpret_cast<const float4 *>(at + 16);
+        const float ks[4] = {k4.x, k4.y, k4.z, k4.w}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
+        keys = 0;
+        vref = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint64_t group = mask & (0xFFFFull << (16 * g));
+            k[g] = 1.f;
+            if (group == 0ull || !(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) continue;
+            keys |= group;
+            k[g] = ks[g];
+            vref = fmaxf(vref, vs[g]);
+        }
+        if (keys == 0ull) vref = 1.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) v[g] = (keys & (0xFFFFull << (16 * g))) != 0ull ? over(vs[g], vref) : 0u;
+    }
+};
+
+// The dims d0..d0+31 (bit i: d0 + i) in which some value of tokens first..last of the sequence is NaN, for each
+// lane's own last (negative: none); blocks out of range or without valid scales hold no tokens.  Called by
+// whole warps: the tokens that every lane has are shared out over the lanes, the few after them are each lane's own.
+template <int HD>
+__device__ __noinline__ uint32_t nan_value_dims(const BlockPrefillArgs &a, int seq, int kvh, int d0, int first, int last) {
+    const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+    uint32_t dims = 0;
+    auto look = [&](int t) {
+        const int32_t blk = bt[t / a.block_size];
+        if (blk < 0 || blk >= a.num_blocks) return;
+        const int64_t s = static_cast<int64_t>(blk) * a.scale_stride + kvh;
+        if (!block_scale_ok(a.key_scales[s]) || !block_scale_ok(a.value_scales[s])) return;
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(
+            a.value_cache + ((static_cast<int64_t>(blk) * a.block_size + t % a.block_size) * a.n_kv + kvh) * HD + d0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t nan = nan_byte_mask(row[i]) & 0x08040201u;
+            dims |= ((nan | nan >> 8 | nan >> 16 | nan >> 24) & 0xFu) << (4 * i);
+        }
+    };
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int all = __reduce_min_sync(0xFFFFFFFFu, last < 0 ? INT32_MAX : last);  // tokens first..all are every lane's
+    if (all != INT32_MAX)
+        for (int t = first + lane; t <= all; t += 32) look(t);
+    dims = __reduce_or_sync(0xFFFFFFFFu, dims);
+    if (last < 0) return 0u;
+    for (int t = max(first, all + 1); t <= last; ++t) look(t);
+    return dims;
+}
+
+// the largest of 16 scores
+__device__ __forceinline__ float max16(const uint32_t *s) {
+    auto v = [&](int c) { return __uint_as_float(s[c]); };
+    const float a = max3f(max3f(v(0), v(1), v(2)), v(3), v(4)), b = max3f(max3f(v(5), v(6), v(7)), v(8), v(9));
+    const float c = max3f(max3f(v(10), v(11), v(12)), v(13), v(14));
+    return fmaxf(max3f(a, b, c), v(15));
+}
+
+// One row of q (HD bf16, or zeros) as two E4M3 parts at part0 and part1 (row `row` of K-major operands); returns what a
+// score is to be multiplied by for it.
+template <int HD, int SEG>
+__device__ __forceinline__ float split_q_row(const __nv_bfloat16 *q, uint8_t *part0, uint8_t *part1, int row) {
+    uint32_t top = 0;  // the largest magnitude's bits, in either half
+    bool odd = false;
+    if (q != nullptr) {
+#pragma unroll 4
+        for (int c = 0; c < HD / 8; ++c) {
+            const uint4 w = reinterpret_cast<const uint4 *>(q)[c];
+            top = __vmaxu2(__vmaxu2(top, w.x & 0x7FFF7FFFu), __vmaxu2(w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu));
+            top = __vmaxu2(top, w.w & 0x7FFF7FFFu);
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+        odd = top >= 0x7F80u;  // an infinity or NaN: the whole row becomes NaN
+    }
+    // 2^(7 - e) of the largest's exponent e, kept where it and its inverse are floats
+    const int e = min(max(static_cast<int>(top >> 7), 20), 254);
+    const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23), down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
+#pragma unroll 2
+    for (int c = 0; c < HD / 16; ++c) {
+        uint32_t w[8] = {};
+        if (q != nullptr) {
+            const uint4 lo = reinterpret_cast<const uint4 *>(q)[2 * c], hi = reinterpret_cast<const uint4 *>(q)[2 * c + 1];
+            w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+        }
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = bf16lo(w[i]) * up, y = bf16hi(w[i]) * up;
+            const uint32_t hi = e4m3x2_from_f32(x, y);
+            const float2 back = __half22float2(h2(f16x2_from_e4m3x2(hi)));
+            const uint32_t rest = e4m3x2_from_f32(x - back.x, y - back.y);
+            a[i / 2] = i & 1 ? a[i / 2] | hi << 16 : hi;
+            b[i / 2] = i & 1 ? b[i / 2] | rest << 16 : rest;
+        }
+        if (odd) a[0] = a[1] = a[2] = a[3] = 0x7F7F7F7Fu;
+        const uint32_t at = static_cast<uint32_t>((16 * c / SEG) * (128 * SEG)) + swz<SEG>(row, 16 * c % SEG / 16);
+        *reinterpret_cast<uint4 *>(part0 + at) = make_uint4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<uint4 *>(part1 + at) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+    return down;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one
+// issuing products (and allocating TMEM), one issuing copies.
+template <int RT>
+struct PbWarps {
+    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + 1, kAll = kTma + 1;
+};
+
+template <int HD, int RT, bool kSplit>
+__global__ void __launch_bounds__(PbWarps<RT>::kAll * 32, 1)
+prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                      const __grid_constant__ BlockPrefillArgs a) {
+    using L = PbSmem<HD, RT>;
+    using W = PbWarps<RT>;
+    constexpr int kRows = 128 * RT;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *bp = smem_raw + (base - raw);
+    volatile uint64_t *meta = reinterpret_cast<volatile uint64_t *>(bp + L::kMeta);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(bp + L::kMisc);
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 4);
+    volatile int32_t *nan_seen = reinterpret_cast<volatile int32_t *>(bp + L::kMisc + 8);
+    auto bar = [&](int off, int i) { return base + static_cast<uint32_t>(off + 8 * i); };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // kv head fastest, then row tiles, then sequence (longest first): a (sequence, kv head)'s CTAs run side by side on
+    // one K/V stream
+    const int kvh = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.n_kv));
+    const int ctile = static_cast<int>((blockIdx.x / static_cast<unsigned>(a.n_kv)) % static_cast<unsigned>(a.row_tiles));
+    const int rank = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.n_kv * a.row_tiles));
+    // (the K tiles are free scratch until the pipeline starts)
+    const int seq = seq_of_rank(a.seq_lens, a.num_seqs, a.max_len, rank, reinterpret_cast<uint32_t *>(bp + L::kK));
+    const int raw_nq = a.qsl ? a.qsl[seq + 1] - a.qsl[seq] : 1;
+    const QueryRange qr = a.qsl ? query_range(a.qsl, seq, a.qmax, a.qrows) : QueryRange{seq, 1};
+    const int Lraw = a.seq_lens[seq];
+    const int Ls = min(max(Lraw, 0), a.max_len);
+    if (ctile == 0 && kvh == 0 && tid == 0 && (!kSplit || blockIdx.y == 0) &&
+        (qr.count != raw_nq || Lraw < 0 || Lraw > a.max_len || (a.qsl && a.causal && qr.count > Ls)))
+        flag(a.status, KVFP8_DEV_BAD_BLOCK);
+    const int nb = qr.count, G = a.group;
+    const int row0 = ctile * kRows;  // first row of this CTA
+    if (row0 >= nb * G) return;
+    const int j_last = min(nb, (row0 + kRows + G - 1) / G) - 1;
+    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;          // keys the CTA's last row may see
+    const int all_see = a.causal ? Ls - nb + row0 / G + 1 : Ls;     // (the keys before it every row sees)
+    int ntiles = kend > 0 ? (kend + kKeys - 1) / kKeys : 0;
+    int tile_lo = 0;  // this CTA's key tiles: ntiles from tile_lo on
+    if constexpr (kSplit) {
+        const int parts = split_parts(a.splits, ntiles, kKeys);
+        const int part = static_cast<int>(blockIdx.y);
+        if (part >= parts) return;
+        tile_lo = static_cast<int>(static_cast<int64_t>(part) * ntiles / parts);
+        ntiles = static_cast<int>(static_cast<int64_t>(part + 1) * ntiles / parts) - tile_lo;
+    }
+    // each of the row tiles side by side starts its pass at its own key tile (the online softmax takes the keys in any
+    // order), so they read different lines of the stream at any one time
+    const int rot = ntiles > 0 ? static_cast<int>((static_cast<int64_t>(ctile) * ntiles) / a.row_tiles) % ntiles : 0;
+    auto key_tile = [&](int i) { const int k = i + rot; return (k >= ntiles ? k - ntiles : k) + tile_lo; };
+
+    if (ntiles == 0) {  // every row of the CTA sees no key: zero rows
+        if (tid < kRows) {
+            const int r = row0 + tid;
+            if (r < nb * G) {
+                uint4 *o = reinterpret_cast<uint4 *>(a.out + ((static_cast<int64_t>(qr.q0) + r / G) * a.n_q + kvh * G + r % G) * HD);
+                for (int c = 0; c < HD / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        for (int i = 0; i < L::kNK; ++i) {
+            mbar_init(bar(L::kKFull, 2 * i), 1);
+            mbar_init(bar(L::kKFull, 2 * i + 1), 1);
+            mbar_init(bar(L::kKFree, i), 1);
+        }
+        for (int i = 0; i < L::kNS; ++i) {
+            mbar_init(bar(L::kVFull, i), 1 + 32);  // the post, and every lane's scale copies
+            mbar_init(bar(L::kVEmpty, i), kConvWarps);
+        }
+        for (int i = 0; i < L::kNV; ++i) {
+            mbar_init(bar(L::kVReady, i), kConvWarps);
+            mbar_init(bar(L::kVFree, i), 1);
+        }
+        mbar_init(bar(L::kQReady, 0), 4 * RT);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::kSReady, i), 1);
+            mbar_init(bar(L::kPReady, 2 * i), 4);
+            mbar_init(bar(L::kPReady, 2 * i + 1), 4);
+            mbar_init(bar(L::kODone, i), 1);
+        }
+        mbar_init(bar(L::kDrain, 0), 1);
+        *abort_flag = 0;
+        *nan_seen = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == W::kMma) {
+        tmem_alloc(base + L::kMisc, L::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == W::kTma && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const volatile int32_t never = 0;
+
+    if (warp == W::kTma) {
+        // ------------------------------------------------------------ copies
+        // half h of the key pass (64 keys of tile h/2): lane p < nbox copies K box p, lane nbox + p V box p
+        const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+        const int bs = a.block_size, br = a.box_rows;
+        const int lbs = __ffs(bs) - 1;
+        const int nbox = kHalf / br;
+        const bool k_lane = lane < nbox;
+        const int p = k_lane ? lane : lane - nbox;
+        const bool box_lane = lane < 2 * nbox;
+        const CUtensorMap *map = k_lane ? &tmk : &tmv;
+        int wbase = -(1 << 30);
+        int32_t win = -1;  // the lane's block-table entry of the window from wbase on
+        int issued = 0;
+        bool aborted = false;
+        for (int h = 0; h < 2 * ntiles; ++h) {
+            const int i = h >> 1, hf = h & 1, kb = i % L::kNK, st = h % L::kNS;
+            const int t0 = key_tile(i) * kKeys + hf * kHalf;
+            if (t0 < kend) {
+                const int e0 = t0 >> lbs, e1 = (min(kend, t0 + kHalf) - 1) >> lbs;
+                if (e0 < wbase || e1 >= wbase + 32) {
+                    wbase = e0;
+                    win = wbase + lane < a.max_blocks_per_seq ? bt[wbase + lane] : -1;
+                }
+            }
+            // this lane's box: its first key t, the block holding it, and whether it is copied (keys past kend are
+            // left out; a bad block is flagged and left out)
+            const int t = t0 + p * br;
+            const int blk = __shfl_sync(0xFFFFFFFFu, win, ((t >> lbs) - wbase) & 31);
+            const bool live = box_lane && t < kend;
+            const bool good = live && blk >= 0 && blk < a.num_blocks;
+            if (live && !good && k_lane) flag(a.status, KVFP8_DEV_BAD_BLOCK);
+            uint64_t part = 0;
+            if (good && k_lane) {
+                const int nk = min(br, kend - t);
+                part = (nk >= 64 ? ~0ull : ((1ull << nk) - 1)) << (p * br);
+            }
+            const uint64_t mask =
+                static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(part))) |
+                static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(part >> 32))) << 32;
+            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, good && k_lane));
+            // and its scale: lanes 0-3 the K scales of 16 keys each, 4-7 the V scales
+            const int ts = t0 + 16 * (lane & 3);
+            const int sblk = __shfl_sync(0xFFFFFFFFu, win, ((ts >> lbs) - wbase) & 31);
+            const uint32_t kfull = bar(L::kKFull, 2 * kb + hf), vfull = bar(L::kVFull, st);
+            if (lane == 0) {
+                if ((hf == 0 && !mbar_wait(bar(L::kKFree, kb), ((i / L::kNK) & 1) ^ 1u, abort_flag)) ||
+                    !mbar_wait(bar(L::kVEmpty, st), ((h / L::kNS) & 1) ^ 1u, abort_flag)) {
+                    aborted = true;
+                } else {
+                    meta[st] = mask;
+                    if (boxes > 0) {
+                        mbar_arrive_tx(kfull, static_cast<uint32_t>(boxes * br * HD));
+                        mbar_arrive_tx(vfull, static_cast<uint32_t>(boxes * br * HD));
+                    } else {
+                        mbar_arrive(kfull);
+                        mbar_arrive(vfull);
+                    }
+                    ++issued;
+                }
+            }
+            aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
+            if (aborted) break;
+            __syncwarp();  // what lane 0 waited for (the buffers have been read) holds for every lane's copies
+            if (good) {  // the expected bytes are posted: each lane with a box copies it
+                const int row = blk * bs + (t & (bs - 1));
+                const uint32_t dst = k_lane ? base + L::kK + kb * L::kKBuf + static_cast<uint32_t>((hf * kHalf + p * br) * L::kSeg)
+                                            : base + L::kStage + st * L::kStageBuf + static_cast<uint32_t>(p * br * L::kSeg);
+                const uint32_t seg = static_cast<uint32_t>((k_lane ? kKeys : kHalf) * L::kSeg);
+#pragma unroll
+                for (int sgi = 0; sgi < L::kSegs; ++sgi)
+                    tma_load_3d(dst + sgi * seg, map, 0, kvh * L::kSegs + sgi, row, k_lane ? kfull : vfull);
+            }
+            if (lane < 8 && ts < kend && sblk >= 0 && sblk < a.num_blocks)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(base + L::kScales + 32 * st + 4 * lane),
+                             "l"((lane < 4 ? a.key_scales : a.value_scales) + static_cast<int64_t>(sblk) * a.scale_stride + kvh)
+                             : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(vfull) : "memory");
+        }
+        if (aborted) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (aborted && lane == 0) {
+            flag(a.status, KVFP8_DEV_TIMEOUT);
+            *abort_flag = 1;
+            // let copies already issued land before the CTA's shared memory goes away
+            for (int k = max(0, issued - max(L::kNS, 2 * L::kNK)); k < issued; ++k) {
+                if (k >= issued - L::kNS) mbar_wait(bar(L::kVFull, k % L::kNS), (k / L::kNS) & 1, &never);
+                mbar_wait(bar(L::kKFull, 2 * ((k >> 1) % L::kNK) + (k & 1)), ((k >> 1) / L::kNK) & 1, &never);
+            }
+        }
+    } else if (warp == W::kMma) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            const uint32_t idesc_s = e4m3_idesc(128, kKeys), idesc_o = f16_idesc(128, HD);
+            // operand descriptors computed once; each product adds its constant offset
+            const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ), kdesc = k_desc<L::kSeg>(base + L::kK),
+                           vdesc = sw128_desc(base + L::kV);
+            auto wait = [&](int off, int i, int phase) {
+                if (!mbar_wait(bar(off, i), static_cast<uint32_t>(phase & 1), abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
+            auto k_there = [&](int i) {
+                return wait(L::kKFull, 2 * (i % L::kNK), i / L::kNK) && wait(L::kKFull, 2 * (i % L::kNK) + 1, i / L::kNK);
+            };
+            auto issue_s = [&](int i, int r, int buf) {  // scores of tile i for row tile r
+                const uint64_t kd = desc_at(kdesc, (i % L::kNK) * L::kKBuf);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < HD / 32; ++k) {
+                        const int seg = 32 * k / L::kSeg, in = 32 * k % L::kSeg;
+                        umma_f8(tmem + L::col_s(buf), desc_at(qdesc, (2 * r + part) * L::kPart + seg * (128 * L::kSeg) + in),
+                                desc_at(kd, seg * (kKeys * L::kSeg) + in), idesc_s, part > 0 || k > 0 ? 1u : 0u);
+                    }
+                umma_commit(bar(L::kSReady, buf));
+                if (r == RT - 1) umma_commit(bar(L::kKFree, i % L::kNK));
+            };
+            auto issue_o = [&](int i, int r, int buf) {  // O += P . V of tile i, half by half
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int h = 2 * i + hf, vb = h % L::kNV;
+                    if (r == 0 && !wait(L::kVReady, vb, h / L::kNV)) return false;
+                    if (!wait(L::kPReady, 2 * buf + hf, RT == 2 ? i : i >> 1)) return false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ts(tmem + L::col_o(r), tmem + L::col_s(buf) + col_p(4 * hf + k),
+                                desc_at(vdesc, vb * L::kVBuf + k * 32), idesc_o, i > 0 || hf > 0 || k > 0 ? 1u : 0u);
+                    if (r == RT - 1) umma_commit(bar(L::kVFree, vb));
+                }
+                return true;
+            };
+            bool ok = wait(L::kQReady, 0, 0) && k_there(0);
+            if constexpr (RT == 2) {
+                // per row tile: O(i), then S(i+1) into the columns that P(i) was read from
+                if (ok) {
+                    issue_s(0, 0, 0);
+                    issue_s(0, 1, 1);
+                }
+                for (int i = 0; i < ntiles && ok; ++i) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (ok) ok = issue_o(i, r, r);
+                        if (!ok) break;
+                        if (i + 1 < ntiles) {
+                            if (r == 0) ok = k_there(i + 1);
+                            if (ok) issue_s(i + 1, r, r);
+                        } else {
+                            umma_commit(bar(L::kODone, r));
+                        }
+                    }
+                }
+            } else {
+                // S(i+1) into the other buffer, whose P(i-1) has been read by O(i-1) before it, then O(i)
+                if (ok) issue_s(0, 0, 0);
+                for (int i = 0; i < ntiles && ok; ++i) {
+                    if (i + 1 < ntiles) {
+                        ok = k_there(i + 1);
+                        if (ok) issue_s(i + 1, 0, (i + 1) & 1);
+                    }
+                    if (ok) ok = issue_o(i, 0, i & 1);
+                    if (ok) umma_commit(bar(L::kODone, i & 1));
+                }
+            }
+            if (!ok) {
+                flag(a.status, KVFP8_DEV_TIMEOUT);
+                *abort_flag = 1;
+                // let the products already issued finish before tensor memory is released
+                umma_commit(bar(L::kDrain, 0));
+                mbar_wait(bar(L::kDrain, 0), 0, &never);
+            }
+        }
+    } else if (warp >= W::kConv) {
+        // ------------------------------------------------------------ V -> f16, transposed
+        // A unit is 8 keys x 64 dims: one ldmatrix gives a lane four dims of one key in each of four 16-dim pieces; the
+        // pairs of dims are stored transposed.  Lanes of the upper half of a key's dims swap their two pairs first, so that
+        // the eight rows of V^T that a matrix goes to are different modulo 8 (different banks).
+        constexpr int kUnits = 8 * (HD / 64) / kConvWarps;  // of a warp in a half
+        const int cw = warp - W::kConv, t4 = lane & 3;
+        const uint32_t swap = t4 < 2 ? 0x3210u : 0x1032u;
+        // the row of V^T (past 64 dims' first, in the first two pieces) that this lane addresses for a store
+        const int m = lane >> 3, c = lane & 7;
+        const int store_dim = 16 * (m >> 1) + 4 * (c >> 1) + (c & 1) + 2 * ((m & 1) ^ (c >> 2));
+        bool ok = true;
+        for (int h = 0; h < 2 * ntiles && ok; ++h) {
+            const int st = h % L::kNS, vb = h % L::kNV;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFull, st), (h / L::kNS) & 1, abort_flag) &&
+                                             mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
+            if (!ok) break;
+            const uint64_t posted = meta[st];
+            HalfScales sc;
+            sc.load(bp + L::kScales + 32 * st, posted);
+            if (cw == 0 && lane == 0) {
+                if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
+                HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
+                const float mul = a.sm_scale * 1.4426950408889634f;  // log2(e)
+                *reinterpret_cast<float4 *>(info->kmul) = make_float4(sc.k[0] * mul, sc.k[1] * mul, sc.k[2] * mul, sc.k[3] * mul);
+                const uint32_t v = __float_as_uint(sc.vref);
+                *reinterpret_cast<uint4 *>(&info->vlog) =
+                    make_uint4(__float_as_uint(static_cast<float>(static_cast<int>(v >> 23) - 134)), (261u << 23) - v,
+                               static_cast<uint32_t>(sc.keys), static_cast<uint32_t>(sc.keys >> 32));
+            }
+            const bool drop_nan = key_tile(h >> 1) * kKeys + ((h & 1) + 1) * kHalf > all_see;
+            const uint32_t stage = base + L::kStage + st * L::kStageBuf, vt = base + L::kV + vb * L::kVBuf;
+            uint32_t r[kUnits][4];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int unit = cw + kConvWarps * u, ko = unit & 7, d0 = 64 * (unit >> 3);
+                const uint32_t addr = stage + static_cast<uint32_t>(d0 / L::kSeg * (kHalf * L::kSeg)) +
+                                      swz<L::kSeg>(8 * ko + (lane & 7), d0 % L::kSeg / 16 + (lane >> 3));
+                ldsm_x4(addr, r[u][0], r[u][1], r[u][2], r[u][3]);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int unit = cw + kConvWarps * u, ko = unit & 7, d0 = 64 * (unit >> 3);
+                const bool there = (sc.keys >> (8 * ko + (lane >> 2))) & 1ull;
+                const uint32_t mul = ko < 4 ? (ko < 2 ? sc.v[0] : sc.v[1]) : (ko < 6 ? sc.v[2] : sc.v[3]);
+                uint32_t f[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w = there ? __byte_perm(r[u][q], 0u, swap) : 0u;
+                    if (drop_nan) {
+                        const uint32_t nan = nan_byte_mask(w);
+                        if (nan != 0u) *nan_seen = 1;
+                        w &= ~nan;
+                    }
+                    f[2 * q] = mul_f16x2(f16x2_from_e4m3x2(w), mul);
+                    f[2 * q + 1] = mul_f16x2(f16x2_from_e4m3x2_hi(w), mul);
+                }
+                stsm_x4_t(vt + sw128(d0 + store_dim, ko), f[0], f[1], f[2], f[3]);
+                stsm_x4_t(vt + sw128(d0 + 32 + store_dim, ko), f[4], f[5], f[6], f[7]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(L::kVEmpty, st));
+                mbar_arrive(bar(L::kVReady, vb));
+            }
+        }
+        if (!ok && lane == 0) {
+            flag(a.status, KVFP8_DEV_TIMEOUT);
+            *abort_flag = 1;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int rt = RT == 2 ? warp >> 2 : 0;     // row tile
+        const int r = row0 + tid;                   // this thread's row
+        const bool row_ok = r < nb * G;
+        const int jq = row_ok ? r / G : 0, gq = row_ok ? r % G : 0;
+        const int64_t row_at = ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD;
+        const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
+        uint8_t *qp = bp + L::kQ + rt * 2 * L::kPart;
+        const float qdown = split_q_row<HD, L::kSeg>(row_ok ? a.query + row_at : nullptr, qp, qp + L::kPart, tid & 127);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kQReady, 0));
+        const bool idle = row0 + (tid & ~31) >= nb * G;  // a warp of padding rows
+
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        float m_used = -INFINITY;
+        uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
+        bool ok = true;
+        for (int i = 0; i < ntiles && ok; ++i) {
+            const int buf = RT == 2 ? rt : i & 1, turn = RT == 2 ? i : i >> 1;
+            const int v0 = 2 * i % L::kNV, v1 = (2 * i + 1) % L::kNV;
+            const uint32_t scol = lane_addr + L::col_s(buf);
+            // RT 2: with S(rt, i) O(rt, i-1) is done
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
+            if (idle) {  // whatever stands there: no other row takes part in these
+                if (ok && lane == 0) {
+                    mbar_arrive(bar(L::kPReady, 2 * buf));
+                    mbar_arrive(bar(L::kPReady, 2 * buf + 1));
+                }
+                continue;
+            }
+            // the halves' keys and scales (stored with their V^T)
+            if (ok)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVReady, v0), (2 * i / L::kNV) & 1, abort_flag) &&
+                                                 mbar_wait(bar(L::kVReady, v1), ((2 * i + 1) / L::kNV) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            auto info = [&](int hf) { return reinterpret_cast<const HalfInfo *>(bp + L::kInfo) + (hf ? v1 : v0); };
+            // the visible keys among columns 32c..32c+31
+            const int seen = pos - key_tile(i) * kKeys + 1;  // keys of the tile up to the row's position
+            auto visible = [&](int c) {
+                const int n = seen - 32 * c;
+                const uint32_t bits = info(c >> 1)->mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+                return row_ok ? bits : ~0u;  // (a padding row holds no warp back)
+            };
+            const bool whole = __all_sync(0xFFFFFFFFu, (visible(0) & visible(1) & visible(2) & visible(3)) == ~0u);
+            auto hide = [&](uint32_t (&s)[32], int c) {
+                if (!whole) {
+                    const uint32_t bits = visible(c);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((bits >> e) & 1u)) s[e] = 0xFF800000u;  // -infinity
+                }
+            };
+            // what 16 keys' scores are multiplied by (kept away from 0 and infinity, which would make a NaN of a score of
+            // infinity or 0)
+            auto score_mul = [&](int g) {
+                return fminf(fmaxf(info(g >> 2)->kmul[g & 3] * qdown, 0x1p-126f), 0x1p126f);
+            };
+            // pass 1: the row's maximum over the tile; chunks 2 and 3, then 0 and 1, which stay for pass 2
+            uint32_t sa[32], sb[32];
+            float mx = -INFINITY;
+            auto chunk_max = [&](uint32_t (&s)[32], int c) {
+                hide(s, c);
+                const float top = fmaxf(max16(s) * score_mul(2 * c), max16(s + 16) * score_mul(2 * c + 1));
+                mx = fmaxf(mx, top + info(c >> 1)->vlog);
+            };
+            tmem_ld32(scol + 64, sa);
+            tmem_ld32(scol + 96, sb);
+            tmem_wait_ld();
+            chunk_max(sa, 2);
+            chunk_max(sb, 3);
+            tmem_ld32(scol, sa);
+            tmem_ld32(scol + 32, sb);
+            tmem_wait_ld();
+            chunk_max(sa, 0);
+            chunk_max(sb, 1);
+            // the reference moves, and O is rescaled, only when the maximum has risen far above it (first visible keys: O
+            // is still zero for this row, nothing to rescale)
+            float factor = 1.f;
+            if (mx > -INFINITY) {
+                if (m_used == -INFINITY) {
+                    m_used = mx - kHead;
+                } else if (mx > m_used + (kLag + kHead)) {
+                    factor = ex2(m_used - (mx - kHead));
+                    m_used = mx - kHead;
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, factor != 1.f)) {
+                if (RT == 1) {  // (i > 0: the row had a reference)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, (i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                lsum2 = mul_f32x2(lsum2, pk2(factor, factor));
+#pragma unroll 1
+                for (int c0 = 0; c0 < HD; c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(lane_addr + L::col_o(rt) + c0, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                    tmem_st16(lane_addr + L::col_o(rt) + c0, o);
+                }
+            }
+            // pass 2: P = 2^(s + log2 vs - m) as f16 pairs, written over the first half of each chunk's own scores; its
+            // float values are summed
+            const float msub = m_used == -INFINITY ? 0.f : m_used;
+            auto chunk_p = [&](uint32_t (&s)[32], int c) {
+                const float shift = info(c >> 1)->vlog - msub;
+                const uint64_t shift2 = pk2(shift, shift);
+                uint64_t sum2 = pk2(0.f, 0.f);
+                uint32_t p[16];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float mul = score_mul(2 * c + g);
+                    const uint64_t mul2 = pk2(mul, mul);
+#pragma unroll
+                    for (int w = 8 * g; w < 8 * g + 8; ++w) {
+                        const float2 x = upk2(fma_f32x2(pk2u(s[2 * w], s[2 * w + 1]), mul2, shift2));
+                        const float e0 = ex2(x.x), e1 = ex2(x.y);
+                        p[w] = f16x2_from_f32(e0, e1);
+                        sum2 = add_f32x2(sum2, pk2(e0, e1));
+                    }
+                }
+                const float vinv = info(c >> 1)->vinv;
+                lsum2 = fma_f32x2(sum2, pk2(vinv, vinv), lsum2);
+                tmem_st16(scol + 32 * c, p);
+            };
+            auto p_ready = [&](int hf) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kPReady, 2 * buf + hf));
+            };
+            chunk_p(sa, 0);
+            tmem_ld32(scol + 64, sa);  // chunk 2's scores: its columns are not written yet
+            chunk_p(sb, 1);
+            p_ready(0);
+            tmem_ld32(scol + 96, sb);  // chunk 3's
+            tmem_wait_ld();
+            hide(sa, 2);
+            chunk_p(sa, 2);
+            hide(sb, 3);
+            chunk_p(sb, 3);
+            p_ready(1);
+        }
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, RT == 2 ? rt : (ntiles - 1) & 1),
+                                                       RT == 2 ? 0 : ((ntiles - 1) >> 1) & 1, abort_flag));
+        if (ok && !idle) {
+            tc_fence_after();
+            const float2 ls = upk2(lsum2);
+            const float lsum = ls.x + ls.y;
+            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // (a NaN sum makes the row NaN)
+            // this row in the parts' results, when there are several
+            const int64_t prow = kSplit ? ((((static_cast<int64_t>(seq) * a.row_tiles + ctile) * a.n_kv + kvh) * a.splits +
+                                            blockIdx.y) * kRows) + tid : 0;
+            if (kSplit && row_ok) a.part_lse[prow] = lsum == 0.f ? -INFINITY : m_used + __log2f(lsum);
+            // what this row sees of the values that were taken out as NaN: from the first such half on
+            const bool any_nan = *nan_seen != 0;
+            const int key0 = kSplit ? tile_lo * kKeys : 0;
+            const int nan_first = max(key0, max(all_see, 0) / kHalf * kHalf);
+            const int nan_last = row_ok ? min(pos, key0 + ntiles * kKeys - 1) : -1;
+#pragma unroll 1
+            for (int c0 = 0; c0 < HD; c0 += 32) {
+                uint32_t nan = 0;
+                if (any_nan) nan = nan_value_dims<HD>(a, seq, kvh, c0, nan_first, nan_last);
+                uint32_t o[32];
+                tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
+                tmem_wait_ld();
+                if (!row_ok) continue;
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] = (nan >> e) & 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[e]) * inv;
+                if constexpr (kSplit) {
+                    float4 *to = reinterpret_cast<float4 *>(a.part_o + prow * HD + c0);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                } else {
+                    uint4 *to = reinterpret_cast<uint4 *>(a.out + row_at + c0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        to[e] = make_uint4(bf16x2_from_f32(v[8 * e], v[8 * e + 1]), bf16x2_from_f32(v[8 * e + 2], v[8 * e + 3]),
+                                           bf16x2_from_f32(v[8 * e + 4], v[8 * e + 5]), bf16x2_from_f32(v[8 * e + 6], v[8 * e + 7]));
+                }
+            }
+        } else if (!ok && lane == 0) {
+            flag(a.status, KVFP8_DEV_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W::kMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+// Joins the parts of each row: CTA (x, y) takes 256 / (HD / 4) rows of the row tiles x (tile_rows rows).
+template <int HD>
+__global__ void __launch_bounds__(256) join_blocks_kernel(const __grid_constant__ BlockPrefillArgs a, int tile_rows) {
+    constexpr int kLanes = HD / 4;  // threads of a row, four dims each
+    const int kvh = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.n_kv));
+    const int tile = static_cast<int>((blockIdx.x / static_cast<unsigned>(a.n_kv)) % static_cast<unsigned>(a.row_tiles));
+    const int seq = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.n_kv * a.row_tiles));
+    const int lr = static_cast<int>(blockIdx.y) * (256 / kLanes) + static_cast<int>(threadIdx.x) / kLanes;
+    const int d = static_cast<int>(threadIdx.x) % kLanes * 4;
+    pdl_wait();  // the parts are visible from here on
+    const QueryRange qr = a.qsl ? query_range(a.qsl, seq, a.qmax, a.qrows) : QueryRange{seq, 1};
+    const int Ls = min(max(a.seq_lens[seq], 0), a.max_len);
+    const int nb = qr.count, G = a.group, row0 = tile * tile_rows, r = row0 + lr;
+    if (r >= nb * G) return;
+    // the row tiles' parts, as their CTAs worked them out
+    const int j_last = min(nb, (row0 + tile_rows + G - 1) / G) - 1;
+    const int kend = a.causal ? Ls - nb + j_last + 1 : Ls;
+    if (kend <= 0) return;  // zeroed by its CTA
+    const int parts = split_parts(a.splits, (kend + kKeys - 1) / kKeys, kKeys);
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
+    PartMerge mg;
+    for (int c0 = 0; c0 < parts; c0 += 8) {
+        float l[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            l[i] = -INFINITY;
+            if (c0 + i < parts) {
+                const int64_t p = p0 + static_cast<int64_t>(c0 + i) * tile_rows;
+                l[i] = a.part_lse[p];
+                v[i] = *reinterpret_cast<const float4 *>(a.part_o + p * HD + d);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mg.add(l[i], v[i]);
+    }
+    *reinterpret_cast<uint2 *>(a.out + ((static_cast<int64_t>(qr.q0) + r / G) * a.n_q + kvh * G + r % G) * HD + d) =
+        mg.result(1.f);
+}
+
+// How a call is cut: the rows of a CTA, and the parts that fill the SMs.
+struct BlockSplitPlan {
+    int tile_rows = kPfRows, splits = 1;
+    size_t lse_off = 0, total = 0;  // workspace
+};
+BlockSplitPlan block_split_plan(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax, int64_t max_len) {
+    BlockSplitPlan p;
+    const int64_t group_rows = static_cast<int64_t>(qmax) * (n_q / n_kv);
+    if (head_dim <= 128 && group_rows > kPfRows) p.tile_rows = 2 * kPfRows;
+    const int64_t tiles = (group_rows + p.tile_rows - 1) / p.tile_rows;
+    if (tiles > kSplitSms || tiles * n_kv > kSplitSms || tiles * n_kv * num_seqs > kSplitSms / 2) return p;
+    const int64_t ctas = tiles * n_kv * num_seqs;
+    p.splits = static_cast<int>(std::max<int64_t>(1, std::min(kSplitSms / ctas, max_len / kMinPartKeys)));
+    if (p.splits == 1) return p;
+    const size_t part_rows = static_cast<size_t>(ctas) * p.splits * p.tile_rows;
+    p.lse_off = part_rows * head_dim * sizeof(float);
+    p.total = p.lse_off + part_rows * sizeof(float);
+    return p;
+}
+
+template <int HD, int RT>
+cudaError_t run_row_tiles(const DecodeArgs &d, const BlockSplitPlan &sp, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                          BlockPrefillArgs a, cudaStream_t stream) {
+    const size_t smem = PbSmem<HD, RT>::kTotal + 1024;
+    constexpr int kThreads = PbWarps<RT>::kAll * 32;
+    auto kern = sp.splits > 1 ? prefill_blocks_kernel<HD, RT, true> : prefill_blocks_kernel<HD, RT, false>;
+    cudaError_t err;
+    int occ = 0;  // also raises the kernel's shared memory limit, once per device
+    if ((err = kernel_occupancy(kern, kThreads, smem, &occ)) != cudaSuccess) return err;
+    const int group_rows = d.qmax * a.group;  // (prefill_takes: below 2^31 - 511)
+    a.row_tiles = (group_rows + 128 * RT - 1) / (128 * RT);
+    const int64_t ctas = static_cast<int64_t>(d.num_seqs) * a.row_tiles * d.n_kv;
+    kern<<<dim3(static_cast<unsigned>(ctas), sp.splits), kThreads, smem, stream>>>(tmk, tmv, a);
+    if ((err = cudaGetLastError()) != cudaSuccess || sp.splits == 1) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 128 * RT / (256 / (HD / 4)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_blocks_kernel<HD>, a, 128 * RT);
+}
+
+template <int HD>
+cudaError_t run_prefill_blocks(const DecodeArgs &d, cudaStream_t stream) {
+    constexpr int kSeg = HD < 128 ? HD : 128;
+    const int box_rows = std::min(d.block_size, kHalf);
+    const int64_t rows = static_cast<int64_t>(d.num_blocks) * d.block_size;
+    CUtensorMap tmk, tmv;
+    cudaError_t err;
+    if ((err = encode_cache_map(&tmk, d.key_cache, rows, d.n_kv * HD, kSeg, box_rows)) != cudaSuccess ||
+        (err = encode_cache_map(&tmv, d.value_cache, rows, d.n_kv * HD, kSeg, box_rows)) != cudaSuccess)
+        return err;
+    BlockPrefillArgs a = {};
+    a.out = static_cast<__nv_bfloat16 *>(d.out);
+    a.query = static_cast<const __nv_bfloat16 *>(d.query);
+    a.qsl = d.qsl;
+    a.qmax = d.qmax;
+    a.qrows = d.qrows;
+    a.block_tables = d.block_tables;
+    a.max_blocks_per_seq = d.max_blocks_per_seq;
+    a.seq_lens = d.seq_lens;
+    a.num_seqs = d.num_seqs;
+    a.n_q = d.n_q;
+    a.n_kv = d.n_kv;
+    a.group = d.n_q / d.n_kv;
+    a.block_size = d.block_size;
+    a.num_blocks = d.num_blocks;
+    a.max_len = d.max_blocks_per_seq * d.block_size;
+    a.sm_scale = d.sm_scale;
+    a.status = d.status;
+    a.box_rows = box_rows;
+    a.value_cache = d.value_cache;
+    a.key_scales = d.key_block_scales;
+    a.value_scales = d.value_block_scales;
+    a.scale_stride = d.block_scale_stride;
+    a.causal = d.causal != 0;
+    const BlockSplitPlan sp = block_split_plan(d.num_seqs, d.n_q, d.n_kv, HD, d.qmax, a.max_len);
+    a.splits = sp.splits;
+    a.part_o = static_cast<float *>(d.workspace);
+    a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(d.workspace) + sp.lse_off);
+    if constexpr (HD <= 128) {
+        if (sp.tile_rows == 2 * kPfRows) return run_row_tiles<HD, 2>(d, sp, tmk, tmv, a, stream);
+    }
+    return run_row_tiles<HD, 1>(d, sp, tmk, tmv, a, stream);
+}
+
+}  // namespace
+
+size_t block_scaled_prefill_workspace_size(int32_t num_seqs, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t qmax,
+                                           int64_t max_len) {
+    return block_split_plan(num_seqs, n_q, n_kv, head_dim, qmax, max_len).total;
+}
+
+cudaError_t launch_prefill_block_scaled(const DecodeArgs &d, cudaStream_t stream) {
+    if (d.num_seqs == 0) return cudaSuccess;
+    if (!prefill_takes(d.n_q, d.n_kv, d.qmax, d.num_seqs)) return cudaErrorNotSupported;
+    switch (d.head_dim) {
+        case 64: return run_prefill_blocks<64>(d, stream);
+        case 128: return run_prefill_blocks<128>(d, stream);
+        case 256: return run_prefill_blocks<256>(d, stream);
+        default: return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace kvfp8
