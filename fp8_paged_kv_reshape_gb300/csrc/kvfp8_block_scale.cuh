@@ -15,7 +15,7 @@ constexpr int kMinScaleExp = -60, kMaxScaleExp = 120;
 // (0 is a block that nothing was written to)
 __device__ __forceinline__ bool block_scale_ok(float s) {
     const uint32_t bits = __float_as_uint(s);
-    constexpr uint32_t kLow = (kMinScaleExp + 127u) << 23, kHigh = (kMaxScaleExp + 127u) << 23;
+    constexpr uint32_t kLow = static_cast<uint32_t>(kMinScaleExp + 127) << 23, kHigh = static_cast<uint32_t>(kMaxScaleExp + 127) << 23;
     return (bits & 0x7FFFFFu) == 0u && bits - kLow <= kHigh - kLow;
 }
 // 1 / s, exactly

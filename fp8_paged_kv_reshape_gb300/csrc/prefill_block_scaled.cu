@@ -18,8 +18,6 @@
 //    highest s + log2 vs, within fp16's range whatever the scales, and the row's sum adds 64 keys' weights
 //    times 1 / vs.  Weights are held as over the 4-bit cache: m lies 2^7 below the highest at the time, weights reach
 //    2^15, so they keep 11 bits down to 2^-21 of the highest and are above zero down to 2^-32.
-//  * P is handed over in two halves of 64 keys: the product with V starts while the second half's exponentials are
-//    taken.
 //
 // Two row tiles (head_dim 64 and 128, more than 128 rows) share the converted V and take turns on the tensor core;
 // one row tile has two score buffers, the next tile's scores being computed meanwhile.
@@ -73,8 +71,8 @@ struct PbSmem {
     static constexpr int kVFull = kKFree + 8 * kNK, kVEmpty = kVFull + 8 * kNS;
     static constexpr int kVReady = kVEmpty + 8 * kNS, kVFree = kVReady + 8 * kNV;
     static constexpr int kQReady = kVFree + 8 * kNV;
-    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;  // (per score buffer; per half of it)
-    static constexpr int kODone = kPReady + 32, kDrain = kODone + 16;
+    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;
+    static constexpr int kODone = kPReady + 16, kDrain = kODone + 16;
     static constexpr int kMeta = kDrain + 8;                             // valid keys per staged half
     static constexpr int kMisc = kMeta + 8 * kNS;                        // tmem base, abort flag, NaN seen
     static constexpr int kTotal = kMisc + 16;
@@ -241,14 +239,30 @@ __device__ __forceinline__ float split_q_row(const __nv_bfloat16 *q, uint8_t *pa
     return down;
 }
 
+// what a row's scores are multiplied by, of 16 keys and its own (kept away from 0 and infinity, which would make a NaN of
+// a score of infinity or 0)
+__device__ __forceinline__ float score_mul(float kmul, float qdown) { return fminf(fmaxf(kmul * qdown, 0x1p-126f), 0x1p126f); }
+
 // ---------------------------------------------------------------- the kernel
 
 // Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one
-// issuing products (and allocating TMEM), one issuing copies.
+// issuing products (and allocating TMEM), one issuing copies.  Two row tiles: warpgroups trade registers, 128 a thread at the
+// launch, so that the softmax keeps its scores without spills (two warps make up the last group).
 template <int RT>
 struct PbWarps {
-    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + 1, kAll = kTma + 1;
+    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + 1, kAll = RT == 2 ? 16 : kTma + 1;
+    static constexpr int kSoftmaxRegs = 184, kConvRegs = 72, kIssueRegs = 72;
+    static_assert(RT != 2 || 256 * kSoftmaxRegs + 128 * kConvRegs + 128 * kIssueRegs <= 512 * 128, "registers at launch");
 };
+template <int RT, int kRegs>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (RT == 2) {
+        if constexpr (kRegs > 128)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+    }
+}
 
 template <int HD, int RT, bool kSplit>
 __global__ void __launch_bounds__(PbWarps<RT>::kAll * 32, 1)
@@ -330,8 +344,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         mbar_init(bar(L::kQReady, 0), 4 * RT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::kSReady, i), 1);
-            mbar_init(bar(L::kPReady, 2 * i), 4);
-            mbar_init(bar(L::kPReady, 2 * i + 1), 4);
+            mbar_init(bar(L::kPReady, i), 4);
             mbar_init(bar(L::kODone, i), 1);
         }
         mbar_init(bar(L::kDrain, 0), 1);
@@ -353,7 +366,9 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
     const uint32_t tmem = *tmem_slot;
     const volatile int32_t never = 0;
 
-    if (warp == W::kTma) {
+    if (warp >= W::kMma) {
+      take_registers<RT, W::kIssueRegs>();
+      if (warp == W::kTma) {
         // ------------------------------------------------------------ copies
         // half h of the key pass (64 keys of tile h/2): lane p < nbox copies K box p, lane nbox + p V box p
         const int32_t *bt = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
@@ -442,7 +457,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 mbar_wait(bar(L::kKFull, 2 * ((k >> 1) % L::kNK) + (k & 1)), ((k >> 1) / L::kNK) & 1, &never);
             }
         }
-    } else if (warp == W::kMma) {
+      } else if (warp == W::kMma) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
             const uint32_t idesc_s = e4m3_idesc(128, kKeys), idesc_o = f16_idesc(128, HD);
@@ -470,19 +485,19 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 umma_commit(bar(L::kSReady, buf));
                 if (r == RT - 1) umma_commit(bar(L::kKFree, i % L::kNK));
             };
-            auto issue_o = [&](int i, int r, int buf) {  // O += P . V of tile i, half by half
+            auto v_there = [&](int i) {
+                return wait(L::kVReady, 2 * i % L::kNV, 2 * i / L::kNV) && wait(L::kVReady, (2 * i + 1) % L::kNV, (2 * i + 1) / L::kNV);
+            };
+            auto issue_o = [&](int i, int r, int buf) {  // O += P . V of tile i
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int h = 2 * i + hf, vb = h % L::kNV;
-                    if (r == 0 && !wait(L::kVReady, vb, h / L::kNV)) return false;
-                    if (!wait(L::kPReady, 2 * buf + hf, RT == 2 ? i : i >> 1)) return false;
+                    const int vb = (2 * i + hf) % L::kNV;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_ts(tmem + L::col_o(r), tmem + L::col_s(buf) + col_p(4 * hf + k),
                                 desc_at(vdesc, vb * L::kVBuf + k * 32), idesc_o, i > 0 || hf > 0 || k > 0 ? 1u : 0u);
                     if (r == RT - 1) umma_commit(bar(L::kVFree, vb));
                 }
-                return true;
             };
             bool ok = wait(L::kQReady, 0, 0) && k_there(0);
             if constexpr (RT == 2) {
@@ -492,16 +507,17 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     issue_s(0, 1, 1);
                 }
                 for (int i = 0; i < ntiles && ok; ++i) {
+                    // (what P does not have to be waited for first: the row tile's chain is what bounds the kernel)
+                    ok = v_there(i) && (i + 1 == ntiles || k_there(i + 1));
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        if (ok) ok = issue_o(i, r, r);
+                        if (ok) ok = wait(L::kPReady, r, i);
                         if (!ok) break;
-                        if (i + 1 < ntiles) {
-                            if (r == 0) ok = k_there(i + 1);
-                            if (ok) issue_s(i + 1, r, r);
-                        } else {
+                        issue_o(i, r, r);
+                        if (i + 1 < ntiles)
+                            issue_s(i + 1, r, r);
+                        else
                             umma_commit(bar(L::kODone, r));
-                        }
                     }
                 }
             } else {
@@ -512,8 +528,10 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                         ok = k_there(i + 1);
                         if (ok) issue_s(i + 1, 0, (i + 1) & 1);
                     }
-                    if (ok) ok = issue_o(i, 0, i & 1);
-                    if (ok) umma_commit(bar(L::kODone, i & 1));
+                    if (ok) ok = v_there(i) && wait(L::kPReady, i & 1, i >> 1);
+                    if (!ok) break;
+                    issue_o(i, 0, i & 1);
+                    umma_commit(bar(L::kODone, i & 1));
                 }
             }
             if (!ok) {
@@ -524,7 +542,9 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 mbar_wait(bar(L::kDrain, 0), 0, &never);
             }
         }
+      }
     } else if (warp >= W::kConv) {
+        take_registers<RT, W::kConvRegs>();
         // ------------------------------------------------------------ V -> f16, transposed
         // A unit is 8 keys x 64 dims: one ldmatrix gives a lane four dims of one key in each of four 16-dim pieces; the
         // pairs of dims are stored transposed.  Lanes of the upper half of a key's dims swap their two pairs first, so that
@@ -535,15 +555,29 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         // the row of V^T (past 64 dims' first, in the first two pieces) that this lane addresses for a store
         const int m = lane >> 3, c = lane & 7;
         const int store_dim = 16 * (m >> 1) + 4 * (c >> 1) + (c & 1) + 2 * ((m & 1) ^ (c >> 2));
+        constexpr int kBatch = kUnits < 4 ? kUnits : 4;  // units whose codes are loaded together
+        uint32_t r[kBatch][4];
+        auto load = [&](uint32_t stage, int u0) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int un = cw + kConvWarps * (u0 + u), d0 = 64 * (un >> 3);
+                const uint32_t addr = stage + static_cast<uint32_t>(d0 / L::kSeg * (kHalf * L::kSeg)) +
+                                      swz<L::kSeg>(8 * (un & 7) + (lane & 7), d0 % L::kSeg / 16 + (lane >> 3));
+                ldsm_x4(addr, r[u][0], r[u][1], r[u][2], r[u][3]);
+            }
+        };
         bool ok = true;
         for (int h = 0; h < 2 * ntiles && ok; ++h) {
             const int st = h % L::kNS, vb = h % L::kNV;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFull, st), (h / L::kNS) & 1, abort_flag) &&
-                                             mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFull, st), (h / L::kNS) & 1, abort_flag));
             if (!ok) break;
+            const uint32_t stage = base + L::kStage + st * L::kStageBuf, vt = base + L::kV + vb * L::kVBuf;
+            load(stage, 0);
             const uint64_t posted = meta[st];
             HalfScales sc;
             sc.load(bp + L::kScales + 32 * st, posted);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
+            if (!ok) break;
             if (cw == 0 && lane == 0) {
                 if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
                 HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
@@ -554,35 +588,34 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     make_uint4(__float_as_uint(static_cast<float>(static_cast<int>(v >> 23) - 134)), (261u << 23) - v,
                                static_cast<uint32_t>(sc.keys), static_cast<uint32_t>(sc.keys >> 32));
             }
+            static_assert(kConvWarps == 4 && kUnits % 2 == 0, "a warp's units are of key groups cw and cw + 4 in turn");
+            const uint32_t vmul[2] = {cw < 2 ? sc.v[0] : sc.v[1], cw < 2 ? sc.v[2] : sc.v[3]};
             const bool drop_nan = key_tile(h >> 1) * kKeys + ((h & 1) + 1) * kHalf > all_see;
-            const uint32_t stage = base + L::kStage + st * L::kStageBuf, vt = base + L::kV + vb * L::kVBuf;
-            uint32_t r[kUnits][4];
+#pragma unroll 1
+            for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+                if (u0 > 0) load(stage, u0);
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const int unit = cw + kConvWarps * u, ko = unit & 7, d0 = 64 * (unit >> 3);
-                const uint32_t addr = stage + static_cast<uint32_t>(d0 / L::kSeg * (kHalf * L::kSeg)) +
-                                      swz<L::kSeg>(8 * ko + (lane & 7), d0 % L::kSeg / 16 + (lane >> 3));
-                ldsm_x4(addr, r[u][0], r[u][1], r[u][2], r[u][3]);
-            }
+                for (int u = 0; u < kBatch; ++u) {
+                    const int un = cw + kConvWarps * (u0 + u), ko = un & 7, d0 = 64 * (un >> 3);
+                    const bool there = (sc.keys >> (8 * ko + (lane >> 2))) & 1ull;
+                    // (units 4 apart: two groups of 16 keys further)
+                    const uint32_t mul = there ? vmul[u & 1] : 0u, take = there ? swap : 0x4444u;
+                    uint32_t f[8];
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const int unit = cw + kConvWarps * u, ko = unit & 7, d0 = 64 * (unit >> 3);
-                const bool there = (sc.keys >> (8 * ko + (lane >> 2))) & 1ull;
-                const uint32_t mul = ko < 4 ? (ko < 2 ? sc.v[0] : sc.v[1]) : (ko < 6 ? sc.v[2] : sc.v[3]);
-                uint32_t f[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w = there ? __byte_perm(r[u][q], 0u, swap) : 0u;
-                    if (drop_nan) {
-                        const uint32_t nan = nan_byte_mask(w);
-                        if (nan != 0u) *nan_seen = 1;
-                        w &= ~nan;
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w = __byte_perm(r[u][q], 0u, take);
+                        if (drop_nan) {
+                            const uint32_t nan = nan_byte_mask(w);
+                            if (nan != 0u) *nan_seen = 1;
+                            w &= ~nan;
+                        }
+                        f[2 * q] = mul_f16x2(f16x2_from_e4m3x2(w), mul);
+                        f[2 * q + 1] = mul_f16x2(f16x2_from_e4m3x2_hi(w), mul);
                     }
-                    f[2 * q] = mul_f16x2(f16x2_from_e4m3x2(w), mul);
-                    f[2 * q + 1] = mul_f16x2(f16x2_from_e4m3x2_hi(w), mul);
+                    const uint32_t to = vt + sw128(d0 + store_dim, ko);
+                    stsm_x4_t(to, f[0], f[1], f[2], f[3]);
+                    stsm_x4_t(to + 32 * 128, f[4], f[5], f[6], f[7]);
                 }
-                stsm_x4_t(vt + sw128(d0 + store_dim, ko), f[0], f[1], f[2], f[3]);
-                stsm_x4_t(vt + sw128(d0 + 32 + store_dim, ko), f[4], f[5], f[6], f[7]);
             }
             fence_proxy_async();
             __syncwarp();
@@ -597,6 +630,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         }
     } else {
         // ------------------------------------------------------------ softmax
+        take_registers<RT, W::kSoftmaxRegs>();
         const int rt = RT == 2 ? warp >> 2 : 0;     // row tile
         const int r = row0 + tid;                   // this thread's row
         const bool row_ok = r < nb * G;
@@ -618,61 +652,61 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             const int buf = RT == 2 ? rt : i & 1, turn = RT == 2 ? i : i >> 1;
             const int v0 = 2 * i % L::kNV, v1 = (2 * i + 1) % L::kNV;
             const uint32_t scol = lane_addr + L::col_s(buf);
-            // RT 2: with S(rt, i) O(rt, i-1) is done
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
             if (idle) {  // whatever stands there: no other row takes part in these
-                if (ok && lane == 0) {
-                    mbar_arrive(bar(L::kPReady, 2 * buf));
-                    mbar_arrive(bar(L::kPReady, 2 * buf + 1));
-                }
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
+                if (ok && lane == 0) mbar_arrive(bar(L::kPReady, buf));
                 continue;
             }
-            // the halves' keys and scales (stored with their V^T)
-            if (ok)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVReady, v0), (2 * i / L::kNV) & 1, abort_flag) &&
-                                                 mbar_wait(bar(L::kVReady, v1), ((2 * i + 1) / L::kNV) & 1, abort_flag));
+            // the halves' keys and scales (stored with their V^T, which is there before the scores as a rule)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVReady, v0), (2 * i / L::kNV) & 1, abort_flag) &&
+                                             mbar_wait(bar(L::kVReady, v1), ((2 * i + 1) / L::kNV) & 1, abort_flag));
             if (!ok) break;
-            tc_fence_after();
-            auto info = [&](int hf) { return reinterpret_cast<const HalfInfo *>(bp + L::kInfo) + (hf ? v1 : v0); };
+            const HalfInfo *in[2] = {reinterpret_cast<const HalfInfo *>(bp + L::kInfo) + v0,
+                                     reinterpret_cast<const HalfInfo *>(bp + L::kInfo) + v1};
             // the visible keys among columns 32c..32c+31
             const int seen = pos - key_tile(i) * kKeys + 1;  // keys of the tile up to the row's position
             auto visible = [&](int c) {
                 const int n = seen - 32 * c;
-                const uint32_t bits = info(c >> 1)->mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+                const uint32_t bits = in[c >> 1]->mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
                 return row_ok ? bits : ~0u;  // (a padding row holds no warp back)
             };
             const bool whole = __all_sync(0xFFFFFFFFu, (visible(0) & visible(1) & visible(2) & visible(3)) == ~0u);
-            auto hide = [&](uint32_t (&s)[32], int c) {
-                if (!whole) {
+            float mul[8], vlog[2], vinv[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(in[hf]->kmul);
+                const float2 v2 = *reinterpret_cast<const float2 *>(&in[hf]->vlog);
+                mul[4 * hf] = score_mul(k4.x, qdown);
+                mul[4 * hf + 1] = score_mul(k4.y, qdown);
+                mul[4 * hf + 2] = score_mul(k4.z, qdown);
+                mul[4 * hf + 3] = score_mul(k4.w, qdown);
+                vlog[hf] = v2.x;
+                vinv[hf] = v2.y;
+            }
+            // RT 2: with S(rt, i) O(rt, i-1) is done
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];  // the row's scores of the tile, read once
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, s[c]);
+            tmem_wait_ld();
+            if (!whole) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     const uint32_t bits = visible(c);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (!((bits >> e) & 1u)) s[e] = 0xFF800000u;  // -infinity
+                        if (!((bits >> e) & 1u)) s[c][e] = 0xFF800000u;  // -infinity
                 }
-            };
-            // what 16 keys' scores are multiplied by (kept away from 0 and infinity, which would make a NaN of a score of
-            // infinity or 0)
-            auto score_mul = [&](int g) {
-                return fminf(fmaxf(info(g >> 2)->kmul[g & 3] * qdown, 0x1p-126f), 0x1p126f);
-            };
-            // pass 1: the row's maximum over the tile; chunks 2 and 3, then 0 and 1, which stay for pass 2
-            uint32_t sa[32], sb[32];
+            }
             float mx = -INFINITY;
-            auto chunk_max = [&](uint32_t (&s)[32], int c) {
-                hide(s, c);
-                const float top = fmaxf(max16(s) * score_mul(2 * c), max16(s + 16) * score_mul(2 * c + 1));
-                mx = fmaxf(mx, top + info(c >> 1)->vlog);
-            };
-            tmem_ld32(scol + 64, sa);
-            tmem_ld32(scol + 96, sb);
-            tmem_wait_ld();
-            chunk_max(sa, 2);
-            chunk_max(sb, 3);
-            tmem_ld32(scol, sa);
-            tmem_ld32(scol + 32, sb);
-            tmem_wait_ld();
-            chunk_max(sa, 0);
-            chunk_max(sb, 1);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t(&h)[32] = s[2 * hf], (&g)[32] = s[2 * hf + 1];
+                const float *mh = mul + 4 * hf;
+                mx = fmaxf(mx, fmaxf(max3f(max16(h) * mh[0], max16(h + 16) * mh[1], max16(g) * mh[2]), max16(g + 16) * mh[3]) + vlog[hf]);
+            }
             // the reference moves, and O is rescaled, only when the maximum has risen far above it (first visible keys: O
             // is still zero for this row, nothing to rescale)
             float factor = 1.f;
@@ -701,47 +735,29 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     tmem_st16(lane_addr + L::col_o(rt) + c0, o);
                 }
             }
-            // pass 2: P = 2^(s + log2 vs - m) as f16 pairs, written over the first half of each chunk's own scores; its
-            // float values are summed
+            // P = 2^(s + log2 vs - m) as f16 pairs, written over the first half of each 32 scores; its float values are summed
             const float msub = m_used == -INFINITY ? 0.f : m_used;
-            auto chunk_p = [&](uint32_t (&s)[32], int c) {
-                const float shift = info(c >> 1)->vlog - msub;
-                const uint64_t shift2 = pk2(shift, shift);
-                uint64_t sum2 = pk2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float shift = vlog[c >> 1] - msub;
+                const uint64_t shift2 = pk2(shift, shift), vinv2 = pk2(vinv[c >> 1], vinv[c >> 1]);
+                uint64_t sum2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
                 uint32_t p[16];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float mul = score_mul(2 * c + g);
-                    const uint64_t mul2 = pk2(mul, mul);
-#pragma unroll
-                    for (int w = 8 * g; w < 8 * g + 8; ++w) {
-                        const float2 x = upk2(fma_f32x2(pk2u(s[2 * w], s[2 * w + 1]), mul2, shift2));
-                        const float e0 = ex2(x.x), e1 = ex2(x.y);
-                        p[w] = f16x2_from_f32(e0, e1);
-                        sum2 = add_f32x2(sum2, pk2(e0, e1));
-                    }
+                for (int w = 0; w < 16; ++w) {
+                    const uint64_t mul2 = pk2(mul[2 * c + (w >> 3)], mul[2 * c + (w >> 3)]);
+                    const float2 x = upk2(fma_f32x2(pk2u(s[c][2 * w], s[c][2 * w + 1]), mul2, shift2));
+                    const float e0 = ex2(x.x), e1 = ex2(x.y);
+                    p[w] = f16x2_from_f32(e0, e1);
+                    sum2[w & 1] = add_f32x2(sum2[w & 1], pk2(e0, e1));
                 }
-                const float vinv = info(c >> 1)->vinv;
-                lsum2 = fma_f32x2(sum2, pk2(vinv, vinv), lsum2);
+                lsum2 = fma_f32x2(add_f32x2(sum2[0], sum2[1]), vinv2, lsum2);
                 tmem_st16(scol + 32 * c, p);
-            };
-            auto p_ready = [&](int hf) {
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::kPReady, 2 * buf + hf));
-            };
-            chunk_p(sa, 0);
-            tmem_ld32(scol + 64, sa);  // chunk 2's scores: its columns are not written yet
-            chunk_p(sb, 1);
-            p_ready(0);
-            tmem_ld32(scol + 96, sb);  // chunk 3's
-            tmem_wait_ld();
-            hide(sa, 2);
-            chunk_p(sa, 2);
-            hide(sb, 3);
-            chunk_p(sb, 3);
-            p_ready(1);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kPReady, buf));
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, RT == 2 ? rt : (ntiles - 1) & 1),
                                                        RT == 2 ? 0 : ((ntiles - 1) >> 1) & 1, abort_flag));
