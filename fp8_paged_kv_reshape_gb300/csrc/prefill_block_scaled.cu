@@ -71,9 +71,9 @@ struct PbSmem {
     static constexpr int kVFull = kKFree + 8 * kNK, kVEmpty = kVFull + 8 * kNS;
     static constexpr int kVReady = kVEmpty + 8 * kNS, kVFree = kVReady + 8 * kNV;
     static constexpr int kQReady = kVFree + 8 * kNV;
-    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;
+    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;   // (per score buffer)
     static constexpr int kODone = kPReady + 16, kDrain = kODone + 16;
-    static constexpr int kMeta = kDrain + 8;                             // valid keys per staged half
+    static constexpr int kMeta = kDrain + 16;                            // valid keys per staged half
     static constexpr int kMisc = kMeta + 8 * kNS;                        // tmem base, abort flag, NaN seen
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal + 1024 <= 232448, "shared memory");
@@ -122,13 +122,11 @@ __device__ __forceinline__ uint64_t k_desc(uint32_t saddr) {
 
 // ---------------------------------------------------------------- block scales
 
-// The V scales of 64 keys over 2^-7 of the largest of them, as fp16 pairs, and that one; the keys whose block has
-// valid scales (of either side).
+// The scales of 64 keys, taken apart by a whole warp: lane l has those of keys 16(l%4)..+15.
 struct HalfScales {
-    uint64_t keys;
-    float vref;        // 1 without any
-    float k[4];
-    uint32_t v[4];
+    uint64_t keys;  // those whose block has valid scales of both sides
+    float k, vref;  // the lane's K scale (1 without keys); the largest V scale (1 without keys)
+    uint32_t v;     // the lane's V scale over 2^-7 of vref, as an fp16 pair (0 without keys)
 
     __device__ __forceinline__ static uint32_t over(float s, float ref) {
         // 2^(7 - d), d = log2(ref / s): an fp16 number, or one of its denormals, or 0
@@ -136,24 +134,18 @@ struct HalfScales {
         const uint32_t h = e >= 1 ? static_cast<uint32_t>(e) << 10 : e >= -9 ? 1u << (9 + e) : 0u;
         return h * 0x10001u;
     }
-    // (a group without keys has no scales either: what stands there is of another tile)
-    __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask) {
-        const float4 k4 = *reinterpret_cast<const float4 *>(at), v4 = *reinterpret_cast<const float4 *>(at + 16);
-        const float ks[4] = {k4.x, k4.y, k4.z, k4.w}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
-        keys = 0;
-        vref = 0.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint64_t group = mask & (0xFFFFull << (16 * g));
-            k[g] = 1.f;
-            if (group == 0ull || !(block_scale_ok(ks[g]) && block_scale_ok(vs[g]))) continue;
-            keys |= group;
-            k[g] = ks[g];
-            vref = fmaxf(vref, vs[g]);
-        }
+    // at: four K scales, then four V scales (stale where a group has no key in mask)
+    __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask, int lane) {
+        const int g = lane & 3;
+        const float ks = *reinterpret_cast<const float *>(at + 4 * g), vs = *reinterpret_cast<const float *>(at + 16 + 4 * g);
+        const uint64_t group = mask & (0xFFFFull << (16 * g));
+        const bool ok = group != 0ull && block_scale_ok(ks) && block_scale_ok(vs);
+        keys = static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, ok ? static_cast<uint32_t>(group) : 0u)) |
+               static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, ok ? static_cast<uint32_t>(group >> 32) : 0u)) << 32;
+        vref = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, ok ? __float_as_uint(vs) : 0u));
         if (keys == 0ull) vref = 1.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) v[g] = (keys & (0xFFFFull << (16 * g))) != 0ull ? over(vs[g], vref) : 0u;
+        k = ok ? ks : 1.f;
+        v = ok ? over(vs, vref) : 0u;
     }
 };
 
@@ -195,46 +187,51 @@ __device__ __forceinline__ float max16(const uint32_t *s) {
     return fmaxf(max3f(a, b, c), v(15));
 }
 
-// One row of q (HD bf16, or zeros) as two E4M3 parts at part0 and part1 (row `row` of K-major operands); returns what a
-// score is to be multiplied by for it.
+// A warp's 32 rows of q (bf16 at q + the lane's row_at, or zeros where the lane has none) as two E4M3 parts at part0 and
+// part1 (rows row..row+31 of K-major operands).  Returns what a score of the lane's row is to be multiplied by.  HD/8 lanes
+// share a row.  (A lane to a row took 13000 cycles of a CTA's 160000: lines apart, read twice.)
 template <int HD, int SEG>
-__device__ __forceinline__ float split_q_row(const __nv_bfloat16 *q, uint8_t *part0, uint8_t *part1, int row) {
-    uint32_t top = 0;  // the largest magnitude's bits, in either half
-    bool odd = false;
-    if (q != nullptr) {
-#pragma unroll 4
-        for (int c = 0; c < HD / 8; ++c) {
-            const uint4 w = reinterpret_cast<const uint4 *>(q)[c];
-            top = __vmaxu2(__vmaxu2(top, w.x & 0x7FFF7FFFu), __vmaxu2(w.y & 0x7FFF7FFFu, w.z & 0x7FFF7FFFu));
-            top = __vmaxu2(top, w.w & 0x7FFF7FFFu);
-        }
-        top = max(top & 0xFFFFu, top >> 16);
-        odd = top >= 0x7F80u;  // an infinity or NaN: the whole row becomes NaN
-    }
-    // 2^(7 - e) of the largest's exponent e, kept where it and its inverse are floats
-    const int e = min(max(static_cast<int>(top >> 7), 20), 254);
-    const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23), down = __uint_as_float(static_cast<uint32_t>(e - 7) << 23);
-#pragma unroll 2
-    for (int c = 0; c < HD / 16; ++c) {
-        uint32_t w[8] = {};
-        if (q != nullptr) {
-            const uint4 lo = reinterpret_cast<const uint4 *>(q)[2 * c], hi = reinterpret_cast<const uint4 *>(q)[2 * c + 1];
-            w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
-        }
-        uint32_t a[4], b[4];
+__device__ __forceinline__ float split_q_rows(const __nv_bfloat16 *q, int64_t row_at, bool row_ok, uint8_t *part0, uint8_t *part1, int row) {
+    constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes, kBatch = 8;
+    const int lane = static_cast<int>(threadIdx.x & 31), k = lane % kLanes;
+    const uint32_t at = static_cast<uint32_t>((8 * k / SEG) * (128 * SEG) + (k & 1) * 8);
+    float down = 1.f;
+#pragma unroll 1
+    for (int it0 = 0; it0 < kLanes; it0 += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = bf16lo(w[i]) * up, y = bf16hi(w[i]) * up;
-            const uint32_t hi = e4m3x2_from_f32(x, y);
-            const float2 back = __half22float2(h2(f16x2_from_e4m3x2(hi)));
-            const uint32_t rest = e4m3x2_from_f32(x - back.x, y - back.y);
-            a[i / 2] = i & 1 ? a[i / 2] | hi << 16 : hi;
-            b[i / 2] = i & 1 ? b[i / 2] | rest << 16 : rest;
+        for (int b = 0; b < kBatch; ++b) {
+            const int from = (it0 + b) * kAtOnce + lane / kLanes;
+            const int64_t src = __shfl_sync(0xFFFFFFFFu, row_at, from);
+            const bool there = __shfl_sync(0xFFFFFFFFu, row_ok, from);
+            w[b] = there ? reinterpret_cast<const uint4 *>(q + src)[k] : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (odd) a[0] = a[1] = a[2] = a[3] = 0x7F7F7F7Fu;
-        const uint32_t at = static_cast<uint32_t>((16 * c / SEG) * (128 * SEG)) + swz<SEG>(row, 16 * c % SEG / 16);
-        *reinterpret_cast<uint4 *>(part0 + at) = make_uint4(a[0], a[1], a[2], a[3]);
-        *reinterpret_cast<uint4 *>(part1 + at) = make_uint4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+            uint32_t top = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu), __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
+            top = max(top & 0xFFFFu, top >> 16);  // the largest magnitude's bits
+#pragma unroll
+            for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            // 2^(7 - e) of the largest's exponent e, kept where it and its inverse are floats
+            const int e = min(max(static_cast<int>(top >> 7), 20), 254);
+            const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = bf16lo(x[i]) * up, v = bf16hi(x[i]) * up;
+                hi[i] = e4m3x2_from_f32(u, v);
+                const float2 back = __half22float2(h2(f16x2_from_e4m3x2(hi[i])));
+                lo[i] = e4m3x2_from_f32(u - back.x, v - back.y);
+            }
+            uint2 a = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            if (top >= 0x7F80u) a = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // an infinity or NaN: the whole row becomes NaN
+            const uint32_t to = at + swz<SEG>(row + (it0 + b) * kAtOnce + lane / kLanes, 8 * k % SEG / 16);
+            *reinterpret_cast<uint2 *>(part0 + to) = a;
+            *reinterpret_cast<uint2 *>(part1 + to) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            const float d = __shfl_sync(0xFFFFFFFFu, __uint_as_float(static_cast<uint32_t>(e - 7) << 23), lane % kAtOnce * kLanes);
+            if (it0 + b == lane / kAtOnce) down = d;
+        }
     }
     return down;
 }
@@ -245,12 +242,12 @@ __device__ __forceinline__ float score_mul(float kmul, float qdown) { return fmi
 
 // ---------------------------------------------------------------- the kernel
 
-// Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one
-// issuing products (and allocating TMEM), one issuing copies.  Two row tiles: warpgroups trade registers, 128 a thread at the
-// launch, so that the softmax keeps its scores without spills (two warps make up the last group).
+// Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one per
+// row tile issuing products (the first allocates TMEM), one issuing copies.  Two row tiles: warpgroups trade registers, 128 a
+// thread at the launch, so that the softmax keeps its scores (a warp without work makes up the last group).
 template <int RT>
 struct PbWarps {
-    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + 1, kAll = RT == 2 ? 16 : kTma + 1;
+    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + RT, kAll = kMma + (RT == 2 ? 4 : 2);
     static constexpr int kSoftmaxRegs = 184, kConvRegs = 72, kIssueRegs = 72;
     static_assert(RT != 2 || 256 * kSoftmaxRegs + 128 * kConvRegs + 128 * kIssueRegs <= 512 * 128, "registers at launch");
 };
@@ -331,7 +328,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         for (int i = 0; i < L::kNK; ++i) {
             mbar_init(bar(L::kKFull, 2 * i), 1);
             mbar_init(bar(L::kKFull, 2 * i + 1), 1);
-            mbar_init(bar(L::kKFree, i), 1);
+            mbar_init(bar(L::kKFree, i), RT);
         }
         for (int i = 0; i < L::kNS; ++i) {
             mbar_init(bar(L::kVFull, i), 1 + 32);  // the post, and every lane's scale copies
@@ -339,15 +336,15 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         }
         for (int i = 0; i < L::kNV; ++i) {
             mbar_init(bar(L::kVReady, i), kConvWarps);
-            mbar_init(bar(L::kVFree, i), 1);
+            mbar_init(bar(L::kVFree, i), RT);
         }
         mbar_init(bar(L::kQReady, 0), 4 * RT);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::kSReady, i), 1);
             mbar_init(bar(L::kPReady, i), 4);
             mbar_init(bar(L::kODone, i), 1);
+            mbar_init(bar(L::kDrain, i), 1);
         }
-        mbar_init(bar(L::kDrain, 0), 1);
         *abort_flag = 0;
         *nan_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -457,12 +454,13 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 mbar_wait(bar(L::kKFull, 2 * ((k >> 1) % L::kNK) + (k & 1)), ((k >> 1) / L::kNK) & 1, &never);
             }
         }
-      } else if (warp == W::kMma) {
+      } else if (warp < W::kMma + RT) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
+            const int r = warp - W::kMma;  // its row tile
             const uint32_t idesc_s = e4m3_idesc(128, kKeys), idesc_o = f16_idesc(128, HD);
             // operand descriptors computed once; each product adds its constant offset
-            const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ), kdesc = k_desc<L::kSeg>(base + L::kK),
+            const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ + r * 2 * L::kPart), kdesc = k_desc<L::kSeg>(base + L::kK),
                            vdesc = sw128_desc(base + L::kV);
             auto wait = [&](int off, int i, int phase) {
                 if (!mbar_wait(bar(off, i), static_cast<uint32_t>(phase & 1), abort_flag)) return false;
@@ -472,23 +470,23 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             auto k_there = [&](int i) {
                 return wait(L::kKFull, 2 * (i % L::kNK), i / L::kNK) && wait(L::kKFull, 2 * (i % L::kNK) + 1, i / L::kNK);
             };
-            auto issue_s = [&](int i, int r, int buf) {  // scores of tile i for row tile r
+            auto issue_s = [&](int i, int buf) {  // scores of tile i
                 const uint64_t kd = desc_at(kdesc, (i % L::kNK) * L::kKBuf);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < HD / 32; ++k) {
                         const int seg = 32 * k / L::kSeg, in = 32 * k % L::kSeg;
-                        umma_f8(tmem + L::col_s(buf), desc_at(qdesc, (2 * r + part) * L::kPart + seg * (128 * L::kSeg) + in),
+                        umma_f8(tmem + L::col_s(buf), desc_at(qdesc, part * L::kPart + seg * (128 * L::kSeg) + in),
                                 desc_at(kd, seg * (kKeys * L::kSeg) + in), idesc_s, part > 0 || k > 0 ? 1u : 0u);
                     }
                 umma_commit(bar(L::kSReady, buf));
-                if (r == RT - 1) umma_commit(bar(L::kKFree, i % L::kNK));
+                umma_commit(bar(L::kKFree, i % L::kNK));
             };
-            auto v_there = [&](int i) {
-                return wait(L::kVReady, 2 * i % L::kNV, 2 * i / L::kNV) && wait(L::kVReady, (2 * i + 1) % L::kNV, (2 * i + 1) / L::kNV);
-            };
-            auto issue_o = [&](int i, int r, int buf) {  // O += P . V of tile i
+            auto issue_o = [&](int i, int buf) {  // O += P . V of tile i
+                if (!wait(L::kVReady, 2 * i % L::kNV, 2 * i / L::kNV) || !wait(L::kVReady, (2 * i + 1) % L::kNV, (2 * i + 1) / L::kNV) ||
+                    !wait(L::kPReady, buf, RT == 2 ? i : i >> 1))
+                    return false;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int vb = (2 * i + hf) % L::kNV;
@@ -496,51 +494,42 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     for (int k = 0; k < 4; ++k)
                         umma_ts(tmem + L::col_o(r), tmem + L::col_s(buf) + col_p(4 * hf + k),
                                 desc_at(vdesc, vb * L::kVBuf + k * 32), idesc_o, i > 0 || hf > 0 || k > 0 ? 1u : 0u);
-                    if (r == RT - 1) umma_commit(bar(L::kVFree, vb));
+                    umma_commit(bar(L::kVFree, vb));
                 }
+                return true;
             };
             bool ok = wait(L::kQReady, 0, 0) && k_there(0);
             if constexpr (RT == 2) {
-                // per row tile: O(i), then S(i+1) into the columns that P(i) was read from
-                if (ok) {
-                    issue_s(0, 0, 0);
-                    issue_s(0, 1, 1);
-                }
+                // O(i), then S(i+1) into the columns that P(i) was read from.  (One thread for both row tiles: 467 us where
+                // this takes 446, the one's waits holding up the other's products.)
+                if (ok) issue_s(0, r);
                 for (int i = 0; i < ntiles && ok; ++i) {
-                    // (what P does not have to be waited for first: the row tile's chain is what bounds the kernel)
-                    ok = v_there(i) && (i + 1 == ntiles || k_there(i + 1));
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        if (ok) ok = wait(L::kPReady, r, i);
-                        if (!ok) break;
-                        issue_o(i, r, r);
-                        if (i + 1 < ntiles)
-                            issue_s(i + 1, r, r);
-                        else
-                            umma_commit(bar(L::kODone, r));
+                    ok = issue_o(i, r);
+                    if (ok && i + 1 < ntiles) {
+                        ok = k_there(i + 1);
+                        if (ok) issue_s(i + 1, r);
                     }
                 }
+                if (ok) umma_commit(bar(L::kODone, r));
             } else {
                 // S(i+1) into the other buffer, whose P(i-1) has been read by O(i-1) before it, then O(i)
-                if (ok) issue_s(0, 0, 0);
+                if (ok) issue_s(0, 0);
                 for (int i = 0; i < ntiles && ok; ++i) {
                     if (i + 1 < ntiles) {
                         ok = k_there(i + 1);
-                        if (ok) issue_s(i + 1, 0, (i + 1) & 1);
+                        if (ok) issue_s(i + 1, (i + 1) & 1);
                     }
-                    if (ok) ok = v_there(i) && wait(L::kPReady, i & 1, i >> 1);
-                    if (!ok) break;
-                    issue_o(i, 0, i & 1);
-                    umma_commit(bar(L::kODone, i & 1));
+                    if (ok) ok = issue_o(i, i & 1);
+                    if (ok) umma_commit(bar(L::kODone, i & 1));
                 }
             }
             if (!ok) {
                 flag(a.status, KVFP8_DEV_TIMEOUT);
                 *abort_flag = 1;
-                // let the products already issued finish before tensor memory is released
-                umma_commit(bar(L::kDrain, 0));
-                mbar_wait(bar(L::kDrain, 0), 0, &never);
             }
+            // tensor memory is released when the products have finished, whoever gave up
+            umma_commit(bar(L::kDrain, r));
+            mbar_wait(bar(L::kDrain, r), 0, &never);
         }
       }
     } else if (warp >= W::kConv) {
@@ -575,21 +564,23 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             load(stage, 0);
             const uint64_t posted = meta[st];
             HalfScales sc;
-            sc.load(bp + L::kScales + 32 * st, posted);
+            sc.load(bp + L::kScales + 32 * st, posted, lane);
+            // a warp's units are of the 8 keys cw and cw + 4 in turn
+            const uint32_t vmul[2] = {__shfl_sync(0xFFFFFFFFu, sc.v, cw >> 1), __shfl_sync(0xFFFFFFFFu, sc.v, 2 + (cw >> 1))};
+            static_assert(kConvWarps == 4 && kUnits % 2 == 0, "units and vmul");
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
             if (!ok) break;
-            if (cw == 0 && lane == 0) {
-                if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
+            if (cw == 0 && lane < 4) {
                 HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
-                const float mul = a.sm_scale * 1.4426950408889634f;  // log2(e)
-                *reinterpret_cast<float4 *>(info->kmul) = make_float4(sc.k[0] * mul, sc.k[1] * mul, sc.k[2] * mul, sc.k[3] * mul);
-                const uint32_t v = __float_as_uint(sc.vref);
-                *reinterpret_cast<uint4 *>(&info->vlog) =
-                    make_uint4(__float_as_uint(static_cast<float>(static_cast<int>(v >> 23) - 134)), (261u << 23) - v,
-                               static_cast<uint32_t>(sc.keys), static_cast<uint32_t>(sc.keys >> 32));
+                info->kmul[lane] = sc.k * (a.sm_scale * 1.4426950408889634f);  // log2(e)
+                if (lane == 0) {
+                    if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
+                    const uint32_t v = __float_as_uint(sc.vref);
+                    *reinterpret_cast<uint4 *>(&info->vlog) =
+                        make_uint4(__float_as_uint(static_cast<float>(static_cast<int>(v >> 23) - 134)), (261u << 23) - v,
+                                   static_cast<uint32_t>(sc.keys), static_cast<uint32_t>(sc.keys >> 32));
+                }
             }
-            static_assert(kConvWarps == 4 && kUnits % 2 == 0, "a warp's units are of key groups cw and cw + 4 in turn");
-            const uint32_t vmul[2] = {cw < 2 ? sc.v[0] : sc.v[1], cw < 2 ? sc.v[2] : sc.v[3]};
             const bool drop_nan = key_tile(h >> 1) * kKeys + ((h & 1) + 1) * kHalf > all_see;
 #pragma unroll 1
             for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
@@ -598,7 +589,6 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 for (int u = 0; u < kBatch; ++u) {
                     const int un = cw + kConvWarps * (u0 + u), ko = un & 7, d0 = 64 * (un >> 3);
                     const bool there = (sc.keys >> (8 * ko + (lane >> 2))) & 1ull;
-                    // (units 4 apart: two groups of 16 keys further)
                     const uint32_t mul = there ? vmul[u & 1] : 0u, take = there ? swap : 0x4444u;
                     uint32_t f[8];
 #pragma unroll
@@ -638,7 +628,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         const int64_t row_at = ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD;
         const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
         uint8_t *qp = bp + L::kQ + rt * 2 * L::kPart;
-        const float qdown = split_q_row<HD, L::kSeg>(row_ok ? a.query + row_at : nullptr, qp, qp + L::kPart, tid & 127);
+        const float qdown = split_q_rows<HD, L::kSeg>(a.query, row_at, row_ok, qp, qp + L::kPart, tid & 96);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kQReady, 0));
@@ -775,6 +765,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             const int key0 = kSplit ? tile_lo * kKeys : 0;
             const int nan_first = max(key0, max(all_see, 0) / kHalf * kHalf);
             const int nan_last = row_ok ? min(pos, key0 + ntiles * kKeys - 1) : -1;
+            uint8_t *out_at = qp + (tid & 127) * 2 * HD;  // the lane's row
 #pragma unroll 1
             for (int c0 = 0; c0 < HD; c0 += 32) {
                 uint32_t nan = 0;
@@ -782,7 +773,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
-                if (!row_ok) continue;
+                if (kSplit && !row_ok) continue;
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -792,11 +783,24 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 } else {
-                    uint4 *to = reinterpret_cast<uint4 *>(a.out + row_at + c0);
+                    // by way of the row tile's q, which no product reads any more: written a row a lane, read in rows
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        to[e] = make_uint4(bf16x2_from_f32(v[8 * e], v[8 * e + 1]), bf16x2_from_f32(v[8 * e + 2], v[8 * e + 3]),
-                                           bf16x2_from_f32(v[8 * e + 4], v[8 * e + 5]), bf16x2_from_f32(v[8 * e + 6], v[8 * e + 7]));
+                        *reinterpret_cast<uint4 *>(out_at + (((c0 / 8 + e) ^ (lane & 7)) * 16)) =
+                            make_uint4(bf16x2_from_f32(v[8 * e], v[8 * e + 1]), bf16x2_from_f32(v[8 * e + 2], v[8 * e + 3]),
+                                       bf16x2_from_f32(v[8 * e + 4], v[8 * e + 5]), bf16x2_from_f32(v[8 * e + 6], v[8 * e + 7]));
+                }
+            }
+            if constexpr (!kSplit) {
+                constexpr int kLanes = HD / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at once
+                __syncwarp();
+#pragma unroll 4
+                for (int it = 0; it < kLanes; ++it) {
+                    const int from = it * kAtOnce + lane / kLanes, k = lane % kLanes;
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, row_at, from);
+                    const bool there = __shfl_sync(0xFFFFFFFFu, row_ok, from);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(out_at + (from - lane) * 2 * HD + ((k ^ (from & 7)) * 16));
+                    if (there) reinterpret_cast<uint4 *>(a.out + to)[k] = w;
                 }
             }
         } else if (!ok && lane == 0) {
