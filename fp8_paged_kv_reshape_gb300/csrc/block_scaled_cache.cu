@@ -255,9 +255,10 @@ struct Task {
     }
 };
 
+// first: the lane's entry of list (-1 past its end), for a warp on its own
 template <int HD, bool kF32>
 __device__ __forceinline__ void write_task(const BlockWriteArgs &a, TeamTops &tops, int64_t block, const int32_t *list,
-                                           int task, int team, int team_warps, int tw, int lane) {
+                                           int task, int team, int team_warps, int tw, int lane, int first) {
     constexpr int kEsz = kF32 ? 4 : 2;
     constexpr int kLanes = HD / 8;      // lanes of a row
     constexpr int kRows = 32 / kLanes;  // rows of a pass
@@ -284,7 +285,7 @@ __device__ __forceinline__ void write_task(const BlockWriteArgs &a, TeamTops &to
         static_assert(warp_rows<HD, kF32>() <= kMostHeld, "rows");
         __syncwarp();  // (the last task's have been read)
         for (int o0 = 0; o0 < t.bs; o0 += 32) {
-            const int j = o0 + lane < t.bs ? list[o0 + lane] : -1;
+            const int j = o0 == 0 ? first : o0 + lane < t.bs ? list[o0 + lane] : -1;
             const unsigned there = __ballot_sync(0xFFFFFFFFu, j >= 0);
             const int at = count + __popc(there & ((1u << lane) - 1u));
             if (j >= 0 && at < kMostHeld) mine[at] = make_int2(o0 + lane, j);
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) write_rows_kernel(const __grid
         while (team_warps < kWarps && team_warps * kHeld < bs) team_warps *= 2;
     const int teams = kWarps / team_warps, team = warp / team_warps;
     for (int task = static_cast<int>(blockIdx.y) * teams + team; task < 2 * a.n_kv; task += static_cast<int>(gridDim.y) * teams)
-        write_task<HD, kF32>(a, tops, block, list, task, team, team_warps, warp % team_warps, lane);
+        write_task<HD, kF32>(a, tops, block, list, task, team, team_warps, warp % team_warps, lane, lane < bs ? list[lane] : -1);
 }
 
 // ---------------------------------------------------------------- long calls
@@ -455,23 +456,44 @@ __global__ void __launch_bounds__(256) find_blocks_kernel(const __grid_constant_
 }
 
 template <int HD, bool kF32>
-__global__ void __launch_bounds__(32 * kWarps, 4) write_blocks_kernel(const __grid_constant__ BlockWriteArgs a, int team_warps) {
+__global__ void __launch_bounds__(32 * kWarps, 3) write_blocks_kernel(const __grid_constant__ BlockWriteArgs a, int team_warps) {
     __shared__ TeamTops tops;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int tasks = 2 * a.n_kv;
+    const int tasks = 2 * a.n_kv, bs = 1 << a.block_shift;
     const int32_t *blocks = listed_blocks(a);
-    const int64_t num_blocks = a.num_slots >> a.block_shift;
+    const int num_blocks = static_cast<int>(a.num_slots >> a.block_shift);
 #pragma unroll 1
     for (int many = 1; many >= 0; --many) {
         const int w = many ? team_warps : 1;  // warps of a team
-        const int teams = kWarps / w, team = warp / w;
-        const int64_t items = static_cast<int64_t>(listed_counts(a)[many]) * tasks;
+        const int teams = kWarps / w, team = warp / w, count = listed_counts(a)[many];
+        const int step = static_cast<int>(gridDim.x) * teams, start = static_cast<int>(blockIdx.x) * teams + team;
+        // item (block of the list, task); the block's number and its rows are fetched two items and one ahead: each load's
+        // address comes from the one before
+        struct Item {
+            int at, task;
+        };
+        auto next = [&](Item i) {
+            i.at += step / tasks;
+            i.task += step % tasks;
+            if (i.task >= tasks) {
+                i.task -= tasks;
+                ++i.at;
+            }
+            return i;
+        };
+        auto block_of = [&](const Item &i) { return i.at < count ? blocks[many ? num_blocks - 1 - i.at : i.at] : 0; };
+        auto list_of = [&](int block) { return a.row_of + (static_cast<int64_t>(block) << a.block_shift); };
+        auto first_of = [&](const Item &i, int block) { return w == 1 && i.at < count && lane < bs ? list_of(block)[lane] : -1; };
+        Item item = {start / tasks, start % tasks}, item1 = next(item);
+        int block = block_of(item), block1 = block_of(item1), first = first_of(item, block);
 #pragma unroll 1
-        for (int64_t item = static_cast<int64_t>(blockIdx.x) * teams + team; item < items; item += static_cast<int64_t>(gridDim.x) * teams) {
-            const int at = static_cast<int>(item / tasks), task = static_cast<int>(item - static_cast<int64_t>(at) * tasks);
-            const int64_t block = blocks[many ? num_blocks - 1 - at : at];
-            write_task<HD, kF32>(a, tops, block, a.row_of + (block << a.block_shift), task, team, w, warp % w, lane);
+        while (item.at < count) {
+            const Item item2 = next(item1);
+            const int block2 = block_of(item2), first1 = first_of(item1, block1);
+            write_task<HD, kF32>(a, tops, block, list_of(block), item.task, team, w, warp % w, lane, first);
+            item = item1, item1 = item2;
+            block = block1, block1 = block2, first = first1;
         }
     }
 }
