@@ -57,6 +57,63 @@ __host__ __device__ constexpr int bs_max_heads() { return HD == 64 ? 8 : HD == 1
 template <int HD, int NV>
 __host__ __device__ constexpr int bs_ctas_per_sm() { return 2; }
 
+// A chunk in which some column does not see some token: what such tokens could spread through the product with V is taken out
+// of the head's V codes in the stage, which start at `codes`.  (With a body of its own, unrolled like the common one, such a
+// chunk, one per sequence, ran from a cold instruction cache: 10000 cycles where the common one takes 3000, 16 columns.)
+template <int HD>
+struct StagedValues {
+    static constexpr int SEG = HD < 128 ? HD : 128, kPieces = SEG / 16;
+    uint8_t *codes;
+    uint32_t seg_bytes, tile_off;
+    uint32_t mask;  // the tokens that are there
+
+    __device__ __forceinline__ uint8_t *piece(int t, int seg) const { return codes + seg * seg_bytes + (t >> 4) * tile_off; }
+
+    // Tokens that are not there become 0; NaN codes of the others do with zero_nan.  Whether there are any of those.
+    __device__ __noinline__ bool clean(bool zero_nan) const {
+        bool any = false;
+#pragma unroll 1
+        for (int i = static_cast<int>(threadIdx.x & 31); i < kTok * (HD / 16); i += 32) {
+            const int t = i / kPieces % kTok;
+            uint4 *at = reinterpret_cast<uint4 *>(piece(t, i / kPieces / kTok) + (t & 15) * SEG + i % kPieces * 16);
+            const uint4 w = *at;
+            if ((mask >> t) & 1u) {
+                const uint4 n = make_uint4(nan_byte_mask(w.x), nan_byte_mask(w.y), nan_byte_mask(w.z), nan_byte_mask(w.w));
+                if ((n.x | n.y | n.z | n.w) != 0u) {
+                    any = true;
+                    if (zero_nan) *at = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
+                }
+            } else {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the next copy into the stage comes through the async proxy)
+        return __any_sync(0xFFFFFFFFu, any);
+    }
+
+    // Which of the lane's outputs (column v, dim 16 p + 2 gid + r: bit 4 KP v + 2 p + r) see a NaN code; column v sees tokens
+    // up to last[v].
+    template <int NV>
+    __device__ __noinline__ uint64_t nan_outputs(const int (&last)[NV]) const {
+        constexpr int KP = HD / 32;
+        const int gid = static_cast<int>(threadIdx.x & 31) >> 2;
+        uint64_t bits = 0;
+#pragma unroll 1
+        for (int t = 0; t < kTok; ++t) {
+            if (!((mask >> t) & 1u)) continue;
+#pragma unroll 1
+            for (int p = 0; p < 2 * KP; ++p) {
+                const uint8_t *two = piece(t, 16 * p / SEG) + swz<SEG>(t & 15, 16 * p % SEG / 16) + 2 * gid;
+                const uint64_t here = ((two[0] & 0x7F) == 0x7F ? 1u : 0u) | ((two[1] & 0x7F) == 0x7F ? 2u : 0u);
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    if (t <= last[v]) bits |= here << (4 * KP * v + 2 * p);
+            }
+        }
+        return bits;
+    }
+};
+
 template <int HD, int NV, bool kMulti>
 __global__ void __launch_bounds__(32 * (bs_max_heads<HD>() + 1), (bs_ctas_per_sm<HD, NV>()))
 decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -325,16 +382,27 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 if (bad && lane == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
             }
 
-            // kPartial: some column does not see some token of the chunk.  The common chunk has a body
-            // without those tests: one basic block from the weights to the last product.
-            auto chunk = [&](auto partial_tag) {
-                constexpr bool kPartial = decltype(partial_tag)::value;
-                auto sees = [&](int row, int v) {  // row of the chunk
-                    if (((mt.mask >> row) & 1u) == 0u) return false;
-                    if (!kMulti) return true;
-                    const int j = column(v) / a.group;  // its query token; padding columns see nothing
-                    return j < nq && mt.tok0 + row <= first_lim + (f.causal ? j : 0);
-                };
+            // partial: some column does not see some token of the chunk
+            const bool partial = mt.mask != ~0u || (kMulti && mt.tok0 + kTok - 1 > first_lim);
+            auto last_seen = [&](int v) {  // the last token of the chunk that column v sees (padding columns: none)
+                if (!kMulti) return kTok - 1;
+                const int j = column(v) / a.group;  // its query token
+                return j < nq ? first_lim + (f.causal ? j : 0) - mt.tok0 : -1;
+            };
+            if (mt.mask != 0u) {
+                uint64_t poison = 0;  // outputs that become NaN
+                if (partial) {
+                    const StagedValues<HD> values = {base_ptr + stage * stage_bytes + code_bytes + head_codes, seg_bytes, f.tile_off, mt.mask};
+                    if (values.clean(false) && kMulti) {
+                        int last[NV];
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) last[v] = last_seen(v);
+                        poison = values.template nan_outputs<NV>(last);
+                        __syncwarp();  // (every lane has looked)
+                        values.clean(true);
+                    }
+                    __syncwarp();
+                }
 
                 // ---- scores S^T[token][column] = K . q^T, tiles of 16 tokens
                 float sacc[2][NS][4];
@@ -374,14 +442,18 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                 // ---- weights 2^(s + log2 vs - m) per column.  m only has to be near the running maximum less
                 // kHead: it moves when one passes it by more than kLag + kHead, so most chunks take no
                 // maximum over the lanes and rescale nothing.  Tokens a column does not see get -inf.
-                if constexpr (kPartial) {
+                if (partial) {
 #pragma unroll
-                    for (int v = 0; v < NV; ++v)
+                    for (int v = 0; v < NV; ++v) {
+                        const int last = last_seen(v);
 #pragma unroll
                         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (!sees(16 * tt + 8 * h + gid, v)) sacc[tt][v / 2][v % 2 + 2 * h] = -INFINITY;
+                            for (int h = 0; h < 2; ++h) {
+                                const int row = 16 * tt + 8 * h + gid;
+                                if (row > last || !((mt.mask >> row) & 1u)) sacc[tt][v / 2][v % 2 + 2 * h] = -INFINITY;
+                            }
+                    }
                 }
                 auto column_top = [&](int v) {  // this lane's highest of column v
                     const int s = v / 2, c = v % 2;
@@ -452,27 +524,6 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     mma16816(acc, f16x2_from_e4m3x2(x), f16x2_from_e4m3x2_hi(x), f16x2_from_e4m3x2(y),
                              f16x2_from_e4m3x2_hi(y), b0, b1);
                 };
-                // what kPartial does to the codes of a half: tokens that are not there become 0, and NaN codes,
-                // where columns may see different tokens, are taken out and left in nan as codes of 1
-                auto clean = [&](int tt, int h, uint32_t (&r)[4], uint32_t (&nan)[4]) {
-                    const uint32_t two = mt.mask >> (16 * tt + 8 * h + 2 * tig);
-                    const uint32_t there = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r[e] &= there;
-                        const uint32_t bytes = kMulti ? nan_byte_mask(r[e]) : 0u;
-                        nan[e] = bytes & 0x38383838u;  // E4M3 1.0
-                        r[e] &= ~bytes;
-                        any |= bytes;
-                    }
-                    return kMulti && __any_sync(0xFFFFFFFFu, any != 0u);
-                };
-                auto poison = [&](float (&acc)[4], const float (&count)[4]) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (count[i] > 0.f) acc[i] = __uint_as_float(0x7FC00000u);
-                };
 #pragma unroll
                 for (int tt = 0; tt < 2; ++tt) {
 #pragma unroll
@@ -480,26 +531,6 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         uint32_t r[2][4];
                         value_codes(tt, 0, c4, r[0]);
                         value_codes(tt, 1, c4, r[1]);
-                        if constexpr (kPartial) {
-                            uint32_t nan[2][4];
-                            const bool n0 = clean(tt, 0, r[0], nan[0]), n1 = clean(tt, 1, r[1], nan[1]);
-                            if (n0 || n1) {
-#pragma unroll
-                                for (int s = 0; s < NS; ++s) {
-                                    uint32_t seen[2];
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h)
-                                        seen[h] = movm_t((sees(16 * tt + 8 * h + gid, 2 * s) ? 0x3C00u : 0u) |
-                                                         (sees(16 * tt + 8 * h + gid, 2 * s + 1) ? 0x3C000000u : 0u));
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        float count[4] = {0.f, 0.f, 0.f, 0.f};
-                                        product_tokens(nan[0][e], nan[1][e], seen[0], seen[1], count);
-                                        poison(o[s][4 * c4 + e], count);
-                                    }
-                                }
-                            }
-                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -507,11 +538,16 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                                 product_tokens(r[0][e], r[1][e], pw[tt][0][s], pw[tt][1][s], o[s][4 * c4 + e]);
                     }
                 }
-            };
-            if (mt.mask == ~0u && !(kMulti && mt.tok0 + kTok - 1 > first_lim))
-                chunk(std::false_type{});
-            else if (mt.mask != 0u)
-                chunk(std::true_type{});
+                if (poison != 0) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+#pragma unroll
+                        for (int p = 0; p < 2 * KP; ++p)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if ((poison >> (4 * KP * v + 2 * p + r)) & 1u) at(v, p, r) = __uint_as_float(0x7FC00000u);
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + 8 * (S + stage));
             if (++stage == S) {
