@@ -6,8 +6,8 @@
 // (sequence, kv head) and goes over their keys in tiles of 128.  What bounds it is the chain of a row tile's scores,
 // softmax and product with V, so the work beside it is kept small:
 //  * K is not converted.  q is the sum of two E4M3 numbers: with q scaled by a power of two per row, so that its largest
-//    element lies in [128, 256), a = E4M3(q) and b = E4M3(q - a) give a bf16's 8 bits exactly where it is within 2^10 of the
-//    row's largest, and to 2^-18 of that below.  K tiles arrive by TMA as the operand that the product takes
+//    element lies in [128, 256), a = E4M3(q) and b = E4M3(q - a) give a bf16's 8 bits exactly where it is within 2^9 of the
+//    row's largest, and to 2^-17 of that below.  K tiles arrive by TMA as the operand that the product takes
 //    (kind::f8f6f4, twice the rate of f16: two products at half the time), products are exact, sums float.
 //  * V meets fp16 weights, so it is converted to fp16 (exactly) and transposed: ldmatrix gives a lane four
 //    dims of a key, which after the conversion are stored with stmatrix.trans as rows of V^T.

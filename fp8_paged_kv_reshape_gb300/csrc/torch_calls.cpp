@@ -1,5 +1,5 @@
-// The calls of the 4-bit cache, of the cache with block scales, of rotary positions and of pages on torch tensors: argument checks, allocation and the
-// C call, for binding.py.
+// The calls of the 4-bit cache, of the cache with block scales, of rotary positions and of pages on torch
+// tensors: argument checks, allocation and the C call, for binding.py.
 //
 // These run once per layer and step, where a kernel takes a few microseconds, and the checks look at
 // some fifty tensor attributes.  Read from Python each costs 0.06 to 0.15 us, the marshalling of twenty

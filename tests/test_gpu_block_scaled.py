@@ -6,7 +6,7 @@ Bounds of attention, for a row and dim, with A = sum p|v| / sum p and S the larg
   * p * vs enters the product as fp16 (in long chunks with vs the largest of the token's 64 and V's codes times the rest,
     multiples of 2^-24 where 448 max(vs) is 2^15.8), 2^7 at least where it is highest: 2^-11 of each, so 2^-11 A, and
     2^-25 absolute below 2^-14, so 2^-32 of the highest p * vs: L * 2^-32 * max(vs) * 448 covers both, the row's sum
-    being at least its highest p; K scales are within 2^22 of each other here, where its codes times theirs are exact;
+    being at least its highest p;
   * scores are float sums of hd exact products, (hd + 4) * 2^-24 S at most, and in the log2 domain they are
     multiplied, added to log2 vs and to the reference: three roundings of a number of at most 1.45 S + 80 (|log2 vs| <=
     60 here), with exp2's and log2's own 2^-22: a weight moves by at most d = (hd + 8) * 2^-24 (1.45 S + 80) +
@@ -304,7 +304,8 @@ def build(n_q, n_kv, hd, bs, lengths, qlens, seed, spare=3, scale=None):
     return dict(q=q, qsl=qsl, kc=kc, vc=vc, ks=ks, vs=vs, bt=bt, lengths=list(lengths))
 
 
-def check_attention(got, case, causal=True, sm=0.0):
+def check_attention(got, case, causal=True, sm=0.0, more=0.0):
+    """more: by how much scores may be off besides."""
     c = case
     hd, longest = c["q"].shape[2], max(c["lengths"] + [1])
     ref, weight, reach = bso.attention(c["q"].double().numpy(), c["qsl"], c["kc"], c["vc"], c["ks"], c["vs"], c["bt"],
@@ -313,7 +314,7 @@ def check_attention(got, case, causal=True, sm=0.0):
     assert np.array_equal(np.isnan(g), np.isnan(ref))
     fine = ~np.isnan(ref)
     vs = c["vs"][bso.scale_ok(c["vs"])]
-    d = (hd + 8) * 2.0 ** -24 * (1.45 * reach + 80) + 2.0 ** -21
+    d = (hd + 8) * 2.0 ** -24 * (1.45 * reach + 80) + 2.0 ** -21 + more
     bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * d[..., None] + 2 * (longest / 16 + 16) * 2.0 ** -23) * weight \
         + longest * 2.0 ** -32 * vs.max(initial=0.0) * 448 + 1e-37
     over = (np.abs(g - ref) - bound)[fine]
@@ -435,7 +436,7 @@ ROUTES = [(8, 2, 128, 1), (8, 2, 64, 3), (16, 2, 128, 2), (4, 2, 256, 2), (8, 2,
 
 @pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
 def test_scales_of_any_size(n_q, n_kv, hd, qlen):
-    """V scales from 2^-60 to 2^60 side by side, K scales over 2^22 such that scores stay small; and all at one end."""
+    """V scales from 2^-60 to 2^60 side by side, K scales such that scores stay small; and all at one end."""
     lengths, qlens = [300, 77], [qlen, min(qlen, 77)]
 
     def mixed(r, shape):
@@ -547,6 +548,89 @@ def test_attention_repeats_itself_and_replays(qlen):
     g.replay()
     c["q"] = -c["q"]
     check_attention(out, c)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+def test_query_rows_of_any_magnitude(n_q, n_kv, hd, qlen):
+    """Rows of q down to denormals; rows with one element 2^4 to 2^12 times the others, over keys that are 0 there, so that the
+    small elements make the scores; rows with a NaN."""
+    lengths, qlens = [300, 77], [qlen, min(qlen, 77)]
+    c = build(n_q, n_kv, hd, 16, lengths, qlens, 31)
+    r = np.random.default_rng(32)
+    q = c["q"].double().numpy()
+    q *= np.exp2(r.choice([0.0, -3, -20, -110, -130], q.shape[:2]))[..., None]
+    odd = r.random(q.shape[:2]) < 0.3
+    q[odd, 5] = np.abs(q[odd]).max(-1) * np.exp2(r.integers(4, 13, int(odd.sum())))
+    q[0, 1, 7] = math.nan
+    c["q"] = torch.from_numpy(q).bfloat16()
+    c["kc"][..., 5] = 0
+    # In long chunks an element of q is the sum of two E4M3 numbers, the row scaled to a largest of [2^7, 2^8).  The first
+    # leaves 4 bits of a bf16's 8, the last of them 2^-7 of the element's own power of two: the second holds
+    # them from 2^-9 on, so elements from 2^-2, 2^-9 of the largest at least, are exact, and others off by half of
+    # 2^-9, 2^-17 of the largest at most.  Elsewhere q is fp16: off by 2^-25 below 2^-14 at most.  A score is off by the
+    # sum of those times |k|.
+    q = np.abs(np.nan_to_num(c["q"].double().numpy()))
+    top = q.max(-1, keepdims=True)
+    off = np.where(q >= top * 2.0 ** -9, 0.0, 2.0 ** -17 * top) + 2.0 ** -25
+    k = np.abs(bso.decode(c["kc"])) * c["ks"][:, None, :n_kv, None]  # [block, token, head, dim]
+    k = np.repeat(np.nan_to_num(k[c["bt"][c["bt"] >= 0]]).max((0, 1)), n_q // n_kv, 0)
+    check_attention(run(multi, c, qlen), c, more=1.45 / math.sqrt(hd) * (off * k).sum(-1))
+
+
+def test_a_pool_past_32_bits():
+    """Blocks that lie past 4 GB of codes give what the same blocks give at the front of a small pool."""
+    n_kv, hd, bs = 8, 128, 16
+    c = build(16, n_kv, hd, bs, [300, 77], [60, 60], 33)
+    nb = len(c["kc"])
+    at = (1 << 32) // (bs * n_kv * hd) + 5  # the blocks' place in the big pool
+    small = caches(c)
+    big = []
+    for t in small[:4]:
+        p = torch.empty((at + nb,) + t.shape[1:], dtype=t.dtype, device="cuda")
+        p[at:] = t
+        big.append(p)
+    bt = torch.where(small[4] >= 0, small[4] + at, small[4])
+    q, qsl = c["q"].cuda(), dev(c["qsl"])
+    for n in (1, 60):  # a few columns, long chunks
+        st = status()
+        want = kv.paged_attention_multi_block_scaled(q[:2 * n], qsl // 60 * n, n, *small, status=st)
+        got = kv.paged_attention_multi_block_scaled(q[:2 * n], qsl // 60 * n, n, *big[:4], bt, small[5], status=st)
+        assert torch.equal(got, want) and int(st.item()) == 0
+    x = (torch.randn(2000, n_kv, hd, device="cuda") * 30).bfloat16()
+    slots = torch.randperm(nb * bs, device="cuda")
+    for n in (200, min(2000, nb * bs)):  # both ways of finding a block's rows
+        if n > 512:
+            x, slots = x[:n], slots[:n]
+        kv.reshape_and_cache_block_scaled(x[:n], -x[:n], *small[:4], slots[:n])
+        kv.reshape_and_cache_block_scaled(x[:n], -x[:n], *big, slots[:n] + at * bs)
+        for s, b in zip(small[:4], big):
+            assert torch.equal(b[at:], s)
+    assert torch.equal(kv.dequant_block_scaled(big[0], big[2], slots + at * bs), kv.dequant_block_scaled(small[0], small[2], slots))
+
+
+def test_calls_on_two_streams_at_once():
+    """Two streams with workspaces of their own, neither waiting for the other, give what one does."""
+    cases = [build(8, 2, 128, 16, [3000, 260], [qlen, qlen], 34 + qlen) for qlen in (3, 200)]
+    sets = [(c["q"].cuda(), dev(c["qsl"]), c["qsl"][1].item(), caches(c)) for c in cases]
+    rows = [(torch.randn(600, 2, 128, device="cuda") * 3).bfloat16() for _ in sets]
+    slots = torch.arange(600, device="cuda")
+    want = [kv.paged_attention_multi_block_scaled(q, qsl, n, *rest) for q, qsl, n, rest in sets]
+    pools = [[torch.zeros(40, 16, 2, 128, dtype=torch.uint8, device="cuda") for _ in range(2)] +
+             [kv.block_scales(40, 2) for _ in range(2)] for _ in range(4)]
+    for i in range(2):
+        kv.reshape_and_cache_block_scaled(rows[i], rows[i], *pools[i], slots)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    outs = [[], []]
+    for _ in range(5):
+        for i, (q, qsl, n, rest) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                kv.reshape_and_cache_block_scaled(rows[i], rows[i], *pools[2 + i], slots)
+                outs[i].append(kv.paged_attention_multi_block_scaled(q, qsl, n, *rest))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+        assert all(torch.equal(a, b) for a, b in zip(pools[i], pools[2 + i]))
 
 
 # ---------------------------------------------------------------- together
