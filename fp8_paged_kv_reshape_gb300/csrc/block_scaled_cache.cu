@@ -15,7 +15,8 @@
 // bits' order), the scale, the codes.  A scale made here is a power of two, so x / s is an exact
 // multiplication, and when a later call raises it the block's older codes are multiplied by a power of two and lose
 // nothing but what leaves the bottom of E4M3's range.
-// HBM-bound: rows are read once (those past a team's registers again, from L2).
+// HBM-bound: rows are read once (those past a team's registers again, from L2).  Measured, 32768 rows of 8 heads of 128
+// bf16, K and V: mark 2.7 us, find 4.8, write 40 (5 TB/s), a side read back 16 (6.2 TB/s); 256 rows 2.9 in one launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(256) find_blocks_kernel(const __grid_constant_
     }
 }
 
+// (Three CTAs an SM: 88 us for 32768 rows and their read-back, 103 with four, whose 64 registers spill, 90 with two.)
 template <int HD, bool kF32>
 __global__ void __launch_bounds__(32 * kWarps, 3) write_blocks_kernel(const __grid_constant__ BlockWriteArgs a, int team_warps) {
     __shared__ TeamTops tops;

@@ -12,7 +12,10 @@
 //    fp16's range by what they add to the output, whatever the scales; the row's sum adds w_t / vs in
 //    float, one fused multiply-add per tile and column.
 //  * A code is an fp16 number: conversion is one cvt per two codes, and 8 warps of an SM have ~3000 cycles
-//    for 32 tokens each at the HBM rate, of which they issue ~700.  HBM bounds it.
+//    for 32 tokens each at the HBM rate, of which they issue ~700.  HBM bounds it:
+//    64 sequences of 4096 tokens, 32 / 8 heads of 128, 92 us (5.9 TB/s, 86 % of a copy's rate), 8 of 131072 at 8 columns 237
+//    (95 %).  At 16 columns the chain of a chunk does (3000 cycles for two warps a scheduler): four new tokens of 32
+//    sequences of 4096, 54 us.  (Two warps a head with half the columns each: 58, both convert all codes.)
 //  * V (A operand, dims x tokens): ldmatrix.trans gives two tokens' codes of two dims, a byte permute makes
 //    them pairs of tokens.  (The 4-bit kernel's product over (token, dim parity) needs no permute, but its zeros
 //    would spread a NaN code to the dim beside it.)  Up to 4 score columns stand at the even columns of
