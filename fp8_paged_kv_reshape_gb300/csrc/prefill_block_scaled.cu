@@ -61,6 +61,10 @@ struct BlockPrefillArgs : PrefillCommon {
 template <int HD, int RT>
 struct PbSmem {
     static constexpr int kSeg = HD < 128 ? HD : 128, kSegs = HD / kSeg;  // bytes of a TMA box row; of a key's head
+    // Score buffers, taken in turns by the jobs (key tile i, row tile r), number RT * i + r.  One more than row tiles where
+    // tensor memory has room: scores are ahead of the softmax then.
+    static constexpr int kBufs = RT == 2 && HD == 128 ? 2 : RT + 1;
+    static constexpr bool kAhead = kBufs > RT;
     static constexpr int kNK = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // K tiles
     static constexpr int kNV = HD == 256 ? 2 : 4;                        // V^T halves
     static constexpr int kNS = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // staged V halves
@@ -78,17 +82,17 @@ struct PbSmem {
     static constexpr int kVFull = kKFree + 8 * kNK, kVEmpty = kVFull + 8 * kNS;
     static constexpr int kVReady = kVEmpty + 8 * kNS, kVFree = kVReady + 8 * kNV;
     static constexpr int kQReady = kVFree + 8 * kNV;
-    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 16;   // (per score buffer)
-    static constexpr int kODone = kPReady + 16, kDrain = kODone + 16;
+    static constexpr int kSReady = kQReady + 8, kPReady = kSReady + 8 * kBufs;  // (per score buffer)
+    static constexpr int kODone = kPReady + 8 * kBufs, kDrain = kODone + 32;  // (O of odd and even tiles: two may be under way)
     static constexpr int kMeta = kDrain + 16;                            // valid keys per staged half
     static constexpr int kMisc = kMeta + 8 * kNS;                        // tmem base, abort flag, NaN seen
     static constexpr int kTotal = kMisc + 16;
     static_assert(kTotal + 1024 <= 232448, "shared memory");
-    // tensor memory: two score buffers of 128 columns (a row tile's, or in turns), then O of each row tile
+    // tensor memory: score buffers of 128 columns, then O of each row tile
     static constexpr uint32_t kTmemCols = 512;
     __host__ __device__ static constexpr uint32_t col_s(int b) { return static_cast<uint32_t>(128 * b); }
-    __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(256 + HD * r); }
-    static_assert(256 + RT * HD <= 512, "tensor memory");
+    __host__ __device__ static constexpr uint32_t col_o(int r) { return static_cast<uint32_t>(128 * kBufs + HD * r); }
+    static_assert(128 * kBufs + RT * HD <= 512, "tensor memory");
 };
 
 // What the softmax takes of 64 keys: scores (over the row's q scale) times kmul[16 keys] are in the log2 domain, weights
@@ -252,9 +256,10 @@ __device__ __forceinline__ float score_mul(float kmul, float qdown) { return fmi
 // Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one per
 // row tile issuing products (the first allocates TMEM), one issuing copies.  Two row tiles: warpgroups trade registers, 128 a
 // thread at the launch, so that the softmax keeps its scores (a warp without work makes up the last group).
-template <int RT>
+template <int HD, int RT>
 struct PbWarps {
-    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + RT, kAll = kMma + (RT == 2 ? 4 : 2);
+    static constexpr int kIssue = PbSmem<HD, RT>::kAhead ? 1 : RT;  // threads that issue products
+    static constexpr int kConv = 4 * RT, kMma = kConv + kConvWarps, kTma = kMma + kIssue, kAll = kMma + (RT == 2 ? 4 : 2);
     static constexpr int kSoftmaxRegs = 184, kConvRegs = 72, kIssueRegs = 72;
     static_assert(RT != 2 || 256 * kSoftmaxRegs + 128 * kConvRegs + 128 * kIssueRegs <= 512 * 128, "registers at launch");
 };
@@ -269,11 +274,11 @@ __device__ __forceinline__ void take_registers() {
 }
 
 template <int HD, int RT, bool kSplit>
-__global__ void __launch_bounds__(PbWarps<RT>::kAll * 32, 1)
+__global__ void __launch_bounds__(PbWarps<HD, RT>::kAll * 32, 1)
 prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ BlockPrefillArgs a) {
     using L = PbSmem<HD, RT>;
-    using W = PbWarps<RT>;
+    using W = PbWarps<HD, RT>;
     constexpr int kRows = 128 * RT;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -335,7 +340,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         for (int i = 0; i < L::kNK; ++i) {
             mbar_init(bar(L::kKFull, 2 * i), 1);
             mbar_init(bar(L::kKFull, 2 * i + 1), 1);
-            mbar_init(bar(L::kKFree, i), RT);
+            mbar_init(bar(L::kKFree, i), W::kIssue);
         }
         for (int i = 0; i < L::kNS; ++i) {
             mbar_init(bar(L::kVFull, i), 1 + 32);  // the post, and every lane's scale copies
@@ -343,13 +348,16 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         }
         for (int i = 0; i < L::kNV; ++i) {
             mbar_init(bar(L::kVReady, i), kConvWarps);
-            mbar_init(bar(L::kVFree, i), RT);
+            mbar_init(bar(L::kVFree, i), W::kIssue);
         }
         mbar_init(bar(L::kQReady, 0), 4 * RT);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::kBufs; ++i) {
             mbar_init(bar(L::kSReady, i), 1);
             mbar_init(bar(L::kPReady, i), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::kODone, i), 1);
+            mbar_init(bar(L::kODone, 2 + i), 1);
             mbar_init(bar(L::kDrain, i), 1);
         }
         *abort_flag = 0;
@@ -461,13 +469,13 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 mbar_wait(bar(L::kKFull, 2 * ((k >> 1) % L::kNK) + (k & 1)), ((k >> 1) / L::kNK) & 1, &never);
             }
         }
-      } else if (warp < W::kMma + RT) {
+      } else if (warp < W::kMma + W::kIssue) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
-            const int r = warp - W::kMma;  // its row tile
+            const int own = warp - W::kMma;  // its row tile (kAhead: both)
             const uint32_t idesc_s = e4m3_idesc(128, kKeys), idesc_o = f16_idesc(128, HD);
             // operand descriptors computed once; each product adds its constant offset
-            const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ + r * 2 * L::kPart), kdesc = k_desc<L::kSeg>(base + L::kK),
+            const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ), kdesc = k_desc<L::kSeg>(base + L::kK),
                            vdesc = sw128_desc(base + L::kV);
             auto wait = [&](int off, int i, int phase) {
                 if (!mbar_wait(bar(off, i), static_cast<uint32_t>(phase & 1), abort_flag)) return false;
@@ -477,23 +485,23 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             auto k_there = [&](int i) {
                 return wait(L::kKFull, 2 * (i % L::kNK), i / L::kNK) && wait(L::kKFull, 2 * (i % L::kNK) + 1, i / L::kNK);
             };
-            auto issue_s = [&](int i, int buf) {  // scores of tile i
+            auto issue_s = [&](int i, int r, int buf) {  // scores of tile i for row tile r
                 const uint64_t kd = desc_at(kdesc, (i % L::kNK) * L::kKBuf);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < HD / 32; ++k) {
                         const int seg = 32 * k / L::kSeg, in = 32 * k % L::kSeg;
-                        umma_f8(tmem + L::col_s(buf), desc_at(qdesc, part * L::kPart + seg * (128 * L::kSeg) + in),
+                        umma_f8(tmem + L::col_s(buf), desc_at(qdesc, (2 * r + part) * L::kPart + seg * (128 * L::kSeg) + in),
                                 desc_at(kd, seg * (kKeys * L::kSeg) + in), idesc_s, part > 0 || k > 0 ? 1u : 0u);
                     }
                 umma_commit(bar(L::kSReady, buf));
-                umma_commit(bar(L::kKFree, i % L::kNK));
+                if (!L::kAhead || r == RT - 1) umma_commit(bar(L::kKFree, i % L::kNK));
             };
-            auto issue_o = [&](int i, int buf) {  // O += P . V of tile i
-                if (!wait(L::kVReady, 2 * i % L::kNV, 2 * i / L::kNV) || !wait(L::kVReady, (2 * i + 1) % L::kNV, (2 * i + 1) / L::kNV) ||
-                    !wait(L::kPReady, buf, RT == 2 ? i : i >> 1))
-                    return false;
+            auto v_there = [&](int i) {
+                return wait(L::kVReady, 2 * i % L::kNV, 2 * i / L::kNV) && wait(L::kVReady, (2 * i + 1) % L::kNV, (2 * i + 1) / L::kNV);
+            };
+            auto issue_o = [&](int i, int r, int buf) {  // O += P . V of tile i
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const int vb = (2 * i + hf) % L::kNV;
@@ -501,33 +509,39 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     for (int k = 0; k < 4; ++k)
                         umma_ts(tmem + L::col_o(r), tmem + L::col_s(buf) + col_p(4 * hf + k),
                                 desc_at(vdesc, vb * L::kVBuf + k * 32), idesc_o, i > 0 || hf > 0 || k > 0 ? 1u : 0u);
-                    umma_commit(bar(L::kVFree, vb));
+                    if (!L::kAhead || r == RT - 1) umma_commit(bar(L::kVFree, vb));
                 }
-                return true;
+                umma_commit(bar(L::kODone, 2 * r + (i & 1)));
             };
-            bool ok = wait(L::kQReady, 0, 0) && k_there(0);
-            if constexpr (RT == 2) {
+            bool ok = wait(L::kQReady, 0, 0);
+            if constexpr (L::kAhead) {
+                // job n: O, then the scores of job n + kBufs into the buffer that P was read from
+                const int jobs = RT * ntiles;
+                auto scores = [&](int n) {
+                    if (n % RT == 0 && !k_there(n / RT)) return false;
+                    issue_s(n / RT, n % RT, n % L::kBufs);
+                    return true;
+                };
+                for (int n = 0; n < min(L::kBufs, jobs) && ok; ++n) ok = scores(n);
+                for (int n = 0; n < jobs && ok; ++n) {
+                    ok = (n % RT != 0 || v_there(n / RT)) && wait(L::kPReady, n % L::kBufs, n / L::kBufs);
+                    if (!ok) break;
+                    issue_o(n / RT, n % RT, n % L::kBufs);
+                    if (n + L::kBufs < jobs) ok = scores(n + L::kBufs);
+                }
+            } else {
                 // O(i), then S(i+1) into the columns that P(i) was read from.  (One thread for both row tiles: 467 us where
                 // this takes 446, the one's waits holding up the other's products.)
-                if (ok) issue_s(0, r);
+                ok = ok && k_there(0);
+                if (ok) issue_s(0, own, own);
                 for (int i = 0; i < ntiles && ok; ++i) {
-                    ok = issue_o(i, r);
-                    if (ok && i + 1 < ntiles) {
-                        ok = k_there(i + 1);
-                        if (ok) issue_s(i + 1, r);
-                    }
-                }
-                if (ok) umma_commit(bar(L::kODone, r));
-            } else {
-                // S(i+1) into the other buffer, whose P(i-1) has been read by O(i-1) before it, then O(i)
-                if (ok) issue_s(0, 0);
-                for (int i = 0; i < ntiles && ok; ++i) {
+                    ok = v_there(i) && wait(L::kPReady, own, i);
+                    if (!ok) break;
+                    issue_o(i, own, own);
                     if (i + 1 < ntiles) {
                         ok = k_there(i + 1);
-                        if (ok) issue_s(i + 1, (i + 1) & 1);
+                        if (ok) issue_s(i + 1, own, own);
                     }
-                    if (ok) ok = issue_o(i, i & 1);
-                    if (ok) umma_commit(bar(L::kODone, i & 1));
                 }
             }
             if (!ok) {
@@ -535,8 +549,8 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 *abort_flag = 1;
             }
             // tensor memory is released when the products have finished, whoever gave up
-            umma_commit(bar(L::kDrain, r));
-            mbar_wait(bar(L::kDrain, r), 0, &never);
+            umma_commit(bar(L::kDrain, own));
+            mbar_wait(bar(L::kDrain, own), 0, &never);
         }
       }
     } else if (warp >= W::kConv) {
@@ -646,7 +660,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
         bool ok = true;
         for (int i = 0; i < ntiles && ok; ++i) {
-            const int buf = RT == 2 ? rt : i & 1, turn = RT == 2 ? i : i >> 1;
+            const int job = RT * i + rt, buf = job % L::kBufs, turn = job / L::kBufs;
             const int v0 = 2 * i % L::kNV, v1 = (2 * i + 1) % L::kNV;
             const uint32_t scol = lane_addr + L::col_s(buf);
             if (idle) {  // whatever stands there: no other row takes part in these
@@ -680,7 +694,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 vlog[hf] = v2.x;
                 vinv[hf] = v2.y;
             }
-            // RT 2: with S(rt, i) O(rt, i-1) is done
+            // (not kAhead: with S(rt, i) O(rt, i-1) is done)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
@@ -716,8 +730,8 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 }
             }
             if (__any_sync(0xFFFFFFFFu, factor != 1.f)) {
-                if (RT == 1) {  // (i > 0: the row had a reference)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, (i - 1) & 1), ((i - 1) >> 1) & 1, abort_flag));
+                if (L::kAhead) {  // (i > 0: the row had a reference)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, 2 * rt + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -756,8 +770,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kPReady, buf));
         }
-        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, RT == 2 ? rt : (ntiles - 1) & 1),
-                                                       RT == 2 ? 0 : ((ntiles - 1) >> 1) & 1, abort_flag));
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, 2 * rt + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1, abort_flag));
         if (ok && !idle) {
             tc_fence_after();
             const float2 ls = upk2(lsum2);
@@ -887,7 +900,7 @@ template <int HD, int RT>
 cudaError_t run_row_tiles(const DecodeArgs &d, const BlockSplitPlan &sp, const CUtensorMap &tmk, const CUtensorMap &tmv,
                           BlockPrefillArgs a, cudaStream_t stream) {
     const size_t smem = PbSmem<HD, RT>::kTotal + 1024;
-    constexpr int kThreads = PbWarps<RT>::kAll * 32;
+    constexpr int kThreads = PbWarps<HD, RT>::kAll * 32;
     auto kern = sp.splits > 1 ? prefill_blocks_kernel<HD, RT, true> : prefill_blocks_kernel<HD, RT, false>;
     cudaError_t err;
     int occ = 0;  // also raises the kernel's shared memory limit, once per device
