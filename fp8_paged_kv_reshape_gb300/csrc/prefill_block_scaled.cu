@@ -26,8 +26,8 @@
 // Measured: that case 452 us (776 TFLOP/s, the tensor pipe 38 % busy), 225 queries on 1500 states in 24 sequences, 16 heads
 // of 64, 87 us.  A 128-key tile of two row tiles takes 4600 cycles: 2300 of products, 2400 of softmax.
 //
-// Two row tiles (head_dim 64 and 128, more than 128 rows) share the converted V and take turns on the tensor core;
-// one row tile has two score buffers, the next tile's scores being computed meanwhile.
+// Two row tiles (head_dim 64 and 128, more than 128 rows) share K tiles and the converted V.  Where tensor memory has room for a
+// score buffer more than row tiles (all but head_dim 128 with two), the next scores are computed meanwhile.
 //
 // NaN: a NaN code in K makes the key's scores NaN, which the masks keep from rows that do not see it.  One
 // in V may reach all rows where all of them see the key.  Where not (the last tiles of a causal call), such codes are
