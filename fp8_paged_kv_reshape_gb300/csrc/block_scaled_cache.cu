@@ -15,8 +15,9 @@
 // bits' order), the scale, the codes.  A scale made here is a power of two, so x / s is an exact
 // multiplication, and when a later call raises it the block's older codes are multiplied by a power of two and lose
 // nothing but what leaves the bottom of E4M3's range.
-// HBM-bound: rows are read once (but the last part of those past a team's registers again, from L2).  Measured, 32768 rows of 8 heads of 128
-// bf16, K and V: mark 2.7 us, find 4.8, write 40 (5 TB/s), a side read back 16 (6.2 TB/s); 256 rows 2.9 in one launch.
+// HBM-bound: rows are read once (those past a team's registers, but for the last part, again from L2).  Measured, 32768
+// rows of 8 heads of 128 bf16, K and V: in blocks of 16 43 us for all three launches, of 256 68; a side read back 16
+// (6.2 TB/s).  256 rows 8 us in one launch, behind one another.
 #include <cuda_runtime.h>
 
 #include <algorithm>

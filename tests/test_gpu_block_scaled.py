@@ -153,6 +153,24 @@ def test_write_corner_values(dtype):
         Pool(1, 16, 1, 64).write(y, -y, np.array([0, 5, 6]))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n, hd, bs, every", [(1300, 128, 256, 1), (1300, 64, 128, 3), (600, 256, 64, 1), (700, 128, 256, 14), (403, 128, 64, 1),
+                                              (23, 256, 256, 1)])
+def test_corner_values_among_many_rows(dtype, n, hd, bs, every):
+    """Blocks with more rows than a warp holds, whole and with gaps, some of them with infinities, NaN or nothing but zeros; a
+    block's last rows in a second call, under scales that they keep or raise."""
+    r = np.random.default_rng(n + bs)
+    x = rows(r, n, 2, hd, dtype, spread=5.0)
+    x[:, :n // 3][torch.from_numpy(r.random((2, n // 3, 2, hd)) < 0.002).cuda()] = math.nan
+    x[:, n // 4:n // 2][torch.from_numpy(r.random((2, n // 2 - n // 4, 2, hd)) < 0.002).cuda()] = -math.inf
+    x[:, -n // 4:] = 0.0
+    at = np.arange(n, dtype=np.int64) * every
+    pool = Pool(-(-n * every // bs) + 1, bs, 2, hd)
+    pool.write(x[0], x[1], r.permutation(n).astype(np.int64) * every)
+    late = at % bs != 0
+    pool.write(x[1][torch.from_numpy(late).cuda()].contiguous() * 2, x[0][torch.from_numpy(late).cuda()].contiguous() / 4, at[late])
+
+
 def test_every_scale_boundary():
     """Block maxima around 448 times every power of two, under either type, and one binade of bf16 values whole."""
     tops = np.array([448.0 * 2.0 ** e * f for e in range(-75, 118, 3) for f in (1 - 2.0 ** -24, 1, 1 + 2.0 ** -23, 1.5)])
