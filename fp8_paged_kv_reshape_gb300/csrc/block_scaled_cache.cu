@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(32 * kWarps, kMany ? 2 : 3) write_blocks_kerne
     const int tasks = 2 * a.n_kv, bs = 1 << a.block_shift;
     const int32_t *blocks = listed_blocks(a);
     const int num_blocks = static_cast<int>(a.num_slots >> a.block_shift), count = listed_counts(a)[kMany];
-    int w = 1;  // warps of a team: as many as hold the rows of such a block, on average at most
+    int w = kMany ? 2 : 1;  // warps of a team: as many as hold the rows of such a block, on average at most
     if (kMany)
         while (w < team_warps && static_cast<int64_t>(w) * warp_rows<HD, kF32>() * count < a.num_tokens) w *= 2;
     const int teams = kWarps / w, team = warp / w;
