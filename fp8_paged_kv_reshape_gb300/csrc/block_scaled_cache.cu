@@ -10,11 +10,11 @@
 //    was there before.  find_blocks_kernel lets the row of a block's lowest offset check the block's
 //    entries of row_of (-1 for those that do not count) and list the block; persistent grids of write_blocks_kernel
 //    take the listed blocks.
-// The unit of work is a (block, side, kv head), by one warp, or by a team of warps where the block has more rows of the call
-// than a warp's registers hold (and part by part, what the team's do not): rows into registers, their maximum (of the integer bits: a positive float's order is its
-// bits' order), the scale, the codes.  A scale made here is a power of two, so x / s is an exact
-// multiplication, and when a later call raises it the block's older codes are multiplied by a power of two and lose
-// nothing but what leaves the bottom of E4M3's range.
+// The unit of work is a (block, side, kv head), by one warp, or by a team of warps where the block has more rows of the
+// call than a warp's registers hold (and part by part, what the team's do not): rows into registers, their maximum
+// (of the integer bits: a positive float's order is its bits' order), the scale, the codes.  A scale made here is a
+// power of two, so x / s is an exact multiplication, and when a later call raises it the block's older codes are
+// multiplied by a power of two and lose nothing but what leaves the bottom of E4M3's range.
 // HBM-bound: rows are read once (those past a team's registers, but for the last part, again from L2).  Measured, 32768
 // rows of 8 heads of 128 bf16, K and V: in blocks of 16 43 us for all three launches, of 256 68; a side read back 16
 // (6.2 TB/s).  256 rows 8 us in one launch, behind one another.
@@ -641,7 +641,8 @@ cudaError_t run_write(const BlockWriteArgs &a, cudaStream_t stream) {
     auto launch = [&](auto kern) {
         int occ = 0;
         if ((err = kernel_occupancy(kern, 32 * kWarps, 0, &occ)) != cudaSuccess) return err;
-        cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((warps + kWarps - 1) / kWarps, static_cast<int64_t>(f.sms) * std::max(occ, 1))));
+        const int64_t ctas = std::min<int64_t>((warps + kWarps - 1) / kWarps, static_cast<int64_t>(f.sms) * std::max(occ, 1));
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
         return cudaLaunchKernelEx(&cfg, kern, a, team_warps);
     };
     if ((err = launch(write_blocks_kernel<HD, kF32, false>)) != cudaSuccess || team_warps == 1) return err;
