@@ -12,12 +12,11 @@
 //  * V meets fp16 weights, so it is converted to fp16 (exactly) and transposed: ldmatrix gives a lane four
 //    dims of a key, which after the conversion are stored with stmatrix.trans as rows of V^T.
 //  * ks multiplies the scores, 16 keys at a time (a block is 16 keys at least), in the multiplication that takes them
-//    to the log2 domain.  vs: V's codes are multiplied by their scale over 2^-7 of the largest of their 64 keys (a
-//    power of two: exact while scales there are within 2^22 of each other, else to 2^-40 of the largest value that scale
-//    holds), and that one goes into the exponent: the weights that meet V are 2^(s + log2 vs - m) with m near the
-//    highest s + log2 vs, within fp16's range whatever the scales, and the row's sum adds 64 keys' weights
-//    times 1 / vs.  Weights are held as over the 4-bit cache: m lies 2^7 below the highest at the time, weights reach
-//    2^15, so they keep 11 bits down to 2^-21 of the highest and are above zero down to 2^-32.
+//    to the log2 domain.  vs goes into the exponent there: the weights that meet V's codes are 2^(s + log2 vs - m) with
+//    m near the highest s + log2 vs that the row sees, within fp16's range whatever the scales, and the row's sum adds 16 keys'
+//    weights times 1 / vs.  m lies 2^7 below the highest at the time, weights reach 2^15, so they keep 11 bits down to 2^-21 of
+//    the highest and are above zero down to 2^-32.  (V's codes times their scale over the largest of 64 keys', and that one in
+//    the exponent, lost what lies far below a scale that the row may not even see.)
 //  * A row's 128 scores of a tile are read from tensor memory once and stay in its thread's registers from the maximum to
 //    the weights, which takes 184 of them: warpgroups trade registers.  (Read twice, with 128 registers, 512 new
 //    tokens of 16 sequences of 4096 took 612 us where this took 485; one pass half by half, whose sums tell when the reference
@@ -75,7 +74,7 @@ struct PbSmem {
     static constexpr int kVBuf = HD * 128, kV = kK + kNK * kKBuf;        // [HD dims][64 keys] f16
     static constexpr int kStageBuf = kHalf * HD, kStage = kV + kNV * kVBuf;  // [segment][64 keys][kSeg]
     static constexpr int kInfo = kStage + kNS * kStageBuf;               // HalfInfo per V^T half
-    static constexpr int kScales = kInfo + 48 * kNV;                     // [side][16 keys] per staged half
+    static constexpr int kScales = kInfo + 80 * kNV;                     // [side][16 keys] per staged half
     static constexpr int kBars = kScales + 32 * kNS;
     // mbarriers
     static constexpr int kKFull = kBars, kKFree = kKFull + 16 * kNK;     // (a K tile's halves; a K tile)
@@ -95,15 +94,13 @@ struct PbSmem {
     static_assert(128 * kBufs + RT * HD <= 512, "tensor memory");
 };
 
-// What the softmax takes of 64 keys: scores (over the row's q scale) times kmul[16 keys] are in the log2 domain, weights
-// carry vlog, their sum vinv; the keys that are there.
+// What the softmax takes of 64 keys, 16 at a time: scores (over the row's q scale) times kmul are in the log2 domain, weights
+// carry vlog, their sum vinv (twice: the sum is two floats); the keys that are there.
 struct HalfInfo {
-    float kmul[4];
-    float vlog, vinv;
-    uint32_t mask[2];
-    uint32_t pad[4];
+    float4 kmul, vlog, vinv[2];
+    uint32_t mask[2], pad[2];
 };
-static_assert(sizeof(HalfInfo) == 48, "layout");
+static_assert(sizeof(HalfInfo) == 80, "layout");
 
 // P of keys 16k..16k+15 (f16 pairs, 8 columns): the first half of the 32 columns that held the scores of keys
 // 32(k/2)..+31, so each 32-key chunk's P overwrites only its own scores
@@ -136,15 +133,8 @@ __device__ __forceinline__ uint64_t k_desc(uint32_t saddr) {
 // The scales of 64 keys, taken apart by a whole warp: lane l has those of keys 16(l%4)..+15.
 struct HalfScales {
     uint64_t keys;  // those whose block has valid scales of both sides
-    float k, vref;  // the lane's K scale (1 without keys); the largest V scale (1 without keys)
-    uint32_t v;     // the lane's V scale over 2^-7 of vref, as an fp16 pair (0 without keys)
+    float k, v;     // the lane's (1 without keys)
 
-    __device__ __forceinline__ static uint32_t over(float s, float ref) {
-        // 2^(7 - d), d = log2(ref / s): an fp16 number, or one of its denormals, or 0
-        const int e = static_cast<int>(__float_as_uint(s) >> 23) - static_cast<int>(__float_as_uint(ref) >> 23) + 22;
-        const uint32_t h = e >= 1 ? static_cast<uint32_t>(e) << 10 : e >= -9 ? 1u << (9 + e) : 0u;
-        return h * 0x10001u;
-    }
     // at: four K scales, then four V scales (stale where a group has no key in mask)
     __device__ __forceinline__ void load(const uint8_t *at, uint64_t mask, int lane) {
         const int g = lane & 3;
@@ -153,10 +143,8 @@ struct HalfScales {
         const bool ok = group != 0ull && block_scale_ok(ks) && block_scale_ok(vs);
         keys = static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, ok ? static_cast<uint32_t>(group) : 0u)) |
                static_cast<uint64_t>(__reduce_or_sync(0xFFFFFFFFu, ok ? static_cast<uint32_t>(group >> 32) : 0u)) << 32;
-        vref = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, ok ? __float_as_uint(vs) : 0u));
-        if (keys == 0ull) vref = 1.f;
         k = ok ? ks : 1.f;
-        v = ok ? over(vs, vref) : 0u;
+        v = ok ? vs : 1.f;
     }
 };
 
@@ -586,20 +574,18 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             const uint64_t posted = meta[st];
             HalfScales sc;
             sc.load(bp + L::kScales + 32 * st, posted, lane);
-            // a warp's units are of the 8 keys cw and cw + 4 in turn
-            const uint32_t vmul[2] = {__shfl_sync(0xFFFFFFFFu, sc.v, cw >> 1), __shfl_sync(0xFFFFFFFFu, sc.v, 2 + (cw >> 1))};
-            static_assert(kConvWarps == 4 && kUnits % 2 == 0, "units and vmul");
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
             if (!ok) break;
             if (cw == 0 && lane < 4) {
                 HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
-                info->kmul[lane] = sc.k * (a.sm_scale * 1.4426950408889634f);  // log2(e)
+                reinterpret_cast<float *>(&info->kmul)[lane] = sc.k * (a.sm_scale * 1.4426950408889634f);  // log2(e)
+                reinterpret_cast<float *>(&info->vlog)[lane] = static_cast<float>(static_cast<int>(__float_as_uint(sc.v) >> 23) - 127);
+                const float inv = block_scale_inverse(sc.v);
+                reinterpret_cast<float2 *>(info->vinv)[lane] = make_float2(inv, inv);
                 if (lane == 0) {
                     if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
-                    const uint32_t v = __float_as_uint(sc.vref);
-                    *reinterpret_cast<uint4 *>(&info->vlog) =
-                        make_uint4(__float_as_uint(static_cast<float>(static_cast<int>(v >> 23) - 134)), (261u << 23) - v,
-                                   static_cast<uint32_t>(sc.keys), static_cast<uint32_t>(sc.keys >> 32));
+                    info->mask[0] = static_cast<uint32_t>(sc.keys);
+                    info->mask[1] = static_cast<uint32_t>(sc.keys >> 32);
                 }
             }
             const bool drop_nan = key_tile(h >> 1) * kKeys + ((h & 1) + 1) * kHalf > all_see;
@@ -610,7 +596,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 for (int u = 0; u < kBatch; ++u) {
                     const int un = cw + kConvWarps * (u0 + u), ko = un & 7, d0 = 64 * (un >> 3);
                     const bool there = (sc.keys >> (8 * ko + (lane >> 2))) & 1ull;
-                    const uint32_t mul = there ? vmul[u & 1] : 0u, take = there ? swap : 0x4444u;
+                    const uint32_t take = there ? swap : 0x4444u;
                     uint32_t f[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -620,8 +606,8 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                             if (nan != 0u) *nan_seen = 1;
                             w &= ~nan;
                         }
-                        f[2 * q] = mul_f16x2(f16x2_from_e4m3x2(w), mul);
-                        f[2 * q + 1] = mul_f16x2(f16x2_from_e4m3x2_hi(w), mul);
+                        f[2 * q] = f16x2_from_e4m3x2(w);
+                        f[2 * q + 1] = f16x2_from_e4m3x2_hi(w);
                     }
                     const uint32_t to = vt + sw128(d0 + store_dim, ko);
                     stsm_x4_t(to, f[0], f[1], f[2], f[3]);
@@ -682,17 +668,18 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 return row_ok ? bits : ~0u;  // (a padding row holds no warp back)
             };
             const bool whole = __all_sync(0xFFFFFFFFu, (visible(0) & visible(1) & visible(2) & visible(3)) == ~0u);
-            float mul[8], vlog[2], vinv[2];
+            float mul[8], vlog[8];  // of 16 keys each
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(in[hf]->kmul);
-                const float2 v2 = *reinterpret_cast<const float2 *>(&in[hf]->vlog);
+                const float4 k4 = in[hf]->kmul, v4 = in[hf]->vlog;
                 mul[4 * hf] = score_mul(k4.x, qdown);
                 mul[4 * hf + 1] = score_mul(k4.y, qdown);
                 mul[4 * hf + 2] = score_mul(k4.z, qdown);
                 mul[4 * hf + 3] = score_mul(k4.w, qdown);
-                vlog[hf] = v2.x;
-                vinv[hf] = v2.y;
+                vlog[4 * hf] = v4.x;
+                vlog[4 * hf + 1] = v4.y;
+                vlog[4 * hf + 2] = v4.z;
+                vlog[4 * hf + 3] = v4.w;
             }
             // (not kAhead: with S(rt, i) O(rt, i-1) is done)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
@@ -713,11 +700,8 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             }
             float mx = -INFINITY;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t(&h)[32] = s[2 * hf], (&g)[32] = s[2 * hf + 1];
-                const float *mh = mul + 4 * hf;
-                mx = fmaxf(mx, fmaxf(max3f(max16(h) * mh[0], max16(h + 16) * mh[1], max16(g) * mh[2]), max16(g + 16) * mh[3]) + vlog[hf]);
-            }
+            for (int c = 0; c < 4; ++c)
+                mx = max3f(mx, fmaf(max16(s[c]), mul[2 * c], vlog[2 * c]), fmaf(max16(s[c] + 16), mul[2 * c + 1], vlog[2 * c + 1]));
             // the reference moves, and O is rescaled, only when the maximum has risen far above it (first visible keys: O
             // is still zero for this row, nothing to rescale)
             float factor = 1.f;
@@ -750,19 +734,24 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             const float msub = m_used == -INFINITY ? 0.f : m_used;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float shift = vlog[c >> 1] - msub;
-                const uint64_t shift2 = pk2(shift, shift), vinv2 = pk2(vinv[c >> 1], vinv[c >> 1]);
-                uint64_t sum2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+                const float4 inv = in[c >> 1]->vinv[c & 1];
                 uint32_t p[16];
+                uint64_t sum2[2];
 #pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    const uint64_t mul2 = pk2(mul[2 * c + (w >> 3)], mul[2 * c + (w >> 3)]);
-                    const float2 x = upk2(fma_f32x2(pk2u(s[c][2 * w], s[c][2 * w + 1]), mul2, shift2));
-                    const float e0 = ex2(x.x), e1 = ex2(x.y);
-                    p[w] = f16x2_from_f32(e0, e1);
-                    sum2[w & 1] = add_f32x2(sum2[w & 1], pk2(e0, e1));
+                for (int g = 0; g < 2; ++g) {
+                    const float shift = vlog[2 * c + g] - msub;
+                    const uint64_t shift2 = pk2(shift, shift), mul2 = pk2(mul[2 * c + g], mul[2 * c + g]);
+                    sum2[g] = pk2(0.f, 0.f);
+#pragma unroll
+                    for (int w = 8 * g; w < 8 * g + 8; ++w) {
+                        const float2 x = upk2(fma_f32x2(pk2u(s[c][2 * w], s[c][2 * w + 1]), mul2, shift2));
+                        const float e0 = ex2(x.x), e1 = ex2(x.y);
+                        p[w] = f16x2_from_f32(e0, e1);
+                        sum2[g] = add_f32x2(sum2[g], pk2(e0, e1));
+                    }
                 }
-                lsum2 = fma_f32x2(add_f32x2(sum2[0], sum2[1]), vinv2, lsum2);
+                lsum2 = fma_f32x2(sum2[0], pk2(inv.x, inv.y), lsum2);
+                lsum2 = fma_f32x2(sum2[1], pk2(inv.z, inv.w), lsum2);
                 tmem_st16(scol + 32 * c, p);
             }
             tmem_wait_st();

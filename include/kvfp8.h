@@ -563,9 +563,8 @@ KVFP8_API size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_s
  * in long query chunks and wide groups, exactly where it is within 2^9 of its row's largest element and to 2^-17
  * of that one below; a row with an infinity or NaN becomes NaN then.  Scores, the exponential, the sum of the weights and the
  * accumulation are float.  softmax(s)_t * vs_t enters the product with V as fp16, 2^7 to 2^15 at a row's
- * highest: 11 bits down to 2^-21 of the highest, multiples of 2^-24 below, none below 2^-32.
- * (Long query chunks and wide groups take V's codes of 64 tokens times their scales over the largest of those
- * scales: exact while they are within 2^22 of each other, else to 2^-40 of the largest value that scale holds.)
+ * highest (of the tokens that it sees): 11 bits down to 2^-21 of the highest, multiples of 2^-24 below, none
+ * below 2^-32.
  *
  * A block whose scales are not valid (of either side) holds no tokens for that head and sets
  * KVFP8_DEV_BAD_SCALE.  A token's NaN reaches exactly the outputs that see the token (all of a row for

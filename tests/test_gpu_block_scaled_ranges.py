@@ -1,0 +1,115 @@
+"""Attention over the FP8 cache with block scales where scales and scores lie far apart, against the oracle.
+
+Bounds are those of test_gpu_block_scaled.py, but for what a small weight may be off by: the weights softmax * vs that meet V are
+fp16 with a row's highest at 2^7 at least, so one below 2^-14 is off by 2^-25, 2^-32 of the highest, and a V code is 448 at most.
+With H the highest softmax * vs among the tokens that the row sees: L * 2^-32 * H * 448.  |log2 vs| is up to 120 here, and the reference
+that scores are taken against up to 15 from the highest: scores in the log2 domain are numbers of at most 1.45 S + 150.  A term of the
+row's sum is a float, 2^-149 at least, and the highest one 2^(7 - 120): L * 2^-36 of the sum.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_scaled as bso
+from tests.test_gpu_block_scaled import ROUTES, build, multi, run
+
+pytestmark = pytest.mark.gpu
+
+kv = pytest.importorskip("fp8_paged_kv_reshape_gb300")
+
+
+def highest(c, causal):
+    """[rows, n_q]: the highest softmax * vs of the tokens that a row sees (0: none)."""
+    n_q, hd = c["q"].shape[1:]
+    bs, n_kv = c["kc"].shape[1:3]
+    group, q, out = n_q // n_kv, c["q"].double().numpy(), np.zeros(c["q"].shape[:2])
+    for i, length in enumerate(c["lengths"]):
+        r0, n = int(c["qsl"][i]), int(c["qsl"][i + 1] - c["qsl"][i])
+        t = np.arange(length)
+        blk = c["bt"][i, t // bs]
+        for h in range(n_kv):
+            k = bso.decode(c["kc"][blk, t % bs, h]) * c["ks"][blk, h, None].astype(np.float64)
+            for j in range(n):
+                sees = length - n + j + 1 if causal else length
+                if sees < 1:
+                    continue
+                x = q[r0 + j, h * group:(h + 1) * group] @ k[:sees].T / np.sqrt(hd)
+                p = np.exp(x - x.max(-1, keepdims=True))
+                out[r0 + j, h * group:(h + 1) * group] = (p / p.sum(-1, keepdims=True) * c["vs"][blk[:sees], h]).max(-1)
+    return out
+
+
+def check(got, c, causal=True, more=0.0):
+    """more: by how much scores may be off besides."""
+    hd, longest = c["q"].shape[2], max(c["lengths"])
+    ref, weight, reach = bso.attention(c["q"].double().numpy(), c["qsl"], c["kc"], c["vc"], c["ks"], c["vs"], c["bt"], c["lengths"],
+                                       causal)
+    g = got.double().cpu().numpy()
+    d = (hd + 8) * 2.0 ** -24 * (1.45 * reach + 150) + 2.0 ** -21 + more
+    d = d + longest * 2.0 ** -36
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * d[..., None] + 2 * (longest / 16 + 16) * 2.0 ** -23) * weight \
+        + (longest * 2.0 ** -32 * 448 * highest(c, causal))[..., None] + 1e-37
+    over = np.abs(g - ref) - bound
+    assert np.isfinite(g).all() and over.max() <= 0, (over.max(), np.abs(g - ref).max())
+
+
+def no_large_codes(c):
+    """V codes of 128 at most, so that values under a scale of 2^120 are floats."""
+    c["vc"] = np.where((c["vc"] & 0x7F) > 0x70, (c["vc"] & 0x80) | 0x70, c["vc"]).astype(np.uint8)
+    return c
+
+
+LENGTHS = [[300, 77], [3000, 260, 16]]
+ORDERS = {"small first": lambda i, n: i >= n // 2, "large first": lambda i, n: i < n // 2, "in turn": lambda i, n: i % 2 == 0,
+          "large last": lambda i, n: i == n - 1, "large alone": lambda i, n: i == n // 3, "small alone": lambda i, n: i != n // 3}
+
+
+def two_scales(order, lengths, small, large):
+    """For build(): each sequence's blocks at one of two scales."""
+    def scale(r, shape):
+        n = [-(-x // 16) for x in lengths]
+        return np.concatenate([np.where(ORDERS[order](np.arange(m), m), large, small) for m in n])[:, None] * np.ones(shape)
+    return scale
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+@pytest.mark.parametrize("order", ORDERS)
+def test_small_and_large_scales_share_a_row(order, n_q, n_kv, hd, qlen):
+    """V scales 60 octaves apart; causal rows that see the small ones alone have those to give back."""
+    lengths = LENGTHS[0]
+    c = build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 41, scale=two_scales(order, lengths, 2.0 ** -40, 2.0 ** 20))
+    c["ks"][c["ks"] > 0] = 2.0 ** -8
+    for causal in (True, False):
+        check(run(multi, c, qlen, causal=causal), c, causal)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+@pytest.mark.parametrize("small, octaves", [(2.0 ** -30, 30), (2.0 ** -60, 40), (2.0 ** -60, 55)])
+def test_small_scales_hold_the_highest_scores(small, octaves, n_q, n_kv, hd, qlen):
+    """A block of a small V scale takes nearly all of the softmax, the others, `octaves` lower in score, nearly all of the output."""
+    lengths = [128, 60]
+    c = build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 44, scale=two_scales("small alone", lengths, 1.0, small))
+    c["q"] = torch.ones_like(c["q"])
+    for i in (0, 1):
+        n = -(-lengths[i] // 16)
+        c["kc"][c["bt"][i, :n]] = 0x00
+        c["kc"][c["bt"][i, n // 3]] = 0x38  # 1.0
+    # a score of hd / sqrt(hd) * ks nats against 0: ks the power of two below, and q what is left
+    nats = octaves * np.log(2) / np.sqrt(hd)
+    ks = 2.0 ** np.floor(np.log2(nats))
+    c["ks"][c["ks"] > 0] = ks
+    c["q"] = (c["q"] * (nats / ks)).bfloat16()
+    for causal in (True, False):
+        check(run(multi, c, qlen, causal=causal), c, causal)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+@pytest.mark.parametrize("low, high", [(-60, 1), (-30, 31)])
+def test_scales_and_scores_far_apart(low, high, n_q, n_kv, hd, qlen):
+    """Scales at random, with scores that lie up to a hundred octaves apart."""
+    for lengths, seed in ((LENGTHS[0], 42), (LENGTHS[1], 43)):
+        c = no_large_codes(build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], seed,
+                                 scale=lambda r, shape: np.exp2(r.integers(low, high, shape))))
+        live = c["ks"] > 0
+        c["ks"][live] = np.exp2(np.random.default_rng(seed).integers(-7, 1, int(live.sum())))
+        check(run(multi, c, qlen), c)
