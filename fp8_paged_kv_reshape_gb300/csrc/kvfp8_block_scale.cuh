@@ -21,6 +21,13 @@ __device__ __forceinline__ bool block_scale_ok(float s) {
 // 1 / s, exactly
 __device__ __forceinline__ float block_scale_inverse(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+// V scales ride in the exponent of the attention's weights, 2^(s + log2 vs - m) with m 2^7 below a row's highest, and the row's sum adds
+// them times 1 / vs.  A weight below 2^-126 is 0 in that sum, where 2^(s - m) should be added: under 2^(-126 - log2 vs), while the
+// highest one adds 2^(7 - log2 of its vs) at least.  And when m rises by more than 126, what was summed before (under 2^(15 - log2 vs) a token)
+// is multiplied by 0.  While the V scales met so far are within 2^kSumSpan of each other, that loses under 2^-54 of the sum for each
+// token; from there on the sum takes 2^(s - m) itself, and its factors in two halves.
+constexpr int kSumSpan = 64;
+
 __device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 
 }  // namespace kvfp8

@@ -10,7 +10,7 @@
 //    its barrier with the codes.  ks multiplies the tile's scores.  vs goes into the exponent: the
 //    weights that meet V are w_t = 2^(s_t + log2 vs - m), m near the highest s_t + log2 vs, so they fill
 //    fp16's range by what they add to the output, whatever the scales; the row's sum adds w_t / vs in
-//    float, one fused multiply-add per tile and column.
+//    float, one fused multiply-add per tile and column (and 2^(s_t - m) itself where scales are too far apart for that, kSumSpan).
 //  * A code is an fp16 number: conversion is one cvt per two codes, and 8 warps of an SM have ~3000 cycles
 //    for 32 tokens each at the HBM rate, of which they issue ~700.  HBM bounds it:
 //    64 sequences of 4096 tokens, 32 / 8 heads of 128, 92 us (5.9 TB/s, 86 % of a copy's rate), 8 of 131072 at 8 columns 237
@@ -296,6 +296,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
         // per column: the reference (log2 domain, of s + log2 vs) the weights are taken against, and this
         // lane's part of the sum of weights / vs
         float m[NV], l[NV];
+        float vtop = 0.f, vlow = 0.f;  // log2 of the largest and the smallest V scale so far
         uint32_t qb[2 * KP][NS][2];
         // multi-query form: the sequence's first query row, its query tokens, and the last cache position
         // that the first of them may see; one further each when causal
@@ -353,6 +354,8 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     m[v] = -INFINITY;
                     l[v] = 0.f;
                 }
+                vtop = -INFINITY;
+                vlow = INFINITY;
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -372,8 +375,9 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(at_box));
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(at_box + 64));
                     const uint32_t tile = 0xFFFFu << (16 * tt);
-                    if (!(block_scale_ok(ks) && block_scale_ok(vs))) {
-                        bad |= (mt.mask & tile) != 0u;
+                    const bool there = (mt.mask & tile) != 0u;
+                    if (!(block_scale_ok(ks) && block_scale_ok(vs) && there)) {
+                        bad |= there;
                         mt.mask &= ~tile;
                         ks = vs = 1.f;
                     }
@@ -382,6 +386,8 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     vlog[tt] = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
                     vinv[tt] = block_scale_inverse(vs);
                 }
+                vtop = fmaxf(vtop, fmaxf(vlog[0], vlog[1]));
+                vlow = fminf(vlow, fminf(vlog[0], vlog[1]));
                 if (bad && lane == 0) flag(a.status, KVFP8_DEV_BAD_SCALE);
             }
 
@@ -463,7 +469,8 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                     return fmaxf(fmaf(fmaxf(sacc[0][s][c], sacc[0][s][c + 2]), kmul[0], vlog[0]),
                                  fmaf(fmaxf(sacc[1][s][c], sacc[1][s][c + 2]), kmul[1], vlog[1]));
                 };
-                float top = -INFINITY;  // the highest over its column's m
+                const bool far = vtop - vlow > kSumSpan;
+                float top = far ? INFINITY : -INFINITY;  // the highest over its column's m
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
                     // (m starts at -inf, which any score passes; a column of -inf passes nothing)
@@ -477,13 +484,25 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
                         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16)) - kHead;
                         if (x > m[v]) {
                             // nothing but zeros (or a NaN, which stays) before the first score
-                            const float alpha = m[v] == -INFINITY ? 1.f : ex2(m[v] - x);
+                            const float down = m[v] == -INFINITY ? 0.f : m[v] - x;
+                            const float alpha = ex2(down), root = ex2(0.5f * down);
                             m[v] = x;
-                            l[v] *= alpha;
+                            l[v] = l[v] * root * root;  // (a sum of small scales' tokens may be as large as alpha is small)
 #pragma unroll
                             for (int p = 0; p < 2 * KP; ++p) {
                                 at(v, p, 0) *= alpha;
                                 at(v, p, 1) *= alpha;
+                            }
+                        }
+                    }
+                    if (far) {  // the chunk's part of the sums by itself
+#pragma unroll
+                        for (int tt = 0; tt < 2; ++tt) {
+                            vinv[tt] = 0.f;
+#pragma unroll
+                            for (int v = 0; v < NV; ++v) {
+                                const float less = m[v] == -INFINITY ? 0.f : -m[v];
+                                l[v] += ex2(fmaf(sacc[tt][v / 2][v % 2], kmul[tt], less)) + ex2(fmaf(sacc[tt][v / 2][v % 2 + 2], kmul[tt], less));
                             }
                         }
                     }
@@ -716,10 +735,10 @@ cudaError_t run_blocks(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStrea
     cfg.numAttrs = own ? 0 : 1;  // (only a kernel of this call may be overtaken)
     if ((err = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, f)) != cudaSuccess || whole) return err;
 
-    constexpr int kHeadsPerCta = 256 / (HD / 4);
+    constexpr int kRows = 256 / (HD / 4);  // of a CTA of the combine
     cudaLaunchConfig_t ccfg = cfg;
     ccfg.numAttrs = 1;
-    ccfg.gridDim = dim3(d.num_seqs, (k.rows_per_seq + kHeadsPerCta - 1) / kHeadsPerCta);
+    ccfg.gridDim = dim3(d.num_seqs, (k.rows_per_seq + kRows - 1) / kRows);
     ccfg.dynamicSmemBytes = 0;
     const int64_t parts = (static_cast<int64_t>(num_ctas) + d.num_seqs) / std::max(1, d.num_seqs);
     // few, long sequences: a CTA per row, 512 threads over its parts, while that is one wave
@@ -727,18 +746,18 @@ cudaError_t run_blocks(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStrea
         constexpr int kSlices = 512 / (HD / 4);
         ccfg.gridDim = dim3(d.num_seqs, k.rows_per_seq);
         ccfg.blockDim = dim3(512);
-        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, kSlices, 1>, k);
+        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, kSlices, 1, true>, k);
     }
     if (parts >= 32) {
         ccfg.blockDim = dim3(256 * 4);
-        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 4>, k);
+        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 4, kRows, true>, k);
     }
     if (parts >= 16) {
         ccfg.blockDim = dim3(256 * 2);
-        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 2>, k);
+        return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 2, kRows, true>, k);
     }
     ccfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 1>, k);
+    return cudaLaunchKernelEx(&ccfg, combine_kernel<HD, 1, kRows, true>, k);
 }
 
 template <int HD>

@@ -243,32 +243,60 @@ __device__ __forceinline__ uint32_t swz(int row, int cc) {
 // Running merge of split-KV partials (lse_c in log2 units, o_c normalized):
 // sum_c 2^(lse_c - M) o_c / sum_c 2^(lse_c - M) with M the running maximum; a part with no
 // visible token (lse = -inf) adds nothing.
+// kWide: outputs of parts may be any floats (scales per block).  One of the smallest weight may count, so factors are applied as two
+// halves, neither of which is 0 before the product is; and outputs are summed 2^-kPartDown of their size, so that the sum of
+// 2^20 of them is a float.
+constexpr int kPartDown = 20;
+template <bool kWide>
+struct PartFactor {
+    float f;
+    __device__ __forceinline__ explicit PartFactor(float log2_of_it) : f(ex2(kWide ? 0.5f * log2_of_it : log2_of_it)) {}
+    __device__ __forceinline__ float of(float x) const { return kWide ? x * f * f : x * f; }
+    __device__ __forceinline__ float of_part(float x) const { return kWide ? x * f * (f * (1.f / (1 << kPartDown))) : x * f; }
+};
+template <bool kWide = false>
 struct PartMerge {
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // M becomes l at least, and what has been summed so far goes by it
+    __device__ __forceinline__ void rescale(float l) {
+        if (!(l > M)) return;
+        const PartFactor<kWide> r(M - l);  // 0 while M is still -inf
+        den = r.of(den);
+        acc.x = r.of(acc.x);
+        acc.y = r.of(acc.y);
+        acc.z = r.of(acc.z);
+        acc.w = r.of(acc.w);
+        M = l;
+    }
+    // one part (kWide: M is its l at least already)
     __device__ __forceinline__ void add(float l, const float4 &v) {
         if (l == -INFINITY) return;
-        if (l > M) {  // rescale what has been summed so far
-            const float r = ex2(M - l);  // 0 while M is still -inf
-            den *= r;
-            acc.x *= r;
-            acc.y *= r;
-            acc.z *= r;
-            acc.w *= r;
-            M = l;
+        if (!kWide) rescale(l);
+        const PartFactor<kWide> w(l - M);
+        den += w.of(1.f);
+        acc.x += w.of_part(v.x);
+        acc.y += w.of_part(v.y);
+        acc.z += w.of_part(v.z);
+        acc.w += w.of_part(v.w);
+    }
+    // eight parts
+    __device__ __forceinline__ void add8(const float (&l)[8], const float4 (&v)[8]) {
+        if constexpr (kWide) {  // (the factors' two halves make a longer chain: one change of M for all eight)
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, l[i]);
+            rescale(top);
         }
-        const float w = ex2(l - M);
-        den += w;
-        acc.x += w * v.x;
-        acc.y += w * v.y;
-        acc.z += w * v.z;
-        acc.w += w * v.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add(l[i], v[i]);
     }
     // four bf16 outputs: scale * acc / den (zeros when no part saw a token)
     __device__ __forceinline__ uint2 result(float scale) const {
         const float inv = den == 0.f ? 0.f : scale / den;  // (a NaN part stays NaN)
-        return make_uint2(bf16x2_from_f32(acc.x * inv, acc.y * inv),
-                          bf16x2_from_f32(acc.z * inv, acc.w * inv));
+        constexpr float up = kWide ? 1 << kPartDown : 1;
+        return make_uint2(bf16x2_from_f32(acc.x * inv * up, acc.y * inv * up),
+                          bf16x2_from_f32(acc.z * inv * up, acc.w * inv * up));
     }
 };
 
@@ -429,7 +457,7 @@ __device__ __forceinline__ int cta_of(int64_t x, int64_t T, int64_t P) {
 // kCombineSlices slices of a sequence's parts are merged side by side (256 threads each),
 // then the slices' running states are merged: sequences cut into many parts (few, long
 // sequences over a full grid) get several loads in flight per output element.
-template <int HD, int kCombineSlices, int kRows = 256 / (HD / 4)>
+template <int HD, int kCombineSlices, int kRows = 256 / (HD / 4), bool kWide = false>
 __global__ void __launch_bounds__(kRows * (HD / 4) * kCombineSlices) combine_kernel(const KernelArgs a) {
     constexpr int TPH = HD / 4;       // threads per row
     constexpr int TS = kRows * TPH;   // threads of a slice: kRows rows per CTA
@@ -459,7 +487,7 @@ __global__ void __launch_bounds__(kRows * (HD / 4) * kCombineSlices) combine_ker
     // batch issued before the first is used
     const int k = cl - cf + 1;
     const int c_lo = slice * k / kCombineSlices, c_hi = (slice + 1) * k / kCombineSlices;
-    PartMerge mg;
+    PartMerge<kWide> mg;
     if (valid) {
         const int64_t p0 = static_cast<int64_t>(seq) + cf;
         const float *lse = a.part_lse + p0 * a.rows_per_seq + row;
@@ -476,8 +504,7 @@ __global__ void __launch_bounds__(kRows * (HD / 4) * kCombineSlices) combine_ker
                     v[i] = *reinterpret_cast<const float4 *>(o + (c0 + i) * o_stride);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mg.add(l[i], v[i]);
+            mg.add8(l, v);
         }
     }
     sm_m[slice][t] = mg.M;
@@ -486,27 +513,23 @@ __global__ void __launch_bounds__(kRows * (HD / 4) * kCombineSlices) combine_ker
     __syncthreads();
     if (slice != 0 || !valid) return;
     // merge the slices' running states (a slice that saw no part has den = 0)
-    PartMerge all;
+    PartMerge<kWide> all;
+    if constexpr (kWide) {
+#pragma unroll
+        for (int sl = 0; sl < kCombineSlices; ++sl) all.M = fmaxf(all.M, sm_m[sl][t]);
+    }
 #pragma unroll
     for (int sl = 0; sl < kCombineSlices; ++sl) {
         const float m = sm_m[sl][t];
         if (sm_den[sl][t] == 0.f) continue;
-        if (m > all.M) {
-            const float r = ex2(all.M - m);  // 0 while all.M is still -inf
-            all.den *= r;
-            all.acc.x *= r;
-            all.acc.y *= r;
-            all.acc.z *= r;
-            all.acc.w *= r;
-            all.M = m;
-        }
-        const float w = ex2(m - all.M);
+        if (!kWide) all.rescale(m);
+        const PartFactor<kWide> w(m - all.M);
         const float4 v = sm_acc[sl][t];
-        all.den += w * sm_den[sl][t];
-        all.acc.x += w * v.x;
-        all.acc.y += w * v.y;
-        all.acc.z += w * v.z;
-        all.acc.w += w * v.w;
+        all.den += w.of(sm_den[sl][t]);
+        all.acc.x += w.of(v.x);
+        all.acc.y += w.of(v.y);
+        all.acc.z += w.of(v.z);
+        all.acc.w += w.of(v.w);
     }
     *reinterpret_cast<uint2 *>(a.out + out_row * HD + d) = all.result(sv);
 }

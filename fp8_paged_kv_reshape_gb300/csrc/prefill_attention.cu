@@ -1619,7 +1619,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const PrefillArgs<true>
     if (kend <= 0) return;  // zeroed by its CTA
     const int parts = split_parts(a.splits, (kend + tile_keys - 1) / tile_keys, tile_keys);
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
-    PartMerge mg;
+    PartMerge<> mg;
     for (int c0 = 0; c0 < parts; c0 += 8) {
         float l[8];
         float4 v[8];

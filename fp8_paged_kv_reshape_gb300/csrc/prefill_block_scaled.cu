@@ -95,10 +95,11 @@ struct PbSmem {
 };
 
 // What the softmax takes of 64 keys, 16 at a time: scores (over the row's q scale) times kmul are in the log2 domain, weights
-// carry vlog, their sum vinv (twice: the sum is two floats); the keys that are there.
+// carry vlog, their sum vinv (twice: the sum is two floats); the keys that are there.  far, of a tile's second half: the V scales
+// so far are more than kSumSpan apart.
 struct HalfInfo {
     float4 kmul, vlog, vinv[2];
-    uint32_t mask[2], pad[2];
+    uint32_t mask[2], far, pad;
 };
 static_assert(sizeof(HalfInfo) == 80, "layout");
 
@@ -238,6 +239,103 @@ __device__ __forceinline__ float split_q_rows(const __nv_bfloat16 *q, int64_t ro
 // what a row's scores are multiplied by, of 16 keys and its own (kept away from 0 and infinity, which would make a NaN of
 // a score of infinity or 0)
 __device__ __forceinline__ float score_mul(float kmul, float qdown) { return fminf(fmaxf(kmul * qdown, 0x1p-126f), 0x1p126f); }
+
+// O of a warp's rows times factor
+template <int HD>
+__device__ __forceinline__ void scale_o(uint32_t at, float factor) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < HD; c0 += 16) {
+        uint32_t o[16];
+        tmem_ld16(at + c0, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+        tmem_st16(at + c0, o);
+    }
+}
+
+// A row's reference and sum (two fp32 halves); ok: no wait ran out.
+struct FarRow {
+    float m;
+    uint64_t sum2;
+    bool ok;
+};
+
+// The softmax of tiles i..ntiles - 1 where V scales are too far apart for the sum of weights times 1 / vs (see kSumSpan): 32 keys at a
+// time, the sum's terms by themselves.  last: the last key, from the CTA's first tile on, that the row sees (a padding row: any).
+// (In the loop that other caches run, behind a branch, this cost their calls 2 to 5 %.)
+template <int HD, int RT>
+__device__ __noinline__ FarRow far_tiles(uint32_t base, const uint8_t *bp, uint32_t lane_addr, int rt, int i, int ntiles, int rot, int last,
+                                         float qdown, FarRow row) {
+    using L = PbSmem<HD, RT>;
+    const volatile int32_t *abort_flag = reinterpret_cast<const volatile int32_t *>(bp + L::kMisc + 4);
+    auto wait = [&](int off, int k, int phase) {
+        row.ok = __all_sync(0xFFFFFFFFu, mbar_wait(base + static_cast<uint32_t>(off + 8 * k), static_cast<uint32_t>(phase & 1), abort_flag));
+        return row.ok;
+    };
+#pragma unroll 1
+    for (; i < ntiles; ++i) {
+        const int job = RT * i + rt, buf = job % L::kBufs, v0 = 2 * i % L::kNV;
+        if (!wait(L::kVReady, v0, 2 * i / L::kNV) || !wait(L::kVReady, v0 + 1, 2 * i / L::kNV) || !wait(L::kSReady, buf, job / L::kBufs)) break;
+        static_assert(L::kNV % 2 == 0, "a tile's halves are neighbours");
+        tc_fence_after();
+        const HalfInfo *in = reinterpret_cast<const HalfInfo *>(bp + L::kInfo) + v0;
+        const uint32_t scol = lane_addr + L::col_s(buf);
+        const int tile = i + rot >= ntiles ? i + rot - ntiles : i + rot;
+        const int seen = last == INT32_MAX ? kKeys : last - tile * kKeys + 1;  // keys of the tile up to the row's last
+        uint32_t x[32];
+        float k[2], v[2];  // of 16 keys each
+        auto load = [&](int c) {
+            const HalfInfo &half = in[c >> 1];
+            const float2 k2 = reinterpret_cast<const float2 *>(&half.kmul)[c & 1], v2 = reinterpret_cast<const float2 *>(&half.vlog)[c & 1];
+            k[0] = score_mul(k2.x, qdown), k[1] = score_mul(k2.y, qdown), v[0] = v2.x, v[1] = v2.y;
+            const int n = seen - 32 * c;
+            const uint32_t bits = half.mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+            tmem_ld32(scol + 32 * c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (!((bits >> e) & 1u)) x[e] = 0xFF800000u;  // -infinity
+        };
+        float mx = -INFINITY, down = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            load(c);
+            mx = max3f(mx, fmaf(max16(x), k[0], v[0]), fmaf(max16(x + 16), k[1], v[1]));
+        }
+        if (mx > row.m + (kLag + kHead)) {
+            down = row.m == -INFINITY ? 0.f : row.m - (mx - kHead);
+            row.m = mx - kHead;
+        }
+        if (__any_sync(0xFFFFFFFFu, down != 0.f)) {
+            if (L::kAhead) {  // (i > 0: the row had a reference)
+                if (!wait(L::kODone, 2 * rt + ((i - 1) & 1), (i - 1) >> 1)) break;
+                tc_fence_after();
+            }
+            scale_o<HD>(lane_addr + L::col_o(rt), ex2(down));
+            const float root = ex2(0.5f * down);
+            row.sum2 = mul_f32x2(mul_f32x2(row.sum2, pk2(root, root)), pk2(root, root));
+        }
+        const float msub = row.m == -INFINITY ? 0.f : row.m;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            load(c);
+            uint32_t p[16];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                const float a0 = __uint_as_float(x[2 * w]), a1 = __uint_as_float(x[2 * w + 1]), shift = v[w >> 3] - msub;
+                p[w] = f16x2_from_f32(ex2(fmaf(a0, k[w >> 3], shift)), ex2(fmaf(a1, k[w >> 3], shift)));
+                row.sum2 = add_f32x2(row.sum2, pk2(ex2(fmaf(a0, k[w >> 3], -msub)), ex2(fmaf(a1, k[w >> 3], -msub))));
+            }
+            tmem_st16(scol + 32 * c, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(base + static_cast<uint32_t>(L::kPReady + 8 * buf));
+    }
+    return row;
+}
 
 // ---------------------------------------------------------------- the kernel
 
@@ -565,6 +663,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             }
         };
         bool ok = true;
+        uint32_t vtop = 0, vlow = ~0u;  // bits of the largest and the smallest V scale so far
         for (int h = 0; h < 2 * ntiles && ok; ++h) {
             const int st = h % L::kNS, vb = h % L::kNV;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFull, st), (h / L::kNS) & 1, abort_flag));
@@ -576,6 +675,11 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             sc.load(bp + L::kScales + 32 * st, posted, lane);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kVFree, vb), ((h / L::kNV) & 1) ^ 1u, abort_flag));
             if (!ok) break;
+            if (cw == 0) {
+                const bool has = (sc.keys >> (16 * (lane & 3)) & 0xFFFFull) != 0ull;
+                vtop = max(vtop, __reduce_max_sync(0xFFFFFFFFu, has ? __float_as_uint(sc.v) : 0u));
+                vlow = min(vlow, __reduce_min_sync(0xFFFFFFFFu, has ? __float_as_uint(sc.v) : ~0u));
+            }
             if (cw == 0 && lane < 4) {
                 HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
                 reinterpret_cast<float *>(&info->kmul)[lane] = sc.k * (a.sm_scale * 1.4426950408889634f);  // log2(e)
@@ -586,6 +690,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     if (sc.keys != posted) flag(a.status, KVFP8_DEV_BAD_SCALE);
                     info->mask[0] = static_cast<uint32_t>(sc.keys);
                     info->mask[1] = static_cast<uint32_t>(sc.keys >> 32);
+                    info->far = vtop > vlow && (vtop - vlow) >> 23 > kSumSpan;
                 }
             }
             const bool drop_nan = key_tile(h >> 1) * kKeys + ((h & 1) + 1) * kHalf > all_see;
@@ -645,7 +750,8 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         float m_used = -INFINITY;
         uint64_t lsum2 = pk2(0.f, 0.f);  // the row sum, in two fp32 halves
         bool ok = true;
-        for (int i = 0; i < ntiles && ok; ++i) {
+        int i = 0;
+        for (; i < ntiles && ok; ++i) {
             const int job = RT * i + rt, buf = job % L::kBufs, turn = job / L::kBufs;
             const int v0 = 2 * i % L::kNV, v1 = (2 * i + 1) % L::kNV;
             const uint32_t scol = lane_addr + L::col_s(buf);
@@ -667,8 +773,11 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 const uint32_t bits = in[c >> 1]->mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
                 return row_ok ? bits : ~0u;  // (a padding row holds no warp back)
             };
+            if (in[1]->far != 0u) break;
             const bool whole = __all_sync(0xFFFFFFFFu, (visible(0) & visible(1) & visible(2) & visible(3)) == ~0u);
-            float mul[8], vlog[8];  // of 16 keys each
+            float mul[8], vheld[8];  // of 16 keys each
+            // (one row tile: 168 registers do not hold the V scales as well)
+            auto vlog = [&](int k) { return RT == 1 ? reinterpret_cast<const volatile float *>(&in[k >> 2]->vlog)[k & 3] : vheld[k]; };
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const float4 k4 = in[hf]->kmul, v4 = in[hf]->vlog;
@@ -676,10 +785,10 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 mul[4 * hf + 1] = score_mul(k4.y, qdown);
                 mul[4 * hf + 2] = score_mul(k4.z, qdown);
                 mul[4 * hf + 3] = score_mul(k4.w, qdown);
-                vlog[4 * hf] = v4.x;
-                vlog[4 * hf + 1] = v4.y;
-                vlog[4 * hf + 2] = v4.z;
-                vlog[4 * hf + 3] = v4.w;
+                vheld[4 * hf] = v4.x;
+                vheld[4 * hf + 1] = v4.y;
+                vheld[4 * hf + 2] = v4.z;
+                vheld[4 * hf + 3] = v4.w;
             }
             // (not kAhead: with S(rt, i) O(rt, i-1) is done)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kSReady, buf), turn & 1, abort_flag));
@@ -701,7 +810,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                mx = max3f(mx, fmaf(max16(s[c]), mul[2 * c], vlog[2 * c]), fmaf(max16(s[c] + 16), mul[2 * c + 1], vlog[2 * c + 1]));
+                mx = max3f(mx, fmaf(max16(s[c]), mul[2 * c], vlog(2 * c)), fmaf(max16(s[c] + 16), mul[2 * c + 1], vlog(2 * c + 1)));
             // the reference moves, and O is rescaled, only when the maximum has risen far above it (first visible keys: O
             // is still zero for this row, nothing to rescale)
             float factor = 1.f;
@@ -720,15 +829,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     tc_fence_after();
                 }
                 lsum2 = mul_f32x2(lsum2, pk2(factor, factor));
-#pragma unroll 1
-                for (int c0 = 0; c0 < HD; c0 += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(lane_addr + L::col_o(rt) + c0, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-                    tmem_st16(lane_addr + L::col_o(rt) + c0, o);
-                }
+                scale_o<HD>(lane_addr + L::col_o(rt), factor);
             }
             // P = 2^(s + log2 vs - m) as f16 pairs, written over the first half of each 32 scores; its float values are summed
             const float msub = m_used == -INFINITY ? 0.f : m_used;
@@ -739,7 +840,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 uint64_t sum2[2];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const float shift = vlog[2 * c + g] - msub;
+                    const float shift = vlog(2 * c + g) - msub;
                     const uint64_t shift2 = pk2(shift, shift), mul2 = pk2(mul[2 * c + g], mul[2 * c + g]);
                     sum2[g] = pk2(0.f, 0.f);
 #pragma unroll
@@ -758,6 +859,12 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kPReady, buf));
+        }
+        if (ok && !idle && i < ntiles) {
+            const FarRow row = far_tiles<HD, RT>(base, bp, lane_addr, rt, i, ntiles, rot, row_ok ? pos - tile_lo * kKeys : INT32_MAX, qdown, {m_used, lsum2, true});
+            m_used = row.m;
+            lsum2 = row.sum2;
+            ok = row.ok;
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(L::kODone, 2 * rt + ((ntiles - 1) & 1)), ((ntiles - 1) >> 1) & 1, abort_flag));
         if (ok && !idle) {
@@ -845,7 +952,7 @@ __global__ void __launch_bounds__(256) join_blocks_kernel(const __grid_constant_
     if (kend <= 0) return;  // zeroed by its CTA
     const int parts = split_parts(a.splits, (kend + kKeys - 1) / kKeys, kKeys);
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.splits * tile_rows + lr;
-    PartMerge mg;
+    PartMerge<true> mg;
     for (int c0 = 0; c0 < parts; c0 += 8) {
         float l[8];
         float4 v[8];
@@ -858,8 +965,7 @@ __global__ void __launch_bounds__(256) join_blocks_kernel(const __grid_constant_
                 v[i] = *reinterpret_cast<const float4 *>(a.part_o + p * HD + d);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mg.add(l[i], v[i]);
+        mg.add8(l, v);
     }
     *reinterpret_cast<uint2 *>(a.out + ((static_cast<int64_t>(qr.q0) + r / G) * a.n_q + kvh * G + r % G) * HD + d) =
         mg.result(1.f);

@@ -3,8 +3,9 @@
 Bounds are those of test_gpu_block_scaled.py, but for what a small weight may be off by: the weights softmax * vs that meet V are
 fp16 with a row's highest at 2^7 at least, so one below 2^-14 is off by 2^-25, 2^-32 of the highest, and a V code is 448 at most.
 With H the highest softmax * vs among the tokens that the row sees: L * 2^-32 * H * 448.  |log2 vs| is up to 120 here, and the reference
-that scores are taken against up to 15 from the highest: scores in the log2 domain are numbers of at most 1.45 S + 150.  A term of the
-row's sum is a float, 2^-149 at least, and the highest one 2^(7 - 120): L * 2^-36 of the sum.
+that scores are taken against up to 15 from the highest: scores in the log2 domain are numbers of at most 1.45 S + 150.  The row's sum
+may lose 2^-24 of itself where small weights leave a float's range; a term of it is a float, 2^-149 at least, and the highest one
+2^(7 - 120): L * 2^-36 of the sum.
 """
 import numpy as np
 import pytest
@@ -46,7 +47,7 @@ def check(got, c, causal=True, more=0.0):
                                        causal)
     g = got.double().cpu().numpy()
     d = (hd + 8) * 2.0 ** -24 * (1.45 * reach + 150) + 2.0 ** -21 + more
-    d = d + longest * 2.0 ** -36
+    d = d + 2.0 ** -24 + longest * 2.0 ** -36  # (the row's sum)
     bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2 * d[..., None] + 2 * (longest / 16 + 16) * 2.0 ** -23) * weight \
         + (longest * 2.0 ** -32 * 448 * highest(c, causal))[..., None] + 1e-37
     over = np.abs(g - ref) - bound
@@ -104,9 +105,22 @@ def test_small_scales_hold_the_highest_scores(small, octaves, n_q, n_kv, hd, qle
 
 
 @pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
-@pytest.mark.parametrize("low, high", [(-60, 1), (-30, 31)])
+@pytest.mark.parametrize("lengths", LENGTHS, ids=["whole", "split"])
+@pytest.mark.parametrize("order", ORDERS)
+def test_smallest_and_largest_scales_share_a_row(order, lengths, n_q, n_kv, hd, qlen):
+    """V scales of 2^-60 and of 2^120 in one sequence: what the small ones hold adds nothing to the output, but their tokens' weights
+    belong to the row's sum."""
+    c = no_large_codes(build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 41,
+                             scale=two_scales(order, lengths, 2.0 ** -60, 2.0 ** 120)))
+    c["ks"][c["ks"] > 0] = 2.0 ** -8
+    for causal in (True, False):
+        check(run(multi, c, qlen, causal=causal), c, causal)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+@pytest.mark.parametrize("low, high", [(-60, 1), (-30, 31), (-60, 121), (-30, 121)])
 def test_scales_and_scores_far_apart(low, high, n_q, n_kv, hd, qlen):
-    """Scales at random, with scores that lie up to a hundred octaves apart."""
+    """Scales at random, over the whole range too, with scores that lie up to a hundred octaves apart."""
     for lengths, seed in ((LENGTHS[0], 42), (LENGTHS[1], 43)):
         c = no_large_codes(build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], seed,
                                  scale=lambda r, shape: np.exp2(r.integers(low, high, shape))))
