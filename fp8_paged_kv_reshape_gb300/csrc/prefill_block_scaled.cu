@@ -886,18 +886,20 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             for (int c0 = 0; c0 < HD; c0 += 32) {
                 uint32_t nan = 0;
                 if (any_nan) nan = nan_value_dims<HD>(a, seq, kvh, c0, nan_first, nan_last);
+                __syncwarp();  // (tensor memory is read by whole warps; lanes part above and where rows are stored)
                 uint32_t o[32];
                 tmem_ld32(lane_addr + L::col_o(rt) + c0, o);
                 tmem_wait_ld();
-                if (kSplit && !row_ok) continue;
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     v[e] = (nan >> e) & 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float(o[e]) * inv;
                 if constexpr (kSplit) {
                     float4 *to = reinterpret_cast<float4 *>(a.part_o + prow * HD + c0);
+                    if (row_ok) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) to[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
                 } else {
                     // by way of the row tile's q, which no product reads any more: written a row a lane, read in rows
 #pragma unroll

@@ -127,3 +127,12 @@ def test_scales_and_scores_far_apart(low, high, n_q, n_kv, hd, qlen):
         live = c["ks"] > 0
         c["ks"][live] = np.exp2(np.random.default_rng(seed).integers(-7, 1, int(live.sum())))
         check(run(multi, c, qlen), c)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("rows", [17, 31, 33, 65, 97, 127, 129, 161, 225])
+def test_part_filled_warps_of_split_calls(rows, hd):
+    """One sequence whose keys are split over CTAs, with any number of rows in the last warp that has some."""
+    c = build(1, 1, hd, 16, [2100], [rows], 45)
+    check(run(multi, c, rows), c)
+    check(run(multi, c, rows, causal=False), c, False)
