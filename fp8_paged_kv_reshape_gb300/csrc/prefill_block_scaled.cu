@@ -5,10 +5,12 @@
 // Rows are (query token j, head g of the kv head's group) pairs, row = j*G + g; a CTA takes RT tiles of 128 rows of a
 // (sequence, kv head) and goes over their keys in tiles of 128.  What bounds it is the chain of a row tile's scores,
 // softmax and product with V, so the work beside it is kept small:
-//  * K is not converted.  q is the sum of two E4M3 numbers: with q scaled by a power of two per row, so that its largest
-//    element lies in [128, 256), a = E4M3(q) and b = E4M3(q - a) give a bf16's 8 bits exactly where it is within 2^9 of the
-//    row's largest, and to 2^-17 of that below.  K tiles arrive by TMA as the operand that the product takes
-//    (kind::f8f6f4, twice the rate of f16: two products at half the time), products are exact, sums float.
+//  * K is not converted.  q is the sum of an E4M3 and an E5M2 number: with q scaled by a power of two per row, so that its largest
+//    element lies in [128, 256), a = E4M3(q) leaves q - a of at most 8 of a bf16's last places, which 3 bits hold, so
+//    b = E5M2(q - a) makes the sum exact as long as a is a normal number, within 2^13 of the row's largest.  Below, q - a is 2^-10 at
+//    most and b off by 2^-14, 2^-21 of the largest.  K tiles arrive by TMA as the operand that the product takes
+//    (kind::f8f6f4, twice the rate of f16: two products at half the time), products are exact, sums float.  (With b in E4M3, whose
+//    smallest number is 2^-9, q was exact within 2^9 and to 2^-17 of the largest below, at the same times.)
 //  * V meets fp16 weights, so it is converted to fp16 (exactly) and transposed: ldmatrix gives a lane four
 //    dims of a key, which after the conversion are stored with stmatrix.trans as rows of V^T.
 //  * ks multiplies the scores, 16 keys at a time (a block is 16 keys at least), in the multiplication that takes them
@@ -67,7 +69,7 @@ struct PbSmem {
     static constexpr int kNK = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // K tiles
     static constexpr int kNV = HD == 256 ? 2 : 4;                        // V^T halves
     static constexpr int kNS = HD == 64 ? 4 : HD == 128 ? 3 : 2;         // staged V halves
-    // q: a row tile's two E4M3 parts, 128 rows of [segment][row][kSeg] each
+    // q: a row tile's two parts, 128 rows of [segment][row][kSeg] each
     static constexpr int kPart = 128 * HD;
     static constexpr int kQ = 0;
     static constexpr int kKBuf = kKeys * HD, kK = kQ + RT * 2 * kPart;   // [segment][128 keys][kSeg]
@@ -117,9 +119,14 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: E4M3 A and B, fp32 D, both K-major, M x N.
-__host__ __device__ constexpr uint32_t e4m3_idesc(int m, int n) {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: E4M3 or E5M2 A, E4M3 B, fp32 D, both K-major, M x N.
+__host__ __device__ constexpr uint32_t f8_idesc(bool e5m2, int m, int n) {
+    return (1u << 4) | (e5m2 ? 1u << 7 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 // Shared-memory matrix descriptor: K-major operand of SEG-byte rows (128 or 64) swizzled over them.
 template <int SEG>
@@ -187,8 +194,8 @@ __device__ __forceinline__ float max16(const uint32_t *s) {
     return fmaxf(max3f(a, b, c), v(15));
 }
 
-// A warp's 32 rows of q (bf16 at q + the lane's row_at, or zeros where the lane has none) as two E4M3 parts at part0 and
-// part1 (rows row..row+31 of K-major operands).  Returns what a score of the lane's row is to be multiplied by.  HD/8 lanes
+// A warp's 32 rows of q (bf16 at q + the lane's row_at, or zeros where the lane has none) as an E4M3 part at part0 and an E5M2 part
+// at part1 (rows row..row+31 of K-major operands).  Returns what a score of the lane's row is to be multiplied by.  HD/8 lanes
 // share a row.  (A lane to a row took 13000 cycles of a CTA's 160000: lines apart, read twice.)
 template <int HD, int SEG>
 __device__ __forceinline__ float split_q_rows(const __nv_bfloat16 *q, int64_t row_at, bool row_ok, uint8_t *part0, uint8_t *part1, int row) {
@@ -222,7 +229,7 @@ __device__ __forceinline__ float split_q_rows(const __nv_bfloat16 *q, int64_t ro
                 const float u = bf16lo(x[i]) * up, v = bf16hi(x[i]) * up;
                 hi[i] = e4m3x2_from_f32(u, v);
                 const float2 back = __half22float2(h2(f16x2_from_e4m3x2(hi[i])));
-                lo[i] = e4m3x2_from_f32(u - back.x, v - back.y);
+                lo[i] = e5m2x2_from_f32(u - back.x, v - back.y);
             }
             uint2 a = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
             if (top >= 0x7F80u) a = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);  // an infinity or NaN: the whole row becomes NaN
@@ -559,7 +566,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         // ------------------------------------------------------------ products
         if (lane == 0) {
             const int own = warp - W::kMma;  // its row tile (kAhead: both)
-            const uint32_t idesc_s = e4m3_idesc(128, kKeys), idesc_o = f16_idesc(128, HD);
+            const uint32_t idesc_s[2] = {f8_idesc(false, 128, kKeys), f8_idesc(true, 128, kKeys)}, idesc_o = f16_idesc(128, HD);
             // operand descriptors computed once; each product adds its constant offset
             const uint64_t qdesc = k_desc<L::kSeg>(base + L::kQ), kdesc = k_desc<L::kSeg>(base + L::kK),
                            vdesc = sw128_desc(base + L::kV);
@@ -579,7 +586,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                     for (int k = 0; k < HD / 32; ++k) {
                         const int seg = 32 * k / L::kSeg, in = 32 * k % L::kSeg;
                         umma_f8(tmem + L::col_s(buf), desc_at(qdesc, (2 * r + part) * L::kPart + seg * (128 * L::kSeg) + in),
-                                desc_at(kd, seg * (kKeys * L::kSeg) + in), idesc_s, part > 0 || k > 0 ? 1u : 0u);
+                                desc_at(kd, seg * (kKeys * L::kSeg) + in), idesc_s[part], part > 0 || k > 0 ? 1u : 0u);
                     }
                 umma_commit(bar(L::kSReady, buf));
                 if (!L::kAhead || r == RT - 1) umma_commit(bar(L::kKFree, i % L::kNK));

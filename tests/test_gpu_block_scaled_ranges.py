@@ -136,3 +136,25 @@ def test_part_filled_warps_of_split_calls(rows, hd):
     c = build(1, 1, hd, 16, [2100], [rows], 45)
     check(run(multi, c, rows), c)
     check(run(multi, c, rows, causal=False), c, False)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", ROUTES)
+@pytest.mark.parametrize("octaves", [9, 11, 13, 16])
+def test_small_elements_of_a_query_row_with_a_large_one(octaves, n_q, n_kv, hd, qlen):
+    """One element 2^octaves times the row's others, over keys that are 0 there, so that the small elements make the scores."""
+    lengths = [300, 77]
+    c = build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 46)
+    q = c["q"].double().numpy()
+    q[..., 5] = 0
+    q[..., 5] = np.exp2(np.floor(np.log2(np.abs(q).max(-1))) + octaves)
+    c["q"] = torch.from_numpy(q).bfloat16()
+    c["kc"][..., 5] = 0
+    # Up to 16 score columns (8 at head_dim 256) q is fp16, off by 2^-25 below 2^-14.  Beyond, scaled to a largest element of 2^7: an E4M3
+    # number leaves 8 last places of a bf16's 8 bits, which E5M2's 3 bits hold, while the first is normal, from 2^-6 = 2^-13 of the
+    # largest on; below, what it leaves is 2^-10 at most and E5M2's half step there 2^-14, 2^-21 of the largest.
+    q = np.abs(c["q"].double().numpy())
+    top = q.max(-1, keepdims=True)
+    off = np.where(q >= top * 2.0 ** -13, 0.0, 2.0 ** -21 * top) if qlen >= 30 else np.full(q.shape, 2.0 ** -25)
+    k = np.abs(bso.decode(c["kc"])) * c["ks"][:, None, :n_kv, None]  # [block, token, head, dim]
+    k = np.repeat(np.nan_to_num(k[c["bt"][c["bt"] >= 0]]).max((0, 1)), n_q // n_kv, 0)
+    check(run(multi, c, qlen), c, more=1.45 / np.sqrt(hd) * (off * k).sum(-1))
