@@ -96,7 +96,7 @@ struct PbSmem {
     static_assert(128 * kBufs + RT * HD <= 512, "tensor memory");
 };
 
-// What the softmax takes of 64 keys, 16 at a time: scores (over the row's q scale) times kmul are in the log2 domain, weights
+// What the softmax takes of 64 keys, 16 at a time: scores times kmul (K's scales) and what its row says are in the log2 domain, weights
 // carry vlog, their sum vinv (twice: the sum is two floats); the keys that are there.  far, of a tile's second half: the V scales
 // so far are more than kSumSpan apart.
 struct HalfInfo {
@@ -245,7 +245,7 @@ __device__ __forceinline__ float split_q_rows(const __nv_bfloat16 *q, int64_t ro
 
 // what a row's scores are multiplied by, of 16 keys and its own (kept away from 0 and infinity, which would make a NaN of
 // a score of infinity or 0)
-__device__ __forceinline__ float score_mul(float kmul, float qdown) { return fminf(fmaxf(kmul * qdown, 0x1p-126f), 0x1p126f); }
+__device__ __forceinline__ float score_mul(float kmul, float qmul) { return fminf(fmaxf(kmul * qmul, 0x1p-126f), 0x1p126f); }
 
 // O of a warp's rows times factor
 template <int HD>
@@ -273,7 +273,7 @@ struct FarRow {
 // (In the loop that other caches run, behind a branch, this cost their calls 2 to 5 %.)
 template <int HD, int RT>
 __device__ __noinline__ FarRow far_tiles(uint32_t base, const uint8_t *bp, uint32_t lane_addr, int rt, int i, int ntiles, int rot, int last,
-                                         float qdown, FarRow row) {
+                                         float qmul, FarRow row) {
     using L = PbSmem<HD, RT>;
     const volatile int32_t *abort_flag = reinterpret_cast<const volatile int32_t *>(bp + L::kMisc + 4);
     auto wait = [&](int off, int k, int phase) {
@@ -295,7 +295,7 @@ __device__ __noinline__ FarRow far_tiles(uint32_t base, const uint8_t *bp, uint3
         auto load = [&](int c) {
             const HalfInfo &half = in[c >> 1];
             const float2 k2 = reinterpret_cast<const float2 *>(&half.kmul)[c & 1], v2 = reinterpret_cast<const float2 *>(&half.vlog)[c & 1];
-            k[0] = score_mul(k2.x, qdown), k[1] = score_mul(k2.y, qdown), v[0] = v2.x, v[1] = v2.y;
+            k[0] = score_mul(k2.x, qmul), k[1] = score_mul(k2.y, qmul), v[0] = v2.x, v[1] = v2.y;
             const int n = seen - 32 * c;
             const uint32_t bits = half.mask[c & 1] & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
             tmem_ld32(scol + 32 * c, x);
@@ -689,7 +689,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             }
             if (cw == 0 && lane < 4) {
                 HalfInfo *info = reinterpret_cast<HalfInfo *>(bp + L::kInfo) + vb;
-                reinterpret_cast<float *>(&info->kmul)[lane] = sc.k * (a.sm_scale * 1.4426950408889634f);  // log2(e)
+                reinterpret_cast<float *>(&info->kmul)[lane] = sc.k;
                 reinterpret_cast<float *>(&info->vlog)[lane] = static_cast<float>(static_cast<int>(__float_as_uint(sc.v) >> 23) - 127);
                 const float inv = block_scale_inverse(sc.v);
                 reinterpret_cast<float2 *>(info->vinv)[lane] = make_float2(inv, inv);
@@ -747,7 +747,9 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
         const int64_t row_at = ((static_cast<int64_t>(qr.q0) + jq) * a.n_q + kvh * G + gq) * HD;
         const int pos = a.causal ? Ls - nb + jq : Ls - 1;  // last key position the row may see
         uint8_t *qp = bp + L::kQ + rt * 2 * L::kPart;
-        const float qdown = split_q_rows<HD, L::kSeg>(a.query, row_at, row_ok, qp, qp + L::kPart, tid & 96);
+        // what the row's scores are multiplied by, but for K's scale (which comes last: q's and sm_scale alone stay well inside a float)
+        const float qmul = split_q_rows<HD, L::kSeg>(a.query, row_at, row_ok, qp, qp + L::kPart, tid & 96) *
+                           (a.sm_scale * 1.4426950408889634f);  // log2(e)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kQReady, 0));
@@ -788,10 +790,10 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const float4 k4 = in[hf]->kmul, v4 = in[hf]->vlog;
-                mul[4 * hf] = score_mul(k4.x, qdown);
-                mul[4 * hf + 1] = score_mul(k4.y, qdown);
-                mul[4 * hf + 2] = score_mul(k4.z, qdown);
-                mul[4 * hf + 3] = score_mul(k4.w, qdown);
+                mul[4 * hf] = score_mul(k4.x, qmul);
+                mul[4 * hf + 1] = score_mul(k4.y, qmul);
+                mul[4 * hf + 2] = score_mul(k4.z, qmul);
+                mul[4 * hf + 3] = score_mul(k4.w, qmul);
                 vheld[4 * hf] = v4.x;
                 vheld[4 * hf + 1] = v4.y;
                 vheld[4 * hf + 2] = v4.z;
@@ -868,7 +870,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             if (lane == 0) mbar_arrive(bar(L::kPReady, buf));
         }
         if (ok && !idle && i < ntiles) {
-            const FarRow row = far_tiles<HD, RT>(base, bp, lane_addr, rt, i, ntiles, rot, row_ok ? pos - tile_lo * kKeys : INT32_MAX, qdown, {m_used, lsum2, true});
+            const FarRow row = far_tiles<HD, RT>(base, bp, lane_addr, rt, i, ntiles, rot, row_ok ? pos - tile_lo * kKeys : INT32_MAX, qmul, {m_used, lsum2, true});
             m_used = row.m;
             lsum2 = row.sum2;
             ok = row.ok;

@@ -158,3 +158,20 @@ def test_small_elements_of_a_query_row_with_a_large_one(octaves, n_q, n_kv, hd, 
     k = np.abs(bso.decode(c["kc"])) * c["ks"][:, None, :n_kv, None]  # [block, token, head, dim]
     k = np.repeat(np.nan_to_num(k[c["bt"][c["bt"] >= 0]]).max((0, 1)), n_q // n_kv, 0)
     check(run(multi, c, qlen), c, more=1.45 / np.sqrt(hd) * (off * k).sum(-1))
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", [r for r in ROUTES if r[3] >= 30] + [(20, 1, 128, 1), (36, 4, 256, 1)])
+@pytest.mark.parametrize("octaves", [20, 100, 126])
+def test_long_chunks_and_wide_groups_take_rows_of_any_size(octaves, n_q, n_kv, hd, qlen):
+    """A row 2^octaves times as large, with scales and sm_scale as much smaller, gives the same to the bit: all of these are powers of
+    two.  (126: elements up to 2^127, the largest binade.)"""
+    lengths = [300, 77]
+    c = build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 47)
+    c["q"] = c["q"].clamp(-2, 2)
+    sm = float(np.float32(1 / np.sqrt(hd)))
+    want = run(multi, c, qlen, sm_scale=sm)
+    check(want, c)
+    c["q"] = (c["q"].double() * 2.0 ** octaves).bfloat16()
+    c["ks"] *= np.float32(2.0 ** -20)
+    assert bool(torch.isfinite(c["q"]).all())
+    assert torch.equal(run(multi, c, qlen, sm_scale=sm * 2.0 ** (20 - octaves)), want)
