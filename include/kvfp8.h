@@ -559,11 +559,12 @@ KVFP8_API size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_s
  * block and kv head,
  *   s_t = sm_scale * ks_t * sum_d q[b][h][d] * dec(K(t, kv, d))
  *   out[b][h][d] = sum_t softmax(s)_t * vs_t * dec(V(t, kv, d))
- * Codes enter the tensor cores exactly.  q enters as for the other calls (fp16: exactly from 2^-17 to 65504), or,
- * in long query chunks and wide groups, exactly where it is within 2^13 of its row's largest element and to 2^-21
- * of that one below (one of 2^-107 at least; a smaller row as if its largest were that); a row with an infinity or NaN becomes
- * NaN then.  Scores, the exponential, the sum of the weights and the
- * accumulation are float.  softmax(s)_t * vs_t enters the product with V as fp16, 2^7 to 2^15 at a row's
+ * Codes enter the tensor cores exactly.  q enters as for the other calls (fp16: exactly from 2^-17 to 65504; past
+ * it as an infinity, and the row's result is NaN, or 0 where every score is -infinity).  In long query chunks and
+ * wide groups it may have any size, and enters exactly where it is within 2^13 of its row's largest element, to
+ * 2^-21 of that one below (one of 2^-107 at least; a smaller row as if its largest were that); a row with an
+ * infinity or NaN becomes NaN there.  Scores, the exponential, the sum of the weights and the accumulation are
+ * float.  softmax(s)_t * vs_t enters the product with V as fp16, 2^7 to 2^15 at a row's
  * highest (of the tokens that it sees): 11 bits down to 2^-21 of the highest, multiples of 2^-24 below, none
  * below 2^-32.
  *

@@ -175,3 +175,18 @@ def test_long_chunks_and_wide_groups_take_rows_of_any_size(octaves, n_q, n_kv, h
     c["ks"] *= np.float32(2.0 ** -20)
     assert bool(torch.isfinite(c["q"]).all())
     assert torch.equal(run(multi, c, qlen, sm_scale=sm * 2.0 ** (20 - octaves)), want)
+
+
+@pytest.mark.parametrize("n_q, n_kv, hd, qlen", [r for r in ROUTES if r[3] < 30])
+def test_query_elements_past_fp16_in_a_few_columns(n_q, n_kv, hd, qlen):
+    """They are infinities there: the row is NaN where a score is (here some are positive, some negative), the others stay."""
+    lengths = [300, 77]
+    c = build(n_q, n_kv, hd, 16, lengths, [min(qlen, n) for n in lengths], 48)
+    c["q"][0, 1, 7] = 65280.0  # bf16's largest below 65504
+    want = run(multi, c, qlen)
+    c["q"][0, 1, 7] = 2.0 ** 17
+    c["q"][-1, 0, 3] = -2.0 ** 100
+    got = run(multi, c, qlen)
+    assert bool(torch.isnan(got[0, 1]).all()) and bool(torch.isnan(got[-1, 0]).all())
+    got[0, 1], got[-1, 0] = want[0, 1], want[-1, 0]
+    assert torch.equal(got, want)
