@@ -27,6 +27,11 @@ namespace {
 constexpr int kRotWarps = 8;
 constexpr int kMaxPairs = 128;  // of a head (head_dim <= 256)
 
+// (turns_of's shift: below 2^54)
+__device__ __forceinline__ bool frequency_ok(double f) {
+    return (static_cast<uint64_t>(__double_as_longlong(f)) >> 52 & 0x7FFu) < 1023u + 54u;
+}
+
 // frequency (radians a position) -> 2^-64 turns a position, whole turns dropped, within one unit: its 53 bits
 // times 1 / 2 pi as a 128-bit fraction, shifted to where the exponent says.  (By float64 arithmetic the FP64
 // pipe was busy for 16 us of each call: 2 results a clock and SM.)
@@ -43,7 +48,7 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
     uint64_t t = 0;
     if (s >= 64)
         t = s < 128 ? hi >> (s - 64) : 0;
-    else if (s > 0)  // (frequencies below 2^54)
+    else if (s > 0)
         t = hi << (64 - s) | lo >> s;
     return bits >> 63 ? 0 - t : t;
 }
@@ -112,9 +117,15 @@ __global__ void __launch_bounds__(32 * kRotWarps) rotary_kernel(const RotaryArgs
     const bool active = lane < at_once * units;
     const int heads = a.heads[0] + a.heads[1];
     uint64_t turns[kMaxPairs / 32];
+    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kMaxPairs / 32; ++i)
-        turns[i] = lane + 32 * i < pairs ? turns_of(a.frequencies[lane + 32 * i]) : 0;
+    for (int i = 0; i < kMaxPairs / 32; ++i) {
+        const double f = lane + 32 * i < pairs ? a.frequencies[lane + 32 * i] : 0.;
+        turns[i] = turns_of(f);
+        bad |= !frequency_ok(f);
+    }
+    if (bad) flag(a.status, KVFP8_DEV_BAD_SCALE);
+    const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
 
     const int64_t items = a.num_tokens * splits, step = static_cast<int64_t>(gridDim.x) * kRotWarps;
     for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRotWarps + warp; item < items; item += step) {
@@ -156,6 +167,9 @@ __global__ void __launch_bounds__(32 * kRotWarps) rotary_kernel(const RotaryArgs
                 const float2 cs = cos_sin(static_cast<uint64_t>(pos) * turns[i]);
                 table[warp][lane + 32 * i] = make_float2(cs.x * a.magnitude, cs.y * a.sin_magnitude);
             }
+        if (any_bad)  // a pair without an angle becomes NaN (its frequency is looked up again: no register is spent on it)
+            for (int i = lane; i < pairs; i += 32)
+                if (!frequency_ok(a.frequencies[i])) table[warp][i] = make_float2(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
         __syncwarp();
         float c[8], s[8];
 #pragma unroll

@@ -610,8 +610,9 @@ KVFP8_API kvfp8_status kvfp8_paged_attention_multi_block_scaled(
  *
  * Angles are within 2^-27 turn at any position; cosines, sines, products and sums are float, rounded once to
  * dtype.
- * Frequencies must be finite and below 2^31 in magnitude.  A position outside (-2^31, 2^31) leaves the
- * token's output rows unwritten and sets KVFP8_DEV_BAD_SLOT.
+ * A frequency that is not finite, or 2^54 and more in magnitude, makes its pair NaN in every token and sets
+ * KVFP8_DEV_BAD_SCALE.  A position outside (-2^31, 2^31) leaves the token's output rows unwritten and sets
+ * KVFP8_DEV_BAD_SLOT.
  *
  * query, key, outputs  device, dtype [num_tokens][heads][head_dim], row strides in elements (>= heads *
  *                      head_dim; 16-byte rows); an output may be its own input (the same pointer and stride), and
