@@ -6,7 +6,7 @@
 //
 // The angle is taken in turns as a 64-bit fraction: F = frequency / 2 pi in units of 2^-64 turn (its
 // whole turns dropped, which positions being whole numbers allow), and position * F modulo 2^64
-// drops the whole turns of the product exactly.  What is left is off by at most |position| * 2^-65 turn: far positions
+// drops the whole turns of the product exactly.  What is left is off by at most |position| * 2^-64 turn: far positions
 // are as exact as near ones, at one 64-bit multiplication per pair and token.  The nearest quarter turn is
 // then split off as an integer and sinpif / cospif see |x| <= 1/4.
 //
