@@ -762,6 +762,33 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None 
     return torch.tensor(f, dtype=torch.float64, device=device), magnitude
 
 
+class _Rotary(torch.autograd.Function):
+    """rotary_embedding with a graph: its gradient is the call turned the other way (and so is that one's)."""
+
+    @staticmethod
+    def forward(ctx, query, key, positions, frequencies, interleaved, magnitude, transpose, status, zeroed):
+        ctx.save_for_backward(positions, frequencies)
+        ctx.how = (interleaved, magnitude, not transpose, status)
+        ctx.set_materialize_grads(False)
+        # (a gradient's rows at positions out of range, which no call writes, are zero)
+        outs = [torch.zeros_like(t) if zeroed and t is not None else None for t in (query, key)]
+        return _CALLS.rotary_embedding(query, key, positions, frequencies, interleaved, magnitude, transpose, *outs, status)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        # whole rows of 16-byte pieces, whatever strides a gradient comes with
+        grads = [g.clone(memory_format=torch.contiguous_format)
+                 if g is not None and (not g.is_contiguous() or g.data_ptr() % 16) else g for g in grads]
+        grads = [g if need else None for g, need in zip(grads, ctx.needs_input_grad)]
+        if grads[0] is None and grads[1] is None:
+            back = grads
+        elif grads[0] is None:
+            back = None, _Rotary.apply(grads[1], None, *ctx.saved_tensors, *ctx.how, True)[0]
+        else:
+            back = _Rotary.apply(*grads, *ctx.saved_tensors, *ctx.how, True)
+        return (*back, *[None] * 7)
+
+
 def rotary_embedding(query: torch.Tensor, key: torch.Tensor | None, positions: torch.Tensor,
                      frequencies: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0,
                      transpose: bool = False, query_out: torch.Tensor | None = None,
@@ -772,9 +799,17 @@ def rotary_embedding(query: torch.Tensor, key: torch.Tensor | None, positions: t
     fused row allowed); positions int64 [num_tokens]; frequencies float64 [rot_dim / 2] (rotary_frequencies
     makes them), rot_dim a multiple of 16 up to head_dim.  Pairs are dims (j, j + rot_dim / 2), or (2j, 2j + 1)
     when interleaved.  transpose: turned back (the gradient; at magnitude 1 the inverse).  An output may be
-    its own input.
+    its own input.  Where a position is out of range, a row stays as it was: undefined in an output that is made here.
+    Where query or key requires a gradient, outputs are made here and have a graph (none goes to frequencies).
     """
     with _on(stream):
+        if torch.is_grad_enabled() and (query.requires_grad or (key is not None and key.requires_grad)
+                                        or frequencies.requires_grad):
+            if frequencies.requires_grad:
+                raise ValueError("frequencies get no gradient: detach them")
+            if query_out is not None or key_out is not None:
+                raise ValueError("query_out and key_out have no graph: call without them, or under torch.no_grad()")
+            return _Rotary.apply(query, key, positions, frequencies, interleaved, magnitude, transpose, status, False)
         return _CALLS.rotary_embedding(query, key, positions, frequencies, interleaved, magnitude, transpose,
                                        query_out, key_out, status)
 
