@@ -729,7 +729,7 @@ def paged_attention_multi_block_scaled(query: torch.Tensor, query_start_loc: tor
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
                        original_len: int = 0, low_turns: float = 1.0, high_turns: float = 32.0,
-                       device="cuda"):
+                       device="cuda", ramp: str = "turns", magnitude: float | None = None):
     """(frequencies, magnitude) for rotary_embedding: float64 [rot_dim / 2], radians a position, and what the
     rotated values are multiplied by.
 
@@ -739,7 +739,13 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None 
                 times slower, the fastest as before
       "parts"   by the turns that a pair makes in original_len positions, n_j = original_len * f_j / 2 pi: kept
                 from high_turns on, f_j / factor up to low_turns, in between k f_j + (1 - k) f_j / factor with
-                k = (n_j - low_turns) / (high_turns - low_turns); magnitude 0.1 ln(factor) + 1
+                k = (n_j - low_turns) / (high_turns - low_turns); magnitude 0.1 ln(factor) + 1 (the YaRN paper,
+                arXiv:2309.00071).  With ramp "pairs" k goes by the pair instead, as published checkpoints of that scheme were
+                trained: 1 up to the pair floor(J(high_turns)), 0 from ceil(J(low_turns)) on, linear in between, J(n) =
+                rot_dim ln(original_len / 2 pi n) / (2 ln base) being where a pair makes n turns, both kept within
+                0..rot_dim - 1.
+    magnitude: what to return in the place of the above.  A model whose scheme is "parts" by turns without one has 1.0, and may
+    have other bounds: 1 and 4 turns, say.
     """
     if rot_dim < 2 or rot_dim % 2 != 0:
         raise ValueError("rot_dim must be even and positive")
@@ -747,19 +753,30 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None 
         raise ValueError("base and factor must be positive and finite")
     if scaling not in (None, "linear", "base", "parts"):
         raise ValueError('scaling must be None, "linear", "base" or "parts"')
+    if ramp not in ("turns", "pairs"):
+        raise ValueError('ramp must be "turns" or "pairs"')
+    if magnitude is not None and not math.isfinite(magnitude):
+        raise ValueError("magnitude must be finite")
     if scaling == "base" and rot_dim > 2:
         base *= factor ** (rot_dim / (rot_dim - 2))
     f = [base ** (-2 * j / rot_dim) for j in range(rot_dim // 2)]
-    magnitude = 1.0
+    mag = 1.0
     if scaling == "linear":
         f = [x / factor for x in f]
     elif scaling == "parts":
         if original_len < 1 or not low_turns < high_turns:
             raise ValueError('"parts" needs original_len and low_turns < high_turns')
-        keep = [min(1.0, max(0.0, (original_len * x / (2 * math.pi) - low_turns) / (high_turns - low_turns))) for x in f]
+        if ramp == "pairs":
+            if base <= 1 or low_turns <= 0:
+                raise ValueError('a ramp over pairs needs a base above 1 and positive low_turns')
+            first, last = (rot_dim * math.log(original_len / (2 * math.pi * n)) / (2 * math.log(base)) for n in (high_turns, low_turns))
+            first, last = max(math.floor(first), 0), min(math.ceil(last), rot_dim - 1)
+            keep = [min(1.0, max(0.0, (last - j) / max(last - first, 1e-3))) for j in range(rot_dim // 2)]
+        else:
+            keep = [min(1.0, max(0.0, (original_len * x / (2 * math.pi) - low_turns) / (high_turns - low_turns))) for x in f]
         f = [x * k + x / factor * (1 - k) for x, k in zip(f, keep)]
-        magnitude = 0.1 * math.log(factor) + 1.0
-    return torch.tensor(f, dtype=torch.float64, device=device), magnitude
+        mag = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(f, dtype=torch.float64, device=device), mag if magnitude is None else float(magnitude)
 
 
 class _Rotary(torch.autograd.Function):
