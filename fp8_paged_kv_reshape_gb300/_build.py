@@ -20,6 +20,7 @@ TORCH_SRC = "torch_calls.cpp"
 # test-only variant for the bounded-wait timeout test (never loaded by the package)
 WITHHOLD_LIB = os.path.join(LIB_DIR, "libkvfp8_withhold.so")
 WITHHOLD_DEFINE = "-DKVFP8_TEST_WITHHOLD_FIRST_CHUNK=1"
+WITHHOLD_SOURCES = ["paged_decode.cu", "paged_decode_block_scaled.cu", "prefill_block_scaled.cu"]
 HEADER = os.path.join(ROOT, "include", "kvfp8.h")
 
 SOURCES = ["kvfp8_api.cu", "reshape_and_cache.cu", "paged_decode.cu", "paged_decode_mixed.cu",
@@ -143,11 +144,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_withhold_variant(verbose: bool = False) -> str:
-    """A test-only copy of the library whose single-query decode kernels withhold the copy
-    of every CTA's first chunk and give up any wait after about 1e5 cycles, so that the
-    bounded-wait timeout path can be driven on a GPU with no copy ever in flight.  Built
-    from the same sources (paged_decode.cu recompiled with one define, the other units
-    reused); the package never loads it."""
+    """A test-only copy of the library whose single-query decode kernels, and whose attention
+    kernels over block scales, withhold the copy of every CTA's first chunk and give up any wait
+    after about 1e5 cycles, so that the bounded-wait timeout path can be driven on a GPU with no
+    copy ever in flight.  Built from the same sources (WITHHOLD_SOURCES recompiled with one
+    define, the other units reused); the package never loads it."""
     build(verbose=verbose)
     if not _stale(WITHHOLD_LIB):
         return WITHHOLD_LIB
@@ -155,8 +156,11 @@ def build_withhold_variant(verbose: bool = False) -> str:
     wdir = os.path.join(OBJ_DIR, "withhold")
     os.makedirs(wdir, exist_ok=True)
     objs = [os.path.join(OBJ_DIR, src.replace(".cu", ".o")) for src in SOURCES]
-    objs[SOURCES.index("paged_decode.cu")] = _compile(
-        nvcc, "paged_decode.cu", os.path.join(wdir, "paged_decode.o"), (WITHHOLD_DEFINE,), verbose)
+    with cf.ThreadPoolExecutor(max_workers=len(WITHHOLD_SOURCES)) as pool:
+        made = pool.map(lambda src: _compile(nvcc, src, os.path.join(wdir, src.replace(".cu", ".o")), (WITHHOLD_DEFINE,), verbose),
+                        WITHHOLD_SOURCES)
+        for src, obj in zip(WITHHOLD_SOURCES, made):
+            objs[SOURCES.index(src)] = obj
     return _link(nvcc, objs, WITHHOLD_LIB)
 
 

@@ -224,12 +224,14 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             if (x == chunk_hi - 1 || x == ce - 1) flags |= kLast;
             if (cs >= chunk_lo && ce <= chunk_hi) flags |= kDirect;
             const uint32_t full = bars + 8 * stage;
+            const bool withheld = kWithholdFirstChunk && issued == 0;  // (test build: neither a copy nor an arrival for this stage)
             if (lane == 0) {
                 if (!mbar_wait(bars + 8 * (S + stage), phase ^ 1u, abort_flag)) {
                     aborted = true;
                 } else {
                     meta[stage] = BlockChunk{s, tok0, mask, flags};
-                    if (boxes > 0)
+                    if (withheld) {
+                    } else if (boxes > 0)
                         mbar_arrive_tx(full, boxes * 2 * f.code_box);
                     else
                         mbar_arrive(full);
@@ -239,16 +241,16 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_const
             if (aborted) break;
             __syncwarp();  // what lane 0 waited for (the stage has been read) holds for every lane's copies
             const uint32_t st = base + static_cast<uint32_t>(stage) * stage_bytes;
-            if (good) {  // the expected bytes are posted: each lane copies its box
+            if (good && !withheld) {  // the expected bytes are posted: each lane copies its box
                 const int row = (blk << lbs) + (t & (a.block_size - 1));
                 tma_load_3d(st + lane * f.code_box, &tmk, 0, row, h0 * SEGS, full);
                 tma_load_3d(st + code_bytes + lane * f.code_box, &tmv, 0, row, h0 * SEGS, full);
             }
-            if (shead < hpc && (goods >> sbox) & 1u)
+            if (shead < hpc && (goods >> sbox) & 1u && !withheld)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(st + 2 * code_bytes + lane * 4),
                              "l"(scales + static_cast<int64_t>(sblk) * f.scale_stride)
                              : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+            if (!withheld) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
             ++issued;
             if (++stage == S) {
                 stage = 0;

@@ -518,13 +518,15 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             const int ts = t0 + 16 * (lane & 3);
             const int sblk = __shfl_sync(0xFFFFFFFFu, win, ((ts >> lbs) - wbase) & 31);
             const uint32_t kfull = bar(L::kKFull, 2 * kb + hf), vfull = bar(L::kVFull, st);
+            const bool withheld = kWithholdFirstChunk && h == 0;  // (test build: neither copies nor arrivals for the first half)
             if (lane == 0) {
                 if ((hf == 0 && !mbar_wait(bar(L::kKFree, kb), ((i / L::kNK) & 1) ^ 1u, abort_flag)) ||
                     !mbar_wait(bar(L::kVEmpty, st), ((h / L::kNS) & 1) ^ 1u, abort_flag)) {
                     aborted = true;
                 } else {
                     meta[st] = mask;
-                    if (boxes > 0) {
+                    if (withheld) {
+                    } else if (boxes > 0) {
                         mbar_arrive_tx(kfull, static_cast<uint32_t>(boxes * br * HD));
                         mbar_arrive_tx(vfull, static_cast<uint32_t>(boxes * br * HD));
                     } else {
@@ -537,7 +539,7 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
             aborted = __shfl_sync(0xFFFFFFFFu, aborted, 0);
             if (aborted) break;
             __syncwarp();  // what lane 0 waited for (the buffers have been read) holds for every lane's copies
-            if (good) {  // the expected bytes are posted: each lane with a box copies it
+            if (good && !withheld) {  // the expected bytes are posted: each lane with a box copies it
                 const int row = blk * bs + (t & (bs - 1));
                 const uint32_t dst = k_lane ? base + L::kK + kb * L::kKBuf + static_cast<uint32_t>((hf * kHalf + p * br) * L::kSeg)
                                             : base + L::kStage + st * L::kStageBuf + static_cast<uint32_t>(p * br * L::kSeg);
@@ -546,11 +548,11 @@ prefill_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_cons
                 for (int sgi = 0; sgi < L::kSegs; ++sgi)
                     tma_load_3d(dst + sgi * seg, map, 0, kvh * L::kSegs + sgi, row, k_lane ? kfull : vfull);
             }
-            if (lane < 8 && ts < kend && sblk >= 0 && sblk < a.num_blocks)
+            if (lane < 8 && ts < kend && sblk >= 0 && sblk < a.num_blocks && !withheld)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(base + L::kScales + 32 * st + 4 * lane),
                              "l"((lane < 4 ? a.key_scales : a.value_scales) + static_cast<int64_t>(sblk) * a.scale_stride + kvh)
                              : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(vfull) : "memory");
+            if (!withheld) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(vfull) : "memory");
         }
         if (aborted) asm volatile("cp.async.wait_all;" ::: "memory");
         if (aborted && lane == 0) {
