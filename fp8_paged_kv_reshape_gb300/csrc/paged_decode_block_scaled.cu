@@ -14,8 +14,8 @@
 //  * A code is an fp16 number: conversion is one cvt per two codes, and 8 warps of an SM have ~3000 cycles
 //    for 32 tokens each at the HBM rate, of which they issue ~700.  HBM bounds it:
 //    64 sequences of 4096 tokens, 32 / 8 heads of 128, 92 us (5.9 TB/s, 86 % of a copy's rate), 8 of 131072 at 8 columns 237
-//    (95 %).  At 16 columns the chain of a chunk does (3000 cycles for two warps a scheduler): four new tokens of 32
-//    sequences of 4096, 54 us.  (Two warps a head with half the columns each: 58, both convert all codes.)
+//    (95 %).  At 16 columns the chain of a chunk does (3000 cycles for two warps a scheduler, which 168 registers hold it to): four
+//    new tokens of 32 sequences of 4096, 56 us.  (Two warps a head with half the columns each: 58, both convert all codes.)
 //  * V (A operand, dims x tokens): ldmatrix.trans gives two tokens' codes of two dims, a byte permute makes
 //    them pairs of tokens.  (The 4-bit kernel's product over (token, dim parity) needs no permute, but its zeros
 //    would spread a NaN code to the dim beside it.)  Up to 4 score columns stand at the even columns of
@@ -57,8 +57,7 @@ struct BlockChunk {
 // fit, and two CTAs share an SM.
 template <int HD>
 __host__ __device__ constexpr int bs_max_heads() { return HD == 64 ? 8 : HD == 128 ? 4 : 2; }
-template <int HD, int NV>
-__host__ __device__ constexpr int bs_ctas_per_sm() { return 2; }
+constexpr int kCtasPerSm = 2;
 
 // A chunk in which some column does not see some token: what such tokens could spread through the product with V is taken out
 // of the head's V codes in the stage, which start at `codes`.  (With a body of its own, unrolled like the common one, such a
@@ -118,7 +117,7 @@ struct StagedValues {
 };
 
 template <int HD, int NV, bool kMulti>
-__global__ void __launch_bounds__(32 * (bs_max_heads<HD>() + 1), (bs_ctas_per_sm<HD, NV>()))
+__global__ void __launch_bounds__(32 * (bs_max_heads<HD>() + 1), kCtasPerSm)
 decode_blocks_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const BlockKernelArgs f) {
     const KernelArgs &a = f.k;
@@ -656,7 +655,7 @@ cudaError_t run_blocks(const DecodeArgs &d, const DecodeWorkspace &ws, cudaStrea
     f.tile_off = box_rows == 32 ? 16 * SEG : f.code_box;
     f.stage_bytes = (2u * kTok * hpc * HD + 128u + 1023u) & ~1023u;
     // CTAs of fewer heads than the limit: as many as have that many warps in all
-    const int ctas_per_sm = bs_ctas_per_sm<HD, NV>() * (bs_max_heads<HD>() + 1) / (hpc + 1);
+    const int ctas_per_sm = kCtasPerSm * (bs_max_heads<HD>() + 1) / (hpc + 1);
     constexpr int kMaxStages = 8;
     auto smem_for = [&](int st) { return static_cast<size_t>(st) * (f.stage_bytes + 32) + 16 + 1024; };
     const size_t sm_budget = static_cast<size_t>(smem_optin) + 1024;

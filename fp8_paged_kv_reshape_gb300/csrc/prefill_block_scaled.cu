@@ -24,8 +24,8 @@
 //    tokens of 16 sequences of 4096 took 612 us where this took 485; one pass half by half, whose sums tell when the reference
 //    has to move and the half is done again, 587.)
 //
-// Measured: that case 452 us (776 TFLOP/s, the tensor pipe 38 % busy), 225 queries on 1500 states in 24 sequences, 16 heads
-// of 64, 87 us.  A 128-key tile of two row tiles takes 4600 cycles: 2300 of products, 2400 of softmax.
+// Measured: that case 450 us (778 TFLOP/s, the tensor pipe 38 % busy), 225 queries on 1500 states in 24 sequences, 16 heads
+// of 64, 88 us.  A 128-key tile of two row tiles takes 4600 cycles: 2300 of products, 2400 of softmax.
 //
 // Two row tiles (head_dim 64 and 128, more than 128 rows) share K tiles and the converted V.  Where tensor memory has room for a
 // score buffer more than row tiles (all but head_dim 128 with two), the next scores are computed meanwhile.
@@ -346,6 +346,8 @@ __device__ __noinline__ FarRow far_tiles(uint32_t base, const uint8_t *bp, uint3
 
 // ---------------------------------------------------------------- the kernel
 
+// One row tile: 10 warps have 168 registers each, of which the scores take 128, so the softmax looks V's scales up as it needs them, and 50
+// to 85 bytes are spilled (128 rows of 8 sequences of 4096 at head_dim 256 152 us).
 // Warps: 4 per row tile softmax (warp w reads TMEM lanes 32*(w%4)..+31, a row a thread), 4 converting V, one per
 // row tile issuing products (the first allocates TMEM), one issuing copies.  Two row tiles: warpgroups trade registers, 128 a
 // thread at the launch, so that the softmax keeps its scores (a warp without work makes up the last group).

@@ -502,6 +502,7 @@ KVFP8_API kvfp8_status kvfp8_paged_attention_multi_fp4(
  *                              stay as they are, and have no meaning
  *   s = max(old scale, P)      otherwise; when that raises it, every code c of the block that the call does not
  *                              write becomes E4M3(dec(c) * (old / s)), the products in float, NaN codes kept
+ *                              (where the old scale is 0 they stay as they are, and have no meaning)
  *   code = E4M3(x / s)         the float quotient, as kvfp8_reshape_and_cache: nearest even, saturating
  *                              (infinities too), NaN -> sign | 0x7F
  * P being a power of two, raising a scale loses only what leaves E4M3's range at the bottom, however
