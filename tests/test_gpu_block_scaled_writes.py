@@ -40,3 +40,21 @@ def test_writes_past_32_bits(n_kv, hd, bs, n):
             got = kv.dequant_block_scaled(bc, bsc, dev(slots + at * bs), torch.float32)
             want = kv.dequant_block_scaled(c, s, dev(slots), torch.float32)
             assert torch.equal(got.view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("dst", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n, n_kv, hd", [(1, 1, 64), (37, 3, 64), (700, 8, 128), (5, 2, 256)])
+def test_rows_read_back_to_any_aligned_place(dst, n, n_kv, hd):
+    """out at 16 bytes past a multiple of 32, and nothing beside it written."""
+    r = np.random.default_rng(n)
+    nb, bs = n // 16 + 2, 16
+    codes = dev(r.integers(0, 0x7F, (nb, bs, n_kv, hd)).astype(np.uint8))
+    scales = dev(np.exp2(r.integers(-20, 20, (nb, -(-n_kv // 4) * 4))).astype(np.float32))
+    slots = dev(r.integers(0, nb * bs, n))
+    want = kv.dequant_block_scaled(codes, scales, slots, dst)
+    size, step = n * n_kv * hd, 16 // want.element_size()
+    buffer = torch.full((size + 4 * step,), 7.0, dtype=dst, device="cuda")
+    out = buffer[step:step + size].view(n, n_kv, hd)
+    assert buffer.data_ptr() % 32 == 0 and out.data_ptr() % 32 == 16
+    assert kv.dequant_block_scaled(codes, scales, slots, dst, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want) and bool((buffer[:step] == 7).all()) and bool((buffer[step + size:] == 7).all())
