@@ -50,6 +50,11 @@ kvfp8_status check_block_cache(int32_t num_blocks, int32_t block_size, int32_t n
     return KVFP8_OK;
 }
 
+// tables whose width in tokens, rounded up to a tile of keys, is an int32 (the attention over block scales)
+bool table_width_ok(int32_t max_blocks_per_seq, int32_t block_size) {
+    return static_cast<int64_t>(max_blocks_per_seq) * block_size <= 0x7FFFFFFFLL - 127;
+}
+
 int32_t log2_of(int32_t x) {  // of a power of two
     int32_t n = 0;
     while ((1 << n) < x) ++n;
@@ -837,7 +842,9 @@ kvfp8_status kvfp8_paged_decode_attention_block_scaled(
         n_q, n_kv, head_dim, block_size, num_blocks, sm_scale, KVFP8_F32, &nothing_to_do);
     if (v != KVFP8_OK) return v;
     const kvfp8_status sh = check_block_cache(num_blocks, block_size, n_kv, head_dim, scale_stride);
-    if (sh != KVFP8_OK || nothing_to_do) return sh;
+    if (sh != KVFP8_OK) return sh;
+    if (!table_width_ok(max_blocks_per_seq, block_size)) return KVFP8_ERR_SHAPE;
+    if (nothing_to_do) return KVFP8_OK;
     const size_t need = kvfp8_paged_attention_block_scaled_workspace_size(num_seqs, n_q, n_kv, head_dim, 1,
                                                                           max_blocks_per_seq, block_size);
     if (!key_scales || !value_scales || (need > 0 && !workspace)) return KVFP8_ERR_NULL;
@@ -885,7 +892,7 @@ kvfp8_status kvfp8_paged_attention_multi_block_scaled(
     if (sh != KVFP8_OK) return sh;
     const bool split_kv = kvfp8::multi_uses_decode_kernel(n_q, n_kv, head_dim, max_query_len);
     if (!split_kv && !kvfp8::prefill_takes(n_q, n_kv, max_query_len, num_seqs)) return KVFP8_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7FFFFFFFLL) return KVFP8_ERR_SHAPE;
+    if (!table_width_ok(max_blocks_per_seq, block_size)) return KVFP8_ERR_SHAPE;
     if (std::isnan(sm_scale) || std::isinf(sm_scale)) return KVFP8_ERR_SCALE;
     if (num_seqs == 0 || num_query_rows == 0) return KVFP8_OK;
     const size_t need = kvfp8_paged_attention_block_scaled_workspace_size(

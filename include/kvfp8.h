@@ -572,7 +572,8 @@ KVFP8_API size_t kvfp8_paged_attention_block_scaled_workspace_size(int32_t num_s
  * A block whose scales are not valid (of either side) holds no tokens for that head and sets
  * KVFP8_DEV_BAD_SCALE.  A token's NaN reaches exactly the outputs that see the token (all of a row for
  * one in K, its own dim for one in V).  An n_kv that falls into more than 65535 equal groups of kv heads
- * (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Everything else (group sizes, empty sequences, bad blocks,
+ * (a large prime) returns KVFP8_ERR_UNSUPPORTED.  Block tables of more than 2^31 - 128 tokens a sequence return
+ * KVFP8_ERR_SHAPE.  Everything else (group sizes, empty sequences, bad blocks,
  * errors) as kvfp8_paged_decode_attention.
  */
 KVFP8_API kvfp8_status kvfp8_paged_decode_attention_block_scaled(
